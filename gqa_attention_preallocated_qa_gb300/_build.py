@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqa.so")
-SOURCES = ["qa_api.cu", "k1_norm_rope_append.cu", "k2_prefill_tcgen05.cu", "k3_decode_splitkv.cu"]
+SOURCES = ["qa_api.cu", "k1_norm_rope_append.cu", "k2_prefill_tcgen05.cu", "k3_decode_splitkv.cu",
+           "q4_api.cu", "k4_q4_rows.cu", "k5_q4_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 

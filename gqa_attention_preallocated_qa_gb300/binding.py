@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "QA_OK", 1: "QA_ERR_INVALID_ARG", 2: "QA_ERR_UNSUPPORTED_SHAP
                 3: "QA_ERR_ALIGNMENT", 4: "QA_ERR_CAPACITY", 5: "QA_ERR_STATE", 6: "QA_ERR_CUDA",
                 7: "QA_ERR_DEVICE_TIMEOUT", 8: "QA_ERR_DEVICE_BOUNDS"}
 KERNELS = ("norm_rope_append", "prefill_attn", "decode_attn", "reset")
+Q4_KERNELS = ("norm_rope", "quantise", "dequantise", "prefill_attn", "decode")
 
 
 class QaError(RuntimeError):
@@ -70,6 +71,23 @@ SIGNATURES = {
     "qa_noalloc_get_device_error": (ctypes.c_int, [_u32p, _vp]),
     "qa_prefill_attend": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp]),
     "qa_debug_arm_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint32]),
+    "qa_q4_cache_alloc": (ctypes.c_int, [ctypes.POINTER(qa_config), ctypes.POINTER(_vp)]),
+    "qa_q4_cache_free": (ctypes.c_int, [_vp]),
+    "qa_q4_cache_set_window": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int]),
+    "qa_q4_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
+                                    _vp, _vp]),
+    "qa_q4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp]),
+    "qa_q4_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _vp]),
+    "qa_q4_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qa_q4_decode_step_device_positions": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp,
+                                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                          _vp]),
+    "qa_q4_cache_view": (ctypes.c_int, [_vp, ctypes.c_int] + [ctypes.POINTER(_vp)] * 4 + [_i64p]),
+    "qa_q4_get_device_error": (ctypes.c_int, [_vp, _u32p]),
+    "qa_q4_stats": (ctypes.c_int, [_vp, _u64p]),
+    "qa_q4_memory_info": (ctypes.c_int, [_vp, _u64p, _u64p]),
     "qa_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "qa_abi_version": (ctypes.c_int, []),
 }
@@ -269,3 +287,108 @@ def cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
     vt = torch.as_tensor(_DeviceArray(v, shape, "<i2"), device="cuda").view(torch.bfloat16)
     lt = torch.as_tensor(_DeviceArray(lens, (max_batch,), "<i4"), device="cuda")
     return kt, vt, lt
+
+
+# ---- 4-bit cache: host position lists may be lists or ready ctypes int32 arrays
+
+def _ranges(start, ntok):
+    if len(start) != len(ntok):
+        raise ValueError("start and ntok need one entry per sequence")
+    return len(start), _i32_of(start), _i32_of(ntok)
+
+
+def _i32_of(values):
+    return values if isinstance(values, ctypes.Array) else _i32(values)
+
+
+def qa_q4_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
+                      rope_theta=1e6, rms_eps=1e-6) -> int:
+    cfg = qa_config(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity, rope_theta,
+                    rms_eps)
+    h = _vp()
+    _check(lib.qa_q4_cache_alloc(ctypes.byref(cfg), ctypes.byref(h)), "qa_q4_cache_alloc")
+    return h.value
+
+
+def qa_q4_cache_free(cache) -> None:
+    _check(lib.qa_q4_cache_free(cache), "qa_q4_cache_free")
+
+
+def qa_q4_cache_set_window(cache, layer, window) -> None:
+    _check(lib.qa_q4_cache_set_window(cache, layer, window), "qa_q4_cache_set_window")
+
+
+def qa_q4_append(cache, layer, start, ntok, k, v, k_held=None, v_held=None, stream=None) -> None:
+    n, s, t = _ranges(start, ntok)
+    _check(lib.qa_q4_append(cache, layer, n, s, t, _ptr(k), _ptr(v), _ptr(k_held), _ptr(v_held),
+                            _stream(stream)), "qa_q4_append")
+
+
+def qa_q4_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
+    n, s, t = _ranges(start, ntok)
+    _check(lib.qa_q4_read(cache, layer, n, s, t, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "qa_q4_read")
+
+
+def qa_q4_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
+                  stream=None) -> None:
+    n, s, t = _ranges(start, ntok)
+    _check(lib.qa_q4_prefill(cache, layer, n, s, t, _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
+                             _ptr(k_norm_w), _ptr(out), _stream(stream)), "qa_q4_prefill")
+
+
+def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
+                      v_held=None, stream=None) -> None:
+    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_of(positions), _ptr(q), _ptr(k),
+                                 _ptr(v), _ptr(q_norm_w), _ptr(k_norm_w), _ptr(out), _ptr(k_held),
+                                 _ptr(v_held), _stream(stream)), "qa_q4_decode_step")
+
+
+def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
+                                       out, k_held=None, v_held=None, stream=None) -> None:
+    """positions: int32 device tensor [batch] (see include/qa.h)."""
+    _check(lib.qa_q4_decode_step_device_positions(
+        cache, layer, batch, _ptr(positions), _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
+        _ptr(k_norm_w), _ptr(out), _ptr(k_held), _ptr(v_held), _stream(stream)),
+           "qa_q4_decode_step_device_positions")
+
+
+def qa_q4_cache_view(cache, layer):
+    """([k_codes, k_scales, v_codes, v_scales] pointers, row strides[3]) of one layer."""
+    ptrs = [_vp() for _ in range(4)]
+    strides = (ctypes.c_int64 * 3)()
+    _check(lib.qa_q4_cache_view(cache, layer, *(ctypes.byref(p) for p in ptrs), strides),
+           "qa_q4_cache_view")
+    return [p.value for p in ptrs], list(strides)
+
+
+def qa_q4_get_device_error(cache):
+    """(status, raw error word); reading clears the word."""
+    w = ctypes.c_uint32()
+    st = lib.qa_q4_get_device_error(cache, ctypes.byref(w))
+    return st, w.value
+
+
+def qa_q4_stats(cache) -> dict:
+    buf = (ctypes.c_uint64 * len(Q4_KERNELS))()
+    _check(lib.qa_q4_stats(cache, buf), "qa_q4_stats")
+    return dict(zip(Q4_KERNELS, list(buf)))
+
+
+def qa_q4_memory_info(cache):
+    held, scr = ctypes.c_uint64(), ctypes.c_uint64()
+    _check(lib.qa_q4_memory_info(cache, ctypes.byref(held), ctypes.byref(scr)), "qa_q4_memory_info")
+    return held.value, scr.value
+
+
+def q4_cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
+    """torch uint8 views of one layer: K codes [max_batch, Hkv, cap, D/2], K scale
+    bytes [max_batch, Hkv, cap, D/32], and the same of V."""
+    import torch
+    ptrs, (seq, head, _) = qa_q4_cache_view(cache, layer)
+    got = []
+    for i, ptr in enumerate(ptrs):
+        row = head_dim // 32 if i % 2 else head_dim // 2
+        got.append(torch.as_tensor(_DeviceArray(ptr, (max_batch, n_kv_heads, capacity, row), "|u1",
+                                                (seq * row, head * row, row, 1)), device="cuda"))
+    return got

@@ -1,0 +1,836 @@
+// k5_q4_decode.cu -- K5: one fused launch per decode step of one layer over the
+// 4-bit cache (and per short chunk of up to 8 new tokens per sequence).
+//
+// With q' the normed and rotated query, K_j = (n_j - 8) s_j and V_j likewise
+// (s per group of 32 values):
+//   t_j = q' . K_j * log2(e) / sqrt(D),  p_j = 2^(t_j - m),  out = sum p_j V_j / sum p_j.
+// Per (sequence, kv head, head group, split) CTA:
+//   1. every warp streams its own chunks of 32 keys (codes and scale bytes of K
+//      and V: four contiguous runs, 4352 bytes at D = 128) through its own ring
+//      in shared memory, filled by bulk copies that its lane 0 issues: no warp
+//      waits for another inside the loop;
+//   2. the CTA's query rows (HPC heads x TPS tokens, at most 8) are normed,
+//      rotated and brought to fp16 with one power of two per row; the last
+//      split's CTA quantises the new tokens' k' and v, writes them to the cache
+//      and attends to them as the cache holds them;
+//   3. codes become fp16 numbers times their scale by a mask and one fused
+//      multiply-add per pair (q4_device.cuh), straight into the A fragments of
+//      warp MMAs (m16n8k16, fp32 accumulate): 16 keys x 16 dims for S^T = K q'^T
+//      with the query rows as the 8 columns, 16 dims x 16 keys for
+//      O^T += V^T P^T.  The order of keys and dims inside a fragment is free as
+//      long as both operands agree on it, so a lane reads the codes where they
+//      lie: 32 dims (one group) of a row for K, and for V the codes of one
+//      eighth of a row from two keys, interleaved by one byte permute.  P goes
+//      from the accumulators to a B fragment by one 8x8 transpose per 8 keys;
+//   4. the warps' partials (m, l, o) are combined in shared memory, pushed to
+//      the CTAs of the cluster (the splits of one sequence and kv head) with
+//      st.async and merged there in a fixed order: no scratch in global memory,
+//      no atomics, the same bits every time.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "q4_device.cuh"
+
+namespace qa {
+
+constexpr int q4_recv_floats(int total, int rows) {
+    int best = 0;
+    for (int S = 1; S <= kQ4MaxSplits; ++S) {
+        const int E = ((total + S - 1) / S + 7) & ~7;
+        const int f = S * (E + 2 * rows);
+        best = f > best ? f : best;
+    }
+    return best;
+}
+
+template <int D, int R>
+struct Q4Shape {
+    static constexpr int kRow = D / 2, kScaleRow = D / kQ4Group;  // bytes of a row
+    static constexpr int kCodes = kQ4Chunk * kRow;                // of a chunk of K (or V)
+    static constexpr int kScales = kQ4Chunk * kScaleRow;
+    static constexpr int kStage = 2 * (kCodes + kScales);
+    // Ring stages per warp: as many as let two CTAs share an SM.
+    static constexpr int kStages = D == 128 && R == 8 ? 2 : 3;
+    static constexpr int kWarpRing = kStages * kStage;
+    static constexpr int kRing = kQ4DecodeWarps * kWarpRing;
+    static constexpr int kPartial = R * (D + 2);                  // floats: o [R][D], (m, l) [R][2]
+    static constexpr int kRecv = q4_recv_floats(R * D, R);
+    static constexpr int kQBytes = R * D * 2;
+    static constexpr int kSmemUsed = 128 + kRing + kQBytes + (kPartial + kRecv) * 4;
+    // Two CTAs per SM at most (the launch record counts on it: see k3_max_resident_ctas).
+    static constexpr int kSmemBytes = kSmemUsed > 80 * 1024 ? kSmemUsed : 80 * 1024;
+    static_assert(kPartial * 4 <= kWarpRing, "a warp's partial fits its ring");
+    static_assert(kStage % 16 == 0 && kScales % 16 == 0, "bulk copies are 16-byte multiples");
+};
+
+// Larger of the two; NaN if either is (a NaN score makes its row NaN).
+__device__ __forceinline__ float q4_max(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float q4_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8x8 transpose of 16-bit elements: lane 4i + j holds elements (i, 2j), (i, 2j+1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, __half2 s, __half2 c) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), s, c);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// A scale pair with the offsets it takes away (see q4_device.cuh).
+struct Q4Scale {
+    __half2 s, lo, hi;
+};
+__device__ __forceinline__ Q4Scale q4_scale2(uint32_t pair) {
+    Q4Scale r;
+    r.s = *reinterpret_cast<const __half2 *>(&pair);
+    r.lo = __hmul2(r.s, __float2half2_rn(-1032.f));
+    r.hi = __hmul2(r.s, __float2half2_rn(-1152.f));
+    return r;
+}
+// Codes in bits 0-3 / 4-7 of each half of w (the latter come out 16 times larger).
+__device__ __forceinline__ uint32_t q4_lo(uint32_t w, const Q4Scale &s) {
+    return hfma2_u((w & 0x000F000Fu) | 0x64006400u, s.s, s.lo);
+}
+__device__ __forceinline__ uint32_t q4_hi(uint32_t w, const Q4Scale &s) {
+    return hfma2_u((w & 0x00F000F0u) | 0x64006400u, s.s, s.hi);
+}
+
+// Physical row of index i (0..7) of an 8-key block: odd pairs are swapped, so
+// that the keys the four lanes of a quad read for V lie in both halves of the
+// shared-memory banks.
+__device__ __forceinline__ int q4_key(int i) { return i ^ ((i >> 1) & 1); }
+
+// RMSNorm + RoPE of one head row over D/8 lanes, with the roundings of the
+// bf16 path; cs: (cos_a, sin_a, cos_b, sin_b) of this lane's 8 dims.
+template <int D>
+__device__ __forceinline__ uint4 q4_norm_rope(const __nv_bfloat16 *src, const __nv_bfloat16 *w,
+                                              const float4 (&cs)[4], float eps, int sub) {
+    constexpr int HALF = D / 16;
+    const unsigned FULL = 0xffffffffu;
+    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
+    const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(w) + sub);
+    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss = fmaf(bf16lo(xw[e]), bf16lo(xw[e]), fmaf(bf16hi(xw[e]), bf16hi(xw[e]), ss));
+#pragma unroll
+    for (int o = HALF; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+    const float r = rsqrtf(ss * (1.0f / D) + eps);
+    uint32_t yw[4], pw[4], ow[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        yw[e] = pack_bf16(bf16lo(ww[e]) * round_bf16(bf16lo(xw[e]) * r),
+                          bf16hi(ww[e]) * round_bf16(bf16hi(xw[e]) * r));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pw[e] = __shfl_xor_sync(FULL, yw[e], HALF);
+    const float sgn = sub < HALF ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        ow[e] = pack_bf16(fmaf(sgn * cs[e].y, bf16lo(pw[e]), bf16lo(yw[e]) * cs[e].x),
+                          fmaf(sgn * cs[e].w, bf16hi(pw[e]), bf16hi(yw[e]) * cs[e].z));
+    return make_uint4(ow[0], ow[1], ow[2], ow[3]);
+}
+
+// Running state of a warp: query rows 2c and 2c + 1 (c = lane % 4) of the MMA's
+// columns; o[t] holds dims (d, d + 1) of both rows for this lane's tile t.
+template <int D>
+struct Q4Acc {
+    float m[2], l[2];
+    float o[D / 16][4];
+};
+
+// One chunk of 32 keys at shared address `st` (K codes, V codes, K scales, V
+// scales).  Keys [klo[x], nk) are seen by row 2c + x; [kvlo, nk) by any row;
+// partial: some key of the chunk is not seen by some row.
+template <int D, int R>
+__device__ __forceinline__ void q4_consume(const uint8_t *st, bool partial, int nk, const int (&klo)[2], int kvlo,
+                                           const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
+                                           Q4Acc<D> &a, int lane) {
+    using Sh = Q4Shape<D, R>;
+    const unsigned FULL = 0xffffffffu;
+    const int r = lane >> 2, c = lane & 3;
+    const uint8_t *sk = st, *sv = st + Sh::kCodes;
+    const uint8_t *ssk = st + 2 * Sh::kCodes, *ssv = ssk + Sh::kScales;
+    const int kr = q4_key(r);
+    float s[2][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        const int k0 = mt * 16 + kr, k1 = k0 + 8;
+        uint32_t w0[D / 32], w1[D / 32];
+        if (D == 128) {
+            const uint4 a0 = *reinterpret_cast<const uint4 *>(sk + k0 * Sh::kRow + c * 16);
+            const uint4 a1 = *reinterpret_cast<const uint4 *>(sk + k1 * Sh::kRow + c * 16);
+            w0[0] = a0.x; w0[1] = a0.y; w0[D / 32 - 2] = a0.z; w0[D / 32 - 1] = a0.w;
+            w1[0] = a1.x; w1[1] = a1.y; w1[D / 32 - 2] = a1.z; w1[D / 32 - 1] = a1.w;
+        } else {
+            const uint2 a0 = *reinterpret_cast<const uint2 *>(sk + k0 * Sh::kRow + c * 8);
+            const uint2 a1 = *reinterpret_cast<const uint2 *>(sk + k1 * Sh::kRow + c * 8);
+            w0[0] = a0.x; w0[1] = a0.y;
+            w1[0] = a1.x; w1[1] = a1.y;
+        }
+        const int g = D == 128 ? c : c >> 1;
+        const Q4Scale s0 = q4_scale2(ssk[k0 * Sh::kScaleRow + g] * 0x01000100u);
+        const Q4Scale s1 = q4_scale2(ssk[k1 * Sh::kScaleRow + g] * 0x01000100u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            mma_f16(s[mt], q4_lo(w0[w], s0), q4_lo(w1[w], s1), q4_hi(w0[w], s0), q4_hi(w1[w], s1),
+                    qb[2 * w][0], qb[2 * w][1]);
+            const uint32_t x0 = w0[w] >> 8, x1 = w1[w] >> 8;
+            mma_f16(s[mt], q4_lo(x0, s0), q4_lo(x1, s1), q4_hi(x0, s0), q4_hi(x1, s1),
+                    qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        }
+    }
+    // Scores in units of log2, masked; online softmax.  P is held 2^12 times
+    // larger, so that fp16 keeps weights down to 2^-26 of the largest with all
+    // its bits; l carries the same factor.
+    constexpr float kLift = 12.f;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float t = s[mt][e] * cs[e & 1];
+            if (partial) {
+                const int key = mt * 16 + (e >> 1) * 8 + kr;
+                if (key >= nk || key < klo[e & 1]) t = -INFINITY;
+            }
+            s[mt][e] = t;
+            mx[e & 1] = q4_max(mx[e & 1], t);
+        }
+    float neg[2], alpha[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 4));
+        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 8));
+        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 16));
+        const float mn = q4_max(a.m[x], mx[x]);
+        alpha[x] = a.m[x] == -INFINITY ? 0.f : q4_ex2(a.m[x] - mn);
+        neg[x] = mn == -INFINITY ? 0.f : mn - kLift;  // a row that has seen no key: p = 0
+        a.m[x] = mn;
+        a.l[x] *= alpha[x];
+    }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+        a.o[t][0] *= alpha[0]; a.o[t][1] *= alpha[1];
+        a.o[t][2] *= alpha[0]; a.o[t][3] *= alpha[1];
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            p[e] = q4_ex2(s[ks][e] - neg[e & 1]);
+            a.l[e & 1] += p[e];
+        }
+        const uint32_t b0 = transpose8x8(pack_f16(p[0], p[1]));
+        const uint32_t b1 = transpose8x8(pack_f16(p[2], p[3]));
+        // V of the keys with fragment indices 2c, 2c+1 (block 0) and 2c+8, 2c+9 (block 1).
+        const int ka = ks * 16 + q4_key(2 * c), kb = ks * 16 + q4_key(2 * c + 1);
+        const int g = D == 128 ? r >> 1 : r >> 2;
+        uint32_t ba = ssv[ka * Sh::kScaleRow + g], bb = ssv[kb * Sh::kScaleRow + g];
+        uint32_t bc = ssv[(ka + 8) * Sh::kScaleRow + g], bd = ssv[(kb + 8) * Sh::kScaleRow + g];
+        if (partial) {  // rows that no query row sees may hold anything: a zero scale drops them
+            if (ka >= nk || ka < kvlo) ba = 0;
+            if (kb >= nk || kb < kvlo) bb = 0;
+            if (ka + 8 >= nk || ka + 8 < kvlo) bc = 0;
+            if (kb + 8 >= nk || kb + 8 < kvlo) bd = 0;
+        }
+        const Q4Scale s0 = q4_scale2(__byte_perm(ba, bb, 0x4101));
+        const Q4Scale s1 = q4_scale2(__byte_perm(bc, bd, 0x4101));
+        constexpr int NW = D / 64;  // words of a lane's part of a row
+        uint32_t va[NW], vb[NW], vc[NW], vd[NW];
+        const uint8_t *base = sv + r * (4 * NW);
+        if (NW == 2) {
+            const uint2 xa = *reinterpret_cast<const uint2 *>(base + ka * Sh::kRow);
+            const uint2 xb = *reinterpret_cast<const uint2 *>(base + kb * Sh::kRow);
+            const uint2 xc = *reinterpret_cast<const uint2 *>(base + (ka + 8) * Sh::kRow);
+            const uint2 xd = *reinterpret_cast<const uint2 *>(base + (kb + 8) * Sh::kRow);
+            va[0] = xa.x; va[NW - 1] = xa.y; vb[0] = xb.x; vb[NW - 1] = xb.y;
+            vc[0] = xc.x; vc[NW - 1] = xc.y; vd[0] = xd.x; vd[NW - 1] = xd.y;
+        } else {
+            va[0] = *reinterpret_cast<const uint32_t *>(base + ka * Sh::kRow);
+            vb[0] = *reinterpret_cast<const uint32_t *>(base + kb * Sh::kRow);
+            vc[0] = *reinterpret_cast<const uint32_t *>(base + (ka + 8) * Sh::kRow);
+            vd[0] = *reinterpret_cast<const uint32_t *>(base + (kb + 8) * Sh::kRow);
+        }
+#pragma unroll
+        for (int y = 0; y < NW; ++y)
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {
+                const uint32_t w0 = __byte_perm(va[y], vb[y], hl ? 0x7632 : 0x5410);
+                const uint32_t w1 = __byte_perm(vc[y], vd[y], hl ? 0x7632 : 0x5410);
+                mma_f16(a.o[y * 4 + hl * 2], q4_lo(w0, s0), q4_hi(w0, s0), q4_lo(w1, s1),
+                        q4_hi(w1, s1), b0, b1);
+                mma_f16(a.o[y * 4 + hl * 2 + 1], q4_lo(w0 >> 8, s0), q4_hi(w0 >> 8, s0),
+                        q4_lo(w1 >> 8, s1), q4_hi(w1 >> 8, s1), b0, b1);
+            }
+    }
+}
+
+template <int D, int HPC, int TPS>
+__global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
+    q4_decode_kernel(const __grid_constant__ Q4DecodeParams p) {
+    constexpr int R = HPC * TPS;
+    static_assert(R <= 8, "query rows are the 8 columns of the MMA tile");
+    using Sh = Q4Shape<D, R>;
+    constexpr int NW = kQ4DecodeWarps, NS = Sh::kStages, LPR = D / 8;
+    const unsigned FULL = 0xffffffffu;
+
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar_ring[NW * NS], bar_recv;
+    __shared__ int s_abort;
+    __shared__ __align__(16) __nv_bfloat16 s_newk[TPS * D], s_newv[TPS * D];  // as the cache holds them
+    __shared__ float s_c[R];                                    // log2 units per raw score of a row
+    __shared__ float s_w[R * kQ4MaxSplits], s_linv[R];
+
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    __half *qs = reinterpret_cast<__half *>(smem + Sh::kRing);
+    float *part_new = reinterpret_cast<float *>(smem + Sh::kRing + Sh::kQBytes);
+    float *recv = part_new + Sh::kPartial;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.S, split = blockIdx.x;
+    const int kvh = blockIdx.y / p.HG, hg = blockIdx.y % p.HG;
+    const int z = blockIdx.z;
+    const int ntok = TPS == 1 ? 1 : p.ntok[z];
+    const int64_t row_base = static_cast<int64_t>(p.seq[z]) * p.row_seq + kvh * p.row_head;
+    const int h_first = kvh * p.G + hg * HPC;
+    const bool owner = split == S - 1;
+    const bool dev = p.pos_dev != nullptr;
+    int pos = dev ? 0 : p.pos[z];
+
+    // Merge geometry: the CTA's R x D outputs are dealt to the cluster's CTAs in runs of E.
+    constexpr int total = R * D;
+    const int E = ((total + S - 1) / S + 7) & ~7;
+    const int e_lo = split * E;
+    const int E_me = max(0, min(E, total - e_lo));
+    const int g_lo = e_lo / D;
+    const int nh_me = E_me > 0 ? (e_lo + E_me - 1) / D - g_lo + 1 : 0;
+    float *rcv_o = recv, *rcv_ml = recv + S * E;
+
+    bool pos_ok = false;
+    int c_begin = 0, c_end = 0, c_safe = 0, key_lo = 0;
+    auto plan = [&]() {
+        pos_ok = pos >= 0 && ntok >= 1 && ntok <= TPS && pos + ntok <= p.cap;
+        const int nchunks = pos_ok ? (pos + kQ4Chunk - 1) / kQ4Chunk : 0;
+        key_lo = (pos_ok && p.window > 0) ? max(0, pos + 1 - p.window) : 0;
+        const int c_lo = min(key_lo / kQ4Chunk, nchunks);
+        const int64_t n = nchunks - c_lo;
+        c_begin = c_lo + static_cast<int>(split * n / S);
+        c_end = c_lo + static_cast<int>((split + 1) * n / S);
+        c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
+    };
+    if (!dev) plan();
+
+    uint8_t *ring = smem + warp * Sh::kWarpRing;
+    const uint32_t bar0 = smem_u32(&bar_ring[warp * NS]);
+    auto issue = [&](int c, int st) {  // lane 0 of the warp
+        const uint32_t bar = bar0 + 8 * st, dst = smem_u32(ring + st * Sh::kStage);
+        const int64_t row = row_base + static_cast<int64_t>(c) * kQ4Chunk;
+        mbar_expect_tx(bar, Sh::kStage);
+        bulk_g2s(dst, p.kc + row * Sh::kRow, Sh::kCodes, bar);
+        bulk_g2s(dst + Sh::kCodes, p.vc + row * Sh::kRow, Sh::kCodes, bar);
+        bulk_g2s(dst + 2 * Sh::kCodes, p.ks + row * Sh::kScaleRow, Sh::kScales, bar);
+        bulk_g2s(dst + 2 * Sh::kCodes + Sh::kScales, p.vs + row * Sh::kScaleRow, Sh::kScales, bar);
+    };
+    // Chunks of this warp: c_begin + warp + NW * i; `issued` of them are on the way.
+    int issued = 0;
+    auto fill = [&](int limit) {  // lane 0: the first round, below chunk `limit`
+        for (; issued < NS; ++issued) {
+            const int c = c_begin + warp + NW * issued;
+            if (c >= c_end || c >= limit) break;
+            issue(c, issued);
+        }
+    };
+    if (lane == 0) {
+        for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1);
+        if (warp == 0) {
+            mbar_init(smem_u32(&bar_recv), 1);
+            s_abort = 0;
+            if (E_me > 0) mbar_expect_tx(smem_u32(&bar_recv), S * (E_me * 4 + nh_me * 8));
+        }
+        fence_mbar_init();
+        if (!dev) fill(c_safe);
+    }
+    __syncwarp();
+    cluster_arrive();  // peers may push into this CTA once they have waited on this
+
+    // Programmatic dependent launch.  Cache rows that no running launch writes
+    // are loaded before the wait; with `early` the next launch may start now.
+    if (!dev && p.early) {
+        griddep_launch_dependents();
+    } else {
+        griddep_wait();
+        griddep_launch_dependents();
+        if (dev) {
+            pos = p.pos_dev[p.b0 + z];
+            plan();
+        }
+        if (lane == 0) fill(c_end);
+    }
+    if (!pos_ok) {
+        if (threadIdx.x == 0) set_error(p.err, kErrBounds, kKernQ4Decode, 1);
+        cluster_wait();
+        griddep_wait();
+        return;
+    }
+
+    // ---------------------------------------------------------------- query rows and new tokens
+    const int sub = lane % LPR;
+    uint32_t new_codes[2];  // of the item below, when it is a new token
+    uint32_t new_byte[2];
+    uint4 new_held[2];
+    const int nitems = R + (owner ? ntok : 0);
+    for (int it = NW - 1 - warp; it < nitems; it += NW) {  // warp-uniform
+        const int t = it < R ? it / HPC : it - R;
+        if (t >= ntok) continue;
+        float4 cs[4];
+        const float4 *tab = reinterpret_cast<const float4 *>(
+            p.rope + static_cast<int64_t>(pos + t) * (D / 2) + 8 * (sub % (LPR / 2)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = __ldg(tab + e);
+        if (it < R) {
+            const uint4 x = q4_norm_rope<D>(
+                p.q + (static_cast<int64_t>(p.row0[z] + t) * p.Hq + h_first + it % HPC) * D, p.wq, cs,
+                p.eps, sub);
+            // fp16 with one power of two per row: the largest magnitude goes to
+            // [256, 512), so bf16's 8 bits survive down to 2^-22 of it.
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t mx = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, xw[e] & 0x7fff7fffu);
+            mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, o));
+            // exponent field of the largest magnitude, kept where 2^(8 - e) and its inverse are finite
+            const int ex = min(max(static_cast<int>(mx >> 7), 20), 254) - 127;
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - ex) << 23);
+            uint4 h;
+            h.x = pack_f16(bf16lo(x.x) * up, bf16hi(x.x) * up);
+            h.y = pack_f16(bf16lo(x.y) * up, bf16hi(x.y) * up);
+            h.z = pack_f16(bf16lo(x.z) * up, bf16hi(x.z) * up);
+            h.w = pack_f16(bf16lo(x.w) * up, bf16hi(x.w) * up);
+            if (lane < LPR) {
+                reinterpret_cast<uint4 *>(qs + it * D)[sub] = h;
+                if (lane == 0) s_c[it] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex - 8) << 23);
+            }
+        } else {
+            const int64_t kr = (static_cast<int64_t>(p.row0[z] + t) * p.Hkv + kvh) * D;
+            const uint4 kp = q4_norm_rope<D>(p.k + kr, p.wk, cs, p.eps, sub);
+            const uint4 vv = __ldg(reinterpret_cast<const uint4 *>(p.v + kr) + sub);
+            new_codes[0] = q4_quantise8<true>(kp, new_byte[0], new_held[0]);
+            new_codes[1] = q4_quantise8<true>(vv, new_byte[1], new_held[1]);
+            if (lane < LPR) {
+                reinterpret_cast<uint4 *>(s_newk + t * D)[sub] = new_held[0];
+                reinterpret_cast<uint4 *>(s_newv + t * D)[sub] = new_held[1];
+            }
+        }
+    }
+    __syncthreads();  // query rows and new tokens in shared memory
+
+    // ---------------------------------------------------------------- new tokens
+    // A partial of their own (m, l, o): warp w serves rows w, w + NW, ...
+    if (owner) {
+        for (int row = warp; row < R; row += NW) {
+            const int t = row / HPC;
+            constexpr int PER = D / 32;
+            float M = -INFINITY, L = 0.f, O[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) O[e] = 0.f;
+            if (t < ntok) {
+                float sc[TPS];
+#pragma unroll
+                for (int u = 0; u < TPS; ++u) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e)
+                        x = fmaf(__half2float(qs[row * D + e * 32 + lane]),
+                                 __bfloat162float(s_newk[u * D + e * 32 + lane]), x);
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+                    const bool seen = u <= t && (p.window <= 0 || t - u < p.window);
+                    sc[u] = seen ? x * s_c[row] : -INFINITY;
+                    M = q4_max(M, sc[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < TPS; ++u) {
+                    if (u > t || sc[u] == -INFINITY) continue;
+                    const float w = q4_ex2(sc[u] - M);
+                    L += w;
+#pragma unroll
+                    for (int e = 0; e < PER; ++e)
+                        O[e] = fmaf(w, __bfloat162float(s_newv[u * D + e * 32 + lane]), O[e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < PER; ++e) part_new[row * D + e * 32 + lane] = O[e];
+            if (lane == 0) {
+                part_new[R * D + 2 * row] = M;
+                part_new[R * D + 2 * row + 1] = L;
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- the cache's keys
+    const int r = lane >> 2, c4 = lane & 3;
+    {
+        uint32_t qb[D / 16][2];
+        const int qt = TPS == 1 ? 0 : r / HPC;
+        const bool real = r < R && qt < ntok;
+        // B fragments: this lane's dims are those of its part of a row of K; the
+        // codes of odd dims come 16 times larger, their queries 16 times smaller.
+        const __half *qrow = qs + (real ? r : 0) * D + c4 * (D / 4);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+            const uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
+            const uint32_t even_lo = __byte_perm(q8.x, q8.z, 0x5410);  // dims 0, 4
+            const uint32_t odd_lo = __byte_perm(q8.x, q8.z, 0x7632);   // dims 1, 5
+            const uint32_t even_hi = __byte_perm(q8.y, q8.w, 0x5410);  // dims 2, 6
+            const uint32_t odd_hi = __byte_perm(q8.y, q8.w, 0x7632);   // dims 3, 7
+            const __half2 down = __float2half2_rn(0.0625f), none = __float2half2_rn(0.f);
+            qb[2 * w][0] = real ? even_lo : 0u;
+            qb[2 * w][1] = real ? hfma2_u(odd_lo, down, none) : 0u;
+            qb[2 * w + 1][0] = real ? even_hi : 0u;
+            qb[2 * w + 1][1] = real ? hfma2_u(odd_hi, down, none) : 0u;
+        }
+        float cs[2];
+        int row_lo[2];
+        Q4Acc<D> a;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = 2 * c4 + x;
+            const int t = TPS == 1 ? 0 : col / HPC;
+            cs[x] = col < R && t < ntok ? s_c[col] : 0.f;
+            row_lo[x] = p.window > 0 ? max(0, pos + t + 1 - p.window) : 0;
+            a.m[x] = -INFINITY;
+            a.l[x] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.o[t][e] = 0.f;
+
+        bool waited = !(!dev && p.early);
+        int st = 0;
+        uint32_t phase = 0;
+        int i = 0;
+        for (int c = c_begin + warp; c < c_end; c += NW, ++i) {
+            if (lane == 0 && issued == i) {  // not sent ahead: the chunk holds rows being written
+                if (!waited) {
+                    griddep_wait();
+                    waited = true;
+                }
+                for (int n = 0; n < NS; ++n) {
+                    const int cn = c + NW * n;
+                    if (cn >= c_end) break;
+                    issue(cn, (i + n) % NS);
+                    ++issued;
+                }
+            }
+            bool ok = mbar_wait(bar0 + 8 * st, phase, &s_abort, p.err, kKernQ4Decode, 2);
+            ok = __all_sync(FULL, ok);
+            if (!ok) break;
+            const int base = c * kQ4Chunk;
+            const int klo[2] = {min(kQ4Chunk, max(0, row_lo[0] - base)), min(kQ4Chunk, max(0, row_lo[1] - base))};
+            const bool partial = pos - base < kQ4Chunk || (p.window > 0 && pos + ntok - p.window > base);
+            q4_consume<D, R>(ring + st * Sh::kStage, partial, min(kQ4Chunk, pos - base), klo,
+                             max(0, key_lo - base), qb, cs, a, lane);
+            // The warp's reads of the stage come before the next copy into it.
+            fence_proxy_async_smem();
+            __syncwarp();
+            const int cn = c + NW * NS;
+            if (lane == 0 && cn < c_end && issued == i + NS) {
+                if (!waited && cn >= c_safe) {
+                    griddep_wait();
+                    waited = true;
+                }
+                issue(cn, st);
+                ++issued;
+            }
+            if (++st == NS) {
+                st = 0;
+                phase ^= 1;
+            }
+        }
+        if (lane == 0) {
+            // No copy may land after the CTA exits or into the partial below.
+            for (int k = i; k < issued; ++k) {
+                int dummy = 0;
+                mbar_wait(bar0 + 8 * (k % NS), (k / NS) & 1, &dummy, p.err, kKernQ4Decode, 3);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            a.l[x] += __shfl_xor_sync(FULL, a.l[x], 4);
+            a.l[x] += __shfl_xor_sync(FULL, a.l[x], 8);
+            a.l[x] += __shfl_xor_sync(FULL, a.l[x], 16);
+        }
+        // The warp's partial, in its own ring.
+        float *part = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int col = 2 * c4 + x;
+            if (col < R) {
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t)
+                    *reinterpret_cast<float2 *>(part + col * D + r * (D / 8) + 2 * t) =
+                        make_float2(a.o[t][x], a.o[t][2 + x] * 0.0625f);
+                if (r == 0) {
+                    part[R * D + 2 * col] = a.m[x];
+                    part[R * D + 2 * col + 1] = a.l[x];
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- combine and push
+    __syncthreads();
+    cluster_wait();  // every peer's receive barrier is initialised
+    {
+        constexpr int kWF = Sh::kWarpRing / 4;
+        const float *red = reinterpret_cast<const float *>(smem);
+        const uint32_t a_bar = smem_u32(&bar_recv);
+        const uint32_t a_o = smem_u32(rcv_o + split * E);
+        auto weights = [&](int g, float (&w)[NW + 1], float &M) {
+            M = owner ? part_new[R * D + 2 * g] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) M = q4_max(M, red[i * kWF + R * D + 2 * g]);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                const float mi = red[i * kWF + R * D + 2 * g];
+                w[i] = mi == -INFINITY ? 0.f : q4_ex2(mi - M);
+            }
+            const float mn = owner ? part_new[R * D + 2 * g] : -INFINITY;
+            // the warps' partials carry the factor 2^12 of their P
+            w[NW] = mn == -INFINITY ? 0.f : q4_ex2(mn - M) * 4096.f;
+        };
+        for (int pe = threadIdx.x; pe < total / 2; pe += blockDim.x) {
+            const int e = 2 * pe, g = e / D, d = e % D;
+            float w[NW + 1], M;
+            weights(g, w, M);
+            float2 O = make_float2(0.f, 0.f);
+            if (w[NW] != 0.f) O = make_float2(w[NW] * part_new[g * D + d], w[NW] * part_new[g * D + d + 1]);
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+                if (w[i] != 0.f) {
+                    const float2 x = *reinterpret_cast<const float2 *>(red + i * kWF + g * D + d);
+                    O = make_float2(fmaf(w[i], x.x, O.x), fmaf(w[i], x.y, O.y));
+                }
+            }
+            const int dst = e / E;
+            st_async_f32x2(map_rank(a_o + 4u * (e - dst * E), dst), O.x, O.y, map_rank(a_bar, dst));
+        }
+        for (int k = threadIdx.x; k < R * S; k += blockDim.x) {
+            const int g = k / S, dst = k % S;
+            const int lo = dst * E, hi = min(lo + E, total);
+            if (lo < hi && lo < (g + 1) * D && hi > g * D) {
+                float w[NW + 1], M, L = 0.f;
+                weights(g, w, M);
+                if (w[NW] != 0.f) L = w[NW] * part_new[R * D + 2 * g + 1];
+#pragma unroll
+                for (int i = 0; i < NW; ++i)
+                    if (w[i] != 0.f) L = fmaf(w[i], red[i * kWF + R * D + 2 * g + 1], L);
+                st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L,
+                               map_rank(a_bar, dst));
+            }
+        }
+    }
+
+    // ---------------------------------------------------------------- merge
+    constexpr int kThreads = NW * 32;
+    constexpr int kOutPer = (total + kThreads - 1) / kThreads;
+    float res[kOutPer];
+    bool merged = E_me > 0;
+    if (E_me > 0) {
+        bool ok = mbar_wait_cluster(smem_u32(&bar_recv), 0, &s_abort, p.err, kKernQ4Decode, 4);
+        if (!ok) {  // the peers still push here: their stores land before this CTA exits
+            int dummy = 0;
+            mbar_wait_cluster(smem_u32(&bar_recv), 0, &dummy, p.err, kKernQ4Decode, 5);
+        }
+        merged = __syncthreads_and(ok);
+        if (merged) {
+            for (int hl = warp; hl < nh_me; hl += NW) {
+                const float *ml = rcv_ml + 2 * (g_lo + hl);
+                const float mi = lane < S ? ml[2 * R * lane] : -INFINITY;
+                float M = mi;
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) M = q4_max(M, __shfl_xor_sync(FULL, M, o));
+                float Ls = 0.f;
+                if (lane < S) {
+                    const float w = mi == -INFINITY ? 0.f : q4_ex2(mi - M);
+                    s_w[hl * kQ4MaxSplits + lane] = w;
+                    Ls = w == 0.f ? 0.f : w * ml[2 * R * lane + 1];
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) Ls += __shfl_xor_sync(FULL, Ls, o);
+                if (lane == 0) s_linv[hl] = 1.f / Ls;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kOutPer; ++j) {
+                const int k = threadIdx.x + j * kThreads;
+                res[j] = 0.f;
+                if (k < E_me) {
+                    const int g = (e_lo + k) / D, hl = g - g_lo;
+                    float O = 0.f;
+                    for (int i = 0; i < S; ++i) {
+                        const float w = s_w[hl * kQ4MaxSplits + i];
+                        if (w != 0.f) O = fmaf(w, rcv_o[i * E + k], O);
+                    }
+                    res[j] = O * s_linv[hl];
+                }
+            }
+        }
+    }
+    griddep_wait();  // before any global write
+    // The new rows: each item's warp still holds its codes.
+    if (owner && hg == 0) {
+        for (int it = NW - 1 - warp; it < nitems; it += NW) {
+            if (it < R || lane >= LPR) continue;
+            const int t = it - R;
+            const int64_t row = row_base + pos + t;
+            reinterpret_cast<uint32_t *>(p.kc)[row * LPR + sub] = new_codes[0];
+            reinterpret_cast<uint32_t *>(p.vc)[row * LPR + sub] = new_codes[1];
+            if ((sub & 3) == 0) {
+                p.ks[row * Sh::kScaleRow + sub / 4] = static_cast<uint8_t>(new_byte[0]);
+                p.vs[row * Sh::kScaleRow + sub / 4] = static_cast<uint8_t>(new_byte[1]);
+            }
+            if (p.k_held) {
+                const int64_t kr = (static_cast<int64_t>(p.row0[z] + t) * p.Hkv + kvh) * D;
+                reinterpret_cast<uint4 *>(p.k_held + kr)[sub] = new_held[0];
+                reinterpret_cast<uint4 *>(p.v_held + kr)[sub] = new_held[1];
+            }
+        }
+    }
+    if (!merged) return;
+#pragma unroll
+    for (int j = 0; j < kOutPer; ++j) {
+        const int k = threadIdx.x + j * kThreads;
+        if (k < E_me) {
+            const int e = e_lo + k, g = e / D, d = e % D;
+            const int t = g / HPC, hh = g % HPC;
+            if (t < ntok)
+                p.out[(static_cast<int64_t>(p.row0[z] + t) * p.Hq + h_first + hh) * D + d] =
+                    __float2bfloat16_rn(res[j]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launch
+template <int D, int HPC, int TPS>
+static cudaError_t q4_configure() {
+    auto kern = q4_decode_kernel<D, HPC, TPS>;
+    static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 32 && ((configured.load(std::memory_order_acquire) >> dev) & 1u)) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Q4Shape<D, HPC * TPS>::kSmemBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
+    return e;
+}
+
+template <int D, int HPC, int TPS>
+static void q4_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int S, int gy, int gz,
+                      cudaStream_t stream) {
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = dim3(S, gy, gz);
+    cfg.blockDim = dim3(kQ4DecodeWarps * 32);
+    cfg.dynamicSmemBytes = Q4Shape<D, HPC * TPS>::kSmemBytes;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;  // one cluster = the splits of a group
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+}
+
+template <int D, int HPC, int TPS>
+static cudaError_t q4_launch(const Q4DecodeParams &p, cudaStream_t stream) {
+    cudaError_t e = q4_configure<D, HPC, TPS>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    q4_config<D, HPC, TPS>(cfg, attr, p.S, p.Hkv * p.HG, p.B, stream);
+    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, HPC, TPS>, p);
+}
+
+template <int D, int HPC, int TPS>
+static int q4_capacity(int S) {
+    static std::atomic<int> cache[32][kQ4MaxSplits + 1] = {};  // clusters + 1; 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 32) {
+        const int known = cache[dev][S].load(std::memory_order_acquire);
+        if (known) return known - 1;
+    }
+    int n = 0;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    q4_config<D, HPC, TPS>(cfg, attr, S, 1, 1, nullptr);
+    cfg.numAttrs = 1;
+    if (q4_configure<D, HPC, TPS>() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, q4_decode_kernel<D, HPC, TPS>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (dev < 32) cache[dev][S].store(n + 1, std::memory_order_release);
+    return n;
+}
+
+// Calls f<D, HPC, TPS>(args...) for the run-time shape.
+#define QA_Q4_DISPATCH(f, ...)                                             \
+    do {                                                                   \
+        if (D == 128) {                                                    \
+            if (HPC == 8) return multi ? f<128, 8, 1>(__VA_ARGS__) : f<128, 8, 1>(__VA_ARGS__); \
+            if (HPC == 4) return multi ? f<128, 4, 2>(__VA_ARGS__) : f<128, 4, 1>(__VA_ARGS__); \
+            if (HPC == 2) return multi ? f<128, 2, 4>(__VA_ARGS__) : f<128, 2, 1>(__VA_ARGS__); \
+            if (HPC == 1) return multi ? f<128, 1, 8>(__VA_ARGS__) : f<128, 1, 1>(__VA_ARGS__); \
+        } else if (D == 64) {                                              \
+            if (HPC == 8) return multi ? f<64, 8, 1>(__VA_ARGS__) : f<64, 8, 1>(__VA_ARGS__); \
+            if (HPC == 4) return multi ? f<64, 4, 2>(__VA_ARGS__) : f<64, 4, 1>(__VA_ARGS__); \
+            if (HPC == 2) return multi ? f<64, 2, 4>(__VA_ARGS__) : f<64, 2, 1>(__VA_ARGS__); \
+            if (HPC == 1) return multi ? f<64, 1, 8>(__VA_ARGS__) : f<64, 1, 1>(__VA_ARGS__); \
+        }                                                                  \
+    } while (0)
+
+cudaError_t launch_q4_decode(const Q4DecodeParams &p, int D, int HPC, bool multi, cudaStream_t stream) {
+    QA_Q4_DISPATCH(q4_launch, p, stream);
+    return cudaErrorInvalidValue;
+}
+
+int q4_cluster_capacity(int D, int HPC, bool multi, int S) {
+    if (S < 1 || S > kQ4MaxSplits) return 0;
+    QA_Q4_DISPATCH(q4_capacity, S);
+    return 0;
+}
+
+}  // namespace qa

@@ -1,0 +1,644 @@
+// q4_api.cu -- the 4-bit cache of include/qa.h (qa_q4_*): its memory, argument
+// validation, the split plan of its decode kernel and the order of its
+// launches on the caller's stream.  As in qa_api.cu an unsupported shape or an
+// invalid argument returns a status before anything is enqueued.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "q4_internal.h"
+#include "qa.h"
+
+#define QA_API extern "C" __attribute__((visibility("default")))
+
+struct qa_q4_cache {
+    qa_config cfg{};
+    int device = 0;
+    int num_sms = 0;
+    int G = 1;
+    int rows = 0;              // rows of one (sequence, kv head): the capacity, padded
+    int64_t layer_rows = 0;    // rows of one layer
+    uint8_t *codes[2] = {}, *scales[2] = {};  // K and V
+    // Prefill attention reads one layer's rows in bf16: the sequences of a
+    // launch, dequantised, laid out [slot][kv head][capacity][head_dim].
+    int ws_slots = 0;
+    __nv_bfloat16 *ws[2] = {};
+    cudaEvent_t ws_free = nullptr;  // the last prefill that used the workspace
+    int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
+    float2 *rope = nullptr;
+    uint32_t *err = nullptr;
+    std::vector<int> window;        // per layer: attention window in keys (0: full)
+    // Per (layer, sequence): the position after the last one written, -1 when
+    // only the device knows it.  A decode step that continues there can tell
+    // which rows a launch still running may write.
+    std::vector<int32_t> next_pos;
+    uint64_t cache_bytes = 0, scratch_bytes = 0;
+    std::atomic<uint64_t> launches[QA_Q4_NUM_KERNELS];
+};
+
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Makes the cache's device current for one call.
+class DeviceScope {
+  public:
+    explicit DeviceScope(int device) {
+        ok_ = cudaGetDevice(&before_) == cudaSuccess &&
+              (before_ == device || cudaSetDevice(device) == cudaSuccess);
+        back_ = ok_ && before_ != device;
+    }
+    ~DeviceScope() {
+        if (back_) cudaSetDevice(before_);
+    }
+    bool ok() const { return ok_; }
+
+  private:
+    int before_ = 0;
+    bool ok_ = false, back_ = false;
+};
+
+template <typename T>
+bool dev_alloc(T **p, size_t count, uint64_t &acct) {
+    const size_t bytes = std::max<size_t>(count, 1) * sizeof(T);
+    if (cudaMalloc(reinterpret_cast<void **>(p), bytes) != cudaSuccess) {
+        *p = nullptr;
+        return false;
+    }
+    acct += bytes;
+    return cudaMemset(*p, 0, bytes) == cudaSuccess;
+}
+
+void free_all(qa_q4_cache *c) {
+    for (int i = 0; i < 2; ++i) {
+        cudaFree(c->codes[i]);
+        cudaFree(c->scales[i]);
+        cudaFree(c->ws[i]);
+    }
+    cudaFree(c->ws_lens);
+    cudaFree(c->rope);
+    cudaFree(c->err);
+    if (c->ws_free) cudaEventDestroy(c->ws_free);
+}
+
+qa_status check_layer(const qa_q4_cache *c, int layer, int batch) {
+    if (!c) return QA_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= c->cfg.num_layers) return QA_ERR_INVALID_ARG;
+    if (batch < 1 || batch > c->cfg.max_batch) return QA_ERR_INVALID_ARG;
+    return QA_OK;
+}
+
+// Ranges start[b] .. start[b] + ntok[b] - 1 of the call; T: their rows.
+qa_status check_ranges(const qa_q4_cache *c, int batch, const int32_t *start, const int32_t *ntok,
+                       int64_t *T_out) {
+    if (!start || !ntok) return QA_ERR_INVALID_ARG;
+    int64_t T = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (start[b] < 0 || ntok[b] < 0) return QA_ERR_INVALID_ARG;
+        if (static_cast<int64_t>(start[b]) + ntok[b] > c->cfg.capacity) return QA_ERR_CAPACITY;
+        T += ntok[b];
+    }
+    if (T > (int64_t(1) << 26)) return QA_ERR_INVALID_ARG;
+    *T_out = T;
+    return QA_OK;
+}
+
+int32_t *next_of(qa_q4_cache *c, int layer) {
+    return c->next_pos.data() + static_cast<size_t>(layer) * c->cfg.max_batch;
+}
+
+// Row-kernel parameters common to every launch on `layer`.
+qa::Q4RowsParams make_rows(const qa_q4_cache *c, int layer) {
+    const qa_config &g = c->cfg;
+    qa::Q4RowsParams p{};
+    for (int i = 0; i < 2; ++i) {
+        p.codes[i] = c->codes[i] + layer * c->layer_rows * (g.head_dim / 2);
+        p.scales[i] = c->scales[i] + layer * c->layer_rows * (g.head_dim / qa::kQ4Group);
+    }
+    p.row_head = c->rows;
+    p.row_seq = static_cast<int64_t>(c->rows) * g.n_kv_heads;
+    p.Hkv = g.n_kv_heads;
+    p.kv_first = 0;
+    p.kv_count = 2;
+    return p;
+}
+
+// Packed [T][Hkv][D] rows on either side.
+void packed_rows(const qa_config &g, int64_t &tok, int64_t &head) {
+    tok = static_cast<int64_t>(g.n_kv_heads) * g.head_dim;
+    head = g.head_dim;
+}
+
+// The rows of sequences s0 .. s0 + n - 1 of a call on packed tensors, row0 the
+// first one's first packed row; false when there is none.
+bool fill_ranges(qa::Q4RowsParams &p, const qa_config &g, int s0, int n, const int32_t *start,
+                 const int32_t *ntok, int64_t row0) {
+    const int per = qa::q4_block_tokens(g.head_dim);
+    p.nseq = n;
+    p.seq0 = s0;
+    p.nblocks = 0;
+    for (int i = 0; i < n; ++i) {
+        p.start[i] = start[s0 + i];
+        p.ntok[i] = ntok[s0 + i];
+        p.block0[i] = p.nblocks;
+        p.nblocks += (ntok[s0 + i] + per - 1) / per;
+        p.src_off[i] = p.dst_off[i] = row0 * g.n_kv_heads * g.head_dim;
+        row0 += ntok[s0 + i];
+    }
+    p.block0[n] = p.nblocks;
+    return p.nblocks > 0;
+}
+
+// Largest split count whose clusters of one launch all fit on the device at
+// once, with at least a chunk for each warp.
+int choose_splits(int D, int HPC, bool multi, int groups, int keys) {
+    const int chunks = (keys + qa::kQ4Chunk - 1) / qa::kQ4Chunk;
+    int S = std::min(qa::kQ4MaxSplits, std::max(1, (chunks + qa::kQ4DecodeWarps - 1) / qa::kQ4DecodeWarps));
+    for (; S > 1; --S)
+        if (qa::q4_cluster_capacity(D, HPC, multi, S) >= groups) break;
+    return S;
+}
+
+struct DecodeCall {
+    const void *q, *k, *v, *wq, *wk;
+    void *out, *k_held, *v_held;
+    const int32_t *start;     // host positions (null: device positions)
+    const int32_t *pos_dev;
+    const int32_t *ntok;      // null: one token each
+};
+
+// The new tokens of a call (at most 8 per sequence), one decode launch per 64
+// sequences that have any.
+qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, int tmax, cudaStream_t s) {
+    const qa_config &g = c->cfg;
+    const int D = g.head_dim;
+    const bool multi = tmax > 1;
+    int HPC = c->G;
+    while (multi && HPC > 1 && qa::kQ4MaxTokens / HPC < tmax) HPC /= 2;
+    qa::Q4DecodeParams p{};
+    const int64_t row = layer * c->layer_rows;
+    p.kc = c->codes[0] + row * (D / 2);
+    p.vc = c->codes[1] + row * (D / 2);
+    p.ks = c->scales[0] + row * (D / qa::kQ4Group);
+    p.vs = c->scales[1] + row * (D / qa::kQ4Group);
+    p.q = static_cast<const __nv_bfloat16 *>(a.q);
+    p.k = static_cast<const __nv_bfloat16 *>(a.k);
+    p.v = static_cast<const __nv_bfloat16 *>(a.v);
+    p.wq = static_cast<const __nv_bfloat16 *>(a.wq);
+    p.wk = static_cast<const __nv_bfloat16 *>(a.wk);
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
+    p.k_held = static_cast<__nv_bfloat16 *>(a.k_held);
+    p.v_held = static_cast<__nv_bfloat16 *>(a.v_held);
+    p.rope = c->rope;
+    p.pos_dev = a.pos_dev;
+    p.err = c->err;
+    p.row_head = c->rows;
+    p.row_seq = static_cast<int64_t>(c->rows) * g.n_kv_heads;
+    p.Hq = g.n_q_heads;
+    p.Hkv = g.n_kv_heads;
+    p.G = c->G;
+    p.HG = c->G / HPC;
+    p.cap = g.capacity;
+    p.eps = g.rms_eps;
+    p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+    p.window = c->window[layer];
+
+    // Which cache rows may be read before the previous kernel has finished: all
+    // of them when no launch that may still run writes this layer; when this
+    // call continues every sequence where the last one left it, those below the
+    // rows such launches append; else none, and the launch signals the next one
+    // only after its own wait.
+    int32_t *next = next_of(c, layer);
+    const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
+    const bool settled = qa::launch_order().layer_settled(s, c, layer, resident);
+    bool follows = !a.pos_dev;
+    for (int b = 0; b < batch && follows; ++b)
+        if ((!a.ntok || a.ntok[b] > 0) && next[b] != a.start[b]) follows = false;
+
+    int b = 0, row0 = 0;
+    while (b < batch) {
+        p.b0 = b;
+        int nz = 0, keys = 0, tm = 0;
+        const int first = b;
+        for (; b < batch && nz < qa::kQ4MaxSeqPerLaunch; ++b) {
+            const int n = a.ntok ? a.ntok[b] : 1;
+            if (n > 0) {
+                p.seq[nz] = b;
+                p.ntok[nz] = n;
+                p.row0[nz] = row0;
+                p.pos[nz] = a.pos_dev ? 0 : a.start[b];
+                keys = std::max(keys, a.pos_dev ? g.capacity - 1 : static_cast<int>(a.start[b]));
+                tm = std::max(tm, n);
+                ++nz;
+            }
+            row0 += n;
+        }
+        if (nz == 0) break;
+        if (p.window > 0) keys = std::min(keys, p.window);
+        p.B = nz;
+        p.S = choose_splits(D, HPC, multi, nz * g.n_kv_heads * p.HG, keys);
+        p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
+        const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,
+                                                   p.early != 0, resident);
+        p.guard = settled ? 0 : guard;
+        if (qa::launch_q4_decode(p, D, HPC, multi, s) != cudaSuccess) {
+            cudaGetLastError();
+            return QA_ERR_CUDA;
+        }
+        c->launches[QA_Q4_KERNEL_DECODE]++;
+        for (int i = first; i < b; ++i) {
+            const int n = a.ntok ? a.ntok[i] : 1;
+            if (n > 0) next[i] = a.pos_dev ? -1 : a.start[i] + n;
+        }
+    }
+    return QA_OK;
+}
+
+// One launch group of a prefill: up to ws_slots sequences.
+struct PrefillGroup {
+    qa::K1Params k1;
+    qa::Q4RowsParams quant, held;
+    qa::K2Params k2;
+    int items;
+};
+
+// Builds the launches for sequences s0 .. s0 + n - 1; false when a tensor map
+// cannot be made.
+bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start, const int32_t *ntok,
+                  int64_t row0, const void *q, const void *k, const void *v, const void *wq,
+                  const void *wk, void *out, PrefillGroup &pg) {
+    const qa_config &g = c->cfg;
+    const int D = g.head_dim, Hq = g.n_q_heads, Hkv = g.n_kv_heads;
+    const int64_t ws_head = static_cast<int64_t>(g.capacity) * D, ws_seq = ws_head * Hkv;
+    qa::K1Params &k1 = pg.k1;
+    k1 = qa::K1Params{};
+    k1.q = static_cast<const __nv_bfloat16 *>(q) + row0 * Hq * D;
+    k1.k = static_cast<const __nv_bfloat16 *>(k) + row0 * Hkv * D;
+    k1.v = static_cast<const __nv_bfloat16 *>(v) + row0 * Hkv * D;
+    k1.wq = static_cast<const __nv_bfloat16 *>(wq);
+    k1.wk = static_cast<const __nv_bfloat16 *>(wk);
+    k1.qp = static_cast<__nv_bfloat16 *>(out) + row0 * Hq * D;
+    k1.kc = c->ws[0];
+    k1.vc = c->ws[1];
+    k1.lens = c->ws_lens;
+    k1.rope = c->rope;
+    k1.err = c->err;
+    k1.head_stride = ws_head;
+    k1.seq_stride = ws_seq;
+    k1.Hq = Hq;
+    k1.Hkv = Hkv;
+    k1.cap = g.capacity;
+    k1.eps = g.rms_eps;
+    k1.nseq = n;
+    // The new rows, quantised in place: the workspace then holds what the cache holds.
+    pg.quant = make_rows(c, layer);
+    fill_ranges(pg.quant, g, s0, n, start, ntok, 0);
+    // The rows before them that a new token sees, from the first row of the
+    // 128-key tile that holds the first one.
+    pg.held = make_rows(c, layer);
+    int32_t from[qa::kMaxSeqPerLaunch], count[qa::kMaxSeqPerLaunch];
+    for (int i = 0; i < n; ++i) {
+        const int P = start[s0 + i], W = c->window[layer];
+        from[i] = W > 0 ? std::max(0, P + 1 - W) / 128 * 128 : 0;
+        count[i] = ntok[s0 + i] > 0 ? P - from[i] : 0;
+    }
+    fill_ranges(pg.held, g, 0, n, from, count, 0);
+    pg.held.seq0 = s0;
+    for (qa::Q4RowsParams *r : {&pg.quant, &pg.held}) {
+        r->src_tok = r->dst_tok = D;
+        r->src_head = r->dst_head = ws_head;
+        for (int i = 0; i < 2; ++i) {
+            r->src[i] = c->ws[i];
+            r->dst[i] = c->ws[i];
+        }
+        for (int i = 0; i < n; ++i)
+            r->src_off[i] = r->dst_off[i] = i * ws_seq + static_cast<int64_t>(r->start[i]) * D;
+    }
+    qa::K2Params &k2 = pg.k2;
+    k2 = qa::K2Params{};
+    int nseq = 0, rows = 0, maxqb = 0;
+    pg.items = 0;
+    k1.cu[0] = 0;
+    for (int i = 0; i < n; ++i) {
+        const int L = ntok[s0 + i], P = start[s0 + i];
+        k1.cu[i + 1] = k1.cu[i] + L;
+        k1.start[i] = P;
+        if (L > 0) {
+            if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + i * ws_seq, D, P + L, Hkv, g.capacity, 64) ||
+                !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + i * ws_seq, D, P + L, Hkv, g.capacity, 128))
+                return false;
+            k2.len[nseq] = L;
+            k2.start[nseq] = P;
+            k2.cu[nseq] = rows;
+            maxqb = std::max(maxqb, (L + 127) / 128);
+            pg.items += (L + 127) / 128;
+            ++nseq;
+        }
+        rows += L;
+    }
+    k1.T = rows;
+    if (rows == 0) return true;
+    if (!qa::encode_q_map(&k2.tm_q, k1.qp, D, Hq, rows)) return false;
+    k2.out = k1.qp;
+    k2.err = c->err;
+    k2.nseq = nseq;
+    k2.Hq = Hq;
+    k2.Hkv = Hkv;
+    k2.G = c->G;
+    k2.npairs = (c->G + 1) / 2;
+    k2.max_qblocks = maxqb;
+    k2.window = c->window[layer];
+    k2.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
+    k2.wait_ns = qa::kWaitTimeoutNs;
+    pg.items *= Hkv * k2.npairs;
+    return true;
+}
+
+}  // namespace
+
+QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
+    if (!cfg || !out) return QA_ERR_INVALID_ARG;
+    *out = nullptr;
+    const qa_config g = *cfg;
+    if (g.num_layers <= 0 || g.max_batch <= 0 || g.capacity <= 0 || g.n_q_heads <= 0 ||
+        g.n_kv_heads <= 0 || g.head_dim <= 0 || !(g.rope_theta > 0.f) || !(g.rms_eps >= 0.f))
+        return QA_ERR_INVALID_ARG;
+    if (!qa::supported_geometry(g.n_q_heads, g.n_kv_heads, g.head_dim)) return QA_ERR_UNSUPPORTED_SHAPE;
+    if (g.capacity > (1 << 24) || g.max_batch > 65535 || g.n_q_heads > 65535) return QA_ERR_UNSUPPORTED_SHAPE;
+    qa_q4_cache *c = new (std::nothrow) qa_q4_cache();
+    if (!c) return QA_ERR_CUDA;
+    c->cfg = g;
+    for (auto &x : c->launches) x = 0;
+    c->G = g.n_q_heads / g.n_kv_heads;
+    c->rows = (g.capacity + qa::kQ4RowPad - 1) / qa::kQ4RowPad * qa::kQ4RowPad;
+    c->layer_rows = static_cast<int64_t>(g.max_batch) * g.n_kv_heads * c->rows;
+    c->ws_slots = std::min(g.max_batch, qa::kMaxSeqPerLaunch);
+    const size_t rows = static_cast<size_t>(c->layer_rows) * g.num_layers;
+    const size_t ws = static_cast<size_t>(c->ws_slots) * g.n_kv_heads * g.capacity * g.head_dim;
+    bool ok = cudaGetDevice(&c->device) == cudaSuccess &&
+              cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess;
+    for (int i = 0; ok && i < 2; ++i)
+        ok = dev_alloc(&c->codes[i], rows * (g.head_dim / 2), c->cache_bytes) &&
+             dev_alloc(&c->scales[i], rows * (g.head_dim / qa::kQ4Group), c->cache_bytes) &&
+             dev_alloc(&c->ws[i], ws, c->scratch_bytes);
+    ok = ok && dev_alloc(&c->ws_lens, qa::kMaxSeqPerLaunch, c->scratch_bytes) &&
+         dev_alloc(&c->rope, static_cast<size_t>(g.capacity) * (g.head_dim / 2), c->scratch_bytes) &&
+         dev_alloc(&c->err, 1, c->scratch_bytes) &&
+         cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) == cudaSuccess;
+    if (ok) {
+        std::vector<float2> tab(static_cast<size_t>(g.capacity) * (g.head_dim / 2));
+        qa::fill_rope_table(tab.data(), g.capacity, g.head_dim, g.rope_theta);
+        ok = cudaMemcpy(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
+             cudaDeviceSynchronize() == cudaSuccess;
+    }
+    if (!ok) {
+        free_all(c);
+        delete c;
+        cudaGetLastError();
+        return QA_ERR_CUDA;
+    }
+    c->window.assign(static_cast<size_t>(g.num_layers), 0);
+    c->next_pos.assign(static_cast<size_t>(g.num_layers) * g.max_batch, -1);
+    *out = c;
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_cache_free(qa_q4_cache *c) {
+    if (!c) return QA_OK;
+    DeviceScope dev(c->device);
+    cudaDeviceSynchronize();
+    qa::launch_order().clear();
+    free_all(c);
+    delete c;
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_cache_set_window(qa_q4_cache *c, int layer, int window) {
+    if (!c || layer < 0 || layer >= c->cfg.num_layers || window < 0) return QA_ERR_INVALID_ARG;
+    c->window[layer] = window;
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_append(qa_q4_cache *c, int layer, int batch, const int32_t *start,
+                              const int32_t *ntok, const void *k, const void *v, void *k_held,
+                              void *v_held, void *stream) {
+    qa_status st = check_layer(c, layer, batch);
+    if (st != QA_OK) return st;
+    int64_t T = 0;
+    st = check_ranges(c, batch, start, ntok, &T);
+    if (st != QA_OK) return st;
+    if ((k_held == nullptr) != (v_held == nullptr)) return QA_ERR_INVALID_ARG;
+    if (T == 0) return QA_OK;
+    if (!k || !v) return QA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_held) || !aligned16(v_held)) return QA_ERR_ALIGNMENT;
+    DeviceScope dev(c->device);
+    if (!dev.ok()) return QA_ERR_CUDA;
+    const qa_config &g = c->cfg;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    qa::Q4RowsParams p = make_rows(c, layer);
+    p.src[0] = static_cast<const __nv_bfloat16 *>(k);
+    p.src[1] = static_cast<const __nv_bfloat16 *>(v);
+    p.dst[0] = static_cast<__nv_bfloat16 *>(k_held);
+    p.dst[1] = static_cast<__nv_bfloat16 *>(v_held);
+    packed_rows(g, p.src_tok, p.src_head);
+    packed_rows(g, p.dst_tok, p.dst_head);
+    int32_t *next = next_of(c, layer);
+    int64_t row0 = 0;
+    for (int s0 = 0; s0 < batch; s0 += qa::kQ4MaxSeqPerLaunch) {
+        const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
+        if (fill_ranges(p, g, s0, n, start, ntok, row0)) {
+            if (qa::launch_q4_quantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            qa::launch_order().barrier(s);
+            c->launches[QA_Q4_KERNEL_QUANTISE]++;
+        }
+        for (int i = 0; i < n; ++i) {
+            row0 += ntok[s0 + i];
+            if (ntok[s0 + i] > 0) next[s0 + i] = start[s0 + i] + ntok[s0 + i];
+        }
+    }
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_read(qa_q4_cache *c, int layer, int batch, const int32_t *start,
+                            const int32_t *ntok, void *k_out, void *v_out, void *stream) {
+    qa_status st = check_layer(c, layer, batch);
+    if (st != QA_OK) return st;
+    int64_t T = 0;
+    st = check_ranges(c, batch, start, ntok, &T);
+    if (st != QA_OK) return st;
+    if (T == 0) return QA_OK;
+    if (!k_out && !v_out) return QA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return QA_ERR_ALIGNMENT;
+    DeviceScope dev(c->device);
+    if (!dev.ok()) return QA_ERR_CUDA;
+    const qa_config &g = c->cfg;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    qa::Q4RowsParams p = make_rows(c, layer);
+    p.dst[0] = static_cast<__nv_bfloat16 *>(k_out);
+    p.dst[1] = static_cast<__nv_bfloat16 *>(v_out);
+    p.kv_first = k_out ? 0 : 1;
+    p.kv_count = k_out && v_out ? 2 : 1;
+    packed_rows(g, p.dst_tok, p.dst_head);
+    int64_t row0 = 0;
+    for (int s0 = 0; s0 < batch; s0 += qa::kQ4MaxSeqPerLaunch) {
+        const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
+        if (fill_ranges(p, g, s0, n, start, ntok, row0)) {
+            if (qa::launch_q4_dequantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            qa::launch_order().barrier(s);
+            c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
+        }
+        for (int i = 0; i < n; ++i) row0 += ntok[s0 + i];
+    }
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32_t *start,
+                               const int32_t *ntok, const void *q, const void *k, const void *v,
+                               const void *q_norm_w, const void *k_norm_w, void *out, void *stream) {
+    qa_status st = check_layer(c, layer, batch);
+    if (st != QA_OK) return st;
+    int64_t T = 0;
+    st = check_ranges(c, batch, start, ntok, &T);
+    if (st != QA_OK) return st;
+    if (T == 0) return QA_OK;
+    if (!q || !k || !v || !q_norm_w || !k_norm_w || !out) return QA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_norm_w) ||
+        !aligned16(k_norm_w) || !aligned16(out))
+        return QA_ERR_ALIGNMENT;
+    DeviceScope dev(c->device);
+    if (!dev.ok()) return QA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int tmax = *std::max_element(ntok, ntok + batch);
+    if (tmax <= qa::kQ4MaxTokens) {
+        DecodeCall a{q, k, v, q_norm_w, k_norm_w, out, nullptr, nullptr, start, nullptr, ntok};
+        return run_decode(c, layer, batch, a, tmax, s);
+    }
+    // The longer form goes through the cache's one bf16 workspace: a graph could
+    // be replayed beside another call that uses it, so it is not captured, and
+    // calls on several streams take turns.
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
+        cudaGetLastError();
+        return QA_ERR_STATE;
+    }
+    std::vector<PrefillGroup> groups;
+    int64_t row0 = 0;
+    for (int s0 = 0; s0 < batch; s0 += c->ws_slots) {
+        const int n = std::min(c->ws_slots, batch - s0);
+        PrefillGroup pg;
+        if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
+            return QA_ERR_CUDA;
+        row0 += pg.k1.T;
+        if (pg.k1.T > 0) groups.push_back(pg);
+    }
+    if (cudaStreamWaitEvent(s, c->ws_free, 0) != cudaSuccess) return QA_ERR_CUDA;
+    int32_t *next = next_of(c, layer);
+    for (int b = 0; b < batch; ++b)
+        if (ntok[b] > 0) next[b] = start[b] + ntok[b];
+    for (PrefillGroup &pg : groups) {
+        if (qa::launch_k1(pg.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+        qa::launch_order().barrier(s);
+        c->launches[QA_Q4_KERNEL_NORM_ROPE]++;
+        if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+        c->launches[QA_Q4_KERNEL_QUANTISE]++;
+        if (pg.held.nblocks > 0) {
+            if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
+        }
+        if (qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s) != cudaSuccess) return QA_ERR_CUDA;
+        qa::launch_order().barrier(s);
+        c->launches[QA_Q4_KERNEL_PREFILL_ATTN]++;
+    }
+    return cudaEventRecord(c->ws_free, s) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
+}
+
+namespace {
+qa_status decode_step(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, void *stream) {
+    if (!a.q || !a.k || !a.v || !a.wq || !a.wk || !a.out) return QA_ERR_INVALID_ARG;
+    if ((a.k_held == nullptr) != (a.v_held == nullptr)) return QA_ERR_INVALID_ARG;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.wq) ||
+        !aligned16(a.wk) || !aligned16(a.out) || !aligned16(a.k_held) || !aligned16(a.v_held))
+        return QA_ERR_ALIGNMENT;
+    DeviceScope dev(c->device);
+    if (!dev.ok()) return QA_ERR_CUDA;
+    return run_decode(c, layer, batch, a, 1, static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+QA_API qa_status qa_q4_decode_step(qa_q4_cache *c, int layer, int batch, const int32_t *positions,
+                                   const void *q, const void *k, const void *v, const void *q_norm_w,
+                                   const void *k_norm_w, void *out, void *k_held, void *v_held,
+                                   void *stream) {
+    qa_status st = check_layer(c, layer, batch);
+    if (st != QA_OK) return st;
+    if (!positions) return QA_ERR_INVALID_ARG;
+    for (int b = 0; b < batch; ++b)
+        if (positions[b] < 0) return QA_ERR_INVALID_ARG;
+    for (int b = 0; b < batch; ++b)
+        if (positions[b] >= c->cfg.capacity) return QA_ERR_CAPACITY;
+    return decode_step(c, layer, batch,
+                       {q, k, v, q_norm_w, k_norm_w, out, k_held, v_held, positions, nullptr, nullptr}, stream);
+}
+
+QA_API qa_status qa_q4_decode_step_device_positions(qa_q4_cache *c, int layer, int batch,
+                                                    const int32_t *positions, const void *q,
+                                                    const void *k, const void *v, const void *q_norm_w,
+                                                    const void *k_norm_w, void *out, void *k_held,
+                                                    void *v_held, void *stream) {
+    qa_status st = check_layer(c, layer, batch);
+    if (st != QA_OK) return st;
+    if (!positions) return QA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(positions) & 3u) return QA_ERR_ALIGNMENT;
+    return decode_step(c, layer, batch,
+                       {q, k, v, q_norm_w, k_norm_w, out, k_held, v_held, nullptr, positions, nullptr}, stream);
+}
+
+QA_API qa_status qa_q4_cache_view(qa_q4_cache *c, int layer, void **k_codes, void **k_scales,
+                                  void **v_codes, void **v_scales, int64_t strides[3]) {
+    if (!c || layer < 0 || layer >= c->cfg.num_layers) return QA_ERR_INVALID_ARG;
+    const int64_t row = layer * c->layer_rows;
+    const int D = c->cfg.head_dim;
+    void **codes[2] = {k_codes, v_codes}, **scales[2] = {k_scales, v_scales};
+    for (int i = 0; i < 2; ++i) {
+        if (codes[i]) *codes[i] = c->codes[i] + row * (D / 2);
+        if (scales[i]) *scales[i] = c->scales[i] + row * (D / qa::kQ4Group);
+    }
+    if (strides) {
+        strides[2] = 1;
+        strides[1] = c->rows;
+        strides[0] = static_cast<int64_t>(c->rows) * c->cfg.n_kv_heads;
+    }
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_get_device_error(qa_q4_cache *c, uint32_t *detail) {
+    if (!c) return QA_ERR_INVALID_ARG;
+    DeviceScope dev(c->device);
+    uint32_t word = 0;
+    if (!dev.ok() || cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
+        cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
+        return QA_ERR_CUDA;
+    qa::launch_order().clear();
+    if (detail) *detail = word;
+    switch (word & 0xffu) {
+        case 0: return QA_OK;
+        case qa::kErrTimeout: return QA_ERR_DEVICE_TIMEOUT;
+        default: return QA_ERR_DEVICE_BOUNDS;
+    }
+}
+
+QA_API qa_status qa_q4_stats(qa_q4_cache *c, uint64_t launches[QA_Q4_NUM_KERNELS]) {
+    if (!c || !launches) return QA_ERR_INVALID_ARG;
+    for (int i = 0; i < QA_Q4_NUM_KERNELS; ++i) launches[i] = c->launches[i].load();
+    return QA_OK;
+}
+
+QA_API qa_status qa_q4_memory_info(qa_q4_cache *c, uint64_t *cache_bytes, uint64_t *scratch_bytes) {
+    if (!c) return QA_ERR_INVALID_ARG;
+    if (cache_bytes) *cache_bytes = c->cache_bytes;
+    if (scratch_bytes) *scratch_bytes = c->scratch_bytes;
+    return QA_OK;
+}

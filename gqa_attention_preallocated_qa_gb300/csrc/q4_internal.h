@@ -1,0 +1,91 @@
+// q4_internal.h -- definitions shared by the host side and the kernels of the
+// 4-bit key/value cache (parameter blocks, limits, launchers).  Not part of the
+// public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "launch_order.h"
+#include "qa_internal.h"
+
+namespace qa {
+
+// Kernel numbers in the error word of a 4-bit cache.
+constexpr uint32_t kKernQ4Rows = 4, kKernQ4Decode = 5;
+
+// Values of one row that share a scale.
+constexpr int kQ4Group = 32;
+// Rows of a (sequence, kv head) are padded to a multiple of this, so that the
+// decode kernel's bulk copies of whole chunks stay inside the allocation and
+// start on 16-byte boundaries.
+constexpr int kQ4RowPad = 64;
+
+// Sequences carried in the parameters of one launch.
+constexpr int kQ4MaxSeqPerLaunch = 64;
+
+// The row kernels (quantise, dequantise) work on tokens start[b] .. start[b] +
+// ntok[b] - 1 of each launched sequence.  A row of 16-bit values is addressed
+// by (sequence, token of the call, kv head): base + off[b] + token * tok +
+// head * head_stride, in elements, which covers packed [T][Hkv][D] rows as well
+// as a layer laid out [sequence][head][position][D].
+struct Q4RowsParams {
+    uint8_t *codes[2], *scales[2];       // layer base of K and V
+    const __nv_bfloat16 *src[2];         // quantise: the rows of K and V
+    __nv_bfloat16 *dst[2];               // the rows' values as the cache holds them (may be null)
+    int64_t src_tok, src_head, dst_tok, dst_head;
+    int64_t row_seq, row_head;           // cache strides in rows: sequence, head
+    int nseq, Hkv, nblocks, kv_first, kv_count;  // kv_first/count: K (0) and V (1) served
+    int seq0;                            // cache slot of launched sequence 0
+    int start[kQ4MaxSeqPerLaunch], ntok[kQ4MaxSeqPerLaunch];
+    int block0[kQ4MaxSeqPerLaunch + 1];  // first token block of each launched sequence
+    int64_t src_off[kQ4MaxSeqPerLaunch], dst_off[kQ4MaxSeqPerLaunch];
+};
+static_assert(sizeof(Q4RowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
+
+// Tokens of one head that one warp quantises or dequantises.
+__host__ __device__ constexpr int q4_block_tokens(int D) { return D == 128 ? 16 : 32; }
+
+constexpr int kQ4Chunk = 32;       // keys of one pipeline chunk of the decode kernel
+constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
+constexpr int kQ4MaxSplits = 16;   // splits of one (sequence, kv head) = CTAs of one cluster
+constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode launch
+
+struct Q4DecodeParams {
+    uint8_t *kc, *ks, *vc, *vs;          // layer base: codes and scale bytes of K and V
+    const __nv_bfloat16 *q, *k, *v;      // packed rows of the new tokens
+    const __nv_bfloat16 *wq, *wk;        // [D]
+    __nv_bfloat16 *out;
+    __nv_bfloat16 *k_held, *v_held;      // the new rows as the cache holds them (may be null)
+    const float2 *rope;                  // [cap][D/2] (cos, sin)
+    const int32_t *pos_dev;              // device positions (null: pos[])
+    uint32_t *err;
+    int64_t row_seq, row_head;           // cache strides in rows
+    int B, Hq, Hkv, G, HG, cap, S;
+    float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
+    int window;                          // attention window in keys (0: all earlier keys)
+    int guard;                           // rows below each first new slot that a running launch may write
+    int early;                           // 1: signal the next launch at once, 0: after the wait
+    int b0;                              // first sequence of the call in pos_dev
+    int pos[kQ4MaxSeqPerLaunch];         // slot of each launched sequence's first new token
+    int seq[kQ4MaxSeqPerLaunch];         // its cache slot
+    int ntok[kQ4MaxSeqPerLaunch];        // its new tokens
+    int row0[kQ4MaxSeqPerLaunch];        // its first row in q, k, v, out
+};
+static_assert(sizeof(Q4DecodeParams) <= 4096, "travels in the 4 KB of kernel parameters");
+
+cudaError_t launch_q4_quantise(const Q4RowsParams &p, int D, cudaStream_t stream);
+cudaError_t launch_q4_dequantise(const Q4RowsParams &p, int D, cudaStream_t stream);
+// HPC heads x TPS tokens per CTA (TPS = 1, or 8 / HPC for launches of several tokens).
+cudaError_t launch_q4_decode(const Q4DecodeParams &p, int D, int HPC, bool multi, cudaStream_t stream);
+// Clusters of S decode CTAs resident at once on the current device (cached); 0 on error.
+int q4_cluster_capacity(int D, int HPC, bool multi, int S);
+
+// Shared with the bf16 cache's host side.
+bool encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, int box_rows);
+bool encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T);
+bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);
+LaunchOrder &launch_order();
+// Rotary table [capacity][D/2] of (cos, sin), in fp64, stored as fp32.
+void fill_rope_table(float2 *tab, int capacity, int D, float theta);
+
+}  // namespace qa

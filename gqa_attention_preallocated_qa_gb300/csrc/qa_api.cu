@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "launch_order.h"
+#include "q4_internal.h"
 #include "qa.h"
 #include "qa_internal.h"
 
@@ -82,10 +83,7 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool supported_shape(const qa_config &c) {
-    if (c.head_dim != 64 && c.head_dim != 128) return false;
-    if (c.n_kv_heads <= 0 || c.n_q_heads <= 0 || c.n_q_heads % c.n_kv_heads) return false;
-    const int G = c.n_q_heads / c.n_kv_heads;
-    return G == 1 || G == 2 || G == 4 || G == 8;
+    return qa::supported_geometry(c.n_q_heads, c.n_kv_heads, c.head_dim);
 }
 
 void free_all(qa_cache *c) {
@@ -115,11 +113,13 @@ qa_status check_layer(const qa_cache *c, int layer, int batch) {
     return QA_OK;
 }
 
+}  // namespace
+
 // Per-sequence K (or V) tensor map over one layer's cache: (D, L, Hkv) with the
 // head stride of the cache, 64 x box_rows x 1 boxes, 128-byte swizzle; rows at
 // or beyond L read as zero.  K uses 64-row boxes (the CTA-pair prefill loads
 // half a key tile per CTA), V 128-row boxes.
-bool encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, int box_rows) {
+bool qa::encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, int box_rows) {
     auto enc = get_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(L),
@@ -134,7 +134,7 @@ bool encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, i
 }
 
 // Query tensor map over q' rows: (D, Hq, T) with 64 x 1 x 128 boxes.
-bool encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T) {
+bool qa::encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T) {
     auto enc = get_encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
@@ -148,7 +148,24 @@ bool encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
+qa::LaunchOrder &qa::launch_order() { return g_order; }
+
+bool qa::supported_geometry(int n_q_heads, int n_kv_heads, int head_dim) {
+    if (head_dim != 64 && head_dim != 128) return false;
+    if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads) return false;
+    const int G = n_q_heads / n_kv_heads;
+    return G == 1 || G == 2 || G == 4 || G == 8;
+}
+
+// angle = pos * theta^(-2i/D)
+void qa::fill_rope_table(float2 *tab, int capacity, int D, float theta) {
+    for (int pos = 0; pos < capacity; ++pos)
+        for (int i = 0; i < D / 2; ++i) {
+            const double a = static_cast<double>(pos) * std::pow(static_cast<double>(theta), -2.0 * i / D);
+            tab[static_cast<size_t>(pos) * (D / 2) + i] =
+                make_float2(static_cast<float>(std::cos(a)), static_cast<float>(std::sin(a)));
+        }
+}
 
 qa::FaultPlan qa::take_fault(int kernel) {
     FaultPlan f;
@@ -417,8 +434,8 @@ qa_status plan_k2(qa_cache *c, int layer, int batch, const int32_t *lens, const 
                                     static_cast<int64_t>(s0 + i) * g.n_kv_heads * g.capacity * D;
                 __nv_bfloat16 *vb = c->V + layer * c->layer_elems +
                                     static_cast<int64_t>(s0 + i) * g.n_kv_heads * g.capacity * D;
-                if (!encode_kv_map(&p.tm_k[nseq], kb, D, P + L, g.n_kv_heads, g.capacity, 64) ||
-                    !encode_kv_map(&p.tm_v[nseq], vb, D, P + L, g.n_kv_heads, g.capacity, 128))
+                if (!qa::encode_kv_map(&p.tm_k[nseq], kb, D, P + L, g.n_kv_heads, g.capacity, 64) ||
+                    !qa::encode_kv_map(&p.tm_v[nseq], vb, D, P + L, g.n_kv_heads, g.capacity, 128))
                     return QA_ERR_CUDA;
                 p.len[nseq] = L;
                 p.start[nseq] = P;
@@ -429,7 +446,7 @@ qa_status plan_k2(qa_cache *c, int layer, int batch, const int32_t *lens, const 
             rows += L;
         }
         if (nseq > 0) {
-            if (!encode_q_map(&p.tm_q,
+            if (!qa::encode_q_map(&p.tm_q,
                               const_cast<__nv_bfloat16 *>(static_cast<const __nv_bfloat16 *>(qprime)) +
                                   row0 * g.n_q_heads * D,
                               D, g.n_q_heads, rows))
@@ -522,15 +539,9 @@ QA_API qa_status qa_cache_alloc(const qa_config *cfg, qa_cache **out) {
               dev_alloc(&c->err, 1, scr) &&
               dev_alloc(&c->seq_cnt, static_cast<size_t>(g.max_batch), scr);
     if (ok) {
-        // Rotary table in fp64, stored as fp32 (cos, sin): angle = pos * theta^(-2i/D).
+        // Rotary table in fp64, stored as fp32 (cos, sin).
         std::vector<float2> tab(static_cast<size_t>(g.capacity) * (D / 2));
-        for (int pos = 0; pos < g.capacity; ++pos)
-            for (int i = 0; i < D / 2; ++i) {
-                const double a = static_cast<double>(pos) *
-                                 std::pow(static_cast<double>(g.rope_theta), -2.0 * i / D);
-                tab[static_cast<size_t>(pos) * (D / 2) + i] =
-                    make_float2(static_cast<float>(std::cos(a)), static_cast<float>(std::sin(a)));
-            }
+        qa::fill_rope_table(tab.data(), g.capacity, D, g.rope_theta);
         ok = cudaMemcpy(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) ==
                  cudaSuccess;
     }

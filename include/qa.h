@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define QA_ABI_VERSION 4
+#define QA_ABI_VERSION 5
 
 typedef enum {
     QA_OK = 0,
@@ -48,7 +48,7 @@ typedef enum {
     QA_ERR_UNSUPPORTED_SHAPE = 2,  /* head_dim not in {64,128}, Hq % Hkv != 0, group > 8 ... */
     QA_ERR_ALIGNMENT = 3,          /* a tensor pointer is not 16-byte aligned */
     QA_ERR_CAPACITY = 4,           /* a sequence would exceed the cache capacity (no eviction) */
-    QA_ERR_STATE = 5,              /* reserved (no current entry point returns it) */
+    QA_ERR_STATE = 5,              /* the stream is being captured, and the call cannot be (qa_q4_prefill) */
     QA_ERR_CUDA = 6,               /* a CUDA runtime call failed (no device, launch error ...) */
     QA_ERR_DEVICE_TIMEOUT = 7,     /* a kernel gave up a bounded wait (reported by qa_get_device_error) */
     QA_ERR_DEVICE_BOUNDS = 8       /* a kernel saw a position outside the cache (qa_get_device_error) */
@@ -351,6 +351,135 @@ qa_status qa_decode_step_noalloc(const qa_config *cfg, int batch, const int32_t 
  * nothing: a 4-byte copy into host memory and a 4-byte memset.
  * Errors: CUDA. */
 qa_status qa_noalloc_get_device_error(uint32_t *detail, void *stream);
+
+/* ---- 4-bit cache ----------------------------------------------------------
+ * A key/value cache whose rows are held in 4 bits a value and one scale byte
+ * per 32 values: 4.25 bits instead of 16, so a decode step reads 3.76 times
+ * fewer bytes.  (The pages have no counterpart.)
+ *
+ * Format.  A row (one position of one kv head) is cut into groups of 32
+ * consecutive dimensions.  A group stands for the values (n - 8) * s, n its
+ * codes in 0..15 and s the fp16 number whose upper byte is the group's scale
+ * byte (5 exponent bits, 2 mantissa bits).  Quantising a row x, per group:
+ * s is max|x| / 7 rounded to the nearest such number (ties to the even byte),
+ * at most 56; n - 8 is x / s rounded to the nearest integer, halves away from
+ * zero, held to -8..7; n = 8 where s = 0.  So magnitudes up to 392 keep the
+ * full resolution, larger ones are held to 392 (448 below zero), and a group
+ * whose largest magnitude is at most 7 * 2^-17 becomes zero (below 7 * 2^-14
+ * the scale has fewer bits).  A group with a value that is not finite gets
+ * scale byte 0x7f, which reads as NaN throughout.  Every value has at most 7
+ * significant bits: bf16 holds it exactly, and a row that is read back is
+ * exactly what attention saw.  Byte i of a row's codes holds dimension 2i in
+ * its low four bits and 2i + 1 in its high four.
+ *
+ * The caller keeps the lengths: every call names the positions it is about
+ * (HOST arrays, which travel in the launch parameters), so that a speculative
+ * token is dropped by writing its position again.  A call reads only positions
+ * below the ones it writes; rows that nothing wrote may hold anything.
+ *
+ * Conventions as above.  Calls may be made with another device current; the
+ * stream belongs to the cache's device.  Row kernels and prefill are ordered
+ * on their stream like plain launches; decode steps overlap the previous
+ * kernel like qa_decode_step, with the same condition on q, k, v and the
+ * weights, and on other code's kernels between the calls. */
+typedef struct qa_q4_cache qa_q4_cache; /* opaque */
+
+/* Kernels counted by qa_q4_stats. */
+enum {
+    QA_Q4_KERNEL_NORM_ROPE = 0,    /* K1, writing a prefill's rows to the workspace */
+    QA_Q4_KERNEL_QUANTISE = 1,     /* K4: rows into the cache */
+    QA_Q4_KERNEL_DEQUANTISE = 2,   /* K4: rows out of the cache */
+    QA_Q4_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace */
+    QA_Q4_KERNEL_DECODE = 4,       /* K5: decode steps and chunks of up to 8 tokens */
+    QA_Q4_NUM_KERNELS = 5
+};
+
+/* Allocate a 4-bit cache on the current device, with the geometry that
+ * qa_cache_alloc takes: codes [num_layers][max_batch][n_kv_heads][rows][D/2]
+ * and scale bytes [...][rows][D/32] for K and for V (zero-filled; rows is the
+ * capacity, rounded up to a multiple of 64), the rotary table, an error word,
+ * and one bf16 workspace for prefill attention: K and V of min(max_batch, 8)
+ * sequences of one layer, [slot][n_kv_heads][capacity][D].  Synchronous.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out);
+
+/* Free it.  Synchronises the device first.  NULL is accepted and ignored. */
+qa_status qa_q4_cache_free(qa_q4_cache *cache);
+
+/* Attention window of one layer, as qa_cache_set_window. */
+qa_status qa_q4_cache_set_window(qa_q4_cache *cache, int layer, int window);
+
+/* Quantise rows as they are (keys already normed and rotated) into positions
+ * start[b] .. start[b] + ntok[b] - 1 of sequences 0..batch-1.
+ * k, v: [T][Hkv][D] packed in sequence order, T = sum of ntok.
+ * k_held, v_held: both NULL, or [T][Hkv][D] that receive the values the cache
+ * now holds (they may be k and v themselves).
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY. */
+qa_status qa_q4_append(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
+                       const int32_t *ntok, const void *k, const void *v, void *k_held,
+                       void *v_held, void *stream);
+
+/* Read the same ranges back as bf16 rows [T][Hkv][D].  k_out or v_out may be
+ * NULL (that tensor is not read), not both.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY. */
+qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
+                     const int32_t *ntok, void *k_out, void *v_out, void *stream);
+
+/* Whole prompts (start 0) or the next chunk of them: the ntok[b] new tokens of
+ * sequence b take positions start[b] ..; the cache holds the earlier ones.
+ * Tensors as qa_prefill: q [T][Hq][D], k, v [T][Hkv][D], weights [D], out
+ * [T][Hq][D] (it stages the queries: no alias of q, k, v).
+ * Result: RoPE(RMSNorm(k)) and v are quantised into their positions, and every
+ * new token attends causally to what the cache then holds (its own rows as
+ * held, too), within the layer's window.
+ * With every ntok at most 8 the decode kernel does all of it, one launch per
+ * 64 sequences.  Otherwise K1, K4 and K2 run through the cache's workspace, 8
+ * sequences at a time: such calls on several streams wait for each other, and
+ * they cannot be captured into a graph (QA_ERR_STATE).
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
+qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
+                        const int32_t *ntok, const void *q, const void *k, const void *v,
+                        const void *q_norm_w, const void *k_norm_w, void *out, void *stream);
+
+/* One decode step: one new token for each of sequences 0..batch-1 at
+ * positions[b] (HOST), which attends to positions 0..positions[b], within the
+ * layer's window.  Tensors as qa_decode_step; out must not alias q, k or v.
+ * k_held, v_held: both NULL, or [batch][Hkv][D] that receive the new rows as
+ * the cache holds them.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (a position at or above the
+ * capacity), CUDA. */
+qa_status qa_q4_decode_step(qa_q4_cache *cache, int layer, int batch, const int32_t *positions,
+                            const void *q, const void *k, const void *v, const void *q_norm_w,
+                            const void *k_norm_w, void *out, void *k_held, void *v_held,
+                            void *stream);
+
+/* The same with positions in DEVICE memory (int32 [batch]), read when the
+ * previous kernel on the stream has finished: for graph capture, where the
+ * caller advances them inside the graph.  A position outside 0..capacity-1
+ * leaves its sequence alone and sets QA_ERR_DEVICE_BOUNDS
+ * (qa_q4_get_device_error).  The split count is planned for a full cache.
+ * Capture requires one earlier call of this shape outside capture. */
+qa_status qa_q4_decode_step_device_positions(qa_q4_cache *cache, int layer, int batch,
+                                             const int32_t *positions, const void *q, const void *k,
+                                             const void *v, const void *q_norm_w,
+                                             const void *k_norm_w, void *out, void *k_held,
+                                             void *v_held, void *stream);
+
+/* Device pointers of one layer's codes and scale bytes, and the strides of
+ * (sequence, kv head, position) in rows: a row is D/2 bytes of codes and D/32
+ * scale bytes.  Any output pointer may be NULL. */
+qa_status qa_q4_cache_view(qa_q4_cache *cache, int layer, void **k_codes, void **k_scales,
+                           void **v_codes, void **v_scales, int64_t strides[3]);
+
+/* As qa_get_device_error. */
+qa_status qa_q4_get_device_error(qa_q4_cache *cache, uint32_t *detail);
+
+/* Successful launches per kernel (QA_Q4_KERNEL_*). */
+qa_status qa_q4_stats(qa_q4_cache *cache, uint64_t launches[QA_Q4_NUM_KERNELS]);
+
+/* Device bytes: codes and scale bytes, and scratch (workspace, rotary table,
+ * error word). */
+qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t *scratch_bytes);
 
 /* Static description of a status code. */
 const char *qa_status_str(qa_status status);
