@@ -107,12 +107,19 @@ __device__ __forceinline__ Q4Scale q4_scale2(uint32_t pair) {
     r.hi = __hmul2(r.s, __float2half2_rn(-1152.f));
     return r;
 }
+// (w & mask) | 1024.0 in both halves, as one three-input operation.
+template <uint32_t kMaskBits>
+__device__ __forceinline__ uint32_t q4_field(uint32_t w) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "n"(kMaskBits), "r"(0x64006400u));
+    return y;
+}
 // Codes in bits 0-3 / 4-7 of each half of w (the latter come out 16 times larger).
 __device__ __forceinline__ uint32_t q4_lo(uint32_t w, const Q4Scale &s) {
-    return hfma2_u((w & 0x000F000Fu) | 0x64006400u, s.s, s.lo);
+    return hfma2_u(q4_field<0x000F000Fu>(w), s.s, s.lo);
 }
 __device__ __forceinline__ uint32_t q4_hi(uint32_t w, const Q4Scale &s) {
-    return hfma2_u((w & 0x00F000F0u) | 0x64006400u, s.s, s.hi);
+    return hfma2_u(q4_field<0x00F000F0u>(w), s.s, s.hi);
 }
 
 // Physical row of index i (0..7) of an 8-key block: odd pairs are swapped, so
@@ -152,18 +159,25 @@ __device__ __forceinline__ uint4 q4_norm_rope(const __nv_bfloat16 *src, const __
 }
 
 // Running state of a warp: query rows 2c and 2c + 1 (c = lane % 4) of the MMA's
-// columns; o[t] holds dims (d, d + 1) of both rows for this lane's tile t.
+// columns; o[t] holds dims (d, d + 1) of both rows for this lane's tile t (the
+// odd ones 16 times larger).  Weights are p = 2^(t - ref): ref follows the
+// largest score only when a weight would pass 2^15, so it lies between 12
+// below the largest score so far and 3 more; fp16 then keeps weights down to
+// 2^-26 of the largest with all their bits, and a chunk costs no reduction
+// across lanes and no rescaling unless the largest score grew by 2^3.
 template <int D>
 struct Q4Acc {
-    float m[2], l[2];
+    float ref[2], l[2];
     float o[D / 16][4];
 };
+constexpr float kQ4Lift = 12.f, kQ4Most = 15.f;
+constexpr float kQ4NoRef = -1e30f;  // no key yet: any score is too large for it
 
 // One chunk of 32 keys at shared address `st` (K codes, V codes, K scales, V
-// scales).  Keys [klo[x], nk) are seen by row 2c + x; [kvlo, nk) by any row;
-// partial: some key of the chunk is not seen by some row.
-template <int D, int R>
-__device__ __forceinline__ void q4_consume(const uint8_t *st, bool partial, int nk, const int (&klo)[2], int kvlo,
+// scales).  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
+// row; else every row sees all 32.
+template <int D, int R, bool kMask>
+__device__ __forceinline__ void q4_consume(const uint8_t *st, int nk, const int (&klo)[2], int kvlo,
                                            const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
                                            Q4Acc<D> &a, int lane) {
     using Sh = Q4Shape<D, R>;
@@ -202,46 +216,61 @@ __device__ __forceinline__ void q4_consume(const uint8_t *st, bool partial, int 
                     qb[2 * w + 1][0], qb[2 * w + 1][1]);
         }
     }
-    // Scores in units of log2, masked; online softmax.  P is held 2^12 times
-    // larger, so that fp16 keeps weights down to 2^-26 of the largest with all
-    // its bits; l carries the same factor.
-    constexpr float kLift = 12.f;
-    float mx[2] = {-INFINITY, -INFINITY};
+    // s becomes the exponents t - ref, in units of log2.
+    if (kMask) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = mt * 16 + (e >> 1) * 8 + kr;
+                if (key >= nk || key < klo[e & 1]) s[mt][e] = -INFINITY;
+            }
+    }
+    auto exponent = [&](float x, int e) {
+        // (-inf times the factor 0 of a padding row would be NaN)
+        return kMask && x == -INFINITY ? x : fmaf(x, cs[e & 1], -a.ref[e & 1]);
+    };
+    float u[2][4];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float t = s[mt][e] * cs[e & 1];
-            if (partial) {
-                const int key = mt * 16 + (e >> 1) * 8 + kr;
-                if (key >= nk || key < klo[e & 1]) t = -INFINITY;
+        for (int e = 0; e < 4; ++e) u[mt][e] = exponent(s[mt][e], e);
+    float top = u[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, u[i >> 2][i & 3]);
+    if (__any_sync(FULL, top > kQ4Most)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = s[i >> 1][2 * (i & 1) + x];
+                mx = q4_max(mx, kMask && v == -INFINITY ? v : v * cs[x]);
             }
-            s[mt][e] = t;
-            mx[e & 1] = q4_max(mx[e & 1], t);
+            mx = q4_max(mx, __shfl_xor_sync(FULL, mx, 4));
+            mx = q4_max(mx, __shfl_xor_sync(FULL, mx, 8));
+            mx = q4_max(mx, __shfl_xor_sync(FULL, mx, 16));
+            const float ref = q4_max(a.ref[x] + kQ4Lift, mx) - kQ4Lift;
+            const float alpha = q4_ex2(a.ref[x] - ref);  // 0 from kQ4NoRef
+            a.ref[x] = ref;
+            a.l[x] *= alpha;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                a.o[t][x] *= alpha;
+                a.o[t][2 + x] *= alpha;
+            }
         }
-    float neg[2], alpha[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 4));
-        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 8));
-        mx[x] = q4_max(mx[x], __shfl_xor_sync(FULL, mx[x], 16));
-        const float mn = q4_max(a.m[x], mx[x]);
-        alpha[x] = a.m[x] == -INFINITY ? 0.f : q4_ex2(a.m[x] - mn);
-        neg[x] = mn == -INFINITY ? 0.f : mn - kLift;  // a row that has seen no key: p = 0
-        a.m[x] = mn;
-        a.l[x] *= alpha[x];
-    }
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-        a.o[t][0] *= alpha[0]; a.o[t][1] *= alpha[1];
-        a.o[t][2] *= alpha[0]; a.o[t][3] *= alpha[1];
+            for (int e = 0; e < 4; ++e) u[mt][e] = exponent(s[mt][e], e);
     }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            p[e] = q4_ex2(s[ks][e] - neg[e & 1]);
+            p[e] = q4_ex2(u[ks][e]);
             a.l[e & 1] += p[e];
         }
         const uint32_t b0 = transpose8x8(pack_f16(p[0], p[1]));
@@ -251,7 +280,7 @@ __device__ __forceinline__ void q4_consume(const uint8_t *st, bool partial, int 
         const int g = D == 128 ? r >> 1 : r >> 2;
         uint32_t ba = ssv[ka * Sh::kScaleRow + g], bb = ssv[kb * Sh::kScaleRow + g];
         uint32_t bc = ssv[(ka + 8) * Sh::kScaleRow + g], bd = ssv[(kb + 8) * Sh::kScaleRow + g];
-        if (partial) {  // rows that no query row sees may hold anything: a zero scale drops them
+        if (kMask) {  // rows that no query row sees may hold anything: a zero scale drops them
             if (ka >= nk || ka < kvlo) ba = 0;
             if (kb >= nk || kb < kvlo) bb = 0;
             if (ka + 8 >= nk || ka + 8 < kvlo) bc = 0;
@@ -525,7 +554,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             const int t = TPS == 1 ? 0 : col / HPC;
             cs[x] = col < R && t < ntok ? s_c[col] : 0.f;
             row_lo[x] = p.window > 0 ? max(0, pos + t + 1 - p.window) : 0;
-            a.m[x] = -INFINITY;
+            a.ref[x] = kQ4NoRef;
             a.l[x] = 0.f;
         }
 #pragma unroll
@@ -554,13 +583,18 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             const int base = c * kQ4Chunk;
-            const int klo[2] = {min(kQ4Chunk, max(0, row_lo[0] - base)), min(kQ4Chunk, max(0, row_lo[1] - base))};
-            const bool partial = pos - base < kQ4Chunk || (p.window > 0 && pos + ntok - p.window > base);
-            q4_consume<D, R>(ring + st * Sh::kStage, partial, min(kQ4Chunk, pos - base), klo,
-                             max(0, key_lo - base), qb, cs, a, lane);
-            // The warp's reads of the stage come before the next copy into it.
-            fence_proxy_async_smem();
-            __syncwarp();
+            // Every row sees the whole chunk unless it holds the end or the window's start.
+            const bool whole = base + kQ4Chunk <= pos && (p.window <= 0 || base >= pos + ntok - p.window);
+            const uint8_t *stage = ring + st * Sh::kStage;
+            if (whole) {
+                const int none[2] = {0, 0};
+                q4_consume<D, R, false>(stage, kQ4Chunk, none, 0, qb, cs, a, lane);
+            } else {
+                const int klo[2] = {min(kQ4Chunk, max(0, row_lo[0] - base)), min(kQ4Chunk, max(0, row_lo[1] - base))};
+                q4_consume<D, R, true>(stage, min(kQ4Chunk, pos - base), klo, max(0, key_lo - base),
+                                       qb, cs, a, lane);
+            }
+            __syncwarp();  // the warp's reads of the stage come before the next copy into it
             const int cn = c + NW * NS;
             if (lane == 0 && cn < c_end && issued == i + NS) {
                 if (!waited && cn >= c_safe) {
@@ -599,8 +633,9 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 for (int t = 0; t < D / 16; ++t)
                     *reinterpret_cast<float2 *>(part + col * D + r * (D / 8) + 2 * t) =
                         make_float2(a.o[t][x], a.o[t][2 + x] * 0.0625f);
-                if (r == 0) {
-                    part[R * D + 2 * col] = a.m[x];
+                if (r == 0) {  // a NaN score leaves ref alone: its row is NaN whatever the other warps hold
+                    const float m = a.l[x] != a.l[x] ? a.l[x] : a.ref[x] + kQ4Lift;
+                    part[R * D + 2 * col] = a.ref[x] == kQ4NoRef && a.l[x] == 0.f ? -INFINITY : m;
                     part[R * D + 2 * col + 1] = a.l[x];
                 }
             }
@@ -633,13 +668,11 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             float w[NW + 1], M;
             weights(g, w, M);
             float2 O = make_float2(0.f, 0.f);
-            if (w[NW] != 0.f) O = make_float2(w[NW] * part_new[g * D + d], w[NW] * part_new[g * D + d + 1]);
+            if (owner) O = make_float2(w[NW] * part_new[g * D + d], w[NW] * part_new[g * D + d + 1]);
 #pragma unroll
             for (int i = 0; i < NW; ++i) {
-                if (w[i] != 0.f) {
-                    const float2 x = *reinterpret_cast<const float2 *>(red + i * kWF + g * D + d);
-                    O = make_float2(fmaf(w[i], x.x, O.x), fmaf(w[i], x.y, O.y));
-                }
+                const float2 x = *reinterpret_cast<const float2 *>(red + i * kWF + g * D + d);
+                O = make_float2(fmaf(w[i], x.x, O.x), fmaf(w[i], x.y, O.y));
             }
             const int dst = e / E;
             st_async_f32x2(map_rank(a_o + 4u * (e - dst * E), dst), O.x, O.y, map_rank(a_bar, dst));
@@ -650,10 +683,10 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             if (lo < hi && lo < (g + 1) * D && hi > g * D) {
                 float w[NW + 1], M, L = 0.f;
                 weights(g, w, M);
-                if (w[NW] != 0.f) L = w[NW] * part_new[R * D + 2 * g + 1];
+                if (owner) L = w[NW] * part_new[R * D + 2 * g + 1];
 #pragma unroll
                 for (int i = 0; i < NW; ++i)
-                    if (w[i] != 0.f) L = fmaf(w[i], red[i * kWF + R * D + 2 * g + 1], L);
+                    L = fmaf(w[i], red[i * kWF + R * D + 2 * g + 1], L);
                 st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L,
                                map_rank(a_bar, dst));
             }
@@ -683,7 +716,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 if (lane < S) {
                     const float w = mi == -INFINITY ? 0.f : q4_ex2(mi - M);
                     s_w[hl * kQ4MaxSplits + lane] = w;
-                    Ls = w == 0.f ? 0.f : w * ml[2 * R * lane + 1];
+                    Ls = w * ml[2 * R * lane + 1];
                 }
 #pragma unroll
                 for (int o = 16; o >= 1; o >>= 1) Ls += __shfl_xor_sync(FULL, Ls, o);
@@ -698,8 +731,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                     const int g = (e_lo + k) / D, hl = g - g_lo;
                     float O = 0.f;
                     for (int i = 0; i < S; ++i) {
-                        const float w = s_w[hl * kQ4MaxSplits + i];
-                        if (w != 0.f) O = fmaf(w, rcv_o[i * E + k], O);
+                        O = fmaf(s_w[hl * kQ4MaxSplits + i], rcv_o[i * E + k], O);
                     }
                     res[j] = O * s_linv[hl];
                 }
