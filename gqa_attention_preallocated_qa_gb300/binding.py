@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -74,12 +75,12 @@ SIGNATURES = {
     "qa_q4_cache_alloc": (ctypes.c_int, [ctypes.POINTER(qa_config), ctypes.POINTER(_vp)]),
     "qa_q4_cache_free": (ctypes.c_int, [_vp]),
     "qa_q4_cache_set_window": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int]),
-    "qa_q4_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
+    "qa_q4_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
                                     _vp, _vp]),
-    "qa_q4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp]),
-    "qa_q4_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
+    "qa_q4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp]),
+    "qa_q4_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _vp, _vp, _vp]),
-    "qa_q4_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp,
+    "qa_q4_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
                                          _vp, _vp, _vp, _vp, _vp, _vp]),
     "qa_q4_decode_step_device_positions": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp,
                                                           _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -289,16 +290,48 @@ def cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
     return kt, vt, lt
 
 
-# ---- 4-bit cache: host position lists may be lists or ready ctypes int32 arrays
+# ---- 4-bit cache.  Position lists are sequences of ints, or ready ctypes int32
+# arrays.  These calls are made once per layer and token, so their wrappers
+# look nothing up that they can keep.
+
+_PACK = [struct.Struct(f"{n}i") for n in range(257)]
+
+
+def _i32_bytes(values):
+    if isinstance(values, ctypes.Array):
+        return values
+    n = len(values)
+    return (_PACK[n] if n <= 256 else struct.Struct(f"{n}i")).pack(*values)
+
 
 def _ranges(start, ntok):
     if len(start) != len(ntok):
         raise ValueError("start and ntok need one entry per sequence")
-    return len(start), _i32_of(start), _i32_of(ntok)
+    return len(start), _i32_bytes(start), _i32_bytes(ntok)
 
 
-def _i32_of(values):
-    return values if isinstance(values, ctypes.Array) else _i32(values)
+def _q4_stream(s):
+    if s is None:
+        if _raw_stream is None:
+            _find_raw_stream()
+        return _raw_stream(_current_device())
+    return s if isinstance(s, int) else s.cuda_stream
+
+
+_raw_stream = _current_device = None
+
+
+def _find_raw_stream():
+    """torch's current stream as a handle, without building its Stream object."""
+    global _raw_stream, _current_device
+    import torch
+    if torch.cuda.is_available():
+        torch.cuda.init()
+        _current_device = torch.cuda.current_device
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    else:
+        _current_device, _raw_stream = (lambda: 0), (lambda device: None)
 
 
 def qa_q4_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
@@ -321,12 +354,12 @@ def qa_q4_cache_set_window(cache, layer, window) -> None:
 def qa_q4_append(cache, layer, start, ntok, k, v, k_held=None, v_held=None, stream=None) -> None:
     n, s, t = _ranges(start, ntok)
     _check(lib.qa_q4_append(cache, layer, n, s, t, _ptr(k), _ptr(v), _ptr(k_held), _ptr(v_held),
-                            _stream(stream)), "qa_q4_append")
+                            _q4_stream(stream)), "qa_q4_append")
 
 
 def qa_q4_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
     n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_read(cache, layer, n, s, t, _ptr(k_out), _ptr(v_out), _stream(stream)),
+    _check(lib.qa_q4_read(cache, layer, n, s, t, _ptr(k_out), _ptr(v_out), _q4_stream(stream)),
            "qa_q4_read")
 
 
@@ -334,14 +367,14 @@ def qa_q4_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
                   stream=None) -> None:
     n, s, t = _ranges(start, ntok)
     _check(lib.qa_q4_prefill(cache, layer, n, s, t, _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
-                             _ptr(k_norm_w), _ptr(out), _stream(stream)), "qa_q4_prefill")
+                             _ptr(k_norm_w), _ptr(out), _q4_stream(stream)), "qa_q4_prefill")
 
 
 def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
                       v_held=None, stream=None) -> None:
-    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_of(positions), _ptr(q), _ptr(k),
+    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_bytes(positions), _ptr(q), _ptr(k),
                                  _ptr(v), _ptr(q_norm_w), _ptr(k_norm_w), _ptr(out), _ptr(k_held),
-                                 _ptr(v_held), _stream(stream)), "qa_q4_decode_step")
+                                 _ptr(v_held), _q4_stream(stream)), "qa_q4_decode_step")
 
 
 def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
@@ -349,7 +382,7 @@ def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, 
     """positions: int32 device tensor [batch] (see include/qa.h)."""
     _check(lib.qa_q4_decode_step_device_positions(
         cache, layer, batch, _ptr(positions), _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
-        _ptr(k_norm_w), _ptr(out), _ptr(k_held), _ptr(v_held), _stream(stream)),
+        _ptr(k_norm_w), _ptr(out), _ptr(k_held), _ptr(v_held), _q4_stream(stream)),
            "qa_q4_decode_step_device_positions")
 
 

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(256) q4_quantise_kernel(const __grid_constant_
     uint32_t mine = 0;
 #pragma unroll
     for (int u = 0; u < kQ4Unroll; ++u) {
+        if (u >= t.n) break;  // no lane group has a row u
         const int i = half * kQ4Unroll + u;
         uint32_t byte;
         uint4 held;

@@ -127,16 +127,19 @@ __device__ __forceinline__ uint32_t q4_hi(uint32_t w, const Q4Scale &s) {
 // shared-memory banks.
 __device__ __forceinline__ int q4_key(int i) { return i ^ ((i >> 1) & 1); }
 
-// RMSNorm + RoPE of one head row over D/8 lanes, with the roundings of the
-// bf16 path; cs: (cos_a, sin_a, cos_b, sin_b) of this lane's 8 dims.
+// A head row on D/8 lanes: 8 values, weights and (cos_a, sin_a, cos_b, sin_b) of
+// the lane's dims; for a new token its v as well.
+struct Q4Row {
+    uint4 x, w, v;
+    float4 cs[4];
+};
+
+// RMSNorm + RoPE of a row, with the roundings of the bf16 path.
 template <int D>
-__device__ __forceinline__ uint4 q4_norm_rope(const __nv_bfloat16 *src, const __nv_bfloat16 *w,
-                                              const float4 (&cs)[4], float eps, int sub) {
+__device__ __forceinline__ uint4 q4_norm_rope(const Q4Row &row, float eps, int sub) {
     constexpr int HALF = D / 16;
     const unsigned FULL = 0xffffffffu;
-    const uint4 xv = __ldg(reinterpret_cast<const uint4 *>(src) + sub);
-    const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(w) + sub);
-    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    const uint32_t xw[4] = {row.x.x, row.x.y, row.x.z, row.x.w}, ww[4] = {row.w.x, row.w.y, row.w.z, row.w.w};
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) ss = fmaf(bf16lo(xw[e]), bf16lo(xw[e]), fmaf(bf16hi(xw[e]), bf16hi(xw[e]), ss));
@@ -153,8 +156,8 @@ __device__ __forceinline__ uint4 q4_norm_rope(const __nv_bfloat16 *src, const __
     const float sgn = sub < HALF ? -1.f : 1.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        ow[e] = pack_bf16(fmaf(sgn * cs[e].y, bf16lo(pw[e]), bf16lo(yw[e]) * cs[e].x),
-                          fmaf(sgn * cs[e].w, bf16hi(pw[e]), bf16hi(yw[e]) * cs[e].z));
+        ow[e] = pack_bf16(fmaf(sgn * row.cs[e].y, bf16lo(pw[e]), bf16lo(yw[e]) * row.cs[e].x),
+                          fmaf(sgn * row.cs[e].w, bf16hi(pw[e]), bf16hi(yw[e]) * row.cs[e].z));
     return make_uint4(ow[0], ow[1], ow[2], ow[3]);
 }
 
@@ -332,7 +335,6 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     __shared__ int s_abort;
     __shared__ __align__(16) __nv_bfloat16 s_newk[TPS * D], s_newv[TPS * D];  // as the cache holds them
     __shared__ float s_c[R];                                    // log2 units per raw score of a row
-    __shared__ float s_w[R * kQ4MaxSplits], s_linv[R];
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -342,22 +344,21 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.S, split = blockIdx.x;
-    const int kvh = blockIdx.y / p.HG, hg = blockIdx.y % p.HG;
-    const int z = blockIdx.z;
-    const int ntok = TPS == 1 ? 1 : p.ntok[z];
-    const int64_t row_base = static_cast<int64_t>(p.seq[z]) * p.row_seq + kvh * p.row_head;
+    const int kvh = p.HG == 1 ? blockIdx.y : blockIdx.y / p.HG, hg = blockIdx.y - kvh * p.HG;
+    const Q4Seq seq = p.seq[blockIdx.z];
+    const int ntok = TPS == 1 ? 1 : seq.ntok;
+    const int64_t row_base = static_cast<int64_t>(seq.slot) * p.row_seq + kvh * p.row_head;
     const int h_first = kvh * p.G + hg * HPC;
     const bool owner = split == S - 1;
     const bool dev = p.pos_dev != nullptr;
-    int pos = dev ? 0 : p.pos[z];
+    int pos = dev ? 0 : seq.pos;
 
     // Merge geometry: the CTA's R x D outputs are dealt to the cluster's CTAs in runs of E.
     constexpr int total = R * D;
-    const int E = ((total + S - 1) / S + 7) & ~7;
+    const int E = p.E;
     const int e_lo = split * E;
     const int E_me = max(0, min(E, total - e_lo));
-    const int g_lo = e_lo / D;
-    const int nh_me = E_me > 0 ? (e_lo + E_me - 1) / D - g_lo + 1 : 0;
+    const int nh_me = E_me > 0 ? (e_lo + E_me - 1) / D - e_lo / D + 1 : 0;
     float *rcv_o = recv, *rcv_ml = recv + S * E;
 
     bool pos_ok = false;
@@ -367,33 +368,74 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const int nchunks = pos_ok ? (pos + kQ4Chunk - 1) / kQ4Chunk : 0;
         key_lo = (pos_ok && p.window > 0) ? max(0, pos + 1 - p.window) : 0;
         const int c_lo = min(key_lo / kQ4Chunk, nchunks);
-        const int64_t n = nchunks - c_lo;
-        c_begin = c_lo + static_cast<int>(split * n / S);
-        c_end = c_lo + static_cast<int>((split + 1) * n / S);
+        // (at most 2^19 chunks and 16 splits)
+        const uint32_t n = nchunks - c_lo;
+        c_begin = c_lo + split * n / S;
+        c_end = c_lo + (split + 1) * n / S;
         c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
     };
-    if (!dev) plan();
 
+    // The rows to prepare: query rows 0..R-1, then (on the last split) the new
+    // tokens; warp w takes items NW-1-w and 2NW-1-w.
+    const int sub = lane % LPR;
+    const int nitems = R + (owner ? ntok : 0);
+    auto load_item = [&](int it, Q4Row &row) {
+        const int t = it < R ? it / HPC : it - R;
+        if (it >= nitems || t >= ntok) return;
+        const __nv_bfloat16 *x, *w;
+        if (it < R) {
+            x = p.q + (static_cast<int64_t>(seq.row0 + t) * p.Hq + h_first + it % HPC) * D;
+            w = p.wq;
+        } else {
+            const int64_t kr = (static_cast<int64_t>(seq.row0 + t) * p.Hkv + kvh) * D;
+            x = p.k + kr;
+            w = p.wk;
+            row.v = __ldg(reinterpret_cast<const uint4 *>(p.v + kr) + sub);
+        }
+        row.x = __ldg(reinterpret_cast<const uint4 *>(x) + sub);
+        row.w = __ldg(reinterpret_cast<const uint4 *>(w) + sub);
+        const float4 *tab = reinterpret_cast<const float4 *>(
+            p.rope + static_cast<int64_t>(pos + t) * (D / 2) + 8 * (sub % (LPR / 2)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row.cs[e] = __ldg(tab + e);
+    };
+
+    // Chunks of this warp: c_begin + warp + NW * i, in stage i % NS of its ring;
+    // `issued` of them are on the way.  Lanes 0-3 copy one run each: the codes of
+    // K and of V, the scale bytes of K and of V.
     uint8_t *ring = smem + warp * Sh::kWarpRing;
     const uint32_t bar0 = smem_u32(&bar_ring[warp * NS]);
-    auto issue = [&](int c, int st) {  // lane 0 of the warp
-        const uint32_t bar = bar0 + 8 * st, dst = smem_u32(ring + st * Sh::kStage);
-        const int64_t row = row_base + static_cast<int64_t>(c) * kQ4Chunk;
-        mbar_expect_tx(bar, Sh::kStage);
-        bulk_g2s(dst, p.kc + row * Sh::kRow, Sh::kCodes, bar);
-        bulk_g2s(dst + Sh::kCodes, p.vc + row * Sh::kRow, Sh::kCodes, bar);
-        bulk_g2s(dst + 2 * Sh::kCodes, p.ks + row * Sh::kScaleRow, Sh::kScales, bar);
-        bulk_g2s(dst + 2 * Sh::kCodes + Sh::kScales, p.vs + row * Sh::kScaleRow, Sh::kScales, bar);
-    };
-    // Chunks of this warp: c_begin + warp + NW * i; `issued` of them are on the way.
     int issued = 0;
-    auto fill = [&](int limit) {  // lane 0: the first round, below chunk `limit`
+    const int run = lane & 3;
+    const uint32_t run_row = run < 2 ? Sh::kRow : Sh::kScaleRow;  // bytes of a row in the run
+    const uint8_t *run_base = run == 0 ? p.kc : run == 1 ? p.vc : run == 2 ? p.ks : p.vs;
+    const uint32_t run_dst = smem_u32(ring) + (run < 2 ? run * Sh::kCodes : 2 * Sh::kCodes + (run - 2) * Sh::kScales);
+    auto issue = [&](int c, int st) {
+        if (lane == 0) mbar_expect_tx(bar0 + 8 * st, Sh::kStage);
+        __syncwarp();
+        if (lane < 4)
+            bulk_g2s(run_dst + st * Sh::kStage,
+                     run_base + (row_base + static_cast<int64_t>(c) * kQ4Chunk) * run_row,
+                     kQ4Chunk * run_row, bar0 + 8 * st);
+    };
+    auto fill = [&](int limit) {  // the first round, below chunk `limit`
         for (; issued < NS; ++issued) {
             const int c = c_begin + warp + NW * issued;
             if (c >= c_end || c >= limit) break;
             issue(c, issued);
         }
     };
+
+    // Programmatic dependent launch: with `early` the inputs and the cache rows
+    // that no running launch writes are read before the previous kernel's end
+    // and the next launch may start now; else everything follows the wait.
+    const bool early = !dev && p.early;
+    if (!early) griddep_wait();
+    griddep_launch_dependents();
+    if (dev) pos = p.pos_dev[seq.slot];
+    plan();
+    Q4Row row;
+    if (pos_ok) load_item(NW - 1 - warp, row);
     if (lane == 0) {
         for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1);
         if (warp == 0) {
@@ -402,24 +444,10 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             if (E_me > 0) mbar_expect_tx(smem_u32(&bar_recv), S * (E_me * 4 + nh_me * 8));
         }
         fence_mbar_init();
-        if (!dev) fill(c_safe);
     }
     __syncwarp();
+    fill(early ? c_safe : c_end);
     cluster_arrive();  // peers may push into this CTA once they have waited on this
-
-    // Programmatic dependent launch.  Cache rows that no running launch writes
-    // are loaded before the wait; with `early` the next launch may start now.
-    if (!dev && p.early) {
-        griddep_launch_dependents();
-    } else {
-        griddep_wait();
-        griddep_launch_dependents();
-        if (dev) {
-            pos = p.pos_dev[p.b0 + z];
-            plan();
-        }
-        if (lane == 0) fill(c_end);
-    }
     if (!pos_ok) {
         if (threadIdx.x == 0) set_error(p.err, kErrBounds, kKernQ4Decode, 1);
         cluster_wait();
@@ -428,23 +456,14 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     }
 
     // ---------------------------------------------------------------- query rows and new tokens
-    const int sub = lane % LPR;
-    uint32_t new_codes[2];  // of the item below, when it is a new token
-    uint32_t new_byte[2];
+    uint32_t new_codes[2], new_byte[2];  // of the warp's new token, if it has one
     uint4 new_held[2];
-    const int nitems = R + (owner ? ntok : 0);
     for (int it = NW - 1 - warp; it < nitems; it += NW) {  // warp-uniform
         const int t = it < R ? it / HPC : it - R;
         if (t >= ntok) continue;
-        float4 cs[4];
-        const float4 *tab = reinterpret_cast<const float4 *>(
-            p.rope + static_cast<int64_t>(pos + t) * (D / 2) + 8 * (sub % (LPR / 2)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) cs[e] = __ldg(tab + e);
+        if (it >= NW) load_item(it, row);
+        const uint4 x = q4_norm_rope<D>(row, p.eps, sub);
         if (it < R) {
-            const uint4 x = q4_norm_rope<D>(
-                p.q + (static_cast<int64_t>(p.row0[z] + t) * p.Hq + h_first + it % HPC) * D, p.wq, cs,
-                p.eps, sub);
             // fp16 with one power of two per row: the largest magnitude goes to
             // [256, 512), so bf16's 8 bits survive down to 2^-22 of it.
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
@@ -467,11 +486,8 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 if (lane == 0) s_c[it] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex - 8) << 23);
             }
         } else {
-            const int64_t kr = (static_cast<int64_t>(p.row0[z] + t) * p.Hkv + kvh) * D;
-            const uint4 kp = q4_norm_rope<D>(p.k + kr, p.wk, cs, p.eps, sub);
-            const uint4 vv = __ldg(reinterpret_cast<const uint4 *>(p.v + kr) + sub);
-            new_codes[0] = q4_quantise8<true>(kp, new_byte[0], new_held[0]);
-            new_codes[1] = q4_quantise8<true>(vv, new_byte[1], new_held[1]);
+            new_codes[0] = q4_quantise8<true>(x, new_byte[0], new_held[0]);
+            new_codes[1] = q4_quantise8<true>(row.v, new_byte[1], new_held[1]);
             if (lane < LPR) {
                 reinterpret_cast<uint4 *>(s_newk + t * D)[sub] = new_held[0];
                 reinterpret_cast<uint4 *>(s_newv + t * D)[sub] = new_held[1];
@@ -562,22 +578,17 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) a.o[t][e] = 0.f;
 
-        bool waited = !(!dev && p.early);
+        bool waited = !early;
         int st = 0;
         uint32_t phase = 0;
         int i = 0;
         for (int c = c_begin + warp; c < c_end; c += NW, ++i) {
-            if (lane == 0 && issued == i) {  // not sent ahead: the chunk holds rows being written
+            if (issued == i) {  // not sent ahead: the chunk holds rows being written
                 if (!waited) {
                     griddep_wait();
                     waited = true;
                 }
-                for (int n = 0; n < NS; ++n) {
-                    const int cn = c + NW * n;
-                    if (cn >= c_end) break;
-                    issue(cn, (i + n) % NS);
-                    ++issued;
-                }
+                for (int n = 0; n < NS && c + NW * n < c_end; ++n, ++issued) issue(c + NW * n, (i + n) % NS);
             }
             bool ok = mbar_wait(bar0 + 8 * st, phase, &s_abort, p.err, kKernQ4Decode, 2);
             ok = __all_sync(FULL, ok);
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             }
             __syncwarp();  // the warp's reads of the stage come before the next copy into it
             const int cn = c + NW * NS;
-            if (lane == 0 && cn < c_end && issued == i + NS) {
+            if (cn < c_end && issued == i + NS) {
                 if (!waited && cn >= c_safe) {
                     griddep_wait();
                     waited = true;
@@ -706,34 +717,21 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         }
         merged = __syncthreads_and(ok);
         if (merged) {
-            for (int hl = warp; hl < nh_me; hl += NW) {
-                const float *ml = rcv_ml + 2 * (g_lo + hl);
-                const float mi = lane < S ? ml[2 * R * lane] : -INFINITY;
-                float M = mi;
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) M = q4_max(M, __shfl_xor_sync(FULL, M, o));
-                float Ls = 0.f;
-                if (lane < S) {
-                    const float w = mi == -INFINITY ? 0.f : q4_ex2(mi - M);
-                    s_w[hl * kQ4MaxSplits + lane] = w;
-                    Ls = w * ml[2 * R * lane + 1];
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) Ls += __shfl_xor_sync(FULL, Ls, o);
-                if (lane == 0) s_linv[hl] = 1.f / Ls;
-            }
-            __syncthreads();
 #pragma unroll
             for (int j = 0; j < kOutPer; ++j) {
                 const int k = threadIdx.x + j * kThreads;
                 res[j] = 0.f;
                 if (k < E_me) {
-                    const int g = (e_lo + k) / D, hl = g - g_lo;
-                    float O = 0.f;
+                    const float2 *ml = reinterpret_cast<const float2 *>(rcv_ml) + (e_lo + k) / D;
+                    float M = -INFINITY, L = 0.f, O = 0.f;
+                    for (int i = 0; i < S; ++i) M = q4_max(M, ml[R * i].x);
                     for (int i = 0; i < S; ++i) {
-                        O = fmaf(s_w[hl * kQ4MaxSplits + i], rcv_o[i * E + k], O);
+                        const float2 x = ml[R * i];
+                        const float w = x.x == -INFINITY ? 0.f : q4_ex2(x.x - M);
+                        L = fmaf(w, x.y, L);
+                        O = fmaf(w, rcv_o[i * E + k], O);
                     }
-                    res[j] = O * s_linv[hl];
+                    res[j] = O / L;
                 }
             }
         }
@@ -752,7 +750,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 p.vs[row * Sh::kScaleRow + sub / 4] = static_cast<uint8_t>(new_byte[1]);
             }
             if (p.k_held) {
-                const int64_t kr = (static_cast<int64_t>(p.row0[z] + t) * p.Hkv + kvh) * D;
+                const int64_t kr = (static_cast<int64_t>(seq.row0 + t) * p.Hkv + kvh) * D;
                 reinterpret_cast<uint4 *>(p.k_held + kr)[sub] = new_held[0];
                 reinterpret_cast<uint4 *>(p.v_held + kr)[sub] = new_held[1];
             }
@@ -766,7 +764,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             const int e = e_lo + k, g = e / D, d = e % D;
             const int t = g / HPC, hh = g % HPC;
             if (t < ntok)
-                p.out[(static_cast<int64_t>(p.row0[z] + t) * p.Hq + h_first + hh) * D + d] =
+                p.out[(static_cast<int64_t>(seq.row0 + t) * p.Hq + h_first + hh) * D + d] =
                     __float2bfloat16_rn(res[j]);
         }
     }

@@ -219,16 +219,12 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
 
     int b = 0, row0 = 0;
     while (b < batch) {
-        p.b0 = b;
         int nz = 0, keys = 0, tm = 0;
         const int first = b;
         for (; b < batch && nz < qa::kQ4MaxSeqPerLaunch; ++b) {
             const int n = a.ntok ? a.ntok[b] : 1;
             if (n > 0) {
-                p.seq[nz] = b;
-                p.ntok[nz] = n;
-                p.row0[nz] = row0;
-                p.pos[nz] = a.pos_dev ? 0 : a.start[b];
+                p.seq[nz] = {a.pos_dev ? 0 : a.start[b], b, n, row0};
                 keys = std::max(keys, a.pos_dev ? g.capacity - 1 : static_cast<int>(a.start[b]));
                 tm = std::max(tm, n);
                 ++nz;
@@ -239,6 +235,8 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         if (p.window > 0) keys = std::min(keys, p.window);
         p.B = nz;
         p.S = choose_splits(D, HPC, multi, nz * g.n_kv_heads * p.HG, keys);
+        const int rows = multi ? qa::kQ4MaxTokens : HPC;
+        p.E = ((rows * D + p.S - 1) / p.S + 7) & ~7;
         p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
         const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,
                                                    p.early != 0, resident);

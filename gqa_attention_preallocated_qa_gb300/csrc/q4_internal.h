@@ -50,6 +50,12 @@ constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
 constexpr int kQ4MaxSplits = 16;   // splits of one (sequence, kv head) = CTAs of one cluster
 constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode launch
 
+// A launched sequence: the slot of its first new token, its place in the cache,
+// its new tokens and the first of their rows in q, k, v and out.
+struct alignas(16) Q4Seq {
+    int pos, slot, ntok, row0;
+};
+
 struct Q4DecodeParams {
     uint8_t *kc, *ks, *vc, *vs;          // layer base: codes and scale bytes of K and V
     const __nv_bfloat16 *q, *k, *v;      // packed rows of the new tokens
@@ -61,15 +67,12 @@ struct Q4DecodeParams {
     uint32_t *err;
     int64_t row_seq, row_head;           // cache strides in rows
     int B, Hq, Hkv, G, HG, cap, S;
+    int E;                               // outputs merged by one CTA of a cluster (a multiple of 8)
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
     int window;                          // attention window in keys (0: all earlier keys)
     int guard;                           // rows below each first new slot that a running launch may write
     int early;                           // 1: signal the next launch at once, 0: after the wait
-    int b0;                              // first sequence of the call in pos_dev
-    int pos[kQ4MaxSeqPerLaunch];         // slot of each launched sequence's first new token
-    int seq[kQ4MaxSeqPerLaunch];         // its cache slot
-    int ntok[kQ4MaxSeqPerLaunch];        // its new tokens
-    int row0[kQ4MaxSeqPerLaunch];        // its first row in q, k, v, out
+    Q4Seq seq[kQ4MaxSeqPerLaunch];       // the launched sequences
 };
 static_assert(sizeof(Q4DecodeParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
