@@ -5,10 +5,11 @@
 // (s per group of 32 values):
 //   t_j = q' . K_j * log2(e) / sqrt(D),  p_j = 2^(t_j - m),  out = sum p_j V_j / sum p_j.
 // Per (sequence, kv head, head group, split) CTA:
-//   1. every warp streams its own chunks of 32 keys (codes and scale bytes of K
-//      and V: four contiguous runs, 4352 bytes at D = 128) through its own ring
-//      in shared memory, filled by bulk copies that its lane 0 issues: no warp
-//      waits for another inside the loop;
+//   1. the CTA streams its keys through a ring of stages in shared memory, 256
+//      keys each (32 per warp): a stage is four contiguous runs of the cache
+//      (codes and scale bytes of K and V, 34 KB at D = 128), one bulk copy each.
+//      The warps take turns at sending a stage out again, one iteration after
+//      its use, so none waits for the others in the ordinary case;
 //   2. the CTA's query rows (HPC heads x TPS tokens, at most 8) are normed,
 //      rotated and brought to fp16 with one power of two per row; the last
 //      split's CTA quantises the new tokens' k' and v, writes them to the cache
@@ -47,22 +48,39 @@ constexpr int q4_recv_floats(int total, int rows) {
 template <int D, int R>
 struct Q4Shape {
     static constexpr int kRow = D / 2, kScaleRow = D / kQ4Group;  // bytes of a row
-    static constexpr int kCodes = kQ4Chunk * kRow;                // of a chunk of K (or V)
-    static constexpr int kScales = kQ4Chunk * kScaleRow;
+    static constexpr int kKeys = kQ4DecodeWarps * kQ4Chunk;       // of a stage: one chunk per warp
+    static constexpr int kCodes = kKeys * kRow;                   // bytes of a stage's K (or V) codes
+    static constexpr int kScales = kKeys * kScaleRow;
     static constexpr int kStage = 2 * (kCodes + kScales);
-    // Ring stages per warp: as many as let two CTAs share an SM.
+    // Ring stages: as many as let two CTAs share an SM.
     static constexpr int kStages = D == 128 && R == 8 ? 2 : 3;
-    static constexpr int kWarpRing = kStages * kStage;
-    static constexpr int kRing = kQ4DecodeWarps * kWarpRing;
+    static constexpr int kRing = kStages * kStage;
     static constexpr int kPartial = R * (D + 2);                  // floats: o [R][D], (m, l) [R][2]
     static constexpr int kRecv = q4_recv_floats(R * D, R);
     static constexpr int kQBytes = R * D * 2;
     static constexpr int kSmemUsed = 128 + kRing + kQBytes + (kPartial + kRecv) * 4;
     // Two CTAs per SM at most (the launch record counts on it: see k3_max_resident_ctas).
     static constexpr int kSmemBytes = kSmemUsed > 80 * 1024 ? kSmemUsed : 80 * 1024;
-    static_assert(kPartial * 4 <= kWarpRing, "a warp's partial fits its ring");
-    static_assert(kStage % 16 == 0 && kScales % 16 == 0, "bulk copies are 16-byte multiples");
+    static_assert(kQ4DecodeWarps * kPartial * 4 <= kRing, "the warps' partials fit the ring");
+    static_assert(kScales % 128 == 0 && kScaleRow * kQ4Chunk % 16 == 0, "bulk copies are 16-byte multiples");
 };
+
+// Waits with their slow part out of line (a launch meets its code cold).
+__device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
+                                          uint32_t site) {
+    return mbar_wait(bar, parity, abort, err, kKernQ4Decode, site);
+}
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
+                                        uint32_t site) {
+    return mbar_try_wait(bar, parity) || q4_wait_slow(bar, parity, abort, err, site);
+}
+__device__ __noinline__ bool q4_wait_cluster(uint32_t bar, volatile int *abort, uint32_t *err) {
+    if (mbar_wait_cluster(bar, 0, abort, err, kKernQ4Decode, 4)) return true;
+    // Given up: the peers still push here, and their stores land before this CTA exits.
+    int dummy = 0;
+    mbar_wait_cluster(bar, 0, &dummy, err, kKernQ4Decode, 5);
+    return false;
+}
 
 // Larger of the two; NaN if either is (a NaN score makes its row NaN).
 __device__ __forceinline__ float q4_max(float a, float b) {
@@ -176,18 +194,16 @@ struct Q4Acc {
 constexpr float kQ4Lift = 12.f, kQ4Most = 15.f;
 constexpr float kQ4NoRef = -1e30f;  // no key yet: any score is too large for it
 
-// One chunk of 32 keys at shared address `st` (K codes, V codes, K scales, V
-// scales).  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
+// One chunk of 32 keys: codes sk, sv and scale bytes ssk, ssv.  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
 // row; else every row sees all 32.
 template <int D, int R, bool kMask>
-__device__ __forceinline__ void q4_consume(const uint8_t *st, int nk, const int (&klo)[2], int kvlo,
+__device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv, const uint8_t *ssk,
+                                           const uint8_t *ssv, int nk, const int (&klo)[2], int kvlo,
                                            const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
                                            Q4Acc<D> &a, int lane) {
     using Sh = Q4Shape<D, R>;
     const unsigned FULL = 0xffffffffu;
     const int r = lane >> 2, c = lane & 3;
-    const uint8_t *sk = st, *sv = st + Sh::kCodes;
-    const uint8_t *ssk = st + 2 * Sh::kCodes, *ssv = ssk + Sh::kScales;
     const int kr = q4_key(r);
     float s[2][4];
 #pragma unroll
@@ -331,10 +347,10 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     const unsigned FULL = 0xffffffffu;
 
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_ring[NW * NS], bar_recv;
+    __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_recv;
     __shared__ int s_abort;
     __shared__ __align__(16) __nv_bfloat16 s_newk[TPS * D], s_newv[TPS * D];  // as the cache holds them
-    __shared__ float s_c[R];                                    // log2 units per raw score of a row
+    __shared__ float s_c[R];  // log2 units per raw score of a row
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -351,29 +367,25 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     const int h_first = kvh * p.G + hg * HPC;
     const bool owner = split == S - 1;
     const bool dev = p.pos_dev != nullptr;
-    int pos = dev ? 0 : seq.pos;
 
-    // Merge geometry: the CTA's R x D outputs are dealt to the cluster's CTAs in runs of E.
-    constexpr int total = R * D;
-    const int E = p.E;
-    const int e_lo = split * E;
-    const int E_me = max(0, min(E, total - e_lo));
-    const int nh_me = E_me > 0 ? (e_lo + E_me - 1) / D - e_lo / D + 1 : 0;
-    float *rcv_o = recv, *rcv_ml = recv + S * E;
+    // Programmatic dependent launch: with `early` the inputs and the cache rows
+    // that no running launch writes are read before the previous kernel's end
+    // and the next launch may start now; else everything follows the wait.
+    const bool early = !dev && p.early;
+    if (!early) griddep_wait();
+    griddep_launch_dependents();
+    const int pos = dev ? p.pos_dev[seq.slot] : seq.pos;
 
-    bool pos_ok = false;
-    int c_begin = 0, c_end = 0, c_safe = 0, key_lo = 0;
-    auto plan = [&]() {
-        pos_ok = pos >= 0 && ntok >= 1 && ntok <= TPS && pos + ntok <= p.cap;
-        const int nchunks = pos_ok ? (pos + kQ4Chunk - 1) / kQ4Chunk : 0;
-        key_lo = (pos_ok && p.window > 0) ? max(0, pos + 1 - p.window) : 0;
-        const int c_lo = min(key_lo / kQ4Chunk, nchunks);
-        // (at most 2^19 chunks and 16 splits)
-        const uint32_t n = nchunks - c_lo;
-        c_begin = c_lo + split * n / S;
-        c_end = c_lo + (split + 1) * n / S;
-        c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
-    };
+    // The split's chunks [c_begin, c_end), in stages of NW chunks, one per warp.
+    const bool pos_ok = pos >= 0 && ntok >= 1 && ntok <= TPS && pos + ntok <= p.cap;
+    const int nchunks = pos_ok ? (pos + kQ4Chunk - 1) / kQ4Chunk : 0;
+    const int key_lo = (pos_ok && p.window > 0) ? max(0, pos + 1 - p.window) : 0;
+    const int c_lo = min(key_lo / kQ4Chunk, nchunks);
+    // (at most 2^19 chunks and 16 splits)
+    const int c_begin = c_lo + static_cast<uint32_t>(split) * (nchunks - c_lo) / static_cast<uint32_t>(S);
+    const int c_end = c_lo + static_cast<uint32_t>(split + 1) * (nchunks - c_lo) / static_cast<uint32_t>(S);
+    const int c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
+    const int nstages = (c_end - c_begin + NW - 1) / NW;
 
     // The rows to prepare: query rows 0..R-1, then (on the last split) the new
     // tokens; warp w takes items NW-1-w and 2NW-1-w.
@@ -399,54 +411,43 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) row.cs[e] = __ldg(tab + e);
     };
-
-    // Chunks of this warp: c_begin + warp + NW * i, in stage i % NS of its ring;
-    // `issued` of them are on the way.  Lanes 0-3 copy one run each: the codes of
-    // K and of V, the scale bytes of K and of V.
-    uint8_t *ring = smem + warp * Sh::kWarpRing;
-    const uint32_t bar0 = smem_u32(&bar_ring[warp * NS]);
-    int issued = 0;
-    const int run = lane & 3;
-    const uint32_t run_row = run < 2 ? Sh::kRow : Sh::kScaleRow;  // bytes of a row in the run
-    const uint8_t *run_base = run == 0 ? p.kc : run == 1 ? p.vc : run == 2 ? p.ks : p.vs;
-    const uint32_t run_dst = smem_u32(ring) + (run < 2 ? run * Sh::kCodes : 2 * Sh::kCodes + (run - 2) * Sh::kScales);
-    auto issue = [&](int c, int st) {
-        if (lane == 0) mbar_expect_tx(bar0 + 8 * st, Sh::kStage);
-        __syncwarp();
-        if (lane < 4)
-            bulk_g2s(run_dst + st * Sh::kStage,
-                     run_base + (row_base + static_cast<int64_t>(c) * kQ4Chunk) * run_row,
-                     kQ4Chunk * run_row, bar0 + 8 * st);
-    };
-    auto fill = [&](int limit) {  // the first round, below chunk `limit`
-        for (; issued < NS; ++issued) {
-            const int c = c_begin + warp + NW * issued;
-            if (c >= c_end || c >= limit) break;
-            issue(c, issued);
-        }
-    };
-
-    // Programmatic dependent launch: with `early` the inputs and the cache rows
-    // that no running launch writes are read before the previous kernel's end
-    // and the next launch may start now; else everything follows the wait.
-    const bool early = !dev && p.early;
-    if (!early) griddep_wait();
-    griddep_launch_dependents();
-    if (dev) pos = p.pos_dev[seq.slot];
-    plan();
     Q4Row row;
     if (pos_ok) load_item(NW - 1 - warp, row);
-    if (lane == 0) {
-        for (int s = 0; s < NS; ++s) mbar_init(bar0 + 8 * s, 1);
-        if (warp == 0) {
-            mbar_init(smem_u32(&bar_recv), 1);
-            s_abort = 0;
-            if (E_me > 0) mbar_expect_tx(smem_u32(&bar_recv), S * (E_me * 4 + nh_me * 8));
+
+    // Stage j's rows are contiguous in the cache: four copies, by one thread.
+    auto issue = [&](int j) {
+        const int c = c_begin + j * NW, st = j % NS;
+        const uint32_t keys = min(NW, c_end - c) * kQ4Chunk;
+        const uint32_t bar = smem_u32(&bar_full[st]);
+        const int64_t r0 = row_base + static_cast<int64_t>(c) * kQ4Chunk;
+        uint32_t dst = smem_u32(smem + st * Sh::kStage);
+        mbar_expect_tx(bar, keys * 2 * (Sh::kRow + Sh::kScaleRow));
+        bulk_g2s(dst, p.kc + r0 * Sh::kRow, keys * Sh::kRow, bar);
+        bulk_g2s(dst + 2 * Sh::kCodes, p.ks + r0 * Sh::kScaleRow, keys * Sh::kScaleRow, bar);
+        bulk_g2s(dst + Sh::kCodes, p.vc + r0 * Sh::kRow, keys * Sh::kRow, bar);
+        bulk_g2s(dst + 2 * Sh::kCodes + Sh::kScales, p.vs + r0 * Sh::kScaleRow, keys * Sh::kScaleRow, bar);
+    };
+    int sent = 0;        // thread 0: stages of the first round on the way
+    int my_stage = -1;   // last stage of later rounds that this thread sent
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&bar_full[s]), 1);
+            mbar_init(smem_u32(&bar_empty[s]), NW);
+        }
+        mbar_init(smem_u32(&bar_recv), 1);
+        s_abort = 0;
+        const int E_me = min(p.E, R * D - split * p.E);
+        if (E_me > 0) {
+            const int nh = (split * p.E + E_me - 1) / D - split * p.E / D + 1;
+            mbar_expect_tx(smem_u32(&bar_recv), S * (E_me * 4 + nh * 8));
         }
         fence_mbar_init();
+#pragma unroll 1
+        for (const int limit = early ? c_safe : c_end;
+             sent < min(NS, nstages) && min(c_end, c_begin + (sent + 1) * NW) <= limit; ++sent)
+            issue(sent);
     }
     __syncwarp();
-    fill(early ? c_safe : c_end);
     cluster_arrive();  // peers may push into this CTA once they have waited on this
     if (!pos_ok) {
         if (threadIdx.x == 0) set_error(p.err, kErrBounds, kKernQ4Decode, 1);
@@ -458,6 +459,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     // ---------------------------------------------------------------- query rows and new tokens
     uint32_t new_codes[2], new_byte[2];  // of the warp's new token, if it has one
     uint4 new_held[2];
+#pragma unroll 1
     for (int it = NW - 1 - warp; it < nitems; it += NW) {  // warp-uniform
         const int t = it < R ? it / HPC : it - R;
         if (t >= ntok) continue;
@@ -494,54 +496,59 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             }
         }
     }
-    __syncthreads();  // query rows and new tokens in shared memory
+    __syncthreads();  // barriers, query rows and new tokens in shared memory
+    if (threadIdx.x == 0 && sent < min(NS, nstages)) {  // the rest of the first round
+        griddep_wait();
+#pragma unroll 1
+        for (; sent < min(NS, nstages); ++sent) issue(sent);
+    }
+    __syncwarp();
 
     // ---------------------------------------------------------------- new tokens
-    // A partial of their own (m, l, o): warp w serves rows w, w + NW, ...
-    if (owner) {
-        for (int row = warp; row < R; row += NW) {
-            const int t = row / HPC;
-            constexpr int PER = D / 32;
-            float M = -INFINITY, L = 0.f, O[PER];
+    // A partial of their own (m, l, o): warp w serves row w.
+    if (owner && warp < R) {
+        const int t = warp / HPC;
+        constexpr int PER = D / 32;
+        float M = -INFINITY, L = 0.f, O[PER];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) O[e] = 0.f;
-            if (t < ntok) {
-                float sc[TPS];
+        for (int e = 0; e < PER; ++e) O[e] = 0.f;
+        if (t < ntok) {
+            float q[PER], sc[TPS];
 #pragma unroll
-                for (int u = 0; u < TPS; ++u) {
-                    float x = 0.f;
+            for (int e = 0; e < PER; ++e) q[e] = __half2float(qs[warp * D + e * 32 + lane]);
 #pragma unroll
-                    for (int e = 0; e < PER; ++e)
-                        x = fmaf(__half2float(qs[row * D + e * 32 + lane]),
-                                 __bfloat162float(s_newk[u * D + e * 32 + lane]), x);
+            for (int u = 0; u < TPS; ++u) {
+                float x = 0.f;
 #pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
-                    const bool seen = u <= t && (p.window <= 0 || t - u < p.window);
-                    sc[u] = seen ? x * s_c[row] : -INFINITY;
-                    M = q4_max(M, sc[u]);
-                }
+                for (int e = 0; e < PER; ++e) x = fmaf(q[e], __bfloat162float(s_newk[u * D + e * 32 + lane]), x);
 #pragma unroll
-                for (int u = 0; u < TPS; ++u) {
-                    if (u > t || sc[u] == -INFINITY) continue;
-                    const float w = q4_ex2(sc[u] - M);
-                    L += w;
-#pragma unroll
-                    for (int e = 0; e < PER; ++e)
-                        O[e] = fmaf(w, __bfloat162float(s_newv[u * D + e * 32 + lane]), O[e]);
-                }
+                for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+                const bool seen = u <= t && (p.window <= 0 || t - u < p.window);
+                sc[u] = seen ? x * s_c[warp] : -INFINITY;
+                M = q4_max(M, sc[u]);
             }
 #pragma unroll
-            for (int e = 0; e < PER; ++e) part_new[row * D + e * 32 + lane] = O[e];
-            if (lane == 0) {
-                part_new[R * D + 2 * row] = M;
-                part_new[R * D + 2 * row + 1] = L;
+            for (int u = 0; u < TPS; ++u) {
+                if (u > t || sc[u] == -INFINITY) continue;
+                const float w = q4_ex2(sc[u] - M);
+                L += w;
+#pragma unroll
+                for (int e = 0; e < PER; ++e)
+                    O[e] = fmaf(w, __bfloat162float(s_newv[u * D + e * 32 + lane]), O[e]);
             }
+        }
+        // The warps' partials carry the factor 2^12 of their weights: so does this one.
+#pragma unroll
+        for (int e = 0; e < PER; ++e) part_new[warp * D + e * 32 + lane] = O[e] * 4096.f;
+        if (lane == 0) {
+            part_new[R * D + 2 * warp] = M;
+            part_new[R * D + 2 * warp + 1] = L * 4096.f;
         }
     }
 
     // ---------------------------------------------------------------- the cache's keys
-    const int r = lane >> 2, c4 = lane & 3;
     {
+        const int r = lane >> 2, c4 = lane & 3;
         uint32_t qb[D / 16][2];
         const int qt = TPS == 1 ? 0 : r / HPC;
         const bool real = r < R && qt < ntok;
@@ -550,26 +557,21 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const __half *qrow = qs + (real ? r : 0) * D + c4 * (D / 4);
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            const uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
-            const uint32_t even_lo = __byte_perm(q8.x, q8.z, 0x5410);  // dims 0, 4
-            const uint32_t odd_lo = __byte_perm(q8.x, q8.z, 0x7632);   // dims 1, 5
-            const uint32_t even_hi = __byte_perm(q8.y, q8.w, 0x5410);  // dims 2, 6
-            const uint32_t odd_hi = __byte_perm(q8.y, q8.w, 0x7632);   // dims 3, 7
+            uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
+            if (!real) q8 = make_uint4(0, 0, 0, 0);
             const __half2 down = __float2half2_rn(0.0625f), none = __float2half2_rn(0.f);
-            qb[2 * w][0] = real ? even_lo : 0u;
-            qb[2 * w][1] = real ? hfma2_u(odd_lo, down, none) : 0u;
-            qb[2 * w + 1][0] = real ? even_hi : 0u;
-            qb[2 * w + 1][1] = real ? hfma2_u(odd_hi, down, none) : 0u;
+            qb[2 * w][0] = __byte_perm(q8.x, q8.z, 0x5410);                              // dims 0, 4
+            qb[2 * w][1] = hfma2_u(__byte_perm(q8.x, q8.z, 0x7632), down, none);         // dims 1, 5
+            qb[2 * w + 1][0] = __byte_perm(q8.y, q8.w, 0x5410);                          // dims 2, 6
+            qb[2 * w + 1][1] = hfma2_u(__byte_perm(q8.y, q8.w, 0x7632), down, none);     // dims 3, 7
         }
         float cs[2];
-        int row_lo[2];
         Q4Acc<D> a;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int col = 2 * c4 + x;
             const int t = TPS == 1 ? 0 : col / HPC;
             cs[x] = col < R && t < ntok ? s_c[col] : 0.f;
-            row_lo[x] = p.window > 0 ? max(0, pos + t + 1 - p.window) : 0;
             a.ref[x] = kQ4NoRef;
             a.l[x] = 0.f;
         }
@@ -578,64 +580,74 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) a.o[t][e] = 0.f;
 
-        bool waited = !early;
         int st = 0;
         uint32_t phase = 0;
-        int i = 0;
-        for (int c = c_begin + warp; c < c_end; c += NW, ++i) {
-            if (issued == i) {  // not sent ahead: the chunk holds rows being written
-                if (!waited) {
-                    griddep_wait();
-                    waited = true;
-                }
-                for (int n = 0; n < NS && c + NW * n < c_end; ++n, ++issued) issue(c + NW * n, (i + n) % NS);
-            }
-            bool ok = mbar_wait(bar0 + 8 * st, phase, &s_abort, p.err, kKernQ4Decode, 2);
+        bool ok = true;
+#pragma unroll 1
+        for (int j = 0; j < nstages; ++j) {
+            ok = q4_wait(smem_u32(&bar_full[st]), phase, &s_abort, p.err, 2);
             ok = __all_sync(FULL, ok);
             if (!ok) break;
-            const int base = c * kQ4Chunk;
-            // Every row sees the whole chunk unless it holds the end or the window's start.
-            const bool whole = base + kQ4Chunk <= pos && (p.window <= 0 || base >= pos + ntok - p.window);
-            const uint8_t *stage = ring + st * Sh::kStage;
-            if (whole) {
-                const int none[2] = {0, 0};
-                q4_consume<D, R, false>(stage, kQ4Chunk, none, 0, qb, cs, a, lane);
-            } else {
-                const int klo[2] = {min(kQ4Chunk, max(0, row_lo[0] - base)), min(kQ4Chunk, max(0, row_lo[1] - base))};
-                q4_consume<D, R, true>(stage, min(kQ4Chunk, pos - base), klo, max(0, key_lo - base),
-                                       qb, cs, a, lane);
-            }
-            __syncwarp();  // the warp's reads of the stage come before the next copy into it
-            const int cn = c + NW * NS;
-            if (cn < c_end && issued == i + NS) {
-                if (!waited && cn >= c_safe) {
-                    griddep_wait();
-                    waited = true;
+            const int c = c_begin + j * NW + warp;
+            if (c < c_end) {
+                const int base = c * kQ4Chunk;
+                const uint8_t *stage = smem + st * Sh::kStage;
+                const uint8_t *sk = stage + warp * (kQ4Chunk * Sh::kRow), *sv = sk + Sh::kCodes;
+                const uint8_t *ssk = stage + 2 * Sh::kCodes + warp * (kQ4Chunk * Sh::kScaleRow);
+                const uint8_t *ssv = ssk + Sh::kScales;
+                // Every row sees the whole chunk unless it holds the end or the window's start.
+                const int lo0 = pos + 1 - p.window - base;  // token 0's first key, relative
+                const bool whole = base + kQ4Chunk <= pos && (p.window <= 0 || lo0 + ntok - 1 <= 0);
+                if (whole) {
+                    const int none[2] = {0, 0};
+                    q4_consume<D, R, false>(sk, sv, ssk, ssv, kQ4Chunk, none, 0, qb, cs, a, lane);
+                } else {
+                    int klo[2] = {0, 0};
+                    if (p.window > 0) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int t = TPS == 1 ? 0 : (2 * c4 + x) / HPC;
+                            klo[x] = min(kQ4Chunk, max(0, lo0 + t));
+                        }
+                    }
+                    q4_consume<D, R, true>(sk, sv, ssk, ssv, min(kQ4Chunk, pos - base), klo,
+                                           max(0, key_lo - base), qb, cs, a, lane);
                 }
-                issue(cn, st);
-                ++issued;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bar_empty[st]));
+                // The stage before this one goes out again once every warp has left
+                // it; the warps take turns.
+                const int jn = j - 1 + NS;
+                if (j > 0 && jn < nstages && (j % NW) == warp) {
+                    const int sp = st == 0 ? NS - 1 : st - 1;
+                    if (q4_wait(smem_u32(&bar_empty[sp]), (st == 0 ? phase ^ 1u : phase), &s_abort, p.err, 3)) {
+                        if (early && min(c_end, c_begin + (jn + 1) * NW) > c_safe) griddep_wait();
+                        issue(jn);
+                        my_stage = jn;
+                    }
+                }
             }
             if (++st == NS) {
                 st = 0;
-                phase ^= 1;
+                phase ^= 1u;
             }
         }
-        if (lane == 0) {
-            // No copy may land after the CTA exits or into the partial below.
-            for (int k = i; k < issued; ++k) {
-                int dummy = 0;
-                mbar_wait(bar0 + 8 * (k % NS), (k / NS) & 1, &dummy, p.err, kKernQ4Decode, 3);
-            }
+        if (!ok && lane == 0) {  // given up: no copy may land after the CTA exits
+            int dummy = 0;
+            for (int j = 0; j < sent; ++j) mbar_wait(smem_u32(&bar_full[j]), 0, &dummy, p.err, kKernQ4Decode, 6);
+            if (my_stage >= 0)
+                mbar_wait(smem_u32(&bar_full[my_stage % NS]), (my_stage / NS) & 1, &dummy, p.err, kKernQ4Decode, 6);
         }
-        __syncwarp();
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             a.l[x] += __shfl_xor_sync(FULL, a.l[x], 4);
             a.l[x] += __shfl_xor_sync(FULL, a.l[x], 8);
             a.l[x] += __shfl_xor_sync(FULL, a.l[x], 16);
         }
-        // The warp's partial, in its own ring.
-        float *part = reinterpret_cast<float *>(ring);
+        __syncthreads();  // every warp has left the ring: the partials take its place
+        float *part = reinterpret_cast<float *>(smem) + warp * Sh::kPartial;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int col = 2 * c4 + x;
@@ -654,91 +666,73 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     }
 
     // ---------------------------------------------------------------- combine and push
+    // One pair of outputs per thread and turn: the CTA's partials become one
+    // (M, L, O), which goes to the CTA that owns the pair's run.  The first pair
+    // of a run or of a row carries the row's (M, L).
+    constexpr int total = R * D, kThreads = NW * 32;
+    const int E = p.E;
+    float *rcv_o = recv, *rcv_ml = recv + S * E;
     __syncthreads();
     cluster_wait();  // every peer's receive barrier is initialised
-    {
-        constexpr int kWF = Sh::kWarpRing / 4;
+#pragma unroll 1
+    for (int e = 2 * threadIdx.x; e < total; e += 2 * kThreads) {
+        const int g = e / D;
         const float *red = reinterpret_cast<const float *>(smem);
-        const uint32_t a_bar = smem_u32(&bar_recv);
-        const uint32_t a_o = smem_u32(rcv_o + split * E);
-        auto weights = [&](int g, float (&w)[NW + 1], float &M) {
-            M = owner ? part_new[R * D + 2 * g] : -INFINITY;
+        float m[NW + 1], M = owner ? part_new[R * D + 2 * g] : -INFINITY;
+        m[NW] = M;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) M = q4_max(M, red[i * kWF + R * D + 2 * g]);
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const float mi = red[i * kWF + R * D + 2 * g];
-                w[i] = mi == -INFINITY ? 0.f : q4_ex2(mi - M);
-            }
-            const float mn = owner ? part_new[R * D + 2 * g] : -INFINITY;
-            // the warps' partials carry the factor 2^12 of their P
-            w[NW] = mn == -INFINITY ? 0.f : q4_ex2(mn - M) * 4096.f;
-        };
-        for (int pe = threadIdx.x; pe < total / 2; pe += blockDim.x) {
-            const int e = 2 * pe, g = e / D, d = e % D;
-            float w[NW + 1], M;
-            weights(g, w, M);
-            float2 O = make_float2(0.f, 0.f);
-            if (owner) O = make_float2(w[NW] * part_new[g * D + d], w[NW] * part_new[g * D + d + 1]);
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                const float2 x = *reinterpret_cast<const float2 *>(red + i * kWF + g * D + d);
-                O = make_float2(fmaf(w[i], x.x, O.x), fmaf(w[i], x.y, O.y));
-            }
-            const int dst = e / E;
-            st_async_f32x2(map_rank(a_o + 4u * (e - dst * E), dst), O.x, O.y, map_rank(a_bar, dst));
+        for (int i = 0; i < NW; ++i) {
+            m[i] = red[i * Sh::kPartial + R * D + 2 * g];
+            M = q4_max(M, m[i]);
         }
-        for (int k = threadIdx.x; k < R * S; k += blockDim.x) {
-            const int g = k / S, dst = k % S;
-            const int lo = dst * E, hi = min(lo + E, total);
-            if (lo < hi && lo < (g + 1) * D && hi > g * D) {
-                float w[NW + 1], M, L = 0.f;
-                weights(g, w, M);
-                if (owner) L = w[NW] * part_new[R * D + 2 * g + 1];
+        float L = 0.f;
+        float2 O = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < NW; ++i)
-                    L = fmaf(w[i], red[i * kWF + R * D + 2 * g + 1], L);
-                st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L,
-                               map_rank(a_bar, dst));
-            }
+        for (int i = 0; i <= NW; ++i) {
+            const float *src = i < NW ? red + i * Sh::kPartial : part_new;
+            if (i == NW && !owner) continue;
+            const float w = m[i] == -INFINITY ? 0.f : q4_ex2(m[i] - M);
+            const float2 x = *reinterpret_cast<const float2 *>(src + e);
+            L = fmaf(w, src[R * D + 2 * g + 1], L);
+            O = make_float2(fmaf(w, x.x, O.x), fmaf(w, x.y, O.y));
         }
+        const int dst = e / E;
+        const uint32_t bar = map_rank(smem_u32(&bar_recv), dst);
+        st_async_f32x2(map_rank(smem_u32(rcv_o + split * E + e - dst * E), dst), O.x, O.y, bar);
+        if (e == dst * E || e == g * D)
+            st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L, bar);
     }
 
     // ---------------------------------------------------------------- merge
-    constexpr int kThreads = NW * 32;
+    // The S partials of this CTA's run, in a fixed order.
     constexpr int kOutPer = (total + kThreads - 1) / kThreads;
+    const int e_lo = split * E, E_me = min(E, total - e_lo);
     float res[kOutPer];
-    bool merged = E_me > 0;
-    if (E_me > 0) {
-        bool ok = mbar_wait_cluster(smem_u32(&bar_recv), 0, &s_abort, p.err, kKernQ4Decode, 4);
-        if (!ok) {  // the peers still push here: their stores land before this CTA exits
-            int dummy = 0;
-            mbar_wait_cluster(smem_u32(&bar_recv), 0, &dummy, p.err, kKernQ4Decode, 5);
-        }
-        merged = __syncthreads_and(ok);
-        if (merged) {
+    bool merged = false;
+    if (static_cast<int>(threadIdx.x) < E_me) {
+        merged = q4_wait_cluster(smem_u32(&bar_recv), &s_abort, p.err);
 #pragma unroll
-            for (int j = 0; j < kOutPer; ++j) {
-                const int k = threadIdx.x + j * kThreads;
-                res[j] = 0.f;
-                if (k < E_me) {
-                    const float2 *ml = reinterpret_cast<const float2 *>(rcv_ml) + (e_lo + k) / D;
-                    float M = -INFINITY, L = 0.f, O = 0.f;
-                    for (int i = 0; i < S; ++i) M = q4_max(M, ml[R * i].x);
-                    for (int i = 0; i < S; ++i) {
-                        const float2 x = ml[R * i];
-                        const float w = x.x == -INFINITY ? 0.f : q4_ex2(x.x - M);
-                        L = fmaf(w, x.y, L);
-                        O = fmaf(w, rcv_o[i * E + k], O);
-                    }
-                    res[j] = O / L;
-                }
+        for (int j = 0; j < kOutPer; ++j) {
+            const int k = threadIdx.x + j * kThreads;
+            if (!merged || k >= E_me) continue;
+            const float2 *ml = reinterpret_cast<const float2 *>(rcv_ml) + (e_lo + k) / D;
+            float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < S; ++i) M = q4_max(M, ml[R * i].x);
+#pragma unroll 2
+            for (int i = 0; i < S; ++i) {
+                const float2 x = ml[R * i];
+                const float w = x.x == -INFINITY ? 0.f : q4_ex2(x.x - M);
+                L = fmaf(w, x.y, L);
+                O = fmaf(w, rcv_o[i * E + k], O);
             }
+            res[j] = __fdividef(O, L);
         }
     }
     griddep_wait();  // before any global write
     // The new rows: each item's warp still holds its codes.
     if (owner && hg == 0) {
+#pragma unroll 1
         for (int it = NW - 1 - warp; it < nitems; it += NW) {
             if (it < R || lane >= LPR) continue;
             const int t = it - R;
