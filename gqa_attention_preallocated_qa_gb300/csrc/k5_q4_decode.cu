@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "q4_device.cuh"
 
@@ -194,11 +195,37 @@ struct Q4Acc {
 constexpr float kQ4Lift = 12.f, kQ4Most = 15.f;
 constexpr float kQ4NoRef = -1e30f;  // no key yet: any score is too large for it
 
-// One chunk of 32 keys: codes sk, sv and scale bytes ssk, ssv.  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
+// Shared-memory reads at an address and a constant offset.
+template <int kOffset>
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(x) : "r"(a), "n"(kOffset));
+    return x;
+}
+template <int kOffset, int kWords>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[kWords], uint32_t a) {
+    static_assert(kWords == 1 || kWords == 2 || kWords == 4, "one load");
+    if constexpr (kWords == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4+%5];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a), "n"(kOffset));
+    else if constexpr (kWords == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2+%3];" : "=r"(w[0]), "=r"(w[1]) : "r"(a), "n"(kOffset));
+    else
+        asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(w[0]) : "r"(a), "n"(kOffset));
+}
+
+// What a lane adds to the addresses of its warp's part of a stage.
+struct Q4Lane {
+    uint32_t k, ks;        // its group of its row of K, and the group's scale byte
+    uint32_t va, vb;       // its part of the rows of V with fragment indices 2c and 2c + 1
+    uint32_t vsa, vsb;     // their scale bytes
+};
+
+// One chunk of 32 keys, its codes of K at shared address `codes` and their scale
+// bytes at `scales`.  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
 // row; else every row sees all 32.
 template <int D, int R, bool kMask>
-__device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv, const uint8_t *ssk,
-                                           const uint8_t *ssv, int nk, const int (&klo)[2], int kvlo,
+__device__ __forceinline__ void q4_consume(uint32_t codes, uint32_t scales, const Q4Lane &at, int nk, const int (&klo)[2], int kvlo,
                                            const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
                                            Q4Acc<D> &a, int lane) {
     using Sh = Q4Shape<D, R>;
@@ -206,24 +233,14 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
     const int r = lane >> 2, c = lane & 3;
     const int kr = q4_key(r);
     float s[2][4];
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        const int k0 = mt * 16 + kr, k1 = k0 + 8;
+    auto scores = [&](auto tile) {
+        constexpr int mt = decltype(tile)::value;
+        constexpr int kBlock = 8 * Sh::kRow, kScaleBlock = 8 * Sh::kScaleRow;
         uint32_t w0[D / 32], w1[D / 32];
-        if (D == 128) {
-            const uint4 a0 = *reinterpret_cast<const uint4 *>(sk + k0 * Sh::kRow + c * 16);
-            const uint4 a1 = *reinterpret_cast<const uint4 *>(sk + k1 * Sh::kRow + c * 16);
-            w0[0] = a0.x; w0[1] = a0.y; w0[D / 32 - 2] = a0.z; w0[D / 32 - 1] = a0.w;
-            w1[0] = a1.x; w1[1] = a1.y; w1[D / 32 - 2] = a1.z; w1[D / 32 - 1] = a1.w;
-        } else {
-            const uint2 a0 = *reinterpret_cast<const uint2 *>(sk + k0 * Sh::kRow + c * 8);
-            const uint2 a1 = *reinterpret_cast<const uint2 *>(sk + k1 * Sh::kRow + c * 8);
-            w0[0] = a0.x; w0[1] = a0.y;
-            w1[0] = a1.x; w1[1] = a1.y;
-        }
-        const int g = D == 128 ? c : c >> 1;
-        const Q4Scale s0 = q4_scale2(ssk[k0 * Sh::kScaleRow + g] * 0x01000100u);
-        const Q4Scale s1 = q4_scale2(ssk[k1 * Sh::kScaleRow + g] * 0x01000100u);
+        lds_words<2 * mt * kBlock>(w0, codes + at.k);
+        lds_words<(2 * mt + 1) * kBlock>(w1, codes + at.k);
+        const Q4Scale s0 = q4_scale2(lds8<2 * mt * kScaleBlock>(scales + at.ks) * 0x01000100u);
+        const Q4Scale s1 = q4_scale2(lds8<(2 * mt + 1) * kScaleBlock>(scales + at.ks) * 0x01000100u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[mt][e] = 0.f;
 #pragma unroll
@@ -234,7 +251,9 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
             mma_f16(s[mt], q4_lo(x0, s0), q4_lo(x1, s1), q4_hi(x0, s0), q4_hi(x1, s1),
                     qb[2 * w + 1][0], qb[2 * w + 1][1]);
         }
-    }
+    };
+    scores(std::integral_constant<int, 0>{});
+    scores(std::integral_constant<int, 1>{});
     // s becomes the exponents t - ref, in units of log2.
     if (kMask) {
 #pragma unroll
@@ -284,8 +303,9 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[mt][e] = exponent(s[mt][e], e);
     }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    auto values = [&](auto tile) {
+        constexpr int ks = decltype(tile)::value;
+        constexpr int kBlock = 8 * Sh::kRow, kScaleBlock = 8 * Sh::kScaleRow;
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -295,11 +315,12 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
         const uint32_t b0 = transpose8x8(pack_f16(p[0], p[1]));
         const uint32_t b1 = transpose8x8(pack_f16(p[2], p[3]));
         // V of the keys with fragment indices 2c, 2c+1 (block 0) and 2c+8, 2c+9 (block 1).
-        const int ka = ks * 16 + q4_key(2 * c), kb = ks * 16 + q4_key(2 * c + 1);
-        const int g = D == 128 ? r >> 1 : r >> 2;
-        uint32_t ba = ssv[ka * Sh::kScaleRow + g], bb = ssv[kb * Sh::kScaleRow + g];
-        uint32_t bc = ssv[(ka + 8) * Sh::kScaleRow + g], bd = ssv[(kb + 8) * Sh::kScaleRow + g];
+        uint32_t ba = lds8<Sh::kScales + 2 * ks * kScaleBlock>(scales + at.vsa);
+        uint32_t bb = lds8<Sh::kScales + 2 * ks * kScaleBlock>(scales + at.vsb);
+        uint32_t bc = lds8<Sh::kScales + (2 * ks + 1) * kScaleBlock>(scales + at.vsa);
+        uint32_t bd = lds8<Sh::kScales + (2 * ks + 1) * kScaleBlock>(scales + at.vsb);
         if (kMask) {  // rows that no query row sees may hold anything: a zero scale drops them
+            const int ka = ks * 16 + q4_key(2 * c), kb = ks * 16 + q4_key(2 * c + 1);
             if (ka >= nk || ka < kvlo) ba = 0;
             if (kb >= nk || kb < kvlo) bb = 0;
             if (ka + 8 >= nk || ka + 8 < kvlo) bc = 0;
@@ -309,20 +330,10 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
         const Q4Scale s1 = q4_scale2(__byte_perm(bc, bd, 0x4101));
         constexpr int NW = D / 64;  // words of a lane's part of a row
         uint32_t va[NW], vb[NW], vc[NW], vd[NW];
-        const uint8_t *base = sv + r * (4 * NW);
-        if (NW == 2) {
-            const uint2 xa = *reinterpret_cast<const uint2 *>(base + ka * Sh::kRow);
-            const uint2 xb = *reinterpret_cast<const uint2 *>(base + kb * Sh::kRow);
-            const uint2 xc = *reinterpret_cast<const uint2 *>(base + (ka + 8) * Sh::kRow);
-            const uint2 xd = *reinterpret_cast<const uint2 *>(base + (kb + 8) * Sh::kRow);
-            va[0] = xa.x; va[NW - 1] = xa.y; vb[0] = xb.x; vb[NW - 1] = xb.y;
-            vc[0] = xc.x; vc[NW - 1] = xc.y; vd[0] = xd.x; vd[NW - 1] = xd.y;
-        } else {
-            va[0] = *reinterpret_cast<const uint32_t *>(base + ka * Sh::kRow);
-            vb[0] = *reinterpret_cast<const uint32_t *>(base + kb * Sh::kRow);
-            vc[0] = *reinterpret_cast<const uint32_t *>(base + (ka + 8) * Sh::kRow);
-            vd[0] = *reinterpret_cast<const uint32_t *>(base + (kb + 8) * Sh::kRow);
-        }
+        lds_words<Sh::kCodes + 2 * ks * kBlock>(va, codes + at.va);
+        lds_words<Sh::kCodes + 2 * ks * kBlock>(vb, codes + at.vb);
+        lds_words<Sh::kCodes + (2 * ks + 1) * kBlock>(vc, codes + at.va);
+        lds_words<Sh::kCodes + (2 * ks + 1) * kBlock>(vd, codes + at.vb);
 #pragma unroll
         for (int y = 0; y < NW; ++y)
 #pragma unroll
@@ -334,7 +345,9 @@ __device__ __forceinline__ void q4_consume(const uint8_t *sk, const uint8_t *sv,
                 mma_f16(a.o[y * 4 + hl * 2 + 1], q4_lo(w0 >> 8, s0), q4_hi(w0 >> 8, s0),
                         q4_lo(w1 >> 8, s1), q4_hi(w1 >> 8, s1), b0, b1);
             }
-    }
+    };
+    values(std::integral_constant<int, 0>{});
+    values(std::integral_constant<int, 1>{});
 }
 
 template <int D, int HPC, int TPS>
@@ -580,6 +593,19 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) a.o[t][e] = 0.f;
 
+        const uint32_t codes0 = smem_u32(smem) + warp * (kQ4Chunk * Sh::kRow);
+        const uint32_t scales0 = smem_u32(smem) + 2 * Sh::kCodes + warp * (kQ4Chunk * Sh::kScaleRow);
+        Q4Lane at;
+        {
+            const int kr = q4_key(r), ka = q4_key(2 * c4), kb = q4_key(2 * c4 + 1);
+            const int gk = D == 128 ? c4 : c4 >> 1, gv = D == 128 ? r >> 1 : r >> 2;
+            at.k = kr * Sh::kRow + c4 * (D / 8);
+            at.ks = kr * Sh::kScaleRow + gk;
+            at.va = ka * Sh::kRow + r * (D / 16);
+            at.vb = kb * Sh::kRow + r * (D / 16);
+            at.vsa = ka * Sh::kScaleRow + gv;
+            at.vsb = kb * Sh::kScaleRow + gv;
+        }
         int st = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -591,16 +617,13 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             const int c = c_begin + j * NW + warp;
             if (c < c_end) {
                 const int base = c * kQ4Chunk;
-                const uint8_t *stage = smem + st * Sh::kStage;
-                const uint8_t *sk = stage + warp * (kQ4Chunk * Sh::kRow), *sv = sk + Sh::kCodes;
-                const uint8_t *ssk = stage + 2 * Sh::kCodes + warp * (kQ4Chunk * Sh::kScaleRow);
-                const uint8_t *ssv = ssk + Sh::kScales;
+                const uint32_t codes = codes0 + st * Sh::kStage, scales = scales0 + st * Sh::kStage;
                 // Every row sees the whole chunk unless it holds the end or the window's start.
                 const int lo0 = pos + 1 - p.window - base;  // token 0's first key, relative
                 const bool whole = base + kQ4Chunk <= pos && (p.window <= 0 || lo0 + ntok - 1 <= 0);
                 if (whole) {
                     const int none[2] = {0, 0};
-                    q4_consume<D, R, false>(sk, sv, ssk, ssv, kQ4Chunk, none, 0, qb, cs, a, lane);
+                    q4_consume<D, R, false>(codes, scales, at, kQ4Chunk, none, 0, qb, cs, a, lane);
                 } else {
                     int klo[2] = {0, 0};
                     if (p.window > 0) {
@@ -610,7 +633,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                             klo[x] = min(kQ4Chunk, max(0, lo0 + t));
                         }
                     }
-                    q4_consume<D, R, true>(sk, sv, ssk, ssv, min(kQ4Chunk, pos - base), klo,
+                    q4_consume<D, R, true>(codes, scales, at, min(kQ4Chunk, pos - base), klo,
                                            max(0, key_lo - base), qb, cs, a, lane);
                 }
             }
