@@ -39,7 +39,7 @@ namespace qa {
 constexpr int q4_recv_floats(int total, int rows) {
     int best = 0;
     for (int S = 1; S <= kQ4MaxSplits; ++S) {
-        const int E = ((total + S - 1) / S + 7) & ~7;
+        const int E = ((total + S - 1) / S + 31) & ~31;
         const int f = S * (E + 2 * rows);
         best = f > best ? f : best;
     }
@@ -550,9 +550,11 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                     O[e] = fmaf(w, __bfloat162float(s_newv[u * D + e * 32 + lane]), O[e]);
             }
         }
-        // The warps' partials carry the factor 2^12 of their weights: so does this one.
+        // The warps' partials carry the factor 2^12 of their weights, and 16 more
+        // in the odd dims: so does this one.
+        const float lift = lane & 1 ? 65536.f : 4096.f;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) part_new[warp * D + e * 32 + lane] = O[e] * 4096.f;
+        for (int e = 0; e < PER; ++e) part_new[warp * D + e * 32 + lane] = O[e] * lift;
         if (lane == 0) {
             part_new[R * D + 2 * warp] = M;
             part_new[R * D + 2 * warp + 1] = L * 4096.f;
@@ -563,15 +565,13 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     {
         const int r = lane >> 2, c4 = lane & 3;
         uint32_t qb[D / 16][2];
-        const int qt = TPS == 1 ? 0 : r / HPC;
-        const bool real = r < R && qt < ntok;
         // B fragments: this lane's dims are those of its part of a row of K; the
         // codes of odd dims come 16 times larger, their queries 16 times smaller.
-        const __half *qrow = qs + (real ? r : 0) * D + c4 * (D / 4);
+        // A column past the last row repeats one; nothing reads it.
+        const __half *qrow = qs + (r % R) * D + c4 * (D / 4);
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
-            if (!real) q8 = make_uint4(0, 0, 0, 0);
+            const uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
             const __half2 down = __float2half2_rn(0.0625f), none = __float2half2_rn(0.f);
             qb[2 * w][0] = __byte_perm(q8.x, q8.z, 0x5410);                              // dims 0, 4
             qb[2 * w][1] = hfma2_u(__byte_perm(q8.x, q8.z, 0x7632), down, none);         // dims 1, 5
@@ -582,9 +582,8 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         Q4Acc<D> a;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int col = 2 * c4 + x;
-            const int t = TPS == 1 ? 0 : col / HPC;
-            cs[x] = col < R && t < ntok ? s_c[col] : 0.f;
+            const int col = (2 * c4 + x) % R;
+            cs[x] = TPS == 1 || col / HPC < ntok ? s_c[col] : 0.f;
             a.ref[x] = kQ4NoRef;
             a.l[x] = 0.f;
         }
@@ -678,7 +677,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t)
                     *reinterpret_cast<float2 *>(part + col * D + r * (D / 8) + 2 * t) =
-                        make_float2(a.o[t][x], a.o[t][2 + x] * 0.0625f);
+                        make_float2(a.o[t][x], a.o[t][2 + x]);  // (the odd dim 16 times larger)
                 if (r == 0) {  // a NaN score leaves ref alone: its row is NaN whatever the other warps hold
                     const float m = a.l[x] != a.l[x] ? a.l[x] : a.ref[x] + kQ4Lift;
                     part[R * D + 2 * col] = a.ref[x] == kQ4NoRef && a.l[x] == 0.f ? -INFINITY : m;
@@ -689,66 +688,83 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     }
 
     // ---------------------------------------------------------------- combine and push
-    // One pair of outputs per thread and turn: the CTA's partials become one
-    // (M, L, O), which goes to the CTA that owns the pair's run.  The first pair
-    // of a run or of a row carries the row's (M, L).
+    // One pair of outputs per thread and turn, one row per warp (64 outputs): its
+    // lanes 0..NW weigh the CTA's partials, which become one (M, L, O) that goes
+    // to the CTA owning the outputs' run.  Runs are multiples of 32 outputs; the
+    // first pair of a run or of a row carries the row's (M, L).
     constexpr int total = R * D, kThreads = NW * 32;
     const int E = p.E;
     float *rcv_o = recv, *rcv_ml = recv + S * E;
     __syncthreads();
     cluster_wait();  // every peer's receive barrier is initialised
+    const float *red = reinterpret_cast<const float *>(smem);
 #pragma unroll 1
-    for (int e = 2 * threadIdx.x; e < total; e += 2 * kThreads) {
+    for (int e = 2 * threadIdx.x; e < total; e += 2 * kThreads) {  // warp-uniform
         const int g = e / D;
-        const float *red = reinterpret_cast<const float *>(smem);
-        float m[NW + 1], M = owner ? part_new[R * D + 2 * g] : -INFINITY;
-        m[NW] = M;
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            m[i] = red[i * Sh::kPartial + R * D + 2 * g];
-            M = q4_max(M, m[i]);
+        const int sources = owner ? NW + 1 : NW;
+        float M = -INFINITY, L = 0.f;
+        if (lane < sources) {
+            const float2 ml = *reinterpret_cast<const float2 *>(
+                (lane < NW ? red + lane * Sh::kPartial : part_new) + R * D + 2 * g);
+            M = ml.x;
+            L = ml.y;
         }
-        float L = 0.f;
+        float w = M;
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) M = q4_max(M, __shfl_xor_sync(FULL, M, o));
+        w = w == -INFINITY ? 0.f : q4_ex2(w - M);
+        L *= w;
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
         float2 O = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i <= NW; ++i) {
-            const float *src = i < NW ? red + i * Sh::kPartial : part_new;
-            if (i == NW && !owner) continue;
-            const float w = m[i] == -INFINITY ? 0.f : q4_ex2(m[i] - M);
-            const float2 x = *reinterpret_cast<const float2 *>(src + e);
-            L = fmaf(w, src[R * D + 2 * g + 1], L);
-            O = make_float2(fmaf(w, x.x, O.x), fmaf(w, x.y, O.y));
+        for (int i = 0; i < NW; ++i) {
+            const float wi = __shfl_sync(FULL, w, i);
+            const float2 x = *reinterpret_cast<const float2 *>(red + i * Sh::kPartial + e);
+            O = make_float2(fmaf(wi, x.x, O.x), fmaf(wi, x.y, O.y));
+        }
+        if (owner) {
+            const float wi = __shfl_sync(FULL, w, NW);
+            const float2 x = *reinterpret_cast<const float2 *>(part_new + e);
+            O = make_float2(fmaf(wi, x.x, O.x), fmaf(wi, x.y, O.y));
         }
         const int dst = e / E;
         const uint32_t bar = map_rank(smem_u32(&bar_recv), dst);
-        st_async_f32x2(map_rank(smem_u32(rcv_o + split * E + e - dst * E), dst), O.x, O.y, bar);
+        st_async_f32x2(map_rank(smem_u32(rcv_o + split * E + e - dst * E), dst), O.x, O.y * 0.0625f, bar);
+        // (lanes 16-31 hold the (M, L) of no source: lane 0's are sent, by its neighbours too)
+        M = __shfl_sync(FULL, M, 0);
+        L = __shfl_sync(FULL, L, 0);
         if (e == dst * E || e == g * D)
             st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L, bar);
     }
 
     // ---------------------------------------------------------------- merge
-    // The S partials of this CTA's run, in a fixed order.
+    // The S partials of this CTA's run, in a fixed order; a warp's 32 outputs are
+    // of one row, whose weights its lanes 0..S-1 make.
     constexpr int kOutPer = (total + kThreads - 1) / kThreads;
     const int e_lo = split * E, E_me = min(E, total - e_lo);
     float res[kOutPer];
     bool merged = false;
-    if (static_cast<int>(threadIdx.x) < E_me) {
+    if (warp * 32 < E_me) {
         merged = q4_wait_cluster(smem_u32(&bar_recv), &s_abort, p.err);
+        merged = __all_sync(FULL, merged);
 #pragma unroll
         for (int j = 0; j < kOutPer; ++j) {
             const int k = threadIdx.x + j * kThreads;
-            if (!merged || k >= E_me) continue;
+            if (!merged || warp * 32 + j * kThreads >= E_me) continue;
             const float2 *ml = reinterpret_cast<const float2 *>(rcv_ml) + (e_lo + k) / D;
-            float M = -INFINITY, L = 0.f, O = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < S; ++i) M = q4_max(M, ml[R * i].x);
-#pragma unroll 2
-            for (int i = 0; i < S; ++i) {
-                const float2 x = ml[R * i];
-                const float w = x.x == -INFINITY ? 0.f : q4_ex2(x.x - M);
-                L = fmaf(w, x.y, L);
-                O = fmaf(w, rcv_o[i * E + k], O);
-            }
+            float2 x = make_float2(-INFINITY, 0.f);
+            if (lane < S) x = ml[R * lane];
+            float M = x.x;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) M = q4_max(M, __shfl_xor_sync(FULL, M, o));
+            const float w = x.x == -INFINITY ? 0.f : q4_ex2(x.x - M);
+            float L = w * x.y, O = 0.f;
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+            L = __shfl_sync(FULL, L, 0);
+#pragma unroll 4
+            for (int i = 0; i < S; ++i) O = fmaf(__shfl_sync(FULL, w, i), rcv_o[i * E + k], O);
             res[j] = __fdividef(O, L);
         }
     }

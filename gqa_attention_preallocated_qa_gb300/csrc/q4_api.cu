@@ -233,10 +233,13 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         }
         if (nz == 0) break;
         if (p.window > 0) keys = std::min(keys, p.window);
+        // The longest sequences first: thread blocks start in this order, and the
+        // short ones fill in behind them.
+        std::stable_sort(p.seq, p.seq + nz, [](const qa::Q4Seq &x, const qa::Q4Seq &y) { return x.pos > y.pos; });
         p.B = nz;
         p.S = choose_splits(D, HPC, multi, nz * g.n_kv_heads * p.HG, keys);
         const int rows = multi ? qa::kQ4MaxTokens : HPC;
-        p.E = ((rows * D + p.S - 1) / p.S + 7) & ~7;
+        p.E = ((rows * D + p.S - 1) / p.S + 31) & ~31;
         p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
         const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,
                                                    p.early != 0, resident);
