@@ -9,6 +9,7 @@
 // 32 is four lanes, whose largest magnitude takes two shuffles.  All the warp's
 // loads are issued before any arithmetic (128 bytes a lane).
 #include <algorithm>
+#include <atomic>
 
 #include "q4_device.cuh"
 
@@ -119,6 +120,239 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
             *(reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(t.tok0 + i) * p.dst_tok) + sub) =
                 q4_values8(w[u], s[u]);
     }
+}
+
+// -------------------------------------------------------------------- a prefill's rows
+// RMSNorm + RoPE of the query and key rows and the quantised append of keys and
+// values, in one pass: per token 2 D (Hq + 2 Hkv) bytes in, as many out (q' and
+// the workspace's rows), and the codes.  Without it the workspace's rows would
+// be written, read and written again.  Bound by HBM; a warp walks its share of
+// the tokens with the next token's rows on the way into the other half of its
+// ring (three bulk copies), as K1 does.
+constexpr int kQ4RowWarps = 16;  // warps per CTA, one CTA per SM
+
+// A warp's share of a token: with an even number of kv heads half of the heads
+// (twice the warps hide more of the arithmetic's latency), else all of them.
+__host__ __device__ constexpr int q4_row_parts(int Hkv) { return Hkv % 2 == 0 ? 2 : 1; }
+
+// RMSNorm + RoPE of this lane's 8 values of a row held by D/8 lanes; cs, sn:
+// cosines and sines of its dims, the sines signed for its half.
+template <int D>
+__device__ __forceinline__ uint4 q4_transform(uint4 xv, uint4 wv, const float2 (&cs)[4],
+                                              const float2 (&sn)[4], float eps) {
+    constexpr int HALF = D / 16;
+    const unsigned FULL = 0xffffffffu;
+    const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        ss = fmaf(bf16lo(xw[e]), bf16lo(xw[e]), fmaf(bf16hi(xw[e]), bf16hi(xw[e]), ss));
+#pragma unroll
+    for (int o = HALF; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
+    const float r = rsqrtf(ss * (1.0f / D) + eps);
+    uint32_t y[4], partner[4], out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 h = __fmul2_rn(make_float2(bf16lo(xw[e]), bf16hi(xw[e])), make_float2(r, r));
+        const uint32_t hb = pack_bf16(h.x, h.y);
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&hb),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&ww[e]));
+        y[e] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) partner[e] = __shfl_xor_sync(FULL, y[e], HALF);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 rot = __ffma2_rn(make_float2(bf16lo(partner[e]), bf16hi(partner[e])), sn[e],
+                                      __fmul2_rn(make_float2(bf16lo(y[e]), bf16hi(y[e])), cs[e]));
+        out[e] = pack_bf16(rot.x, rot.y);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kQ4RowWarps * 32, 1)
+    q4_prefill_rows_kernel(const __grid_constant__ Q4PrefillRowsParams p) {
+    constexpr int LPR = D / 8, RPW = 32 / LPR, HALF = LPR / 2, GR = D / kQ4Group;
+    const unsigned FULL = 0xffffffffu;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bar[kQ4RowWarps * 2];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    const K1Params &k = p.k1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = lane % LPR, grp = lane / LPR;
+    // The prefill attention follows as a programmatic dependent: its set-up may
+    // start now; it reads what this kernel writes only after its end.
+    if (k.signal_early) griddep_launch_dependents();
+    const int parts = q4_row_parts(k.Hkv);
+    const int nq = k.Hq / parts, nkv = k.Hkv / parts;  // heads of a share
+    const uint32_t qbytes = static_cast<uint32_t>(nq) * D * 2;
+    const uint32_t kvbytes = static_cast<uint32_t>(nkv) * D * 2;
+    const uint32_t stage_bytes = (qbytes + 2 * kvbytes + 127) & ~127u;
+    uint8_t *ring = smem + static_cast<size_t>(warp) * 2 * stage_bytes;
+    const uint32_t bar0 = smem_u32(&bar[2 * warp]);
+    if (lane == 0) {
+        mbar_init(bar0, 1);
+        mbar_init(bar0 + 8, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const uint4 wq = __ldg(reinterpret_cast<const uint4 *>(k.wq) + sub);
+    const uint4 wk = __ldg(reinterpret_cast<const uint4 *>(k.wk) + sub);
+
+    // Share w of the grid's warps: part w % parts of tokens w / parts, + stride, ...
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kQ4RowWarps + warp;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQ4RowWarps / parts);
+    const int part = static_cast<int>(first % parts), hq0 = part * nq, hkv0 = part * nkv;
+    int64_t t = first / parts;
+    auto load = [&](int64_t tok, int s) {  // lane 0 only
+        const uint32_t dst = smem_u32(ring + s * stage_bytes), b = bar0 + 8 * s;
+        mbar_expect_tx(b, qbytes + 2 * kvbytes);
+        bulk_g2s(dst, k.q + (tok * k.Hq + hq0) * D, qbytes, b);
+        bulk_g2s(dst + qbytes, k.k + (tok * k.Hkv + hkv0) * D, kvbytes, b);
+        bulk_g2s(dst + qbytes + kvbytes, k.v + (tok * k.Hkv + hkv0) * D, kvbytes, b);
+    };
+    // Sequence and position of a token, and its (cos, sin) for this lane's dims.
+    auto locate = [&](int64_t tok, int &b, int &pos, float4 (&c)[4]) {
+        b = 0;
+        while (b + 1 < k.nseq && tok >= k.cu[b + 1]) ++b;
+        pos = k.start[b] + static_cast<int>(tok - k.cu[b]);
+        const float4 *tab = reinterpret_cast<const float4 *>(
+            k.rope + static_cast<int64_t>(pos < k.cap ? pos : 0) * (D / 2) + 8 * (sub % HALF));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = __ldg(tab + e);
+    };
+    if (lane == 0 && t < k.T) load(t, 0);
+    int b = 0, pos = 0;
+    float4 tab[4];
+    if (t < k.T) locate(t, b, pos, tab);
+    int abort_flag = 0;  // each warp gives up on its own
+    bool ok = true;
+    int i = 0;
+    for (; t < k.T; ++i, t += stride) {
+        const int s = i & 1;
+        const int64_t tn = t + stride;
+        if (lane == 0 && tn < k.T) load(tn, s ^ 1);  // the warp is done with that stage
+        int b_next = 0, pos_next = 0;
+        float4 tab_next[4];
+        if (tn < k.T) locate(tn, b_next, pos_next, tab_next);
+        ok = mbar_wait(bar0 + 8 * s, (i >> 1) & 1, &abort_flag, k.err, kKernQ4Rows, 2);
+        ok = __all_sync(FULL, ok);
+        if (!ok) break;
+        const bool in_cap = pos < k.cap;  // always, after host validation
+        if (!in_cap && lane == 0) set_error(k.err, kErrBounds, kKernQ4Rows, 1);
+        float2 cs[4], sn[4];
+        const float sgn = sub < HALF ? -1.f : 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cs[e] = make_float2(tab[e].x, tab[e].z);
+            sn[e] = make_float2(sgn * tab[e].y, sgn * tab[e].w);
+        }
+        const uint8_t *st = ring + s * stage_bytes;
+        auto staged = [&](int r) { return reinterpret_cast<const uint4 *>(st + static_cast<size_t>(r) * D * 2)[sub]; };
+        constexpr int U = 4;  // independent rows per lane group at a time
+#pragma unroll 1
+        for (int r0 = 0; r0 < nq; r0 += RPW * U) {  // warp-uniform
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = staged(min(r0 + u * RPW + grp, nq - 1));
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = q4_transform<D>(x[u], wq, cs, sn, k.eps);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPW + grp;
+                if (r < nq) reinterpret_cast<uint4 *>(k.qp + (t * k.Hq + hq0 + r) * D)[sub] = x[u];
+            }
+        }
+        const int64_t ws = static_cast<int64_t>(k.seq_slot0 + b) * k.seq_stride + static_cast<int64_t>(pos) * D;
+        const int64_t row = static_cast<int64_t>(p.seq0 + b) * p.row_seq + pos;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 2 * nkv; r0 += RPW * U) {  // K rows, then V rows
+            uint4 x[U], held[U];
+            uint32_t codes[U], scale[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = staged(nq + min(r0 + u * RPW + grp, 2 * nkv - 1));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r0 + u * RPW < nkv) {  // warp-uniform: some row of this pass is a key
+                    const uint4 y = q4_transform<D>(x[u], wk, cs, sn, k.eps);
+                    if (r0 + u * RPW + grp < nkv) x[u] = y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                uint32_t byte;
+                codes[u] = q4_quantise8<true>(x[u], byte, held[u]);
+                scale[u] = byte << (8 * (sub / 4));
+                scale[u] |= __shfl_xor_sync(FULL, scale[u], 4);
+                if (GR == 4) scale[u] |= __shfl_xor_sync(FULL, scale[u], 8);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = r0 + u * RPW + grp;
+                if (r >= 2 * nkv || !in_cap) continue;
+                const int kv = r >= nkv, h = hkv0 + (kv ? r - nkv : r);
+                const int64_t at = row + h * p.row_head;
+                reinterpret_cast<uint4 *>((kv ? k.vc : k.kc) + ws + h * k.head_stride)[sub] = held[u];
+                reinterpret_cast<uint32_t *>(p.codes[kv])[at * LPR + sub] = codes[u];
+                if (sub == 0) {
+                    if (GR == 4) reinterpret_cast<uint32_t *>(p.scales[kv])[at] = scale[u];
+                    else reinterpret_cast<uint16_t *>(p.scales[kv])[at] = static_cast<uint16_t>(scale[u]);
+                }
+            }
+        }
+        // The warp's reads of the stage come before the next bulk copy overwrites it.
+        fence_proxy_async_smem();
+        __syncwarp();
+        b = b_next;
+        pos = pos_next;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tab[e] = tab_next[e];
+    }
+    // Given up: a copy requested for a token that was not reached lands first.
+    if (lane == 0 && !ok && t + stride < k.T) {
+        int dummy = 0;
+        mbar_wait(bar0 + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1, &dummy, k.err, kKernQ4Rows, 3);
+    }
+}
+
+static size_t q4_prefill_rows_smem(int Hq, int Hkv, int D) {
+    const int parts = q4_row_parts(Hkv);
+    const size_t stage = (static_cast<size_t>(Hq / parts + 2 * (Hkv / parts)) * D * 2 + 127) & ~static_cast<size_t>(127);
+    return static_cast<size_t>(kQ4RowWarps) * 2 * stage + 128;
+}
+constexpr size_t kQ4RowSmemMost = 200 * 1024 + 128;
+
+bool q4_prefill_rows_fits(int Hq, int Hkv, int D) { return q4_prefill_rows_smem(Hq, Hkv, D) <= kQ4RowSmemMost; }
+
+template <int D>
+static cudaError_t q4_prefill_rows_t(const Q4PrefillRowsParams &p, cudaStream_t stream) {
+    static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
+    static std::atomic<int> sms_of[32] = {};
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    if (dev < 32 && ((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
+        sms = sms_of[dev].load(std::memory_order_relaxed);
+    } else {
+        cudaError_t e = cudaFuncSetAttribute(q4_prefill_rows_kernel<D>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kQ4RowSmemMost);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) {
+            sms_of[dev].store(sms, std::memory_order_relaxed);
+            configured.fetch_or(1u << dev, std::memory_order_release);
+        }
+    }
+    const int64_t need = (static_cast<int64_t>(p.k1.T) * q4_row_parts(p.k1.Hkv) + kQ4RowWarps - 1) / kQ4RowWarps;
+    q4_prefill_rows_kernel<D><<<static_cast<unsigned>(std::min<int64_t>(need, sms)), kQ4RowWarps * 32,
+                                q4_prefill_rows_smem(p.k1.Hq, p.k1.Hkv, D), stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsParams &p, int D, cudaStream_t stream) {
+    if (p.k1.T <= 0) return cudaSuccess;
+    return D == 128 ? q4_prefill_rows_t<128>(p, stream) : q4_prefill_rows_t<64>(p, stream);
 }
 
 static bool q4_rows_grid(const Q4RowsParams &p, unsigned &blocks) {

@@ -259,7 +259,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
 
 // One launch group of a prefill: up to ws_slots sequences.
 struct PrefillGroup {
-    qa::K1Params k1;
+    qa::Q4PrefillRowsParams rows;
     qa::Q4RowsParams quant, held;
     qa::K2Params k2;
     int items;
@@ -273,8 +273,8 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     const qa_config &g = c->cfg;
     const int D = g.head_dim, Hq = g.n_q_heads, Hkv = g.n_kv_heads;
     const int64_t ws_head = static_cast<int64_t>(g.capacity) * D, ws_seq = ws_head * Hkv;
-    qa::K1Params &k1 = pg.k1;
-    k1 = qa::K1Params{};
+    pg.rows = qa::Q4PrefillRowsParams{};
+    qa::K1Params &k1 = pg.rows.k1;
     k1.q = static_cast<const __nv_bfloat16 *>(q) + row0 * Hq * D;
     k1.k = static_cast<const __nv_bfloat16 *>(k) + row0 * Hkv * D;
     k1.v = static_cast<const __nv_bfloat16 *>(v) + row0 * Hkv * D;
@@ -293,8 +293,16 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     k1.cap = g.capacity;
     k1.eps = g.rms_eps;
     k1.nseq = n;
-    // The new rows, quantised in place: the workspace then holds what the cache holds.
+    // The new rows, for the two-kernel form: quantised in place, so that the
+    // workspace holds what the cache holds.
     pg.quant = make_rows(c, layer);
+    for (int i = 0; i < 2; ++i) {
+        pg.rows.codes[i] = pg.quant.codes[i];
+        pg.rows.scales[i] = pg.quant.scales[i];
+    }
+    pg.rows.row_seq = pg.quant.row_seq;
+    pg.rows.row_head = pg.quant.row_head;
+    pg.rows.seq0 = s0;
     fill_ranges(pg.quant, g, s0, n, start, ntok, 0);
     // The rows before them that a new token sees, from the first row of the
     // 128-key tile that holds the first one.
@@ -531,24 +539,39 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         PrefillGroup pg;
         if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
             return QA_ERR_CUDA;
-        row0 += pg.k1.T;
-        if (pg.k1.T > 0) groups.push_back(pg);
+        row0 += pg.rows.k1.T;
+        if (pg.rows.k1.T > 0) groups.push_back(pg);
     }
     if (cudaStreamWaitEvent(s, c->ws_free, 0) != cudaSuccess) return QA_ERR_CUDA;
     int32_t *next = next_of(c, layer);
     for (int b = 0; b < batch; ++b)
         if (ntok[b] > 0) next[b] = start[b] + ntok[b];
+    const bool fused = qa::q4_prefill_rows_fits(c->cfg.n_q_heads, c->cfg.n_kv_heads, c->cfg.head_dim);
     for (PrefillGroup &pg : groups) {
-        if (qa::launch_k1(pg.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-        qa::launch_order().barrier(s);
-        c->launches[QA_Q4_KERNEL_NORM_ROPE]++;
-        if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-        c->launches[QA_Q4_KERNEL_QUANTISE]++;
+        // The older rows first: K2 then follows the kernel that lets it start early.
         if (pg.held.nblocks > 0) {
             if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
         }
-        if (qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s) != cudaSuccess) return QA_ERR_CUDA;
+        if (fused) {
+            pg.rows.k1.signal_early = 1;
+            if (qa::launch_q4_prefill_rows(pg.rows, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            qa::launch_order().barrier(s);
+            c->launches[QA_Q4_KERNEL_QUANTISE]++;
+        } else {
+            if (qa::launch_k1(pg.rows.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            qa::launch_order().barrier(s);
+            c->launches[QA_Q4_KERNEL_NORM_ROPE]++;
+            if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+            c->launches[QA_Q4_KERNEL_QUANTISE]++;
+        }
+        if (qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s) != cudaSuccess) {
+            // A kernel that signalled early is no longer followed by one that
+            // waits for it: let it finish before anything else is enqueued.
+            cudaStreamSynchronize(s);
+            return QA_ERR_CUDA;
+        }
         qa::launch_order().barrier(s);
         c->launches[QA_Q4_KERNEL_PREFILL_ATTN]++;
     }

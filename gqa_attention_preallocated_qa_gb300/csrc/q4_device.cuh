@@ -25,19 +25,25 @@
 
 namespace qa {
 
-constexpr float kQ4MaxScale = 56.f;          // scale byte 0x53
+constexpr uint32_t kQ4MaxScale = 0x53u;      // scale byte of 56
 constexpr uint32_t kQ4NanScale = 0x7Fu;      // group with a value that is not finite
 
-// Byte of the fp16 number with 3 significant bits nearest to t (0 <= t <= 56),
-// ties to the even byte.  t's bits, rounded to 2 mantissa bits; below 2^-14
-// the steps are 2^-16.
-__device__ __forceinline__ uint32_t q4_scale_byte(float t) {
-    if (t < 6.103515625e-05f) return static_cast<uint32_t>(__float2int_rn(t * 65536.f));
-    const uint32_t u = __float_as_uint(t);
-    return ((u + 0x000FFFFFu + ((u >> 21) & 1u)) >> 21) - ((127u - 15u) << 2);
-}
 __device__ __forceinline__ float q4_scale_value(uint32_t byte) {
     return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 8)));
+}
+
+// Scale byte for a largest magnitude with bf16 bits `top` (finite): that of the
+// number with 3 significant bits nearest to top / 7, ties to the even byte;
+// not yet held to kQ4MaxScale.  With top = M 2^(e - 134), M in 128..255, the
+// candidates are 16, 20, 24, 28, 32, 40 times 2^(e - 134), and M / 7 passes
+// the borders between them (ties at M = 154, 182, 210, 252) as the comparisons
+// below say.  Scales below 2^-14 are multiples of 2^-16: their quotient is
+// divided exactly rounded, so that a tie comes out as one.
+__device__ __forceinline__ uint32_t q4_scale_byte(uint32_t top) {
+    const uint32_t e = top >> 7, m = top & 127u;
+    if (e <= 115u)
+        return static_cast<uint32_t>(__float2int_rn(__fdiv_rn(__uint_as_float(top << 16) * 65536.f, 7.f)));
+    return (e - 115u) * 4u + 1u + (m >= 154u - 128u) + (m > 182u - 128u) + (m >= 210u - 128u) + (m > 252u - 128u);
 }
 
 // Quantises the 8 values in xv, whose group's other values are in the three
@@ -45,17 +51,18 @@ __device__ __forceinline__ float q4_scale_value(uint32_t byte) {
 // the 8 codes; `byte` is the group's scale byte and, when kHeld, `held` the
 // 8 values that the codes stand for.
 //
-// max|x| / 7 is divided exactly rounded: a quotient that is a midpoint of two
-// scales (3 + 1 bits, times 7: a bf16 value) comes out as that midpoint, every
-// other one lies at least 2^-8 relative from it.  For the codes x / s may be a
-// product with the reciprocal: a quotient that is a half has (2k + 1) s / 2
-// with 4 + 3 bits, so bf16 values hit halves exactly or miss them by 2^-8
-// relative, and stretching the reciprocal by 2^-14 sends halves away from zero
-// whatever the last bits of the product are.
+// For the codes x / s may be a product with the reciprocal: a quotient that is
+// a half has (2k + 1) s / 2 with 4 + 3 bits, so bf16 values hit halves exactly
+// or miss them by 2^-8 relative, and stretching the reciprocal by 2^-14 sends
+// halves away from zero whatever the last bits of the product are.  Added to
+// 1.5 * 2^23 + 8 the quotient rounds to an integer in the low mantissa bits;
+// |x| / s is at most 7.9 (s is within 1/9 of max|x| / 7), so only codes of 16
+// have to be held to 15; under the largest scale and those below 2^-14, which
+// may be further from max|x| / 7, x itself is held first.
 template <bool kHeld>
 __device__ __forceinline__ uint32_t q4_quantise8(uint4 xv, uint32_t &byte, uint4 &held) {
     const unsigned FULL = 0xffffffffu;
-    const uint32_t w[4] = {xv.x, xv.y, xv.z, xv.w};
+    uint32_t w[4] = {xv.x, xv.y, xv.z, xv.w};
     uint32_t mx = 0;  // largest |x| of the pairs, as bf16 bit patterns (they order like integers)
 #pragma unroll
     for (int e = 0; e < 4; ++e) mx = __vmaxu2(mx, w[e] & 0x7fff7fffu);
@@ -63,30 +70,39 @@ __device__ __forceinline__ uint32_t q4_quantise8(uint4 xv, uint32_t &byte, uint4
     mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
     mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
     const bool finite = mx < 0x7F80u;
-    byte = q4_scale_byte(finite ? fminf(__fdiv_rn(__uint_as_float(mx << 16), 7.f), kQ4MaxScale) : 0.f);
-    const float s = finite ? q4_scale_value(byte) : q4_scale_value(kQ4NanScale);
-    const float r = (finite && byte != 0u) ? __fdividef(1.00006103515625f, s) : 0.f;
-    // kMagic + 8 + x / s rounds to an integer in the low mantissa bits.
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-    constexpr uint32_t kMagicBits = 0x4B400000u;
-    uint32_t codes = 0;
-    uint32_t hw[4];
+    byte = finite ? q4_scale_byte(mx) : kQ4NanScale;
+    if (finite && (byte > kQ4MaxScale || byte < 4u)) {
+        byte = min(byte, kQ4MaxScale);
+        const uint32_t most = (__float_as_uint(8.f * q4_scale_value(byte)) >> 16) * 0x00010001u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // |x| at most 8 s
+            w[e] = (w[e] & 0x80008000u) | __vminu2(w[e] & 0x7fff7fffu, most);
+    }
+    const float s = q4_scale_value(byte);
+    const float r = finite && byte != 0u ? __fdividef(1.00006103515625f, s) : 0.f;
+    constexpr float kMagic = 12582912.f + 8.f;
+    uint32_t n[4];  // codes of pairs, in 16-bit halves
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float y0 = fmaf(bf16lo(w[e]), r, kMagic + 8.f);
-        float y1 = fmaf(bf16hi(w[e]), r, kMagic + 8.f);
-        y0 = fminf(fmaxf(y0, kMagic), kMagic + 15.f);
-        y1 = fminf(fmaxf(y1, kMagic), kMagic + 15.f);
-        codes |= ((__float_as_uint(y0) - kMagicBits) | ((__float_as_uint(y1) - kMagicBits) << 4)) << (8 * e);
-        if (kHeld) hw[e] = pack_bf16((y0 - (kMagic + 8.f)) * s, (y1 - (kMagic + 8.f)) * s);
+        const float y0 = fmaf(bf16lo(w[e]), r, kMagic), y1 = fmaf(bf16hi(w[e]), r, kMagic);
+        n[e] = __vminu2(__byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x5410), 0x000F000Fu);
     }
-    if (!finite) {
-        codes = 0x88888888u;
-        byte = kQ4NanScale;
-        hw[0] = hw[1] = hw[2] = hw[3] = 0x7FFF7FFFu;
+    const uint32_t even = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+    const uint32_t odd = __byte_perm(__byte_perm(n[0], n[1], 0x0062), __byte_perm(n[2], n[3], 0x0062), 0x5410);
+    uint32_t codes = even | (odd << 4);
+    if (kHeld) {
+        const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
+        const __nv_bfloat162 off = __hmul2(s2, __float2bfloat162_rn(-136.f));
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t u = n[e] | 0x43004300u;
+            const __nv_bfloat162 x = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&u), s2, off);
+            h[e] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+        held = make_uint4(h[0], h[1], h[2], h[3]);  // (NaN under the scale NaN)
     }
-    if (kHeld) held = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    return codes;
+    return finite ? codes : 0x88888888u;
 }
 
 // The 8 values of a word of codes with scale byte `byte`, as bf16.

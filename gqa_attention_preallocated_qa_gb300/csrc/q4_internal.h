@@ -45,6 +45,17 @@ static_assert(sizeof(Q4RowsParams) <= 4096, "travels in the 4 KB of kernel param
 // Tokens of one head that one warp quantises or dequantises.
 __host__ __device__ constexpr int q4_block_tokens(int D) { return D == 128 ? 16 : 32; }
 
+// The transform of a prefill's rows (K1) with the keys and values quantised on
+// the way: k1 as for K1, its cache pointers and strides those of the bf16
+// workspace, which receives the values that the codes stand for.
+struct Q4PrefillRowsParams {
+    K1Params k1;
+    uint8_t *codes[2], *scales[2];       // layer base of K and V
+    int64_t row_seq, row_head;           // cache strides in rows
+    int seq0;                            // cache slot of the first sequence
+};
+static_assert(sizeof(Q4PrefillRowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
+
 constexpr int kQ4Chunk = 32;       // keys of one pipeline chunk of the decode kernel
 constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
 constexpr int kQ4MaxSplits = 16;   // splits of one (sequence, kv head) = CTAs of one cluster
@@ -77,6 +88,10 @@ struct Q4DecodeParams {
 static_assert(sizeof(Q4DecodeParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
 cudaError_t launch_q4_quantise(const Q4RowsParams &p, int D, cudaStream_t stream);
+// False when a token of this geometry does not fit the kernel's stages: the
+// rows then go through K1 and launch_q4_quantise.
+bool q4_prefill_rows_fits(int Hq, int Hkv, int D);
+cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q4_dequantise(const Q4RowsParams &p, int D, cudaStream_t stream);
 // HPC heads x TPS tokens per CTA (TPS = 1, or 8 / HPC for launches of several tokens).
 cudaError_t launch_q4_decode(const Q4DecodeParams &p, int D, int HPC, bool multi, cudaStream_t stream);

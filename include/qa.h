@@ -386,8 +386,8 @@ typedef struct qa_q4_cache qa_q4_cache; /* opaque */
 
 /* Kernels counted by qa_q4_stats. */
 enum {
-    QA_Q4_KERNEL_NORM_ROPE = 0,    /* K1, writing a prefill's rows to the workspace */
-    QA_Q4_KERNEL_QUANTISE = 1,     /* K4: rows into the cache */
+    QA_Q4_KERNEL_NORM_ROPE = 0,    /* K1, for geometries whose token does not fit K4's transform */
+    QA_Q4_KERNEL_QUANTISE = 1,     /* K4: rows into the cache (a prefill's: with norm and rotation) */
     QA_Q4_KERNEL_DEQUANTISE = 2,   /* K4: rows out of the cache */
     QA_Q4_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace */
     QA_Q4_KERNEL_DECODE = 4,       /* K5: decode steps and chunks of up to 8 tokens */
@@ -433,7 +433,7 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * new token attends causally to what the cache then holds (its own rows as
  * held, too), within the layer's window.
  * With every ntok at most 8 the decode kernel does all of it, one launch per
- * 64 sequences.  Otherwise K1, K4 and K2 run through the cache's workspace, 8
+ * 64 sequences.  Otherwise K4 and K2 run through the cache's workspace, 8
  * sequences at a time: such calls on several streams wait for each other, and
  * they cannot be captured into a graph (QA_ERR_STATE).
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
