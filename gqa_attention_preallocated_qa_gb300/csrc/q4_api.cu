@@ -131,11 +131,22 @@ void packed_rows(const qa_config &g, int64_t &tok, int64_t &head) {
     head = g.head_dim;
 }
 
+// Tokens per lane group of a quantising launch of T rows.  Eight make the fewest
+// warps and the longest runs (57,000 rows of 8 heads, D 128: 86 us against 91
+// with four), but a grid that the device holds at once loads, computes and
+// stores in step; there four overlap better (5120 rows: 10.7 us against 12.7).
+// The border is about four times what the device holds.
+int quantise_unroll(const qa_q4_cache *c, int64_t T) {
+    const int64_t warps = T / qa::q4_block_tokens(c->cfg.head_dim, 8) * c->cfg.n_kv_heads * 2;
+    return warps > static_cast<int64_t>(c->num_sms) * 128 ? 8 : 4;
+}
+
 // The rows of sequences s0 .. s0 + n - 1 of a call on packed tensors, row0 the
 // first one's first packed row; false when there is none.
 bool fill_ranges(qa::Q4RowsParams &p, const qa_config &g, int s0, int n, const int32_t *start,
-                 const int32_t *ntok, int64_t row0) {
-    const int per = qa::q4_block_tokens(g.head_dim);
+                 const int32_t *ntok, int64_t row0, int unroll) {
+    const int per = qa::q4_block_tokens(g.head_dim, unroll);
+    p.unroll = unroll;
     p.nseq = n;
     p.seq0 = s0;
     p.nblocks = 0;
@@ -303,7 +314,7 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     pg.rows.row_seq = pg.quant.row_seq;
     pg.rows.row_head = pg.quant.row_head;
     pg.rows.seq0 = s0;
-    fill_ranges(pg.quant, g, s0, n, start, ntok, 0);
+    fill_ranges(pg.quant, g, s0, n, start, ntok, 0, 8);
     // The rows before them that a new token sees, from the first row of the
     // 128-key tile that holds the first one.
     pg.held = make_rows(c, layer);
@@ -313,7 +324,7 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         from[i] = W > 0 ? std::max(0, P + 1 - W) / 128 * 128 : 0;
         count[i] = ntok[s0 + i] > 0 ? P - from[i] : 0;
     }
-    fill_ranges(pg.held, g, 0, n, from, count, 0);
+    fill_ranges(pg.held, g, 0, n, from, count, 0, 4);
     pg.held.seq0 = s0;
     for (qa::Q4RowsParams *r : {&pg.quant, &pg.held}) {
         r->src_tok = r->dst_tok = D;
@@ -453,11 +464,12 @@ QA_API qa_status qa_q4_append(qa_q4_cache *c, int layer, int batch, const int32_
     p.dst[1] = static_cast<__nv_bfloat16 *>(v_held);
     packed_rows(g, p.src_tok, p.src_head);
     packed_rows(g, p.dst_tok, p.dst_head);
+    const int unroll = quantise_unroll(c, T);
     int32_t *next = next_of(c, layer);
     int64_t row0 = 0;
     for (int s0 = 0; s0 < batch; s0 += qa::kQ4MaxSeqPerLaunch) {
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
-        if (fill_ranges(p, g, s0, n, start, ntok, row0)) {
+        if (fill_ranges(p, g, s0, n, start, ntok, row0, unroll)) {
             if (qa::launch_q4_quantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
@@ -493,7 +505,7 @@ QA_API qa_status qa_q4_read(qa_q4_cache *c, int layer, int batch, const int32_t 
     int64_t row0 = 0;
     for (int s0 = 0; s0 < batch; s0 += qa::kQ4MaxSeqPerLaunch) {
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
-        if (fill_ranges(p, g, s0, n, start, ntok, row0)) {
+        if (fill_ranges(p, g, s0, n, start, ntok, row0, 4)) {
             if (qa::launch_q4_dequantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;

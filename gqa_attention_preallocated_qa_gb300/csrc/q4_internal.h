@@ -35,6 +35,7 @@ struct Q4RowsParams {
     int64_t src_tok, src_head, dst_tok, dst_head;
     int64_t row_seq, row_head;           // cache strides in rows: sequence, head
     int nseq, Hkv, nblocks, kv_first, kv_count;  // kv_first/count: K (0) and V (1) served
+    int unroll;                          // tokens per lane group of a block: 4 or 8
     int seq0;                            // cache slot of launched sequence 0
     int start[kQ4MaxSeqPerLaunch], ntok[kQ4MaxSeqPerLaunch];
     int block0[kQ4MaxSeqPerLaunch + 1];  // first token block of each launched sequence
@@ -42,8 +43,9 @@ struct Q4RowsParams {
 };
 static_assert(sizeof(Q4RowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
-// Tokens of one head that one warp quantises or dequantises.
-__host__ __device__ constexpr int q4_block_tokens(int D) { return D == 128 ? 16 : 32; }
+// Tokens of one head that one warp quantises or dequantises: `unroll` per lane
+// group, D/8 lanes each.
+__host__ __device__ constexpr int q4_block_tokens(int D, int unroll) { return unroll * (32 / (D / 8)); }
 
 // The transform of a prefill's rows (K1) with the keys and values quantised on
 // the way: k1 as for K1, its cache pointers and strides those of the bf16
