@@ -351,38 +351,46 @@ def qa_q4_cache_set_window(cache, layer, window) -> None:
     _check(lib.qa_q4_cache_set_window(cache, layer, window), "qa_q4_cache_set_window")
 
 
+def _at(x):
+    """Address of a tensor; an address or None as it is."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return x
+
+
 def qa_q4_append(cache, layer, start, ntok, k, v, k_held=None, v_held=None, stream=None) -> None:
     n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_append(cache, layer, n, s, t, _ptr(k), _ptr(v), _ptr(k_held), _ptr(v_held),
+    _check(lib.qa_q4_append(cache, layer, n, s, t, _at(k), _at(v), _at(k_held), _at(v_held),
                             _q4_stream(stream)), "qa_q4_append")
 
 
 def qa_q4_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
     n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_read(cache, layer, n, s, t, _ptr(k_out), _ptr(v_out), _q4_stream(stream)),
+    _check(lib.qa_q4_read(cache, layer, n, s, t, _at(k_out), _at(v_out), _q4_stream(stream)),
            "qa_q4_read")
 
 
 def qa_q4_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
                   stream=None) -> None:
     n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_prefill(cache, layer, n, s, t, _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
-                             _ptr(k_norm_w), _ptr(out), _q4_stream(stream)), "qa_q4_prefill")
+    _check(lib.qa_q4_prefill(cache, layer, n, s, t, _at(q), _at(k), _at(v), _at(q_norm_w),
+                             _at(k_norm_w), _at(out), _q4_stream(stream)), "qa_q4_prefill")
 
 
 def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
                       v_held=None, stream=None) -> None:
-    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_bytes(positions), _ptr(q), _ptr(k),
-                                 _ptr(v), _ptr(q_norm_w), _ptr(k_norm_w), _ptr(out), _ptr(k_held),
-                                 _ptr(v_held), _q4_stream(stream)), "qa_q4_decode_step")
+    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_bytes(positions), _at(q), _at(k),
+                                 _at(v), _at(q_norm_w), _at(k_norm_w), _at(out), _at(k_held),
+                                 _at(v_held), _q4_stream(stream)), "qa_q4_decode_step")
 
 
 def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
                                        out, k_held=None, v_held=None, stream=None) -> None:
     """positions: int32 device tensor [batch] (see include/qa.h)."""
     _check(lib.qa_q4_decode_step_device_positions(
-        cache, layer, batch, _ptr(positions), _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm_w),
-        _ptr(k_norm_w), _ptr(out), _ptr(k_held), _ptr(v_held), _q4_stream(stream)),
+        cache, layer, batch, _at(positions), _at(q), _at(k), _at(v), _at(q_norm_w),
+        _at(k_norm_w), _at(out), _at(k_held), _at(v_held), _q4_stream(stream)),
            "qa_q4_decode_step_device_positions")
 
 

@@ -8,8 +8,8 @@
 //   1. the CTA streams its keys through a ring of stages in shared memory, 256
 //      keys each (32 per warp): a stage is four contiguous runs of the cache
 //      (codes and scale bytes of K and V, 34 KB at D = 128), one bulk copy each.
-//      The warps take turns at sending a stage out again, one iteration after
-//      its use, so none waits for the others in the ordinary case;
+//      The warp that leaves a stage last sends it out again: none waits for
+//      the others;
 //   2. the CTA's query rows (HPC heads x TPS tokens, at most 8) are normed,
 //      rotated and brought to fp16 with one power of two per row; the last
 //      split's CTA quantises the new tokens' k' and v, writes them to the cache
@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 #include <type_traits>
 
 #include "q4_device.cuh"
@@ -65,6 +66,14 @@ struct Q4Shape {
     static_assert(kQ4DecodeWarps * kPartial * 4 <= kRing, "the warps' partials fit the ring");
     static_assert(kScales % 128 == 0 && kScaleRow * kQ4Chunk % 16 == 0, "bulk copies are 16-byte multiples");
 };
+
+// Counts this warp out of a ring stage; returns the count before it.  Whoever
+// sees the last count also sees that every counted warp's reads are done.
+__device__ __forceinline__ uint32_t shared_inc(uint32_t a) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(old) : "r"(a) : "memory");
+    return old;
+}
 
 // Waits with their slow part out of line (a launch meets its code cold).
 __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
@@ -360,7 +369,9 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     const unsigned FULL = 0xffffffffu;
 
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_recv;
+    __shared__ __align__(8) uint64_t bar_full[NS], bar_recv;
+    __shared__ uint32_t s_left[NS];  // warps that have left a ring stage, over all its uses
+    __shared__ int s_sent[NS];       // last stage of keys sent to it (-1: none)
     __shared__ int s_abort;
     __shared__ __align__(16) __nv_bfloat16 s_newk[TPS * D], s_newv[TPS * D];  // as the cache holds them
     __shared__ float s_c[R];  // log2 units per raw score of a row
@@ -434,18 +445,19 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const uint32_t bar = smem_u32(&bar_full[st]);
         const int64_t r0 = row_base + static_cast<int64_t>(c) * kQ4Chunk;
         uint32_t dst = smem_u32(smem + st * Sh::kStage);
+        s_sent[st] = j;
         mbar_expect_tx(bar, keys * 2 * (Sh::kRow + Sh::kScaleRow));
         bulk_g2s(dst, p.kc + r0 * Sh::kRow, keys * Sh::kRow, bar);
         bulk_g2s(dst + 2 * Sh::kCodes, p.ks + r0 * Sh::kScaleRow, keys * Sh::kScaleRow, bar);
         bulk_g2s(dst + Sh::kCodes, p.vc + r0 * Sh::kRow, keys * Sh::kRow, bar);
         bulk_g2s(dst + 2 * Sh::kCodes + Sh::kScales, p.vs + r0 * Sh::kScaleRow, keys * Sh::kScaleRow, bar);
     };
-    int sent = 0;        // thread 0: stages of the first round on the way
-    int my_stage = -1;   // last stage of later rounds that this thread sent
+    int sent = 0;  // thread 0: stages of the first round on the way
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&bar_full[s]), 1);
-            mbar_init(smem_u32(&bar_empty[s]), NW);
+            s_left[s] = 0;
+            s_sent[s] = -1;
         }
         mbar_init(smem_u32(&bar_recv), 1);
         s_abort = 0;
@@ -607,10 +619,9 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         }
         int st = 0;
         uint32_t phase = 0;
-        bool ok = true;
 #pragma unroll 1
         for (int j = 0; j < nstages; ++j) {
-            ok = q4_wait(smem_u32(&bar_full[st]), phase, &s_abort, p.err, 2);
+            bool ok = q4_wait(smem_u32(&bar_full[st]), phase, &s_abort, p.err, 2);
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             const int c = c_begin + j * NW + warp;
@@ -637,30 +648,15 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 }
             }
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&bar_empty[st]));
-                // The stage before this one goes out again once every warp has left
-                // it; the warps take turns.
-                const int jn = j - 1 + NS;
-                if (j > 0 && jn < nstages && (j % NW) == warp) {
-                    const int sp = st == 0 ? NS - 1 : st - 1;
-                    if (q4_wait(smem_u32(&bar_empty[sp]), (st == 0 ? phase ^ 1u : phase), &s_abort, p.err, 3)) {
-                        if (early && min(c_end, c_begin + (jn + 1) * NW) > c_safe) griddep_wait();
-                        issue(jn);
-                        my_stage = jn;
-                    }
-                }
+            // The warp that leaves the stage last sends it out again.
+            if (lane == 0 && j + NS < nstages && (shared_inc(smem_u32(&s_left[st])) + 1u) % NW == 0u) {
+                if (early && min(c_end, c_begin + (j + NS + 1) * NW) > c_safe) griddep_wait();
+                issue(j + NS);
             }
             if (++st == NS) {
                 st = 0;
                 phase ^= 1u;
             }
-        }
-        if (!ok && lane == 0) {  // given up: no copy may land after the CTA exits
-            int dummy = 0;
-            for (int j = 0; j < sent; ++j) mbar_wait(smem_u32(&bar_full[j]), 0, &dummy, p.err, kKernQ4Decode, 6);
-            if (my_stage >= 0)
-                mbar_wait(smem_u32(&bar_full[my_stage % NS]), (my_stage / NS) & 1, &dummy, p.err, kKernQ4Decode, 6);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -669,6 +665,12 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             a.l[x] += __shfl_xor_sync(FULL, a.l[x], 16);
         }
         __syncthreads();  // every warp has left the ring: the partials take its place
+        if (s_abort && threadIdx.x == 0) {  // given up: no copy may land after the CTA exits
+            int dummy = 0;
+            for (int s = 0; s < NS; ++s)
+                if (s_sent[s] >= 0)
+                    mbar_wait(smem_u32(&bar_full[s]), (s_sent[s] / NS) & 1, &dummy, p.err, kKernQ4Decode, 6);
+        }
         float *part = reinterpret_cast<float *>(smem) + warp * Sh::kPartial;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -847,26 +849,28 @@ static cudaError_t q4_launch(const Q4DecodeParams &p, cudaStream_t stream) {
 }
 
 template <int D, int HPC, int TPS>
-static int q4_capacity(int S) {
-    static std::atomic<int> cache[32][kQ4MaxSplits + 1] = {};  // clusters + 1; 0: not asked yet
+static const int *q4_capacities() {
+    static int table[32][kQ4MaxSplits + 1];
+    static std::atomic<unsigned> known{0u};  // devices 0..31
+    static std::mutex mu;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-    if (dev < 32) {
-        const int known = cache[dev][S].load(std::memory_order_acquire);
-        if (known) return known - 1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 32) return nullptr;
+    if ((known.load(std::memory_order_acquire) >> dev) & 1u) return table[dev];
+    std::lock_guard<std::mutex> lock(mu);
+    bool failed = q4_configure<D, HPC, TPS>() != cudaSuccess;
+    for (int S = 1; S <= kQ4MaxSplits && !failed; ++S) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        q4_config<D, HPC, TPS>(cfg, attr, S, 1, 1, nullptr);
+        cfg.numAttrs = 1;
+        failed = cudaOccupancyMaxActiveClusters(&table[dev][S], q4_decode_kernel<D, HPC, TPS>, &cfg) != cudaSuccess;
     }
-    int n = 0;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    q4_config<D, HPC, TPS>(cfg, attr, S, 1, 1, nullptr);
-    cfg.numAttrs = 1;
-    if (q4_configure<D, HPC, TPS>() != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, q4_decode_kernel<D, HPC, TPS>, &cfg) != cudaSuccess) {
+    if (failed) {
         cudaGetLastError();
-        n = 0;
+        return nullptr;
     }
-    if (dev < 32) cache[dev][S].store(n + 1, std::memory_order_release);
-    return n;
+    known.fetch_or(1u << dev, std::memory_order_release);
+    return table[dev];
 }
 
 // Calls f<D, HPC, TPS>(args...) for the run-time shape.
@@ -890,10 +894,9 @@ cudaError_t launch_q4_decode(const Q4DecodeParams &p, int D, int HPC, bool multi
     return cudaErrorInvalidValue;
 }
 
-int q4_cluster_capacity(int D, int HPC, bool multi, int S) {
-    if (S < 1 || S > kQ4MaxSplits) return 0;
-    QA_Q4_DISPATCH(q4_capacity, S);
-    return 0;
+const int *q4_cluster_capacities(int D, int HPC, bool multi) {
+    QA_Q4_DISPATCH(q4_capacities, );
+    return nullptr;
 }
 
 }  // namespace qa

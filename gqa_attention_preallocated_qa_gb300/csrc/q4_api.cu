@@ -162,14 +162,34 @@ bool fill_ranges(qa::Q4RowsParams &p, const qa_config &g, int s0, int n, const i
     return p.nblocks > 0;
 }
 
-// Largest split count whose clusters of one launch all fit on the device at
-// once, with at least a chunk for each warp.
+// Splits of a sequence and kv head (CTAs of a cluster).  A CTA costs a fixed
+// part (its prologue and the merge) and a part per stage of 256 keys; CTAs that
+// share an SM slow each other down.  Fitted on GB300 (D = 128, steps apart from
+// each other, 512 to 16384 keys, 8 to 192 groups): 2.6 us + 1.1 us a stage for a
+// CTA alone on its SM, 3.6 + 1.85 for two; at D = 64 a stage costs 0.66 times
+// that.  CTAs get SMs of their own as long as the launch has at most 96 of them,
+// or 128 in clusters of up to 4.  Only plans whose clusters all fit on the device
+// at once are weighed, the fewest CTAs among equals.  (B = 4, 8 kv heads: 4
+// splits at 2048 keys take 7.8 us and 8 take 8.4; at 16384 keys 23.2 and 21.4.)
 int choose_splits(int D, int HPC, bool multi, int groups, int keys) {
     const int chunks = (keys + qa::kQ4Chunk - 1) / qa::kQ4Chunk;
-    int S = std::min(qa::kQ4MaxSplits, std::max(1, (chunks + qa::kQ4DecodeWarps - 1) / qa::kQ4DecodeWarps));
-    for (; S > 1; --S)
-        if (qa::q4_cluster_capacity(D, HPC, multi, S) >= groups) break;
-    return S;
+    const float stage = D == 128 ? 1.f : 0.66f;
+    const int *held = qa::q4_cluster_capacities(D, HPC, multi);
+    if (!held) return 1;
+    int best = 1;
+    float least = 1e30f;
+    for (int S = 1; S <= qa::kQ4MaxSplits && (S == 1 || S <= chunks); ++S) {
+        if (S > 1 && held[S] < groups) continue;
+        const int64_t ctas = static_cast<int64_t>(groups) * S;
+        const int rounds = ((chunks + S - 1) / S + qa::kQ4DecodeWarps - 1) / qa::kQ4DecodeWarps;
+        const bool alone = ctas <= (S <= 4 ? 128 : 96);
+        const float us = alone ? 2.6f + 1.1f * stage * rounds : 3.6f + 1.85f * stage * rounds;
+        if (us < least - 0.01f) {
+            least = us;
+            best = S;
+        }
+    }
+    return best;
 }
 
 struct DecodeCall {
@@ -276,6 +296,80 @@ struct PrefillGroup {
     int items;
 };
 
+// A run of query blocks of one sequence of a prefill launch: rows first ..
+// first + len - 1 of its new tokens.
+struct QueryRun {
+    int seq, first, len;
+};
+
+// Time of the prefill attention of `runs` in units of key tiles: its items are
+// dealt out level by level (the block within its run, the highest first), then
+// by run, to `workers` in snake order; a block costs its key tiles and about
+// one more.  `copies`: items of a block (kv heads and head groups).
+int prefill_span(const std::vector<QueryRun> &runs, const int32_t *start, int window, int copies, int workers,
+                 std::vector<int> &load) {
+    load.assign(workers, 0);
+    int levels = 0, idx = 0;
+    for (const QueryRun &r : runs) levels = std::max(levels, (r.len + 127) / 128);
+    for (int lvl = levels - 1; lvl >= 0; --lvl)
+        for (const QueryRun &r : runs) {
+            if (r.len <= lvl * 128) continue;
+            const int pos = start[r.seq] + r.first + lvl * 128;
+            const int from = window > 0 ? std::max(0, pos + 1 - window) / 128 : 0;
+            const int tiles = (pos + std::min(r.len - 1 - lvl * 128, 127)) / 128 + 1 - from + 1;
+            for (int k = 0; k < copies; ++k, ++idx) {
+                const int round = idx / workers, at = idx % workers;
+                load[round & 1 ? workers - 1 - at : at] += tiles;
+            }
+        }
+    return *std::max_element(load.begin(), load.end());
+}
+
+// The runs a prefill launch is made of.  The kernel deals its items out by the
+// block's place in its run, which is their weight when every sequence starts at
+// 0; behind caches of different lengths it is not, and heavy blocks dealt late
+// leave most of the device idle at the end.  So the sequences go in by falling
+// start, and the ones that start lowest may be cut into shorter runs (up to the
+// 8 of a launch), whose blocks then come later.  Results are the same bits: an
+// item does not depend on its neighbours.  (777 tokens behind 4099 and 1001
+// behind 1025, 32 / 8 heads: 124 us as two runs, 86 us cut.)
+void plan_runs(std::vector<QueryRun> &runs, const int32_t *start, int window, const qa_q4_cache *c) {
+    const int G = c->G, D = c->cfg.head_dim;
+    std::stable_sort(runs.begin(), runs.end(), [&](const QueryRun &x, const QueryRun &y) { return start[x.seq] > start[y.seq]; });
+    bool same = true;
+    int blocks = 0;
+    for (const QueryRun &r : runs) {
+        same = same && start[r.seq] == start[runs[0].seq];
+        blocks += (r.len + 127) / 128;
+    }
+    // Workers and items of the form that the launch takes: pairs of CTAs on four
+    // heads, else CTAs on two heads or one.
+    int workers = c->num_sms / 2, copies = c->cfg.n_kv_heads * (G / 4);
+    if (D != 128 || G % 4 || blocks * copies < workers) {
+        workers = c->num_sms;
+        copies = c->cfg.n_kv_heads * ((G + 1) / 2);
+        if (G > 1 && blocks * copies < workers) copies = c->cfg.n_kv_heads * G;
+    }
+    if (same || blocks * copies <= workers || blocks > 256) return;
+    std::vector<int> load;
+    std::vector<QueryRun> best = runs;
+    int least = prefill_span(runs, start, window, copies, workers, load);
+    for (size_t cut = 1; cut <= runs.size(); ++cut)        // the last `cut` sequences
+        for (int m : {1, 2, 3, 4, 6, 8}) {                  // into runs of m blocks
+            std::vector<QueryRun> tried(runs.begin(), runs.end() - cut);
+            for (size_t i = runs.size() - cut; i < runs.size(); ++i)
+                for (int at = (runs[i].len - 1) / (128 * m) * (128 * m); at >= 0; at -= 128 * m)
+                    tried.push_back({runs[i].seq, at, std::min(128 * m, runs[i].len - at)});
+            if (tried.size() > static_cast<size_t>(qa::kMaxSeqPerLaunch) || tried.size() == runs.size()) continue;
+            const int span = prefill_span(tried, start, window, copies, workers, load);
+            if (span < least) {
+                least = span;
+                best = tried;
+            }
+        }
+    runs = best;
+}
+
 // Builds the launches for sequences s0 .. s0 + n - 1; false when a tensor map
 // cannot be made.
 bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start, const int32_t *ntok,
@@ -338,25 +432,28 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     }
     qa::K2Params &k2 = pg.k2;
     k2 = qa::K2Params{};
-    int nseq = 0, rows = 0, maxqb = 0;
-    pg.items = 0;
+    std::vector<QueryRun> runs;
     k1.cu[0] = 0;
     for (int i = 0; i < n; ++i) {
-        const int L = ntok[s0 + i], P = start[s0 + i];
-        k1.cu[i + 1] = k1.cu[i] + L;
-        k1.start[i] = P;
-        if (L > 0) {
-            if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + i * ws_seq, D, P + L, Hkv, g.capacity, 64) ||
-                !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + i * ws_seq, D, P + L, Hkv, g.capacity, 128))
-                return false;
-            k2.len[nseq] = L;
-            k2.start[nseq] = P;
-            k2.cu[nseq] = rows;
-            maxqb = std::max(maxqb, (L + 127) / 128);
-            pg.items += (L + 127) / 128;
-            ++nseq;
-        }
-        rows += L;
+        k1.cu[i + 1] = k1.cu[i] + ntok[s0 + i];
+        k1.start[i] = start[s0 + i];
+        if (ntok[s0 + i] > 0) runs.push_back({i, 0, ntok[s0 + i]});
+    }
+    plan_runs(runs, start + s0, c->window[layer], c);
+    int nseq = 0, maxqb = 0;
+    const int rows = k1.cu[n];
+    pg.items = 0;
+    for (const QueryRun &r : runs) {
+        const int P = start[s0 + r.seq] + r.first;
+        if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 64) ||
+            !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 128))
+            return false;
+        k2.len[nseq] = r.len;
+        k2.start[nseq] = P;
+        k2.cu[nseq] = k1.cu[r.seq] + r.first;
+        maxqb = std::max(maxqb, (r.len + 127) / 128);
+        pg.items += (r.len + 127) / 128;
+        ++nseq;
     }
     k1.T = rows;
     if (rows == 0) return true;

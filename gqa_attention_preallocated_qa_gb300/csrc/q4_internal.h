@@ -60,7 +60,7 @@ static_assert(sizeof(Q4PrefillRowsParams) <= 4096, "travels in the 4 KB of kerne
 
 constexpr int kQ4Chunk = 32;       // keys of one pipeline chunk of the decode kernel
 constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
-constexpr int kQ4MaxSplits = 16;   // splits of one (sequence, kv head) = CTAs of one cluster
+constexpr int kQ4MaxSplits = 13;   // splits of one (sequence, kv head) = CTAs of one cluster
 constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode launch
 
 // A launched sequence: the slot of its first new token, its place in the cache,
@@ -97,8 +97,9 @@ cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsParams &p, int D, cudaStre
 cudaError_t launch_q4_dequantise(const Q4RowsParams &p, int D, cudaStream_t stream);
 // HPC heads x TPS tokens per CTA (TPS = 1, or 8 / HPC for launches of several tokens).
 cudaError_t launch_q4_decode(const Q4DecodeParams &p, int D, int HPC, bool multi, cudaStream_t stream);
-// Clusters of S decode CTAs resident at once on the current device (cached); 0 on error.
-int q4_cluster_capacity(int D, int HPC, bool multi, int S);
+// How many clusters of S decode CTAs the current device holds at once, for S =
+// 1..kQ4MaxSplits (entry 0 unused); asked for once per device, null on error.
+const int *q4_cluster_capacities(int D, int HPC, bool multi);
 
 // Shared with the bf16 cache's host side.
 bool encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, int box_rows);

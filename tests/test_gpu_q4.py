@@ -315,6 +315,8 @@ def test_short_chunk(qa, hq, hkv, d, window):
     (8, 2, 128, [0, 0, 0], [129, 1, 300], 0),
     (4, 4, 64, [100, 0, 257], [130, 40, 255], 0),
     (8, 1, 128, [300, 140], [200, 77], 150),
+    (32, 8, 128, [1500, 130, 20, 1500], [700, 900, 60, 130], 0),  # more blocks than the device takes at once
+    (16, 8, 64, [900, 0], [300, 1000], 700),
     (4, 1, 64, [31] * 11, [20, 0, 3, 150, 9, 1, 20, 33, 128, 2, 17], 0),
 ])
 def test_prefill(qa, hq, hkv, d, start, ntok, window):
