@@ -129,10 +129,6 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
 // ring (three bulk copies), as K1 does.
 constexpr int kQ4RowWarps = 16;  // warps per CTA, one CTA per SM
 
-// A warp's share of a token: with an even number of kv heads half of the heads
-// (twice the warps hide more of the arithmetic's latency), else all of them.
-__host__ __device__ constexpr int q4_row_parts(int Hkv) { return Hkv % 2 == 0 ? 2 : 1; }
-
 // RMSNorm + RoPE of this lane's 8 values of a row held by D/8 lanes; cs, sn:
 // cosines and sines of its dims, the sines signed for its half.
 template <int D>
@@ -183,7 +179,7 @@ __global__ void __launch_bounds__(kQ4RowWarps * 32, 1)
     // The prefill attention follows as a programmatic dependent: its set-up may
     // start now; it reads what this kernel writes only after its end.
     if (k.signal_early) griddep_launch_dependents();
-    const int parts = q4_row_parts(k.Hkv);
+    const int parts = p.parts;
     const int nq = k.Hq / parts, nkv = k.Hkv / parts;  // heads of a share
     const uint32_t qbytes = static_cast<uint32_t>(nq) * D * 2;
     const uint32_t kvbytes = static_cast<uint32_t>(nkv) * D * 2;
@@ -315,17 +311,30 @@ __global__ void __launch_bounds__(kQ4RowWarps * 32, 1)
     }
 }
 
-static size_t q4_prefill_rows_smem(int Hq, int Hkv, int D) {
-    const int parts = q4_row_parts(Hkv);
+static size_t q4_prefill_rows_smem(int Hq, int Hkv, int D, int parts) {
     const size_t stage = (static_cast<size_t>(Hq / parts + 2 * (Hkv / parts)) * D * 2 + 127) & ~static_cast<size_t>(127);
     return static_cast<size_t>(kQ4RowWarps) * 2 * stage + 128;
 }
 constexpr size_t kQ4RowSmemMost = 200 * 1024 + 128;
 
-bool q4_prefill_rows_fits(int Hq, int Hkv, int D) { return q4_prefill_rows_smem(Hq, Hkv, D) <= kQ4RowSmemMost; }
+// Shares that a token is cut into, by heads (0: no number of them fits): the
+// fewest that fit (two at 32 + 2 x 8 heads of 128), and four as long as every
+// share still has a warp of its own.  (Prefill of 256 tokens: 14.5 us with four
+// shares and 16.6 with two; of 1024: 29.5 and 27.0; eight leave lanes idle.)
+static int q4_row_parts(int Hq, int Hkv, int D, int64_t T, int sms) {
+    int parts = 1;
+    while (q4_prefill_rows_smem(Hq, Hkv, D, parts) > kQ4RowSmemMost) {
+        parts *= 2;
+        if (Hkv % parts) return 0;
+    }
+    while (parts < 4 && Hkv % (2 * parts) == 0 && 2 * T * parts <= static_cast<int64_t>(sms) * kQ4RowWarps) parts *= 2;
+    return parts;
+}
+
+bool q4_prefill_rows_fits(int Hq, int Hkv, int D) { return q4_row_parts(Hq, Hkv, D, int64_t(1) << 40, 1) > 0; }
 
 template <int D>
-static cudaError_t q4_prefill_rows_t(const Q4PrefillRowsParams &p, cudaStream_t stream) {
+static cudaError_t q4_prefill_rows_t(const Q4PrefillRowsParams &params, cudaStream_t stream) {
     static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
     static std::atomic<int> sms_of[32] = {};
     int dev = 0, sms = 0;
@@ -342,9 +351,12 @@ static cudaError_t q4_prefill_rows_t(const Q4PrefillRowsParams &p, cudaStream_t 
             configured.fetch_or(1u << dev, std::memory_order_release);
         }
     }
-    const int64_t need = (static_cast<int64_t>(p.k1.T) * q4_row_parts(p.k1.Hkv) + kQ4RowWarps - 1) / kQ4RowWarps;
+    Q4PrefillRowsParams p = params;
+    p.parts = q4_row_parts(p.k1.Hq, p.k1.Hkv, D, p.k1.T, sms);
+    if (p.parts == 0) return cudaErrorInvalidConfiguration;
+    const int64_t need = (static_cast<int64_t>(p.k1.T) * p.parts + kQ4RowWarps - 1) / kQ4RowWarps;
     q4_prefill_rows_kernel<D><<<static_cast<unsigned>(std::min<int64_t>(need, sms)), kQ4RowWarps * 32,
-                                q4_prefill_rows_smem(p.k1.Hq, p.k1.Hkv, D), stream>>>(p);
+                                q4_prefill_rows_smem(p.k1.Hq, p.k1.Hkv, D, p.parts), stream>>>(p);
     return cudaGetLastError();
 }
 

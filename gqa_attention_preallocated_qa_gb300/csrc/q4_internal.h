@@ -55,6 +55,7 @@ struct Q4PrefillRowsParams {
     uint8_t *codes[2], *scales[2];       // layer base of K and V
     int64_t row_seq, row_head;           // cache strides in rows
     int seq0;                            // cache slot of the first sequence
+    int parts;                           // shares of a token (set at launch)
 };
 static_assert(sizeof(Q4PrefillRowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
