@@ -57,7 +57,12 @@ struct Q4Shape {
     // Ring stages: as many as let two CTAs share an SM.
     static constexpr int kStages = D == 128 && R == 8 ? 2 : 3;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kPartial = R * (D + 2);                  // floats: o [R][D], (m, l) [R][2]
+    // A partial in floats: o [R][D], rows 8 apart so that the stores of a warp
+    // meet no bank twice, then (m, l) [R][2].  The D outputs of a row stand in
+    // the order of the accumulators (q4_place).
+    static constexpr int kRowStride = D + 8;
+    static constexpr int kMl = R * kRowStride;
+    static constexpr int kPartial = kMl + 2 * R;
     static constexpr int kRecv = q4_recv_floats(R * D, R);
     static constexpr int kQBytes = R * D * 2;
     static constexpr int kSmemUsed = 128 + kRing + kQBytes + (kPartial + kRecv) * 4;
@@ -73,6 +78,17 @@ __device__ __forceinline__ uint32_t shared_inc(uint32_t a) {
     uint32_t old;
     asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(old) : "r"(a) : "memory");
     return old;
+}
+
+// The place of dimension d in a row of outputs: the accumulators of tile t hold
+// dims r D/8 + 2t and + 1 on the lanes of row r, which lie side by side.
+template <int D>
+__device__ __forceinline__ int q4_place(int d) {
+    return (d % (D / 8)) / 2 * 16 + d / (D / 8) * 2 + (d & 1);
+}
+template <int D>
+__device__ __forceinline__ int q4_dim(int place) {
+    return (place % 16) / 2 * (D / 8) + place / 16 * 2 + (place & 1);
 }
 
 // Waits with their slow part out of line (a launch meets its code cold).
@@ -378,7 +394,10 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~static_cast<uintptr_t>(127));
-    __half *qs = reinterpret_cast<__half *>(smem + Sh::kRing);
+    // Query rows as the B fragments want them: 8 dims of a row are 16 bytes, dims
+    // (0, 4), (1, 5) / 16, (2, 6), (3, 7) / 16; unit (w, row, c) at (w R + row) 4 + c
+    // holds dims c D/4 + 8w ..., what lane (row, c) reads for its words w of K.
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + Sh::kRing);
     float *part_new = reinterpret_cast<float *>(smem + Sh::kRing + Sh::kQBytes);
     float *recv = part_new + Sh::kPartial;
 
@@ -405,38 +424,13 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     const int nchunks = pos_ok ? (pos + kQ4Chunk - 1) / kQ4Chunk : 0;
     const int key_lo = (pos_ok && p.window > 0) ? max(0, pos + 1 - p.window) : 0;
     const int c_lo = min(key_lo / kQ4Chunk, nchunks);
-    // (at most 2^19 chunks and 16 splits)
-    const int c_begin = c_lo + static_cast<uint32_t>(split) * (nchunks - c_lo) / static_cast<uint32_t>(S);
-    const int c_end = c_lo + static_cast<uint32_t>(split + 1) * (nchunks - c_lo) / static_cast<uint32_t>(S);
+    // Divided by S as a product with ceil(2^32 / S): exact below 2^32 / S, and
+    // there are at most 2^19 chunks and 13 splits.  (S = 1: the product is 0.)
+    const uint32_t n = nchunks - c_lo;
+    const int c_begin = c_lo + __umulhi(split * n, p.inv_S);
+    const int c_end = split == S - 1 ? nchunks : c_lo + __umulhi((split + 1) * n, p.inv_S);
     const int c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
     const int nstages = (c_end - c_begin + NW - 1) / NW;
-
-    // The rows to prepare: query rows 0..R-1, then (on the last split) the new
-    // tokens; warp w takes items NW-1-w and 2NW-1-w.
-    const int sub = lane % LPR;
-    const int nitems = R + (owner ? ntok : 0);
-    auto load_item = [&](int it, Q4Row &row) {
-        const int t = it < R ? it / HPC : it - R;
-        if (it >= nitems || t >= ntok) return;
-        const __nv_bfloat16 *x, *w;
-        if (it < R) {
-            x = p.q + (static_cast<int64_t>(seq.row0 + t) * p.Hq + h_first + it % HPC) * D;
-            w = p.wq;
-        } else {
-            const int64_t kr = (static_cast<int64_t>(seq.row0 + t) * p.Hkv + kvh) * D;
-            x = p.k + kr;
-            w = p.wk;
-            row.v = __ldg(reinterpret_cast<const uint4 *>(p.v + kr) + sub);
-        }
-        row.x = __ldg(reinterpret_cast<const uint4 *>(x) + sub);
-        row.w = __ldg(reinterpret_cast<const uint4 *>(w) + sub);
-        const float4 *tab = reinterpret_cast<const float4 *>(
-            p.rope + static_cast<int64_t>(pos + t) * (D / 2) + 8 * (sub % (LPR / 2)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) row.cs[e] = __ldg(tab + e);
-    };
-    Q4Row row;
-    if (pos_ok) load_item(NW - 1 - warp, row);
 
     // Stage j's rows are contiguous in the cache: four copies, by one thread.
     auto issue = [&](int j) {
@@ -472,6 +466,32 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
              sent < min(NS, nstages) && min(c_end, c_begin + (sent + 1) * NW) <= limit; ++sent)
             issue(sent);
     }
+    // The rows to prepare: query rows 0..R-1, then (on the last split) the new
+    // tokens; warp w takes items NW-1-w and 2NW-1-w.
+    const int sub = lane % LPR;
+    const int nitems = R + (owner ? ntok : 0);
+    auto load_item = [&](int it, Q4Row &row) {
+        const int t = it < R ? it / HPC : it - R;
+        if (it >= nitems || t >= ntok) return;
+        const __nv_bfloat16 *x, *w;
+        if (it < R) {
+            x = p.q + (static_cast<int64_t>(seq.row0 + t) * p.Hq + h_first + it % HPC) * D;
+            w = p.wq;
+        } else {
+            const int64_t kr = (static_cast<int64_t>(seq.row0 + t) * p.Hkv + kvh) * D;
+            x = p.k + kr;
+            w = p.wk;
+            row.v = __ldg(reinterpret_cast<const uint4 *>(p.v + kr) + sub);
+        }
+        row.x = __ldg(reinterpret_cast<const uint4 *>(x) + sub);
+        row.w = __ldg(reinterpret_cast<const uint4 *>(w) + sub);
+        const float4 *tab = reinterpret_cast<const float4 *>(
+            p.rope + static_cast<int64_t>(pos + t) * (D / 2) + 8 * (sub % (LPR / 2)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row.cs[e] = __ldg(tab + e);
+    };
+    Q4Row row;
+    if (pos_ok) load_item(NW - 1 - warp, row);
     __syncwarp();
     cluster_arrive();  // peers may push into this CTA once they have waited on this
     if (!pos_ok) {
@@ -503,13 +523,15 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             // exponent field of the largest magnitude, kept where 2^(8 - e) and its inverse are finite
             const int ex = min(max(static_cast<int>(mx >> 7), 20), 254) - 127;
             const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - ex) << 23);
+            // The codes of odd dims come 16 times larger, their queries 16 times smaller.
+            const float down = up * 0.0625f;
             uint4 h;
-            h.x = pack_f16(bf16lo(x.x) * up, bf16hi(x.x) * up);
-            h.y = pack_f16(bf16lo(x.y) * up, bf16hi(x.y) * up);
-            h.z = pack_f16(bf16lo(x.z) * up, bf16hi(x.z) * up);
-            h.w = pack_f16(bf16lo(x.w) * up, bf16hi(x.w) * up);
+            h.x = pack_f16(bf16lo(x.x) * up, bf16lo(x.z) * up);
+            h.y = pack_f16(bf16hi(x.x) * down, bf16hi(x.z) * down);
+            h.z = pack_f16(bf16lo(x.y) * up, bf16lo(x.w) * up);
+            h.w = pack_f16(bf16hi(x.y) * down, bf16hi(x.w) * down);
             if (lane < LPR) {
-                reinterpret_cast<uint4 *>(qs + it * D)[sub] = h;
+                qs[(sub % (D / 32) * R + it) * 4 + sub / (D / 32)] = h;
                 if (lane == 0) s_c[it] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex - 8) << 23);
             }
         } else {
@@ -538,9 +560,14 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
         for (int e = 0; e < PER; ++e) O[e] = 0.f;
         if (t < ntok) {
+            // q of dims e * 32 + lane
             float q[PER], sc[TPS];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) q[e] = __half2float(qs[warp * D + e * 32 + lane]);
+            for (int e = 0; e < PER; ++e) {
+                const int d = e * 32 + lane, u = d / 8;
+                const __half *unit = reinterpret_cast<const __half *>(qs + (u % (D / 32) * R + warp) * 4 + u / (D / 32));
+                q[e] = __half2float(unit[(d & 3) * 2 + (d >> 2 & 1)]) * (d & 1 ? 16.f : 1.f);
+            }
 #pragma unroll
             for (int u = 0; u < TPS; ++u) {
                 float x = 0.f;
@@ -566,10 +593,10 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         // in the odd dims: so does this one.
         const float lift = lane & 1 ? 65536.f : 4096.f;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) part_new[warp * D + e * 32 + lane] = O[e] * lift;
+        for (int e = 0; e < PER; ++e) part_new[warp * Sh::kRowStride + q4_place<D>(e * 32 + lane)] = O[e] * lift;
         if (lane == 0) {
-            part_new[R * D + 2 * warp] = M;
-            part_new[R * D + 2 * warp + 1] = L * 4096.f;
+            part_new[Sh::kMl + 2 * warp] = M;
+            part_new[Sh::kMl + 2 * warp + 1] = L * 4096.f;
         }
     }
 
@@ -577,18 +604,14 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     {
         const int r = lane >> 2, c4 = lane & 3;
         uint32_t qb[D / 16][2];
-        // B fragments: this lane's dims are those of its part of a row of K; the
-        // codes of odd dims come 16 times larger, their queries 16 times smaller.
-        // A column past the last row repeats one; nothing reads it.
-        const __half *qrow = qs + (r % R) * D + c4 * (D / 4);
+        // B fragments.  A column past the last row repeats one; nothing reads it.
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-            const uint4 q8 = *reinterpret_cast<const uint4 *>(qrow + 8 * w);
-            const __half2 down = __float2half2_rn(0.0625f), none = __float2half2_rn(0.f);
-            qb[2 * w][0] = __byte_perm(q8.x, q8.z, 0x5410);                              // dims 0, 4
-            qb[2 * w][1] = hfma2_u(__byte_perm(q8.x, q8.z, 0x7632), down, none);         // dims 1, 5
-            qb[2 * w + 1][0] = __byte_perm(q8.y, q8.w, 0x5410);                          // dims 2, 6
-            qb[2 * w + 1][1] = hfma2_u(__byte_perm(q8.y, q8.w, 0x7632), down, none);     // dims 3, 7
+            const uint4 h = qs[(w * R + r % R) * 4 + c4];
+            qb[2 * w][0] = h.x;
+            qb[2 * w][1] = h.y;
+            qb[2 * w + 1][0] = h.z;
+            qb[2 * w + 1][1] = h.w;
         }
         float cs[2];
         Q4Acc<D> a;
@@ -678,12 +701,12 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             if (col < R) {
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t)
-                    *reinterpret_cast<float2 *>(part + col * D + r * (D / 8) + 2 * t) =
+                    *reinterpret_cast<float2 *>(part + col * Sh::kRowStride + 16 * t + 2 * r) =
                         make_float2(a.o[t][x], a.o[t][2 + x]);  // (the odd dim 16 times larger)
                 if (r == 0) {  // a NaN score leaves ref alone: its row is NaN whatever the other warps hold
                     const float m = a.l[x] != a.l[x] ? a.l[x] : a.ref[x] + kQ4Lift;
-                    part[R * D + 2 * col] = a.ref[x] == kQ4NoRef && a.l[x] == 0.f ? -INFINITY : m;
-                    part[R * D + 2 * col + 1] = a.l[x];
+                    part[Sh::kMl + 2 * col] = a.ref[x] == kQ4NoRef && a.l[x] == 0.f ? -INFINITY : m;
+                    part[Sh::kMl + 2 * col + 1] = a.l[x];
                 }
             }
         }
@@ -707,7 +730,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         float M = -INFINITY, L = 0.f;
         if (lane < sources) {
             const float2 ml = *reinterpret_cast<const float2 *>(
-                (lane < NW ? red + lane * Sh::kPartial : part_new) + R * D + 2 * g);
+                (lane < NW ? red + lane * Sh::kPartial : part_new) + Sh::kMl + 2 * g);
             M = ml.x;
             L = ml.y;
         }
@@ -722,12 +745,12 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             const float wi = __shfl_sync(FULL, w, i);
-            const float2 x = *reinterpret_cast<const float2 *>(red + i * Sh::kPartial + e);
+            const float2 x = *reinterpret_cast<const float2 *>(red + i * Sh::kPartial + e + 8 * g);
             O = make_float2(fmaf(wi, x.x, O.x), fmaf(wi, x.y, O.y));
         }
         if (owner) {
             const float wi = __shfl_sync(FULL, w, NW);
-            const float2 x = *reinterpret_cast<const float2 *>(part_new + e);
+            const float2 x = *reinterpret_cast<const float2 *>(part_new + e + 8 * g);
             O = make_float2(fmaf(wi, x.x, O.x), fmaf(wi, x.y, O.y));
         }
         const int dst = e / E;
@@ -796,7 +819,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     for (int j = 0; j < kOutPer; ++j) {
         const int k = threadIdx.x + j * kThreads;
         if (k < E_me) {
-            const int e = e_lo + k, g = e / D, d = e % D;
+            const int e = e_lo + k, g = e / D, d = q4_dim<D>(e % D);
             const int t = g / HPC, hh = g % HPC;
             if (t < ntok)
                 p.out[(static_cast<int64_t>(seq.row0 + t) * p.Hq + h_first + hh) * D + d] =

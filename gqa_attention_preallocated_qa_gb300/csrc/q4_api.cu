@@ -270,6 +270,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         p.B = nz;
         p.S = choose_splits(D, HPC, multi, nz * g.n_kv_heads * p.HG, keys);
         const int rows = multi ? qa::kQ4MaxTokens : HPC;
+        p.inv_S = p.S == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + p.S - 1) / p.S);
         p.E = ((rows * D + p.S - 1) / p.S + 31) & ~31;
         p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
         const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,

@@ -82,6 +82,7 @@ struct Q4DecodeParams {
     int64_t row_seq, row_head;           // cache strides in rows
     int B, Hq, Hkv, G, HG, cap, S;
     int E;                               // outputs merged by one CTA of a cluster (a multiple of 32)
+    uint32_t inv_S;                      // ceil(2^32 / S), 0 for S = 1
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
     int window;                          // attention window in keys (0: all earlier keys)
     int guard;                           // rows below each first new slot that a running launch may write
