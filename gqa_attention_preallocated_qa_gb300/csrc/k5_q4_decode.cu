@@ -93,18 +93,18 @@ __device__ __forceinline__ int q4_dim(int place) {
 
 // Waits with their slow part out of line (a launch meets its code cold).
 __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
-                                          uint32_t site) {
-    return mbar_wait(bar, parity, abort, err, kKernQ4Decode, site);
+                                          uint32_t site, uint64_t wait_ns) {
+    return mbar_wait(bar, parity, abort, err, kKernQ4Decode, site, wait_ns);
 }
 __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int *abort, uint32_t *err,
-                                        uint32_t site) {
-    return mbar_try_wait(bar, parity) || q4_wait_slow(bar, parity, abort, err, site);
+                                        uint32_t site, uint64_t wait_ns) {
+    return mbar_try_wait(bar, parity) || q4_wait_slow(bar, parity, abort, err, site, wait_ns);
 }
-__device__ __noinline__ bool q4_wait_cluster(uint32_t bar, volatile int *abort, uint32_t *err) {
-    if (mbar_wait_cluster(bar, 0, abort, err, kKernQ4Decode, 4)) return true;
+__device__ __noinline__ bool q4_wait_cluster(uint32_t bar, volatile int *abort, uint32_t *err, uint64_t wait_ns) {
+    if (mbar_wait_cluster(bar, 0, abort, err, kKernQ4Decode, 4, wait_ns)) return true;
     // Given up: the peers still push here, and their stores land before this CTA exits.
     int dummy = 0;
-    mbar_wait_cluster(bar, 0, &dummy, err, kKernQ4Decode, 5);
+    mbar_wait_cluster(bar, 0, &dummy, err, kKernQ4Decode, 5, wait_ns);
     return false;
 }
 
@@ -439,6 +439,8 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const uint32_t bar = smem_u32(&bar_full[st]);
         const int64_t r0 = row_base + static_cast<int64_t>(c) * kQ4Chunk;
         uint32_t dst = smem_u32(smem + st * Sh::kStage);
+        // Test hook: nothing completes the first stage of the first cluster's CTAs.
+        if (p.fault && j == 0 && blockIdx.y == 0 && blockIdx.z == 0) return;
         s_sent[st] = j;
         mbar_expect_tx(bar, keys * 2 * (Sh::kRow + Sh::kScaleRow));
         bulk_g2s(dst, p.kc + r0 * Sh::kRow, keys * Sh::kRow, bar);
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         uint32_t phase = 0;
 #pragma unroll 1
         for (int j = 0; j < nstages; ++j) {
-            bool ok = q4_wait(smem_u32(&bar_full[st]), phase, &s_abort, p.err, 2);
+            bool ok = q4_wait(smem_u32(&bar_full[st]), phase, &s_abort, p.err, 2, p.wait_ns);
             ok = __all_sync(FULL, ok);
             if (!ok) break;
             const int c = c_begin + j * NW + warp;
@@ -692,7 +694,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             int dummy = 0;
             for (int s = 0; s < NS; ++s)
                 if (s_sent[s] >= 0)
-                    mbar_wait(smem_u32(&bar_full[s]), (s_sent[s] / NS) & 1, &dummy, p.err, kKernQ4Decode, 6);
+                    mbar_wait(smem_u32(&bar_full[s]), (s_sent[s] / NS) & 1, &dummy, p.err, kKernQ4Decode, 6, p.wait_ns);
         }
         float *part = reinterpret_cast<float *>(smem) + warp * Sh::kPartial;
 #pragma unroll
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     float res[kOutPer];
     bool merged = false;
     if (warp * 32 < E_me) {
-        merged = q4_wait_cluster(smem_u32(&bar_recv), &s_abort, p.err);
+        merged = q4_wait_cluster(smem_u32(&bar_recv), &s_abort, p.err, p.wait_ns);
         merged = __all_sync(FULL, merged);
 #pragma unroll
         for (int j = 0; j < kOutPer; ++j) {

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "q4_internal.h"
+#include "q4_plan.h"
 #include "qa.h"
 
 #define QA_API extern "C" __attribute__((visibility("default")))
@@ -59,6 +60,16 @@ class DeviceScope {
     int before_ = 0;
     bool ok_ = false, back_ = false;
 };
+
+// The body of an entry point whose host side allocates: no exception leaves it.
+template <typename F>
+qa_status no_throw(F &&body) {
+    try {
+        return body();
+    } catch (...) {
+        return QA_ERR_CUDA;
+    }
+}
 
 template <typename T>
 bool dev_alloc(T **p, size_t count, uint64_t &acct) {
@@ -162,36 +173,6 @@ bool fill_ranges(qa::Q4RowsParams &p, const qa_config &g, int s0, int n, const i
     return p.nblocks > 0;
 }
 
-// Splits of a sequence and kv head (CTAs of a cluster).  A CTA costs a fixed
-// part (its prologue and the merge) and a part per stage of 256 keys; CTAs that
-// share an SM slow each other down.  Fitted on GB300 (D = 128, steps apart from
-// each other, 512 to 16384 keys, 8 to 192 groups): 2.6 us + 1.1 us a stage for a
-// CTA alone on its SM, 3.6 + 1.85 for two; at D = 64 a stage costs 0.66 times
-// that.  CTAs get SMs of their own as long as the launch has at most 96 of them,
-// or 128 in clusters of up to 4.  Only plans whose clusters all fit on the device
-// at once are weighed, the fewest CTAs among equals.  (B = 4, 8 kv heads: 4
-// splits at 2048 keys take 7.8 us and 8 take 8.4; at 16384 keys 23.2 and 21.4.)
-int choose_splits(int D, int HPC, bool multi, int groups, int keys) {
-    const int chunks = (keys + qa::kQ4Chunk - 1) / qa::kQ4Chunk;
-    const float stage = D == 128 ? 1.f : 0.66f;
-    const int *held = qa::q4_cluster_capacities(D, HPC, multi);
-    if (!held) return 1;
-    int best = 1;
-    float least = 1e30f;
-    for (int S = 1; S <= qa::kQ4MaxSplits && (S == 1 || S <= chunks); ++S) {
-        if (S > 1 && held[S] < groups) continue;
-        const int64_t ctas = static_cast<int64_t>(groups) * S;
-        const int rounds = ((chunks + S - 1) / S + qa::kQ4DecodeWarps - 1) / qa::kQ4DecodeWarps;
-        const bool alone = ctas <= (S <= 4 ? 128 : 96);
-        const float us = alone ? 2.6f + 1.1f * stage * rounds : 3.6f + 1.85f * stage * rounds;
-        if (us < least - 0.01f) {
-            least = us;
-            best = S;
-        }
-    }
-    return best;
-}
-
 struct DecodeCall {
     const void *q, *k, *v, *wq, *wk;
     void *out, *k_held, *v_held;
@@ -268,7 +249,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         // short ones fill in behind them.
         std::stable_sort(p.seq, p.seq + nz, [](const qa::Q4Seq &x, const qa::Q4Seq &y) { return x.pos > y.pos; });
         p.B = nz;
-        p.S = choose_splits(D, HPC, multi, nz * g.n_kv_heads * p.HG, keys);
+        p.S = qa::choose_splits(D, qa::q4_cluster_capacities(D, HPC, multi), nz * g.n_kv_heads * p.HG, keys);
         const int rows = multi ? qa::kQ4MaxTokens : HPC;
         p.inv_S = p.S == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + p.S - 1) / p.S);
         p.E = ((rows * D + p.S - 1) / p.S + 31) & ~31;
@@ -276,6 +257,9 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,
                                                    p.early != 0, resident);
         p.guard = settled ? 0 : guard;
+        const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
+        p.fault = f.fault;
+        p.wait_ns = f.wait_ns;
         if (qa::launch_q4_decode(p, D, HPC, multi, s) != cudaSuccess) {
             cudaGetLastError();
             return QA_ERR_CUDA;
@@ -296,80 +280,6 @@ struct PrefillGroup {
     qa::K2Params k2;
     int items;
 };
-
-// A run of query blocks of one sequence of a prefill launch: rows first ..
-// first + len - 1 of its new tokens.
-struct QueryRun {
-    int seq, first, len;
-};
-
-// Time of the prefill attention of `runs` in units of key tiles: its items are
-// dealt out level by level (the block within its run, the highest first), then
-// by run, to `workers` in snake order; a block costs its key tiles and about
-// one more.  `copies`: items of a block (kv heads and head groups).
-int prefill_span(const std::vector<QueryRun> &runs, const int32_t *start, int window, int copies, int workers,
-                 std::vector<int> &load) {
-    load.assign(workers, 0);
-    int levels = 0, idx = 0;
-    for (const QueryRun &r : runs) levels = std::max(levels, (r.len + 127) / 128);
-    for (int lvl = levels - 1; lvl >= 0; --lvl)
-        for (const QueryRun &r : runs) {
-            if (r.len <= lvl * 128) continue;
-            const int pos = start[r.seq] + r.first + lvl * 128;
-            const int from = window > 0 ? std::max(0, pos + 1 - window) / 128 : 0;
-            const int tiles = (pos + std::min(r.len - 1 - lvl * 128, 127)) / 128 + 1 - from + 1;
-            for (int k = 0; k < copies; ++k, ++idx) {
-                const int round = idx / workers, at = idx % workers;
-                load[round & 1 ? workers - 1 - at : at] += tiles;
-            }
-        }
-    return *std::max_element(load.begin(), load.end());
-}
-
-// The runs a prefill launch is made of.  The kernel deals its items out by the
-// block's place in its run, which is their weight when every sequence starts at
-// 0; behind caches of different lengths it is not, and heavy blocks dealt late
-// leave most of the device idle at the end.  So the sequences go in by falling
-// start, and the ones that start lowest may be cut into shorter runs (up to the
-// 8 of a launch), whose blocks then come later.  Results are the same bits: an
-// item does not depend on its neighbours.  (777 tokens behind 4099 and 1001
-// behind 1025, 32 / 8 heads: 124 us as two runs, 86 us cut.)
-void plan_runs(std::vector<QueryRun> &runs, const int32_t *start, int window, const qa_q4_cache *c) {
-    const int G = c->G, D = c->cfg.head_dim;
-    std::stable_sort(runs.begin(), runs.end(), [&](const QueryRun &x, const QueryRun &y) { return start[x.seq] > start[y.seq]; });
-    bool same = true;
-    int blocks = 0;
-    for (const QueryRun &r : runs) {
-        same = same && start[r.seq] == start[runs[0].seq];
-        blocks += (r.len + 127) / 128;
-    }
-    // Workers and items of the form that the launch takes: pairs of CTAs on four
-    // heads, else CTAs on two heads or one.
-    int workers = c->num_sms / 2, copies = c->cfg.n_kv_heads * (G / 4);
-    if (D != 128 || G % 4 || blocks * copies < workers) {
-        workers = c->num_sms;
-        copies = c->cfg.n_kv_heads * ((G + 1) / 2);
-        if (G > 1 && blocks * copies < workers) copies = c->cfg.n_kv_heads * G;
-    }
-    if (same || blocks * copies <= workers || blocks > 256) return;
-    std::vector<int> load;
-    std::vector<QueryRun> best = runs;
-    int least = prefill_span(runs, start, window, copies, workers, load);
-    for (size_t cut = 1; cut <= runs.size(); ++cut)        // the last `cut` sequences
-        for (int m : {1, 2, 3, 4, 6, 8}) {                  // into runs of m blocks
-            std::vector<QueryRun> tried(runs.begin(), runs.end() - cut);
-            for (size_t i = runs.size() - cut; i < runs.size(); ++i)
-                for (int at = (runs[i].len - 1) / (128 * m) * (128 * m); at >= 0; at -= 128 * m)
-                    tried.push_back({runs[i].seq, at, std::min(128 * m, runs[i].len - at)});
-            if (tried.size() > static_cast<size_t>(qa::kMaxSeqPerLaunch) || tried.size() == runs.size()) continue;
-            const int span = prefill_span(tried, start, window, copies, workers, load);
-            if (span < least) {
-                least = span;
-                best = tried;
-            }
-        }
-    runs = best;
-}
 
 // Builds the launches for sequences s0 .. s0 + n - 1; false when a tensor map
 // cannot be made.
@@ -433,18 +343,18 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     }
     qa::K2Params &k2 = pg.k2;
     k2 = qa::K2Params{};
-    std::vector<QueryRun> runs;
+    std::vector<qa::QueryRun> runs;
     k1.cu[0] = 0;
     for (int i = 0; i < n; ++i) {
         k1.cu[i + 1] = k1.cu[i] + ntok[s0 + i];
         k1.start[i] = start[s0 + i];
         if (ntok[s0 + i] > 0) runs.push_back({i, 0, ntok[s0 + i]});
     }
-    plan_runs(runs, start + s0, c->window[layer], c);
+    qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
     int nseq = 0, maxqb = 0;
     const int rows = k1.cu[n];
     pg.items = 0;
-    for (const QueryRun &r : runs) {
+    for (const qa::QueryRun &r : runs) {
         const int P = start[s0 + r.seq] + r.first;
         if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 64) ||
             !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 128))
@@ -469,7 +379,6 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     k2.max_qblocks = maxqb;
     k2.window = c->window[layer];
     k2.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
-    k2.wait_ns = qa::kWaitTimeoutNs;
     pg.items *= Hkv * k2.npairs;
     return true;
 }
@@ -505,20 +414,22 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
          dev_alloc(&c->rope, static_cast<size_t>(g.capacity) * (g.head_dim / 2), c->scratch_bytes) &&
          dev_alloc(&c->err, 1, c->scratch_bytes) &&
          cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) == cudaSuccess;
-    if (ok) {
+    ok = ok && no_throw([&] {
+        c->window.assign(static_cast<size_t>(g.num_layers), 0);
+        c->next_pos.assign(static_cast<size_t>(g.num_layers) * g.max_batch, -1);
         std::vector<float2> tab(static_cast<size_t>(g.capacity) * (g.head_dim / 2));
         qa::fill_rope_table(tab.data(), g.capacity, g.head_dim, g.rope_theta);
-        ok = cudaMemcpy(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
-             cudaDeviceSynchronize() == cudaSuccess;
-    }
+        return cudaMemcpy(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
+                       cudaDeviceSynchronize() == cudaSuccess
+                   ? QA_OK
+                   : QA_ERR_CUDA;
+    }) == QA_OK;
     if (!ok) {
         free_all(c);
         delete c;
         cudaGetLastError();
         return QA_ERR_CUDA;
     }
-    c->window.assign(static_cast<size_t>(g.num_layers), 0);
-    c->next_pos.assign(static_cast<size_t>(g.num_layers) * g.max_batch, -1);
     *out = c;
     return QA_OK;
 }
@@ -632,7 +543,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     const int tmax = *std::max_element(ntok, ntok + batch);
     if (tmax <= qa::kQ4MaxTokens) {
         DecodeCall a{q, k, v, q_norm_w, k_norm_w, out, nullptr, nullptr, start, nullptr, ntok};
-        return run_decode(c, layer, batch, a, tmax, s);
+        return no_throw([&] { return run_decode(c, layer, batch, a, tmax, s); });
     }
     // The longer form goes through the cache's one bf16 workspace: a graph could
     // be replayed beside another call that uses it, so it is not captured, and
@@ -643,15 +554,20 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         return QA_ERR_STATE;
     }
     std::vector<PrefillGroup> groups;
-    int64_t row0 = 0;
-    for (int s0 = 0; s0 < batch; s0 += c->ws_slots) {
-        const int n = std::min(c->ws_slots, batch - s0);
-        PrefillGroup pg;
-        if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
-            return QA_ERR_CUDA;
-        row0 += pg.rows.k1.T;
-        if (pg.rows.k1.T > 0) groups.push_back(pg);
-    }
+    st = no_throw([&] {
+        int64_t row0 = 0;
+        for (int s0 = 0; s0 < batch; s0 += c->ws_slots) {
+            const int n = std::min(c->ws_slots, batch - s0);
+            groups.emplace_back();
+            PrefillGroup &pg = groups.back();
+            if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
+                return QA_ERR_CUDA;
+            row0 += pg.rows.k1.T;
+            if (pg.rows.k1.T == 0) groups.pop_back();
+        }
+        return QA_OK;
+    });
+    if (st != QA_OK) return st;
     if (cudaStreamWaitEvent(s, c->ws_free, 0) != cudaSuccess) return QA_ERR_CUDA;
     int32_t *next = next_of(c, layer);
     for (int b = 0; b < batch; ++b)
@@ -676,6 +592,9 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
         }
+        const qa::FaultPlan f = qa::take_fault(QA_KERNEL_PREFILL_ATTN);
+        pg.k2.fault = f.fault;
+        pg.k2.wait_ns = f.wait_ns;
         if (qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s) != cudaSuccess) {
             // A kernel that signalled early is no longer followed by one that
             // waits for it: let it finish before anything else is enqueued.
@@ -697,7 +616,7 @@ qa_status decode_step(qa_q4_cache *c, int layer, int batch, const DecodeCall &a,
         return QA_ERR_ALIGNMENT;
     DeviceScope dev(c->device);
     if (!dev.ok()) return QA_ERR_CUDA;
-    return run_decode(c, layer, batch, a, 1, static_cast<cudaStream_t>(stream));
+    return no_throw([&] { return run_decode(c, layer, batch, a, 1, static_cast<cudaStream_t>(stream)); });
 }
 }  // namespace
 

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "launch_order.h"
+#include "q4_plan.h"
 #include "qa_internal.h"
 
 namespace qa {
@@ -59,9 +60,6 @@ struct Q4PrefillRowsParams {
 };
 static_assert(sizeof(Q4PrefillRowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
-constexpr int kQ4Chunk = 32;       // keys of one pipeline chunk of the decode kernel
-constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
-constexpr int kQ4MaxSplits = 13;   // splits of one (sequence, kv head) = CTAs of one cluster
 constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode launch
 
 // A launched sequence: the slot of its first new token, its place in the cache,
@@ -86,6 +84,8 @@ struct Q4DecodeParams {
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
     int window;                          // attention window in keys (0: all earlier keys)
     int guard;                           // rows below each first new slot that a running launch may write
+    int fault;                           // test hook: withhold the first stage of cluster 0 (FaultPlan)
+    uint64_t wait_ns;                    // limit of every bounded wait
     int early;                           // 1: signal the next launch at once, 0: after the wait
     Q4Seq seq[kQ4MaxSeqPerLaunch];       // the launched sequences
 };

@@ -1,0 +1,131 @@
+// q4_plan.h -- how the 4-bit cache's launches are cut: splits of a decode step
+// and runs of query blocks of a prefill (host code only, no CUDA dependency).
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+#include <vector>
+
+namespace qa {
+
+constexpr int kQ4Chunk = 32;       // keys of one warp's part of a stage of the decode kernel
+constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
+constexpr int kQ4MaxSplits = 13;   // splits of one (sequence, kv head) = CTAs of one cluster
+
+// Splits of a sequence and kv head (CTAs of a cluster).  A CTA costs a fixed
+// part (its prologue and the merge) and a part per stage of 256 keys; CTAs that
+// share an SM slow each other down.  Fitted on GB300 (D = 128, steps apart from
+// each other, 512 to 16384 keys, 8 to 192 groups): 2.6 us + 1.1 us a stage for a
+// CTA alone on its SM, 3.6 + 1.85 for two; at D = 64 a stage costs 0.66 times
+// that.  CTAs get SMs of their own as long as the launch has at most 96 of them,
+// or 128 in clusters of up to 4.  Only plans whose clusters all fit on the device
+// at once (held[S] clusters of S CTAs) are weighed, the fewest CTAs among
+// equals.  (B = 4, 8 kv heads: 4 splits at 2048 keys take 7.8 us and 8 take 8.4;
+// at 16384 keys 23.2 and 21.4.)
+inline int choose_splits(int D, const int *held, int groups, int keys) {
+    const int chunks = (keys + kQ4Chunk - 1) / kQ4Chunk;
+    const float stage = D == 128 ? 1.f : 0.66f;
+    if (!held) return 1;
+    int best = 1;
+    float least = 1e30f;
+    for (int S = 1; S <= kQ4MaxSplits && (S == 1 || S <= chunks); ++S) {
+        if (S > 1 && held[S] < groups) continue;
+        const int64_t ctas = static_cast<int64_t>(groups) * S;
+        const int rounds = ((chunks + S - 1) / S + kQ4DecodeWarps - 1) / kQ4DecodeWarps;
+        const bool alone = ctas <= (S <= 4 ? 128 : 96);
+        const float us = alone ? 2.6f + 1.1f * stage * rounds : 3.6f + 1.85f * stage * rounds;
+        if (us < least - 0.01f) {
+            least = us;
+            best = S;
+        }
+    }
+    return best;
+}
+
+// A run of query blocks of one sequence of a prefill launch: rows first ..
+// first + len - 1 of its new tokens.
+struct QueryRun {
+    int seq, first, len;
+};
+
+// Time of the prefill attention of `runs` in units of key tiles: its items are
+// dealt out level by level (the block within its run, the highest first), then
+// by run, to `workers` in snake order; a block costs its key tiles and about
+// one more.  `copies`: items of a block (kv heads and head groups).
+inline int prefill_span(const std::vector<QueryRun> &runs, const int *start, int window, int copies, int workers,
+                        std::vector<int> &load) {
+    load.assign(workers, 0);
+    int levels = 0, idx = 0;
+    for (const QueryRun &r : runs) levels = std::max(levels, (r.len + 127) / 128);
+    for (int lvl = levels - 1; lvl >= 0; --lvl)
+        for (const QueryRun &r : runs) {
+            if (r.len <= lvl * 128) continue;
+            const int pos = start[r.seq] + r.first + lvl * 128;
+            const int from = window > 0 ? std::max(0, pos + 1 - window) / 128 : 0;
+            const int tiles = (pos + std::min(r.len - 1 - lvl * 128, 127)) / 128 + 1 - from + 1;
+            for (int k = 0; k < copies; ++k, ++idx) {
+                const int round = idx / workers, at = idx % workers;
+                load[round & 1 ? workers - 1 - at : at] += tiles;
+            }
+        }
+    return *std::max_element(load.begin(), load.end());
+}
+
+// The form that a launch of so many query blocks takes: pairs of CTAs on four
+// heads when every pair gets an item, else CTAs on two heads, or on one when
+// there are fewer items than SMs.  copies: items of a block.
+inline void prefill_form(int blocks, int D, int G, int Hkv, int sms, int &workers, int &copies) {
+    workers = sms / 2;
+    copies = Hkv * (G / 4);
+    if (D == 128 && G % 4 == 0 && blocks * copies >= workers) return;
+    workers = sms;
+    copies = Hkv * ((G + 1) / 2);
+    if (G > 1 && blocks * copies < workers) copies = Hkv * G;
+}
+
+// The runs a prefill launch is made of.  The kernel deals its items out by the
+// block's place in its run, which is their weight when every sequence starts at
+// 0; behind caches of different lengths it is not, and heavy blocks dealt late
+// leave most of the device idle at the end.  So the sequences may go in by falling
+// start, and the ones that start lowest may be cut into shorter runs (up to the
+// 8 of a launch), whose blocks then come later.  Results are the same bits: an
+// item does not depend on its neighbours.  (777 tokens behind 4099 and 1001
+// behind 1025, 32 / 8 heads: 124 us as two runs, 86 us cut.)
+inline void plan_runs(std::vector<QueryRun> &runs, const int *start, int window, int D, int G, int Hkv, int sms,
+                      int max_runs) {
+    bool same = true;
+    int blocks = 0;
+    for (const QueryRun &r : runs) {
+        same = same && start[r.seq] == start[runs[0].seq];
+        blocks += (r.len + 127) / 128;
+    }
+    int workers, copies;
+    prefill_form(blocks, D, G, Hkv, sms, workers, copies);
+    if (same || blocks * copies <= workers || blocks > 256) return;
+    std::vector<int> load;
+    std::vector<QueryRun> best = runs;
+    int least = prefill_span(runs, start, window, copies, workers, load);
+    std::stable_sort(runs.begin(), runs.end(),
+                     [&](const QueryRun &x, const QueryRun &y) { return start[x.seq] > start[y.seq]; });
+    int span = prefill_span(runs, start, window, copies, workers, load);
+    if (span < least) {
+        least = span;
+        best = runs;
+    }
+    for (size_t cut = 1; cut <= runs.size(); ++cut)        // the last `cut` sequences
+        for (int m : {1, 2, 3, 4, 6, 8}) {                  // into runs of m blocks
+            std::vector<QueryRun> tried(runs.begin(), runs.end() - cut);
+            for (size_t i = runs.size() - cut; i < runs.size(); ++i)
+                for (int at = (runs[i].len - 1) / (128 * m) * (128 * m); at >= 0; at -= 128 * m)
+                    tried.push_back({runs[i].seq, at, std::min(128 * m, runs[i].len - at)});
+            if (tried.size() > static_cast<size_t>(max_runs) || tried.size() == runs.size()) continue;
+            span = prefill_span(tried, start, window, copies, workers, load);
+            if (span < least) {
+                least = span;
+                best = tried;
+            }
+        }
+    runs = best;
+}
+
+}  // namespace qa

@@ -272,7 +272,7 @@ qa_status qa_get_device_error(qa_cache *cache, uint32_t *detail);
 
 /* Failure-detection test hook.  Arms the next launch of `kernel`
  * (QA_KERNEL_PREFILL_ATTN, or QA_KERNEL_DECODE_ATTN: decode steps, short
- * chunks and qa_decode_step_noalloc), process-wide: in that launch one tile
+ * chunks and qa_decode_step_noalloc, and those of a 4-bit cache), process-wide: in that launch one tile
  * copy is withheld (prefill: a V tile of the first thread block, or both
  * halves of it in the first CTA pair of the pair form; decode: the first cache
  * chunk of each block of the first sequence's first kv-head group that streams
@@ -443,9 +443,9 @@ qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t 
 
 /* One decode step: one new token for each of sequences 0..batch-1 at
  * positions[b] (HOST), which attends to positions 0..positions[b], within the
- * layer's window.  Tensors as qa_decode_step; out must not alias q, k or v.
+ * layer's window.  Tensors as qa_decode_step.
  * k_held, v_held: both NULL, or [batch][Hkv][D] that receive the new rows as
- * the cache holds them.
+ * the cache holds them.  out, k_held and v_held must not alias q, k or v.
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (a position at or above the
  * capacity), CUDA. */
 qa_status qa_q4_decode_step(qa_q4_cache *cache, int layer, int batch, const int32_t *positions,

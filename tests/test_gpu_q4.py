@@ -516,3 +516,134 @@ def test_memory_info(qa):
         assert scratch >= 2 * 8 * 2 * 100 * 128 * 2
     finally:
         qa.qa_q4_cache_free(c)
+
+
+def test_sequences_behind_the_batch_are_left_alone(qa):
+    # A cache of four sequences, calls on the first two: the others' bytes stay.
+    with Cache(qa, 1, 4, 8, 2, 128, 160) as c:
+        c.fill(0, [64, 100], 5)
+        for ntok, what in (([1, 1], "step"), ([3, 2], "chunk"), ([20, 9], "prefill")):
+            start = [64, 100] if what == "step" else [65, 101] if what == "chunk" else [68, 103]
+            q, k, v = c.tokens(ntok, 6)
+            out = torch.empty_like(q)
+            if what == "step":
+                qa.qa_q4_decode_step(c.h, 0, start, q, k, v, c.wq, c.wk, out)
+            else:
+                qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+            qp, kp = c.transform(start, ntok, q, k, v)
+            c.note(0, start, ntok, kp, f64(v))
+            c.check_bytes()
+            want, mag = c.want(start, ntok, qp)
+            close(out, want, mag, PREFILL_BITS if max(ntok) > 8 else DECODE_BITS, what)
+
+
+def test_offsets_past_32_bits(qa):
+    # 2^26 rows of K and of V: 2^32 bytes of codes each; the last sequence lies
+    # behind that border, and its last rows at its end.
+    cap, batch, hkv = 1 << 19, 16, 8
+    h = qa.qa_q4_cache_alloc(1, batch, hkv, hkv, 128, cap, THETA, EPS)
+    try:
+        n = 300
+        start, ntok = [0] * 15 + [cap - n - 1], [1] * 15 + [n]
+        k, v = rows(1, sum(ntok), hkv, 128), rows(2, sum(ntok), hkv, 128)
+        kh, vh = torch.empty_like(k), torch.empty_like(v)
+        qa.qa_q4_append(h, 0, start, ntok, k, v, kh, vh)
+        kr, vr = torch.empty_like(k), torch.empty_like(v)
+        qa.qa_q4_read(h, 0, start, ntok, kr, vr)
+        assert torch.equal(kr, kh) and torch.equal(vr, vh)
+        codes, scales = q4_ref.quantise(f64(k))
+        np.testing.assert_array_equal(f64(kh), q4_ref.values(codes, scales))
+        # A window keeps the step on the rows that were written.
+        qa.qa_q4_cache_set_window(h, 0, n + 1)
+        one = torch.ones(128, device="cuda").bfloat16()
+        pos = [1] * 15 + [cap - 1]
+        q, kn, vn = rows(3, 16, hkv, 128), rows(4, 16, hkv, 128), rows(5, 16, hkv, 128)
+        out, kn_h, vn_h = torch.empty_like(q), torch.empty_like(kn), torch.empty_like(vn)
+        qa.qa_q4_decode_step(h, 0, pos, q, kn, vn, one, one, out, kn_h, vn_h)
+        assert qa.qa_q4_get_device_error(h) == (0, 0)
+        # the last sequence's step, against its rows as they are held
+        ang = (cap - 1) * THETA ** (-2.0 * np.arange(64) / 128)
+        f = q[15].double()
+        y = (f / torch.sqrt((f * f).mean(-1, keepdim=True) + EPS)).bfloat16().double()
+        cs, sn = torch.from_numpy(np.cos(ang)).cuda(), torch.from_numpy(np.sin(ang)).cuda()
+        qp = torch.cat((y[:, :64] * cs - y[:, 64:] * sn, y[:, 64:] * cs + y[:, :64] * sn), -1).bfloat16().double()
+        kk = torch.cat((kh[15:].double(), kn_h[15:].double())).transpose(0, 1)
+        vv = torch.cat((vh[15:].double(), vn_h[15:].double())).transpose(0, 1)
+        want, mag = q4_ref.attend(qp[None], kk, vv, n)
+        # A query rounded the other way by the kernel's fp32 root moves a score by
+        # 2^-8 |q_i k_i| / sqrt(D): below 2^-8 * 4 * 4 / 11 = 2^-8 * 1.5 of a weight's size.
+        close(out[15:], want, mag, 7)
+    finally:
+        qa.qa_q4_cache_free(h)
+
+
+def test_steps_beside_a_bf16_cache_on_one_stream(qa):
+    # Both caches' decode steps back to back, as a model with some layers in each
+    # would make them: neither disturbs the other's order.
+    steps = 12
+    with Cache(qa, 1, 2, 8, 2, 128, 128) as c:
+        c.fill(0, [100, 37], 5)
+        h = qa.qa_cache_alloc(1, 2, 8, 2, 128, 128, THETA, EPS)
+        try:
+            ks, vs, _ = qa.cache_tensors(h, 0, 2, 2, 128, 128)
+            ks.copy_(rows(71, 2, 2, 128, 128))
+            vs.copy_(rows(72, 2, 2, 128, 128))
+            qa.qa_cache_set_lengths(h, 0, [100, 37])
+            calls = [(c.tokens([1, 1], 300 + 10 * i), [100 + i, 37 + i]) for i in range(steps)]
+            got4, got16 = ([torch.empty_like(x[0][0]) for x in calls] for _ in range(2))
+            torch.cuda.synchronize()
+            for ((q, k, v), pos), o4, o16 in zip(calls, got4, got16):
+                qa.qa_q4_decode_step(c.h, 0, pos, q, k, v, c.wq, c.wk, o4)
+                qa.qa_decode_step(h, 0, 2, q, k, v, c.wq, c.wk, o16)
+            torch.cuda.synchronize()
+            for i, ((q, k, v), pos) in enumerate(calls):
+                qp, kp = c.transform(pos, [1, 1], q, k, v)
+                c.note(0, pos, [1, 1], kp, f64(v))
+                want, mag = c.want(pos, [1, 1], qp)
+                close(got4[i], want, mag, DECODE_BITS, f"4-bit step {i}")
+                kp = torch.from_numpy(kp).cuda()
+                outs = [q4_ref.attend(qp[b:b + 1],
+                                      torch.cat((ks[b, :, :n].double(), kp[b, :, None]), 1),
+                                      torch.cat((vs[b, :, :n].double(), v[b, :, None].double()), 1), n) for b, n in enumerate(pos)]
+                close(got16[i], torch.cat([o for o, _ in outs]), torch.cat([m for _, m in outs]), PREFILL_BITS, f"bf16 step {i}")
+        finally:
+            qa.qa_cache_free(h)
+
+
+def test_calls_allocate_nothing(qa):
+    with Cache(qa, 1, 2, 8, 2, 128, 600) as c:
+        sets = {n: c.tokens([n, n], n) for n in (1, 4, 200)}
+        outs = {n: torch.empty_like(s[0]) for n, s in sets.items()}
+
+        def calls():
+            for n, (q, k, v) in sets.items():
+                qa.qa_q4_prefill(c.h, 0, [300, 7], [n, n], q, k, v, c.wq, c.wk, outs[n])
+                qa.qa_q4_append(c.h, 0, [300, 7], [n, n], k, v)
+                qa.qa_q4_read(c.h, 0, [300, 7], [n, n], k, v)
+            qa.qa_q4_decode_step(c.h, 0, [300, 7], *sets[1], c.wq, c.wk, outs[1])
+            torch.cuda.synchronize()
+
+        calls()
+        free = torch.cuda.mem_get_info()[0]
+        for _ in range(20):
+            calls()
+        assert torch.cuda.mem_get_info()[0] == free
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_cache_stays_usable(qa):
+    lens = [700, 300]
+    with Cache(qa, 1, 2, 32, 8, 128, 1024) as c:
+        c.fill(0, lens, 5)
+        q, k, v = c.tokens([1, 1], 6)
+        out = torch.empty_like(q)
+        qa.qa_debug_arm_wait_timeout(2, 20000)  # the next decode launch: 20 ms
+        qa.qa_q4_decode_step(c.h, 0, lens, q, k, v, c.wq, c.wk, out)
+        st, word = qa.qa_q4_get_device_error(c.h)
+        assert st == 7 and word & 0xff == 1 and word >> 8 & 0xff == 5
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        qa.qa_q4_decode_step(c.h, 0, lens, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        qp, kp = c.transform(lens, [1, 1], q, k, v)
+        c.note(0, lens, [1, 1], kp, f64(v))
+        want, mag = c.want(lens, [1, 1], qp)
+        close(out, want, mag, DECODE_BITS)
