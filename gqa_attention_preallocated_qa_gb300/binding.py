@@ -291,47 +291,46 @@ def cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
 
 
 # ---- 4-bit cache.  Position lists are sequences of ints, or ready ctypes int32
-# arrays.  These calls are made once per layer and token, so their wrappers
-# look nothing up that they can keep.
+# arrays.  The calls below are made once per layer and token, and on a host
+# thread they cost more than their kernels: their wrappers look nothing up that
+# they can keep, and take tensors first (addresses go the longer way).
 
-_PACK = [struct.Struct(f"{n}i") for n in range(257)]
+_PACK = [struct.Struct(f"{n}i").pack for n in range(257)]
 
 
 def _i32_bytes(values):
     if isinstance(values, ctypes.Array):
         return values
     n = len(values)
-    return (_PACK[n] if n <= 256 else struct.Struct(f"{n}i")).pack(*values)
-
-
-def _ranges(start, ntok):
-    if len(start) != len(ntok):
-        raise ValueError("start and ntok need one entry per sequence")
-    return len(start), _i32_bytes(start), _i32_bytes(ntok)
+    return (_PACK[n] if n <= 256 else struct.Struct(f"{n}i").pack)(*values)
 
 
 def _q4_stream(s):
-    if s is None:
-        if _raw_stream is None:
-            _find_raw_stream()
-        return _raw_stream(_current_device())
     return s if isinstance(s, int) else s.cuda_stream
 
 
-_raw_stream = _current_device = None
-
-
-def _find_raw_stream():
+def _current_stream():
     """torch's current stream as a handle, without building its Stream object."""
-    global _raw_stream, _current_device
+    global _current_stream
     import torch
-    if torch.cuda.is_available():
-        torch.cuda.init()
-        _current_device = torch.cuda.current_device
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda device: torch.cuda.current_stream(device).cuda_stream)
+    if not torch.cuda.is_available():
+        return None
+    torch.cuda.init()
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw and device:
+        _current_stream = lambda: raw(device())  # noqa: E731
     else:
-        _current_device, _raw_stream = (lambda: 0), (lambda device: None)
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
+
+
+def _at(x):
+    """Address of a tensor; an address or None as it is."""
+    return x.data_ptr() if hasattr(x, "data_ptr") else x
+
+
+_q4_append, _q4_read, _q4_prefill = lib.qa_q4_append, lib.qa_q4_read, lib.qa_q4_prefill
+_q4_decode, _q4_decode_device = lib.qa_q4_decode_step, lib.qa_q4_decode_step_device_positions
 
 
 def qa_q4_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
@@ -351,47 +350,69 @@ def qa_q4_cache_set_window(cache, layer, window) -> None:
     _check(lib.qa_q4_cache_set_window(cache, layer, window), "qa_q4_cache_set_window")
 
 
-def _at(x):
-    """Address of a tensor; an address or None as it is."""
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        return x
+def _q4_lens(start, ntok):
+    n = len(start)
+    if len(ntok) != n:
+        raise ValueError("start and ntok need one entry per sequence")
+    return n
 
 
 def qa_q4_append(cache, layer, start, ntok, k, v, k_held=None, v_held=None, stream=None) -> None:
-    n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_append(cache, layer, n, s, t, _at(k), _at(v), _at(k_held), _at(v_held),
-                            _q4_stream(stream)), "qa_q4_append")
+    n = _q4_lens(start, ntok)
+    s = _current_stream() if stream is None else _q4_stream(stream)
+    try:
+        at = (k.data_ptr(), v.data_ptr(), k_held.data_ptr(), v_held.data_ptr())
+    except AttributeError:
+        at = (_at(k), _at(v), _at(k_held), _at(v_held))
+    st = _q4_append(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), *at, s)
+    if st:
+        raise QaError(st, "qa_q4_append")
 
 
 def qa_q4_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
-    n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_read(cache, layer, n, s, t, _at(k_out), _at(v_out), _q4_stream(stream)),
-           "qa_q4_read")
+    n = _q4_lens(start, ntok)
+    s = _current_stream() if stream is None else _q4_stream(stream)
+    st = _q4_read(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), _at(k_out), _at(v_out), s)
+    if st:
+        raise QaError(st, "qa_q4_read")
 
 
 def qa_q4_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
                   stream=None) -> None:
-    n, s, t = _ranges(start, ntok)
-    _check(lib.qa_q4_prefill(cache, layer, n, s, t, _at(q), _at(k), _at(v), _at(q_norm_w),
-                             _at(k_norm_w), _at(out), _q4_stream(stream)), "qa_q4_prefill")
+    n = _q4_lens(start, ntok)
+    s = _current_stream() if stream is None else _q4_stream(stream)
+    try:
+        at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
+              out.data_ptr())
+    except AttributeError:
+        at = tuple(map(_at, (q, k, v, q_norm_w, k_norm_w, out)))
+    st = _q4_prefill(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), *at, s)
+    if st:
+        raise QaError(st, "qa_q4_prefill")
 
 
 def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
                       v_held=None, stream=None) -> None:
-    _check(lib.qa_q4_decode_step(cache, layer, len(positions), _i32_bytes(positions), _at(q), _at(k),
-                                 _at(v), _at(q_norm_w), _at(k_norm_w), _at(out), _at(k_held),
-                                 _at(v_held), _q4_stream(stream)), "qa_q4_decode_step")
+    s = _current_stream() if stream is None else _q4_stream(stream)
+    try:
+        at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
+              out.data_ptr())
+    except AttributeError:
+        at = tuple(map(_at, (q, k, v, q_norm_w, k_norm_w, out)))
+    st = _q4_decode(cache, layer, len(positions), _i32_bytes(positions), *at, _at(k_held),
+                    _at(v_held), s)
+    if st:
+        raise QaError(st, "qa_q4_decode_step")
 
 
 def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
                                        out, k_held=None, v_held=None, stream=None) -> None:
     """positions: int32 device tensor [batch] (see include/qa.h)."""
-    _check(lib.qa_q4_decode_step_device_positions(
-        cache, layer, batch, _at(positions), _at(q), _at(k), _at(v), _at(q_norm_w),
-        _at(k_norm_w), _at(out), _at(k_held), _at(v_held), _q4_stream(stream)),
-           "qa_q4_decode_step_device_positions")
+    s = _current_stream() if stream is None else _q4_stream(stream)
+    at = map(_at, (positions, q, k, v, q_norm_w, k_norm_w, out, k_held, v_held))
+    st = _q4_decode_device(cache, layer, batch, *at, s)
+    if st:
+        raise QaError(st, "qa_q4_decode_step_device_positions")
 
 
 def qa_q4_cache_view(cache, layer):
