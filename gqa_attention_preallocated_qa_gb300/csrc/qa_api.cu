@@ -159,9 +159,11 @@ bool qa::supported_geometry(int n_q_heads, int n_kv_heads, int head_dim) {
 
 // angle = pos * theta^(-2i/D)
 void qa::fill_rope_table(float2 *tab, int capacity, int D, float theta) {
+    double freq[64];
+    for (int i = 0; i < D / 2; ++i) freq[i] = std::pow(static_cast<double>(theta), -2.0 * i / D);
     for (int pos = 0; pos < capacity; ++pos)
         for (int i = 0; i < D / 2; ++i) {
-            const double a = static_cast<double>(pos) * std::pow(static_cast<double>(theta), -2.0 * i / D);
+            const double a = static_cast<double>(pos) * freq[i];
             tab[static_cast<size_t>(pos) * (D / 2) + i] =
                 make_float2(static_cast<float>(std::cos(a)), static_cast<float>(std::sin(a)));
         }
