@@ -1,4 +1,6 @@
-"""Builds ``libqa.so`` (the C ABI of include/qa.h) in-tree with nvcc for sm_103a.
+"""Builds ``libqa.so`` (the C ABI of include/qa.h) in-tree with nvcc for sm_103a,
+and beside it ``_q4calls.so``, the binding's native marshalling of the calls
+that are made once per layer and token.
 
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
@@ -10,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqa.so")
+CALLS = os.path.join(PKG, "_q4calls.so")
 SOURCES = ["qa_api.cu", "k1_norm_rope_append.cu", "k2_prefill_tcgen05.cu", "k3_decode_splitkv.cu",
            "q4_api.cu", "k4_q4_rows.cu", "k5_q4_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,9 +43,9 @@ def _inputs():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -58,14 +62,30 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _build_calls() -> None:
+    """_q4calls.so: plain C++ against this interpreter's headers, no CUDA."""
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("g++ not found: it is required to build _q4calls.so")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-fwrapv",
+           "-I", sysconfig.get_path("include"), os.path.join(CSRC, "q4_calls.cpp"), "-o", tmp]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on q4_calls.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, extra=()) -> str:
-    """Compile and link libqa.so if any source changed (or ``force``)."""
+    """Compile and link libqa.so and _q4calls.so if any source changed (or ``force``)."""
     with _lock:
         if not force and not stale():
             return LIB
         os.makedirs(BUILD, exist_ok=True)
-        with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+            calls = ex.submit(_build_calls)
             objs = list(ex.map(lambda s: _compile(s, list(extra)), SOURCES))
+            calls.result()
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static",
                "-Xlinker", "--version-script=" + os.path.join(CSRC, "libqa.map"), "-o", tmp, *objs]

@@ -3,6 +3,7 @@
 Argument marshalling only: tensors are passed as device pointers (torch
 tensors or plain integers), host arrays as int32 buffers, streams as
 cudaStream_t handles.  Every step of the path runs in the library's kernels.
+The 4-bit cache's per-token calls are marshalled by ``_q4calls.so`` instead.
 Importing this module loads the library and raises ImportError if it has not
 been built; there is no fallback.
 """
@@ -10,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 from . import _build
 
@@ -75,12 +75,12 @@ SIGNATURES = {
     "qa_q4_cache_alloc": (ctypes.c_int, [ctypes.POINTER(qa_config), ctypes.POINTER(_vp)]),
     "qa_q4_cache_free": (ctypes.c_int, [_vp]),
     "qa_q4_cache_set_window": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int]),
-    "qa_q4_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+    "qa_q4_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
                                     _vp, _vp]),
-    "qa_q4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp]),
-    "qa_q4_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+    "qa_q4_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp]),
+    "qa_q4_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
                                      _vp, _vp, _vp, _vp]),
-    "qa_q4_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
+    "qa_q4_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp,
                                          _vp, _vp, _vp, _vp, _vp, _vp]),
     "qa_q4_decode_step_device_positions": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp,
                                                           _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -107,6 +107,8 @@ def _load():
 
 
 lib = _load()
+
+from . import _q4calls  # noqa: E402  (built beside the library)
 
 
 def _ptr(x) -> int | None:
@@ -290,47 +292,35 @@ def cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
     return kt, vt, lt
 
 
-# ---- 4-bit cache.  Position lists are sequences of ints, or ready ctypes int32
-# arrays.  The calls below are made once per layer and token, and on a host
-# thread they cost more than their kernels: their wrappers look nothing up that
-# they can keep, and take tensors first (addresses go the longer way).
-
-_PACK = [struct.Struct(f"{n}i").pack for n in range(257)]
-
-
-def _i32_bytes(values):
-    if isinstance(values, ctypes.Array):
-        return values
-    n = len(values)
-    return (_PACK[n] if n <= 256 else struct.Struct(f"{n}i").pack)(*values)
-
-
-def _q4_stream(s):
-    return s if isinstance(s, int) else s.cuda_stream
-
+# ---- 4-bit cache.  Tensors are torch tensors, addresses or None; position lists
+# are sequences of ints or int32 buffers.  The calls that are made once per layer
+# and token go through _q4calls (csrc/q4_calls.cpp), which marshals the same
+# arguments as ctypes would in a quarter of the time.
 
 def _current_stream():
     """torch's current stream as a handle, without building its Stream object."""
-    global _current_stream
     import torch
     if not torch.cuda.is_available():
         return None
     torch.cuda.init()
     raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
     if raw and device:
-        _current_stream = lambda: raw(device())  # noqa: E731
+        def now():
+            return raw(device())
     else:
-        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-    return _current_stream()
+        def now():
+            return torch.cuda.current_stream().cuda_stream
+    _bind_calls(now)
+    return now()
 
 
-def _at(x):
-    """Address of a tensor; an address or None as it is."""
-    return x.data_ptr() if hasattr(x, "data_ptr") else x
+def _bind_calls(current_stream) -> None:
+    _q4calls.bind(*(ctypes.cast(getattr(lib, name), _vp).value
+                    for name in ("qa_q4_append", "qa_q4_read", "qa_q4_prefill", "qa_q4_decode_step",
+                                 "qa_q4_decode_step_device_positions")), current_stream)
 
 
-_q4_append, _q4_read, _q4_prefill = lib.qa_q4_append, lib.qa_q4_read, lib.qa_q4_prefill
-_q4_decode, _q4_decode_device = lib.qa_q4_decode_step, lib.qa_q4_decode_step_device_positions
+_bind_calls(_current_stream)  # replaced by what it finds at the first call
 
 
 def qa_q4_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
@@ -350,57 +340,29 @@ def qa_q4_cache_set_window(cache, layer, window) -> None:
     _check(lib.qa_q4_cache_set_window(cache, layer, window), "qa_q4_cache_set_window")
 
 
-def _q4_lens(start, ntok):
-    n = len(start)
-    if len(ntok) != n:
-        raise ValueError("start and ntok need one entry per sequence")
-    return n
-
-
 def qa_q4_append(cache, layer, start, ntok, k, v, k_held=None, v_held=None, stream=None) -> None:
-    n = _q4_lens(start, ntok)
-    s = _current_stream() if stream is None else _q4_stream(stream)
-    try:
-        at = (k.data_ptr(), v.data_ptr(), k_held.data_ptr(), v_held.data_ptr())
-    except AttributeError:
-        at = (_at(k), _at(v), _at(k_held), _at(v_held))
-    st = _q4_append(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), *at, s)
+    st = _q4calls.append(cache, layer, start, ntok, k, v, k_held, v_held, stream)
     if st:
         raise QaError(st, "qa_q4_append")
 
 
 def qa_q4_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
-    n = _q4_lens(start, ntok)
-    s = _current_stream() if stream is None else _q4_stream(stream)
-    st = _q4_read(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), _at(k_out), _at(v_out), s)
+    st = _q4calls.read(cache, layer, start, ntok, k_out, v_out, stream)
     if st:
         raise QaError(st, "qa_q4_read")
 
 
 def qa_q4_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
                   stream=None) -> None:
-    n = _q4_lens(start, ntok)
-    s = _current_stream() if stream is None else _q4_stream(stream)
-    try:
-        at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
-              out.data_ptr())
-    except AttributeError:
-        at = tuple(map(_at, (q, k, v, q_norm_w, k_norm_w, out)))
-    st = _q4_prefill(cache, layer, n, _i32_bytes(start), _i32_bytes(ntok), *at, s)
+    st = _q4calls.prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out, stream)
     if st:
         raise QaError(st, "qa_q4_prefill")
 
 
 def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
                       v_held=None, stream=None) -> None:
-    s = _current_stream() if stream is None else _q4_stream(stream)
-    try:
-        at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
-              out.data_ptr())
-    except AttributeError:
-        at = tuple(map(_at, (q, k, v, q_norm_w, k_norm_w, out)))
-    st = _q4_decode(cache, layer, len(positions), _i32_bytes(positions), *at, _at(k_held),
-                    _at(v_held), s)
+    st = _q4calls.decode(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held, v_held,
+                         stream)
     if st:
         raise QaError(st, "qa_q4_decode_step")
 
@@ -408,9 +370,8 @@ def qa_q4_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out,
 def qa_q4_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
                                        out, k_held=None, v_held=None, stream=None) -> None:
     """positions: int32 device tensor [batch] (see include/qa.h)."""
-    s = _current_stream() if stream is None else _q4_stream(stream)
-    at = map(_at, (positions, q, k, v, q_norm_w, k_norm_w, out, k_held, v_held))
-    st = _q4_decode_device(cache, layer, batch, *at, s)
+    st = _q4calls.decode_device(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w, out,
+                                k_held, v_held, stream)
     if st:
         raise QaError(st, "qa_q4_decode_step_device_positions")
 

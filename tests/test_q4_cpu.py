@@ -76,3 +76,24 @@ def test_alloc_rejects_bad_geometry(qa, kw, status):
 def test_ranges_need_one_entry_per_sequence(qa):
     with pytest.raises(ValueError):
         qa.qa_q4_append(None, 0, [0, 0], [1], 16, 16)
+
+
+def test_arguments_of_the_native_calls(qa):
+    """Tensors, addresses, None; lists, tuples, int32 buffers: all reach the C
+    entry point (which refuses the null cache), and nothing else does."""
+    import torch
+    x = torch.zeros(16, dtype=torch.bfloat16)
+    for pos in ([0, 0], (0, 0), (ctypes.c_int32 * 2)(0, 0), np.zeros(2, np.int32), np.zeros(2, np.int64),
+                torch.zeros(2, dtype=torch.int32)):
+        with pytest.raises(qa.QaError) as e:
+            qa.qa_q4_decode_step(None, 0, pos, x, x.data_ptr(), x, x, x, x, stream=0)
+        assert e.value.status == 1
+    for bad in ([0.5], ["0"], 3, None, [None]):
+        with pytest.raises(TypeError):
+            qa.qa_q4_decode_step(None, 0, bad, x, x, x, x, x, x, stream=0)
+    with pytest.raises(OverflowError):
+        qa.qa_q4_decode_step(None, 0, [1 << 31], x, x, x, x, x, x, stream=0)
+    with pytest.raises(AttributeError):  # not a tensor
+        qa.qa_q4_read(None, 0, [0], [1], np.zeros(4, np.uint16), x, stream=0)
+    with pytest.raises(TypeError):
+        qa._q4calls.read(None, 0, [0], [1])
