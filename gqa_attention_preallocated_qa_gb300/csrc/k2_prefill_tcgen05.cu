@@ -52,6 +52,8 @@ __device__ __forceinline__ float k2_ex2(float x) {
 // The softmax rescales O only when a row's max grows by more than this many
 // powers of two (in the exp2 domain).
 constexpr float kRescaleLog2 = 8.f;
+// ... and one that has summed nothing goes down by more than this.
+constexpr float kFollowLog2 = -64.f;
 
 
 // ==================================================================== the kernel
@@ -382,10 +384,14 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                     if (j == 0) {
                         mref = mx == -INFINITY ? 0.f : mx;  // a window can mask a whole tile
                     } else {
-                        const bool grow = (mx - mref) * c > kRescaleLog2;
+                        // Behind masked tiles mref is still 0: scores far below it
+                        // would all vanish, so nothing summed yet, it follows them down.
+                        const float up = (mx - mref) * c;
+                        const bool down = kWindow && l == 0.f && up < kFollowLog2 && mx > -INFINITY;
+                        const bool grow = up > kRescaleLog2 || down;
                         rescale = __any_sync(FULL, grow);
                         if (grow) {
-                            alpha = k2_ex2((mref - mx) * c);
+                            alpha = down ? 0.f : k2_ex2((mref - mx) * c);
                             mref = mx;
                             l *= alpha;
                         }
@@ -830,10 +836,12 @@ __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
                 if (j == 0) {
                     mref = mx == -INFINITY ? 0.f : mx;
                 } else {
-                    const bool grow = (mx - mref) * c > kRescaleLog2;
+                    const float up = (mx - mref) * c;
+                    const bool down = kWindow && l == 0.f && up < kFollowLog2 && mx > -INFINITY;
+                    const bool grow = up > kRescaleLog2 || down;
                     rescale = __any_sync(FULL, grow);
                     if (grow) {
-                        alpha = k2_ex2((mref - mx) * c);
+                        alpha = down ? 0.f : k2_ex2((mref - mx) * c);
                         mref = mx;
                         l *= alpha;
                     }
