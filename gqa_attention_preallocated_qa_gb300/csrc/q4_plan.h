@@ -101,7 +101,10 @@ inline void plan_runs(std::vector<QueryRun> &runs, const int *start, int window,
     }
     int workers, copies;
     prefill_form(blocks, D, G, Hkv, sms, workers, copies);
-    if (same || blocks * copies <= workers || blocks > 256) return;
+    // One item or less per worker: no order matters.  Many per worker: none helps
+    // much, and trying them would cost the host more.
+    const int64_t items = static_cast<int64_t>(blocks) * copies;
+    if (same || items <= workers || items > 16 * static_cast<int64_t>(workers)) return;
     std::vector<int> load;
     std::vector<QueryRun> best = runs;
     int least = prefill_span(runs, start, window, copies, workers, load);

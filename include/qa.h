@@ -377,7 +377,9 @@ qa_status qa_noalloc_get_device_error(uint32_t *detail, void *stream);
  * token is dropped by writing its position again.  A call reads only positions
  * below the ones it writes; rows that nothing wrote may hold anything.
  *
- * Conventions as above.  Calls may be made with another device current; the
+ * Conventions as above; a call on more than 64 sequences is several launches,
+ * and an error of a later one leaves the earlier ones enqueued.  Calls may be
+ * made with another device current; the
  * stream belongs to the cache's device.  Row kernels and prefill are ordered
  * on their stream like plain launches; decode steps overlap the previous
  * kernel like qa_decode_step, with the same condition on q, k, v and the
