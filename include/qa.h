@@ -437,7 +437,10 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * With every ntok at most 8 the decode kernel does all of it, one launch per
  * 64 sequences.  Otherwise K4 and K2 run through the cache's workspace, 8
  * sequences at a time: such calls on several streams wait for each other, and
- * they cannot be captured into a graph (QA_ERR_STATE).
+ * they cannot be captured into a graph (QA_ERR_STATE).  In that form a key or
+ * value that is not finite can reach other new tokens of its sequence in the
+ * call, also those before it (as in qa_prefill: the tensor cores multiply it by
+ * their weight of zero).
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
 qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
                         const int32_t *ntok, const void *q, const void *k, const void *v,
