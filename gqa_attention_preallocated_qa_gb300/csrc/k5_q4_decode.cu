@@ -4,7 +4,8 @@
 // With q' the normed and rotated query, K_j = (n_j - 8) s_j and V_j likewise
 // (s per group of 32 values):
 //   t_j = q' . K_j * log2(e) / sqrt(D),  p_j = 2^(t_j - m),  out = sum p_j V_j / sum p_j.
-// Per (sequence, kv head, head group, split) CTA:
+// Per (sequence, kv head, head group, split) CTA (the splits of one group are in
+// one cluster; short sequences have fewer, and several groups share a cluster):
 //   1. the CTA streams its keys through a ring of stages in shared memory, 256
 //      keys each (32 per warp): a stage is four contiguous runs of the cache
 //      (codes and scale bytes of K and V, 34 KB at D = 128), one bulk copy each.
@@ -24,7 +25,7 @@
 //      eighth of a row from two keys, interleaved by one byte permute.  P goes
 //      from the accumulators to a B fragment by one 8x8 transpose per 8 keys;
 //   4. the warps' partials (m, l, o) are combined in shared memory, pushed to
-//      the CTAs of the cluster (the splits of one sequence and kv head) with
+//      the CTAs of the cluster that hold the group's other splits with
 //      st.async and merged there in a fixed order: no scratch in global memory,
 //      no atomics, the same bits every time.
 #include <algorithm>
@@ -402,9 +403,25 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     float *recv = part_new + Sh::kPartial;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = p.S, split = blockIdx.x;
-    const int kvh = p.HG == 1 ? blockIdx.y : blockIdx.y / p.HG, hg = blockIdx.y - kvh * p.HG;
-    const Q4Seq seq = p.seq[blockIdx.z];
+    int z = blockIdx.z, group = blockIdx.y, split = blockIdx.x;
+    int rank0 = 0;  // the cluster's CTA with this group's split 0
+    if (p.mixed) {  // several numbers of splits: all CTAs along one axis
+        if (static_cast<int>(blockIdx.x) >= p.ctas) {  // fills up the last cluster
+            cluster_arrive();
+            cluster_wait();
+            griddep_wait();
+            return;
+        }
+        z = p.seq_of[blockIdx.x / static_cast<uint32_t>(p.groups)];
+        const uint32_t cta = blockIdx.x - p.seq[z].cta0;
+        // (exact: S is 2, 4 or 8)
+        group = p.seq[z].S == 1 ? cta : __umulhi(cta, p.seq[z].inv_S);
+        split = cta - group * p.seq[z].S;
+        rank0 = cluster_ctarank() - split;
+    }
+    const Q4Seq seq = p.seq[z];
+    const int S = seq.S;
+    const int kvh = p.HG == 1 ? group : group / p.HG, hg = group - kvh * p.HG;
     const int ntok = TPS == 1 ? 1 : seq.ntok;
     const int64_t row_base = static_cast<int64_t>(seq.slot) * p.row_seq + kvh * p.row_head;
     const int h_first = kvh * p.G + hg * HPC;
@@ -427,8 +444,8 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     // Divided by S as a product with ceil(2^32 / S): exact below 2^32 / S, and
     // there are at most 2^19 chunks and 13 splits.  (S = 1: the product is 0.)
     const uint32_t n = nchunks - c_lo;
-    const int c_begin = c_lo + __umulhi(split * n, p.inv_S);
-    const int c_end = split == S - 1 ? nchunks : c_lo + __umulhi((split + 1) * n, p.inv_S);
+    const int c_begin = c_lo + __umulhi(split * n, seq.inv_S);
+    const int c_end = split == S - 1 ? nchunks : c_lo + __umulhi((split + 1) * n, seq.inv_S);
     const int c_safe = p.guard <= 0 ? nchunks : (pos > p.guard ? (pos - p.guard) / kQ4Chunk : 0);
     const int nstages = (c_end - c_begin + NW - 1) / NW;
 
@@ -439,8 +456,8 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const uint32_t bar = smem_u32(&bar_full[st]);
         const int64_t r0 = row_base + static_cast<int64_t>(c) * kQ4Chunk;
         uint32_t dst = smem_u32(smem + st * Sh::kStage);
-        // Test hook: nothing completes the first stage of the first cluster's CTAs.
-        if (p.fault && j == 0 && blockIdx.y == 0 && blockIdx.z == 0) return;
+        // Test hook: nothing completes the first stage of the first group's CTAs.
+        if (p.fault && j == 0 && z == 0 && group == 0) return;
         s_sent[st] = j;
         mbar_expect_tx(bar, keys * 2 * (Sh::kRow + Sh::kScaleRow));
         bulk_g2s(dst, p.kc + r0 * Sh::kRow, keys * Sh::kRow, bar);
@@ -457,9 +474,9 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         }
         mbar_init(smem_u32(&bar_recv), 1);
         s_abort = 0;
-        const int E_me = min(p.E, R * D - split * p.E);
+        const int E_me = min(seq.E, R * D - split * seq.E);
         if (E_me > 0) {
-            const int nh = (split * p.E + E_me - 1) / D - split * p.E / D + 1;
+            const int nh = (split * seq.E + E_me - 1) / D - split * seq.E / D + 1;
             mbar_expect_tx(smem_u32(&bar_recv), S * (E_me * 4 + nh * 8));
         }
         fence_mbar_init();
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     // to the CTA owning the outputs' run.  Runs are multiples of 32 outputs; the
     // first pair of a run or of a row carries the row's (M, L).
     constexpr int total = R * D, kThreads = NW * 32;
-    const int E = p.E;
+    const int E = seq.E;
     float *rcv_o = recv, *rcv_ml = recv + S * E;
     __syncthreads();
     cluster_wait();  // every peer's receive barrier is initialised
@@ -756,13 +773,13 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
             O = make_float2(fmaf(wi, x.x, O.x), fmaf(wi, x.y, O.y));
         }
         const int dst = e / E;
-        const uint32_t bar = map_rank(smem_u32(&bar_recv), dst);
-        st_async_f32x2(map_rank(smem_u32(rcv_o + split * E + e - dst * E), dst), O.x, O.y * 0.0625f, bar);
+        const uint32_t bar = map_rank(smem_u32(&bar_recv), rank0 + dst);
+        st_async_f32x2(map_rank(smem_u32(rcv_o + split * E + e - dst * E), rank0 + dst), O.x, O.y * 0.0625f, bar);
         // (lanes 16-31 hold the (M, L) of no source: lane 0's are sent, by its neighbours too)
         M = __shfl_sync(FULL, M, 0);
         L = __shfl_sync(FULL, L, 0);
         if (e == dst * E || e == g * D)
-            st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), dst), M, L, bar);
+            st_async_f32x2(map_rank(smem_u32(rcv_ml + (split * R + g) * 2), rank0 + dst), M, L, bar);
     }
 
     // ---------------------------------------------------------------- merge
@@ -846,15 +863,15 @@ static cudaError_t q4_configure() {
 }
 
 template <int D, int HPC, int TPS>
-static void q4_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int S, int gy, int gz,
+static void q4_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], int cluster, dim3 grid,
                       cudaStream_t stream) {
     cfg = cudaLaunchConfig_t{};
-    cfg.gridDim = dim3(S, gy, gz);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kQ4DecodeWarps * 32);
     cfg.dynamicSmemBytes = Q4Shape<D, HPC * TPS>::kSmemBytes;
     cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;  // one cluster = the splits of a group
-    attr[0].val.clusterDim.x = S;
+    attr[0].id = cudaLaunchAttributeClusterDimension;  // holds the splits of one group or of several
+    attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -869,7 +886,8 @@ static cudaError_t q4_launch(const Q4DecodeParams &p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
-    q4_config<D, HPC, TPS>(cfg, attr, p.S, p.Hkv * p.HG, p.B, stream);
+    const dim3 grid = p.mixed ? dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster) : dim3(p.cluster, p.groups, p.B);
+    q4_config<D, HPC, TPS>(cfg, attr, p.cluster, grid, stream);
     return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, HPC, TPS>, p);
 }
 
@@ -886,7 +904,7 @@ static const int *q4_capacities() {
     for (int S = 1; S <= kQ4MaxSplits && !failed; ++S) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
-        q4_config<D, HPC, TPS>(cfg, attr, S, 1, 1, nullptr);
+        q4_config<D, HPC, TPS>(cfg, attr, S, dim3(S), nullptr);
         cfg.numAttrs = 1;
         failed = cudaOccupancyMaxActiveClusters(&table[dev][S], q4_decode_kernel<D, HPC, TPS>, &cfg) != cudaSuccess;
     }

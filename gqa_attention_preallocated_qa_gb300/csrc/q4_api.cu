@@ -212,6 +212,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     p.Hkv = g.n_kv_heads;
     p.G = c->G;
     p.HG = c->G / HPC;
+    p.groups = p.Hkv * p.HG;
     p.cap = g.capacity;
     p.eps = g.rms_eps;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
@@ -231,30 +232,45 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
 
     int b = 0, row0 = 0;
     while (b < batch) {
-        int nz = 0, keys = 0, tm = 0;
+        int nz = 0, tm = 0;
         const int first = b;
         for (; b < batch && nz < qa::kQ4MaxSeqPerLaunch; ++b) {
             const int n = a.ntok ? a.ntok[b] : 1;
             if (n > 0) {
-                p.seq[nz] = {a.pos_dev ? 0 : a.start[b], b, n, row0};
-                keys = std::max(keys, a.pos_dev ? g.capacity - 1 : static_cast<int>(a.start[b]));
+                p.seq[nz] = {a.pos_dev ? 0 : a.start[b], b, n, row0, 0, 1, 0, 0};
                 tm = std::max(tm, n);
                 ++nz;
             }
             row0 += n;
         }
         if (nz == 0) break;
-        if (p.window > 0) keys = std::min(keys, p.window);
         // The longest sequences first: thread blocks start in this order, and the
         // short ones fill in behind them.
         std::stable_sort(p.seq, p.seq + nz, [](const qa::Q4Seq &x, const qa::Q4Seq &y) { return x.pos > y.pos; });
-        p.B = nz;
-        p.S = qa::choose_splits(D, qa::q4_cluster_capacities(D, HPC, multi), nz * g.n_kv_heads * p.HG, keys);
+        int keys[qa::kQ4MaxSeqPerLaunch];
+        for (int i = 0; i < nz; ++i) {
+            keys[i] = a.pos_dev ? g.capacity - 1 : p.seq[i].pos;
+            if (p.window > 0) keys[i] = std::min(keys[i], p.window);
+        }
+        qa::DecodePlan plan;
+        qa::plan_decode(D, qa::q4_cluster_capacities(D, HPC, multi), p.groups, nz, keys, plan);
         const int rows = multi ? qa::kQ4MaxTokens : HPC;
-        p.inv_S = p.S == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + p.S - 1) / p.S);
-        p.E = ((rows * D + p.S - 1) / p.S + 31) & ~31;
+        p.ctas = 0;
+        int units = 0;
+        for (int i = 0; i < nz; ++i) {
+            const int S = plan.splits[i];
+            p.seq[i].cta0 = p.ctas;
+            p.seq[i].S = S;
+            p.seq[i].E = ((rows * D + S - 1) / S + 31) & ~31;
+            p.seq[i].inv_S = S == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + S - 1) / S);
+            for (int k = 0; k < S; ++k) p.seq_of[units++] = static_cast<uint8_t>(i);
+            p.ctas += p.groups * S;
+        }
+        p.B = nz;
+        p.cluster = plan.cluster;
+        p.mixed = plan.splits[nz - 1] != plan.cluster ? 1 : 0;
         p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
-        const int guard = qa::launch_order().admit(s, c, layer, p.S * g.n_kv_heads * p.HG * nz, tm,
+        const int guard = qa::launch_order().admit(s, c, layer, p.ctas, tm,
                                                    p.early != 0, resident);
         p.guard = settled ? 0 : guard;
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);

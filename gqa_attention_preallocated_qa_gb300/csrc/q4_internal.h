@@ -21,9 +21,6 @@ constexpr int kQ4Group = 32;
 // start on 16-byte boundaries.
 constexpr int kQ4RowPad = 64;
 
-// Sequences carried in the parameters of one launch.
-constexpr int kQ4MaxSeqPerLaunch = 64;
-
 // The row kernels (quantise, dequantise) work on tokens start[b] .. start[b] +
 // ntok[b] - 1 of each launched sequence.  A row of 16-bit values is addressed
 // by (sequence, token of the call, kv head): base + off[b] + token * tok +
@@ -64,8 +61,12 @@ constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode laun
 
 // A launched sequence: the slot of its first new token, its place in the cache,
 // its new tokens and the first of their rows in q, k, v and out.
+// Its CTAs are cta0 .. of a mixed launch, S for each kv head and head group; each
+// of the S merges a run of E outputs (a multiple of 32); inv_S: ceil(2^32 / S), 0 for 1.
 struct alignas(16) Q4Seq {
     int pos, slot, ntok, row0;
+    int cta0, S, E;
+    uint32_t inv_S;
 };
 
 struct Q4DecodeParams {
@@ -78,9 +79,10 @@ struct Q4DecodeParams {
     const int32_t *pos_dev;              // device positions (null: pos[])
     uint32_t *err;
     int64_t row_seq, row_head;           // cache strides in rows
-    int B, Hq, Hkv, G, HG, cap, S;
-    int E;                               // outputs merged by one CTA of a cluster (a multiple of 32)
-    uint32_t inv_S;                      // ceil(2^32 / S), 0 for S = 1
+    int Hq, Hkv, G, HG, cap;
+    int groups;                          // Hkv * HG
+    int B, ctas, cluster;                // sequences, CTAs with work, CTAs of a cluster
+    int mixed;                           // 0: every sequence has `cluster` splits, grid (cluster, groups, B)
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
     int window;                          // attention window in keys (0: all earlier keys)
     int guard;                           // rows below each first new slot that a running launch may write
@@ -88,6 +90,7 @@ struct Q4DecodeParams {
     uint64_t wait_ns;                    // limit of every bounded wait
     int early;                           // 1: signal the next launch at once, 0: after the wait
     Q4Seq seq[kQ4MaxSeqPerLaunch];       // the launched sequences
+    uint8_t seq_of[kQ4MaxSeqPerLaunch * kQ4MaxSplits];  // mixed: the sequence of `groups` CTAs at a time
 };
 static_assert(sizeof(Q4DecodeParams) <= 4096, "travels in the 4 KB of kernel parameters");
 

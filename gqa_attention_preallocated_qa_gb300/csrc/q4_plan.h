@@ -12,34 +12,85 @@ constexpr int kQ4Chunk = 32;       // keys of one warp's part of a stage of the 
 constexpr int kQ4DecodeWarps = 8;  // warps of a decode CTA
 constexpr int kQ4MaxSplits = 13;   // splits of one (sequence, kv head) = CTAs of one cluster
 
-// Splits of a sequence and kv head (CTAs of a cluster).  A CTA costs a fixed
-// part (its prologue and the merge) and a part per stage of 256 keys; CTAs that
-// share an SM slow each other down.  Fitted on GB300 (D = 128, steps apart from
-// each other, 512 to 16384 keys, 8 to 192 groups): 2.6 us + 1.1 us a stage for a
-// CTA alone on its SM, 3.6 + 1.85 for two; at D = 64 a stage costs 0.66 times
-// that.  CTAs get SMs of their own as long as the launch has at most 96 of them,
-// or 128 in clusters of up to 4.  Only plans whose clusters all fit on the device
-// at once (held[S] clusters of S CTAs) are weighed, the fewest CTAs among
-// equals.  (B = 4, 8 kv heads: 4 splits at 2048 keys take 7.8 us and 8 take 8.4;
-// at 16384 keys 23.2 and 21.4.)
-inline int choose_splits(int D, const int *held, int groups, int keys) {
-    const int chunks = (keys + kQ4Chunk - 1) / kQ4Chunk;
+constexpr int kQ4MaxSeqPerLaunch = 64;  // sequences carried in the parameters of one launch
+
+// How a decode launch is cut: splits[i] CTAs work on each kv head (and head
+// group) of sequence i, and clusters are of `cluster` CTAs, which every
+// splits[i] divides.
+struct DecodePlan {
+    int cluster = 1;
+    int splits[kQ4MaxSeqPerLaunch];
+};
+
+// A CTA costs a fixed part (its prologue and the merge) and a part per stage of
+// 256 keys; CTAs that share an SM slow each other down.  Fitted on GB300 (D =
+// 128, steps apart from each other, 512 to 16384 keys, 8 to 192 groups): 2.6 us
+// + 1.1 us a stage for a CTA alone on its SM, 3.6 + 1.85 for two; at D = 64 a
+// stage costs 0.66 times that.  CTAs get SMs of their own as long as the launch
+// has at most 96 of them, or 128 in clusters of up to 4.
+inline bool decode_alone(int cluster, int64_t ctas) { return ctas <= (cluster <= 4 ? 128 : 96); }
+inline float decode_cta_us(int D, bool alone, int stages) {
     const float stage = D == 128 ? 1.f : 0.66f;
-    if (!held) return 1;
-    int best = 1;
+    return alone ? 2.6f + 1.1f * stage * stages : 3.6f + 1.85f * stage * stages;
+}
+
+// The plan of least cost for n sequences of keys[i] cached keys (in falling
+// order), `groups` kv heads x head groups each.  Either every sequence has the
+// same number of splits, all clusters on the device at once (held[S] clusters of
+// S CTAs; the fewest splits among equals; B = 4, 8 kv heads: 4 splits at 2048
+// keys take 7.8 us and 8 take 8.4; at 16384 keys 23.2 and 21.4); a short
+// sequence's CTAs may then be left without keys.  Or, for mixed lengths, the
+// longest has 2, 4 or 8 and the others as few (1, 2, 4, 8) as give no CTA more
+// stages than the longest's.  A launch takes as long as its longest CTA; one of
+// more CTAs than the device holds at least as long as their sum shared out and
+// then its shortest, which starts last.  (8 kv heads, D = 128: one sequence of
+// 16384 keys beside 3 of 2048 and 4 of 512 takes 14.8 us, with 4 splits each
+// 23.5; 24 of 8000 down to 1 key 19.2, unsplit 40.4; 4 of 8192 beside 60 of 512,
+// with 4 splits and 1, 25.6, unsplit 42.1.)
+inline void plan_decode(int D, const int *held, int groups, int n, const int *keys, DecodePlan &plan) {
+    int chunks[kQ4MaxSeqPerLaunch];
+    for (int i = 0; i < n; ++i) chunks[i] = (keys[i] + kQ4Chunk - 1) / kQ4Chunk;
+    plan.cluster = 1;
+    std::fill(plan.splits, plan.splits + n, 1);
+    if (!held) return;
+    auto stages = [](int chunks, int S) { return (chunks + S * kQ4DecodeWarps - 1) / (S * kQ4DecodeWarps); };
+    auto cost = [&](int S, const int *splits, int64_t ctas) {
+        const float longest = decode_cta_us(D, decode_alone(S, ctas), stages(chunks[0], splits[0]));
+        if ((ctas + S - 1) / S <= held[S]) return longest;
+        float sum = 0.f;
+        for (int i = 0; i < n; ++i) sum += splits[i] * decode_cta_us(D, false, stages(chunks[i], splits[i]));
+        return std::max(longest, sum * groups / (held[S] * S) + decode_cta_us(D, false, stages(chunks[n - 1], splits[n - 1])));
+    };
     float least = 1e30f;
-    for (int S = 1; S <= kQ4MaxSplits && (S == 1 || S <= chunks); ++S) {
-        if (S > 1 && held[S] < groups) continue;
-        const int64_t ctas = static_cast<int64_t>(groups) * S;
-        const int rounds = ((chunks + S - 1) / S + kQ4DecodeWarps - 1) / kQ4DecodeWarps;
-        const bool alone = ctas <= (S <= 4 ? 128 : 96);
-        const float us = alone ? 2.6f + 1.1f * stage * rounds : 3.6f + 1.85f * stage * rounds;
+    int s[kQ4MaxSeqPerLaunch];
+    const int64_t total = static_cast<int64_t>(groups) * n;
+    for (int S = 1; S <= kQ4MaxSplits && (S == 1 || S <= chunks[0]); ++S) {
+        if (S > 1 && held[S] < total) continue;
+        std::fill(s, s + n, S);
+        const float us = cost(S, s, total * S);
         if (us < least - 0.01f) {
             least = us;
-            best = S;
+            plan.cluster = S;
         }
     }
-    return best;
+    std::fill(plan.splits, plan.splits + n, plan.cluster);
+    for (int S = 2; S <= 8 && S <= chunks[0] && held[S] > 0; S *= 2) {
+        const int most = stages(chunks[0], S) * kQ4DecodeWarps;  // chunks of a CTA
+        int64_t ctas = 0;
+        for (int i = 0; i < n; ++i) {
+            s[i] = 1;
+            while (s[i] * most < chunks[i]) s[i] *= 2;
+            ctas += static_cast<int64_t>(groups) * s[i];
+        }
+        if (s[0] < S || s[n - 1] == S) continue;  // a smaller cluster's, or equal splits
+        // 0.3 us for what the fit leaves out
+        const float us = cost(S, s, ctas);
+        if (us < least - 0.3f) {
+            least = us;
+            plan.cluster = S;
+            std::copy(s, s + n, plan.splits);
+        }
+    }
 }
 
 // A run of query blocks of one sequence of a prefill launch: rows first ..

@@ -1,5 +1,5 @@
 // Command-line driver of csrc/q4_plan.h for the CPU tests, one command per line:
-//   splits <D> <groups> <keys> <held 1..13>           -> S
+//   decode <D> <groups> <held 1..13> <n> <keys>*n   -> cluster, then the splits
 //   runs <window> <D> <G> <Hkv> <sms> <n> <start len>*n
 //     -> span before, span after, then "seq first len" of every run
 #include <iostream>
@@ -15,11 +15,17 @@ int main() {
         std::istringstream in(line);
         std::string cmd;
         in >> cmd;
-        if (cmd == "splits") {
-            int D, groups, keys, held[qa::kQ4MaxSplits + 1] = {};
-            in >> D >> groups >> keys;
+        if (cmd == "decode") {
+            int D, groups, n, held[qa::kQ4MaxSplits + 1] = {}, keys[qa::kQ4MaxSeqPerLaunch];
+            in >> D >> groups;
             for (int S = 1; S <= qa::kQ4MaxSplits; ++S) in >> held[S];
-            std::cout << qa::choose_splits(D, held, groups, keys) << "\n";
+            in >> n;
+            for (int i = 0; i < n; ++i) in >> keys[i];
+            qa::DecodePlan plan;
+            qa::plan_decode(D, held, groups, n, keys, plan);
+            std::cout << plan.cluster;
+            for (int i = 0; i < n; ++i) std::cout << " " << plan.splits[i];
+            std::cout << "\n";
         } else if (cmd == "runs") {
             int window, D, G, Hkv, sms, n;
             in >> window >> D >> G >> Hkv >> sms >> n;

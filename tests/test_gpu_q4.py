@@ -227,6 +227,31 @@ def test_decode_long_cache_and_peaked_scores(qa):
         close(out, want, mag, DECODE_BITS)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (4, 2, 64), (8, 1, 64), (3, 3, 128), (6, 3, 128)])
+@pytest.mark.parametrize("tokens", [1, 3])
+@pytest.mark.parametrize("lens", [[300, 90, 9000, 7], [100, 6000, 33, 2500, 0, 1200, 700, 300, 7], [5000] + [17] * 12])
+def test_decode_batches_of_mixed_lengths(qa, hq, hkv, d, tokens, lens):
+    # Lengths that get different numbers of splits: several groups in a cluster,
+    # the last cluster filled up (3 kv heads).
+    ntok = [tokens] * len(lens)
+    with Cache(qa, 1, len(lens), hq, hkv, d, max(lens) + 8) as c:
+        c.fill(0, lens, 5)
+        q, k, v = c.tokens(ntok, 6)
+        outs = [torch.full_like(q, float("nan")) for _ in range(2)]
+        for out in outs:
+            if tokens == 1:
+                qa.qa_q4_decode_step(c.h, 0, lens, q, k, v, c.wq, c.wk, out)
+            else:
+                qa.qa_q4_prefill(c.h, 0, lens, ntok, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        assert torch.equal(*outs)
+        qp, kp = c.transform(lens, ntok, q, k, v)
+        c.note(0, lens, ntok, kp, f64(v))
+        c.check_bytes()
+        want, mag = c.want(lens, ntok, qp)
+        close(outs[0], want, mag, DECODE_BITS)
+
+
 def test_decode_more_sequences_than_a_launch(qa):
     lens = [(i * 37) % 150 for i in range(70)]
     one = [1] * 70

@@ -28,16 +28,48 @@ def driver(tmp_path_factory):
     return run
 
 
-def test_splits_fit_and_have_work(driver):
-    cases = [(d, g, k) for d in (64, 128) for g in (1, 8, 16, 32, 48, 96, 128, 192, 300, 5000)
+def decode(driver, cases):
+    """[(cluster, splits)] of cases (D, groups, keys in falling order)."""
+    got = driver([f"decode {d} {g} {' '.join(map(str, HELD))} {len(keys)} {' '.join(map(str, keys))}" for d, g, keys in cases])
+    return [(line[0], line[1:]) for line in got]
+
+
+def check_plan(groups, keys, cluster, splits):
+    chunks = [(k + 31) // 32 for k in keys]
+    ctas = groups * sum(splits)
+    assert 1 <= cluster <= 13 and all(1 <= s <= cluster and cluster % s == 0 for s in splits)
+    # No CTA without a chunk of its own; equal splits are chosen by the longest
+    # sequence, and shorter ones beside it may leave CTAs without keys.
+    shared = zip(splits, chunks) if len(set(splits)) > 1 else [(splits[0], chunks[0])]
+    assert all(s == 1 or s <= c for s, c in shared)
+    if len(set(splits)) == 1 and cluster > 1:
+        assert ctas <= cluster * HELD[cluster - 1]                          # all clusters at once
+    assert splits == sorted(splits, reverse=True)                           # no group straddles a cluster
+
+
+def test_splits_of_equal_sequences(driver):
+    cases = [(d, g, [k] * n) for d in (64, 128) for g in (1, 2, 8, 16, 5000) for n in (1, 3, 24, 64)
              for k in (0, 1, 31, 32, 33, 256, 512, 2048, 16384, 1 << 24)]
-    got = driver([f"splits {d} {g} {k} " + " ".join(map(str, HELD)) for d, g, k in cases])
-    for (d, g, k), (s,) in zip(cases, got):
-        assert 1 <= s <= 13
-        assert s == 1 or (HELD[s - 1] >= g and s <= (k + 31) // 32), (d, g, k, s)
-    one = dict(zip(cases, (s for s, in got)))
-    assert one[(128, 32, 2048)] == 4 and one[(128, 32, 16384)] == 8  # the two sides of the rule
-    assert one[(128, 5000, 16384)] == 1
+    for (d, g, keys), (cluster, splits) in zip(cases, decode(driver, cases)):
+        check_plan(g, keys, cluster, splits)
+        assert set(splits) == {cluster}
+    # the two sides of the rule, and a launch that is larger than the device
+    short, long, many = decode(driver, [(128, 8, [2048] * 4), (128, 8, [16384] * 4), (128, 5000, [16384])])
+    assert short[0] == 4 and long[0] == 8 and many[0] == 1
+
+
+def test_splits_of_mixed_sequences(driver):
+    rng = random.Random(5)
+    cases = []
+    for _ in range(400):
+        n = rng.randint(1, 64)
+        top = rng.choice([300, 3000, 16384, 100000])
+        cases.append((rng.choice([64, 128]), rng.choice([1, 2, 4, 8, 16]), sorted((int(top ** rng.random()) for _ in range(n)), reverse=True)))
+    mixed = 0
+    for (d, g, keys), (cluster, splits) in zip(cases, decode(driver, cases)):
+        check_plan(g, keys, cluster, splits)
+        mixed += len(set(splits)) > 1
+    assert mixed > 40
 
 
 def test_runs_cover_every_row_once_and_never_cost_more(driver):
