@@ -589,7 +589,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     for (int b = 0; b < batch; ++b)
         if (ntok[b] > 0) next[b] = start[b] + ntok[b];
     const bool fused = qa::q4_prefill_rows_fits(c->cfg.n_q_heads, c->cfg.n_kv_heads, c->cfg.head_dim);
-    for (PrefillGroup &pg : groups) {
+    auto launch = [&](PrefillGroup &pg) {
         // The older rows first: K2 then follows the kernel that lets it start early.
         if (pg.held.nblocks > 0) {
             if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
@@ -619,8 +619,12 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         }
         qa::launch_order().barrier(s);
         c->launches[QA_Q4_KERNEL_PREFILL_ATTN]++;
-    }
-    return cudaEventRecord(c->ws_free, s) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
+        return QA_OK;
+    };
+    for (size_t i = 0; i < groups.size() && st == QA_OK; ++i) st = launch(groups[i]);
+    // After a failure too: what was enqueued uses the workspace.
+    if (cudaEventRecord(c->ws_free, s) != cudaSuccess) return QA_ERR_CUDA;
+    return st;
 }
 
 namespace {
