@@ -181,11 +181,17 @@ struct DecodeCall {
     const int32_t *ntok;      // null: one token each
 };
 
-// The new tokens of a call (at most 8 per sequence), one decode launch per 64
-// sequences that have any.
-qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, int tmax, cudaStream_t s) {
+// Tokens first .. first + 7 of the call's sequences (only of those whose tokens
+// come this way), one decode launch per 64 sequences that have any.
+qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, int first, cudaStream_t s) {
     const qa_config &g = c->cfg;
     const int D = g.head_dim;
+    auto tokens = [&](int b) {
+        if (!a.ntok) return 1;
+        return qa::few_tokens(a.start[b], a.ntok[b], c->window[layer]) ? std::min(a.ntok[b] - first, qa::kQ4MaxTokens) : 0;
+    };
+    int tmax = 1;
+    for (int b = 0; b < batch && a.ntok; ++b) tmax = std::max(tmax, tokens(b));
     const bool multi = tmax > 1;
     int HPC = c->G;
     while (multi && HPC > 1 && qa::kQ4MaxTokens / HPC < tmax) HPC /= 2;
@@ -228,20 +234,20 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     const bool settled = qa::launch_order().layer_settled(s, c, layer, resident);
     bool follows = !a.pos_dev;
     for (int b = 0; b < batch && follows; ++b)
-        if ((!a.ntok || a.ntok[b] > 0) && next[b] != a.start[b]) follows = false;
+        if (tokens(b) > 0 && next[b] != a.start[b] + first) follows = false;
 
     int b = 0, row0 = 0;
     while (b < batch) {
         int nz = 0, tm = 0;
-        const int first = b;
+        const int b0 = b;
         for (; b < batch && nz < qa::kQ4MaxSeqPerLaunch; ++b) {
-            const int n = a.ntok ? a.ntok[b] : 1;
+            const int n = tokens(b);
             if (n > 0) {
-                p.seq[nz] = {a.pos_dev ? 0 : a.start[b], b, n, row0, 0, 1, 0, 0};
+                p.seq[nz] = {a.pos_dev ? 0 : a.start[b] + first, b, n, row0 + first, 0, 1, 0, 0};
                 tm = std::max(tm, n);
                 ++nz;
             }
-            row0 += n;
+            row0 += a.ntok ? a.ntok[b] : 1;
         }
         if (nz == 0) break;
         // The longest sequences first: thread blocks start in this order, and the
@@ -281,10 +287,8 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
             return QA_ERR_CUDA;
         }
         c->launches[QA_Q4_KERNEL_DECODE]++;
-        for (int i = first; i < b; ++i) {
-            const int n = a.ntok ? a.ntok[i] : 1;
-            if (n > 0) next[i] = a.pos_dev ? -1 : a.start[i] + n;
-        }
+        for (int i = b0; i < b; ++i)
+            if (tokens(i) > 0) next[i] = a.pos_dev ? -1 : a.start[i] + first + tokens(i);
     }
     return QA_OK;
 }
@@ -556,38 +560,57 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     DeviceScope dev(c->device);
     if (!dev.ok()) return QA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int tmax = *std::max_element(ntok, ntok + batch);
-    if (tmax <= qa::kQ4MaxTokens) {
-        DecodeCall a{q, k, v, q_norm_w, k_norm_w, out, nullptr, nullptr, start, nullptr, ntok};
-        return no_throw([&] { return run_decode(c, layer, batch, a, tmax, s); });
-    }
-    // The longer form goes through the cache's one bf16 workspace: a graph could
-    // be replayed beside another call that uses it, so it is not captured, and
-    // calls on several streams take turns.
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
-        cudaGetLastError();
-        return QA_ERR_STATE;
+    auto few_tokens = [&](int b) { return qa::few_tokens(start[b], ntok[b], c->window[layer]); };
+    int few = 0;  // the most tokens of a sequence that takes the decode kernel
+    bool long_form = false;
+    for (int b = 0; b < batch; ++b) {
+        if (few_tokens(b))
+            few = std::max(few, ntok[b]);
+        else
+            long_form = true;
     }
     std::vector<PrefillGroup> groups;
-    st = no_throw([&] {
-        int64_t row0 = 0;
-        for (int s0 = 0; s0 < batch; s0 += c->ws_slots) {
-            const int n = std::min(c->ws_slots, batch - s0);
-            groups.emplace_back();
-            PrefillGroup &pg = groups.back();
-            if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
-                return QA_ERR_CUDA;
-            row0 += pg.rows.k1.T;
-            if (pg.rows.k1.T == 0) groups.pop_back();
+    if (long_form) {
+        // It goes through the cache's one bf16 workspace: a graph could be replayed
+        // beside another call that uses it, so it is not captured, and calls on
+        // several streams take turns.
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
+            cudaGetLastError();
+            return QA_ERR_STATE;
         }
-        return QA_OK;
-    });
-    if (st != QA_OK) return st;
+        // A group's rows are packed one after the other, so sequences that take
+        // the decode kernel stand between groups.
+        st = no_throw([&] {
+            int64_t row0 = 0;
+            for (int s0 = 0; s0 < batch;) {
+                int n = 0;
+                while (s0 + n < batch && n < c->ws_slots &&
+                       (!few_tokens(s0 + n) || (n > 0 && ntok[s0 + n] == 0)))
+                    ++n;
+                if (n == 0) {
+                    row0 += ntok[s0++];
+                    continue;
+                }
+                groups.emplace_back();
+                PrefillGroup &pg = groups.back();
+                if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
+                    return QA_ERR_CUDA;
+                row0 += pg.rows.k1.T;
+                s0 += n;
+            }
+            return QA_OK;
+        });
+        if (st != QA_OK) return st;
+    }
+    const DecodeCall a{q, k, v, q_norm_w, k_norm_w, out, nullptr, nullptr, start, nullptr, ntok};
+    for (int first = 0; first < few && st == QA_OK; first += qa::kQ4MaxTokens)
+        st = no_throw([&] { return run_decode(c, layer, batch, a, first, s); });
+    if (st != QA_OK || !long_form) return st;
     if (cudaStreamWaitEvent(s, c->ws_free, 0) != cudaSuccess) return QA_ERR_CUDA;
     int32_t *next = next_of(c, layer);
     for (int b = 0; b < batch; ++b)
-        if (ntok[b] > 0) next[b] = start[b] + ntok[b];
+        if (!few_tokens(b)) next[b] = start[b] + ntok[b];
     const bool fused = qa::q4_prefill_rows_fits(c->cfg.n_q_heads, c->cfg.n_kv_heads, c->cfg.head_dim);
     auto launch = [&](PrefillGroup &pg) {
         // The older rows first: K2 then follows the kernel that lets it start early.
@@ -636,7 +659,7 @@ qa_status decode_step(qa_q4_cache *c, int layer, int batch, const DecodeCall &a,
         return QA_ERR_ALIGNMENT;
     DeviceScope dev(c->device);
     if (!dev.ok()) return QA_ERR_CUDA;
-    return no_throw([&] { return run_decode(c, layer, batch, a, 1, static_cast<cudaStream_t>(stream)); });
+    return no_throw([&] { return run_decode(c, layer, batch, a, 0, static_cast<cudaStream_t>(stream)); });
 }
 }  // namespace
 

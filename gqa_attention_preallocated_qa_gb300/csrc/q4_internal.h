@@ -57,7 +57,6 @@ struct Q4PrefillRowsParams {
 };
 static_assert(sizeof(Q4PrefillRowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
-constexpr int kQ4MaxTokens = 8;    // new tokens per sequence of one decode launch
 
 // A launched sequence: the slot of its first new token, its place in the cache,
 // its new tokens and the first of their rows in q, k, v and out.

@@ -93,6 +93,19 @@ inline void plan_decode(int D, const int *held, int groups, int n, const int *ke
     }
 }
 
+// Whether a sequence's new tokens go through the decode kernel, eight at a time,
+// or through the prefill kernel on the dequantised cache.  The latter walks the
+// keys of a head in one CTA pair: 11.5 ns a key beside 12 us, for up to 128
+// tokens.  (8 kv heads, 32 query heads, D = 128, eight tokens / prefill kernel:
+// nothing cached 4.0 / 12.5 us for one sequence, 5.6 / 14.5 for four, 14 / 33 for
+// 16; 512 keys 4.6 / 22, 7.4 / 25, 21 / 67; 2048 keys 7.0 / 39, 12.5 / 45,
+// 37 / 150; 16384 keys 17.8 / 197, 53 / 235, 198 / 910.  D = 64 the same way.)
+constexpr int kQ4MaxTokens = 8;  // new tokens per sequence of one decode launch
+inline bool few_tokens(int start, int ntok, int window) {
+    const int keys = window > 0 ? std::min(start, window) : start;
+    return ntok <= kQ4MaxTokens * (keys < 512 ? 2 : keys < 4096 ? 3 : 4);
+}
+
 // A run of query blocks of one sequence of a prefill launch: rows first ..
 // first + len - 1 of its new tokens.
 struct QueryRun {

@@ -392,7 +392,7 @@ enum {
     QA_Q4_KERNEL_QUANTISE = 1,     /* K4: rows into the cache (a prefill's: with norm and rotation) */
     QA_Q4_KERNEL_DEQUANTISE = 2,   /* K4: rows out of the cache */
     QA_Q4_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace */
-    QA_Q4_KERNEL_DECODE = 4,       /* K5: decode steps and chunks of up to 8 tokens */
+    QA_Q4_KERNEL_DECODE = 4,       /* K5: decode steps and short chunks, 8 tokens a launch */
     QA_Q4_NUM_KERNELS = 5
 };
 
@@ -434,13 +434,15 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * Result: RoPE(RMSNorm(k)) and v are quantised into their positions, and every
  * new token attends causally to what the cache then holds (its own rows as
  * held, too), within the layer's window.
- * With every ntok at most 8 the decode kernel does all of it, one launch per
- * 64 sequences.  Otherwise K4 and K2 run through the cache's workspace, 8
- * sequences at a time: such calls on several streams wait for each other, and
- * they cannot be captured into a graph (QA_ERR_STATE).  In that form a key or
- * value that is not finite can reach other new tokens of its sequence in the
- * call, also those before it (as in qa_prefill: the tensor cores multiply it by
- * their weight of zero).
+ * Sequences with few new tokens (up to 16; up to 24 behind 512 cached
+ * positions and up to 32 behind 4096, at most a window of which count) take the
+ * decode kernel, 8 tokens a launch, one launch per 64 sequences.  The others
+ * take K4 and K2 through the cache's workspace, up to 8 sequences at a time:
+ * calls with such sequences on several streams wait for each other, and they
+ * cannot be captured into a graph (QA_ERR_STATE).  In that form a key or value
+ * that is not finite can reach other new tokens of its sequence in the call,
+ * also those before it (as in qa_prefill: the tensor cores multiply it by their
+ * weight of zero).
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
 qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
                         const int32_t *ntok, const void *q, const void *k, const void *v,

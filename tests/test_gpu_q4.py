@@ -333,6 +333,55 @@ def test_short_chunk(qa, hq, hkv, d, window):
         assert qa.qa_q4_stats(c.h)["decode"] == 1 and qa.qa_q4_stats(c.h)["prefill_attn"] == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("window", [0, 600])
+def test_chunks_of_several_launches_beside_long_ones(qa, hq, hkv, d, window):
+    # Each sequence by its own length: up to 16, 24 or 32 tokens in the decode
+    # kernel, eight at a time; the longer ones, in groups with those between them
+    # left out, in the prefill kernel.
+    start, ntok = [100, 0, 6000, 0, 0, 700, 33, 511, 5, 4100], [1, 300, 24, 16, 0, 24, 17, 16, 40, 9]
+    long = [17 <= n and (n > 24 or s < 512) for s, n in zip(start, ntok)]
+    with Cache(qa, 1, len(start), hq, hkv, d, 6040) as c:
+        qa.qa_q4_cache_set_window(c.h, 0, window)
+        c.fill(0, start, 5)
+        q, k, v = c.tokens(ntok, 6)
+        out = torch.full_like(q, float("nan"))
+        qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        assert qa.qa_q4_stats(c.h)["decode"] == 3 and qa.qa_q4_stats(c.h)["prefill_attn"] == 3
+        qp, kp = c.transform(start, ntok, q, k, v)
+        c.note(0, start, ntok, kp, f64(v))
+        c.check_bytes()
+        want, mag = c.want(start, ntok, qp, window=window)
+        rows = torch.tensor(long).repeat_interleave(torch.tensor(ntok)).cuda()
+        close(out[rows], want[rows], mag[rows], PREFILL_BITS)
+        close(out[~rows], want[~rows], mag[~rows], DECODE_BITS)
+
+
+def test_chunk_of_sixteen_in_a_graph(qa):
+    # The same chunk replayed: written twice, the same bits as the eager call.
+    start, ntok = [40, 300], [16, 13]
+    with Cache(qa, 1, 2, 8, 2, 128, 330) as c:
+        c.fill(0, start, 5)
+        q, k, v = c.tokens(ntok, 6)
+        eager, out = torch.empty_like(q), torch.empty_like(q)
+        qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, eager)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+        qp, kp = c.transform(start, ntok, q, k, v)
+        c.note(0, start, ntok, kp, f64(v))
+        want, mag = c.want(start, ntok, qp)
+        for _ in range(2):
+            out.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager)
+        close(out, want, mag, DECODE_BITS)
+        c.check_bytes()
+
+
 # ------------------------------------------------------------------ prefill
 @pytest.mark.parametrize("hq,hkv,d,start,ntok,window", [
     (8, 2, 128, [0], [9], 0),
@@ -483,7 +532,7 @@ def test_prefill_on_two_streams_shares_the_workspace(qa):
 def test_refusals_change_nothing(qa):
     with Cache(qa, 1, 2, 8, 2, 128, 64) as c:
         c.fill(0, [20, 20], 5)
-        q, k, v = c.tokens([9, 9], 6)
+        q, k, v = c.tokens([17, 9], 6)
         out = torch.full_like(q, 3.0)
         w = (c.wq, c.wk)
 
@@ -508,7 +557,7 @@ def test_refusals_change_nothing(qa):
         refused(4, qa.qa_q4_read, 0, [64], [1], k, v)
         refused(1, qa.qa_q4_read, 0, [0], [1], None, None)
         refused(3, qa.qa_q4_read, 0, [0], [1], k, odd)
-        for n in (3, 9):
+        for n in (3, 9, 17):
             refused(4, qa.qa_q4_prefill, 0, [60], [n + 2], q, k, v, *w, out)
             refused(1, qa.qa_q4_prefill, 0, [0], [n], q, k, v, None, c.wk, out)
             refused(3, qa.qa_q4_prefill, 0, [0], [n], q, k, v, *w, odd)
@@ -523,7 +572,7 @@ def test_refusals_change_nothing(qa):
         with torch.cuda.stream(side):
             graph.capture_begin()
             try:
-                refused(5, qa.qa_q4_prefill, 0, [20], [9], q, k, v, *w, out, side)
+                refused(5, qa.qa_q4_prefill, 0, [20], [17], q, k, v, *w, out, side)
             finally:
                 graph.capture_end()
         torch.cuda.synchronize()
