@@ -26,12 +26,17 @@
 // two key tiles of a block removes them from the softmax, and an attention
 // window adds a lower band (keys before position + 1 - W) and starts the
 // block at its window's first tile.
+// Few query blocks behind many keys leave most SMs idle: there (the 4-bit
+// cache's prefill) the one-CTA form also runs with the keys of a block cut into
+// parts, each an item whose sums go out in fp32, and a small kernel joins them.
 // Every mbarrier wait is bounded (qa_device.cuh): a stuck pipeline records a
 // timeout in the error word and the CTA still frees its TMEM and exits.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "k2_items.h"
+#include "k2_parts.h"
 #include "qa_device.cuh"
 
 namespace qa {
@@ -103,9 +108,22 @@ __device__ __forceinline__ bool k2p_item(const K2Params &p, int k, K2Walk &w, K2
     return k2_item_at<kWindow>(p, k2_snake_index(k, gridDim.x >> shift, blockIdx.x >> shift), w, it);
 }
 
-template <int D, bool kWindow>
+// A part of it: the block's key tiles within the part.
+template <bool kWindow>
+__device__ __forceinline__ bool k2p_item(const K2PartParams &p, int k, K2Walk &w, K2Item &it) {
+    if (!k2_item_at<kWindow>(p, k2_snake_index(k, gridDim.x, blockIdx.x), w, it)) return false;
+    const int end = min(it.j0 + it.nkv, p.part_hi[it.b]);
+    it.j0 = max(it.j0, p.part_lo[it.b]);
+    it.nkv = end - it.j0;
+    return true;
+}
+
+// P: K2Params, or K2PartParams for the form whose items are parts of a block's
+// keys and whose outputs are the parts' sums in fp32.
+template <int D, bool kWindow, class P>
 __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
-    k2p_prefill_kernel(const __grid_constant__ K2Params p) {
+    k2p_prefill_kernel(const __grid_constant__ P p) {
+    constexpr bool kParts = std::is_same<P, K2PartParams>::value;
     using Lay = K2PLayout<D>;
     constexpr int NS = Lay::kStages;
     const unsigned FULL = 0xffffffffu;
@@ -147,6 +165,7 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     griddep_wait();  // as in the CTA-pair form: global data only after this
+    if (kParts) griddep_launch_dependents();  // the join sets up beside this
 
     if (warp == Lay::kTmaWarp) {
         // ------------------------------------------------------------ TMA producer
@@ -451,9 +470,27 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                 if (!ok) break;
                 ++nitem;
                 tc_fence_after();
-                const float inv = 1.f / l;
                 const int row = it.qb * 128 + r;  // new token index within the sequence
                 const bool valid = row < it.L;
+                if constexpr (kParts) {
+                    // The part's sums as they are: rows that saw none of its keys
+                    // (l = 0) have no weight in the join.
+                    const int64_t at = static_cast<int64_t>(p.part_row[it.b] + row) * p.Hq + it.h0 + t;
+                    if (valid) p.part_ml[at] = make_float2(l == 0.f ? -INFINITY : mref * c, l);
+#pragma unroll
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        uint32_t u[32];
+                        tmem_ld32(tO + ch * 32, u);
+                        if (valid) {
+                            uint4 *d4 = reinterpret_cast<uint4 *>(p.part_o + at * D + ch * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                d4[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                        }
+                    }
+                    continue;
+                }
+                const float inv = 1.f / l;
                 __nv_bfloat16 *dst =
                     p.out + (static_cast<int64_t>(p.cu[it.b] + row) * p.Hq + it.h0 + t) * D;
 #pragma unroll
@@ -1039,7 +1076,7 @@ static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t strea
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 32 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
-        cudaError_t e = cudaFuncSetAttribute(k2p_prefill_kernel<D, kWindow>,
+        cudaError_t e = cudaFuncSetAttribute(k2p_prefill_kernel<D, kWindow, K2Params>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
@@ -1067,7 +1104,7 @@ static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k2p_prefill_kernel<D, kWindow>, q);
+    return cudaLaunchKernelEx(&cfg, k2p_prefill_kernel<D, kWindow, K2Params>, q);
 }
 
 cudaError_t launch_k2(const K2Params &p, int D, int nitems, cudaStream_t stream) {
@@ -1078,6 +1115,118 @@ cudaError_t launch_k2(const K2Params &p, int D, int nitems, cudaStream_t stream)
     if (D == 64)
         return win ? launch_k2_t<64, true>(p, nitems, stream) : launch_k2_t<64, false>(p, nitems, stream);
     return cudaErrorInvalidValue;
+}
+
+// ==================================================================== parts
+template <int D, bool kWindow>
+static cudaError_t launch_parts_t(const K2PartParams &p, int nitems, cudaStream_t stream) {
+    using Lay = K2PLayout<D>;
+    auto kern = k2p_prefill_kernel<D, kWindow, K2PartParams>;
+    static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 32 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
+    }
+    const int sms = k2_num_sms();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    K2PartParams q = p;
+    q.nitems = nitems;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(nitems, sms), 1, 1);
+    cfg.blockDim = dim3(Lay::kThreads);
+    cfg.dynamicSmemBytes = Lay::kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, q);
+}
+
+// nitems: query blocks of all parts x kv heads x p.npairs; p.hpi query heads each.
+cudaError_t launch_k2_parts(const K2PartParams &p, int D, int nitems, cudaStream_t stream) {
+    if (nitems <= 0) return cudaSuccess;
+    const bool win = p.window > 0;
+    if (D == 128)
+        return win ? launch_parts_t<128, true>(p, nitems, stream) : launch_parts_t<128, false>(p, nitems, stream);
+    if (D == 64)
+        return win ? launch_parts_t<64, true>(p, nitems, stream) : launch_parts_t<64, false>(p, nitems, stream);
+    return cudaErrorInvalidValue;
+}
+
+// One warp per (row, query head): its parts' sums, each read once.  Bound by
+// those reads out of L2 (128 rows, 32 heads, 8 parts, D = 128: 17 MB).
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) k2_join_kernel(const __grid_constant__ K2JoinParams p) {
+    constexpr int E = D / 32;  // dims of a lane
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const int64_t idx = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const int row = static_cast<int>(idx / p.Hq), h = static_cast<int>(idx - static_cast<int64_t>(row) * p.Hq);
+    if (row >= p.rows) return;
+    int run = 0;
+    while (run + 1 < p.nruns && row >= p.row0[run + 1]) ++run;
+    const int r = row - p.row0[run], n = p.parts[run];
+    const int64_t first = static_cast<int64_t>(p.part_row[run] + r) * p.Hq + h;
+    const int64_t step = static_cast<int64_t>(p.len[run]) * p.Hq;
+    griddep_wait();  // the parts are written
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = p.part_ml[first + lane * step];
+    float M = ml.x;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    const float w = ml.x == -INFINITY ? -1.f : k2_ex2(ml.x - M);  // -1: no key of the part counts
+    float L = fmaxf(w, 0.f) * ml.y;
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) L += __shfl_xor_sync(FULL, L, o);
+    L = __shfl_sync(FULL, L, 0);
+    float acc[E] = {};
+#pragma unroll
+    for (int i = 0; i < kMaxSeqPerLaunch; ++i) {
+        const float wi = __shfl_sync(FULL, w, i);
+        if (i >= n || wi < 0.f) continue;
+        const float *o = p.part_o + (first + i * step) * D + E * lane;
+        if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(o);
+            acc[0] = fmaf(wi, x.x, acc[0]);
+            acc[1] = fmaf(wi, x.y, acc[1]);
+            acc[2] = fmaf(wi, x.z, acc[2]);
+            acc[3] = fmaf(wi, x.w, acc[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(o);
+            acc[0] = fmaf(wi, x.x, acc[0]);
+            acc[1] = fmaf(wi, x.y, acc[1]);
+        }
+    }
+    const float inv = 1.f / L;
+    uint32_t v[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) v[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    __nv_bfloat16 *dst = p.out + (static_cast<int64_t>(p.cu[run] + r) * p.Hq + h) * D + E * lane;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(v[0], v[1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = v[0];
+}
+
+cudaError_t launch_k2_join(const K2JoinParams &p, int D, cudaStream_t stream) {
+    const int64_t warps = static_cast<int64_t>(p.rows) * p.Hq;
+    if (warps <= 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return D == 128 ? cudaLaunchKernelEx(&cfg, k2_join_kernel<128>, p) : cudaLaunchKernelEx(&cfg, k2_join_kernel<64>, p);
 }
 
 }  // namespace qa

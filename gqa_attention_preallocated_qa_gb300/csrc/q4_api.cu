@@ -8,6 +8,7 @@
 #include <new>
 #include <vector>
 
+#include "k2_parts.h"
 #include "q4_internal.h"
 #include "q4_plan.h"
 #include "qa.h"
@@ -26,6 +27,8 @@ struct qa_q4_cache {
     // launch, dequantised, laid out [slot][kv head][capacity][head_dim].
     int ws_slots = 0;
     __nv_bfloat16 *ws[2] = {};
+    float *part_o = nullptr;        // sums of the parts of a block's keys (k2_parts.h)
+    float2 *part_ml = nullptr;
     cudaEvent_t ws_free = nullptr;  // the last prefill that used the workspace
     int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
     float2 *rope = nullptr;
@@ -88,6 +91,8 @@ void free_all(qa_q4_cache *c) {
         cudaFree(c->scales[i]);
         cudaFree(c->ws[i]);
     }
+    cudaFree(c->part_o);
+    cudaFree(c->part_ml);
     cudaFree(c->ws_lens);
     cudaFree(c->rope);
     cudaFree(c->err);
@@ -297,7 +302,9 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
 struct PrefillGroup {
     qa::Q4PrefillRowsParams rows;
     qa::Q4RowsParams quant, held;
-    qa::K2Params k2;
+    qa::K2PartParams k2;
+    qa::K2JoinParams join;
+    bool parts;                     // k2 is of parts, join follows it
     int items;
 };
 
@@ -361,8 +368,8 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         for (int i = 0; i < n; ++i)
             r->src_off[i] = r->dst_off[i] = i * ws_seq + static_cast<int64_t>(r->start[i]) * D;
     }
-    qa::K2Params &k2 = pg.k2;
-    k2 = qa::K2Params{};
+    qa::K2PartParams &k2 = pg.k2;
+    k2 = qa::K2PartParams{};
     std::vector<qa::QueryRun> runs;
     k1.cu[0] = 0;
     for (int i = 0; i < n; ++i) {
@@ -370,11 +377,21 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         k1.start[i] = start[s0 + i];
         if (ntok[s0 + i] > 0) runs.push_back({i, 0, ntok[s0 + i]});
     }
-    qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
-    int nseq = 0, maxqb = 0;
+    k2.hpi = std::min(c->G, 2);
+    std::vector<qa::KeyPart> parts;
+    pg.parts = c->part_o && qa::plan_parts(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms,
+                                           qa::kMaxSeqPerLaunch, parts, k2.hpi);
+    k2.npairs = c->G / k2.hpi;
+    if (!pg.parts) {
+        qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
+        for (size_t i = 0; i < runs.size(); ++i) parts.push_back({static_cast<int>(i), 0, 1 << 30});
+    }
+    pg.join = qa::K2JoinParams{};
+    int nseq = 0, maxqb = 0, part_row = 0;
     const int rows = k1.cu[n];
     pg.items = 0;
-    for (const qa::QueryRun &r : runs) {
+    for (const qa::KeyPart &part : parts) {
+        const qa::QueryRun &r = runs[part.run];
         const int P = start[s0 + r.seq] + r.first;
         if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 64) ||
             !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 128))
@@ -382,6 +399,17 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         k2.len[nseq] = r.len;
         k2.start[nseq] = P;
         k2.cu[nseq] = k1.cu[r.seq] + r.first;
+        k2.part_lo[nseq] = part.lo;
+        k2.part_hi[nseq] = part.hi;
+        k2.part_row[nseq] = part_row;
+        if (pg.join.parts[part.run]++ == 0) {
+            pg.join.row0[part.run] = pg.join.rows;
+            pg.join.len[part.run] = r.len;
+            pg.join.cu[part.run] = k2.cu[nseq];
+            pg.join.part_row[part.run] = part_row;
+            pg.join.rows += r.len;
+        }
+        part_row += r.len;
         maxqb = std::max(maxqb, (r.len + 127) / 128);
         pg.items += (r.len + 127) / 128;
         ++nseq;
@@ -395,11 +423,17 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     k2.Hq = Hq;
     k2.Hkv = Hkv;
     k2.G = c->G;
-    k2.npairs = (c->G + 1) / 2;
     k2.max_qblocks = maxqb;
     k2.window = c->window[layer];
     k2.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
     pg.items *= Hkv * k2.npairs;
+    k2.part_o = c->part_o;
+    k2.part_ml = c->part_ml;
+    pg.join.part_o = c->part_o;
+    pg.join.part_ml = c->part_ml;
+    pg.join.out = k1.qp;
+    pg.join.Hq = Hq;
+    pg.join.nruns = static_cast<int>(runs.size());
     return true;
 }
 
@@ -431,6 +465,11 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
              dev_alloc(&c->scales[i], rows * (g.head_dim / qa::kQ4Group), c->cache_bytes) &&
              dev_alloc(&c->ws[i], ws, c->scratch_bytes);
     ok = ok && dev_alloc(&c->ws_lens, qa::kMaxSeqPerLaunch, c->scratch_bytes) &&
+         // The parts of a launch have at most two heads' blocks of 128 rows per SM;
+         // caches this short are not cut.
+         (g.capacity < 1024 ||
+          (dev_alloc(&c->part_o, static_cast<size_t>(c->num_sms) * 256 * g.head_dim, c->scratch_bytes) &&
+           dev_alloc(&c->part_ml, static_cast<size_t>(c->num_sms) * 256, c->scratch_bytes))) &&
          dev_alloc(&c->rope, static_cast<size_t>(g.capacity) * (g.head_dim / 2), c->scratch_bytes) &&
          dev_alloc(&c->err, 1, c->scratch_bytes) &&
          cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) == cudaSuccess;
@@ -634,7 +673,9 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_PREFILL_ATTN);
         pg.k2.fault = f.fault;
         pg.k2.wait_ns = f.wait_ns;
-        if (qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s) != cudaSuccess) {
+        const cudaError_t e = pg.parts ? qa::launch_k2_parts(pg.k2, c->cfg.head_dim, pg.items, s)
+                                       : qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s);
+        if (e != cudaSuccess || (pg.parts && qa::launch_k2_join(pg.join, c->cfg.head_dim, s) != cudaSuccess)) {
             // A kernel that signalled early is no longer followed by one that
             // waits for it: let it finish before anything else is enqueued.
             cudaStreamSynchronize(s);

@@ -94,12 +94,11 @@ inline void plan_decode(int D, const int *held, int groups, int n, const int *ke
 }
 
 // Whether a sequence's new tokens go through the decode kernel, eight at a time,
-// or through the prefill kernel on the dequantised cache.  The latter walks the
-// keys of a head in one CTA pair: 11.5 ns a key beside 12 us, for up to 128
-// tokens.  (8 kv heads, 32 query heads, D = 128, eight tokens / prefill kernel:
-// nothing cached 4.0 / 12.5 us for one sequence, 5.6 / 14.5 for four, 14 / 33 for
-// 16; 512 keys 4.6 / 22, 7.4 / 25, 21 / 67; 2048 keys 7.0 / 39, 12.5 / 45,
-// 37 / 150; 16384 keys 17.8 / 197, 53 / 235, 198 / 910.  D = 64 the same way.)
+// or through the prefill kernel on the dequantised cache, where up to 128 tokens
+// cost the same.  (8 kv heads, 32 query heads, D = 128, eight tokens / prefill
+// kernel: nothing cached 4.0 / 12.5 us for one sequence, 5.6 / 14.5 for four,
+// 14 / 33 for 16; 512 keys 4.6 / 22, 7.4 / 25, 21 / 67; 2048 keys 7.0 / 28,
+// 12.5 / 45, 37 / 150; 16384 keys 17.8 / 62, 53 / 178, 198 / 910.)
 constexpr int kQ4MaxTokens = 8;  // new tokens per sequence of one decode launch
 inline bool few_tokens(int start, int ntok, int window) {
     const int keys = window > 0 ? std::min(start, window) : start;
@@ -193,6 +192,70 @@ inline void plan_runs(std::vector<QueryRun> &runs, const int *start, int window,
             }
         }
     runs = best;
+}
+
+// A part of a run's keys: tiles lo .. hi - 1 of 128.
+struct KeyPart {
+    int run, lo, hi;
+};
+
+// Cuts the keys of few query blocks behind many keys into parts, so that the
+// device's SMs share them, and says how many query heads an item takes; false
+// when it does not pay.  Fitted on GB300 (D = 128; 1 to 4 sequences of 40 to 512
+// tokens behind 1000 to 65536 keys): a key tile takes 1.75 us with two heads and
+// 1.3 with one (the launch without parts: one head an item here), the join 5 us
+// and 0.2 ns for each part of a row and head.  (32 / 8 heads, 128 tokens behind
+// 16384 keys: 196 us without, 8 parts of two heads 68, 4 of one head 80; behind
+// 2048 keys 39 and 33; behind 1000 keys 27.6, and 31.5 with 2 parts.  8 / 1 heads
+// behind 16384 keys: 183, 8 parts of two heads 52, of one head 44.)
+inline bool plan_parts(const std::vector<QueryRun> &runs, const int *start, int window, int D, int G, int Hkv, int sms,
+                       int max_parts, std::vector<KeyPart> &parts, int &hpi) {
+    const int nruns = static_cast<int>(runs.size());
+    if (nruns == 0 || 2 * nruns > max_parts) return false;
+    const float tile_us[3] = {0.f, D == 128 ? 1.3f : 1.2f, D == 128 ? 1.75f : 1.45f};
+    int blocks[kQ4MaxSeqPerLaunch], from[kQ4MaxSeqPerLaunch], tiles[kQ4MaxSeqPerLaunch];
+    int total = 0, most = 0, rows = 0;
+    for (int i = 0; i < nruns; ++i) {
+        const int pos = start[runs[i].seq] + runs[i].first;
+        blocks[i] = (runs[i].len + 127) / 128;
+        from[i] = window > 0 ? std::max(0, pos + 1 - window) / 128 : 0;
+        tiles[i] = pos / 128 + 1 - from[i];  // of the first block, up to the one its first row is in
+        total += blocks[i];
+        rows += runs[i].len;
+        most = std::max(most, tiles[i] + blocks[i] - 1);
+    }
+    // Parts of run i when the most are n.  A later block's window starts up to
+    // blocks - 1 tiles later: every part of it keeps a tile at least.
+    auto cut = [&](int i, int n) {
+        int m = std::min(n, tiles[i]);
+        while (m > 1 && window > 0 && tiles[i] / m <= blocks[i]) --m;
+        return m;
+    };
+    float least = tile_us[1] * most - 1.f;
+    int best = 1;
+    for (int h = std::min(G, 2); h >= 1; --h) {
+        const int items = total * Hkv * (G / h);
+        for (int n = 2; n * nruns <= max_parts && n * items <= sms; ++n) {
+            int longest = 0;
+            for (int i = 0; i < nruns; ++i) {
+                const int m = cut(i, n);
+                longest = std::max(longest, (tiles[i] + m - 1) / m + blocks[i] - 1);
+            }
+            const float us = tile_us[h] * longest + 5.f + 0.2e-3f * (D / 128.f) * rows * (Hkv * G) * n;
+            if (us < least) {
+                least = us;
+                best = n;
+                hpi = h;
+            }
+        }
+    }
+    if (best == 1) return false;
+    parts.clear();
+    for (int i = 0; i < nruns; ++i)
+        for (int k = 0, m = cut(i, best); k < m; ++k)
+            parts.push_back({i, from[i] + static_cast<int>(int64_t(tiles[i]) * k / m),
+                             k == m - 1 ? 1 << 30 : from[i] + static_cast<int>(int64_t(tiles[i]) * (k + 1) / m)});
+    return true;
 }
 
 }  // namespace qa

@@ -391,7 +391,7 @@ enum {
     QA_Q4_KERNEL_NORM_ROPE = 0,    /* K1, for geometries whose token does not fit K4's transform */
     QA_Q4_KERNEL_QUANTISE = 1,     /* K4: rows into the cache (a prefill's: with norm and rotation) */
     QA_Q4_KERNEL_DEQUANTISE = 2,   /* K4: rows out of the cache */
-    QA_Q4_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace */
+    QA_Q4_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace (and the join of its parts) */
     QA_Q4_KERNEL_DECODE = 4,       /* K5: decode steps and short chunks, 8 tokens a launch */
     QA_Q4_NUM_KERNELS = 5
 };
@@ -401,7 +401,8 @@ enum {
  * and scale bytes [...][rows][D/32] for K and for V (zero-filled; rows is the
  * capacity, rounded up to a multiple of 64), the rotary table, an error word,
  * and one bf16 workspace for prefill attention: K and V of min(max_batch, 8)
- * sequences of one layer, [slot][n_kv_heads][capacity][D].  Synchronous.
+ * sequences of one layer, [slot][n_kv_heads][capacity][D], and from capacity
+ * 1024 on the fp32 sums of keys in parts (20 MB at D = 128).  Synchronous.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
 qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out);
 
@@ -484,8 +485,8 @@ qa_status qa_q4_get_device_error(qa_q4_cache *cache, uint32_t *detail);
 /* Successful launches per kernel (QA_Q4_KERNEL_*). */
 qa_status qa_q4_stats(qa_q4_cache *cache, uint64_t launches[QA_Q4_NUM_KERNELS]);
 
-/* Device bytes: codes and scale bytes, and scratch (workspace, rotary table,
- * error word). */
+/* Device bytes: codes and scale bytes, and scratch (workspace, sums of
+ * parts, rotary table, error word). */
 qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t *scratch_bytes);
 
 /* Static description of a status code. */

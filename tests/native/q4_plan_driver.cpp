@@ -1,5 +1,7 @@
 // Command-line driver of csrc/q4_plan.h for the CPU tests, one command per line:
 //   decode <D> <groups> <held 1..13> <n> <keys>*n   -> cluster, then the splits
+//   parts <window> <D> <G> <Hkv> <sms> <n> (<start> <len>)*n
+//                                      -> 1 when cut, heads an item, (run, lo, hi) per part
 //   runs <window> <D> <G> <Hkv> <sms> <n> <start len>*n
 //     -> span before, span after, then "seq first len" of every run
 #include <iostream>
@@ -25,6 +27,20 @@ int main() {
             qa::plan_decode(D, held, groups, n, keys, plan);
             std::cout << plan.cluster;
             for (int i = 0; i < n; ++i) std::cout << " " << plan.splits[i];
+            std::cout << "\n";
+        } else if (cmd == "parts") {
+            int window, D, G, Hkv, sms, n, hpi = 0;
+            in >> window >> D >> G >> Hkv >> sms >> n;
+            std::vector<int> start(n);
+            std::vector<qa::QueryRun> runs;
+            for (int i = 0; i < n; ++i) {
+                int len;
+                in >> start[i] >> len;
+                runs.push_back({i, 0, len});
+            }
+            std::vector<qa::KeyPart> parts;
+            std::cout << qa::plan_parts(runs, start.data(), window, D, G, Hkv, sms, 8, parts, hpi) << " " << hpi;
+            for (const qa::KeyPart &k : parts) std::cout << " " << k.run << " " << k.lo << " " << k.hi;
             std::cout << "\n";
         } else if (cmd == "runs") {
             int window, D, G, Hkv, sms, n;

@@ -410,6 +410,34 @@ def test_prefill(qa, hq, hkv, d, start, ntok, window):
 
 
 # ------------------------------------------------------------------ together
+@pytest.mark.parametrize("hq,hkv,d,start,ntok,window", [
+    (8, 2, 128, [5000], [100], 0),
+    (32, 8, 128, [6001, 2500], [60, 33], 0),
+    (8, 1, 64, [9000], [300], 0),
+    (4, 4, 64, [5000, 0, 300], [130, 40, 257], 0),     # one sequence with parts, others without
+    (3, 3, 128, [4096], [128], 0),
+    (8, 2, 128, [9000], [257], 3000),                   # the window starts inside the first part
+    (16, 8, 64, [7000, 40], [129, 33], 2500),
+    (4, 2, 128, [8191], [40], 8000),
+])
+def test_prefill_keys_in_parts(qa, hq, hkv, d, start, ntok, window):
+    # Few query blocks behind many keys: the keys are cut into parts and joined.
+    with Cache(qa, 1, len(start), hq, hkv, d, max(start) + max(ntok)) as c:
+        qa.qa_q4_cache_set_window(c.h, 0, window)
+        c.fill(0, start, 5)
+        q, k, v = c.tokens(ntok, 6)
+        outs = [torch.full_like(q, float("nan")) for _ in range(2)]
+        for out in outs:
+            qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        assert torch.equal(*outs)
+        qp, kp = c.transform(start, ntok, q, k, v)
+        c.note(0, start, ntok, kp, f64(v))
+        c.check_bytes()
+        want, mag = c.want(start, ntok, qp, window=window)
+        close(outs[0], want, mag, PREFILL_BITS)
+
+
 def test_generate_steps_back_to_back(qa):
     # A prompt, then decode steps over two layers with nothing between the
     # launches, a verify chunk whose last tokens are dropped, and more steps.

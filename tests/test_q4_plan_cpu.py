@@ -72,6 +72,45 @@ def test_splits_of_mixed_sequences(driver):
     assert mixed > 40
 
 
+def test_key_parts_cover_every_tile_once(driver):
+    rng = random.Random(7)
+    cases = []
+    for _ in range(600):
+        seqs = [(int(80000 ** rng.random()), int(600 ** rng.random()) + 17) for _ in range(rng.randint(1, 5))]
+        window = rng.choice([0, 0, 1, 200, 1000, 5000, 20000])
+        cases.append((window, rng.choice([64, 128]), rng.choice([1, 2, 4, 8]), rng.choice([1, 2, 3, 8]), seqs))
+    got = driver([f"parts {w} {d} {g} {h} 152 {len(s)} {' '.join(f'{a} {b}' for a, b in s)}" for w, d, g, h, s in cases])
+    cut = 0
+    for (window, d, g, hkv, seqs), (yes, hpi, *flat) in zip(cases, got):
+        if not yes:
+            continue
+        cut += 1
+        parts = list(zip(flat[0::3], flat[1::3], flat[2::3]))
+        assert len(parts) <= 8 and hpi in (1, 2) and g % hpi == 0
+        blocks = [-(-n // 128) for _, n in seqs]
+        assert sum(blocks[r] for r, _, _ in parts) * hkv * (g // hpi) <= 152       # one item an SM
+        assert sum(seqs[r][1] for r, _, _ in parts) * hkv * g <= 256 * 152         # what the cache has room for
+        assert sorted(r for r, _, _ in parts) == [r for r, _, _ in parts] and {r for r, _, _ in parts} == set(range(len(seqs)))
+        for i, (start, n) in enumerate(seqs):
+            mine = [(lo, hi) for r, lo, hi in parts if r == i]
+            for b in range(blocks[i]):
+                pos = start + 128 * b
+                first = max(0, pos + 1 - window) // 128 if window else 0
+                end = (start + min(n, 128 * b + 128) - 1) // 128 + 1
+                seen = [t for lo, hi in mine for t in range(max(lo, first), min(hi, end))]
+                assert seen == list(range(first, end))
+                assert all(max(lo, first) < min(hi, end) for lo, hi in mine)           # none without a tile
+    assert cut > 150
+
+
+def test_key_parts_where_they_pay(driver):
+    one = [f"parts 0 128 4 8 152 1 {start} {n}" for start, n in ((16384, 128), (2048, 128), (1000, 128), (2048, 512), (0, 128))]
+    assert [line[0] for line in driver(one)] == [1, 1, 0, 0, 0]
+    assert driver(["parts 0 128 8 1 152 1 16384 128", "parts 0 128 4 8 152 1 16384 128"]) == [
+        [1, 1] + [x for k in range(8) for x in (0, 129 * k // 8, 129 * (k + 1) // 8 if k < 7 else 1 << 30)],
+        [1, 2] + [x for k in range(8) for x in (0, 129 * k // 8, 129 * (k + 1) // 8 if k < 7 else 1 << 30)]]
+
+
 def test_runs_cover_every_row_once_and_never_cost_more(driver):
     rng = random.Random(3)
     cases = []
