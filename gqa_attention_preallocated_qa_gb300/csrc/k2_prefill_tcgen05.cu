@@ -1087,9 +1087,9 @@ static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t strea
     q.hpi = p.G > 1 ? 2 : 1;
     q.npairs = (p.G + q.hpi - 1) / q.hpi;
     q.nitems = nitems / p.npairs * q.npairs;
-    if (q.hpi == 2 && q.nitems < sms) {
+    if (q.hpi == 2 && q.nitems < sms && p.hpi != 2) {
         // Fewer two-head items than SMs (a short prompt or chunk): one query
-        // head per item, twice the work units.
+        // head per item, twice the work units (unless the caller asks for two).
         q.hpi = 1;
         q.npairs = p.G;
         q.nitems = nitems / p.npairs * q.npairs;

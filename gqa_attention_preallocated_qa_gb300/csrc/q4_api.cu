@@ -384,6 +384,7 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     k2.npairs = c->G / k2.hpi;
     if (!pg.parts) {
         qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
+        k2.hpi = qa::two_heads(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms) ? 2 : 0;
         for (size_t i = 0; i < runs.size(); ++i) parts.push_back({static_cast<int>(i), 0, 1 << 30});
     }
     pg.join = qa::K2JoinParams{};

@@ -97,12 +97,12 @@ inline void plan_decode(int D, const int *held, int groups, int n, const int *ke
 // or through the prefill kernel on the dequantised cache, where up to 128 tokens
 // cost the same.  (8 kv heads, 32 query heads, D = 128, eight tokens / prefill
 // kernel: nothing cached 4.0 / 12.5 us for one sequence, 5.6 / 14.5 for four,
-// 14 / 33 for 16; 512 keys 4.6 / 22, 7.4 / 25, 21 / 67; 2048 keys 7.0 / 28,
-// 12.5 / 45, 37 / 150; 16384 keys 17.8 / 62, 53 / 178, 198 / 910.)
+// 14 / 29 for 16; 512 keys 4.7 / 23, 7.4 / 25, 21 / 56; 2048 keys 7.0 / 26,
+// 12.5 / 45, 37 / 115; 16384 keys 17.9 / 62, 53 / 179, 198 / 661.)
 constexpr int kQ4MaxTokens = 8;  // new tokens per sequence of one decode launch
 inline bool few_tokens(int start, int ntok, int window) {
     const int keys = window > 0 ? std::min(start, window) : start;
-    return ntok <= kQ4MaxTokens * (keys < 512 ? 2 : keys < 4096 ? 3 : 4);
+    return ntok <= kQ4MaxTokens * (keys < 512 ? 2 : 3);
 }
 
 // A run of query blocks of one sequence of a prefill launch: rows first ..
@@ -194,6 +194,25 @@ inline void plan_runs(std::vector<QueryRun> &runs, const int *start, int window,
     runs = best;
 }
 
+// A key tile of the one-CTA prefill kernel with h heads an item, us.
+inline float tile_us(int D, int h) { return h == 2 ? (D == 128 ? 1.75f : 1.45f) : (D == 128 ? 1.3f : 1.2f); }
+
+// Whether a launch that has fewer two-head items than SMs, but more one-head
+// items, does better with two heads: one round of 1.75 us a key tile instead of
+// two of 1.3.  (32 / 8 heads, D = 128: 8
+// sequences of 128 tokens behind 16384 keys 458 -> 336 us, 5 of 100 behind 2048
+// 72 -> 55, 4 prompts of 256 21.2 -> 20.4.)
+inline bool two_heads(const std::vector<QueryRun> &runs, const int *start, int window, int D, int G, int Hkv, int sms) {
+    int blocks = 0;
+    for (const QueryRun &r : runs) blocks += (r.len + 127) / 128;
+    const int64_t items = static_cast<int64_t>(blocks) * Hkv * (G / 2);
+    if (G < 2 || items >= sms || 2 * items <= sms) return false;
+    std::vector<int> load;
+    const int two = prefill_span(runs, start, window, Hkv * (G / 2), sms, load);
+    const int one = prefill_span(runs, start, window, Hkv * G, sms, load);
+    return two * tile_us(D, 2) < one * tile_us(D, 1);
+}
+
 // A part of a run's keys: tiles lo .. hi - 1 of 128.
 struct KeyPart {
     int run, lo, hi;
@@ -212,7 +231,6 @@ inline bool plan_parts(const std::vector<QueryRun> &runs, const int *start, int 
                        int max_parts, std::vector<KeyPart> &parts, int &hpi) {
     const int nruns = static_cast<int>(runs.size());
     if (nruns == 0 || 2 * nruns > max_parts) return false;
-    const float tile_us[3] = {0.f, D == 128 ? 1.3f : 1.2f, D == 128 ? 1.75f : 1.45f};
     int blocks[kQ4MaxSeqPerLaunch], from[kQ4MaxSeqPerLaunch], tiles[kQ4MaxSeqPerLaunch];
     int total = 0, most = 0, rows = 0;
     for (int i = 0; i < nruns; ++i) {
@@ -231,7 +249,7 @@ inline bool plan_parts(const std::vector<QueryRun> &runs, const int *start, int 
         while (m > 1 && window > 0 && tiles[i] / m <= blocks[i]) --m;
         return m;
     };
-    float least = tile_us[1] * most - 1.f;
+    float least = tile_us(D, 1) * most - 1.f;
     int best = 1;
     for (int h = std::min(G, 2); h >= 1; --h) {
         const int items = total * Hkv * (G / h);
@@ -241,7 +259,7 @@ inline bool plan_parts(const std::vector<QueryRun> &runs, const int *start, int 
                 const int m = cut(i, n);
                 longest = std::max(longest, (tiles[i] + m - 1) / m + blocks[i] - 1);
             }
-            const float us = tile_us[h] * longest + 5.f + 0.2e-3f * (D / 128.f) * rows * (Hkv * G) * n;
+            const float us = tile_us(D, h) * longest + 5.f + 0.2e-3f * (D / 128.f) * rows * (Hkv * G) * n;
             if (us < least) {
                 least = us;
                 best = n;

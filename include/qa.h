@@ -436,11 +436,11 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * new token attends causally to what the cache then holds (its own rows as
  * held, too), within the layer's window.
  * Sequences with few new tokens (up to 16; up to 24 behind 512 cached
- * positions and up to 32 behind 4096, at most a window of which count) take the
- * decode kernel, 8 tokens a launch, one launch per 64 sequences.  The others
- * take K4 and K2 through the cache's workspace, up to 8 sequences at a time:
- * calls with such sequences on several streams wait for each other, and they
- * cannot be captured into a graph (QA_ERR_STATE).  In that form a key or value
+ * positions, at most a window of which count) take the decode kernel, 8 tokens
+ * a launch, one launch per 64 sequences.  The others take K4 and K2 through the
+ * cache's workspace, up to 8 sequences at a time: calls with such sequences on
+ * several streams wait for each other, and they cannot be captured into a
+ * graph (QA_ERR_STATE).  In that form a key or value
  * that is not finite can reach other new tokens of its sequence in the call,
  * also those before it (as in qa_prefill: the tensor cores multiply it by their
  * weight of zero).

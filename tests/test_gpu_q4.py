@@ -391,6 +391,8 @@ def test_chunk_of_sixteen_in_a_graph(qa):
     (8, 1, 128, [300, 140], [200, 77], 150),
     (32, 8, 128, [1500, 130, 20, 1500], [700, 900, 60, 130], 0),  # more blocks than the device takes at once
     (16, 8, 64, [900, 0], [300, 1000], 700),
+    (32, 8, 128, [2000, 1500, 1800, 2000, 700], [100, 90, 128, 33, 64], 0),  # two-head items, fewer than SMs
+    (16, 8, 64, [900] * 6, [200] * 6, 300),
     (4, 1, 64, [31] * 11, [20, 0, 3, 150, 9, 1, 20, 33, 128, 2, 17], 0),
 ])
 def test_prefill(qa, hq, hkv, d, start, ntok, window):
