@@ -93,6 +93,13 @@ template <int D, int kU>
 __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constant__ Q4RowsParams p) {
     constexpr int LPR = D / 8;
     constexpr int GR = D / kQ4Group;
+    // In a prefill it runs beside the kernel of the new rows, which touches none
+    // of these, and the attention kernel after it sets up beside both.  That one
+    // waits for this grid, whose last block is not done before the new rows are.
+    if (p.beside) {
+        griddep_launch_dependents();
+        if (blockIdx.x == gridDim.x - 1) griddep_wait();
+    }
     const Q4Task t = q4_task<D, kU>(p);
     if (t.n <= 0) return;
     const int lane = threadIdx.x & 31, sub = lane % LPR, half = lane / LPR;
@@ -176,8 +183,8 @@ __global__ void __launch_bounds__(kQ4RowWarps * 32, 1)
     const K1Params &k = p.k1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane % LPR, grp = lane / LPR;
-    // The prefill attention follows as a programmatic dependent: its set-up may
-    // start now; it reads what this kernel writes only after its end.
+    // The next kernel (the older rows', or the attention) is a programmatic
+    // dependent: it may start now and reads what this one writes only after its end.
     if (k.signal_early) griddep_launch_dependents();
     const int parts = p.parts;
     const int nq = k.Hq / parts, nkv = k.Hkv / parts;  // heads of a share
@@ -396,9 +403,17 @@ cudaError_t launch_q4_dequantise(const Q4RowsParams &p, int D, cudaStream_t stre
     if (p.nblocks <= 0) return cudaSuccess;
     unsigned blocks;
     if (!q4_rows_grid(p, blocks) || p.unroll != 4) return cudaErrorInvalidConfiguration;
-    if (D == 128) q4_dequantise_kernel<128, 4><<<blocks, 256, 0, stream>>>(p);
-    else q4_dequantise_kernel<64, 4><<<blocks, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.beside ? 1 : 0;
+    return D == 128 ? cudaLaunchKernelEx(&cfg, q4_dequantise_kernel<128, 4>, p)
+                    : cudaLaunchKernelEx(&cfg, q4_dequantise_kernel<64, 4>, p);
 }
 
 }  // namespace qa

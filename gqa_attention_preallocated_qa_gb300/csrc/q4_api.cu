@@ -653,18 +653,25 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         if (!few_tokens(b)) next[b] = start[b] + ntok[b];
     const bool fused = qa::q4_prefill_rows_fits(c->cfg.n_q_heads, c->cfg.n_kv_heads, c->cfg.head_dim);
     auto launch = [&](PrefillGroup &pg) {
-        // The older rows first: K2 then follows the kernel that lets it start early.
-        if (pg.held.nblocks > 0) {
-            if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
+        auto older_rows = [&](bool beside) {
+            if (pg.held.nblocks == 0) return true;
+            pg.held.beside = beside ? 1 : 0;
+            if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return false;
             qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
-        }
+            return true;
+        };
         if (fused) {
             pg.rows.k1.signal_early = 1;
             if (qa::launch_q4_prefill_rows(pg.rows, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
+            if (!older_rows(true)) {
+                cudaStreamSynchronize(s);  // as below
+                return QA_ERR_CUDA;
+            }
         } else {
+            if (!older_rows(false)) return QA_ERR_CUDA;
             if (qa::launch_k1(pg.rows.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             qa::launch_order().barrier(s);
             c->launches[QA_Q4_KERNEL_NORM_ROPE]++;

@@ -35,6 +35,7 @@ struct Q4RowsParams {
     int nseq, Hkv, nblocks, kv_first, kv_count;  // kv_first/count: K (0) and V (1) served
     int unroll;                          // tokens per lane group of a block: 4 or 8
     int seq0;                            // cache slot of launched sequence 0
+    int beside;                          // dequantise: starts beside the kernel before it, signals at once
     int start[kQ4MaxSeqPerLaunch], ntok[kQ4MaxSeqPerLaunch];
     int block0[kQ4MaxSeqPerLaunch + 1];  // first token block of each launched sequence
     int64_t src_off[kQ4MaxSeqPerLaunch], dst_off[kQ4MaxSeqPerLaunch];
