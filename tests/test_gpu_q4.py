@@ -751,3 +751,26 @@ def test_a_wait_that_runs_out_is_reported_and_the_cache_stays_usable(qa):
         c.note(0, lens, [1, 1], kp, f64(v))
         want, mag = c.want(lens, [1, 1], qp)
         close(out, want, mag, DECODE_BITS)
+
+
+@pytest.mark.parametrize("lens,ntok,kernel", [
+    ([300, 4000, 90, 7], [1] * 4, 2),       # splits by length, several groups in a cluster
+    ([5000, 0], [100, 0], 1),               # the prefill kernel with the keys in parts, and the join behind it
+])
+def test_a_wait_that_runs_out_in_the_other_forms(qa, lens, ntok, kernel):
+    with Cache(qa, 1, len(lens), 32, 8, 128, 5200) as c:
+        c.fill(0, lens, 5)
+        q, k, v = c.tokens(ntok, 6)
+        out = torch.empty_like(q)
+        qa.qa_debug_arm_wait_timeout(kernel, 20000)
+        qa.qa_q4_prefill(c.h, 0, lens, ntok, q, k, v, c.wq, c.wk, out)
+        st, word = qa.qa_q4_get_device_error(c.h)
+        assert st == 7 and word & 0xff == 1
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        qa.qa_q4_prefill(c.h, 0, lens, ntok, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        qp, kp = c.transform(lens, ntok, q, k, v)
+        c.note(0, lens, ntok, kp, f64(v))
+        c.check_bytes()
+        want, mag = c.want(lens, ntok, qp)
+        close(out, want, mag, DECODE_BITS if kernel == 2 else PREFILL_BITS)
