@@ -134,8 +134,6 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
 // be written, read and written again.  Bound by HBM; a warp walks its share of
 // the tokens with the next token's rows on the way into the other half of its
 // ring (three bulk copies), as K1 does.
-constexpr int kQ4RowWarps = 16;  // warps per CTA, one CTA per SM
-
 // RMSNorm + RoPE of this lane's 8 values of a row held by D/8 lanes; cs, sn:
 // cosines and sines of its dims, the sines signed for its half.
 template <int D>
@@ -318,26 +316,6 @@ __global__ void __launch_bounds__(kQ4RowWarps * 32, 1)
     }
 }
 
-static size_t q4_prefill_rows_smem(int Hq, int Hkv, int D, int parts) {
-    const size_t stage = (static_cast<size_t>(Hq / parts + 2 * (Hkv / parts)) * D * 2 + 127) & ~static_cast<size_t>(127);
-    return static_cast<size_t>(kQ4RowWarps) * 2 * stage + 128;
-}
-constexpr size_t kQ4RowSmemMost = 200 * 1024 + 128;
-
-// Shares that a token is cut into, by heads (0: no number of them fits): the
-// fewest that fit (two at 32 + 2 x 8 heads of 128), and four as long as every
-// share still has a warp of its own.  (Prefill of 256 tokens: 14.5 us with four
-// shares and 16.6 with two; of 1024: 29.5 and 27.0; eight leave lanes idle.)
-static int q4_row_parts(int Hq, int Hkv, int D, int64_t T, int sms) {
-    int parts = 1;
-    while (q4_prefill_rows_smem(Hq, Hkv, D, parts) > kQ4RowSmemMost) {
-        parts *= 2;
-        if (Hkv % parts) return 0;
-    }
-    while (parts < 4 && Hkv % (2 * parts) == 0 && 2 * T * parts <= static_cast<int64_t>(sms) * kQ4RowWarps) parts *= 2;
-    return parts;
-}
-
 bool q4_prefill_rows_fits(int Hq, int Hkv, int D) { return q4_row_parts(Hq, Hkv, D, int64_t(1) << 40, 1) > 0; }
 
 template <int D>
@@ -360,7 +338,7 @@ static cudaError_t q4_prefill_rows_t(const Q4PrefillRowsParams &params, cudaStre
     }
     Q4PrefillRowsParams p = params;
     p.parts = q4_row_parts(p.k1.Hq, p.k1.Hkv, D, p.k1.T, sms);
-    if (p.parts == 0) return cudaErrorInvalidConfiguration;
+    if (p.parts < 1 || kQ4RowWarps % p.parts) return cudaErrorInvalidConfiguration;
     const int64_t need = (static_cast<int64_t>(p.k1.T) * p.parts + kQ4RowWarps - 1) / kQ4RowWarps;
     q4_prefill_rows_kernel<D><<<static_cast<unsigned>(std::min<int64_t>(need, sms)), kQ4RowWarps * 32,
                                 q4_prefill_rows_smem(p.k1.Hq, p.k1.Hkv, D, p.parts), stream>>>(p);

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 #include <vector>
 
@@ -103,6 +104,30 @@ constexpr int kQ4MaxTokens = 8;  // new tokens per sequence of one decode launch
 inline bool few_tokens(int start, int ntok, int window) {
     const int keys = window > 0 ? std::min(start, window) : start;
     return ntok <= kQ4MaxTokens * (keys < 512 ? 2 : 3);
+}
+
+// A prefill's rows (K4): warps of a CTA, one CTA per SM, each with a ring of two
+// stages that hold one share of a token's query, key and value rows.
+constexpr int kQ4RowWarps = 16;
+constexpr size_t kQ4RowSmemMost = 200 * 1024 + 128;
+inline size_t q4_prefill_rows_smem(int Hq, int Hkv, int D, int parts) {
+    const size_t stage = (static_cast<size_t>(Hq / parts + 2 * (Hkv / parts)) * D * 2 + 127) & ~static_cast<size_t>(127);
+    return static_cast<size_t>(kQ4RowWarps) * 2 * stage + 128;
+}
+
+// Shares that a token is cut into, by heads (0: no number of them fits): the
+// fewest that fit (two at 32 + 2 x 8 heads of 128), and four as long as every
+// share still has a warp of its own.  A power of two, and at most one for each
+// warp of a CTA: a warp steps by gridDim * (warps / shares) tokens.  (Prefill of 256 tokens: 14.5 us with four
+// shares and 16.6 with two; of 1024: 29.5 and 27.0; eight leave lanes idle.)
+inline int q4_row_parts(int Hq, int Hkv, int D, int64_t T, int sms) {
+    int parts = 1;
+    while (q4_prefill_rows_smem(Hq, Hkv, D, parts) > kQ4RowSmemMost) {
+        parts *= 2;
+        if (parts > kQ4RowWarps || Hkv % parts) return 0;
+    }
+    while (parts < 4 && Hkv % (2 * parts) == 0 && 2 * T * parts <= static_cast<int64_t>(sms) * kQ4RowWarps) parts *= 2;
+    return parts;
 }
 
 // A run of query blocks of one sequence of a prefill launch: rows first ..
