@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -22,17 +23,19 @@ struct qa_q4_cache {
     int G = 1;
     int rows = 0;              // rows of one (sequence, kv head): the capacity, padded
     int64_t layer_rows = 0;    // rows of one layer
+    void *mem = nullptr;       // one allocation: codes, scale bytes, error word, ws_lens
     uint8_t *codes[2] = {}, *scales[2] = {};  // K and V
+    uint32_t *err = nullptr;
+    int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
+    const float2 *rope = nullptr;   // shared (RopeTables)
     // Prefill attention reads one layer's rows in bf16: the sequences of a
-    // launch, dequantised, laid out [slot][kv head][capacity][head_dim].
+    // launch, dequantised, laid out [slot][kv head][capacity][head_dim].  Every
+    // row that it reads is written before it, so nothing is zeroed.
     int ws_slots = 0;
-    __nv_bfloat16 *ws[2] = {};
-    float *part_o = nullptr;        // sums of the parts of a block's keys (k2_parts.h)
+    __nv_bfloat16 *ws[2] = {};      // taken by the first call that needs it
+    float *part_o = nullptr;        // sums of the parts of a block's keys (k2_parts.h); likewise
     float2 *part_ml = nullptr;
     cudaEvent_t ws_free = nullptr;  // the last prefill that used the workspace
-    int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
-    float2 *rope = nullptr;
-    uint32_t *err = nullptr;
     std::vector<int> window;        // per layer: attention window in keys (0: full)
     // Per (layer, sequence): the position after the last one written, -1 when
     // only the device knows it.  A decode step that continues there can tell
@@ -74,29 +77,128 @@ qa_status no_throw(F &&body) {
     }
 }
 
-template <typename T>
-bool dev_alloc(T **p, size_t count, uint64_t &acct) {
-    const size_t bytes = std::max<size_t>(count, 1) * sizeof(T);
-    if (cudaMalloc(reinterpret_cast<void **>(p), bytes) != cudaSuccess) {
-        *p = nullptr;
-        return false;
+constexpr size_t align256(size_t bytes) { return (bytes + 255) & ~size_t(255); }
+
+// Angles of the pairs of dims: position * theta^(-2i/D), i below D / 2.
+struct RopeFreqs {
+    double f[64];
+};
+
+// As qa::fill_rope_table: the same product in fp64, its cosine and sine in fp64,
+// rounded once (2^20 positions, D 64 and 128, theta 10^4 and 10^6: no bit
+// differs from the host's).  Bound by the fp64 units: 16,385 positions of 64
+// pairs take 0.06 ms and 2^20 3.5 ms; one host thread takes 18 ms for the former.
+__global__ void rope_table_kernel(float2 *tab, int64_t n, int half, const __grid_constant__ RopeFreqs freqs) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+        const int64_t pos = i / half;
+        double s, c;
+        sincos(static_cast<double>(pos) * freqs.f[i - pos * half], &s, &c);
+        tab[i] = make_float2(static_cast<float>(c), static_cast<float>(s));
     }
-    acct += bytes;
-    return cudaMemset(*p, 0, bytes) == cudaSuccess;
 }
 
-void free_all(qa_q4_cache *c) {
-    for (int i = 0; i < 2; ++i) {
-        cudaFree(c->codes[i]);
-        cudaFree(c->scales[i]);
-        cudaFree(c->ws[i]);
+// The rotary tables of the caches that are alive.  A table depends on theta and
+// head_dim alone and a longer one begins with the shorter ones, so caches of one
+// device share it.
+class RopeTables {
+  public:
+    // A table of at least `rows` positions on the current device; null on error.
+    const float2 *take(int device, float theta, int D, int rows) {
+        std::lock_guard<std::mutex> lock(mu_);
+        for (Table &t : tables_)
+            if (t.device == device && t.theta == theta && t.D == D && t.rows >= rows) {
+                ++t.users;
+                return t.tab;
+            }
+        tables_.reserve(tables_.size() + 1);
+        RopeFreqs freqs{};
+        for (int i = 0; i < D / 2; ++i) freqs.f[i] = std::pow(static_cast<double>(theta), -2.0 * i / D);
+        const int64_t n = static_cast<int64_t>(rows) * (D / 2);
+        float2 *tab = nullptr;
+        if (cudaMalloc(reinterpret_cast<void **>(&tab), n * sizeof(float2)) != cudaSuccess) return nullptr;
+        rope_table_kernel<<<static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 4096)), 256>>>(tab, n, D / 2, freqs);
+        if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+            cudaFree(tab);
+            return nullptr;
+        }
+        tables_.push_back({device, theta, D, rows, 1, tab});
+        return tab;
     }
+    // Gives one back; the caller has synchronised its device.
+    void give(const float2 *tab) {
+        if (!tab) return;
+        std::lock_guard<std::mutex> lock(mu_);
+        for (size_t i = 0; i < tables_.size(); ++i)
+            if (tables_[i].tab == tab && --tables_[i].users == 0) {
+                cudaFree(tables_[i].tab);
+                tables_.erase(tables_.begin() + i);
+                return;
+            }
+    }
+
+  private:
+    struct Table {
+        int device;
+        float theta;
+        int D, rows, users;
+        float2 *tab;
+    };
+    std::mutex mu_;
+    std::vector<Table> tables_;
+};
+RopeTables g_rope;
+
+void free_all(qa_q4_cache *c) {
+    g_rope.give(c->rope);
+    cudaFree(c->mem);
+    cudaFree(c->ws[0]);
     cudaFree(c->part_o);
-    cudaFree(c->part_ml);
-    cudaFree(c->ws_lens);
-    cudaFree(c->rope);
-    cudaFree(c->err);
     if (c->ws_free) cudaEventDestroy(c->ws_free);
+}
+
+// Allocations of a call that is not captured itself are no part of a capture
+// that is under way on another stream.
+class OutsideCapture {
+  public:
+    OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+  private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
+size_t workspace_bytes(const qa_q4_cache *c) {  // of K or of V
+    return static_cast<size_t>(c->ws_slots) * c->cfg.n_kv_heads * c->cfg.capacity * c->cfg.head_dim * 2;
+}
+bool take_workspace(qa_q4_cache *c) {
+    if (c->ws[0]) return true;
+    OutsideCapture scope;
+    if (!c->ws_free && cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) != cudaSuccess) {
+        c->ws_free = nullptr;
+        return false;
+    }
+    const size_t one = align256(workspace_bytes(c));
+    void *p = nullptr;
+    if (cudaMalloc(&p, 2 * one) != cudaSuccess) return false;
+    c->ws[0] = static_cast<__nv_bfloat16 *>(p);
+    c->ws[1] = c->ws[0] + one / 2;
+    return true;
+}
+
+// The parts of a launch have at most two heads' blocks of 128 rows per SM;
+// caches this short are not cut.
+constexpr int kQ4PartsCapacity = 1024;
+size_t part_rows(const qa_q4_cache *c) { return static_cast<size_t>(c->num_sms) * 256; }
+bool take_sums(qa_q4_cache *c) {
+    if (c->part_o) return true;
+    OutsideCapture scope;
+    const size_t sums = part_rows(c) * c->cfg.head_dim;  // (a multiple of 256 bytes)
+    void *p = nullptr;
+    if (cudaMalloc(&p, sums * sizeof(float) + part_rows(c) * sizeof(float2)) != cudaSuccess) return false;
+    c->part_o = static_cast<float *>(p);
+    c->part_ml = reinterpret_cast<float2 *>(c->part_o + sums);
+    return true;
 }
 
 qa_status check_layer(const qa_q4_cache *c, int layer, int batch) {
@@ -309,7 +411,7 @@ struct PrefillGroup {
 };
 
 // Builds the launches for sequences s0 .. s0 + n - 1; false when a tensor map
-// cannot be made.
+// cannot be made or the sums of parts find no memory.
 bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start, const int32_t *ntok,
                   int64_t row0, const void *q, const void *k, const void *v, const void *wq,
                   const void *wk, void *out, PrefillGroup &pg) {
@@ -379,8 +481,10 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     }
     k2.hpi = std::min(c->G, 2);
     std::vector<qa::KeyPart> parts;
-    pg.parts = c->part_o && qa::plan_parts(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms,
-                                           qa::kMaxSeqPerLaunch, parts, k2.hpi);
+    pg.parts = g.capacity >= kQ4PartsCapacity &&
+               qa::plan_parts(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms,
+                              qa::kMaxSeqPerLaunch, parts, k2.hpi);
+    if (pg.parts && !take_sums(c)) return false;
     k2.npairs = c->G / k2.hpi;
     if (!pg.parts) {
         qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
@@ -458,32 +562,27 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
     c->layer_rows = static_cast<int64_t>(g.max_batch) * g.n_kv_heads * c->rows;
     c->ws_slots = std::min(g.max_batch, qa::kMaxSeqPerLaunch);
     const size_t rows = static_cast<size_t>(c->layer_rows) * g.num_layers;
-    const size_t ws = static_cast<size_t>(c->ws_slots) * g.n_kv_heads * g.capacity * g.head_dim;
+    const size_t codes = rows * (g.head_dim / 2), scales = rows * (g.head_dim / qa::kQ4Group);
+    const size_t total = 2 * (align256(codes) + align256(scales)) + 256;
     bool ok = cudaGetDevice(&c->device) == cudaSuccess &&
-              cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess;
-    for (int i = 0; ok && i < 2; ++i)
-        ok = dev_alloc(&c->codes[i], rows * (g.head_dim / 2), c->cache_bytes) &&
-             dev_alloc(&c->scales[i], rows * (g.head_dim / qa::kQ4Group), c->cache_bytes) &&
-             dev_alloc(&c->ws[i], ws, c->scratch_bytes);
-    ok = ok && dev_alloc(&c->ws_lens, qa::kMaxSeqPerLaunch, c->scratch_bytes) &&
-         // The parts of a launch have at most two heads' blocks of 128 rows per SM;
-         // caches this short are not cut.
-         (g.capacity < 1024 ||
-          (dev_alloc(&c->part_o, static_cast<size_t>(c->num_sms) * 256 * g.head_dim, c->scratch_bytes) &&
-           dev_alloc(&c->part_ml, static_cast<size_t>(c->num_sms) * 256, c->scratch_bytes))) &&
-         dev_alloc(&c->rope, static_cast<size_t>(g.capacity) * (g.head_dim / 2), c->scratch_bytes) &&
-         dev_alloc(&c->err, 1, c->scratch_bytes) &&
-         cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) == cudaSuccess;
+              cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess &&
+              cudaMalloc(&c->mem, total) == cudaSuccess && cudaMemsetAsync(c->mem, 0, total, nullptr) == cudaSuccess;
     ok = ok && no_throw([&] {
+        uint8_t *at = static_cast<uint8_t *>(c->mem);
+        for (int i = 0; i < 2; ++i, at += align256(codes)) c->codes[i] = at;
+        for (int i = 0; i < 2; ++i, at += align256(scales)) c->scales[i] = at;
+        c->err = reinterpret_cast<uint32_t *>(at);
+        c->ws_lens = reinterpret_cast<int32_t *>(at + 128);
+        static_assert(qa::kMaxSeqPerLaunch * sizeof(int32_t) <= 128, "behind the error word");
         c->window.assign(static_cast<size_t>(g.num_layers), 0);
         c->next_pos.assign(static_cast<size_t>(g.num_layers) * g.max_batch, -1);
-        std::vector<float2> tab(static_cast<size_t>(g.capacity) * (g.head_dim / 2));
-        qa::fill_rope_table(tab.data(), g.capacity, g.head_dim, g.rope_theta);
-        return cudaMemcpy(c->rope, tab.data(), tab.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
-                       cudaDeviceSynchronize() == cudaSuccess
-                   ? QA_OK
-                   : QA_ERR_CUDA;
+        c->rope = g_rope.take(c->device, g.rope_theta, g.head_dim, g.capacity);
+        return c->rope && cudaStreamSynchronize(nullptr) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
     }) == QA_OK;
+    c->cache_bytes = 2 * (codes + scales);
+    c->scratch_bytes = 256 + 2 * workspace_bytes(c) +
+                       (g.capacity < kQ4PartsCapacity ? 0 : part_rows(c) * (g.head_dim * sizeof(float) + sizeof(float2))) +
+                       static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
     if (!ok) {
         free_all(c);
         delete c;
@@ -619,6 +718,10 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             cudaGetLastError();
             return QA_ERR_STATE;
         }
+        if (!take_workspace(c)) {
+            cudaGetLastError();
+            return QA_ERR_CUDA;
+        }
         // A group's rows are packed one after the other, so sequences that take
         // the decode kernel stand between groups.
         st = no_throw([&] {
@@ -634,8 +737,10 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
                 }
                 groups.emplace_back();
                 PrefillGroup &pg = groups.back();
-                if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg))
+                if (!plan_prefill(c, layer, s0, n, start, ntok, row0, q, k, v, q_norm_w, k_norm_w, out, pg)) {
+                    cudaGetLastError();
                     return QA_ERR_CUDA;
+                }
                 row0 += pg.rows.k1.T;
                 s0 += n;
             }

@@ -399,10 +399,14 @@ enum {
 /* Allocate a 4-bit cache on the current device, with the geometry that
  * qa_cache_alloc takes: codes [num_layers][max_batch][n_kv_heads][rows][D/2]
  * and scale bytes [...][rows][D/32] for K and for V (zero-filled; rows is the
- * capacity, rounded up to a multiple of 64), the rotary table, an error word,
- * and one bf16 workspace for prefill attention: K and V of min(max_batch, 8)
- * sequences of one layer, [slot][n_kv_heads][capacity][D], and from capacity
- * 1024 on the fp32 sums of keys in parts (20 MB at D = 128).  Synchronous.
+ * capacity, rounded up to a multiple of 64), an error word, and the rotary
+ * table (computed on the device; the caches of one device, rope_theta and
+ * head_dim that are alive share one).  Synchronous.
+ * What prefill attention needs beside them is allocated by the first
+ * qa_q4_prefill that takes it, and kept: a bf16 workspace of K and V of
+ * min(max_batch, 8) sequences of one layer, [slot][n_kv_heads][capacity][D],
+ * and, at capacity 1024 or more, the fp32 sums of keys in parts (20 MB at D =
+ * 128).  No other call allocates.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
 qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out);
 
@@ -485,8 +489,9 @@ qa_status qa_q4_get_device_error(qa_q4_cache *cache, uint32_t *detail);
 /* Successful launches per kernel (QA_Q4_KERNEL_*). */
 qa_status qa_q4_stats(qa_q4_cache *cache, uint64_t launches[QA_Q4_NUM_KERNELS]);
 
-/* Device bytes: codes and scale bytes, and scratch (workspace, sums of
- * parts, rotary table, error word). */
+/* Device bytes: codes and scale bytes, and the scratch that the cache comes to
+ * use: error word and rotary table (which other caches may share), and the
+ * workspace and the sums of parts, whether or not a call has taken them yet. */
 qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t *scratch_bytes);
 
 /* Static description of a status code. */
