@@ -21,13 +21,44 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <deque>
+#include <iterator>
 #include <mutex>
 #include <unordered_map>
 
 namespace qa {
+
+// A stream by what its handle stands for.  The legacy default stream (NULL, or
+// the handle 1) and the per-thread one (2) have the same handle on every device,
+// and the latter in every thread, but each device, and each thread, has its own.
+struct StreamRef {
+    uintptr_t handle;
+    uint64_t thread = 0;  // of the per-thread stream
+    int device;
+
+    StreamRef(const void *stream, int device_ = 0) : handle(reinterpret_cast<uintptr_t>(stream)), device(device_) {
+        if (handle == 1) handle = 0;
+        if (handle == 2) thread = this_thread();
+    }
+    bool operator==(const StreamRef &o) const {
+        return handle == o.handle && thread == o.thread && device == o.device;
+    }
+    struct Hash {
+        size_t operator()(const StreamRef &r) const {
+            return std::hash<uint64_t>()(r.handle ^ (r.thread << 40) ^ (static_cast<uint64_t>(r.device) << 56));
+        }
+    };
+
+  private:
+    static uint64_t this_thread() {  // ids are not used again, unlike the system's
+        static std::atomic<uint64_t> threads{0};
+        thread_local const uint64_t id = ++threads;
+        return id;
+    }
+};
 
 class LaunchOrder {
   public:
@@ -40,7 +71,7 @@ class LaunchOrder {
     // running append to the same (cache, layer).  early: the launch signals its
     // dependents before waiting for its predecessor.  resident_max: the most
     // thread blocks of this family the device holds at once.
-    int admit(const void *stream, const void *cache, int layer, int ctas, int tmax, bool early,
+    int admit(const StreamRef &stream, const void *cache, int layer, int ctas, int tmax, bool early,
               int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
         Hist &h = hist_[stream];
@@ -71,7 +102,7 @@ class LaunchOrder {
     // starts appends to (cache, layer): the same walk as admit, nothing recorded.
     // A launch for which this holds may read that layer's device lengths
     // before its own wait.
-    bool layer_settled(const void *stream, const void *cache, int layer, int64_t resident_max) {
+    bool layer_settled(const StreamRef &stream, const void *cache, int layer, int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
         auto found = hist_.find(stream);
         if (found == hist_.end()) return true;
@@ -89,7 +120,7 @@ class LaunchOrder {
     // What the next launch on `stream` may run beside: 0 nothing (no launch
     // recorded since the last barrier), 1 launches of other layers only, 2 a
     // launch that appends to (cache, layer).
-    int in_flight(const void *stream, const void *cache, int layer, int64_t resident_max) {
+    int in_flight(const StreamRef &stream, const void *cache, int layer, int64_t resident_max) {
         {
             std::lock_guard<std::mutex> lock(mu_);
             auto found = hist_.find(stream);
@@ -100,15 +131,17 @@ class LaunchOrder {
 
     // A kernel that never signals early was enqueued on `stream`, or the
     // stream was synchronised.
-    void barrier(const void *stream) {
+    void barrier(const StreamRef &stream) {
         std::lock_guard<std::mutex> lock(mu_);
         hist_.erase(stream);
     }
 
-    // The device was synchronised.
-    void clear() {
+    // The device was synchronised (kAllDevices: all of them).
+    static constexpr int kAllDevices = -1;
+    void clear(int device = kAllDevices) {
         std::lock_guard<std::mutex> lock(mu_);
-        hist_.clear();
+        for (auto it = hist_.begin(); it != hist_.end();)
+            it = device == kAllDevices || it->first.device == device ? hist_.erase(it) : std::next(it);
     }
 
     // Launches kept per stream; the walk needs at most resident_max of them.
@@ -125,7 +158,7 @@ class LaunchOrder {
         bool truncated = false;
     };
     std::mutex mu_;
-    std::unordered_map<const void *, Hist> hist_;
+    std::unordered_map<StreamRef, Hist, StreamRef::Hash> hist_;
 };
 
 }  // namespace qa

@@ -338,7 +338,8 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     // only after its own wait.
     int32_t *next = next_of(c, layer);
     const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
-    const bool settled = qa::launch_order().layer_settled(s, c, layer, resident);
+    const qa::StreamRef at(s, c->device);
+    const bool settled = qa::launch_order().layer_settled(at, c, layer, resident);
     bool follows = !a.pos_dev;
     for (int b = 0; b < batch && follows; ++b)
         if (tokens(b) > 0 && next[b] != a.start[b] + first) follows = false;
@@ -383,7 +384,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
         p.cluster = plan.cluster;
         p.mixed = plan.splits[nz - 1] != plan.cluster ? 1 : 0;
         p.early = !a.pos_dev && (settled || follows) ? 1 : 0;
-        const int guard = qa::launch_order().admit(s, c, layer, p.ctas, tm,
+        const int guard = qa::launch_order().admit(at, c, layer, p.ctas, tm,
                                                    p.early != 0, resident);
         p.guard = settled ? 0 : guard;
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
@@ -597,7 +598,7 @@ QA_API qa_status qa_q4_cache_free(qa_q4_cache *c) {
     if (!c) return QA_OK;
     DeviceScope dev(c->device);
     cudaDeviceSynchronize();
-    qa::launch_order().clear();
+    qa::launch_order().clear(c->device);
     free_all(c);
     delete c;
     return QA_OK;
@@ -639,7 +640,7 @@ QA_API qa_status qa_q4_append(qa_q4_cache *c, int layer, int batch, const int32_
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
         if (fill_ranges(p, g, s0, n, start, ntok, row0, unroll)) {
             if (qa::launch_q4_quantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier(s);
+            qa::launch_order().barrier({s, c->device});
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
         }
         for (int i = 0; i < n; ++i) {
@@ -675,7 +676,7 @@ QA_API qa_status qa_q4_read(qa_q4_cache *c, int layer, int batch, const int32_t 
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
         if (fill_ranges(p, g, s0, n, start, ntok, row0, 4)) {
             if (qa::launch_q4_dequantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier(s);
+            qa::launch_order().barrier({s, c->device});
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
         }
         for (int i = 0; i < n; ++i) row0 += ntok[s0 + i];
@@ -762,14 +763,14 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             if (pg.held.nblocks == 0) return true;
             pg.held.beside = beside ? 1 : 0;
             if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return false;
-            qa::launch_order().barrier(s);
+            qa::launch_order().barrier({s, c->device});
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
             return true;
         };
         if (fused) {
             pg.rows.k1.signal_early = 1;
             if (qa::launch_q4_prefill_rows(pg.rows, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier(s);
+            qa::launch_order().barrier({s, c->device});
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
             if (!older_rows(true)) {
                 cudaStreamSynchronize(s);  // as below
@@ -778,7 +779,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         } else {
             if (!older_rows(false)) return QA_ERR_CUDA;
             if (qa::launch_k1(pg.rows.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier(s);
+            qa::launch_order().barrier({s, c->device});
             c->launches[QA_Q4_KERNEL_NORM_ROPE]++;
             if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
@@ -794,7 +795,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             cudaStreamSynchronize(s);
             return QA_ERR_CUDA;
         }
-        qa::launch_order().barrier(s);
+        qa::launch_order().barrier({s, c->device});
         c->launches[QA_Q4_KERNEL_PREFILL_ATTN]++;
         return QA_OK;
     };
@@ -871,7 +872,7 @@ QA_API qa_status qa_q4_get_device_error(qa_q4_cache *c, uint32_t *detail) {
         cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
         return QA_ERR_CUDA;
-    qa::launch_order().clear();
+    qa::launch_order().clear(c->device);
     if (detail) *detail = word;
     switch (word & 0xffu) {
         case 0: return QA_OK;

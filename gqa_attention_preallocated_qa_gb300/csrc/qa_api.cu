@@ -51,8 +51,14 @@ struct qa_cache {
 namespace {
 
 // Launch ordering of the decode kernel family (launch_order.h): one record of
-// recent launches per stream, shared by every cache of the process.
+// recent launches per stream of a device, shared by every cache of the process.
 qa::LaunchOrder g_order;
+
+// After a synchronisation of the current device.
+void order_synchronised() {
+    int device = 0;
+    if (cudaGetDevice(&device) == cudaSuccess) g_order.clear(device);
+}
 
 // Failure-detection test hook (qa_debug_arm_wait_timeout): the kernel index
 // whose next launch withholds a copy (-1: none) and that launch's wait limit.
@@ -204,7 +210,7 @@ namespace {
 // loop over layers).
 int plan_overlap(const qa_cache *c, cudaStream_t stream, int layer, int64_t resident_max) {
     if (c->overlap_fixed) return c->overlap;
-    switch (g_order.in_flight(stream, c, layer, resident_max)) {
+    switch (g_order.in_flight({stream, c->device}, c, layer, resident_max)) {
         case 0: return 1;
         case 2: return std::min(2, c->overlap);
         default: return c->overlap;
@@ -306,7 +312,7 @@ qa_status run_k1(qa_cache *c, int layer, int batch, const int32_t *lens, const v
         p.signal_early = then_k2 ? 1 : 0;
         if (p.T > 0) {
             if (qa::launch_k1(p, D, s) != cudaSuccess) return QA_ERR_CUDA;
-            g_order.barrier(s);
+            g_order.barrier({s, c->device});
             c->launches[QA_KERNEL_NORM_ROPE_APPEND]++;
         }
         row0 += p.T;
@@ -390,7 +396,7 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
     for (auto &l : launches) {
         int tm = 0;
         for (int z = 0; z < l.first.B; ++z) tm = std::max(tm, l.second.ntok[z]);
-        l.first.guard = g_order.admit(s, c, layer, l.first.S * g.n_kv_heads * l.first.HG * l.first.B,
+        l.first.guard = g_order.admit({s, c->device}, c, layer, l.first.S * g.n_kv_heads * l.first.HG * l.first.B,
                                       tm, true, resident_max);
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
         l.first.fault = f.fault;
@@ -481,7 +487,7 @@ qa_status launch_k2s(qa_cache *c, std::vector<PrefillLaunch> &launches, cudaStre
         l.p.fault = f.fault;
         l.p.wait_ns = f.wait_ns;
         if (qa::launch_k2(l.p, c->cfg.head_dim, l.items, s) != cudaSuccess) return QA_ERR_CUDA;
-        g_order.barrier(s);
+        g_order.barrier({s, c->device});
         c->launches[QA_KERNEL_PREFILL_ATTN]++;
     }
     return QA_OK;
@@ -576,7 +582,7 @@ QA_API qa_status qa_cache_alloc(const qa_config *cfg, qa_cache **out) {
 QA_API qa_status qa_cache_free(qa_cache *c) {
     if (!c) return QA_OK;
     cudaDeviceSynchronize();
-    g_order.clear();
+    order_synchronised();
     free_all(c);
     delete c;
     return QA_OK;
@@ -589,7 +595,7 @@ QA_API qa_status qa_cache_reset(qa_cache *c, void *stream) {
     qa_reset_kernel<<<1, 256, 0, static_cast<cudaStream_t>(stream)>>>(c->lens_dev, n_lens,
                                                                        c->seq_cnt, g.max_batch);
     if (cudaGetLastError() != cudaSuccess) return QA_ERR_CUDA;
-    g_order.barrier(static_cast<cudaStream_t>(stream));
+    g_order.barrier({static_cast<cudaStream_t>(stream), c->device});
     c->launches[QA_KERNEL_RESET]++;
     std::fill(c->lens_host.begin(), c->lens_host.end(), 0);
     return QA_OK;
@@ -715,7 +721,7 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
     // otherwise it waits for its predecessor before reading them and nothing
     // overlaps.
     const bool settled =
-        dev_pos && g_order.layer_settled(static_cast<cudaStream_t>(stream), c, layer, resident_max);
+        dev_pos && g_order.layer_settled({stream, c->device}, c, layer, resident_max);
     p.dev_pos = dev_pos ? (settled ? 2 : 1) : 0;
     for (int b0 = 0; b0 < batch; b0 += qa::kK3MaxSeqPerLaunch) {
         const int nb = std::min(qa::kK3MaxSeqPerLaunch, batch - b0);
@@ -736,7 +742,7 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
                             dev_pos ? c->overlap
                                     : plan_overlap(c, static_cast<cudaStream_t>(stream), layer,
                                                    resident_max));
-        p.guard = g_order.admit(static_cast<cudaStream_t>(stream), c, layer,
+        p.guard = g_order.admit({stream, c->device}, c, layer,
                                 p.S * g.n_kv_heads * c->HG * nb, 1, !dev_pos || settled,
                                 resident_max);
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
@@ -791,7 +797,7 @@ QA_API qa_status qa_cache_sync_lengths(qa_cache *c, int layer, void *stream) {
                         sizeof(int32_t) * g.max_batch, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return QA_ERR_CUDA;
-    g_order.barrier(s);
+    g_order.barrier({s, c->device});
     return QA_OK;
 }
 
@@ -822,7 +828,7 @@ QA_API qa_status qa_cache_set_lengths(qa_cache *c, int layer, const int32_t *len
                         sizeof(int32_t) * g.max_batch, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return QA_ERR_CUDA;
-    g_order.barrier(s);
+    g_order.barrier({s, c->device});
     std::copy(lens_host, lens_host + g.max_batch,
               c->lens_host.begin() + static_cast<size_t>(layer) * g.max_batch);
     return QA_OK;
@@ -842,7 +848,7 @@ QA_API qa_status qa_get_device_error(qa_cache *c, uint32_t *detail) {
         cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
         return QA_ERR_CUDA;
-    g_order.clear();
+    order_synchronised();
     if (detail) *detail = word;
     switch (word & 0xffu) {
         case 0: return QA_OK;
