@@ -34,16 +34,23 @@ namespace qa {
 // A stream by what its handle stands for.  The legacy default stream (NULL, or
 // the handle 1) and the per-thread one (2) have the same handle on every device,
 // and the latter in every thread, but each device, and each thread, has its own.
+// `capture`: the id of the capture that the stream's launches go into (0: they
+// run).  Captured launches are ordered among themselves (a graph's first kernels
+// start after everything before its replay).  They do not end what the stream
+// still runs: a walk of its own launches passes over them, counting the rows
+// that they append as if they had run.
 struct StreamRef {
     uintptr_t handle;
     uint64_t thread = 0;  // of the per-thread stream
+    uint64_t capture;
     int device;
 
-    StreamRef(const void *stream, int device_ = 0) : handle(reinterpret_cast<uintptr_t>(stream)), device(device_) {
+    StreamRef(const void *stream, int device_ = 0, uint64_t capture_ = 0)
+        : handle(reinterpret_cast<uintptr_t>(stream)), capture(capture_), device(device_) {
         if (handle == 1) handle = 0;
         if (handle == 2) thread = this_thread();
     }
-    bool operator==(const StreamRef &o) const {
+    bool operator==(const StreamRef &o) const {  // the same stream
         return handle == o.handle && thread == o.thread && device == o.device;
     }
     struct Hash {
@@ -74,11 +81,12 @@ class LaunchOrder {
     int admit(const StreamRef &stream, const void *cache, int layer, int ctas, int tmax, bool early,
               int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
-        Hist &h = hist_[stream];
+        Hist &h = hist(stream);
         int64_t guard = 0, resident = 0;
         bool bounded = false;
         for (auto it = h.recs.rbegin(); it != h.recs.rend(); ++it) {
             if (it->cache == cache && it->layer == layer) guard += it->tmax;
+            if (it->passed) continue;
             if (!it->early) {  // it waited before signalling: nothing before it still runs
                 bounded = true;
                 break;
@@ -90,11 +98,8 @@ class LaunchOrder {
             }
         }
         if (!bounded && h.truncated) guard = kGuardAll;  // the older launches are not known
-        h.recs.push_back({cache, layer, std::max(ctas, 1), tmax, early});
-        if (h.recs.size() > kCap) {
-            h.recs.pop_front();
-            h.truncated = true;
-        }
+        h.add({cache, layer, std::max(ctas, 1), tmax, early, false});
+        if (stream.capture != 0) streams_[0][stream].add({cache, layer, 0, tmax, true, true});
         return static_cast<int>(std::min<int64_t>(guard, kGuardAll));
     }
 
@@ -104,12 +109,13 @@ class LaunchOrder {
     // before its own wait.
     bool layer_settled(const StreamRef &stream, const void *cache, int layer, int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
-        auto found = hist_.find(stream);
-        if (found == hist_.end()) return true;
-        const Hist &h = found->second;
+        const Hist *found = find(stream);
+        if (!found) return true;
+        const Hist &h = *found;
         int64_t resident = 0;
         for (auto it = h.recs.rbegin(); it != h.recs.rend(); ++it) {
             if (it->cache == cache && it->layer == layer) return false;
+            if (it->passed) continue;
             if (!it->early) return true;
             resident += it->ctas;
             if (resident + 1 > resident_max) return true;
@@ -123,8 +129,8 @@ class LaunchOrder {
     int in_flight(const StreamRef &stream, const void *cache, int layer, int64_t resident_max) {
         {
             std::lock_guard<std::mutex> lock(mu_);
-            auto found = hist_.find(stream);
-            if (found == hist_.end() || found->second.recs.empty()) return 0;
+            const Hist *found = find(stream);
+            if (!found || found->recs.empty()) return 0;
         }
         return layer_settled(stream, cache, layer, resident_max) ? 1 : 2;
     }
@@ -133,15 +139,16 @@ class LaunchOrder {
     // stream was synchronised.
     void barrier(const StreamRef &stream) {
         std::lock_guard<std::mutex> lock(mu_);
-        hist_.erase(stream);
+        if (find(stream)) streams_[stream.capture != 0].erase(stream);
     }
 
     // The device was synchronised (kAllDevices: all of them).
     static constexpr int kAllDevices = -1;
     void clear(int device = kAllDevices) {
         std::lock_guard<std::mutex> lock(mu_);
-        for (auto it = hist_.begin(); it != hist_.end();)
-            it = device == kAllDevices || it->first.device == device ? hist_.erase(it) : std::next(it);
+        auto &run = streams_[0];  // (a synchronisation cannot be part of a capture)
+        for (auto it = run.begin(); it != run.end();)
+            it = device == kAllDevices || it->first.device == device ? run.erase(it) : std::next(it);
     }
 
     // Launches kept per stream; the walk needs at most resident_max of them.
@@ -152,13 +159,34 @@ class LaunchOrder {
         const void *cache;
         int layer, ctas, tmax;
         bool early;
+        bool passed;  // captured, in the record of what the stream runs
     };
     struct Hist {
         std::deque<Rec> recs;
         bool truncated = false;
+        uint64_t capture = 0;
+        void add(const Rec &r) {
+            recs.push_back(r);
+            if (recs.size() > kCap) {
+                recs.pop_front();
+                truncated = true;
+            }
+        }
     };
+    const Hist *find(const StreamRef &stream) const {
+        const auto &map = streams_[stream.capture != 0];
+        const auto found = map.find(stream);
+        return found == map.end() || found->second.capture != stream.capture ? nullptr : &found->second;
+    }
+    Hist &hist(const StreamRef &stream) {
+        Hist &h = streams_[stream.capture != 0][stream];
+        if (h.capture != stream.capture) h = Hist{};  // of an earlier capture
+        h.capture = stream.capture;
+        return h;
+    }
     std::mutex mu_;
-    std::unordered_map<StreamRef, Hist, StreamRef::Hash> hist_;
+    // What each stream runs, and what goes into its capture.
+    std::unordered_map<StreamRef, Hist, StreamRef::Hash> streams_[2];
 };
 
 }  // namespace qa

@@ -338,7 +338,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     // only after its own wait.
     int32_t *next = next_of(c, layer);
     const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
-    const qa::StreamRef at(s, c->device);
+    const qa::StreamRef at = qa::stream_ref(s, c->device);
     const bool settled = qa::launch_order().layer_settled(at, c, layer, resident);
     bool follows = !a.pos_dev;
     for (int b = 0; b < batch && follows; ++b)
@@ -640,7 +640,7 @@ QA_API qa_status qa_q4_append(qa_q4_cache *c, int layer, int batch, const int32_
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
         if (fill_ranges(p, g, s0, n, start, ntok, row0, unroll)) {
             if (qa::launch_q4_quantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier({s, c->device});
+            qa::launch_order().barrier(qa::stream_ref(s, c->device));
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
         }
         for (int i = 0; i < n; ++i) {
@@ -676,7 +676,7 @@ QA_API qa_status qa_q4_read(qa_q4_cache *c, int layer, int batch, const int32_t 
         const int n = std::min(qa::kQ4MaxSeqPerLaunch, batch - s0);
         if (fill_ranges(p, g, s0, n, start, ntok, row0, 4)) {
             if (qa::launch_q4_dequantise(p, g.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier({s, c->device});
+            qa::launch_order().barrier(qa::stream_ref(s, c->device));
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
         }
         for (int i = 0; i < n; ++i) row0 += ntok[s0 + i];
@@ -758,19 +758,20 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     for (int b = 0; b < batch; ++b)
         if (!few_tokens(b)) next[b] = start[b] + ntok[b];
     const bool fused = qa::q4_prefill_rows_fits(c->cfg.n_q_heads, c->cfg.n_kv_heads, c->cfg.head_dim);
+    const qa::StreamRef at(s, c->device);  // (not being captured)
     auto launch = [&](PrefillGroup &pg) {
         auto older_rows = [&](bool beside) {
             if (pg.held.nblocks == 0) return true;
             pg.held.beside = beside ? 1 : 0;
             if (qa::launch_q4_dequantise(pg.held, c->cfg.head_dim, s) != cudaSuccess) return false;
-            qa::launch_order().barrier({s, c->device});
+            qa::launch_order().barrier(at);
             c->launches[QA_Q4_KERNEL_DEQUANTISE]++;
             return true;
         };
         if (fused) {
             pg.rows.k1.signal_early = 1;
             if (qa::launch_q4_prefill_rows(pg.rows, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier({s, c->device});
+            qa::launch_order().barrier(at);
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
             if (!older_rows(true)) {
                 cudaStreamSynchronize(s);  // as below
@@ -779,7 +780,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
         } else {
             if (!older_rows(false)) return QA_ERR_CUDA;
             if (qa::launch_k1(pg.rows.k1, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
-            qa::launch_order().barrier({s, c->device});
+            qa::launch_order().barrier(at);
             c->launches[QA_Q4_KERNEL_NORM_ROPE]++;
             if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
@@ -795,7 +796,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             cudaStreamSynchronize(s);
             return QA_ERR_CUDA;
         }
-        qa::launch_order().barrier({s, c->device});
+        qa::launch_order().barrier(at);
         c->launches[QA_Q4_KERNEL_PREFILL_ATTN]++;
         return QA_OK;
     };

@@ -111,6 +111,8 @@ bool encode_kv_map(CUtensorMap *m, void *base, int D, int L, int Hkv, int cap, i
 bool encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T);
 bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);
 LaunchOrder &launch_order();
+// `stream` of `device` as the launch record takes it now: captured or not.
+StreamRef stream_ref(cudaStream_t stream, int device);
 // Rotary table [capacity][D/2] of (cos, sin), in fp64, stored as fp32.
 void fill_rope_table(float2 *tab, int capacity, int D, float theta);
 

@@ -156,6 +156,18 @@ bool qa::encode_q_map(CUtensorMap *m, void *base, int D, int Hq, int T) {
 
 qa::LaunchOrder &qa::launch_order() { return g_order; }
 
+qa::StreamRef qa::stream_ref(cudaStream_t stream, int device) {
+    StreamRef r(stream, device);
+    if (r.handle == 0) return r;  // the legacy stream is never captured
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess)
+        cudaGetLastError();
+    else if (status == cudaStreamCaptureStatusActive)
+        r.capture = id;
+    return r;
+}
+
 bool qa::supported_geometry(int n_q_heads, int n_kv_heads, int head_dim) {
     if (head_dim != 64 && head_dim != 128) return false;
     if (n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads) return false;
@@ -208,9 +220,9 @@ namespace {
 // the rows they append are read only after the wait, so fewer launches overlap
 // usefully), and the cache's setting when only other layers' launches may (a
 // loop over layers).
-int plan_overlap(const qa_cache *c, cudaStream_t stream, int layer, int64_t resident_max) {
+int plan_overlap(const qa_cache *c, const qa::StreamRef &stream, int layer, int64_t resident_max) {
     if (c->overlap_fixed) return c->overlap;
-    switch (g_order.in_flight({stream, c->device}, c, layer, resident_max)) {
+    switch (g_order.in_flight(stream, c, layer, resident_max)) {
         case 0: return 1;
         case 2: return std::min(2, c->overlap);
         default: return c->overlap;
@@ -312,7 +324,7 @@ qa_status run_k1(qa_cache *c, int layer, int batch, const int32_t *lens, const v
         p.signal_early = then_k2 ? 1 : 0;
         if (p.T > 0) {
             if (qa::launch_k1(p, D, s) != cudaSuccess) return QA_ERR_CUDA;
-            g_order.barrier({s, c->device});
+            g_order.barrier(qa::stream_ref(s, c->device));
             c->launches[QA_KERNEL_NORM_ROPE_APPEND]++;
         }
         row0 += p.T;
@@ -371,7 +383,8 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
     qa::K3Multi m{};
     int nz = 0, row = 0, pos_max = 0;
     const int resident_max = qa::k3_max_resident_ctas();
-    const int ov = plan_overlap(c, s, layer, resident_max);
+    const qa::StreamRef at = qa::stream_ref(s, c->device);
+    const int ov = plan_overlap(c, at, layer, resident_max);
     auto flush = [&]() {
         if (nz == 0) return;
         p.B = nz;
@@ -396,7 +409,7 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
     for (auto &l : launches) {
         int tm = 0;
         for (int z = 0; z < l.first.B; ++z) tm = std::max(tm, l.second.ntok[z]);
-        l.first.guard = g_order.admit({s, c->device}, c, layer, l.first.S * g.n_kv_heads * l.first.HG * l.first.B,
+        l.first.guard = g_order.admit(at, c, layer, l.first.S * g.n_kv_heads * l.first.HG * l.first.B,
                                       tm, true, resident_max);
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
         l.first.fault = f.fault;
@@ -487,7 +500,7 @@ qa_status launch_k2s(qa_cache *c, std::vector<PrefillLaunch> &launches, cudaStre
         l.p.fault = f.fault;
         l.p.wait_ns = f.wait_ns;
         if (qa::launch_k2(l.p, c->cfg.head_dim, l.items, s) != cudaSuccess) return QA_ERR_CUDA;
-        g_order.barrier({s, c->device});
+        g_order.barrier(qa::stream_ref(s, c->device));
         c->launches[QA_KERNEL_PREFILL_ATTN]++;
     }
     return QA_OK;
@@ -595,7 +608,7 @@ QA_API qa_status qa_cache_reset(qa_cache *c, void *stream) {
     qa_reset_kernel<<<1, 256, 0, static_cast<cudaStream_t>(stream)>>>(c->lens_dev, n_lens,
                                                                        c->seq_cnt, g.max_batch);
     if (cudaGetLastError() != cudaSuccess) return QA_ERR_CUDA;
-    g_order.barrier({static_cast<cudaStream_t>(stream), c->device});
+    g_order.barrier(qa::stream_ref(static_cast<cudaStream_t>(stream), c->device));
     c->launches[QA_KERNEL_RESET]++;
     std::fill(c->lens_host.begin(), c->lens_host.end(), 0);
     return QA_OK;
@@ -715,13 +728,14 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
             if (mirror[b] + 1 > g.capacity) return QA_ERR_CAPACITY;
     K3Params p = make_k3(c, layer, q, k, v, q_norm_w, k_norm_w, out);
     const int64_t resident_max = qa::k3_max_resident_ctas();
+    const qa::StreamRef at = qa::stream_ref(static_cast<cudaStream_t>(stream), c->device);
     // Device positions: when no launch that may still be running writes this
     // layer (a multi-layer loop, e.g. a captured layer stack), the kernel reads
     // them at once and overlaps its predecessor like a host-position step;
     // otherwise it waits for its predecessor before reading them and nothing
     // overlaps.
     const bool settled =
-        dev_pos && g_order.layer_settled({stream, c->device}, c, layer, resident_max);
+        dev_pos && g_order.layer_settled(at, c, layer, resident_max);
     p.dev_pos = dev_pos ? (settled ? 2 : 1) : 0;
     for (int b0 = 0; b0 < batch; b0 += qa::kK3MaxSeqPerLaunch) {
         const int nb = std::min(qa::kK3MaxSeqPerLaunch, batch - b0);
@@ -740,9 +754,8 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
         // eagerly agree bit for bit.  Host positions: the plan follows the stream.
         p.S = choose_splits(c, nb, pos_max,
                             dev_pos ? c->overlap
-                                    : plan_overlap(c, static_cast<cudaStream_t>(stream), layer,
-                                                   resident_max));
-        p.guard = g_order.admit({stream, c->device}, c, layer,
+                                    : plan_overlap(c, at, layer, resident_max));
+        p.guard = g_order.admit(at, c, layer,
                                 p.S * g.n_kv_heads * c->HG * nb, 1, !dev_pos || settled,
                                 resident_max);
         const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
@@ -797,7 +810,7 @@ QA_API qa_status qa_cache_sync_lengths(qa_cache *c, int layer, void *stream) {
                         sizeof(int32_t) * g.max_batch, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return QA_ERR_CUDA;
-    g_order.barrier({s, c->device});
+    g_order.barrier(qa::stream_ref(s, c->device));
     return QA_OK;
 }
 
@@ -828,7 +841,7 @@ QA_API qa_status qa_cache_set_lengths(qa_cache *c, int layer, const int32_t *len
                         sizeof(int32_t) * g.max_batch, cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return QA_ERR_CUDA;
-    g_order.barrier({s, c->device});
+    g_order.barrier(qa::stream_ref(s, c->device));
     std::copy(lens_host, lens_host + g.max_batch,
               c->lens_host.begin() + static_cast<size_t>(layer) * g.max_batch);
     return QA_OK;

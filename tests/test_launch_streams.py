@@ -1,7 +1,8 @@
 """The launch record (csrc/launch_order.h) keeps streams apart that share a handle,
 on the CPU through a small driver built with g++: the default streams of two
 devices, and the per-thread default streams of two threads.  What is recorded for
-one must leave the guard of the other's launches alone."""
+one must leave the guard of the other's launches alone.  Nor do launches that go
+into a graph end what the stream that captures them still runs."""
 import os
 import shutil
 import subprocess
@@ -53,3 +54,23 @@ def test_each_thread_has_its_own_per_thread_stream(driver):
     assert driver("admit 2 0 0 10", "admit 2 0 1 304", "admit 2 0 0 10") == [0, 0, 1]
     # any other stream is the same in every thread
     assert driver("admit 77 0 0 10", "settled 77 0 1", "barrier 77 0 1", "settled 77 0 0") == [0, 0, 1]
+
+
+def test_captured_launches_do_not_hide_what_the_stream_still_runs(driver):
+    # 304 captured blocks, and a captured kernel that never signals early, between
+    # two steps of one layer that run: the second's guard still counts the first
+    # (and the captured step's row)
+    run, captured = "77 0 0", "77 0 0 {} 5"
+    assert driver(f"admit {run} 10", f"admit {captured.format(304)}", f"settled {run}", f"admit {run} 10") == [0, 0, 0, 2]
+    assert driver(f"admit {run} 10", f"barrier {captured.format(0)}", f"settled {run}", f"admit {run} 10") == [0, 0, 1]
+
+
+def test_captured_launches_are_ordered_among_themselves(driver):
+    first, second = "77 0 0 {} 5", "77 0 0 {} 6"
+    assert driver("admit 77 0 0 10", f"settled {first.format(0)}", *[f"admit {first.format(10)}"] * 3,
+                  f"settled {first.format(0)}", f"barrier {first.format(0)}", f"admit {first.format(10)}") == [0, 1, 0, 1, 2, 0, 0]
+    # the next capture on the stream starts anew
+    assert driver(f"admit {first.format(10)}", f"settled {second.format(0)}", f"barrier {second.format(0)}",
+                  f"admit {second.format(10)}", f"admit {second.format(10)}") == [0, 1, 0, 1]
+    # a synchronisation is of what runs
+    assert driver(f"admit {first.format(10)}", "admit 77 0 0 10", "clear 0", f"settled {first.format(0)}", "settled 77 0 0") == [0, 1, 0, 1]
