@@ -249,10 +249,10 @@ struct Q4Lane {
 
 // One chunk of 32 keys, its codes of K at shared address `codes` and their scale
 // bytes at `scales`.  kMask: keys [klo[x], nk) are seen by row 2c + x, [kvlo, nk) by any
-// row; else every row sees all 32.
+// row, and those from khi on by all; else every row sees all 32.
 template <int D, int R, bool kMask>
 __device__ __forceinline__ void q4_consume(uint32_t codes, uint32_t scales, const Q4Lane &at, int nk, const int (&klo)[2], int kvlo,
-                                           const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
+                                           int khi, const uint32_t (&qb)[D / 16][2], const float (&cs)[2],
                                            Q4Acc<D> &a, int lane) {
     using Sh = Q4Shape<D, R>;
     const unsigned FULL = 0xffffffffu;
@@ -345,12 +345,18 @@ __device__ __forceinline__ void q4_consume(uint32_t codes, uint32_t scales, cons
         uint32_t bb = lds8<Sh::kScales + 2 * ks * kScaleBlock>(scales + at.vsb);
         uint32_t bc = lds8<Sh::kScales + (2 * ks + 1) * kScaleBlock>(scales + at.vsa);
         uint32_t bd = lds8<Sh::kScales + (2 * ks + 1) * kScaleBlock>(scales + at.vsb);
-        if (kMask) {  // rows that no query row sees may hold anything: a zero scale drops them
+        if (kMask) {
+            // Rows that no query row sees may hold anything: a zero scale drops them.
+            // So it does groups that are not finite of rows that only some see, as a
+            // weight of zero would not; the caller makes the outputs NaN that see them.
             const int ka = ks * 16 + q4_key(2 * c), kb = ks * 16 + q4_key(2 * c + 1);
-            if (ka >= nk || ka < kvlo) ba = 0;
-            if (kb >= nk || kb < kvlo) bb = 0;
-            if (ka + 8 >= nk || ka + 8 < kvlo) bc = 0;
-            if (kb + 8 >= nk || kb + 8 < kvlo) bd = 0;
+            auto kept = [&](uint32_t byte, int key) {
+                return key >= nk || key < kvlo || (key < khi && (byte & 0x7Cu) == 0x7Cu) ? 0u : byte;
+            };
+            ba = kept(ba, ka);
+            bb = kept(bb, kb);
+            bc = kept(bc, ka + 8);
+            bd = kept(bd, kb + 8);
         }
         const Q4Scale s0 = q4_scale2(__byte_perm(ba, bb, 0x4101));
         const Q4Scale s1 = q4_scale2(__byte_perm(bc, bd, 0x4101));
@@ -376,10 +382,29 @@ __device__ __forceinline__ void q4_consume(uint32_t codes, uint32_t scales, cons
     values(std::integral_constant<int, 1>{});
 }
 
-template <int D, int HPC, int TPS>
+// Rows [from, to) of a chunk (its scale bytes of V at `scales`) whose group that
+// this lane's outputs belong to is not finite, as bits.
+template <int D>
+__device__ __forceinline__ uint32_t q4_not_finite(uint32_t scales, int from, int to, int lane) {
+    constexpr int GR = D / kQ4Group;
+    const int mine = D == 128 ? lane >> 3 : lane >> 4;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int g = 0; g < GR; ++g) {
+        const bool odd = lane >= from && lane < to && (lds8<0>(scales + lane * GR + g) & 0x7Cu) == 0x7Cu;
+        const uint32_t rows = __ballot_sync(0xffffffffu, odd);
+        if (g == mine) bad = rows;
+    }
+    return bad;
+}
+
+// kSlide: several tokens under a window, whose windows start at different rows
+// (a form of its own: its masks cost the others 2 %).
+template <int D, int HPC, int TPS, bool kSlide>
 __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     q4_decode_kernel(const __grid_constant__ Q4DecodeParams p) {
     constexpr int R = HPC * TPS;
+    static_assert(TPS > 1 || !kSlide, "one token has one window");
     static_assert(R <= 8, "query rows are the 8 columns of the MMA tile");
     using Sh = Q4Shape<D, R>;
     constexpr int NW = kQ4DecodeWarps, NS = Sh::kStages, LPR = D / 8;
@@ -675,7 +700,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                 const bool whole = base + kQ4Chunk <= pos && (p.window <= 0 || lo0 + ntok - 1 <= 0);
                 if (whole) {
                     const int none[2] = {0, 0};
-                    q4_consume<D, R, false>(codes, scales, at, kQ4Chunk, none, 0, qb, cs, a, lane);
+                    q4_consume<D, R, false>(codes, scales, at, kQ4Chunk, none, 0, 0, qb, cs, a, lane);
                 } else {
                     int klo[2] = {0, 0};
                     if (p.window > 0) {
@@ -685,8 +710,22 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
                             klo[x] = min(kQ4Chunk, max(0, lo0 + t));
                         }
                     }
-                    q4_consume<D, R, true>(codes, scales, at, min(kQ4Chunk, pos - base), klo,
-                                           max(0, key_lo - base), qb, cs, a, lane);
+                    const int nk = min(kQ4Chunk, pos - base), kvlo = max(0, key_lo - base);
+                    int khi = 0;
+                    uint32_t bad = 0;  // rows that some tokens see, whose values of this lane's dims are not finite
+                    if (kSlide) {
+                        khi = min(nk, lo0 + ntok - 1);
+                        if (khi > kvlo) bad = q4_not_finite<D>(scales + Sh::kScales, kvlo, khi, lane);
+                    }
+                    q4_consume<D, R, true>(codes, scales, at, nk, klo, kvlo, khi, qb, cs, a, lane);
+                    if (kSlide && bad != 0u) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (klo[x] < kQ4Chunk && bad >> klo[x] != 0u) {
+#pragma unroll
+                                for (int t = 0; t < D / 16; ++t) a.o[t][x] = a.o[t][2 + x] = __int_as_float(0x7fffffff);
+                            }
+                    }
                 }
             }
             __syncwarp();
@@ -848,16 +887,24 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 }
 
 // ------------------------------------------------------------------ launch
+template <int D, int HPC, int TPS, bool kSlide>
+static cudaError_t q4_configure_form() {
+    auto kern = q4_decode_kernel<D, HPC, TPS, kSlide>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Q4Shape<D, HPC * TPS>::kSmemBytes);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    return e;
+}
+
+// Both forms at once: a window may be set between a call and its capture.
 template <int D, int HPC, int TPS>
 static cudaError_t q4_configure() {
-    auto kern = q4_decode_kernel<D, HPC, TPS>;
     static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 32 && ((configured.load(std::memory_order_acquire) >> dev) & 1u)) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Q4Shape<D, HPC * TPS>::kSmemBytes);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = q4_configure_form<D, HPC, TPS, false>();
+    if (e == cudaSuccess && TPS > 1) e = q4_configure_form<D, HPC, TPS, (TPS > 1)>();
     if (e == cudaSuccess && dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
     return e;
 }
@@ -888,9 +935,11 @@ static cudaError_t q4_launch(const Q4DecodeParams &p, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const dim3 grid = p.mixed ? dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster) : dim3(p.cluster, p.groups, p.B);
     q4_config<D, HPC, TPS>(cfg, attr, p.cluster, grid, stream);
-    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, HPC, TPS>, p);
+    if (TPS > 1 && p.window > 0) return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, HPC, TPS, (TPS > 1)>, p);
+    return cudaLaunchKernelEx(&cfg, q4_decode_kernel<D, HPC, TPS, false>, p);
 }
 
+// (Of the form without a window; the other takes the same registers and shared memory.)
 template <int D, int HPC, int TPS>
 static const int *q4_capacities() {
     static int table[32][kQ4MaxSplits + 1];
@@ -906,7 +955,7 @@ static const int *q4_capacities() {
         cudaLaunchAttribute attr[2];
         q4_config<D, HPC, TPS>(cfg, attr, S, dim3(S), nullptr);
         cfg.numAttrs = 1;
-        failed = cudaOccupancyMaxActiveClusters(&table[dev][S], q4_decode_kernel<D, HPC, TPS>, &cfg) != cudaSuccess;
+        failed = cudaOccupancyMaxActiveClusters(&table[dev][S], q4_decode_kernel<D, HPC, TPS, false>, &cfg) != cudaSuccess;
     }
     if (failed) {
         cudaGetLastError();
