@@ -108,12 +108,13 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
     const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.codes[t.kv]) + row * (D / 8);
     const uint8_t *scales = p.scales[t.kv] + row * GR;
     __nv_bfloat16 *dst = p.dst[t.kv] + p.dst_off[t.z] + t.h * p.dst_head;
+    const int hidden = p.hidden[t.z] - p.start[t.z] - t.tok0;  // rows of the block that nothing may see
     uint32_t w[kU], s[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const int i = half * kU + u;
-        w[u] = s[u] = 0;
-        if (i < t.n) {
+        w[u] = s[u] = 0;  // (a scale of zero: zeros)
+        if (i < t.n && i >= hidden) {
             w[u] = codes[static_cast<int64_t>(i) * LPR + sub];
             s[u] = scales[i * GR + sub / 4];
         }

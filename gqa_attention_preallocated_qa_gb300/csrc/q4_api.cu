@@ -451,7 +451,9 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     pg.rows.seq0 = s0;
     fill_ranges(pg.quant, g, s0, n, start, ntok, 0, 8);
     // The rows before them that a new token sees, from the first row of the
-    // 128-key tile that holds the first one.
+    // 128-key tile that holds the first one.  Those of the tile that none sees may
+    // hold anything, and the attention kernel multiplies them by weights of zero:
+    // they are zeros in the workspace.
     pg.held = make_rows(c, layer);
     int32_t from[qa::kMaxSeqPerLaunch], count[qa::kMaxSeqPerLaunch];
     for (int i = 0; i < n; ++i) {
@@ -460,6 +462,10 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         count[i] = ntok[s0 + i] > 0 ? P - from[i] : 0;
     }
     fill_ranges(pg.held, g, 0, n, from, count, 0, 4);
+    for (int i = 0; i < n; ++i) {
+        const int W = c->window[layer];
+        pg.held.hidden[i] = W > 0 ? std::max(0, start[s0 + i] + 1 - W) : 0;
+    }
     pg.held.seq0 = s0;
     for (qa::Q4RowsParams *r : {&pg.quant, &pg.held}) {
         r->src_tok = r->dst_tok = D;

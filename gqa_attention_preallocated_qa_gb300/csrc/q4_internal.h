@@ -37,6 +37,7 @@ struct Q4RowsParams {
     int seq0;                            // cache slot of launched sequence 0
     int beside;                          // dequantise: starts beside the kernel before it, signals at once
     int start[kQ4MaxSeqPerLaunch], ntok[kQ4MaxSeqPerLaunch];
+    int hidden[kQ4MaxSeqPerLaunch];      // dequantise: rows below this position come out as zeros
     int block0[kQ4MaxSeqPerLaunch + 1];  // first token block of each launched sequence
     int64_t src_off[kQ4MaxSeqPerLaunch], dst_off[kQ4MaxSeqPerLaunch];
 };

@@ -445,9 +445,10 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * cache's workspace, up to 8 sequences at a time: calls with such sequences on
  * several streams wait for each other, and they cannot be captured into a
  * graph (QA_ERR_STATE).  In that form a key or value
- * that is not finite can reach other new tokens of its sequence in the call,
- * also those before it (as in qa_prefill: the tensor cores multiply it by their
- * weight of zero).
+ * that is not finite and that some new token of the call sees can reach the
+ * others of its sequence, also those before it (as in qa_prefill: the tensor
+ * cores multiply it by their weight of zero).  Otherwise what a token does not
+ * see reaches none of its outputs, whatever it holds.
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
 qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
                         const int32_t *ntok, const void *q, const void *k, const void *v,

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import f64
-from test_gpu_q4 import DECODE_BITS, Cache, close
+from test_gpu_q4 import DECODE_BITS, PREFILL_BITS, Cache, close
 
 pytestmark = pytest.mark.gpu
 NAN = 0x7F
@@ -55,3 +55,31 @@ def test_a_row_that_only_the_first_tokens_of_a_chunk_see(qa, hq, hkv, d, ntok, k
         assert torch.equal(nan[:half], seen.expand(half, hq, d))
         assert not nan[half:].any()
         close(out[half:], want[half:], mag[half:], DECODE_BITS)
+
+
+@pytest.mark.parametrize("hq,hkv,d,start,ntok,window", [
+    (8, 2, 128, [300, 140], [200, 77], 150),
+    (32, 8, 128, [1000] * 4, [300, 140, 129, 400], 200),
+    (16, 8, 64, [900, 700], [300, 40], 170),
+    (8, 2, 128, [5000], [100], 3000),          # keys in parts
+    (24, 3, 128, [500, 90], [60, 200], 130),   # the transform kernel and a quantiser after it
+])
+@pytest.mark.parametrize("kv", ["k", "v"])
+def test_rows_below_every_window_of_a_prefill(qa, hq, hkv, d, start, ntok, window, kv):
+    # They may never have been written: NaN scales up to the row before the first
+    # token's window, which lies inside a tile of 128 keys.
+    with Cache(qa, 1, len(start), hq, hkv, d, max(s + n for s, n in zip(start, ntok))) as c:
+        qa.qa_q4_cache_set_window(c.h, 0, window)
+        c.fill(0, start, 5)
+        for b, s in enumerate(start):
+            for i in ((1,) if kv == "k" else (3,)):
+                c.views()[i][b, :, :max(0, s + 1 - window)] = NAN
+        q, k, v = c.tokens(ntok, 6)
+        out = torch.empty_like(q)
+        qa.qa_q4_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        assert qa.qa_q4_stats(c.h)["prefill_attn"] > 0
+        qp, kp = c.transform(start, ntok, q, k, v)
+        c.note(0, start, ntok, kp, f64(v))
+        want, mag = c.want(start, ntok, qp, window=window)
+        close(out, want, mag, PREFILL_BITS)
