@@ -1,6 +1,8 @@
 """Builds ``libqa.so`` (the C ABI of include/qa.h) in-tree with nvcc for sm_103a,
-and beside it ``_q4calls.so``, the binding's native marshalling of the calls
-that are made once per layer and token.
+and beside it ``_q4calls``, the binding's native marshalling of the calls that
+are made once per layer and token, under the name that this interpreter gives
+its extension modules.  Where g++ or Python's headers are missing the library is
+built alone; the binding then lacks those calls.
 
 Each .cu file compiles to an object in parallel; the objects link into one
 shared library with the CUDA runtime linked statically, so the library loads
@@ -14,6 +16,7 @@ import shutil
 import subprocess
 import sysconfig
 import threading
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqa.so")
-CALLS = os.path.join(PKG, "_q4calls.so")
+CALLS = os.path.join(PKG, "_q4calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["qa_api.cu", "k1_norm_rope_append.cu", "k2_prefill_tcgen05.cu", "k3_decode_splitkv.cu",
            "q4_api.cu", "k4_q4_rows.cu", "k5_q4_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +45,19 @@ def _inputs():
     return files
 
 
+def _cxx() -> str | None:
+    return os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+
+
+def can_build_calls() -> bool:
+    return bool(_cxx()) and os.path.exists(os.path.join(sysconfig.get_path("include"), "Python.h"))
+
+
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    made = [LIB] + ([CALLS] if can_build_calls() else [])
+    if not all(os.path.exists(f) for f in made):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(f) for f in made)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -63,12 +75,12 @@ def _compile(src: str, extra) -> str:
 
 
 def _build_calls() -> None:
-    """_q4calls.so: plain C++ against this interpreter's headers, no CUDA."""
-    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
-    if not cxx:
-        raise RuntimeError("g++ not found: it is required to build _q4calls.so")
+    """_q4calls: plain C++ against this interpreter's headers, no CUDA."""
+    if not can_build_calls():
+        warnings.warn("g++ or Python.h not found: the binding will lack the 4-bit cache's per-token calls")
+        return
     tmp = CALLS + f".tmp{os.getpid()}"
-    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-fwrapv",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-fwrapv",
            "-I", sysconfig.get_path("include"), os.path.join(CSRC, "q4_calls.cpp"), "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -77,7 +89,7 @@ def _build_calls() -> None:
 
 
 def build(force: bool = False, extra=()) -> str:
-    """Compile and link libqa.so and _q4calls.so if any source changed (or ``force``)."""
+    """Compile and link libqa.so and _q4calls if any source changed (or ``force``)."""
     with _lock:
         if not force and not stale():
             return LIB

@@ -3,13 +3,14 @@
 Argument marshalling only: tensors are passed as device pointers (torch
 tensors or plain integers), host arrays as int32 buffers, streams as
 cudaStream_t handles.  Every step of the path runs in the library's kernels.
-The 4-bit cache's per-token calls are marshalled by ``_q4calls.so`` instead.
+The 4-bit cache's per-token calls are marshalled by ``_q4calls`` instead.
 Importing this module loads the library and raises ImportError if it has not
-been built; there is no fallback.
+been built; there is no fallback.  Without ``_q4calls`` those calls alone raise it.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import _build
@@ -108,7 +109,31 @@ def _load():
 
 lib = _load()
 
-from . import _q4calls  # noqa: E402  (built beside the library)
+
+class _NoCalls:
+    """In the place of _q4calls: its calls say why there is none."""
+
+    def __init__(self, why):
+        self.why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the 4-bit cache's per-token calls need _q4calls: {self.why}")
+
+
+def _load_calls():
+    """csrc/q4_calls.cpp as built for this interpreter (and no other's)."""
+    if not os.path.exists(_build.CALLS):
+        return _NoCalls(f"{_build.CALLS} is missing: build it with __graft_entry__.build()")
+    spec = importlib.util.spec_from_file_location(__package__ + "._q4calls", _build.CALLS)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return _NoCalls(str(e))
+    return module
+
+
+_q4calls = _load_calls()
 
 
 def _ptr(x) -> int | None:
@@ -320,7 +345,8 @@ def _bind_calls(current_stream) -> None:
                                  "qa_q4_decode_step_device_positions")), current_stream)
 
 
-_bind_calls(_current_stream)  # replaced by what it finds at the first call
+if not isinstance(_q4calls, _NoCalls):
+    _bind_calls(_current_stream)  # replaced by what it finds at the first call
 
 
 def qa_q4_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
