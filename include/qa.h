@@ -380,10 +380,14 @@ qa_status qa_noalloc_get_device_error(uint32_t *detail, void *stream);
  * Conventions as above; a call on more than 64 sequences is several launches,
  * and an error of a later one leaves the earlier ones enqueued.  Calls may be
  * made with another device current; the
- * stream belongs to the cache's device.  Row kernels and prefill are ordered
- * on their stream like plain launches; decode steps overlap the previous
- * kernel like qa_decode_step, with the same condition on q, k, v and the
- * weights, and on other code's kernels between the calls. */
+ * stream belongs to the cache's device.  qa_q4_append and qa_q4_read are
+ * ordered on their stream like plain launches.  Decode steps, and in a prefill
+ * the sequences of few tokens (qa_q4_prefill says which), overlap earlier
+ * kernels of the stream like qa_decode_step, with the same condition on other
+ * code's kernels between the calls.  They read q, k, v and the weights before
+ * an earlier decode step or prefill has finished: what such a call writes (out,
+ * k_held, v_held) is no input of a later one unless another kernel or copy on
+ * the stream lies between them. */
 typedef struct qa_q4_cache qa_q4_cache; /* opaque */
 
 /* Kernels counted by qa_q4_stats. */
@@ -441,14 +445,14 @@ qa_status qa_q4_read(qa_q4_cache *cache, int layer, int batch, const int32_t *st
  * held, too), within the layer's window.
  * Sequences with few new tokens (up to 16; up to 24 behind 512 cached
  * positions, at most a window of which count) take the decode kernel, 8 tokens
- * a launch, one launch per 64 sequences.  The others take K4 and K2 through the
- * cache's workspace, up to 8 sequences at a time: calls with such sequences on
- * several streams wait for each other, and they cannot be captured into a
- * graph (QA_ERR_STATE).  In that form a key or value
- * that is not finite and that some new token of the call sees can reach the
- * others of its sequence, also those before it (as in qa_prefill: the tensor
- * cores multiply it by their weight of zero).  Otherwise what a token does not
- * see reaches none of its outputs, whatever it holds.
+ * a launch, one launch per 64 sequences, with a decode step's condition on the
+ * inputs.  The others take K4 and K2 through the cache's workspace, up to 8
+ * sequences at a time: calls with such sequences on several streams wait for
+ * each other, and they cannot be captured into a graph (QA_ERR_STATE).  In that
+ * form a key or value that is not finite and that some new token of the call
+ * sees can reach the others of its sequence, also those before it (as in
+ * qa_prefill: the tensor cores multiply it by their weight of zero).  Otherwise
+ * what a token does not see reaches none of its outputs, whatever it holds.
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
 qa_status qa_q4_prefill(qa_q4_cache *cache, int layer, int batch, const int32_t *start,
                         const int32_t *ntok, const void *q, const void *k, const void *v,

@@ -92,3 +92,36 @@ def test_the_border_between_the_two_kernels(qa, start, ntok, window, decode):
         stats = qa.qa_q4_stats(c.h)
         assert (stats["decode"], stats["prefill_attn"]) == (decode, 0 if decode else 1)
         close(out, want, mag, DECODE_BITS if decode else PREFILL_BITS)
+
+
+@pytest.mark.parametrize("ntok", [1, 4, 16, 17])
+def test_an_output_copied_into_the_next_calls_inputs(qa, ntok):
+    # A chain of calls, each one's queries, keys and values made of the last one's
+    # outputs by kernels in between, with nothing else that waits: the same bits as
+    # with a synchronisation after every call.
+    layers, n = 3, [ntok, ntok]
+    with Cache(qa, layers, 2, 8, 2, 128, 700 + 6 * ntok) as c:
+        q0, k0, v0 = c.tokens(n, 6)
+        got = []
+        for wait in (False, True):
+            for layer in range(layers):
+                c.fill(layer, [600, 600], 5)
+            q, k, v, out = q0.clone(), k0.clone(), v0.clone(), torch.empty_like(q0)
+            outs = []
+            torch.cuda.synchronize()
+            for i in range(6):
+                for layer in range(layers):
+                    at = [600 + i * ntok] * 2
+                    if ntok == 1:
+                        qa.qa_q4_decode_step(c.h, layer, at, q, k, v, c.wq, c.wk, out)
+                    else:
+                        qa.qa_q4_prefill(c.h, layer, at, n, q, k, v, c.wq, c.wk, out)
+                    q.copy_(out)
+                    k.copy_(out[:, :2])
+                    v.copy_(out[:, 2:4])
+                    outs.append(out.clone())
+                    if wait:
+                        torch.cuda.synchronize()
+            got.append(outs)
+        assert qa.qa_q4_get_device_error(c.h) == (0, 0)
+        assert all(torch.equal(a, b) for a, b in zip(*got))
