@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
 // the tokens with the next token's rows on the way into the other half of its
 // ring (three bulk copies), as K1 does.
 // RMSNorm + RoPE of this lane's 8 values of a row held by D/8 lanes; cs, sn:
-// cosines and sines of its dims, the sines signed for its half.
+// cosines and sines of its dims, the sines signed for its half.  Its sums are in the
+// order of q4_norm_rope (K5): a key gets the same codes from a prefill and from a
+// decode step.
 template <int D>
 __device__ __forceinline__ uint4 q4_transform(uint4 xv, uint4 wv, const float2 (&cs)[4],
                                               const float2 (&sn)[4], float eps) {

@@ -179,7 +179,9 @@ struct Q4Row {
     float4 cs[4];
 };
 
-// RMSNorm + RoPE of a row, with the roundings of the bf16 path.
+// RMSNorm + RoPE of a row, with the roundings of the bf16 path.  Its sums are in
+// the order of q4_transform (K4): a key gets the same codes from a decode step and
+// from a prefill.
 template <int D>
 __device__ __forceinline__ uint4 q4_norm_rope(const Q4Row &row, float eps, int sub) {
     constexpr int HALF = D / 16;
@@ -965,16 +967,16 @@ static const int *q4_capacities() {
     return table[dev];
 }
 
-// Calls f<D, HPC, TPS>(args...) for the run-time shape.
+// Calls f<D, HPC, TPS>(args...) for the run-time shape (8 heads: one token alone).
 #define QA_Q4_DISPATCH(f, ...)                                             \
     do {                                                                   \
         if (D == 128) {                                                    \
-            if (HPC == 8) return multi ? f<128, 8, 1>(__VA_ARGS__) : f<128, 8, 1>(__VA_ARGS__); \
+            if (HPC == 8) return f<128, 8, 1>(__VA_ARGS__);                 \
             if (HPC == 4) return multi ? f<128, 4, 2>(__VA_ARGS__) : f<128, 4, 1>(__VA_ARGS__); \
             if (HPC == 2) return multi ? f<128, 2, 4>(__VA_ARGS__) : f<128, 2, 1>(__VA_ARGS__); \
             if (HPC == 1) return multi ? f<128, 1, 8>(__VA_ARGS__) : f<128, 1, 1>(__VA_ARGS__); \
         } else if (D == 64) {                                              \
-            if (HPC == 8) return multi ? f<64, 8, 1>(__VA_ARGS__) : f<64, 8, 1>(__VA_ARGS__); \
+            if (HPC == 8) return f<64, 8, 1>(__VA_ARGS__);                  \
             if (HPC == 4) return multi ? f<64, 4, 2>(__VA_ARGS__) : f<64, 4, 1>(__VA_ARGS__); \
             if (HPC == 2) return multi ? f<64, 2, 4>(__VA_ARGS__) : f<64, 2, 1>(__VA_ARGS__); \
             if (HPC == 1) return multi ? f<64, 1, 8>(__VA_ARGS__) : f<64, 1, 1>(__VA_ARGS__); \

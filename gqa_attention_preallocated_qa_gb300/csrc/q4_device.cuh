@@ -6,9 +6,10 @@
 // every value exactly.  Byte i of a row's codes holds dimension 2i in its low
 // half and 2i + 1 in its high half.
 //
-// Codes become numbers without a conversion: a code put into the low mantissa
-// bits of a power of two is that power plus the code, and one fused
-// multiply-add takes the offset away and applies the scale.  Both products of
+// Codes become numbers without a conversion (the method published by Kim, Henry,
+// Fahim and Hassan Awadalla, "Who Says Elephants Can't Run", 2022): a code put into
+// the low mantissa bits of a power of two is that power plus the code, and one
+// fused multiply-add takes the offset away and applies the scale.  Both products of
 // that multiply-add are exact because s has 3 significant bits:
 //   fp16, code in bits 0-3:  (1024 + n) * s - 1032 * s        = (n - 8) * s
 //   fp16, code in bits 4-7:  (1024 + 16 n) * s - 1152 * s     = 16 (n - 8) * s
