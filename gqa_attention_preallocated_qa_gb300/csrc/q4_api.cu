@@ -9,7 +9,7 @@
 #include <new>
 #include <vector>
 
-#include "k2_parts.h"
+#include "prefill_ws.h"
 #include "q4_internal.h"
 #include "q4_plan.h"
 #include "qa.h"
@@ -27,15 +27,8 @@ struct qa_q4_cache {
     uint8_t *codes[2] = {}, *scales[2] = {};  // K and V
     uint32_t *err = nullptr;
     int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
-    const float2 *rope = nullptr;   // shared (RopeTables)
-    // Prefill attention reads one layer's rows in bf16: the sequences of a
-    // launch, dequantised, laid out [slot][kv head][capacity][head_dim].  Every
-    // row that it reads is written before it, so nothing is zeroed.
-    int ws_slots = 0;
-    __nv_bfloat16 *ws[2] = {};      // taken by the first call that needs it
-    float *part_o = nullptr;        // sums of the parts of a block's keys (k2_parts.h); likewise
-    float2 *part_ml = nullptr;
-    cudaEvent_t ws_free = nullptr;  // the last prefill that used the workspace
+    const float2 *rope = nullptr;   // shared (rope_table_take)
+    qa::PrefillWorkspace ws;        // what prefill attention needs
     std::vector<int> window;        // per layer: attention window in keys (0: full)
     // Per (layer, sequence): the position after the last one written, -1 when
     // only the device knows it.  A decode step that continues there can tell
@@ -47,158 +40,15 @@ struct qa_q4_cache {
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Makes the cache's device current for one call.
-class DeviceScope {
-  public:
-    explicit DeviceScope(int device) {
-        ok_ = cudaGetDevice(&before_) == cudaSuccess &&
-              (before_ == device || cudaSetDevice(device) == cudaSuccess);
-        back_ = ok_ && before_ != device;
-    }
-    ~DeviceScope() {
-        if (back_) cudaSetDevice(before_);
-    }
-    bool ok() const { return ok_; }
-
-  private:
-    int before_ = 0;
-    bool ok_ = false, back_ = false;
-};
-
-// The body of an entry point whose host side allocates: no exception leaves it.
-template <typename F>
-qa_status no_throw(F &&body) {
-    try {
-        return body();
-    } catch (...) {
-        return QA_ERR_CUDA;
-    }
-}
-
-constexpr size_t align256(size_t bytes) { return (bytes + 255) & ~size_t(255); }
-
-// Angles of the pairs of dims: position * theta^(-2i/D), i below D / 2.
-struct RopeFreqs {
-    double f[64];
-};
-
-// As qa::fill_rope_table: the same product in fp64, its cosine and sine in fp64,
-// rounded once (2^20 positions, D 64 and 128, theta 10^4 and 10^6: no bit
-// differs from the host's).  Bound by the fp64 units: 16,385 positions of 64
-// pairs take 0.06 ms and 2^20 3.5 ms; one host thread takes 18 ms for the former.
-__global__ void rope_table_kernel(float2 *tab, int64_t n, int half, const __grid_constant__ RopeFreqs freqs) {
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-        const int64_t pos = i / half;
-        double s, c;
-        sincos(static_cast<double>(pos) * freqs.f[i - pos * half], &s, &c);
-        tab[i] = make_float2(static_cast<float>(c), static_cast<float>(s));
-    }
-}
-
-// The rotary tables of the caches that are alive.  A table depends on theta and
-// head_dim alone and a longer one begins with the shorter ones, so caches of one
-// device share it.
-class RopeTables {
-  public:
-    // A table of at least `rows` positions on the current device; null on error.
-    const float2 *take(int device, float theta, int D, int rows) {
-        std::lock_guard<std::mutex> lock(mu_);
-        for (Table &t : tables_)
-            if (t.device == device && t.theta == theta && t.D == D && t.rows >= rows) {
-                ++t.users;
-                return t.tab;
-            }
-        tables_.reserve(tables_.size() + 1);
-        RopeFreqs freqs{};
-        for (int i = 0; i < D / 2; ++i) freqs.f[i] = std::pow(static_cast<double>(theta), -2.0 * i / D);
-        const int64_t n = static_cast<int64_t>(rows) * (D / 2);
-        float2 *tab = nullptr;
-        if (cudaMalloc(reinterpret_cast<void **>(&tab), n * sizeof(float2)) != cudaSuccess) return nullptr;
-        rope_table_kernel<<<static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 4096)), 256>>>(tab, n, D / 2, freqs);
-        if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
-            cudaFree(tab);
-            return nullptr;
-        }
-        tables_.push_back({device, theta, D, rows, 1, tab});
-        return tab;
-    }
-    // Gives one back; the caller has synchronised its device.
-    void give(const float2 *tab) {
-        if (!tab) return;
-        std::lock_guard<std::mutex> lock(mu_);
-        for (size_t i = 0; i < tables_.size(); ++i)
-            if (tables_[i].tab == tab && --tables_[i].users == 0) {
-                cudaFree(tables_[i].tab);
-                tables_.erase(tables_.begin() + i);
-                return;
-            }
-    }
-
-  private:
-    struct Table {
-        int device;
-        float theta;
-        int D, rows, users;
-        float2 *tab;
-    };
-    std::mutex mu_;
-    std::vector<Table> tables_;
-};
-RopeTables g_rope;
+using qa::align256;
+using qa::aligned16;
+using qa::DeviceScope;
+using qa::no_throw;
 
 void free_all(qa_q4_cache *c) {
-    g_rope.give(c->rope);
+    qa::rope_table_give(c->rope);
     cudaFree(c->mem);
-    cudaFree(c->ws[0]);
-    cudaFree(c->part_o);
-    if (c->ws_free) cudaEventDestroy(c->ws_free);
-}
-
-// Allocations of a call that is not captured itself are no part of a capture
-// that is under way on another stream.
-class OutsideCapture {
-  public:
-    OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
-    ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
-
-  private:
-    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
-};
-
-size_t workspace_bytes(const qa_q4_cache *c) {  // of K or of V
-    return static_cast<size_t>(c->ws_slots) * c->cfg.n_kv_heads * c->cfg.capacity * c->cfg.head_dim * 2;
-}
-bool take_workspace(qa_q4_cache *c) {
-    if (c->ws[0]) return true;
-    OutsideCapture scope;
-    if (!c->ws_free && cudaEventCreateWithFlags(&c->ws_free, cudaEventDisableTiming) != cudaSuccess) {
-        c->ws_free = nullptr;
-        return false;
-    }
-    const size_t one = align256(workspace_bytes(c));
-    void *p = nullptr;
-    if (cudaMalloc(&p, 2 * one) != cudaSuccess) return false;
-    c->ws[0] = static_cast<__nv_bfloat16 *>(p);
-    c->ws[1] = c->ws[0] + one / 2;
-    return true;
-}
-
-// The parts of a launch have at most two heads' blocks of 128 rows per SM;
-// caches this short are not cut.
-constexpr int kQ4PartsCapacity = 1024;
-size_t part_rows(const qa_q4_cache *c) { return static_cast<size_t>(c->num_sms) * 256; }
-bool take_sums(qa_q4_cache *c) {
-    if (c->part_o) return true;
-    OutsideCapture scope;
-    const size_t sums = part_rows(c) * c->cfg.head_dim;  // (a multiple of 256 bytes)
-    void *p = nullptr;
-    if (cudaMalloc(&p, sums * sizeof(float) + part_rows(c) * sizeof(float2)) != cudaSuccess) return false;
-    c->part_o = static_cast<float *>(p);
-    c->part_ml = reinterpret_cast<float2 *>(c->part_o + sums);
-    return true;
+    c->ws.release();
 }
 
 qa_status check_layer(const qa_q4_cache *c, int layer, int batch) {
@@ -405,10 +255,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
 struct PrefillGroup {
     qa::Q4PrefillRowsParams rows;
     qa::Q4RowsParams quant, held;
-    qa::K2PartParams k2;
-    qa::K2JoinParams join;
-    bool parts;                     // k2 is of parts, join follows it
-    int items;
+    qa::K2Job k2;
 };
 
 // Builds the launches for sequences s0 .. s0 + n - 1; false when a tensor map
@@ -418,7 +265,7 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
                   const void *wk, void *out, PrefillGroup &pg) {
     const qa_config &g = c->cfg;
     const int D = g.head_dim, Hq = g.n_q_heads, Hkv = g.n_kv_heads;
-    const int64_t ws_head = static_cast<int64_t>(g.capacity) * D, ws_seq = ws_head * Hkv;
+    const int64_t ws_head = c->ws.head_stride(), ws_seq = c->ws.seq_stride();
     pg.rows = qa::Q4PrefillRowsParams{};
     qa::K1Params &k1 = pg.rows.k1;
     k1.q = static_cast<const __nv_bfloat16 *>(q) + row0 * Hq * D;
@@ -427,8 +274,8 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
     k1.wq = static_cast<const __nv_bfloat16 *>(wq);
     k1.wk = static_cast<const __nv_bfloat16 *>(wk);
     k1.qp = static_cast<__nv_bfloat16 *>(out) + row0 * Hq * D;
-    k1.kc = c->ws[0];
-    k1.vc = c->ws[1];
+    k1.kc = c->ws.rows(0);
+    k1.vc = c->ws.rows(1);
     k1.lens = c->ws_lens;
     k1.rope = c->rope;
     k1.err = c->err;
@@ -471,82 +318,19 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         r->src_tok = r->dst_tok = D;
         r->src_head = r->dst_head = ws_head;
         for (int i = 0; i < 2; ++i) {
-            r->src[i] = c->ws[i];
-            r->dst[i] = c->ws[i];
+            r->src[i] = c->ws.rows(i);
+            r->dst[i] = c->ws.rows(i);
         }
         for (int i = 0; i < n; ++i)
             r->src_off[i] = r->dst_off[i] = i * ws_seq + static_cast<int64_t>(r->start[i]) * D;
     }
-    qa::K2PartParams &k2 = pg.k2;
-    k2 = qa::K2PartParams{};
-    std::vector<qa::QueryRun> runs;
     k1.cu[0] = 0;
     for (int i = 0; i < n; ++i) {
         k1.cu[i + 1] = k1.cu[i] + ntok[s0 + i];
         k1.start[i] = start[s0 + i];
-        if (ntok[s0 + i] > 0) runs.push_back({i, 0, ntok[s0 + i]});
     }
-    k2.hpi = std::min(c->G, 2);
-    std::vector<qa::KeyPart> parts;
-    pg.parts = g.capacity >= kQ4PartsCapacity &&
-               qa::plan_parts(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms,
-                              qa::kMaxSeqPerLaunch, parts, k2.hpi);
-    if (pg.parts && !take_sums(c)) return false;
-    k2.npairs = c->G / k2.hpi;
-    if (!pg.parts) {
-        qa::plan_runs(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms, qa::kMaxSeqPerLaunch);
-        k2.hpi = qa::two_heads(runs, start + s0, c->window[layer], D, c->G, Hkv, c->num_sms) ? 2 : 0;
-        for (size_t i = 0; i < runs.size(); ++i) parts.push_back({static_cast<int>(i), 0, 1 << 30});
-    }
-    pg.join = qa::K2JoinParams{};
-    int nseq = 0, maxqb = 0, part_row = 0;
-    const int rows = k1.cu[n];
-    pg.items = 0;
-    for (const qa::KeyPart &part : parts) {
-        const qa::QueryRun &r = runs[part.run];
-        const int P = start[s0 + r.seq] + r.first;
-        if (!qa::encode_kv_map(&k2.tm_k[nseq], c->ws[0] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 64) ||
-            !qa::encode_kv_map(&k2.tm_v[nseq], c->ws[1] + r.seq * ws_seq, D, P + r.len, Hkv, g.capacity, 128))
-            return false;
-        k2.len[nseq] = r.len;
-        k2.start[nseq] = P;
-        k2.cu[nseq] = k1.cu[r.seq] + r.first;
-        k2.part_lo[nseq] = part.lo;
-        k2.part_hi[nseq] = part.hi;
-        k2.part_row[nseq] = part_row;
-        if (pg.join.parts[part.run]++ == 0) {
-            pg.join.row0[part.run] = pg.join.rows;
-            pg.join.len[part.run] = r.len;
-            pg.join.cu[part.run] = k2.cu[nseq];
-            pg.join.part_row[part.run] = part_row;
-            pg.join.rows += r.len;
-        }
-        part_row += r.len;
-        maxqb = std::max(maxqb, (r.len + 127) / 128);
-        pg.items += (r.len + 127) / 128;
-        ++nseq;
-    }
-    k1.T = rows;
-    if (rows == 0) return true;
-    if (!qa::encode_q_map(&k2.tm_q, k1.qp, D, Hq, rows)) return false;
-    k2.out = k1.qp;
-    k2.err = c->err;
-    k2.nseq = nseq;
-    k2.Hq = Hq;
-    k2.Hkv = Hkv;
-    k2.G = c->G;
-    k2.max_qblocks = maxqb;
-    k2.window = c->window[layer];
-    k2.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(D)));
-    pg.items *= Hkv * k2.npairs;
-    k2.part_o = c->part_o;
-    k2.part_ml = c->part_ml;
-    pg.join.part_o = c->part_o;
-    pg.join.part_ml = c->part_ml;
-    pg.join.out = k1.qp;
-    pg.join.Hq = Hq;
-    pg.join.nruns = static_cast<int>(runs.size());
-    return true;
+    k1.T = k1.cu[n];
+    return k1.T == 0 || c->ws.plan(c->window[layer], n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, pg.k2);
 }
 
 }  // namespace
@@ -567,7 +351,6 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
     c->G = g.n_q_heads / g.n_kv_heads;
     c->rows = (g.capacity + qa::kQ4RowPad - 1) / qa::kQ4RowPad * qa::kQ4RowPad;
     c->layer_rows = static_cast<int64_t>(g.max_batch) * g.n_kv_heads * c->rows;
-    c->ws_slots = std::min(g.max_batch, qa::kMaxSeqPerLaunch);
     const size_t rows = static_cast<size_t>(c->layer_rows) * g.num_layers;
     const size_t codes = rows * (g.head_dim / 2), scales = rows * (g.head_dim / qa::kQ4Group);
     const size_t total = 2 * (align256(codes) + align256(scales)) + 256;
@@ -583,13 +366,12 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
         static_assert(qa::kMaxSeqPerLaunch * sizeof(int32_t) <= 128, "behind the error word");
         c->window.assign(static_cast<size_t>(g.num_layers), 0);
         c->next_pos.assign(static_cast<size_t>(g.num_layers) * g.max_batch, -1);
-        c->rope = g_rope.take(c->device, g.rope_theta, g.head_dim, g.capacity);
+        c->rope = qa::rope_table_take(c->device, g.rope_theta, g.head_dim, g.capacity);
         return c->rope && cudaStreamSynchronize(nullptr) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
     }) == QA_OK;
     c->cache_bytes = 2 * (codes + scales);
-    c->scratch_bytes = 256 + 2 * workspace_bytes(c) +
-                       (g.capacity < kQ4PartsCapacity ? 0 : part_rows(c) * (g.head_dim * sizeof(float) + sizeof(float2))) +
-                       static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
+    c->ws.init(g, c->num_sms);
+    c->scratch_bytes = 256 + c->ws.bytes() + static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
     if (!ok) {
         free_all(c);
         delete c;
@@ -725,7 +507,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             cudaGetLastError();
             return QA_ERR_STATE;
         }
-        if (!take_workspace(c)) {
+        if (!c->ws.take()) {
             cudaGetLastError();
             return QA_ERR_CUDA;
         }
@@ -735,7 +517,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             int64_t row0 = 0;
             for (int s0 = 0; s0 < batch;) {
                 int n = 0;
-                while (s0 + n < batch && n < c->ws_slots &&
+                while (s0 + n < batch && n < c->ws.slots() &&
                        (!few_tokens(s0 + n) || (n > 0 && ntok[s0 + n] == 0)))
                     ++n;
                 if (n == 0) {
@@ -759,7 +541,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     for (int first = 0; first < few && st == QA_OK; first += qa::kQ4MaxTokens)
         st = no_throw([&] { return run_decode(c, layer, batch, a, first, s); });
     if (st != QA_OK || !long_form) return st;
-    if (cudaStreamWaitEvent(s, c->ws_free, 0) != cudaSuccess) return QA_ERR_CUDA;
+    if (cudaStreamWaitEvent(s, c->ws.free_event(), 0) != cudaSuccess) return QA_ERR_CUDA;
     int32_t *next = next_of(c, layer);
     for (int b = 0; b < batch; ++b)
         if (!few_tokens(b)) next[b] = start[b] + ntok[b];
@@ -791,12 +573,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
             if (qa::launch_q4_quantise(pg.quant, c->cfg.head_dim, s) != cudaSuccess) return QA_ERR_CUDA;
             c->launches[QA_Q4_KERNEL_QUANTISE]++;
         }
-        const qa::FaultPlan f = qa::take_fault(QA_KERNEL_PREFILL_ATTN);
-        pg.k2.fault = f.fault;
-        pg.k2.wait_ns = f.wait_ns;
-        const cudaError_t e = pg.parts ? qa::launch_k2_parts(pg.k2, c->cfg.head_dim, pg.items, s)
-                                       : qa::launch_k2(pg.k2, c->cfg.head_dim, pg.items, s);
-        if (e != cudaSuccess || (pg.parts && qa::launch_k2_join(pg.join, c->cfg.head_dim, s) != cudaSuccess)) {
+        if (c->ws.launch(pg.k2, s) != cudaSuccess) {
             // A kernel that signalled early is no longer followed by one that
             // waits for it: let it finish before anything else is enqueued.
             cudaStreamSynchronize(s);
@@ -808,7 +585,7 @@ QA_API qa_status qa_q4_prefill(qa_q4_cache *c, int layer, int batch, const int32
     };
     for (size_t i = 0; i < groups.size() && st == QA_OK; ++i) st = launch(groups[i]);
     // After a failure too: what was enqueued uses the workspace.
-    if (cudaEventRecord(c->ws_free, s) != cudaSuccess) return QA_ERR_CUDA;
+    if (cudaEventRecord(c->ws.free_event(), s) != cudaSuccess) return QA_ERR_CUDA;
     return st;
 }
 
