@@ -3,7 +3,7 @@
 Argument marshalling only: tensors are passed as device pointers (torch
 tensors or plain integers), host arrays as int32 buffers, streams as
 cudaStream_t handles.  Every step of the path runs in the library's kernels.
-The 4-bit cache's per-token calls are marshalled by ``_q4calls`` instead.
+The 4-bit and 8-bit caches' per-token calls are marshalled by ``_q4calls`` instead.
 Importing this module loads the library and raises ImportError if it has not
 been built; there is no fallback.  Without ``_q4calls`` those calls alone raise it.
 """
@@ -23,6 +23,7 @@ STATUS_NAMES = {0: "QA_OK", 1: "QA_ERR_INVALID_ARG", 2: "QA_ERR_UNSUPPORTED_SHAP
                 7: "QA_ERR_DEVICE_TIMEOUT", 8: "QA_ERR_DEVICE_BOUNDS"}
 KERNELS = ("norm_rope_append", "prefill_attn", "decode_attn", "reset")
 Q4_KERNELS = ("norm_rope", "quantise", "dequantise", "prefill_attn", "decode")
+Q8_KERNELS = ("norm_rope", "write", "read", "prefill_attn", "decode", "select")
 
 
 class QaError(RuntimeError):
@@ -90,6 +91,25 @@ SIGNATURES = {
     "qa_q4_get_device_error": (ctypes.c_int, [_vp, _u32p]),
     "qa_q4_stats": (ctypes.c_int, [_vp, _u64p]),
     "qa_q4_memory_info": (ctypes.c_int, [_vp, _u64p, _u64p]),
+    "qa_q8_cache_alloc": (ctypes.c_int, [ctypes.POINTER(qa_config), ctypes.POINTER(_vp)]),
+    "qa_q8_cache_free": (ctypes.c_int, [_vp]),
+    "qa_q8_append": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp]),
+    "qa_q8_read": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp]),
+    "qa_q8_prefill": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _i32p, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _vp]),
+    "qa_q8_decode_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qa_q8_decode_step_device_positions": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp,
+                                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                                          _vp]),
+    "qa_q8_sparse_step": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, ctypes.c_int, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qa_q8_sparse_step_device_positions": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _vp,
+                                                          ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+                                                          _vp, _vp, _vp, _vp, _vp]),
+    "qa_q8_get_device_error": (ctypes.c_int, [_vp, _u32p]),
+    "qa_q8_stats": (ctypes.c_int, [_vp, _u64p]),
+    "qa_q8_memory_info": (ctypes.c_int, [_vp, _u64p, _u64p]),
     "qa_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "qa_abi_version": (ctypes.c_int, []),
 }
@@ -342,7 +362,10 @@ def _current_stream():
 def _bind_calls(current_stream) -> None:
     _q4calls.bind(*(ctypes.cast(getattr(lib, name), _vp).value
                     for name in ("qa_q4_append", "qa_q4_read", "qa_q4_prefill", "qa_q4_decode_step",
-                                 "qa_q4_decode_step_device_positions")), current_stream)
+                                 "qa_q4_decode_step_device_positions", "qa_q8_append", "qa_q8_read",
+                                 "qa_q8_prefill", "qa_q8_decode_step",
+                                 "qa_q8_decode_step_device_positions", "qa_q8_sparse_step",
+                                 "qa_q8_sparse_step_device_positions")), current_stream)
 
 
 if not isinstance(_q4calls, _NoCalls):
@@ -441,3 +464,93 @@ def q4_cache_tensors(cache, layer, max_batch, n_kv_heads, capacity, head_dim):
         got.append(torch.as_tensor(_DeviceArray(ptr, (max_batch, n_kv_heads, capacity, row), "|u1",
                                                 (seq * row, head * row, row, 1)), device="cuda"))
     return got
+
+
+# ---- 8-bit cache.  Arguments as the 4-bit cache's.
+
+def qa_q8_cache_alloc(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity,
+                      rope_theta=1e6, rms_eps=1e-6) -> int:
+    cfg = qa_config(num_layers, max_batch, n_q_heads, n_kv_heads, head_dim, capacity, rope_theta,
+                    rms_eps)
+    h = _vp()
+    _check(lib.qa_q8_cache_alloc(ctypes.byref(cfg), ctypes.byref(h)), "qa_q8_cache_alloc")
+    return h.value
+
+
+def qa_q8_cache_free(cache) -> None:
+    _check(lib.qa_q8_cache_free(cache), "qa_q8_cache_free")
+
+
+def qa_q8_append(cache, layer, start, ntok, k, v, stream=None) -> None:
+    st = _q4calls.q8_append(cache, layer, start, ntok, k, v, stream)
+    if st:
+        raise QaError(st, "qa_q8_append")
+
+
+def qa_q8_read(cache, layer, start, ntok, k_out, v_out, stream=None) -> None:
+    st = _q4calls.q8_read(cache, layer, start, ntok, k_out, v_out, stream)
+    if st:
+        raise QaError(st, "qa_q8_read")
+
+
+def qa_q8_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out,
+                  stream=None) -> None:
+    st = _q4calls.q8_prefill(cache, layer, start, ntok, q, k, v, q_norm_w, k_norm_w, out, stream)
+    if st:
+        raise QaError(st, "qa_q8_prefill")
+
+
+def qa_q8_decode_step(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held=None,
+                      v_held=None, stream=None) -> None:
+    """q_norm_w and k_norm_w None: q and k come normed and rotated."""
+    st = _q4calls.q8_decode(cache, layer, positions, q, k, v, q_norm_w, k_norm_w, out, k_held,
+                            v_held, stream)
+    if st:
+        raise QaError(st, "qa_q8_decode_step")
+
+
+def qa_q8_decode_step_device_positions(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w,
+                                       out, k_held=None, v_held=None, stream=None) -> None:
+    """positions: int32 device tensor [batch] (see include/qa.h)."""
+    st = _q4calls.q8_decode_device(cache, layer, batch, positions, q, k, v, q_norm_w, k_norm_w, out,
+                                   k_held, v_held, stream)
+    if st:
+        raise QaError(st, "qa_q8_decode_step_device_positions")
+
+
+def qa_q8_sparse_step(cache, layer, positions, n_blocks, q, k, v, q_norm_w, k_norm_w, out, blocks,
+                      k_held=None, v_held=None, stream=None) -> None:
+    """blocks: int32 device tensor [batch, n_kv_heads, n_blocks], written (see include/qa.h)."""
+    st = _q4calls.q8_sparse(cache, layer, positions, n_blocks, q, k, v, q_norm_w, k_norm_w, out,
+                            blocks, k_held, v_held, stream)
+    if st:
+        raise QaError(st, "qa_q8_sparse_step")
+
+
+def qa_q8_sparse_step_device_positions(cache, layer, batch, positions, n_blocks, q, k, v, q_norm_w,
+                                       k_norm_w, out, blocks, k_held=None, v_held=None,
+                                       stream=None) -> None:
+    """positions: int32 device tensor [batch]; blocks as qa_q8_sparse_step."""
+    st = _q4calls.q8_sparse_device(cache, layer, batch, positions, n_blocks, q, k, v, q_norm_w,
+                                   k_norm_w, out, blocks, k_held, v_held, stream)
+    if st:
+        raise QaError(st, "qa_q8_sparse_step_device_positions")
+
+
+def qa_q8_get_device_error(cache):
+    """(status, raw error word); reading clears the word."""
+    w = ctypes.c_uint32()
+    st = lib.qa_q8_get_device_error(cache, ctypes.byref(w))
+    return st, w.value
+
+
+def qa_q8_stats(cache) -> dict:
+    buf = (ctypes.c_uint64 * len(Q8_KERNELS))()
+    _check(lib.qa_q8_stats(cache, buf), "qa_q8_stats")
+    return dict(zip(Q8_KERNELS, list(buf)))
+
+
+def qa_q8_memory_info(cache):
+    held, scr = ctypes.c_uint64(), ctypes.c_uint64()
+    _check(lib.qa_q8_memory_info(cache, ctypes.byref(held), ctypes.byref(scr)), "qa_q8_memory_info")
+    return held.value, scr.value

@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(256) q4_dequantise_kernel(const __grid_constan
 // ring (three bulk copies), as K1 does.
 // RMSNorm + RoPE of this lane's 8 values of a row held by D/8 lanes; cs, sn:
 // cosines and sines of its dims, the sines signed for its half.  Its sums are in the
-// order of q4_norm_rope (K5): a key gets the same codes from a prefill and from a
+// order of norm_rope_row (K5): a key gets the same codes from a prefill and from a
 // decode step.
 template <int D>
 __device__ __forceinline__ uint4 q4_transform(uint4 xv, uint4 wv, const float2 (&cs)[4],

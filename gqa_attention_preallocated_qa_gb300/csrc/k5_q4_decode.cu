@@ -34,6 +34,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "norm_rope.cuh"
 #include "q4_device.cuh"
 
 namespace qa {
@@ -171,42 +172,6 @@ __device__ __forceinline__ uint32_t q4_hi(uint32_t w, const Q4Scale &s) {
 // that the keys the four lanes of a quad read for V lie in both halves of the
 // shared-memory banks.
 __device__ __forceinline__ int q4_key(int i) { return i ^ ((i >> 1) & 1); }
-
-// A head row on D/8 lanes: 8 values, weights and (cos_a, sin_a, cos_b, sin_b) of
-// the lane's dims; for a new token its v as well.
-struct Q4Row {
-    uint4 x, w, v;
-    float4 cs[4];
-};
-
-// RMSNorm + RoPE of a row, with the roundings of the bf16 path.  Its sums are in
-// the order of q4_transform (K4): a key gets the same codes from a decode step and
-// from a prefill.
-template <int D>
-__device__ __forceinline__ uint4 q4_norm_rope(const Q4Row &row, float eps, int sub) {
-    constexpr int HALF = D / 16;
-    const unsigned FULL = 0xffffffffu;
-    const uint32_t xw[4] = {row.x.x, row.x.y, row.x.z, row.x.w}, ww[4] = {row.w.x, row.w.y, row.w.z, row.w.w};
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) ss = fmaf(bf16lo(xw[e]), bf16lo(xw[e]), fmaf(bf16hi(xw[e]), bf16hi(xw[e]), ss));
-#pragma unroll
-    for (int o = HALF; o >= 1; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
-    const float r = rsqrtf(ss * (1.0f / D) + eps);
-    uint32_t yw[4], pw[4], ow[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        yw[e] = pack_bf16(bf16lo(ww[e]) * round_bf16(bf16lo(xw[e]) * r),
-                          bf16hi(ww[e]) * round_bf16(bf16hi(xw[e]) * r));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) pw[e] = __shfl_xor_sync(FULL, yw[e], HALF);
-    const float sgn = sub < HALF ? -1.f : 1.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        ow[e] = pack_bf16(fmaf(sgn * row.cs[e].y, bf16lo(pw[e]), bf16lo(yw[e]) * row.cs[e].x),
-                          fmaf(sgn * row.cs[e].w, bf16hi(pw[e]), bf16hi(yw[e]) * row.cs[e].z));
-    return make_uint4(ow[0], ow[1], ow[2], ow[3]);
-}
 
 // Running state of a warp: query rows 2c and 2c + 1 (c = lane % 4) of the MMA's
 // columns; o[t] holds dims (d, d + 1) of both rows for this lane's tile t (the
@@ -516,7 +481,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
     // tokens; warp w takes items NW-1-w and 2NW-1-w.
     const int sub = lane % LPR;
     const int nitems = R + (owner ? ntok : 0);
-    auto load_item = [&](int it, Q4Row &row) {
+    auto load_item = [&](int it, NormRow &row) {
         const int t = it < R ? it / HPC : it - R;
         if (it >= nitems || t >= ntok) return;
         const __nv_bfloat16 *x, *w;
@@ -536,7 +501,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) row.cs[e] = __ldg(tab + e);
     };
-    Q4Row row;
+    NormRow row;
     if (pos_ok) load_item(NW - 1 - warp, row);
     __syncwarp();
     cluster_arrive();  // peers may push into this CTA once they have waited on this
@@ -555,7 +520,7 @@ __global__ void __launch_bounds__(kQ4DecodeWarps * 32, 2)
         const int t = it < R ? it / HPC : it - R;
         if (t >= ntok) continue;
         if (it >= NW) load_item(it, row);
-        const uint4 x = q4_norm_rope<D>(row, p.eps, sub);
+        const uint4 x = norm_rope_row<D>(row, p.eps, sub);
         if (it < R) {
             // fp16 with one power of two per row: the largest magnitude goes to
             // [256, 512), so bf16's 8 bits survive down to 2^-22 of it.

@@ -1,5 +1,5 @@
-// q4_calls.cpp -- the Python side of the 4-bit cache's calls that are made once
-// per layer and token: argument marshalling only, for binding.py.
+// q4_calls.cpp -- the Python side of the 4-bit and 8-bit caches' calls that are made
+// once per layer and token: argument marshalling only, for binding.py.
 //
 // A decode step of a short cache takes 2.5 us on the GPU, and a call through
 // ctypes with its conversions took the host 2.2 us beside the launch itself.
@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <cstdint>
+#include <type_traits>
 #include <vector>
 
 namespace {
@@ -19,7 +20,11 @@ PyObject *g_data_ptr = nullptr, *g_cuda_stream = nullptr;  // attribute names
 PyObject *g_current_stream = nullptr;                      // callable: torch's current stream as a handle
 
 using Fn = void (*)();
-enum { kAppend, kRead, kPrefill, kDecode, kDecodeDevice, kCount };
+enum {
+    kAppend, kRead, kPrefill, kDecode, kDecodeDevice,
+    kQ8Append, kQ8Read, kQ8Prefill, kQ8Decode, kQ8DecodeDevice, kQ8Sparse, kQ8SparseDevice,
+    kCount
+};
 Fn g_fn[kCount] = {};
 
 // A device pointer from a tensor, an address or None.
@@ -162,59 +167,92 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-PyObject *read(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return ranged<2>("read", a, n, [](void *c, int l, int b, const int32_t *s, const int32_t *t, void **p, void *st) {
+// K and V rows: a read, or the 8-bit cache's append.
+template <int kFn>
+PyObject *rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return ranged<2>(kFn == kQ8Append ? "append" : "read", a, n,
+                     [](void *c, int l, int b, const int32_t *s, const int32_t *t, void **p, void *st) {
         using F = int (*)(void *, int, int, const int32_t *, const int32_t *, void *, void *, void *);
-        return reinterpret_cast<F>(g_fn[kRead])(c, l, b, s, t, p[0], p[1], st);
+        return reinterpret_cast<F>(g_fn[kFn])(c, l, b, s, t, p[0], p[1], st);
     });
 }
+constexpr auto read = rows<kRead>;
+constexpr auto q8_read = rows<kQ8Read>;
+constexpr auto q8_append = rows<kQ8Append>;
 
-PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t n) {
+template <int kFn>
+PyObject *prefills(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return ranged<6>("prefill", a, n, [](void *c, int l, int b, const int32_t *s, const int32_t *t, void **p, void *st) {
         using F = int (*)(void *, int, int, const int32_t *, const int32_t *, void *, void *, void *, void *, void *,
                           void *, void *);
-        return reinterpret_cast<F>(g_fn[kPrefill])(c, l, b, s, t, p[0], p[1], p[2], p[3], p[4], p[5], st);
+        return reinterpret_cast<F>(g_fn[kFn])(c, l, b, s, t, p[0], p[1], p[2], p[3], p[4], p[5], st);
     });
 }
+constexpr auto prefill = prefills<kPrefill>;
+constexpr auto q8_prefill = prefills<kQ8Prefill>;
 
 using Step = int (*)(void *, int, int, const int32_t *, void *, void *, void *, void *, void *, void *, void *, void *,
                      void *);
+using SparseStep = int (*)(void *, int, int, const int32_t *, int, void *, void *, void *, void *, void *, void *, void *,
+                           void *, void *, void *);
 
-// (cache, layer, positions, 8 pointers, stream)
-PyObject *decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *cache, *p[8], *s;
-    int layer;
+int step(int fn, void *cache, int layer, int batch, const int32_t *pos, int, void **p, void *s, Step) {
+    return reinterpret_cast<Step>(g_fn[fn])(cache, layer, batch, pos, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], s);
+}
+int step(int fn, void *cache, int layer, int batch, const int32_t *pos, int n_blocks, void **p, void *s, SparseStep) {
+    return reinterpret_cast<SparseStep>(g_fn[fn])(cache, layer, batch, pos, n_blocks, p[0], p[1], p[2], p[3], p[4], p[5],
+                                                  p[6], p[7], p[8], s);
+}
+
+// (cache, layer, positions, [n_blocks,] 8 or 9 pointers, stream)
+template <int kFn, class F>
+PyObject *steps(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    constexpr bool sparse = std::is_same<F, SparseStep>::value;
+    constexpr int N = sparse ? 9 : 8, P = sparse ? 4 : 3;
+    void *cache, *p[N], *s;
+    int layer, n_blocks = 0;
     Ints pos;
-    if (!wants("decode", n, 12) || !pointer(a[0], cache) || !small_int(a[1], layer) || !pos.take(a[2])) return nullptr;
-    for (int i = 0; i < 8; ++i)
-        if (!pointer(a[3 + i], p[i])) return nullptr;
-    if (!stream(a[11], s)) return nullptr;
-    int st;
-    Py_BEGIN_ALLOW_THREADS
-    st = reinterpret_cast<Step>(g_fn[kDecode])(cache, layer, pos.size(), pos.data(), p[0], p[1], p[2], p[3], p[4], p[5],
-                                               p[6], p[7], s);
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(st);
-}
-
-// (cache, layer, batch, 9 pointers, stream)
-PyObject *decode_device(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *cache, *p[9], *s;
-    int layer, batch;
-    if (!wants("decode_device", n, 13) || !pointer(a[0], cache) || !small_int(a[1], layer) || !small_int(a[2], batch))
+    if (!wants(sparse ? "sparse" : "decode", n, P + N + 1) || !pointer(a[0], cache) || !small_int(a[1], layer) ||
+        !pos.take(a[2]) || (sparse && !small_int(a[3], n_blocks)))
         return nullptr;
-    for (int i = 0; i < 9; ++i)
-        if (!pointer(a[3 + i], p[i])) return nullptr;
-    if (!stream(a[12], s)) return nullptr;
+    for (int i = 0; i < N; ++i)
+        if (!pointer(a[P + i], p[i])) return nullptr;
+    if (!stream(a[P + N], s)) return nullptr;
     int st;
     Py_BEGIN_ALLOW_THREADS
-    st = reinterpret_cast<Step>(g_fn[kDecodeDevice])(cache, layer, batch, static_cast<const int32_t *>(p[0]), p[1], p[2],
-                                                     p[3], p[4], p[5], p[6], p[7], p[8], s);
+    st = step(kFn, cache, layer, pos.size(), pos.data(), n_blocks, p, s, F());
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
+constexpr auto decode = steps<kDecode, Step>;
+constexpr auto q8_decode = steps<kQ8Decode, Step>;
+constexpr auto q8_sparse = steps<kQ8Sparse, SparseStep>;
 
-// (addresses of append, read, prefill, decode, decode_device; current-stream callable)
+// (cache, layer, batch, positions, [n_blocks,] 8 or 9 pointers, stream)
+template <int kFn, class F>
+PyObject *device_steps(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    constexpr bool sparse = std::is_same<F, SparseStep>::value;
+    constexpr int N = sparse ? 9 : 8, P = sparse ? 5 : 4;
+    void *cache, *pos, *p[N], *s;
+    int layer, batch, n_blocks = 0;
+    if (!wants(sparse ? "sparse_device" : "decode_device", n, P + N + 1) || !pointer(a[0], cache) ||
+        !small_int(a[1], layer) || !small_int(a[2], batch) || !pointer(a[3], pos) ||
+        (sparse && !small_int(a[4], n_blocks)))
+        return nullptr;
+    for (int i = 0; i < N; ++i)
+        if (!pointer(a[P + i], p[i])) return nullptr;
+    if (!stream(a[P + N], s)) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS
+    st = step(kFn, cache, layer, batch, static_cast<const int32_t *>(pos), n_blocks, p, s, F());
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+constexpr auto decode_device = device_steps<kDecodeDevice, Step>;
+constexpr auto q8_decode_device = device_steps<kQ8DecodeDevice, Step>;
+constexpr auto q8_sparse_device = device_steps<kQ8SparseDevice, SparseStep>;
+
+// (addresses of the library's functions in the order of the enum; current-stream callable)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!wants("bind", n, kCount + 1)) return nullptr;
     for (int i = 0; i < kCount; ++i) {
@@ -228,9 +266,11 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define QA_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {QA_FAST(append), QA_FAST(read),          QA_FAST(prefill),
-                           QA_FAST(decode), QA_FAST(decode_device), QA_FAST(bind),
-                           {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {QA_FAST(append),    QA_FAST(read),             QA_FAST(prefill),
+                           QA_FAST(decode),    QA_FAST(decode_device),    QA_FAST(q8_append),
+                           QA_FAST(q8_read),   QA_FAST(q8_prefill),       QA_FAST(q8_decode),
+                           QA_FAST(q8_sparse), QA_FAST(q8_decode_device), QA_FAST(q8_sparse_device),
+                           QA_FAST(bind),      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_q4calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

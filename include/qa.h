@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define QA_ABI_VERSION 5
+#define QA_ABI_VERSION 6
 
 typedef enum {
     QA_OK = 0,
@@ -498,6 +498,157 @@ qa_status qa_q4_stats(qa_q4_cache *cache, uint64_t launches[QA_Q4_NUM_KERNELS]);
  * use: error word and rotary table (which other caches may share), and the
  * workspace and the sums of parts, whether or not a call has taken them yet. */
 qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t *scratch_bytes);
+
+/* ---- 8-bit cache ----------------------------------------------------------
+ * A key/value cache whose rows are held in 8 bits a value with one scale for each
+ * block of 64 positions and kv head, and a decode step that attends to a few blocks
+ * which a cheap score picks for its queries.  Against the 4-bit cache it holds 127
+ * steps to each side instead of 7 and is 1.9 times smaller than bf16 instead of 3.76.
+ * (The pages have no counterpart.)
+ *
+ * Format.  A block is 64 consecutive positions of one kv head, from a multiple of
+ * 64.  When its last row is written the block is complete: its keys and its values
+ * are each held as 64 x D integers n in -127..127 and one fp32 scale s, and stand for
+ * n * s.  With a the largest magnitude in the block, s = a / 127 and n is x * (127 / a)
+ * rounded to the nearest integer, halves to even; the two quotients and the product
+ * are rounded to fp32.  A block with a < 2^-64 becomes zeros (s = 0), and one with a
+ * value that is not finite reads as NaN throughout.
+ * The rows of a block that is not complete are held in bf16 as they came, so what the
+ * cache holds does not depend on how its rows were cut into calls.  A call sees the
+ * rows that it brings itself in bf16, and complete blocks of earlier calls in 8 bits.
+ *
+ * The caller keeps the lengths: every call names the positions it is about, and a
+ * speculative token is dropped by writing its position again.  Writing a position
+ * of a block again begins that block anew from there: its earlier rows are needed as
+ * they came.  The cache has them while the position lies in one of the last two blocks
+ * of which it kept rows (the one being filled and the one before, as far as each was
+ * not written as a whole at once); further back they are the block's values, rounded
+ * to bf16.  A call reads only positions below the ones it writes; rows that nothing
+ * wrote may hold anything.
+ *
+ * Conventions as above; a call on more than 64 sequences is several launches, and an
+ * error of a later one leaves the earlier ones enqueued.  Calls may be made with
+ * another device current; the stream belongs to the cache's device.  Every kernel
+ * here waits for the one before it on the stream before it reads or writes anything,
+ * so calls on this cache are ordered like plain launches, and may be captured into
+ * graphs (but qa_q8_prefill).  It lets the next kernel start its set-up once it has
+ * waited: the decode calls of the other caches, which read q, k, v and the weights
+ * early, must not take what a call on this cache writes (out, k_held, v_held) as their
+ * inputs unless another kernel or copy on the stream lies between them.  Outputs must
+ * share no byte with inputs or with each other (INVALID_ARG). */
+typedef struct qa_q8_cache qa_q8_cache; /* opaque */
+
+/* Kernels counted by qa_q8_stats. */
+enum {
+    QA_Q8_KERNEL_NORM_ROPE = 0,    /* K1: a prefill's rows into the workspace */
+    QA_Q8_KERNEL_WRITE = 1,        /* K6: rows into the cache */
+    QA_Q8_KERNEL_READ = 2,         /* K6: rows out of the cache */
+    QA_Q8_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace (and the join of its parts) */
+    QA_Q8_KERNEL_DECODE = 4,       /* K7: decode steps */
+    QA_Q8_KERNEL_SELECT = 5,       /* K8: the choice of a sparse step's blocks */
+    QA_Q8_NUM_KERNELS = 6
+};
+
+/* Allocate an 8-bit cache on the current device, with the geometry that
+ * qa_cache_alloc takes and a capacity of at most 2^20: codes, scales, the least and
+ * the largest code of each dimension of a block's keys, and per sequence and kv head
+ * 2 x 64 rows of K and V in bf16 (zero-filled); an error word; and the rotary table
+ * (shared as qa_q4_cache_alloc says).  Synchronous.
+ * What prefill attention needs beside them is allocated by the first qa_q8_prefill,
+ * and kept: the workspace that qa_q4_cache_alloc describes.  No other call allocates.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, CUDA. */
+qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out);
+
+/* Free it.  Synchronises the device first.  NULL is accepted and ignored. */
+qa_status qa_q8_cache_free(qa_q8_cache *cache);
+
+/* Write rows as they are (keys already normed and rotated) to positions start[b] ..
+ * start[b] + ntok[b] - 1 of sequences 0..batch-1.
+ * k, v: [T][Hkv][D] packed in sequence order, T = sum of ntok.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY. */
+qa_status qa_q8_append(qa_q8_cache *cache, int layer, int batch, const int32_t *start,
+                       const int32_t *ntok, const void *k, const void *v, void *stream);
+
+/* Read the same ranges as bf16 rows [T][Hkv][D]: n * s rounded to fp32 and then to
+ * bf16 where the block is complete, else the row as it came.  k_out or v_out may be
+ * NULL (that tensor is not read), not both.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY. */
+qa_status qa_q8_read(qa_q8_cache *cache, int layer, int batch, const int32_t *start,
+                     const int32_t *ntok, void *k_out, void *v_out, void *stream);
+
+/* Whole prompts (start 0) or the next chunk of them, with the arguments of
+ * qa_q4_prefill: RoPE(RMSNorm(k)) and v are written to their positions, and every new
+ * token attends causally to the earlier positions and to its own call's rows.  Values
+ * of complete blocks enter the attention as qa_q8_read gives them.
+ * All sequences go through the cache's workspace, up to 8 at a time: calls on several
+ * streams wait for each other, and they cannot be captured into a graph (QA_ERR_STATE).
+ * A key or value that is not finite and that some new token of the call sees can reach
+ * the others of its sequence, also those before it (as in qa_prefill).  A single
+ * new token is cheaper as a decode step.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY, STATE, CUDA. */
+qa_status qa_q8_prefill(qa_q8_cache *cache, int layer, int batch, const int32_t *start,
+                        const int32_t *ntok, const void *q, const void *k, const void *v,
+                        const void *q_norm_w, const void *k_norm_w, void *out, void *stream);
+
+/* One decode step: one new token for each of sequences 0..batch-1 at positions[b]
+ * (HOST), which attends to positions 0..positions[b].  Tensors as qa_decode_step.
+ * q_norm_w and k_norm_w may both be NULL: q and k are then taken as they are (already
+ * normed and rotated).
+ * k_held, v_held: both NULL, or [batch][Hkv][D] that receive the new rows as the step
+ * attends to them.
+ * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (a position at or above the capacity), CUDA. */
+qa_status qa_q8_decode_step(qa_q8_cache *cache, int layer, int batch, const int32_t *positions,
+                            const void *q, const void *k, const void *v, const void *q_norm_w,
+                            const void *k_norm_w, void *out, void *k_held, void *v_held,
+                            void *stream);
+
+/* The same with positions in DEVICE memory (int32 [batch]), read when the previous
+ * kernel on the stream has finished: for graph capture, where the caller advances
+ * them inside the graph.  A position outside 0..capacity-1 leaves its sequence alone
+ * and sets QA_ERR_DEVICE_BOUNDS (qa_q8_get_device_error).  The split count is planned
+ * for a full cache. */
+qa_status qa_q8_decode_step_device_positions(qa_q8_cache *cache, int layer, int batch,
+                                             const int32_t *positions, const void *q, const void *k,
+                                             const void *v, const void *q_norm_w,
+                                             const void *k_norm_w, void *out, void *k_held,
+                                             void *v_held, void *stream);
+
+/* A decode step whose token attends, for each kv head, to n_blocks of the complete
+ * blocks before it and to the rows of the block that it is in itself (at positions
+ * that are a multiple of 64 that is the new row alone).  The blocks are those of the
+ * highest scores, the lower index first among equals.  With lo and hi the least and
+ * the largest n of each dimension of the block's keys, s their scale, and c the queries
+ * of the kv head's group as integers in -127..127 (one scale for the group, made like
+ * n above), a block's score is
+ *     s * sum over the group's heads and the dimensions of max(c lo, c hi),
+ * the integer sum times s rounded to fp32.  The first and the last complete block, and
+ * those with a key that is not finite, score infinity.  Queries that are not finite, or
+ * all below 2^-64, have c = 0.
+ * n_blocks: 1 .. ceil(capacity / 64).  blocks: int32 [batch][Hkv][n_blocks] in DEVICE memory, 4-byte
+ * aligned; receives the chosen blocks in rising order, then -1 where there were fewer.
+ * Its contents are the step's own list until the step has finished.
+ * Everything else as qa_q8_decode_step; two launches per 64 sequences. */
+qa_status qa_q8_sparse_step(qa_q8_cache *cache, int layer, int batch, const int32_t *positions,
+                            int n_blocks, const void *q, const void *k, const void *v,
+                            const void *q_norm_w, const void *k_norm_w, void *out, int32_t *blocks,
+                            void *k_held, void *v_held, void *stream);
+
+/* The same with positions in DEVICE memory.  A sequence whose position is outside the
+ * cache gets a list of -1. */
+qa_status qa_q8_sparse_step_device_positions(qa_q8_cache *cache, int layer, int batch,
+                                             const int32_t *positions, int n_blocks, const void *q,
+                                             const void *k, const void *v, const void *q_norm_w,
+                                             const void *k_norm_w, void *out, int32_t *blocks,
+                                             void *k_held, void *v_held, void *stream);
+
+/* As qa_get_device_error. */
+qa_status qa_q8_get_device_error(qa_q8_cache *cache, uint32_t *detail);
+
+/* Successful launches per kernel (QA_Q8_KERNEL_*). */
+qa_status qa_q8_stats(qa_q8_cache *cache, uint64_t launches[QA_Q8_NUM_KERNELS]);
+
+/* Device bytes, as qa_q4_memory_info. */
+qa_status qa_q8_memory_info(qa_q8_cache *cache, uint64_t *cache_bytes, uint64_t *scratch_bytes);
 
 /* Static description of a status code. */
 const char *qa_status_str(qa_status status);
