@@ -19,6 +19,19 @@ struct alignas(64) K2PartParams : K2Params {
 };
 static_assert(sizeof(K2PartParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
+// Keys and values that stand for multiples of what the layer holds: 64 keys share
+// (a, log2 b, 1 / b), the keys being a times their rows and the values b times theirs.
+// The scores of those keys are multiplied by a, and their weights become b 2^(t - m):
+// log2 b goes into the exponent, and their sum is divided by b again, so no key costs more.
+struct K2Factors {
+    const float4 *factors;           // [slot][kv head][factor_stride]: of 64 keys each, for whole tiles of 128
+    int factor_stride;
+    int slot[kMaxSeqPerLaunch];      // of each launched sequence
+};
+struct alignas(64) K2ScaledParams : K2Params, K2Factors {};
+struct alignas(64) K2ScaledPartParams : K2PartParams, K2Factors {};
+static_assert(sizeof(K2ScaledParams) <= 4096 && sizeof(K2ScaledPartParams) <= 4096, "travel in the 4 KB of kernel parameters");
+
 // out = sum over parts of 2^(m - max m) o / sum of 2^(m - max m) l, per run of
 // rows that share their parts.
 struct K2JoinParams {
@@ -34,6 +47,9 @@ struct K2JoinParams {
 };
 
 cudaError_t launch_k2_parts(const K2PartParams &p, int D, int nitems, cudaStream_t stream);
+// The same with factors (no window).
+cudaError_t launch_k2_scaled(const K2ScaledParams &p, int D, int nitems, cudaStream_t stream);
+cudaError_t launch_k2_scaled_parts(const K2ScaledPartParams &p, int D, int nitems, cudaStream_t stream);
 cudaError_t launch_k2_join(const K2JoinParams &p, int D, cudaStream_t stream);
 
 }  // namespace qa

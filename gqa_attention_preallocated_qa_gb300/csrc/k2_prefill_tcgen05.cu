@@ -54,6 +54,22 @@ __device__ __forceinline__ float k2_ex2(float x) {
     return y;
 }
 
+// The largest of a row's scores in columns kLo .. kHi - 1.
+template <int kLo, int kHi>
+__device__ __forceinline__ float k2_row_max(const uint32_t (&sr)[128]) {
+    float mx8[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        mx8[q] = fmaxf(__uint_as_float(sr[kLo + q]), __uint_as_float(sr[kLo + 8 + q]));
+#pragma unroll
+    for (int i = kLo + 16; i < kHi; i += 16) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            mx8[q] = fmax3(mx8[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + 8 + q]));
+    }
+    return fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+}
+
 // The softmax rescales O only when a row's max grows by more than this many
 // powers of two (in the exp2 domain).
 constexpr float kRescaleLog2 = 8.f;
@@ -119,11 +135,16 @@ __device__ __forceinline__ bool k2p_item(const K2PartParams &p, int k, K2Walk &w
 }
 
 // P: K2Params, or K2PartParams for the form whose items are parts of a block's
-// keys and whose outputs are the parts' sums in fp32.
+// keys and whose outputs are the parts' sums in fp32; or one of these with the
+// factors of 64 keys (K2Factors).
+template <class P>
+constexpr bool k2_scaled = std::is_base_of<K2Factors, P>::value;
+
 template <int D, bool kWindow, class P>
 __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
     k2p_prefill_kernel(const __grid_constant__ P p) {
-    constexpr bool kParts = std::is_same<P, K2PartParams>::value;
+    constexpr bool kParts = std::is_base_of<K2PartParams, P>::value;
+    constexpr bool kScaled = k2_scaled<P>;
     using Lay = K2PLayout<D>;
     constexpr int NS = Lay::kStages;
     const unsigned FULL = 0xffffffffu;
@@ -360,6 +381,12 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                 // out = O / l is exact for any mref.
                 float mref = -INFINITY, l = 0.f;
                 for (int j = 0; j < it.nkv; ++j, ++iter) {
+                    float4 fa = {}, fb = {};  // factors of the tile's first and second 64 keys
+                    if constexpr (kScaled) {
+                        const float4 *f = p.factors + (static_cast<int64_t>(p.slot[it.b]) * p.Hkv + it.kvh) * p.factor_stride + 2 * (it.j0 + j);
+                        fa = __ldg(f);
+                        fb = __ldg(f + 1);
+                    }
                     ok = mbar_wait(smem_u32(&bar_s[t]), iter & 1, &s_abort, p.err, kKernK2, 31,
                                    p.wait_ns);
                     ok = __all_sync(FULL, ok);
@@ -385,19 +412,8 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                         for (int i = 0; i < 128; ++i)
                             if (i > thr || i < tlo) sr[i] = __float_as_uint(-INFINITY);
                     }
-                    float mx8[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        mx8[q] = fmaxf(__uint_as_float(sr[q]), __uint_as_float(sr[8 + q]));
-#pragma unroll
-                    for (int i = 16; i < 128; i += 16) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            mx8[q] = fmax3(mx8[q], __uint_as_float(sr[i + q]),
-                                           __uint_as_float(sr[i + 8 + q]));
-                    }
-                    const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
-                                           fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+                    const float mx = kScaled ? fmaxf(k2_row_max<0, 64>(sr) * fa.x, k2_row_max<64, 128>(sr) * fb.x)
+                                             : k2_row_max<0, 128>(sr);
                     bool rescale = false;
                     float alpha = 1.f;
                     if (j == 0) {
@@ -415,13 +431,27 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                             l *= alpha;
                         }
                     }
-                    const float2 c2 = make_float2(c, c);
-                    const float2 n2 = make_float2(-mref * c, -mref * c);
+                    float2 c2 = make_float2(c, c);
+                    float2 n2 = make_float2(-mref * c, -mref * c);
+                    float first = 0.f;  // sum of the first 64 keys' weights
+                    if constexpr (kScaled) {
+                        c2 = make_float2(c * fa.x, c * fa.x);
+                        n2 = make_float2(fa.y - mref * c, fa.y - mref * c);
+                    }
                     float2 sum4[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) sum4[q] = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) {
+                        if constexpr (kScaled) {
+                            if (ch == 2) {
+                                const float2 sp = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
+                                first = (sp.x + sp.y) * fa.z;
+                                for (int q = 0; q < 4; ++q) sum4[q] = make_float2(0.f, 0.f);
+                                c2 = make_float2(c * fb.x, c * fb.x);
+                                n2 = make_float2(fb.y - mref * c, fb.y - mref * c);
+                            }
+                        }
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -437,7 +467,7 @@ __global__ void __launch_bounds__(K2PLayout<D>::kThreads, 1)
                     }
                     const float2 sp =
                         __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
-                    l += sp.x + sp.y;
+                    l += kScaled ? fmaf(sp.x + sp.y, fb.z, first) : sp.x + sp.y;
                     if (rescale) {
                         // P.V_t(j-1) is complete: the commit that signalled S_t(j)
                         // tracks every tcgen05 operation issued before it.
@@ -558,9 +588,10 @@ struct K2CLayout {
     static constexpr int kTmaWarp = 8, kMmaWarp = 9, kQWarp = 10;
 };
 
-template <bool kWindow>
+template <bool kWindow, class P>
 __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
-    k2c_prefill_kernel(const __grid_constant__ K2Params p) {
+    k2c_prefill_kernel(const __grid_constant__ P p) {
+    constexpr bool kScaled = k2_scaled<P>;
     using Lay = K2CLayout;
     constexpr int NS = Lay::kStages;
     constexpr int D = Lay::D;
@@ -831,6 +862,12 @@ __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
             const int qpos = it.qmin + r;
             float mref = -INFINITY, l = 0.f;  // as in the one-CTA form
             for (int j = 0; j < it.nkv; ++j, ++iter) {
+                float4 fa = {}, fb = {};  // factors of the tile's first and second 64 keys
+                if constexpr (kScaled) {
+                    const float4 *f = p.factors + (static_cast<int64_t>(p.slot[it.b]) * p.Hkv + it.kvh) * p.factor_stride + 2 * (it.j0 + j);
+                    fa = __ldg(f);
+                    fb = __ldg(f + 1);
+                }
                 ok = mbar_wait(smem_u32(&bar_s[t]), iter & 1, &s_abort, p.err, kKernK2, 51,
                                p.wait_ns);
                 ok = __all_sync(FULL, ok);
@@ -856,18 +893,8 @@ __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
                     for (int i = 0; i < 128; ++i)
                         if (i > thr || i < tlo) sr[i] = __float_as_uint(-INFINITY);
                 }
-                float mx8[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    mx8[q] = fmaxf(__uint_as_float(sr[q]), __uint_as_float(sr[8 + q]));
-#pragma unroll
-                for (int i = 16; i < 128; i += 16) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        mx8[q] = fmax3(mx8[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + 8 + q]));
-                }
-                const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
-                                       fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+                const float mx = kScaled ? fmaxf(k2_row_max<0, 64>(sr) * fa.x, k2_row_max<64, 128>(sr) * fb.x)
+                                         : k2_row_max<0, 128>(sr);
                 bool rescale = false;
                 float alpha = 1.f;
                 if (j == 0) {
@@ -883,13 +910,27 @@ __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
                         l *= alpha;
                     }
                 }
-                const float2 c2 = make_float2(c, c);
-                const float2 n2 = make_float2(-mref * c, -mref * c);
+                float2 c2 = make_float2(c, c);
+                float2 n2 = make_float2(-mref * c, -mref * c);
+                float first = 0.f;  // sum of the first 64 keys' weights
+                if constexpr (kScaled) {
+                    c2 = make_float2(c * fa.x, c * fa.x);
+                    n2 = make_float2(fa.y - mref * c, fa.y - mref * c);
+                }
                 float2 sum4[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) sum4[q] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
+                    if constexpr (kScaled) {
+                        if (ch == 2) {
+                            const float2 sp = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
+                            first = (sp.x + sp.y) * fa.z;
+                            for (int q = 0; q < 4; ++q) sum4[q] = make_float2(0.f, 0.f);
+                            c2 = make_float2(c * fb.x, c * fb.x);
+                            n2 = make_float2(fb.y - mref * c, fb.y - mref * c);
+                        }
+                    }
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -904,7 +945,7 @@ __global__ void __launch_bounds__(K2CLayout::kThreads, 1)
                     tmem_st16(tS + ch * 16, pk);
                 }
                 const float2 sp = __fadd2_rn(__fadd2_rn(sum4[0], sum4[1]), __fadd2_rn(sum4[2], sum4[3]));
-                l += sp.x + sp.y;
+                l += kScaled ? fmaf(sp.x + sp.y, fb.z, first) : sp.x + sp.y;
                 if (rescale) {
                     const float2 a2 = make_float2(alpha, alpha);
 #pragma unroll
@@ -1001,7 +1042,7 @@ static int k2_num_sms() {
 
 // Clusters of two CTA-pair prefill CTAs that can be resident at once on the
 // current device (cached per device; 0 when the device cannot hold one).
-template <bool kWindow>
+template <bool kWindow, class P>
 static int k2c_clusters() {
     static std::atomic<int> cache[32] = {};
     int dev = 0;
@@ -1012,7 +1053,7 @@ static int k2c_clusters() {
     }
     int n = 0;
     bool failed = false;
-    if (cudaFuncSetAttribute(k2c_prefill_kernel<kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(k2c_prefill_kernel<kWindow, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              K2CLayout::kSmemBytes) != cudaSuccess) {
         failed = true;
     } else {
@@ -1027,7 +1068,7 @@ static int k2c_clusters() {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, k2c_prefill_kernel<kWindow>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, k2c_prefill_kernel<kWindow, P>, &cfg) != cudaSuccess) {
             n = 0;
             failed = true;
         }
@@ -1039,9 +1080,9 @@ static int k2c_clusters() {
 
 // The CTA-pair form: items of four query heads, one cluster of two per item
 // at a time, as many clusters as can be resident (persistent).
-template <bool kWindow>
-static cudaError_t launch_k2c(const K2Params &p, int items4, int clusters, cudaStream_t stream) {
-    K2Params q = p;
+template <bool kWindow, class P>
+static cudaError_t launch_k2c(const P &p, int items4, int clusters, cudaStream_t stream) {
+    P q = p;
     q.hpi = 4;
     q.npairs = p.G / 4;
     q.nitems = items4;
@@ -1059,15 +1100,15 @@ static cudaError_t launch_k2c(const K2Params &p, int items4, int clusters, cudaS
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k2c_prefill_kernel<kWindow>, q);
+    return cudaLaunchKernelEx(&cfg, k2c_prefill_kernel<kWindow, P>, q);
 }
 
-template <int D, bool kWindow>
-static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t stream) {
+template <int D, bool kWindow, class P>
+static cudaError_t launch_k2_t(const P &p, int nitems, cudaStream_t stream) {
     if (D == 128 && p.G % 4 == 0) {
         // Four-head items on CTA pairs whenever every resident pair gets one.
         const int items4 = nitems / p.npairs * (p.G / 4);
-        const int clusters = k2c_clusters<kWindow>();
+        const int clusters = k2c_clusters<kWindow, P>();
         if (clusters > 0 && items4 >= clusters) return launch_k2c<kWindow>(p, items4, clusters, stream);
     }
     using Lay = K2PLayout<D>;
@@ -1076,14 +1117,14 @@ static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t strea
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 32 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
-        cudaError_t e = cudaFuncSetAttribute(k2p_prefill_kernel<D, kWindow, K2Params>,
+        cudaError_t e = cudaFuncSetAttribute(k2p_prefill_kernel<D, kWindow, P>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
     }
     const int sms = k2_num_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    K2Params q = p;
+    P q = p;
     q.hpi = p.G > 1 ? 2 : 1;
     q.npairs = (p.G + q.hpi - 1) / q.hpi;
     q.nitems = nitems / p.npairs * q.npairs;
@@ -1104,7 +1145,7 @@ static cudaError_t launch_k2_t(const K2Params &p, int nitems, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k2p_prefill_kernel<D, kWindow, K2Params>, q);
+    return cudaLaunchKernelEx(&cfg, k2p_prefill_kernel<D, kWindow, P>, q);
 }
 
 cudaError_t launch_k2(const K2Params &p, int D, int nitems, cudaStream_t stream) {
@@ -1117,11 +1158,19 @@ cudaError_t launch_k2(const K2Params &p, int D, int nitems, cudaStream_t stream)
     return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_k2_scaled(const K2ScaledParams &p, int D, int nitems, cudaStream_t stream) {
+    if (nitems <= 0) return cudaSuccess;
+    if (p.window > 0) return cudaErrorInvalidValue;  // no caller has both
+    if (D == 128) return launch_k2_t<128, false>(p, nitems, stream);
+    if (D == 64) return launch_k2_t<64, false>(p, nitems, stream);
+    return cudaErrorInvalidValue;
+}
+
 // ==================================================================== parts
-template <int D, bool kWindow>
-static cudaError_t launch_parts_t(const K2PartParams &p, int nitems, cudaStream_t stream) {
+template <int D, bool kWindow, class P>
+static cudaError_t launch_parts_t(const P &p, int nitems, cudaStream_t stream) {
     using Lay = K2PLayout<D>;
-    auto kern = k2p_prefill_kernel<D, kWindow, K2PartParams>;
+    auto kern = k2p_prefill_kernel<D, kWindow, P>;
     static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1132,7 +1181,7 @@ static cudaError_t launch_parts_t(const K2PartParams &p, int nitems, cudaStream_
     }
     const int sms = k2_num_sms();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    K2PartParams q = p;
+    P q = p;
     q.nitems = nitems;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(nitems, sms), 1, 1);
@@ -1155,6 +1204,14 @@ cudaError_t launch_k2_parts(const K2PartParams &p, int D, int nitems, cudaStream
         return win ? launch_parts_t<128, true>(p, nitems, stream) : launch_parts_t<128, false>(p, nitems, stream);
     if (D == 64)
         return win ? launch_parts_t<64, true>(p, nitems, stream) : launch_parts_t<64, false>(p, nitems, stream);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_k2_scaled_parts(const K2ScaledPartParams &p, int D, int nitems, cudaStream_t stream) {
+    if (nitems <= 0) return cudaSuccess;
+    if (p.window > 0) return cudaErrorInvalidValue;
+    if (D == 128) return launch_parts_t<128, false>(p, nitems, stream);
+    if (D == 64) return launch_parts_t<64, false>(p, nitems, stream);
     return cudaErrorInvalidValue;
 }
 

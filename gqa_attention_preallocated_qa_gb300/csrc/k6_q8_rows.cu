@@ -70,7 +70,11 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
 }
 
 // The codes of a block pass through shared memory, so that both sides move whole lines.
-template <int D>
+// kFactors: the rows before a chunk of a prefill, into the attention's workspace.
+// There a row of a complete block is its codes (bf16 holds them exactly) and the
+// scales are factors of the block; its product with the scale would be rounded once
+// more.  Blocks of zeros and of NaN, and rows in bf16, have the factor 1.
+template <int D, bool kFactors>
 __global__ void __launch_bounds__(256) q8_read_kernel(const __grid_constant__ Q8RowsParams p) {
     __shared__ alignas(16) uint8_t codes[2][kQ8Block * D];
     griddep_wait();
@@ -80,9 +84,21 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const __grid_constant__ Q8
     const int blk = start / kQ8Block + blockIdx.x - p.item0[z];
     const int lo = max(start - blk * kQ8Block, 0), hi = min(end - blk * kQ8Block, kQ8Block);
     const int64_t sh = static_cast<int64_t>(p.seq0 + z) * p.layer.Hkv + h;
+    const bool held = kFactors && hi == kQ8Block;  // complete, for the chunk
+    float2 scale = make_float2(0.f, 0.f);
+    if (hi > lo) scale = p.layer.scales[sh * p.layer.nblk + blk];
+    if (kFactors) {
+        const bool fk = held && scale.x > 0.f, fv = held && scale.y > 0.f;  // (not 0, not NaN)
+        if (threadIdx.x == 0)
+            p.factors[(static_cast<int64_t>(z) * p.layer.Hkv + h) * p.factor_stride + blk] =
+                make_float4(fk ? scale.x : 1.f, fv ? log2f(scale.y) : 0.f, fv ? 1.f / scale.y : 1.f, 0.f);
+        if (hi <= lo) return;
+        if (fk) scale.x = 1.f;
+        if (fv) scale.y = 1.f;
+    }
     const Q8Tail state = p.layer.state[sh];
-    const float2 scale = p.layer.scales[sh * p.layer.nblk + blk];
-    if (q8_tail_of(state, blk, hi - 1, p.raw != 0) < 0) {
+    auto buffer_of = [&](int r) { return held ? -1 : q8_tail_of(state, blk, r, kFactors); };
+    if (buffer_of(hi - 1) < 0) {
         const uint4 *from = reinterpret_cast<const uint4 *>(p.layer.codes + (sh * p.layer.nblk + blk) * static_cast<int64_t>(2 * kQ8Block * D));
 #pragma unroll
         for (int k = 0; k < 2 * kQ8Block * D / (16 * 256); ++k) {
@@ -97,7 +113,7 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const __grid_constant__ Q8
         __nv_bfloat16 *dst = p.rows[kv] + p.off[z] + h * p.head;
         for (int k = threadIdx.x; k < (hi - lo) * (D / 8); k += 256) {
             const int r = lo + k / (D / 8), d0 = k % (D / 8) * 8;
-            const int buffer = q8_tail_of(state, blk, r, p.raw != 0);
+            const int buffer = buffer_of(r);
             const uint4 x = buffer >= 0 ? *reinterpret_cast<const uint4 *>(q8_tail_rows<D>(p.layer, sh, buffer, kv) + r * D + d0)
                                         : q8_row8<D>(codes[kv], kv != 0, kv ? scale.y : scale.x, r, d0);
             *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(blk * kQ8Block + r - p.first[z]) * p.tok + d0) = x;
@@ -125,7 +141,8 @@ cudaError_t launch_q8_write(const Q8RowsParams &p, int D, cudaStream_t stream) {
     return q8_launch_rows(D == 128 ? q8_write_kernel<128> : q8_write_kernel<64>, p, stream);
 }
 cudaError_t launch_q8_read(const Q8RowsParams &p, int D, cudaStream_t stream) {
-    return q8_launch_rows(D == 128 ? q8_read_kernel<128> : q8_read_kernel<64>, p, stream);
+    if (p.factors) return q8_launch_rows(D == 128 ? q8_read_kernel<128, true> : q8_read_kernel<64, true>, p, stream);
+    return q8_launch_rows(D == 128 ? q8_read_kernel<128, false> : q8_read_kernel<64, false>, p, stream);
 }
 
 }  // namespace qa

@@ -88,8 +88,9 @@ namespace qa {
 const float2 *rope_table_take(int device, float theta, int D, int rows) { return g_rope.take(device, theta, D, rows); }
 void rope_table_give(const float2 *tab) { g_rope.give(tab); }
 
-void PrefillWorkspace::init(const qa_config &cfg, int num_sms) {
+void PrefillWorkspace::init(const qa_config &cfg, int num_sms, bool factors) {
     cfg_ = cfg;
+    has_factors_ = factors;
     num_sms_ = num_sms;
     slots_ = std::min(cfg.max_batch, kMaxSeqPerLaunch);
     G_ = cfg.n_q_heads / cfg.n_kv_heads;
@@ -103,8 +104,12 @@ void PrefillWorkspace::release() {
 
 size_t PrefillWorkspace::kv_bytes() const { return static_cast<size_t>(slots_) * seq_stride() * 2; }
 
+size_t PrefillWorkspace::factor_bytes() const {
+    return has_factors_ ? static_cast<size_t>(slots_) * cfg_.n_kv_heads * factor_stride() * sizeof(float4) : 0;
+}
+
 size_t PrefillWorkspace::bytes() const {
-    return 2 * kv_bytes() +
+    return 2 * kv_bytes() + factor_bytes() +
            (cfg_.capacity < kPartsCapacity ? 0 : part_rows() * (cfg_.head_dim * sizeof(float) + sizeof(float2)));
 }
 
@@ -117,9 +122,10 @@ bool PrefillWorkspace::take() {
     }
     const size_t one = align256(kv_bytes());
     void *p = nullptr;
-    if (cudaMalloc(&p, 2 * one) != cudaSuccess) return false;
+    if (cudaMalloc(&p, 2 * one + factor_bytes()) != cudaSuccess) return false;
     ws_[0] = static_cast<__nv_bfloat16 *>(p);
     ws_[1] = ws_[0] + one / 2;
+    if (has_factors_) factors_ = reinterpret_cast<float4 *>(ws_[0] + one);
     return true;
 }
 
@@ -135,10 +141,13 @@ bool PrefillWorkspace::take_sums() {
 }
 
 bool PrefillWorkspace::plan(int window, int n, const int32_t *start, const int32_t *ntok, const int *cu,
-                            __nv_bfloat16 *qp, uint32_t *err, K2Job &job) {
+                            __nv_bfloat16 *qp, uint32_t *err, bool scaled, K2Job &job) {
     const int D = cfg_.head_dim, Hq = cfg_.n_q_heads, Hkv = cfg_.n_kv_heads;
-    K2PartParams &k2 = job.k2;
-    k2 = K2PartParams{};
+    K2ScaledPartParams &k2 = job.k2;
+    k2 = K2ScaledPartParams{};
+    job.scaled = scaled;
+    k2.factors = factors_;
+    k2.factor_stride = factor_stride();
     std::vector<QueryRun> runs;
     for (int i = 0; i < n; ++i)
         if (ntok[i] > 0) runs.push_back({i, 0, ntok[i]});
@@ -166,6 +175,7 @@ bool PrefillWorkspace::plan(int window, int n, const int32_t *start, const int32
             return false;
         k2.len[nseq] = r.len;
         k2.start[nseq] = P;
+        k2.slot[nseq] = r.seq;
         k2.cu[nseq] = cu[r.seq] + r.first;
         k2.part_lo[nseq] = part.lo;
         k2.part_hi[nseq] = part.hi;
@@ -207,9 +217,16 @@ cudaError_t PrefillWorkspace::launch(K2Job &job, cudaStream_t s) const {
     const FaultPlan f = take_fault(QA_KERNEL_PREFILL_ATTN);
     job.k2.fault = f.fault;
     job.k2.wait_ns = f.wait_ns;
-    if (!job.parts) return launch_k2(job.k2, cfg_.head_dim, job.items, s);
-    const cudaError_t e = launch_k2_parts(job.k2, cfg_.head_dim, job.items, s);
-    return e == cudaSuccess ? launch_k2_join(job.join, cfg_.head_dim, s) : e;
+    const int D = cfg_.head_dim;
+    if (!job.parts) {
+        if (!job.scaled) return launch_k2(job.k2, D, job.items, s);
+        K2ScaledParams p;
+        static_cast<K2Params &>(p) = job.k2;
+        static_cast<K2Factors &>(p) = job.k2;
+        return launch_k2_scaled(p, D, job.items, s);
+    }
+    const cudaError_t e = job.scaled ? launch_k2_scaled_parts(job.k2, D, job.items, s) : launch_k2_parts(job.k2, D, job.items, s);
+    return e == cudaSuccess ? launch_k2_join(job.join, D, s) : e;
 }
 
 }  // namespace qa

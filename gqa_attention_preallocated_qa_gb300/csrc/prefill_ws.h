@@ -63,9 +63,10 @@ void rope_table_give(const float2 *tab);
 
 // K2's launches for one group of sequences.
 struct K2Job {
-    K2PartParams k2;
+    K2ScaledPartParams k2;
     K2JoinParams join;
     bool parts;                     // k2 is of parts, join follows it
+    bool scaled;                    // the rows have factors
     int items;
 };
 
@@ -74,7 +75,8 @@ struct K2Job {
 // reads is written before it, so nothing is zeroed.
 class PrefillWorkspace {
   public:
-    void init(const qa_config &cfg, int num_sms);
+    // factors: the rows of 64 positions may have some (K2Factors).
+    void init(const qa_config &cfg, int num_sms, bool factors = false);
     void release();                 // frees it; the device has been synchronised
     // The workspace and its event, allocated by the first call; false on error.
     bool take();
@@ -82,17 +84,21 @@ class PrefillWorkspace {
     __nv_bfloat16 *rows(int kv) const { return ws_[kv]; }
     int64_t head_stride() const { return static_cast<int64_t>(cfg_.capacity) * cfg_.head_dim; }
     int64_t seq_stride() const { return head_stride() * cfg_.n_kv_heads; }
+    float4 *factors() const { return factors_; }  // [slot][kv head][factor_stride()]
+    int factor_stride() const { return (cfg_.capacity + 127) / 128 * 2; }
     cudaEvent_t free_event() const { return free_; }
     size_t bytes() const;           // of all that may come to be allocated
     // K2's launches for n sequences: ntok[i] new tokens at start[i] .., whose rows
-    // in qp and out begin at cu[i] (cu[n]: their number, above 0).  False when a tensor map
-    // cannot be made or the sums of parts find no memory.
+    // in qp and out begin at cu[i] (cu[n]: their number, above 0).  scaled: by the factors
+    // (no window).  False when a tensor map cannot be made or the sums of parts find no
+    // memory.
     bool plan(int window, int n, const int32_t *start, const int32_t *ntok, const int *cu,
-              __nv_bfloat16 *qp, uint32_t *err, K2Job &job);
+              __nv_bfloat16 *qp, uint32_t *err, bool scaled, K2Job &job);
     cudaError_t launch(K2Job &job, cudaStream_t s) const;
 
   private:
     size_t kv_bytes() const;        // of K or of V
+    size_t factor_bytes() const;
     // The parts of a launch have at most two heads' blocks of 128 rows per SM;
     // caches this short are not cut.
     static constexpr int kPartsCapacity = 1024;
@@ -101,7 +107,9 @@ class PrefillWorkspace {
 
     qa_config cfg_{};
     int num_sms_ = 0, slots_ = 0, G_ = 1;
+    bool has_factors_ = false;
     __nv_bfloat16 *ws_[2] = {};     // taken by the first call that needs it
+    float4 *factors_ = nullptr;     // behind it, if any
     float *part_o_ = nullptr;       // sums of the parts of a block's keys (k2_parts.h); likewise
     float2 *part_ml_ = nullptr;
     cudaEvent_t free_ = nullptr;    // the last prefill that used the workspace

@@ -330,7 +330,7 @@ bool plan_prefill(qa_q4_cache *c, int layer, int s0, int n, const int32_t *start
         k1.start[i] = start[s0 + i];
     }
     k1.T = k1.cu[n];
-    return k1.T == 0 || c->ws.plan(c->window[layer], n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, pg.k2);
+    return k1.T == 0 || c->ws.plan(c->window[layer], n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, false, pg.k2);
 }
 
 }  // namespace

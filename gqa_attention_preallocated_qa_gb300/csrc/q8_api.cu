@@ -258,16 +258,20 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
     pg.older.head = c->ws.head_stride();
     pg.older.nseq = n;
     pg.older.seq0 = s0;
-    pg.older.raw = 1;
     pg.write = pg.older;
+    pg.older.factors = c->ws.factors();
+    pg.older.factor_stride = c->ws.factor_stride();
+    bool scaled = false, older = false;  // some chunk sees a complete block; an earlier row
     for (int i = 0; i < n; ++i) {
         const int P = start[s0 + i], N = ntok[s0 + i], first = P / qa::kQ8Block * qa::kQ8Block;
         k1.cu[i + 1] = k1.cu[i] + N;
         k1.start[i] = P;
-        // The rows before the new ones, unless the sequence has no new ones.
-        pg.older.ntok[i] = N > 0 ? P : 0;
+        // The rows before the new ones, and the factors of all its tiles.
+        pg.older.ntok[i] = P;
         pg.older.off[i] = i * ws_seq;
-        pg.older.item0[i + 1] = pg.older.item0[i] + (pg.older.ntok[i] > 0 ? qa::q8_read_items(0, P) : 0);
+        pg.older.item0[i + 1] = pg.older.item0[i] + (N > 0 ? qa::q8_tile_items(P + N) : 0);
+        scaled = scaled || (N > 0 && P >= qa::kQ8Block);
+        older = older || (N > 0 && P > 0);
         // All rows of the first block are in the workspace by then.
         pg.write.start[i] = P;
         pg.write.ntok[i] = N;
@@ -275,8 +279,9 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
         pg.write.off[i] = i * ws_seq + static_cast<int64_t>(first) * D;
         pg.write.item0[i + 1] = pg.write.item0[i] + (N > 0 ? qa::q8_write_items(P, P + N) : 0);
     }
+    if (!older) pg.older.item0[n] = 0;  // nothing to read
     k1.T = k1.cu[n];
-    return k1.T == 0 || c->ws.plan(0, n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, pg.k2);
+    return k1.T == 0 || c->ws.plan(0, n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, scaled, pg.k2);
 }
 
 }  // namespace
@@ -323,7 +328,7 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
         c->rope = qa::rope_table_take(c->device, g.rope_theta, g.head_dim, g.capacity);
         return c->rope && cudaStreamSynchronize(nullptr) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
     }) == QA_OK;
-    c->ws.init(g, c->num_sms);
+    c->ws.init(g, c->num_sms, true);
     c->cache_bytes = codes + scales + bounds + tail + state;
     c->scratch_bytes = 256 + c->ws.bytes() + static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
     if (!ok) {
@@ -475,7 +480,7 @@ QA_API qa_status qa_q8_prefill(qa_q8_cache *c, int layer, int batch, const int32
             return true;
         };
         if (pg.k1.T == 0) return QA_OK;
-        if (pg.older.item0[pg.older.nseq] > 0 &&
+        if (pg.older.item0[pg.older.nseq] > 0 &&  // (of no older row: no factors either)
             !done(qa::launch_q8_read(pg.older, g.head_dim, s), QA_Q8_KERNEL_READ))
             return QA_ERR_CUDA;
         if (!done(qa::launch_k1(pg.k1, g.head_dim, s), QA_Q8_KERNEL_NORM_ROPE) ||

@@ -36,7 +36,11 @@ struct Q8RowsParams {
     __nv_bfloat16 *rows[2];              // of K and V (write: read only; read: either may be null)
     int64_t tok, head;
     int nseq, seq0;                      // seq0: cache slot of launched sequence 0
-    int raw;                             // read: rows as they came, where they are still there
+    // A read for prefill attention of a chunk at position ntok: codes as they are, with the
+    // factors of their blocks here ([slot][head][factor_stride], all of the sequence's
+    // tiles of 128); null otherwise.
+    float4 *factors;
+    int factor_stride;
     int start[kQ8MaxSeqPerLaunch], ntok[kQ8MaxSeqPerLaunch];
     int first[kQ8MaxSeqPerLaunch];       // position of the row at off (write: start, or its block's first)
     int item0[kQ8MaxSeqPerLaunch + 1];   // first work item (block) of each launched sequence
@@ -69,6 +73,8 @@ QA_HD int q8_write_items(int start, int end) {
     const int first = start / kQ8Block, last = (end - 1) / kQ8Block;
     return last - first + 1 - (last > first && end % kQ8Block != 0 ? 1 : 0);
 }
+// Of a read: its blocks.  For prefill attention: those of all tiles of 128 below end.
+QA_HD int q8_tile_items(int end) { return (end + 127) / 128 * 2; }
 QA_HD int q8_read_items(int start, int end) { return (end - 1) / kQ8Block - start / kQ8Block + 1; }
 
 cudaError_t launch_q8_write(const Q8RowsParams &p, int D, cudaStream_t stream);

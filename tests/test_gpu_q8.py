@@ -200,3 +200,190 @@ def test_decode_steps_follow_each_other_through_blocks(qa, d):
                     close(out[b:b + 1], *c.want(b, pos, q[b:b + 1].double()), what=f"step {step}, position {pos}")
             lens = [n + 1 for n in lens]
         c.check_read(lens)
+
+
+def transform(qa, c, start, ntok, q, k, v):
+    """q', k' of the bf16 path's kernel for prompts, as bf16 tensors."""
+    bf16 = qa.qa_cache_alloc(1, c.batch, c.hq, c.hkv, c.d, c.cap, THETA, EPS)
+    try:
+        kt, _, _ = qa.cache_tensors(bf16, 0, c.batch, c.hkv, c.cap, c.d)
+        qa.qa_cache_set_lengths(bf16, 0, list(start) + [0] * (c.batch - len(start)))
+        qp = torch.empty_like(q)
+        qa.qa_prefill_transform(bf16, 0, list(ntok), q, k, v, c.wq, c.wk, qp)
+        kp = torch.cat([kt[b, :, s:s + n].transpose(0, 1) for b, (s, n) in enumerate(zip(start, ntok))])
+        return qp, kp.contiguous()
+    finally:
+        qa.qa_cache_free(bf16)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (32, 8, 128)])
+def test_norm_and_rotation_inside_the_step(qa, hq, hkv, d):
+    """The step gives the same bits for raw rows as for rows that another kernel normed."""
+    lens = [0, 5, 63, 300]
+    with Cache(qa, 4, hq, hkv, d, 400) as c, Cache(qa, 4, hq, hkv, d, 400) as other:
+        c.fill(lens, 3)
+        other.fill(lens, 3)
+        q, k, v = c.tokens(4, 50)
+        qp, kp = transform(qa, c, lens, [1] * 4, q, k, v)
+        outs, held = [], []
+        for cache, x, y, w in ((c, q, k, (c.wq, c.wk)), (other, qp, kp, (None, None))):
+            out, kh, vh = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+            qa.qa_q8_decode_step(cache.h, 0, lens, x, y, v, *w, out, kh, vh)
+            outs.append(out)
+            held.append(kh)
+        assert torch.equal(held[0], kp) and torch.equal(held[1], kp)
+        assert torch.equal(outs[0], outs[1])
+
+
+# ------------------------------------------------------------------ sparse steps
+def check_sparse(qa, c, lens, n_blocks, seed, gain=1.0):
+    q, k, v = c.tokens(len(lens), seed)
+    q = q * gain
+    out = torch.empty_like(q)
+    blocks = torch.full((len(lens), c.hkv, n_blocks), 12345, device="cuda", dtype=torch.int32)
+    qa.qa_q8_sparse_step(c.h, 0, lens, n_blocks, q, k, v, None, None, out, blocks)
+    got = blocks.cpu().numpy()
+    c.ref.write(lens, [1] * len(lens), f64(k), f64(v))
+    g = c.hq // c.hkv
+    for b, pos in enumerate(lens):
+        qs = f64(q[b]).reshape(c.hkv, g, c.d)
+        for h in range(c.hkv):
+            full = pos // BLOCK
+            want = q8_ref.select(qs[h], c.ref.n[0, b, h, :full], c.ref.s[0, b, h, :full], n_blocks)
+            np.testing.assert_array_equal(got[b, h], want, err_msg=f"position {pos}, kv head {h}")
+        close(out[b:b + 1], *c.want(b, pos, q[b:b + 1].double(), got[b]), what=f"position {pos}")
+    return [n + 1 for n in lens]
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(1, 1, 64), (8, 1, 128), (32, 8, 128), (8, 4, 64)])
+@pytest.mark.parametrize("n_blocks", [1, 2, 5, 16])
+def test_sparse_step_is_the_definition(qa, hq, hkv, d, n_blocks):
+    lens = [0, 63, 64, 65, 128, 319, 1000, 2047]
+    with Cache(qa, len(lens), hq, hkv, d, 2100) as c:
+        c.fill(lens, 7)
+        for step in range(2):
+            lens = check_sparse(qa, c, lens, n_blocks, 70 + 3 * step)
+
+
+def test_sparse_choice_among_equal_scores(qa):
+    """Blocks that are copies of each other: the lower index first; zeros; a block of NaN."""
+    d, hkv, full = 64, 2, 40
+    block = rows(1, BLOCK, hkv, d)
+    k = block.repeat(full, 1, 1)
+    k[BLOCK * 7:BLOCK * 9] = 0
+    k[BLOCK * 20 + 3, 1, 5] = float("nan")  # of one kv head
+    v = rows(2, full * BLOCK, hkv, d)
+    with Cache(qa, 1, 4, hkv, d, full * BLOCK + 5) as c:
+        c.append([0], [full * BLOCK], k, v)
+        q, kn, vn = c.tokens(1, 9)
+        out, blocks = torch.empty_like(q), torch.empty(1, hkv, 6, device="cuda", dtype=torch.int32)
+        qa.qa_q8_sparse_step(c.h, 0, [full * BLOCK], 6, q, kn, vn, None, None, out, blocks)
+        assert blocks[0, 0].tolist() == [0, 1, 2, 3, 4, 39]
+        assert blocks[0, 1].tolist() == [0, 1, 2, 3, 20, 39]
+        assert torch.isfinite(out[0, :2]).all() and torch.isnan(out[0, 2:]).all()
+        # queries of zeros: every score is zero
+        qa.qa_q8_sparse_step(c.h, 0, [full * BLOCK], 4, torch.zeros_like(q), kn, vn, None, None, out, blocks[:, :, :4].contiguous())
+        z = torch.empty(1, hkv, 4, device="cuda", dtype=torch.int32)
+        qa.qa_q8_sparse_step(c.h, 0, [full * BLOCK], 4, torch.zeros_like(q), kn, vn, None, None, out, z)
+        assert z[0, 0].tolist() == [0, 1, 2, 39] and z[0, 1].tolist() == [0, 1, 20, 39]
+
+
+@pytest.mark.parametrize("n_blocks", [1, 300, 2500])
+def test_sparse_over_the_longest_cache(qa, n_blocks):
+    """16384 blocks, more than the threads keep in registers."""
+    cap, d = 1 << 20, 64
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn(cap - 1, 1, d, generator=gen, device="cuda").bfloat16()
+    with Cache(qa, 1, 2, 1, d, cap) as c:
+        c.append([0], [cap - 1], k, k)
+        check_sparse(qa, c, [cap - 1], n_blocks, 5)
+
+
+# ------------------------------------------------------------------ prefill
+def check_prefill(qa, c, start, ntok, seed):
+    t = sum(ntok)
+    q, k, v = c.tokens(t, seed)
+    out = torch.empty_like(q)
+    qa.qa_q8_prefill(c.h, 0, start, ntok, q, k, v, c.wq, c.wk, out)
+    qp, kp = transform(qa, c, start, ntok, q, k, v)
+    g, at = c.hq // c.hkv, 0
+    for b, (s, n) in enumerate(zip(start, ntok)):
+        if n == 0:
+            continue
+        outs, mags, flats = [], [], []
+        for h in range(c.hkv):
+            kk, vv = (torch.cat((torch.from_numpy(c.ref.held(i, b, s)[h]).cuda(), x[at:at + n, h].double()))[None]
+                      for i, x in enumerate((kp, v)))
+            o, m, f = q8_ref.attend(qp[at:at + n, h * g:(h + 1) * g].double(), kk, vv, s)
+            outs.append(o)
+            mags.append(m)
+            flats.append(f)
+        close(out[at:at + n], torch.cat(outs, 1), torch.cat(mags, 1), torch.cat(flats, 1), p_bits=8,
+              what=f"{n} tokens at {s}")
+        at += n
+    c.ref.write(start, ntok, f64(kp), f64(v))
+    return [s + n for s, n in zip(start, ntok)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(2, 1, 64), (4, 4, 128), (32, 8, 128), (16, 2, 64)])
+def test_prefill_of_prompts_and_chunks(qa, hq, hkv, d):
+    with Cache(qa, 4, hq, hkv, d, 1200) as c:
+        lens = check_prefill(qa, c, [0, 0, 0, 0], [130, 1, 64, 0], 40)
+        lens = check_prefill(qa, c, lens, [500, 63, 129, 5], 50)
+        lens = check_prefill(qa, c, lens, [1, 64, 300, 59], 60)
+        c.check_read(lens)
+        assert qa.qa_q8_get_device_error(c.h)[0] == 0
+
+
+def test_prefill_of_few_blocks_behind_many_keys(qa):
+    """Keys in parts, and the same with a sequence that has nothing before it."""
+    with Cache(qa, 2, 16, 2, 128, 5000) as c:
+        c.fill([4500, 0], 3)
+        lens = check_prefill(qa, c, [4500, 0], [100, 70], 40)
+        assert qa.qa_q8_stats(c.h)["prefill_attn"] == 1
+        check_prefill(qa, c, lens, [70, 0], 50)
+
+
+def test_prefill_of_more_sequences_than_the_workspace_holds(qa):
+    n = 11
+    with Cache(qa, n, 4, 1, 64, 300) as c:
+        start = [(37 * i) % 150 for i in range(n)]
+        c.fill(start, 3)
+        lens = check_prefill(qa, c, start, [(53 * i) % 140 for i in range(n)], 40)
+        c.check_read(lens)
+
+
+def test_prefill_behind_values_of_every_size(qa):
+    """Blocks of zeros, of large and of small values before a chunk: their scales are
+    factors of the attention kernel's weights."""
+    d, n = 128, 6 * BLOCK
+    v = rows(1, n, 1, d)
+    for j, size in enumerate([0.0, 2.0 ** 40, 2.0 ** -40, 2.0 ** -63, 1.0, 2.0 ** 100]):
+        v[j * BLOCK:(j + 1) * BLOCK] *= size
+    k = rows(2, n, 1, d)
+    k[BLOCK:2 * BLOCK] = 0
+    with Cache(qa, 1, 4, 1, d, 600) as c:
+        for last in (5, 6):  # with and without the largest
+            c.append([0], [last * BLOCK], k[:last * BLOCK].contiguous(), v[:last * BLOCK].contiguous())
+            check_prefill(qa, c, [last * BLOCK], [70], 40)
+
+
+# ------------------------------------------------------------------ all of it as it is used
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (4, 2, 64)])
+def test_a_conversation(qa, hq, hkv, d):
+    with Cache(qa, 3, hq, hkv, d, 1500) as c:
+        lens = check_prefill(qa, c, [0, 0, 0], [600, 130, 1], 40)
+        for turn in range(2):
+            for step in range(5):
+                q, k, v = c.tokens(3, 500 + 50 * turn + 3 * step)
+                out, kh, vh = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+                qa.qa_q8_decode_step(c.h, 0, lens, q, k, v, c.wq, c.wk, out, kh, vh)
+                qp, kp = transform(qa, c, lens, [1] * 3, q, k, v)
+                assert torch.equal(kh, kp) and torch.equal(vh, v)
+                c.ref.write(lens, [1] * 3, f64(kp), f64(v))
+                for b, pos in enumerate(lens):
+                    close(out[b:b + 1], *c.want(b, pos, qp[b:b + 1].double()), what=f"position {pos}")
+                lens = [n + 1 for n in lens]
+            lens = check_sparse(qa, c, lens, 3, 700 + turn)
+            lens = check_prefill(qa, c, lens, [60, 128, 200], 800 + 10 * turn)
+        c.check_read(lens)
