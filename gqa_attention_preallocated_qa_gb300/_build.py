@@ -27,7 +27,7 @@ LIB = os.path.join(PKG, "libqa.so")
 CALLS = os.path.join(PKG, "_q4calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["qa_api.cu", "k1_norm_rope_append.cu", "k2_prefill_tcgen05.cu", "k3_decode_splitkv.cu",
            "q4_api.cu", "k4_q4_rows.cu", "k5_q4_decode.cu",
-           "prefill_ws.cu", "q8_api.cu", "k6_q8_rows.cu", "k7_q8_decode.cu", "k8_q8_select.cu"]
+           "prefill_ws.cu", "q8_api.cu", "k6_q8_rows.cu", "k7_q8_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 

@@ -1,9 +1,9 @@
-// k7_q8_decode.cu -- K7: one decode step over the 8-bit cache.
+// k7_q8_decode.cu -- K7: one decode step over the 8-bit cache, dense or sparse.
 //
 // For each sequence and query head, with q' the normed and rotated query and
 // n_j, s the codes and scale of a block's keys (likewise of its values):
 //   t_j = log2(e) / sqrt(D) * s * (q' . n_j),  out = sum_j 2^t_j V_j / sum_j 2^t_j
-// over the complete blocks (or those that a list names), and over the bf16 rows of
+// over the complete blocks (or the chosen ones of them), and over the bf16 rows of
 // the block that the new token is in, itself among them.
 //
 // Bound by the bytes of the codes: a block of K and V is 16 KB (D = 128), and
@@ -20,17 +20,33 @@
 // per accumulator and 64 keys.
 //   The running maximum lags: weights are 2^(t - ref), and ref moves only when one
 // would pass 2^8.
-//   The splits of a (sequence, kv head) form a cluster and merge through
-// distributed shared memory.
+//   S CTAs (a power of two) of a cluster share a (sequence, kv head); each sends its
+// sums to the CTAs that finish them, through distributed shared memory.
+//
+// A sparse step first chooses its blocks.  A block keeps the least and the largest
+// code of each dim of its keys (lo, hi).  With c the group's queries as integers in
+// -127..127 (one scale for the group),
+//   score_j = s_j sum over heads and dims of max(c lo_j, c hi_j)
+//           = s_j sum over dims of (C+ hi_j + C- lo_j),
+// C+ and C- the sums over the heads of c's positive and negative parts: what the
+// group's products with the block's keys can come to at most ("Quest: Query-Aware
+// Sparsity for Efficient Long-Context LLM Inference", Tang et al., 2024, has such
+// bounds for each head).  All sums are of integers and below 2^24, so the one
+// rounding is that of the product with s_j, and the choice does not depend on the
+// order of anything.  The bounds are 2 D bytes a block and kv head (1/64 of its
+// codes): 16 lanes (D = 128) take a block, in 8 two-way integer dot products each.
+// Every CTA of a (sequence, kv head) scores a share, sends the scores to the others,
+// and finds the n-th largest for itself, two bits at a time.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
 
-#include "q8_step.cuh"
+#include "norm_rope.cuh"
+#include "q8_device.cuh"
 
 namespace qa {
 
-constexpr int kQ8Warps = 8;
+constexpr int kQ8Warps = 4, kQ8Threads = kQ8Warps * 32;
 constexpr float kQ8NoRef = -3e38f;   // no key yet
 constexpr float kQ8Lag = 8.f;
 
@@ -69,10 +85,16 @@ __device__ __forceinline__ uint4 q8_load(const uint8_t *p) {
                  : "l"(p));
     return x;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-    return x;
+__device__ __forceinline__ void q8_cp_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void q8_cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Into the shared memory of any CTA of the cluster.
+__device__ __forceinline__ void q8_st_cluster(uint32_t addr, uint32_t x) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void q8_st_cluster(uint32_t addr, float a, float b) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 // Sums of a warp: columns (heads) 2 t and 2 t + 1 of the MMAs (t = lane % 4); o[m] holds
@@ -108,16 +130,31 @@ __device__ __forceinline__ void q8_raise(Q8Acc<D> &a, float m0, float m1) {
     }
 }
 
+// Scores as unsigned integers in their order (NaN does not occur).
+__device__ __forceinline__ uint32_t q8_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);  // (-0 is 0)
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
 template <int D>
-struct alignas(16) Q8DecodeSmem {
+struct alignas(16) Q8StepSmem {
     __half qh[8][D + 8];            // queries, each row times a power of two
     __nv_bfloat16 qb[8][D + 8];     // queries as they are
     float qscale[8], qstart[8];     // log2(e) / sqrt(D) over that power; what S starts from
+    union {
+        __nv_bfloat16 rows[2][kQ8Block][D + 8];   // K and V of the block that the new token is in
+        float o[kQ8Warps][8][D + 8];              // then a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
+        Q8SealSmem<D> seal;                       // then these
+    };
     float ref[kQ8Warps][8], l[kQ8Warps][8];
-    float o[kQ8Warps][8][D + 8];    // a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
-    float cta_ref[8], cta_l[8];
-    float cta_o[8][D];
-    Q8SealSmem<D> seal;
+    // From the CTAs of the (sequence, kv head): references and sums of weights (of a
+    // head), and this CTA's share of the outputs.
+    float2 got_l[kQ8MaxSplits][8];
+    float got_o[8 * D];
+    // A sparse step's
+    uint32_t top[kQ8Warps];
+    alignas(16) short up[D], down[D];             // C+, C-
+    uint2 part[2][kQ8Warps];
 };
 
 template <int D>
@@ -126,79 +163,269 @@ __device__ __forceinline__ int q8_slot(int d) {
     return (r >> 1) * 16 + 2 * g + (r & 1);
 }
 
+// Sums of a and b over the CTA's threads; `turn` alternates between calls.
+__device__ __forceinline__ uint2 q8_cta_sum(uint32_t a, uint32_t b, uint2 (&part)[2][kQ8Warps], int turn) {
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_uint2(a, b);
+    __syncthreads();
+    uint2 sum = part[turn][0];
+#pragma unroll
+    for (int w = 1; w < kQ8Warps; ++w) {
+        sum.x += part[turn][w].x;
+        sum.y += part[turn][w].y;
+    }
+    return sum;
+}
+
+// Scores the blocks of this CTA's share (me of S) and sends them to keys[] of all S.
 template <int D>
-__global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __grid_constant__ Q8StepParams p) {
+__device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int me, int S, uint32_t first_rank,
+                                         const Q8StepSmem<D> &sm, uint32_t *keys) {
+    constexpr int LPB = D / 8, BPW = 32 / LPB, U = 4;  // lanes a block, blocks a warp, loads ahead
+    // A lane holds 16 codes of a block's 2 D: lo's in the first half of its lanes, hi's in the other.
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPB, d0 = sub % (D / 16) * 16;
+    const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
+    const uint4 wa = w4[0], wb = w4[1];
+    const int per = (full + S - 1) / S, lo = me * per, hi = min(full, lo + per);
+    const int8_t *bounds = l.bounds + base * (2 * D) + sub * 16;
+    const uint32_t to = smem_u32(keys);
+    for (int j0 = lo + warp * BPW; j0 < hi; j0 += U * BPW * kQ8Warps) {
+        uint4 x[U];
+        float s[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * BPW * kQ8Warps + lane / LPB;
+            x[u] = make_uint4(0, 0, 0, 0);
+            s[u] = 0.f;
+            if (j < hi) {
+                x[u] = *reinterpret_cast<const uint4 *>(bounds + static_cast<int64_t>(j) * (2 * D));
+                s[u] = l.scales[base + j].x;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u * BPW * kQ8Warps + lane / LPB;
+            int dot = 0;
+            dot = __dp2a_lo(static_cast<int>(wa.x), static_cast<int>(x[u].x), dot);
+            dot = __dp2a_hi(static_cast<int>(wa.y), static_cast<int>(x[u].x), dot);
+            dot = __dp2a_lo(static_cast<int>(wa.z), static_cast<int>(x[u].y), dot);
+            dot = __dp2a_hi(static_cast<int>(wa.w), static_cast<int>(x[u].y), dot);
+            dot = __dp2a_lo(static_cast<int>(wb.x), static_cast<int>(x[u].z), dot);
+            dot = __dp2a_hi(static_cast<int>(wb.y), static_cast<int>(x[u].z), dot);
+            dot = __dp2a_lo(static_cast<int>(wb.z), static_cast<int>(x[u].w), dot);
+            dot = __dp2a_hi(static_cast<int>(wb.w), static_cast<int>(x[u].w), dot);
+#pragma unroll
+            for (int o = LPB / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (j < hi) {
+                float score = __fmul_rn(static_cast<float>(dot), s[u]);
+                if (j == 0 || j == full - 1 || s[u] != s[u]) score = INFINITY;
+                const uint32_t key = q8_key(score);
+                if (S == 1) {
+                    if (sub == 0) keys[j] = key;
+                } else {
+                    for (int r = sub; r < S; r += LPB) q8_st_cluster(map_rank(to + 4 * j, first_rank + r), key);
+                }
+            }
+        }
+    }
+}
+
+// The n blocks of the largest of keys[0 .. full - 1] (full > n), in rising order: those at
+// places lo .. hi - 1 go to list[], all of them to `all` (may be null).
+template <int D>
+__device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n, int lo, int hi, Q8StepSmem<D> &sm,
+                                          uint16_t *list, int32_t *all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int R = 8;  // keys of a thread in registers; the others are read again
+    uint32_t mine[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int j = threadIdx.x + i * kQ8Threads;
+        mine[i] = j < full ? keys[j] : 0u;  // (0 is below every score's key)
+    }
+    auto count = [&](uint32_t least) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) c += mine[i] >= least;
+        for (int j = threadIdx.x + R * kQ8Threads; j < full; j += kQ8Threads) c += keys[j] >= least;
+        return c;
+    };
+    // The n-th largest key, two bits at a time from the highest: the largest value that
+    // at least n keys reach.  (Counts stay below 2^15.)
+    uint32_t nth = 0;
+    int reach = full, turn = 0;  // keys that are at least nth
+    for (int shift = 30; shift >= 0 && reach != n; shift -= 2, turn ^= 1) {
+        const uint32_t c1 = count(nth | 1u << shift), c2 = count(nth | 2u << shift), c3 = count(nth | 3u << shift);
+        const uint2 c = q8_cta_sum(c1 | c2 << 16, c3, sm.part, turn);
+        const int n1 = c.x & 0xffff, n2 = c.x >> 16, n3 = c.y;
+        if (n1 >= n) {
+            const uint32_t digit = n3 >= n ? 3 : n2 >= n ? 2 : 1;
+            nth |= digit << shift;
+            reach = n3 >= n ? n3 : n2 >= n ? n2 : n1;
+        }
+    }
+    // All above it, and of those that equal it the first ones: in order, a run of
+    // blocks for each thread.
+    const int run = (full + kQ8Threads - 1) / kQ8Threads;
+    const int j_lo = min(full, static_cast<int>(threadIdx.x) * run), j_hi = min(full, j_lo + run);
+    uint32_t both = 0;  // above it, and equal to it in the upper half
+    for (int j = j_lo; j < j_hi; ++j) both += keys[j] > nth ? 1u : keys[j] == nth ? 1u << 16 : 0u;
+    uint32_t before = both;  // sums over the threads before this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) sm.part[turn][warp].x = before;
+    __syncthreads();
+    before -= both;
+    uint32_t total = 0;
+    for (int w = 0; w < kQ8Warps; ++w) {
+        if (w < warp) before += sm.part[turn][w].x;
+        total += sm.part[turn][w].x;
+    }
+    const int take = n - static_cast<int>(total & 0xffff);  // of the equal ones
+    int equals = before >> 16, at = static_cast<int>(before & 0xffff) + min(equals, take);
+    for (int j = j_lo; j < j_hi; ++j) {
+        const uint32_t key = keys[j];
+        if (key > nth || (key == nth && equals < take)) {
+            if (at >= lo && at < hi) list[at - lo] = static_cast<uint16_t>(j);
+            if (all) all[at] = j;
+            ++at;
+        }
+        equals += key == nth;
+    }
+    __syncthreads();
+}
+
+template <int D, bool kSparse>
+__global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_constant__ Q8StepParams p) {
     constexpr int NV = D / 8;   // 16-byte vectors of a lane for K, and for V, of a block
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const unsigned FULL = 0xffffffffu;
-    __shared__ Q8DecodeSmem<D> sm;
+    extern __shared__ uint32_t keys[];    // sparse: of every block; behind them the chosen ones of this CTA
+    __shared__ Q8StepSmem<D> sm;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int S = p.cluster, rank = blockIdx.x, h = blockIdx.y, b = p.b0 + blockIdx.z;
-    const int64_t sh = static_cast<int64_t>(b) * p.layer.Hkv + h;
 
-    griddep_wait();
-    griddep_launch_dependents();
-    const int pos = q8_position(p, blockIdx.z, kKernQ8Decode);
-    if (pos < 0) return;  // (the whole cluster)
-    const int full = pos / kQ8Block, row = pos % kQ8Block;
-
-    // ---------------------------------------------------------------- this warp's blocks
-    const int32_t *list = p.blocks ? p.blocks + sh * p.n_blocks : nullptr;
-    const int items = list ? p.n_blocks : full;
-    const int item_hi = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / S);
-    int item = static_cast<int>(static_cast<int64_t>(items) * rank / S) + warp;
-    const int64_t base = sh * p.layer.nblk;
-    const uint8_t *codes = p.layer.codes + base * (2 * kQ8Block * D) + lane * 16;
-    // The next block of the warp, -1 at the end.
-    auto next_block = [&]() {
-        while (item < item_hi) {
-            const int j = list ? list[item] : item;
-            item += kQ8Warps;
-            if (j >= 0 && j < full) return j;
+    // ---------------------------------------------------------------- this CTA's share
+    const bool clustered = p.cluster > 1;
+    if (clustered) cluster_arrive();  // peers may write into this CTA once they have waited on this
+    if (!p.early) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+    int z = 0, pos = -1;
+    if (static_cast<int>(blockIdx.x) < p.ctas) {
+        int hi = p.nseq;  // seq[z].cta0 <= blockIdx.x < seq[hi].cta0
+        while (hi - z > 1) {
+            const int mid = (z + hi) / 2;
+            if (p.seq[mid].cta0 <= static_cast<int>(blockIdx.x)) z = mid; else hi = mid;
         }
-        return -1;
-    };
+        pos = p.pos_dev ? p.pos_dev[p.seq[z].slot] : p.seq[z].pos;
+        if (pos < 0 || pos >= p.cap) {
+            if (threadIdx.x == 0) set_error(p.err, kErrBounds, kKernQ8Decode, 1);
+            pos = -1;
+        }
+    }
+    const int b = p.seq[z].slot, S = p.seq[z].S, unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0;
+    const int me = unit & (S - 1), h = unit / S;
+    if (pos < 0) {  // nothing to do here: the cluster's barriers alone
+        if (kSparse && me == 0 && static_cast<int>(blockIdx.x) < p.ctas) {
+            if (p.early) griddep_wait();
+            for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads)
+                p.blocks[(static_cast<int64_t>(b) * p.layer.Hkv + h) * p.n_blocks + i] = -1;
+        }
+        __syncwarp();
+        if (clustered) {
+            cluster_wait();
+            if (kSparse) cluster_sync_all();
+            cluster_sync_all();
+        }
+        if (p.early) {
+            griddep_wait();
+            griddep_launch_dependents();
+        }
+        return;
+    }
+    const uint32_t first_rank = cluster_ctarank() - me;
+    const int64_t sh = static_cast<int64_t>(b) * p.layer.Hkv + h, base = sh * p.layer.nblk;
+    const int full = pos / kQ8Block, row = pos % kQ8Block;
+    const bool choose = kSparse && full > p.n_blocks;
+    const int items = choose ? p.n_blocks : full;
+    const int item_lo = static_cast<int>(static_cast<int64_t>(items) * me / S);
+    const int item_hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / S);
+    int item = item_lo + warp;
+    uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.layer.nblk);
+    const uint8_t *codes = p.layer.codes + base * (2 * kQ8Block * D) + lane * 16;
     uint4 k[NV], v[NV];
     float2 scale = make_float2(0.f, 0.f);
-    int blk = next_block();
-    if (blk >= 0) {
+    int blk = -1;
+    // The next block of the warp, -1 at the end.
+    auto next_block = [&]() {
+        if (item >= item_hi) return -1;
+        const int j = choose ? static_cast<int>(list[item - item_lo]) : item;
+        item += kQ8Warps;
+        return j;
+    };
+    auto load_first = [&]() {
+        blk = next_block();
+        if (blk < 0) return;
         const uint8_t *c = codes + static_cast<int64_t>(blk) * (2 * kQ8Block * D);
 #pragma unroll
         for (int i = 0; i < NV; ++i) k[i] = q8_load(c + i * 512);
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[i] = q8_load(c + kQ8Block * D + i * 512);
         scale = p.layer.scales[base + blk];
-    }
+    };
+    if (!choose) load_first();
 
-    // ---------------------------------------------------------------- query rows, the new token's row
+    // ---------------------------------------------------------------- query rows, and the new token's
+    // CTA 0 of the S has the rows of the block that the token is in.
     Q8TailPlan plan;
-    __nv_bfloat16 *tail = nullptr;   // rows of K of the block that the token is in; V's follow
-    {
-        const int r = warp * RPW + lane / LPR, sub = lane % LPR;  // 0..7: queries, 8: the key
-        const uint4 x = q8_step_row<D>(p, b, h, r, pos, sub);
-        if (rank == 0) {
-            plan = q8_plan_tail(p.layer.state[sh], pos, pos + 1, true);
-            tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
-            if (plan.from_rows < row) {  // earlier rows of the block are in its codes alone
-                const uint8_t *c = p.layer.codes + (base + full) * (2 * kQ8Block * D);
-                const float2 s = p.layer.scales[base + full];
-                for (int e = threadIdx.x; e < (row - plan.from_rows) * 2 * LPR; e += kQ8Warps * 32) {
-                    const int kv = e / ((row - plan.from_rows) * LPR), w = e % ((row - plan.from_rows) * LPR);
-                    const int rr = plan.from_rows + w / LPR, d0 = w % LPR * 8;
-                    *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + rr) * D + d0) =
-                        q8_row8<D>(c + kv * kQ8Block * D, kv != 0, kv ? s.y : s.x, rr, d0);
-                }
+    __nv_bfloat16 *tail = nullptr;   // where they are kept: 64 rows of K, then of V
+    if (me == 0) {
+        plan = q8_plan_tail(p.layer.state[sh], pos, pos + 1, true);
+        tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
+        for (int e = threadIdx.x; e < plan.from_rows * LPR; e += kQ8Threads) {
+            const int r = e / LPR, d0 = e % LPR * 8;
+            q8_cp_async(&sm.rows[0][r][d0], tail + r * D + d0);
+            q8_cp_async(&sm.rows[1][r][d0], tail + (kQ8Block + r) * D + d0);
+        }
+    }
+    uint4 new_k = make_uint4(0, 0, 0, 0), new_v = new_k;
+    uint32_t top = 0;
+    const int sub = lane % LPR, key_row = p.G < 8 ? p.G : 8;
+    bool has_new = false;
+#pragma unroll 1
+    for (int r0 = warp * RPW; r0 < (p.G < 8 ? 8 : 9); r0 += kQ8Warps * RPW) {  // (uniform in a warp)
+        const int r = r0 + lane / LPR;
+        const bool is_q = r < p.G, is_key = r == key_row && me == 0;
+        NormRow in;
+        in.x = make_uint4(0, 0, 0, 0);
+        if (is_q || is_key)
+            in.x = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.q + (static_cast<int64_t>(b) * p.Hq + h * p.G + r) * D : p.k + sh * D) + sub);
+        if (is_key) new_v = __ldg(reinterpret_cast<const uint4 *>(p.v + sh * D) + sub);
+        uint4 x = in.x;
+        if (p.wq) {
+            in.w = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) in.cs[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (is_q || is_key) {
+                in.w = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.wq : p.wk) + sub);
+                const float4 *tab = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(pos) * (D / 2) + 8 * (sub % (D / 16)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) in.cs[e] = __ldg(tab + e);
             }
-            if (r == 8) {
-                const int64_t at = (static_cast<int64_t>(b) * p.layer.Hkv + h) * D + 8 * sub;
-                const uint4 vx = __ldg(reinterpret_cast<const uint4 *>(p.v + at));
-                *reinterpret_cast<uint4 *>(tail + row * D + 8 * sub) = x;
-                *reinterpret_cast<uint4 *>(tail + (kQ8Block + row) * D + 8 * sub) = vx;
-                if (p.k_held) {
-                    *reinterpret_cast<uint4 *>(p.k_held + at) = x;
-                    *reinterpret_cast<uint4 *>(p.v_held + at) = vx;
-                }
-            }
+            x = norm_rope_row<D>(in, p.eps, sub);
+            if (!is_q && !is_key) x = make_uint4(0, 0, 0, 0);
+        }
+        if (is_key) {
+            new_k = x;
+            has_new = true;
+            *reinterpret_cast<uint4 *>(&sm.rows[0][row][8 * sub]) = x;
+            *reinterpret_cast<uint4 *>(&sm.rows[1][row][8 * sub]) = new_v;
+            x = make_uint4(0, 0, 0, 0);
         }
         // fp16 with one power of two per row: the largest magnitude goes to [256, 512),
         // so bf16's 8 bits survive down to 2^-22 of it.
@@ -209,13 +436,14 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
         mx = max(mx & 0xffffu, mx >> 16);
 #pragma unroll
         for (int o = LPR / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(FULL, mx, o));
+        top = max(top, mx);
         const int ex = min(max(static_cast<int>(mx >> 7), 20), 254) - 127;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 8 - ex) << 23);
+        const float by = __uint_as_float(static_cast<uint32_t>(127 + 8 - ex) << 23);
         uint32_t hw[4];
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            hw[e] = q8_pack_f16(bf16lo(xw[e]) * up, bf16hi(xw[e]) * up);
+            hw[e] = q8_pack_f16(bf16lo(xw[e]) * by, bf16hi(xw[e]) * by);
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hw[e]));
             sum += f.x + f.y;
         }
@@ -230,7 +458,75 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
             }
         }
     }
+    if (kSparse) {
+        top = __reduce_max_sync(FULL, top);
+        if (lane == 0) sm.top[warp] = top;
+    }
+    // What is read so far, nothing that may still run writes; from here on the earlier
+    // kernels have finished.
+    if (p.early) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
+    if (me == 0) {
+        if (plan.from_rows < row) {  // earlier rows of the block are in its codes alone
+            const uint8_t *c = p.layer.codes + (base + full) * (2 * kQ8Block * D);
+            const float2 s = p.layer.scales[base + full];
+            for (int e = threadIdx.x; e < (row - plan.from_rows) * 2 * LPR; e += kQ8Threads) {
+                const int kv = e / ((row - plan.from_rows) * LPR), w = e % ((row - plan.from_rows) * LPR);
+                const int rr = plan.from_rows + w / LPR, d0 = w % LPR * 8;
+                const uint4 x = q8_row8<D>(c + kv * kQ8Block * D, kv != 0, kv ? s.y : s.x, rr, d0);
+                *reinterpret_cast<uint4 *>(&sm.rows[kv][rr][d0]) = x;
+                *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + rr) * D + d0) = x;
+            }
+        }
+        if (has_new) {
+            *reinterpret_cast<uint4 *>(tail + row * D + 8 * sub) = new_k;
+            *reinterpret_cast<uint4 *>(tail + (kQ8Block + row) * D + 8 * sub) = new_v;
+            if (p.k_held) {
+                *reinterpret_cast<uint4 *>(p.k_held + sh * D + 8 * sub) = new_k;
+                *reinterpret_cast<uint4 *>(p.v_held + sh * D + 8 * sub) = new_v;
+            }
+        }
+        q8_cp_wait();
+    }
     __syncthreads();
+    if (clustered) cluster_wait();
+
+    // ---------------------------------------------------------------- the choice
+    if (kSparse) {
+        if (choose) {
+            const uint32_t mx = max(max(sm.top[0], sm.top[1]), max(sm.top[2], sm.top[3]));
+            const float a = __uint_as_float(mx << 16);
+            const float inv = mx < 0x7F80u && a >= kQ8Small ? __fdiv_rn(127.f, a) : 0.f;
+            if (threadIdx.x < D / 2) {
+                int up[2] = {0, 0}, down[2] = {0, 0};
+                if (inv > 0.f) {
+                    for (int r = 0; r < p.G; ++r) {
+                        const uint32_t c = q8_code2(*reinterpret_cast<const uint32_t *>(&sm.qb[r][2 * threadIdx.x]), inv);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int n = static_cast<int>((c >> (8 * e)) & 255u) - 128;
+                            up[e] += max(n, 0);
+                            down[e] += min(n, 0);
+                        }
+                    }
+                }
+                *reinterpret_cast<short2 *>(&sm.up[2 * threadIdx.x]) = make_short2(up[0], up[1]);
+                *reinterpret_cast<short2 *>(&sm.down[2 * threadIdx.x]) = make_short2(down[0], down[1]);
+            }
+            __syncthreads();
+            q8_score<D>(p.layer, base, full, me, S, first_rank, sm, keys);
+        }
+        if (clustered) cluster_sync_all(); else __syncthreads();
+        int32_t *all = me == 0 ? p.blocks + sh * p.n_blocks : nullptr;
+        if (choose) {
+            q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list, all);
+            load_first();
+        } else if (all) {
+            for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads) all[i] = i < full ? i : -1;
+        }
+    }
 
     // ---------------------------------------------------------------- complete blocks
     Q8Acc<D> a;
@@ -315,9 +611,10 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
     }
 
     // ---------------------------------------------------------------- rows in bf16
-    // 16 of them a warp, the last warps first.  Weights as the sum of two bf16 numbers.
+    // 16 of them a warp, the last warps (which have the fewest blocks) first.  Weights as
+    // the sum of two bf16 numbers.
     const int tile = kQ8Warps - 1 - warp;
-    if (rank == 0 && 16 * tile <= row) {
+    if (me == 0 && 16 * tile <= row) {
         const int r0 = 16 * tile + g, r8 = r0 + 8;
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -325,8 +622,8 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
         for (int c = 0; c < D / 32; ++c) {
             const int d0 = 32 * c + 8 * t;
             const uint4 q = *reinterpret_cast<const uint4 *>(&sm.qb[g][d0]);
-            const uint4 x = r0 <= row ? *reinterpret_cast<const uint4 *>(tail + r0 * D + d0) : zero;
-            const uint4 y = r8 <= row ? *reinterpret_cast<const uint4 *>(tail + r8 * D + d0) : zero;
+            const uint4 x = r0 <= row ? *reinterpret_cast<const uint4 *>(&sm.rows[0][r0][d0]) : zero;
+            const uint4 y = r8 <= row ? *reinterpret_cast<const uint4 *>(&sm.rows[0][r8][d0]) : zero;
             q8_mma_bf16(s, x.x, y.x, x.y, y.y, q.x, q.y);
             q8_mma_bf16(s, x.z, y.z, x.w, y.w, q.z, q.w);
         }
@@ -349,14 +646,13 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
         q8_mma_bf16(l, kOne, kOne, kOne, kOne, lo[0], lo[1]);
         a.l[0] += l[0];
         a.l[1] += l[1];
-        const __nv_bfloat16 *vt = tail + kQ8Block * D + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {  // 8 dims of the lane's D / 8, of 4 keys
             uint4 x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 16 * tile + 2 * t + (e & 1) + 8 * (e >> 1);
-                x[e] = r <= row ? *reinterpret_cast<const uint4 *>(vt + r * D + 8 * i) : zero;
+                x[e] = r <= row ? *reinterpret_cast<const uint4 *>(&sm.rows[1][r][g * (D / 8) + 8 * i]) : zero;
             }
             const uint32_t xa[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, xb[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
             const uint32_t xc[4] = {x[2].x, x[2].y, x[2].z, x[2].w}, xd[4] = {x[3].x, x[3].y, x[3].z, x[3].w};
@@ -372,8 +668,9 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
             }
         }
     }
+    __syncthreads();  // the rows' shared memory becomes the sums'
 
-    // ---------------------------------------------------------------- merge: warps, then splits
+    // ---------------------------------------------------------------- merge: warps, then CTAs
     if (g == 0) {
         sm.ref[warp][2 * t] = a.ref[0];
         sm.ref[warp][2 * t + 1] = a.ref[1];
@@ -386,65 +683,83 @@ __global__ void __launch_bounds__(kQ8Warps * 32, 1) q8_decode_kernel(const __gri
         *reinterpret_cast<float2 *>(&sm.o[warp][2 * t + 1][16 * m + 2 * g]) = make_float2(a.o[m][1], a.o[m][3]);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.G * D; e += kQ8Warps * 32) {
-        const int head = e / D, slot = e % D;
-        float top = kQ8NoRef;
+    // CTA r of the S finishes outputs r E .. (r + 1) E - 1 of the group's G D.
+    const int E = p.G * D / S;
+    __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h * p.G) * D;
+    const uint32_t to_o = smem_u32(sm.got_o), to_l = smem_u32(&sm.got_l[me][0]);
+    for (int e = 2 * threadIdx.x; e < p.G * D; e += 2 * kQ8Threads) {
+        const int head = e / D, slot = q8_slot<D>(e % D);
+        float f[kQ8Warps], most = kQ8NoRef, l = 0.f;
 #pragma unroll
-        for (int w = 0; w < kQ8Warps; ++w) top = fmaxf(top, sm.ref[w][head]);
-        float o = 0.f, l = 0.f;
+        for (int w = 0; w < kQ8Warps; ++w) most = fmaxf(most, sm.ref[w][head]);
+        float2 o = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kQ8Warps; ++w) {
-            const float f = q8_exp2(sm.ref[w][head] - top);
-            o = fmaf(f, sm.o[w][head][slot], o);
-            l = fmaf(f, sm.l[w][head], l);
+            f[w] = q8_exp2(sm.ref[w][head] - most);
+            const float2 x = *reinterpret_cast<const float2 *>(&sm.o[w][head][slot]);
+            o.x = fmaf(f[w], x.x, o.x);
+            o.y = fmaf(f[w], x.y, o.y);
+            l = fmaf(f[w], sm.l[w][head], l);
         }
-        sm.cta_o[head][slot] = o;
-        if (slot == 0) {
-            sm.cta_ref[head] = top;
-            sm.cta_l[head] = l;
+        if (S == 1) {
+            const float inv = 16777216.f / l;
+            *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
+        } else {
+            const int r = e / E;
+            q8_st_cluster(map_rank(to_o + (me * E + e - r * E) * 4, first_rank + r), o.x, o.y);
+            if (e % D < 2 * S)  // the head's first S pairs of dims: one CTA each
+                q8_st_cluster(map_rank(to_l + head * 8, first_rank + e % D / 2), most, l);
         }
     }
-    if (S > 1) cluster_sync_all(); else __syncthreads();
-    const int pairs = p.G * D / 2;
-    const int e_lo = pairs * rank / S, e_hi = pairs * (rank + 1) / S;
-    const uint32_t a_o = smem_u32(&sm.cta_o[0][0]), a_ref = smem_u32(sm.cta_ref), a_l = smem_u32(sm.cta_l);
-    for (int e = e_lo + threadIdx.x; e < e_hi; e += kQ8Warps * 32) {
-        const int head = 2 * e / D, d = 2 * e % D;
-        const uint32_t at = a_o + (head * D + q8_slot<D>(d)) * 4;
-        float ref[kQ8MaxCluster], top = kQ8NoRef;
-#pragma unroll
-        for (int r = 0; r < kQ8MaxCluster; ++r) {
-            ref[r] = r < S ? ld_cluster_f32(map_rank(a_ref + 4 * head, r)) : kQ8NoRef;
-            top = fmaxf(top, ref[r]);
+    if (clustered) cluster_sync_all();
+    if (S > 1) {
+        for (int i = 2 * threadIdx.x; i < E; i += 2 * kQ8Threads) {
+            const int e = me * E + i, head = e / D;
+            float most = kQ8NoRef, l = 0.f;
+            for (int r = 0; r < S; ++r) most = fmaxf(most, sm.got_l[r][head].x);
+            float2 o = make_float2(0.f, 0.f);
+            for (int r = 0; r < S; ++r) {
+                const float2 x = *reinterpret_cast<const float2 *>(&sm.got_o[r * E + i]), y = sm.got_l[r][head];
+                const float f = q8_exp2(y.x - most);
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                l = fmaf(f, y.y, l);
+            }
+            const float inv = 16777216.f / l;
+            *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         }
-        float o0 = 0.f, o1 = 0.f, l = 0.f;
-#pragma unroll
-        for (int r = 0; r < kQ8MaxCluster; ++r) {
-            if (r >= S) continue;
-            const float f = q8_exp2(ref[r] - top);
-            o0 = fmaf(f, ld_cluster_f32(map_rank(at, r)), o0);
-            o1 = fmaf(f, ld_cluster_f32(map_rank(at + 4, r)), o1);
-            l = fmaf(f, ld_cluster_f32(map_rank(a_l + 4 * head, r)), l);
-        }
-        const float inv = 1.f / l;
-        *reinterpret_cast<uint32_t *>(p.out + (static_cast<int64_t>(b) * p.Hq + h * p.G + head) * D + d) =
-            pack_bf16(o0 * inv * 16777216.f, o1 * inv * 16777216.f);
     }
-    if (rank == 0) {
-        if (row == kQ8Block - 1)  // the block is complete
-            q8_seal<D>(p.layer, sh, full, sm.seal, [&](int kv, int r, int d0) {
-                return *reinterpret_cast<const uint4 *>(tail + (kv * kQ8Block + r) * D + d0);
-            });
+    if (me == 0) {
+        if (row == kQ8Block - 1) {  // the block is complete
+            __syncthreads();
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv)
+                q8_seal<D>(p.layer, sh, full, kv, warp, sm.seal, [&](int kv_, int r, int d0) {
+                    return *reinterpret_cast<const uint4 *>(tail + (kv_ * kQ8Block + r) * D + d0);
+                });
+        }
         if (threadIdx.x == 0) p.layer.state[sh] = plan.next;
     }
-    if (S > 1) cluster_sync_all();  // peers may still read this CTA's sums
 }
 
 // ------------------------------------------------------------------ launch
-cudaError_t launch_q8_decode(const Q8StepParams &p, int D, int batch, cudaStream_t stream) {
+template <int D, bool kSparse>
+static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
+    static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
+    auto kern = q8_decode_kernel<D, kSparse>;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 32 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && kSparse)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8MaxBlocks * 6);
+        if (e != cudaSuccess) return e;
+        if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(p.cluster, p.layer.Hkv, batch);
-    cfg.blockDim = dim3(kQ8Warps * 32);
+    cfg.gridDim = dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster);
+    cfg.blockDim = dim3(kQ8Threads);
+    cfg.dynamicSmemBytes = kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + (static_cast<size_t>(p.n_blocks) * 2 + 15) / 16 * 16 : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -455,7 +770,12 @@ cudaError_t launch_q8_decode(const Q8StepParams &p, int D, int batch, cudaStream
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return D == 128 ? cudaLaunchKernelEx(&cfg, q8_decode_kernel<128>, p) : cudaLaunchKernelEx(&cfg, q8_decode_kernel<64>, p);
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+cudaError_t launch_q8_decode(const Q8StepParams &p, int D, cudaStream_t stream) {
+    if (p.blocks) return D == 128 ? q8_launch<128, true>(p, stream) : q8_launch<64, true>(p, stream);
+    return D == 128 ? q8_launch<128, false>(p, stream) : q8_launch<64, false>(p, stream);
 }
 
 }  // namespace qa

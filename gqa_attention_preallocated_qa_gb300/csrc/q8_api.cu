@@ -3,9 +3,10 @@
 // qa_api.cu an unsupported shape or an invalid argument returns a status before
 // anything is enqueued.
 //
-// Every kernel of this cache waits for the kernel before it on the stream before it
-// reads or writes anything, and lets the next one start only then: launches overlap
-// in their set-up alone.
+// Every kernel of this cache waits for the one before it on the stream before it writes
+// anything, and lets the next one start only after that: while a kernel sets up, at most
+// its predecessor still runs.  A step reads before its wait where the launch record says
+// that the predecessor writes another layer or nothing here.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -159,31 +160,30 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
     p.eps = g.rms_eps;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.head_dim)));
     const qa::StreamRef at = qa::stream_ref(s, c->device);
+    const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
     for (int b0 = 0; b0 < batch; b0 += qa::kQ8MaxSeqPerLaunch) {
         const int n = std::min(qa::kQ8MaxSeqPerLaunch, batch - b0);
-        p.b0 = b0;
-        int full = a.pos_dev ? (g.capacity - 1) / qa::kQ8Block : 0;
-        for (int i = 0; i < n && !a.pos_dev; ++i) {
-            p.pos[i] = a.positions[b0 + i];
-            full = std::max(full, p.pos[i] / qa::kQ8Block);
+        for (int i = 0; i < n; ++i) p.seq[i] = {a.pos_dev ? g.capacity - 1 : a.positions[b0 + i], b0 + i, 0, 1};
+        // The longest sequences, which have the most CTAs, first.
+        std::stable_sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos > y.pos; });
+        int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
+        for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(p.seq[i].pos / qa::kQ8Block, a.n_blocks);
+        p.cluster = qa::q8_plan_step(2 * c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
+        p.nseq = n;
+        p.ctas = 0;
+        for (int i = 0; i < n; ++i) {
+            p.seq[i].cta0 = p.ctas;
+            p.seq[i].S = splits[i];
+            p.ctas += splits[i] * g.n_kv_heads;
         }
-        const int64_t pairs = static_cast<int64_t>(n) * g.n_kv_heads;
-        if (a.blocks) {
-            p.cluster = qa::q8_select_cluster(c->num_sms, pairs, full);
-            if (qa::launch_q8_select(p, g.head_dim, n, s) != cudaSuccess) {
-                cudaGetLastError();
-                return QA_ERR_CUDA;
-            }
-            qa::launch_order().barrier(at);
-            c->launches[QA_Q8_KERNEL_SELECT]++;
-        }
-        p.cluster = qa::q8_decode_cluster(c->num_sms, pairs, a.blocks ? std::min(full, a.n_blocks) : full);
-        if (qa::launch_q8_decode(p, g.head_dim, n, s) != cudaSuccess) {
+        p.early = !a.pos_dev && qa::launch_order().layer_settled(at, c, layer, resident) ? 1 : 0;
+        if (qa::launch_q8_decode(p, g.head_dim, s) != cudaSuccess) {
             cudaGetLastError();
             return QA_ERR_CUDA;
         }
-        qa::launch_order().barrier(at);
-        c->launches[QA_Q8_KERNEL_DECODE]++;
+        // It lets the next launch start once it has itself waited.
+        qa::launch_order().admit(at, c, layer, p.ctas, 1, false, resident);
+        c->launches[a.blocks ? QA_Q8_KERNEL_SPARSE : QA_Q8_KERNEL_DECODE]++;
     }
     return QA_OK;
 }
@@ -377,7 +377,8 @@ QA_API qa_status qa_q8_append(qa_q8_cache *c, int layer, int batch, const int32_
                     cudaGetLastError();
                     return QA_ERR_CUDA;
                 }
-                qa::launch_order().barrier(qa::stream_ref(s, c->device));
+                // It lets the next launch start once it has itself waited, while it writes.
+                qa::launch_order().admit(qa::stream_ref(s, c->device), c, layer, 1, 1, false, 1);
                 c->launches[QA_Q8_KERNEL_WRITE]++;
             }
             for (int i = 0; i < n; ++i) row0 += ntok[s0 + i];

@@ -92,15 +92,14 @@ struct Q8SealSmem {
     uint32_t least[4][D / 2], most[4][D / 2];
 };
 
-// Makes block `blk` of (slot, head) `sh` complete from its 64 rows: load8(kv, row, d0)
-// gives 8 dims of one.  Called by 256 threads together; the first four warps take K, the
-// others V, 16 rows each.
+// Makes K (kv 0) or V of block `blk` of (slot, head) `sh` complete from its 64 rows:
+// load8(kv, row, d0) gives 8 dims of one.  kt: the 16 rows of this warp, of which four
+// take part; every thread of the CTA calls this together, with its warp's kv.
 template <int D, typename Load>
-__device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, Q8SealSmem<D> &sm, Load &&load8) {
+__device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, int kv, int kt, Q8SealSmem<D> &sm, Load &&load8) {
     constexpr int NX = D / 16;  // loads of 8 dims per lane
     const unsigned FULL = 0xffffffffu;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int kv = warp >> 2, kt = warp & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint4 x[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
@@ -116,7 +115,7 @@ __device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, Q
         mx = __vmaxu2(mx, x[i].w & 0x7fff7fffu);
     }
     mx = __reduce_max_sync(FULL, max(mx & 0xffffu, mx >> 16));
-    if (lane == 0) sm.top[warp] = mx;
+    if (lane == 0) sm.top[4 * kv + kt] = mx;
     if (kv == 0) {
         // Codes rise with values: the least code of a dim is its least value's.
 #pragma unroll
@@ -183,7 +182,7 @@ __device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, Q
     const float s = finite ? (used ? __fdiv_rn(a, 127.f) : 0.f) : __uint_as_float(0x7fffffffu);
     if (kt == 0 && lane == 0) reinterpret_cast<float *>(l.scales + sh * l.nblk + blk)[kv] = s;
     if (kv == 0) {
-        const int i = threadIdx.x;  // 0..127: words of least, then of most
+        const int i = 32 * kt + lane;  // words of least, then of most
         if (i < D) {
             const bool high = i >= D / 2;
             const int w = i % (D / 2);

@@ -12,11 +12,11 @@
 namespace qa {
 
 // Kernel numbers in the error word of an 8-bit cache.
-constexpr uint32_t kKernQ8Rows = 6, kKernQ8Decode = 7, kKernQ8Select = 8;
+constexpr uint32_t kKernQ8Rows = 6, kKernQ8Decode = 7;
 
 constexpr int kQ8MaxSeqPerLaunch = 64;  // sequences carried in the parameters of one launch
 constexpr int kQ8MaxBlocks = 16384;     // blocks of a sequence: the selection's scores fit shared memory
-constexpr int kQ8MaxCluster = 8;        // CTAs that share a (sequence, kv head)
+constexpr int kQ8MaxSplits = 16;    // CTAs that share a (sequence, kv head)
 
 // One layer.  A block's codes are the 64 D bytes of K, then those of V, each in
 // the order that the decode kernel's MMA fragments take them (q8_device.cuh).
@@ -48,6 +48,12 @@ struct Q8RowsParams {
 };
 static_assert(sizeof(Q8RowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
+// A launched sequence: the position of its new token, its place in the cache, and its
+// first CTA; each kv head has S of them, a power of two.
+struct alignas(16) Q8Seq {
+    int pos, slot, cta0, S;
+};
+
 struct Q8StepParams {
     Q8Layer layer;
     const __nv_bfloat16 *q, *k, *v;      // [batch][Hq|Hkv][D]
@@ -55,15 +61,15 @@ struct Q8StepParams {
     __nv_bfloat16 *out;
     __nv_bfloat16 *k_held, *v_held;      // the new rows as the step attends to them (may be null)
     const float2 *rope;                  // [cap][D/2] (cos, sin)
-    const int32_t *pos_dev;              // device positions (null: pos[])
-    int32_t *blocks;                     // [batch][Hkv][n_blocks]: chosen blocks (null: every block)
+    const int32_t *pos_dev;              // device positions, by slot (null: Q8Seq::pos)
+    int32_t *blocks;                     // [batch][Hkv][n_blocks]: receives the chosen blocks (null: all are)
     uint32_t *err;
     int n_blocks;
     int Hq, G, cap;
-    int b0;                              // sequence of launched sequence 0
-    int cluster;                         // CTAs of a (sequence, kv head)
+    int nseq, ctas, cluster;             // sequences, CTAs with work, CTAs of a cluster (a multiple of every S)
+    int early;                           // nothing that may still run writes this layer
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
-    int pos[kQ8MaxSeqPerLaunch];
+    Q8Seq seq[kQ8MaxSeqPerLaunch];       // by falling S
 };
 static_assert(sizeof(Q8StepParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
@@ -79,8 +85,7 @@ QA_HD int q8_read_items(int start, int end) { return (end - 1) / kQ8Block - star
 
 cudaError_t launch_q8_write(const Q8RowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8RowsParams &p, int D, cudaStream_t stream);
-cudaError_t launch_q8_decode(const Q8StepParams &p, int D, int batch, cudaStream_t stream);
-cudaError_t launch_q8_select(const Q8StepParams &p, int D, int batch, cudaStream_t stream);
+cudaError_t launch_q8_decode(const Q8StepParams &p, int D, cudaStream_t stream);
 
 // Shared with the other caches' host sides.
 bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);

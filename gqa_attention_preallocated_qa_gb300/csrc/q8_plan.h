@@ -7,17 +7,28 @@
 
 namespace qa {
 
-// Decode: `pairs` (sequence, kv head) pairs, at most `items` blocks each, one CTA of
-// 8 warps per SM.
-inline int q8_decode_cluster(int num_sms, int64_t pairs, int items) {
-    const int64_t fit = std::max<int64_t>(1, num_sms / pairs);
-    return static_cast<int>(std::min<int64_t>({8, fit, std::max(1, (items + 7) / 8)}));
+// A sequence's work in a step, in blocks of 16 KB (D = 128): all complete ones, or the chosen
+// ones and the scoring of all (their bounds are 1/64 of their codes).
+inline int q8_step_work(int full, int n_blocks) {
+    return n_blocks > 0 && full > n_blocks ? n_blocks + full / 32 : full;
 }
 
-// Selection: a CTA scores 64 blocks in one go.
-inline int q8_select_cluster(int num_sms, int64_t pairs, int blocks) {
-    const int64_t fit = std::max<int64_t>(1, 2 * num_sms / pairs);
-    return static_cast<int>(std::min<int64_t>({8, fit, std::max(1, blocks / 64)}));
+// splits[i], powers of two up to `most`, for n sequences of work[i] blocks for each of Hkv
+// kv heads: as few blocks for a warp (4 of them a CTA) as leave every CTA its place on the
+// device (`room` of them).  Returns the largest.
+inline int q8_plan_step(int64_t room, int Hkv, int most, int n, const int *work, int *splits) {
+    for (int per = 1;; ++per) {
+        int64_t ctas = 0;
+        int top = 1;
+        for (int i = 0; i < n; ++i) {
+            int s = 1;
+            while (s < most && static_cast<int64_t>(s) * 4 * per < work[i]) s *= 2;
+            splits[i] = s;
+            top = std::max(top, s);
+            ctas += static_cast<int64_t>(Hkv) * s;
+        }
+        if (ctas <= room || top == 1) return top;
+    }
 }
 
 }  // namespace qa

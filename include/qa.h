@@ -545,7 +545,7 @@ enum {
     QA_Q8_KERNEL_READ = 2,         /* K6: rows out of the cache */
     QA_Q8_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace (and the join of its parts) */
     QA_Q8_KERNEL_DECODE = 4,       /* K7: decode steps */
-    QA_Q8_KERNEL_SELECT = 5,       /* K8: the choice of a sparse step's blocks */
+    QA_Q8_KERNEL_SPARSE = 5,       /* K7: sparse steps */
     QA_Q8_NUM_KERNELS = 6
 };
 
