@@ -41,7 +41,8 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
     const int kv_of_warp = threadIdx.x >> 7, kt = threadIdx.x >> 5 & 3;  // four warps for K, four for V
     if (i > 0) {  // every row of the block is new
         const int blk = first + i;
-        q8_seal<D>(p.layer, sh, blk, kv_of_warp, kt, sm, [&](int kv, int r, int d0) { return source8(kv, blk * kQ8Block + r, d0); });
+        q8_store<D>(p.layer, sh, blk, kv_of_warp, kt,
+                    q8_seal<D>(kv_of_warp, kt, sm, [&](int kv, int r, int d0) { return source8(kv, blk * kQ8Block + r, d0); }));
         return;
     }
     const Q8Tail state = p.layer.state[sh];
@@ -55,7 +56,11 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
             return *reinterpret_cast<const uint4 *>(q8_tail_rows<D>(p.layer, sh, plan.from, kv) + r * D + d0);
         return q8_row8<D>(codes + kv * kQ8Block * D, kv != 0, kv ? scale.y : scale.x, r, d0);
     };
-    if (end >= (first + 1) * kQ8Block) q8_seal<D>(p.layer, sh, first, kv_of_warp, kt, sm, row8);
+    if (end >= (first + 1) * kQ8Block) {
+        const Q8Sealed<D> done = q8_seal<D>(kv_of_warp, kt, sm, row8);
+        __syncthreads();  // every warp has read what it needs of the old codes
+        q8_store<D>(p.layer, sh, first, kv_of_warp, kt, done);
+    }
     if (plan.dst >= 0) {
         const int last = (end - 1) / kQ8Block, rest = end - last * kQ8Block;
         const int from = last == first ? plan.from_rows : 0;  // (below it the buffer has them)

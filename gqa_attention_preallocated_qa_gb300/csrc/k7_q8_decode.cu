@@ -144,8 +144,9 @@ struct alignas(16) Q8StepSmem {
     union {
         __nv_bfloat16 rows[2][kQ8Block][D + 8];   // K and V of the block that the new token is in
         float o[kQ8Warps][8][D + 8];              // then a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
-        Q8SealSmem<D> seal;                       // then these
     };
+    __nv_bfloat16 fresh[2][D];      // the new rows
+    Q8SealSmem<D> seal;
     float ref[kQ8Warps][8], l[kQ8Warps][8];
     // From the CTAs of the (sequence, kv head): references and sums of weights (of a
     // head), and this CTA's share of the outputs.
@@ -232,10 +233,10 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
 }
 
 // The n blocks of the largest of keys[0 .. full - 1] (full > n), in rising order: those at
-// places lo .. hi - 1 go to list[], all of them to `all` (may be null).
+// places lo .. hi - 1 go to list[].
 template <int D>
 __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n, int lo, int hi, Q8StepSmem<D> &sm,
-                                          uint16_t *list, int32_t *all) {
+                                          uint16_t *list) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int R = 8;  // keys of a thread in registers; the others are read again
     uint32_t mine[R];
@@ -291,7 +292,6 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
         const uint32_t key = keys[j];
         if (key > nth || (key == nth && equals < take)) {
             if (at >= lo && at < hi) list[at - lo] = static_cast<uint16_t>(j);
-            if (all) all[at] = j;
             ++at;
         }
         equals += key == nth;
@@ -311,10 +311,10 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     // ---------------------------------------------------------------- this CTA's share
     const bool clustered = p.cluster > 1;
     if (clustered) cluster_arrive();  // peers may write into this CTA once they have waited on this
-    if (!p.early) {
-        griddep_wait();
-        griddep_launch_dependents();
-    }
+    // An early launch signals at once, reads and computes beside its predecessors, which
+    // write nothing that it reads, and waits for them before it writes.
+    if (!p.early) griddep_wait();
+    griddep_launch_dependents();
     int z = 0, pos = -1;
     if (static_cast<int>(blockIdx.x) < p.ctas) {
         int hi = p.nseq;  // seq[z].cta0 <= blockIdx.x < seq[hi].cta0
@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const int b = p.seq[z].slot, S = p.seq[z].S, unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0;
     const int me = unit & (S - 1), h = unit / S;
     if (pos < 0) {  // nothing to do here: the cluster's barriers alone
+        griddep_wait();
         if (kSparse && me == 0 && static_cast<int>(blockIdx.x) < p.ctas) {
-            if (p.early) griddep_wait();
             for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads)
                 p.blocks[(static_cast<int64_t>(b) * p.layer.Hkv + h) * p.n_blocks + i] = -1;
         }
@@ -341,10 +341,6 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             cluster_wait();
             if (kSparse) cluster_sync_all();
             cluster_sync_all();
-        }
-        if (p.early) {
-            griddep_wait();
-            griddep_launch_dependents();
         }
         return;
     }
@@ -393,10 +389,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             q8_cp_async(&sm.rows[1][r][d0], tail + (kQ8Block + r) * D + d0);
         }
     }
-    uint4 new_k = make_uint4(0, 0, 0, 0), new_v = new_k;
     uint32_t top = 0;
     const int sub = lane % LPR, key_row = p.G < 8 ? p.G : 8;
-    bool has_new = false;
 #pragma unroll 1
     for (int r0 = warp * RPW; r0 < (p.G < 8 ? 8 : 9); r0 += kQ8Warps * RPW) {  // (uniform in a warp)
         const int r = r0 + lane / LPR;
@@ -405,6 +399,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         in.x = make_uint4(0, 0, 0, 0);
         if (is_q || is_key)
             in.x = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.q + (static_cast<int64_t>(b) * p.Hq + h * p.G + r) * D : p.k + sh * D) + sub);
+        uint4 new_v;
         if (is_key) new_v = __ldg(reinterpret_cast<const uint4 *>(p.v + sh * D) + sub);
         uint4 x = in.x;
         if (p.wq) {
@@ -421,10 +416,10 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             if (!is_q && !is_key) x = make_uint4(0, 0, 0, 0);
         }
         if (is_key) {
-            new_k = x;
-            has_new = true;
             *reinterpret_cast<uint4 *>(&sm.rows[0][row][8 * sub]) = x;
             *reinterpret_cast<uint4 *>(&sm.rows[1][row][8 * sub]) = new_v;
+            *reinterpret_cast<uint4 *>(&sm.fresh[0][8 * sub]) = x;
+            *reinterpret_cast<uint4 *>(&sm.fresh[1][8 * sub]) = new_v;
             x = make_uint4(0, 0, 0, 0);
         }
         // fp16 with one power of two per row: the largest magnitude goes to [256, 512),
@@ -462,14 +457,9 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         top = __reduce_max_sync(FULL, top);
         if (lane == 0) sm.top[warp] = top;
     }
-    // What is read so far, nothing that may still run writes; from here on the earlier
-    // kernels have finished.
-    if (p.early) {
-        griddep_wait();
-        griddep_launch_dependents();
-    }
     if (me == 0) {
         if (plan.from_rows < row) {  // earlier rows of the block are in its codes alone
+            griddep_wait();
             const uint8_t *c = p.layer.codes + (base + full) * (2 * kQ8Block * D);
             const float2 s = p.layer.scales[base + full];
             for (int e = threadIdx.x; e < (row - plan.from_rows) * 2 * LPR; e += kQ8Threads) {
@@ -478,14 +468,6 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 const uint4 x = q8_row8<D>(c + kv * kQ8Block * D, kv != 0, kv ? s.y : s.x, rr, d0);
                 *reinterpret_cast<uint4 *>(&sm.rows[kv][rr][d0]) = x;
                 *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + rr) * D + d0) = x;
-            }
-        }
-        if (has_new) {
-            *reinterpret_cast<uint4 *>(tail + row * D + 8 * sub) = new_k;
-            *reinterpret_cast<uint4 *>(tail + (kQ8Block + row) * D + 8 * sub) = new_v;
-            if (p.k_held) {
-                *reinterpret_cast<uint4 *>(p.k_held + sh * D + 8 * sub) = new_k;
-                *reinterpret_cast<uint4 *>(p.v_held + sh * D + 8 * sub) = new_v;
             }
         }
         q8_cp_wait();
@@ -519,12 +501,9 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             q8_score<D>(p.layer, base, full, me, S, first_rank, sm, keys);
         }
         if (clustered) cluster_sync_all(); else __syncthreads();
-        int32_t *all = me == 0 ? p.blocks + sh * p.n_blocks : nullptr;
         if (choose) {
-            q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list, all);
+            q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
             load_first();
-        } else if (all) {
-            for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads) all[i] = i < full ? i : -1;
         }
     }
 
@@ -668,6 +647,15 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             }
         }
     }
+    const bool completes = me == 0 && row == kQ8Block - 1;  // the block that the token is in
+    Q8Sealed<D> sealed[2];
+    if (completes) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+            sealed[kv] = q8_seal<D>(kv, warp, sm.seal, [&](int, int r, int d0) {
+                return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
+            });
+    }
     __syncthreads();  // the rows' shared memory becomes the sums'
 
     // ---------------------------------------------------------------- merge: warps, then CTAs
@@ -703,6 +691,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         }
         if (S == 1) {
             const float inv = 16777216.f / l;
+            griddep_wait();
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         } else {
             const int r = e / E;
@@ -712,6 +701,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         }
     }
     if (clustered) cluster_sync_all();
+    griddep_wait();  // everything before has finished: from here on this writes
     if (S > 1) {
         for (int i = 2 * threadIdx.x; i < E; i += 2 * kQ8Threads) {
             const int e = me * E + i, head = e / D;
@@ -729,14 +719,25 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         }
     }
+    if (kSparse) {
+        int32_t *to = p.blocks + sh * p.n_blocks;
+        if (choose) {
+            for (int i = item_lo + threadIdx.x; i < item_hi; i += kQ8Threads) to[i] = list[i - item_lo];
+        } else if (me == 0) {
+            for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads) to[i] = i < full ? i : -1;
+        }
+    }
     if (me == 0) {
-        if (row == kQ8Block - 1) {  // the block is complete
-            __syncthreads();
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv)
-                q8_seal<D>(p.layer, sh, full, kv, warp, sm.seal, [&](int kv_, int r, int d0) {
-                    return *reinterpret_cast<const uint4 *>(tail + (kv_ * kQ8Block + r) * D + d0);
-                });
+        if (threadIdx.x < 2 * LPR) {
+            const int kv = threadIdx.x / LPR, d0 = threadIdx.x % LPR * 8;
+            const uint4 x = *reinterpret_cast<const uint4 *>(&sm.fresh[kv][d0]);
+            *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + row) * D + d0) = x;
+            __nv_bfloat16 *held = kv ? p.v_held : p.k_held;
+            if (held) *reinterpret_cast<uint4 *>(held + sh * D + d0) = x;
+        }
+        if (completes) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) q8_store<D>(p.layer, sh, full, kv, warp, sealed[kv]);
         }
         if (threadIdx.x == 0) p.layer.state[sh] = plan.next;
     }

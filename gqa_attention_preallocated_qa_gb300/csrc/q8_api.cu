@@ -4,9 +4,9 @@
 // anything is enqueued.
 //
 // Every kernel of this cache waits for the one before it on the stream before it writes
-// anything, and lets the next one start only after that: while a kernel sets up, at most
-// its predecessor still runs.  A step reads before its wait where the launch record says
-// that the predecessor writes another layer or nothing here.
+// anything.  A step signals the next launch at once, reads and computes before that wait
+// where the launch record (launch_order.h) says that nothing that may still run writes its
+// layer; otherwise it waits first.  The others wait, then signal.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -181,8 +181,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
             cudaGetLastError();
             return QA_ERR_CUDA;
         }
-        // It lets the next launch start once it has itself waited.
-        qa::launch_order().admit(at, c, layer, p.ctas, 1, false, resident);
+        qa::launch_order().admit(at, c, layer, p.ctas, 1, p.early != 0, resident);
         c->launches[a.blocks ? QA_Q8_KERNEL_SPARSE : QA_Q8_KERNEL_DECODE]++;
     }
     return QA_OK;

@@ -92,11 +92,20 @@ struct Q8SealSmem {
     uint32_t least[4][D / 2], most[4][D / 2];
 };
 
-// Makes K (kv 0) or V of block `blk` of (slot, head) `sh` complete from its 64 rows:
-// load8(kv, row, d0) gives 8 dims of one.  kt: the 16 rows of this warp, of which four
-// take part; every thread of the CTA calls this together, with its warp's kv.
+// A warp's part of a complete block's K or V: 16 rows.
+template <int D>
+struct Q8Sealed {
+    uint4 codes[D / 32];
+    float scale;
+    uint32_t bounds;  // K: codes of two dims, least ones from the first D / 2 lanes of the four warps, then largest
+};
+
+// K (kv 0) or V of a block from its 64 rows: load8(kv, row, d0) gives 8 dims of one.  kt:
+// the 16 rows of this warp, of which four take part; every thread of the CTA calls this
+// together, with its warp's kv.
 template <int D, typename Load>
-__device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, int kv, int kt, Q8SealSmem<D> &sm, Load &&load8) {
+__device__ __forceinline__ Q8Sealed<D> q8_seal(int kv, int kt, Q8SealSmem<D> &sm, Load &&load8) {
+    Q8Sealed<D> done;
     constexpr int NX = D / 16;  // loads of 8 dims per lane
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -154,8 +163,6 @@ __device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, i
     const float a = __uint_as_float(mx << 16);
     const bool used = finite && a >= kQ8Small;
     const float inv = used ? __fdiv_rn(127.f, a) : 0.f;
-    uint8_t *codes = l.codes + (sh * l.nblk + blk) * static_cast<int64_t>(2 * kQ8Block * D) + kv * kQ8Block * D;
-    uint4 *out = reinterpret_cast<uint4 *>(codes) + kt * (D / 32) * 32 + lane;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
         uint32_t w[4];
@@ -177,23 +184,34 @@ __device__ __forceinline__ void q8_seal(const Q8Layer &l, int64_t sh, int blk, i
                 w[e] = __byte_perm(q8_code2(pa, inv), q8_code2(pb, inv), 0x5140);
             }
         }
-        out[c * 32] = finite ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(kQ8Zero, kQ8Zero, kQ8Zero, kQ8Zero);
+        done.codes[c] = finite ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(kQ8Zero, kQ8Zero, kQ8Zero, kQ8Zero);
     }
-    const float s = finite ? (used ? __fdiv_rn(a, 127.f) : 0.f) : __uint_as_float(0x7fffffffu);
-    if (kt == 0 && lane == 0) reinterpret_cast<float *>(l.scales + sh * l.nblk + blk)[kv] = s;
+    done.scale = finite ? (used ? __fdiv_rn(a, 127.f) : 0.f) : __uint_as_float(0x7fffffffu);
+    done.bounds = 0;
     if (kv == 0) {
-        const int i = 32 * kt + lane;  // words of least, then of most
+        const int i = 32 * kt + lane;
         if (i < D) {
             const bool high = i >= D / 2;
             const int w = i % (D / 2);
             uint32_t v = high ? sm.most[0][w] : sm.least[0][w];
 #pragma unroll
             for (int k = 1; k < 4; ++k) v = high ? bf16x2_max(v, sm.most[k][w]) : bf16x2_min(v, sm.least[k][w]);
-            const uint32_t code = (finite ? q8_code2(v, inv) : 0x8080u) ^ 0x8080u;  // without the offset
-            reinterpret_cast<uint16_t *>(l.bounds + (sh * l.nblk + blk) * static_cast<int64_t>(2 * D))[i] =
-                static_cast<uint16_t>(code);
+            done.bounds = (finite ? q8_code2(v, inv) : 0x8080u) ^ 0x8080u;  // without the offset
         }
     }
+    return done;
+}
+
+// Into block `blk` of (slot, head) `sh`.
+template <int D>
+__device__ __forceinline__ void q8_store(const Q8Layer &l, int64_t sh, int blk, int kv, int kt, const Q8Sealed<D> &x) {
+    const int lane = threadIdx.x & 31, i = 32 * kt + lane;
+    const int64_t at = sh * l.nblk + blk;
+    uint4 *out = reinterpret_cast<uint4 *>(l.codes + (at * 2 + kv) * (kQ8Block * D)) + kt * (D / 32) * 32 + lane;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) out[c * 32] = x.codes[c];
+    if (i == 0) reinterpret_cast<float *>(l.scales + at)[kv] = x.scale;
+    if (kv == 0 && i < D) reinterpret_cast<uint16_t *>(l.bounds + at * (2 * D))[i] = static_cast<uint16_t>(x.bounds);
 }
 
 }  // namespace qa
