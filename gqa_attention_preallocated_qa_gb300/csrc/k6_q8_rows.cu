@@ -39,10 +39,12 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
         return *reinterpret_cast<const uint4 *>((kv ? src[1] : src[0]) + static_cast<int64_t>(pos - p.first[z]) * p.tok + d0);
     };
     const int kv_of_warp = threadIdx.x >> 7, kt = threadIdx.x >> 5 & 3;  // four warps for K, four for V
+    uint4 x[D / 16];
     if (i > 0) {  // every row of the block is new
         const int blk = first + i;
-        q8_store<D>(p.layer, sh, blk, kv_of_warp, kt,
-                    q8_seal<D>(kv_of_warp, kt, sm, [&](int kv, int r, int d0) { return source8(kv, blk * kQ8Block + r, d0); }));
+        q8_seal_rows<D>(kv_of_warp, kt, sm, x, [&](int kv, int r, int d0) { return source8(kv, blk * kQ8Block + r, d0); });
+        __syncthreads();
+        q8_store<D>(p.layer, sh, blk, kv_of_warp, kt, q8_seal_codes<D>(kv_of_warp, kt, sm, x));
         return;
     }
     const Q8Tail state = p.layer.state[sh];
@@ -56,20 +58,30 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
             return *reinterpret_cast<const uint4 *>(q8_tail_rows<D>(p.layer, sh, plan.from, kv) + r * D + d0);
         return q8_row8<D>(codes + kv * kQ8Block * D, kv != 0, kv ? scale.y : scale.x, r, d0);
     };
-    if (end >= (first + 1) * kQ8Block) {
-        const Q8Sealed<D> done = q8_seal<D>(kv_of_warp, kt, sm, row8);
-        __syncthreads();  // every warp has read what it needs of the old codes
-        q8_store<D>(p.layer, sh, first, kv_of_warp, kt, done);
-    }
-    if (plan.dst >= 0) {
+    if (plan.dst >= 0) {  // rows of the last block: all of a lane's on the way at once
         const int last = (end - 1) / kQ8Block, rest = end - last * kQ8Block;
         const int from = last == first ? plan.from_rows : 0;  // (below it the buffer has them)
-        for (int k = threadIdx.x; k < (rest - from) * 2 * (D / 8); k += blockDim.x) {
-            const int kv = k / ((rest - from) * (D / 8)), e = k % ((rest - from) * (D / 8));
-            const int r = from + e / (D / 8), d0 = e % (D / 8) * 8;
-            const uint4 x = last == first ? row8(kv, r, d0) : source8(kv, last * kQ8Block + r, d0);
-            *reinterpret_cast<uint4 *>(q8_tail_rows<D>(p.layer, sh, plan.dst, kv) + r * D + d0) = x;
+        constexpr int kRows = 256 / (D / 8), kTurns = kQ8Block / kRows;  // rows of a turn of the CTA
+        const int d0 = threadIdx.x % (D / 8) * 8;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            uint4 y[kTurns];
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                const int r = from + k * kRows + threadIdx.x / (D / 8);
+                if (r < rest) y[k] = last == first ? row8(kv, r, d0) : source8(kv, last * kQ8Block + r, d0);
+            }
+#pragma unroll
+            for (int k = 0; k < kTurns; ++k) {
+                const int r = from + k * kRows + threadIdx.x / (D / 8);
+                if (r < rest) *reinterpret_cast<uint4 *>(q8_tail_rows<D>(p.layer, sh, plan.dst, kv) + r * D + d0) = y[k];
+            }
         }
+    }
+    if (end >= (first + 1) * kQ8Block) {
+        q8_seal_rows<D>(kv_of_warp, kt, sm, x, row8);
+        __syncthreads();  // (and every warp has read what it needs of the old codes)
+        q8_store<D>(p.layer, sh, first, kv_of_warp, kt, q8_seal_codes<D>(kv_of_warp, kt, sm, x));
     }
     __syncthreads();  // every thread has read the state
     if (threadIdx.x == 0) p.layer.state[sh] = plan.next;

@@ -89,12 +89,10 @@ __device__ __forceinline__ void q8_cp_async(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void q8_cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// Into the shared memory of any CTA of the cluster.
-__device__ __forceinline__ void q8_st_cluster(uint32_t addr, uint32_t x) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ void q8_st_cluster(uint32_t addr, float a, float b) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+// Four bytes into the shared memory of a CTA of the cluster, counted on an mbarrier there.
+__device__ __forceinline__ void q8_send(uint32_t addr, uint32_t x, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(x), "r"(bar)
+                 : "memory");
 }
 
 // Sums of a warp: columns (heads) 2 t and 2 t + 1 of the MMAs (t = lane % 4); o[m] holds
@@ -155,7 +153,12 @@ struct alignas(16) Q8StepSmem {
     // A sparse step's
     uint32_t top[kQ8Warps];
     alignas(16) short up[D], down[D];             // C+, C-
-    uint2 part[2][kQ8Warps];
+    uint32_t part[kQ8Warps][4];
+    uint32_t found[4];
+    alignas(16) uint32_t hist[256];
+    // Transactions of what the other CTAs send: sums, scores.
+    alignas(8) uint64_t bar[2];
+    int abort;
 };
 
 template <int D>
@@ -164,33 +167,18 @@ __device__ __forceinline__ int q8_slot(int d) {
     return (r >> 1) * 16 + 2 * g + (r & 1);
 }
 
-// Sums of a and b over the CTA's threads; `turn` alternates between calls.
-__device__ __forceinline__ uint2 q8_cta_sum(uint32_t a, uint32_t b, uint2 (&part)[2][kQ8Warps], int turn) {
-    a = __reduce_add_sync(0xffffffffu, a);
-    b = __reduce_add_sync(0xffffffffu, b);
-    if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_uint2(a, b);
-    __syncthreads();
-    uint2 sum = part[turn][0];
-#pragma unroll
-    for (int w = 1; w < kQ8Warps; ++w) {
-        sum.x += part[turn][w].x;
-        sum.y += part[turn][w].y;
-    }
-    return sum;
-}
-
 // Scores the blocks of this CTA's share (me of S) and sends them to keys[] of all S.
 template <int D>
 __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int me, int S, uint32_t first_rank,
-                                         const Q8StepSmem<D> &sm, uint32_t *keys) {
-    constexpr int LPB = D / 8, BPW = 32 / LPB, U = 4;  // lanes a block, blocks a warp, loads ahead
+                                         Q8StepSmem<D> &sm, uint32_t *keys) {
+    constexpr int LPB = D / 8, BPW = 32 / LPB, U = 8;  // lanes a block, blocks a warp, loads ahead
     // A lane holds 16 codes of a block's 2 D: lo's in the first half of its lanes, hi's in the other.
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPB, d0 = sub % (D / 16) * 16;
     const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
     const uint4 wa = w4[0], wb = w4[1];
     const int per = (full + S - 1) / S, lo = me * per, hi = min(full, lo + per);
     const int8_t *bounds = l.bounds + base * (2 * D) + sub * 16;
-    const uint32_t to = smem_u32(keys);
+    const uint32_t to = smem_u32(keys), bar = smem_u32(&sm.bar[1]);
     for (int j0 = lo + warp * BPW; j0 < hi; j0 += U * BPW * kQ8Warps) {
         uint4 x[U];
         float s[U];
@@ -225,7 +213,8 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
                 if (S == 1) {
                     if (sub == 0) keys[j] = key;
                 } else {
-                    for (int r = sub; r < S; r += LPB) q8_st_cluster(map_rank(to + 4 * j, first_rank + r), key);
+                    for (int r = sub; r < S; r += LPB)
+                        q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
                 }
             }
         }
@@ -234,40 +223,77 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
 
 // The n blocks of the largest of keys[0 .. full - 1] (full > n), in rising order: those at
 // places lo .. hi - 1 go to list[].
+//   The n-th largest key is found by counting keys in 256 equal steps of the range that
+// holds it, which then shrinks to one step: two or three times for scores as they come,
+// four at most.  Infinite ones are set apart, so that the first range is that of numbers.
 template <int D>
 __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n, int lo, int hi, Q8StepSmem<D> &sm,
                                           uint16_t *list) {
+    const unsigned FULL = 0xffffffffu;
+    constexpr uint32_t kInf = 0xff800000u;  // q8_key(INFINITY)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int R = 8;  // keys of a thread in registers; the others are read again
-    uint32_t mine[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int j = threadIdx.x + i * kQ8Threads;
-        mine[i] = j < full ? keys[j] : 0u;  // (0 is below every score's key)
+    uint32_t least = kInf, most = 0, infinite = 0;
+    for (int j = threadIdx.x; j < full; j += kQ8Threads) {
+        const uint32_t key = keys[j];
+        infinite += key >= kInf;
+        least = min(least, key);
+        most = max(most, key >= kInf ? 0u : key);
     }
-    auto count = [&](uint32_t least) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i) c += mine[i] >= least;
-        for (int j = threadIdx.x + R * kQ8Threads; j < full; j += kQ8Threads) c += keys[j] >= least;
-        return c;
-    };
-    // The n-th largest key, two bits at a time from the highest: the largest value that
-    // at least n keys reach.  (Counts stay below 2^15.)
-    uint32_t nth = 0;
-    int reach = full, turn = 0;  // keys that are at least nth
-    for (int shift = 30; shift >= 0 && reach != n; shift -= 2, turn ^= 1) {
-        const uint32_t c1 = count(nth | 1u << shift), c2 = count(nth | 2u << shift), c3 = count(nth | 3u << shift);
-        const uint2 c = q8_cta_sum(c1 | c2 << 16, c3, sm.part, turn);
-        const int n1 = c.x & 0xffff, n2 = c.x >> 16, n3 = c.y;
-        if (n1 >= n) {
-            const uint32_t digit = n3 >= n ? 3 : n2 >= n ? 2 : 1;
-            nth |= digit << shift;
-            reach = n3 >= n ? n3 : n2 >= n ? n2 : n1;
+    least = __reduce_min_sync(FULL, least);
+    most = __reduce_max_sync(FULL, most);
+    infinite = __reduce_add_sync(FULL, infinite);
+    if (lane == 0) *reinterpret_cast<uint4 *>(sm.part[warp]) = make_uint4(least, most, infinite, 0);
+    for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
+    __syncthreads();
+    for (int w = 0; w < kQ8Warps; ++w) {
+        least = min(least, sm.part[w][0]);
+        most = max(most, sm.part[w][1]);
+    }
+    infinite = sm.part[0][2] + sm.part[1][2] + sm.part[2][2] + sm.part[3][2];
+    // All keys above nth belong to them, and the first `take` of those that equal it.
+    uint32_t nth = kInf;
+    int need = n - static_cast<int>(infinite), take = n;
+    while (need > 0) {
+        const int shift = max(0, 24 - __clz(most - least));  // (most - least) >> shift is below 256
+        for (int j = threadIdx.x; j < full; j += kQ8Threads) {
+            const uint32_t key = keys[j];
+            if (key >= least && key <= most) atomicAdd(&sm.hist[(key - least) >> shift], 1u);
         }
+        __syncthreads();
+        if (warp == 0) {  // a lane has 8 steps, the last lane the largest
+            const uint4 a = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane]), b = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane + 4]);
+            const uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const int mine = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
+            int from = mine;  // keys in this lane's steps and higher ones
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_down_sync(FULL, from, o);
+                if (lane + o < 32) from += y;
+            }
+            int above = from - mine;
+            if (above < need && from >= need) {  // one lane: the n-th largest is in its steps
+                int step = 7;
+                while (above + static_cast<int>(c[step]) < need) above += c[step--];
+                sm.found[0] = 8 * lane + step;
+                sm.found[1] = above;
+                sm.found[2] = c[step];
+            }
+        }
+        __syncthreads();
+        const uint32_t step = sm.found[0];
+        const int above = sm.found[1], in = sm.found[2];
+        least += step << shift;
+        need -= above;
+        if (need == in || shift == 0) {  // all keys of the step, or equal ones
+            nth = need == in && least > 0 ? least - 1 : least;
+            take = need == in ? 0 : need;
+            break;
+        }
+        most = min(most, least + ((1u << shift) - 1u));
+        for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
+        __syncthreads();
     }
-    // All above it, and of those that equal it the first ones: in order, a run of
-    // blocks for each thread.
+    // In order, a run of blocks for each thread.
     const int run = (full + kQ8Threads - 1) / kQ8Threads;
     const int j_lo = min(full, static_cast<int>(threadIdx.x) * run), j_hi = min(full, j_lo + run);
     uint32_t both = 0;  // above it, and equal to it in the upper half
@@ -275,18 +301,14 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
     uint32_t before = both;  // sums over the threads before this one
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+        const uint32_t y = __shfl_up_sync(FULL, before, o);
         if (lane >= o) before += y;
     }
-    if (lane == 31) sm.part[turn][warp].x = before;
+    __syncthreads();  // (part has been read)
+    if (lane == 31) sm.part[warp][0] = before;
     __syncthreads();
     before -= both;
-    uint32_t total = 0;
-    for (int w = 0; w < kQ8Warps; ++w) {
-        if (w < warp) before += sm.part[turn][w].x;
-        total += sm.part[turn][w].x;
-    }
-    const int take = n - static_cast<int>(total & 0xffff);  // of the equal ones
+    for (int w = 0; w < warp; ++w) before += sm.part[w][0];
     int equals = before >> 16, at = static_cast<int>(before & 0xffff) + min(equals, take);
     for (int j = j_lo; j < j_hi; ++j) {
         const uint32_t key = keys[j];
@@ -309,18 +331,20 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
     // ---------------------------------------------------------------- this CTA's share
-    const bool clustered = p.cluster > 1;
-    if (clustered) cluster_arrive();  // peers may write into this CTA once they have waited on this
     // An early launch signals at once, reads and computes beside its predecessors, which
     // write nothing that it reads, and waits for them before it writes.
     if (!p.early) griddep_wait();
     griddep_launch_dependents();
     int z = 0, pos = -1;
     if (static_cast<int>(blockIdx.x) < p.ctas) {
-        int hi = p.nseq;  // seq[z].cta0 <= blockIdx.x < seq[hi].cta0
-        while (hi - z > 1) {
-            const int mid = (z + hi) / 2;
-            if (p.seq[mid].cta0 <= static_cast<int>(blockIdx.x)) z = mid; else hi = mid;
+        if (p.per_seq > 0) {
+            z = blockIdx.x / static_cast<uint32_t>(p.per_seq);
+        } else {
+            int hi = p.nseq;  // seq[z].cta0 <= blockIdx.x < seq[hi].cta0
+            while (hi - z > 1) {
+                const int mid = (z + hi) / 2;
+                if (p.seq[mid].cta0 <= static_cast<int>(blockIdx.x)) z = mid; else hi = mid;
+            }
         }
         pos = p.pos_dev ? p.pos_dev[p.seq[z].slot] : p.seq[z].pos;
         if (pos < 0 || pos >= p.cap) {
@@ -330,24 +354,22 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     }
     const int b = p.seq[z].slot, S = p.seq[z].S, unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0;
     const int me = unit & (S - 1), h = unit / S;
-    if (pos < 0) {  // nothing to do here: the cluster's barriers alone
+    if (pos < 0) {  // nothing to do here
+        if (p.cluster > 1) cluster_arrive();
         griddep_wait();
         if (kSparse && me == 0 && static_cast<int>(blockIdx.x) < p.ctas) {
             for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads)
                 p.blocks[(static_cast<int64_t>(b) * p.layer.Hkv + h) * p.n_blocks + i] = -1;
         }
         __syncwarp();
-        if (clustered) {
-            cluster_wait();
-            if (kSparse) cluster_sync_all();
-            cluster_sync_all();
-        }
+        if (p.cluster > 1) cluster_wait();
         return;
     }
     const uint32_t first_rank = cluster_ctarank() - me;
     const int64_t sh = static_cast<int64_t>(b) * p.layer.Hkv + h, base = sh * p.layer.nblk;
     const int full = pos / kQ8Block, row = pos % kQ8Block;
     const bool choose = kSparse && full > p.n_blocks;
+    bool listed = true;  // (false: a wait ran out)
     const int items = choose ? p.n_blocks : full;
     const int item_lo = static_cast<int>(static_cast<int64_t>(items) * me / S);
     const int item_hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / S);
@@ -374,14 +396,48 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         for (int i = 0; i < NV; ++i) v[i] = q8_load(c + kQ8Block * D + i * 512);
         scale = p.layer.scales[base + blk];
     };
-    if (!choose) load_first();
+    // What the other CTAs of the S send: sums of weights and outputs, scores.
+    if (p.cluster > 1) {
+        if (threadIdx.x == 0) {
+            sm.abort = 0;
+            mbar_init(smem_u32(&sm.bar[0]), 1);
+            mbar_init(smem_u32(&sm.bar[1]), 1);
+            fence_mbar_init();
+            mbar_expect_tx(smem_u32(&sm.bar[0]), p.G * D * 4 + S * p.G * 8);
+            if (choose) mbar_expect_tx(smem_u32(&sm.bar[1]), full * 4);
+        }
+        __syncwarp();
+        cluster_arrive();  // peers send once they have waited on this
+    }
 
     // ---------------------------------------------------------------- query rows, and the new token's
-    // CTA 0 of the S has the rows of the block that the token is in.
+    // Their loads go out first, before the codes', which would hold them up.  CTA 0 of the
+    // S has the rows of the block that the token is in.
+    const int sub = lane % LPR, key_row = p.G < 8 ? p.G : 8;
+    const bool two = p.G == 8 && kQ8Warps * RPW < 9;  // a second turn, for the key alone
+    auto is_key = [&](int r) { return r == key_row && me == 0; };
+    auto load_row = [&](int r, NormRow &in) {
+        const bool is_q = r < p.G;
+        in.x = in.w = in.v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in.cs[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!is_q && !is_key(r)) return;
+        in.x = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.q + (static_cast<int64_t>(b) * p.Hq + h * p.G + r) * D : p.k + sh * D) + sub);
+        if (!is_q) in.v = __ldg(reinterpret_cast<const uint4 *>(p.v + sh * D) + sub);
+        if (!p.wq) return;
+        in.w = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.wq : p.wk) + sub);
+        const float4 *tab = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(pos) * (D / 2) + 8 * (sub % (D / 16)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in.cs[e] = __ldg(tab + e);
+    };
+    NormRow in;
+    load_row(warp * RPW + lane / LPR, in);
     Q8TailPlan plan;
     __nv_bfloat16 *tail = nullptr;   // where they are kept: 64 rows of K, then of V
+    if (me == 0) plan.next = p.layer.state[sh];
+    if (!choose) load_first();
     if (me == 0) {
-        plan = q8_plan_tail(p.layer.state[sh], pos, pos + 1, true);
+        plan = q8_plan_tail(plan.next, pos, pos + 1, true);
         tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
         for (int e = threadIdx.x; e < plan.from_rows * LPR; e += kQ8Threads) {
             const int r = e / LPR, d0 = e % LPR * 8;
@@ -390,36 +446,17 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         }
     }
     uint32_t top = 0;
-    const int sub = lane % LPR, key_row = p.G < 8 ? p.G : 8;
 #pragma unroll 1
-    for (int r0 = warp * RPW; r0 < (p.G < 8 ? 8 : 9); r0 += kQ8Warps * RPW) {  // (uniform in a warp)
-        const int r = r0 + lane / LPR;
-        const bool is_q = r < p.G, is_key = r == key_row && me == 0;
-        NormRow in;
-        in.x = make_uint4(0, 0, 0, 0);
-        if (is_q || is_key)
-            in.x = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.q + (static_cast<int64_t>(b) * p.Hq + h * p.G + r) * D : p.k + sh * D) + sub);
-        uint4 new_v;
-        if (is_key) new_v = __ldg(reinterpret_cast<const uint4 *>(p.v + sh * D) + sub);
-        uint4 x = in.x;
-        if (p.wq) {
-            in.w = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) in.cs[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (is_q || is_key) {
-                in.w = __ldg(reinterpret_cast<const uint4 *>(is_q ? p.wq : p.wk) + sub);
-                const float4 *tab = reinterpret_cast<const float4 *>(p.rope + static_cast<int64_t>(pos) * (D / 2) + 8 * (sub % (D / 16)));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) in.cs[e] = __ldg(tab + e);
-            }
-            x = norm_rope_row<D>(in, p.eps, sub);
-            if (!is_q && !is_key) x = make_uint4(0, 0, 0, 0);
-        }
-        if (is_key) {
+    for (int turn = 0; turn <= (two ? 1 : 0); ++turn) {  // (uniform in a warp)
+        const int r = (turn * kQ8Warps + warp) * RPW + lane / LPR;
+        if (turn > 0) load_row(r, in);
+        uint4 x = p.wq ? norm_rope_row<D>(in, p.eps, sub) : in.x;
+        if (r >= p.G && !is_key(r)) x = make_uint4(0, 0, 0, 0);
+        if (is_key(r)) {
             *reinterpret_cast<uint4 *>(&sm.rows[0][row][8 * sub]) = x;
-            *reinterpret_cast<uint4 *>(&sm.rows[1][row][8 * sub]) = new_v;
+            *reinterpret_cast<uint4 *>(&sm.rows[1][row][8 * sub]) = in.v;
             *reinterpret_cast<uint4 *>(&sm.fresh[0][8 * sub]) = x;
-            *reinterpret_cast<uint4 *>(&sm.fresh[1][8 * sub]) = new_v;
+            *reinterpret_cast<uint4 *>(&sm.fresh[1][8 * sub]) = in.v;
             x = make_uint4(0, 0, 0, 0);
         }
         // fp16 with one power of two per row: the largest magnitude goes to [256, 512),
@@ -473,7 +510,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         q8_cp_wait();
     }
     __syncthreads();
-    if (clustered) cluster_wait();
+    if (p.cluster > 1) cluster_wait();
 
     // ---------------------------------------------------------------- the choice
     if (kSparse) {
@@ -500,10 +537,14 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             __syncthreads();
             q8_score<D>(p.layer, base, full, me, S, first_rank, sm, keys);
         }
-        if (clustered) cluster_sync_all(); else __syncthreads();
         if (choose) {
-            q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
-            load_first();
+            const bool ok = S == 1 || mbar_wait_cluster(smem_u32(&sm.bar[1]), 0, &sm.abort, p.err, kKernQ8Decode, 2, p.wait_ns);
+            if (__syncthreads_and(ok)) {
+                q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
+                load_first();
+            } else {
+                listed = false;
+            }
         }
     }
 
@@ -650,11 +691,13 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const bool completes = me == 0 && row == kQ8Block - 1;  // the block that the token is in
     Q8Sealed<D> sealed[2];
     if (completes) {
+        uint4 x[2][D / 16];
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv)
-            sealed[kv] = q8_seal<D>(kv, warp, sm.seal, [&](int, int r, int d0) {
-                return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
-            });
+            q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) { return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]); });
+        __syncthreads();
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) sealed[kv] = q8_seal_codes<D>(kv, warp, sm.seal, x[kv]);
     }
     __syncthreads();  // the rows' shared memory becomes the sums'
 
@@ -674,7 +717,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     // CTA r of the S finishes outputs r E .. (r + 1) E - 1 of the group's G D.
     const int E = p.G * D / S;
     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h * p.G) * D;
-    const uint32_t to_o = smem_u32(sm.got_o), to_l = smem_u32(&sm.got_l[me][0]);
+    const uint32_t to_o = smem_u32(sm.got_o), to_l = smem_u32(&sm.got_l[me][0]), bar = smem_u32(&sm.bar[0]);
     for (int e = 2 * threadIdx.x; e < p.G * D; e += 2 * kQ8Threads) {
         const int head = e / D, slot = q8_slot<D>(e % D);
         float f[kQ8Warps], most = kQ8NoRef, l = 0.f;
@@ -695,12 +738,12 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         } else {
             const int r = e / E;
-            q8_st_cluster(map_rank(to_o + (me * E + e - r * E) * 4, first_rank + r), o.x, o.y);
+            st_async_f32x2(map_rank(to_o + (me * E + e - r * E) * 4, first_rank + r), o.x, o.y, map_rank(bar, first_rank + r));
             if (e % D < 2 * S)  // the head's first S pairs of dims: one CTA each
-                q8_st_cluster(map_rank(to_l + head * 8, first_rank + e % D / 2), most, l);
+                st_async_f32x2(map_rank(to_l + head * 8, first_rank + e % D / 2), most, l, map_rank(bar, first_rank + e % D / 2));
         }
     }
-    if (clustered) cluster_sync_all();
+    if (S > 1) mbar_wait_cluster(bar, 0, &sm.abort, p.err, kKernQ8Decode, 3, p.wait_ns);
     griddep_wait();  // everything before has finished: from here on this writes
     if (S > 1) {
         for (int i = 2 * threadIdx.x; i < E; i += 2 * kQ8Threads) {
@@ -722,7 +765,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     if (kSparse) {
         int32_t *to = p.blocks + sh * p.n_blocks;
         if (choose) {
-            for (int i = item_lo + threadIdx.x; i < item_hi; i += kQ8Threads) to[i] = list[i - item_lo];
+            for (int i = item_lo + threadIdx.x; i < item_hi; i += kQ8Threads) to[i] = listed ? list[i - item_lo] : -1;
         } else if (me == 0) {
             for (int i = threadIdx.x; i < p.n_blocks; i += kQ8Threads) to[i] = i < full ? i : -1;
         }

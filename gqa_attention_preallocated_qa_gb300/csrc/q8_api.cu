@@ -157,6 +157,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
     p.Hq = g.n_q_heads;
     p.G = g.n_q_heads / g.n_kv_heads;
     p.cap = g.capacity;
+    p.wait_ns = qa::kWaitTimeoutNs;
     p.eps = g.rms_eps;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.head_dim)));
     const qa::StreamRef at = qa::stream_ref(s, c->device);
@@ -171,6 +172,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         p.cluster = qa::q8_plan_step(2 * c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
         p.nseq = n;
         p.ctas = 0;
+        p.per_seq = splits[n - 1] == p.cluster ? p.cluster * g.n_kv_heads : 0;
         for (int i = 0; i < n; ++i) {
             p.seq[i].cta0 = p.ctas;
             p.seq[i].S = splits[i];

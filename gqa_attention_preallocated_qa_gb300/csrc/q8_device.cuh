@@ -100,16 +100,14 @@ struct Q8Sealed {
     uint32_t bounds;  // K: codes of two dims, least ones from the first D / 2 lanes of the four warps, then largest
 };
 
-// K (kv 0) or V of a block from its 64 rows: load8(kv, row, d0) gives 8 dims of one.  kt:
-// the 16 rows of this warp, of which four take part; every thread of the CTA calls this
-// together, with its warp's kv.
+// K (kv 0) or V of a block from its 64 rows: load8(kv, row, d0) gives 8 dims of one.  Four
+// warps take part, kt: the 16 rows of this one.  Two steps, between them __syncthreads():
+// the rows and what they come to, then the codes.
 template <int D, typename Load>
-__device__ __forceinline__ Q8Sealed<D> q8_seal(int kv, int kt, Q8SealSmem<D> &sm, Load &&load8) {
-    Q8Sealed<D> done;
+__device__ __forceinline__ void q8_seal_rows(int kv, int kt, Q8SealSmem<D> &sm, uint4 (&x)[D / 16], Load &&load8) {
     constexpr int NX = D / 16;  // loads of 8 dims per lane
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint4 x[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
         if (kv == 0) x[i] = load8(0, 16 * kt + g + 8 * (i & 1), 32 * (i >> 1) + 8 * t);
@@ -156,9 +154,14 @@ __device__ __forceinline__ Q8Sealed<D> q8_seal(int kv, int kt, Q8SealSmem<D> &sm
             }
         }
     }
-    __syncthreads();
+}
+
+template <int D>
+__device__ __forceinline__ Q8Sealed<D> q8_seal_codes(int kv, int kt, const Q8SealSmem<D> &sm, const uint4 (&x)[D / 16]) {
+    Q8Sealed<D> done;
+    const int lane = threadIdx.x & 31;
     const uint32_t *tops = sm.top + 4 * kv;
-    mx = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    const uint32_t mx = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
     const bool finite = mx < 0x7F80u;
     const float a = __uint_as_float(mx << 16);
     const bool used = finite && a >= kQ8Small;
