@@ -95,7 +95,10 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
 template <int D, bool kFactors>
 __global__ void __launch_bounds__(256) q8_read_kernel(const __grid_constant__ Q8RowsParams p) {
     __shared__ alignas(16) uint8_t codes[2][kQ8Block * D];
-    griddep_wait();
+    // For a prefill it runs beside the kernel of the new rows, which starts after all
+    // that came before and touches none of these.  The next kernel waits for this grid,
+    // whose last block is not done before the new rows are.
+    if (!kFactors || (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)) griddep_wait();
     griddep_launch_dependents();
     const int z = q8_sequence(p, blockIdx.x), h = blockIdx.y;
     const int start = p.start[z], end = start + p.ntok[z];

@@ -144,7 +144,10 @@ struct alignas(16) Q8StepSmem {
         float o[kQ8Warps][8][D + 8];              // then a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
     };
     __nv_bfloat16 fresh[2][D];      // the new rows
-    Q8SealSmem<D> seal;
+    union {
+        alignas(16) uint32_t hist[256];   // a sparse step's, for its choice
+        Q8SealSmem<D> seal;               // at its end
+    };
     float ref[kQ8Warps][8], l[kQ8Warps][8];
     // From the CTAs of the (sequence, kv head): references and sums of weights (of a
     // head), and this CTA's share of the outputs.
@@ -155,7 +158,6 @@ struct alignas(16) Q8StepSmem {
     alignas(16) short up[D], down[D];             // C+, C-
     uint32_t part[kQ8Warps][4];
     uint32_t found[4];
-    alignas(16) uint32_t hist[256];
     // Transactions of what the other CTAs send: sums, scores.
     alignas(8) uint64_t bar[2];
     int abort;
@@ -249,7 +251,8 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
         least = min(least, sm.part[w][0]);
         most = max(most, sm.part[w][1]);
     }
-    infinite = sm.part[0][2] + sm.part[1][2] + sm.part[2][2] + sm.part[3][2];
+    infinite = 0;
+    for (int w = 0; w < kQ8Warps; ++w) infinite += sm.part[w][2];
     // All keys above nth belong to them, and the first `take` of those that equal it.
     uint32_t nth = kInf;
     int need = n - static_cast<int>(infinite), take = n;
@@ -515,7 +518,9 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     // ---------------------------------------------------------------- the choice
     if (kSparse) {
         if (choose) {
-            const uint32_t mx = max(max(sm.top[0], sm.top[1]), max(sm.top[2], sm.top[3]));
+            uint32_t mx = sm.top[0];
+#pragma unroll
+            for (int w = 1; w < kQ8Warps; ++w) mx = max(mx, sm.top[w]);
             const float a = __uint_as_float(mx << 16);
             const float inv = mx < 0x7F80u && a >= kQ8Small ? __fdiv_rn(127.f, a) : 0.f;
             if (threadIdx.x < D / 2) {
@@ -694,7 +699,9 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         uint4 x[2][D / 16];
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv)
-            q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) { return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]); });
+            q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) {
+                return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
+            });
         __syncthreads();
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) sealed[kv] = q8_seal_codes<D>(kv, warp, sm.seal, x[kv]);

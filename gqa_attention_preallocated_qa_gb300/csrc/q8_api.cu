@@ -169,7 +169,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         std::stable_sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos > y.pos; });
         int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
         for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(p.seq[i].pos / qa::kQ8Block, a.n_blocks);
-        p.cluster = qa::q8_plan_step(2 * c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
+        p.cluster = qa::q8_plan_step(c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
         p.nseq = n;
         p.ctas = 0;
         p.per_seq = splits[n - 1] == p.cluster ? p.cluster * g.n_kv_heads : 0;
@@ -482,13 +482,17 @@ QA_API qa_status qa_q8_prefill(qa_q8_cache *c, int layer, int batch, const int32
             return true;
         };
         if (pg.k1.T == 0) return QA_OK;
-        if (pg.older.item0[pg.older.nseq] > 0 &&  // (of no older row: no factors either)
-            !done(qa::launch_q8_read(pg.older, g.head_dim, s), QA_Q8_KERNEL_READ))
-            return QA_ERR_CUDA;
-        if (!done(qa::launch_k1(pg.k1, g.head_dim, s), QA_Q8_KERNEL_NORM_ROPE) ||
+        pg.k1.signal_early = 1;  // what follows waits for it, or runs beside it
+        if (!done(qa::launch_k1(pg.k1, g.head_dim, s), QA_Q8_KERNEL_NORM_ROPE)) return QA_ERR_CUDA;
+        const bool older = pg.older.item0[pg.older.nseq] > 0;  // (of no older row: no factors either)
+        if ((older && !done(qa::launch_q8_read(pg.older, g.head_dim, s), QA_Q8_KERNEL_READ)) ||
             !done(qa::launch_q8_write(pg.write, g.head_dim, s), QA_Q8_KERNEL_WRITE) ||
-            !done(c->ws.launch(pg.k2, s), QA_Q8_KERNEL_PREFILL_ATTN))
+            !done(c->ws.launch(pg.k2, s), QA_Q8_KERNEL_PREFILL_ATTN)) {
+            // A kernel that signalled early may no longer be followed by one that waits for
+            // it: let it finish before anything else is enqueued.
+            cudaStreamSynchronize(s);
             return QA_ERR_CUDA;
+        }
         return QA_OK;
     };
     for (size_t i = 0; i < groups.size() && st == QA_OK; ++i) st = no_throw([&] { return launch(groups[i]); });

@@ -14,12 +14,20 @@ inline int q8_step_work(int full, int n_blocks) {
 }
 
 // splits[i], powers of two up to `most`, for n sequences of work[i] blocks for each of Hkv
-// kv heads: as few blocks for a warp (4 of them a CTA) as leave every CTA its place on the
-// device (`room` of them).  Returns the largest.
-inline int q8_plan_step(int64_t room, int Hkv, int most, int n, const int *work, int *splits) {
-    for (int per = 1;; ++per) {
+// kv heads; returns the largest.  One SM holds two CTAs of four warps.
+//   A CTA costs its set-up and merge, and a warp its blocks one after the other, so a step
+// alone is fastest with one block a warp, and a chain of steps, which run side by side,
+// with fewer CTAs.  Up to three blocks a warp are taken where that leaves room for several
+// launches, up to four for two of them, and as few as fit the device otherwise.  us, in a chain / alone
+// from call to end on the host (32/8 heads, D = 128): B 4, 2048 keys, 8 splits 6.0 / 19.1,
+// 4 (taken) 5.1 / 18.8, 2 4.2 / 20.6; sparse, B 4, 16 of 64 blocks, 8 splits 8.1 / 21.1, 2
+// (taken) 4.6 / 22.0; B 1, 32 of 1024, 16 splits 7.8 / 23.0, 8 (taken) 5.2 / 23.7.
+inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, int *splits) {
+    int top = 1;
+    // Splits that leave a warp at most `per` blocks; their CTAs.
+    auto cut = [&](int per) {
         int64_t ctas = 0;
-        int top = 1;
+        top = 1;
         for (int i = 0; i < n; ++i) {
             int s = 1;
             while (s < most && static_cast<int64_t>(s) * 4 * per < work[i]) s *= 2;
@@ -27,8 +35,14 @@ inline int q8_plan_step(int64_t room, int Hkv, int most, int n, const int *work,
             top = std::max(top, s);
             ctas += static_cast<int64_t>(Hkv) * s;
         }
-        if (ctas <= room || top == 1) return top;
-    }
+        return ctas;
+    };
+    for (int per = 1; per <= 3; ++per)
+        if (cut(per) <= num_sms / 2 - num_sms / 16) return top;
+    for (int per = 1; per <= 4; ++per)
+        if (cut(per) <= num_sms) return top;
+    for (int per = 1;; ++per)
+        if (cut(per) <= 2 * num_sms || top == 1) return top;
 }
 
 }  // namespace qa
