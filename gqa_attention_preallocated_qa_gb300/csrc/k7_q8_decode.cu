@@ -156,8 +156,9 @@ struct alignas(16) Q8StepSmem {
     // A sparse step's
     uint32_t top[kQ8Warps];
     alignas(16) short up[D], down[D];             // C+, C-
-    uint32_t part[kQ8Warps][4];
-    uint32_t found[4];
+    alignas(16) uint32_t part[kQ8Warps][4];
+    alignas(16) uint32_t found[4];
+    uint32_t runs[32];
     // Transactions of what the other CTAs send: sums, scores.
     alignas(8) uint64_t bar[2];
     int abort;
@@ -169,24 +170,24 @@ __device__ __forceinline__ int q8_slot(int d) {
     return (r >> 1) * 16 + 2 * g + (r & 1);
 }
 
-// Scores the blocks of this CTA's share (me of S) and sends them to keys[] of all S.
+// The bounds and scales of a batch of blocks of this CTA's share (me of S), 16 bytes a lane:
+// lo's in the first half of a block's lanes, hi's in the other.
 template <int D>
-__device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int me, int S, uint32_t first_rank,
-                                         Q8StepSmem<D> &sm, uint32_t *keys) {
-    constexpr int LPB = D / 8, BPW = 32 / LPB, U = 8;  // lanes a block, blocks a warp, loads ahead
-    // A lane holds 16 codes of a block's 2 D: lo's in the first half of its lanes, hi's in the other.
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPB, d0 = sub % (D / 16) * 16;
-    const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
-    const uint4 wa = w4[0], wb = w4[1];
-    const int per = (full + S - 1) / S, lo = me * per, hi = min(full, lo + per);
-    const int8_t *bounds = l.bounds + base * (2 * D) + sub * 16;
-    const uint32_t to = smem_u32(keys), bar = smem_u32(&sm.bar[1]);
-    for (int j0 = lo + warp * BPW; j0 < hi; j0 += U * BPW * kQ8Warps) {
-        uint4 x[U];
-        float s[U];
+struct Q8Bounds {
+    static constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 8;  // lanes a block, blocks a warp and load, loads
+    static constexpr int kBatch = kAhead * kPer * kQ8Warps;
+    uint4 x[kAhead];
+    float s[kAhead];
+
+    __device__ __forceinline__ static int block(int first, int u) {
+        return first + ((u * kQ8Warps + (threadIdx.x >> 5)) * kPer) + (threadIdx.x & 31) / kLanes;
+    }
+    // Of blocks first .. first + kBatch - 1, below hi.
+    __device__ __forceinline__ void load(const Q8Layer &l, int64_t base, int first, int hi) {
+        const int8_t *bounds = l.bounds + base * (2 * D) + (threadIdx.x % kLanes) * 16;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u * BPW * kQ8Warps + lane / LPB;
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = block(first, u);
             x[u] = make_uint4(0, 0, 0, 0);
             s[u] = 0.f;
             if (j < hi) {
@@ -194,30 +195,52 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
                 s[u] = l.scales[base + j].x;
             }
         }
+    }
+};
+
+// Scores blocks lo .. hi - 1 and sends them to keys[] of all S CTAs; at: their first batch.
+template <int D>
+__device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int lo, int hi, int S,
+                                         uint32_t first_rank, Q8StepSmem<D> &sm, uint32_t *keys, Q8Bounds<D> &at) {
+    constexpr int LPB = Q8Bounds<D>::kLanes;
+    const int sub = threadIdx.x % LPB, d0 = sub % (D / 16) * 16;
+    const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
+    const uint4 wa = w4[0], wb = w4[1];
+    const uint32_t to = smem_u32(keys), bar = smem_u32(&sm.bar[1]);
+    for (int j0 = lo; j0 < hi; j0 += Q8Bounds<D>::kBatch) {
+        int dot[Q8Bounds<D>::kAhead];
+        float s[Q8Bounds<D>::kAhead];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u * BPW * kQ8Warps + lane / LPB;
-            int dot = 0;
-            dot = __dp2a_lo(static_cast<int>(wa.x), static_cast<int>(x[u].x), dot);
-            dot = __dp2a_hi(static_cast<int>(wa.y), static_cast<int>(x[u].x), dot);
-            dot = __dp2a_lo(static_cast<int>(wa.z), static_cast<int>(x[u].y), dot);
-            dot = __dp2a_hi(static_cast<int>(wa.w), static_cast<int>(x[u].y), dot);
-            dot = __dp2a_lo(static_cast<int>(wb.x), static_cast<int>(x[u].z), dot);
-            dot = __dp2a_hi(static_cast<int>(wb.y), static_cast<int>(x[u].z), dot);
-            dot = __dp2a_lo(static_cast<int>(wb.z), static_cast<int>(x[u].w), dot);
-            dot = __dp2a_hi(static_cast<int>(wb.w), static_cast<int>(x[u].w), dot);
+        for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) {
+            const uint4 x = at.x[u];
+            s[u] = at.s[u];
+            dot[u] = __dp2a_lo(static_cast<int>(wa.x), static_cast<int>(x.x), 0);
+            dot[u] = __dp2a_hi(static_cast<int>(wa.y), static_cast<int>(x.x), dot[u]);
+            dot[u] = __dp2a_lo(static_cast<int>(wa.z), static_cast<int>(x.y), dot[u]);
+            dot[u] = __dp2a_hi(static_cast<int>(wa.w), static_cast<int>(x.y), dot[u]);
+            dot[u] = __dp2a_lo(static_cast<int>(wb.x), static_cast<int>(x.z), dot[u]);
+            dot[u] = __dp2a_hi(static_cast<int>(wb.y), static_cast<int>(x.z), dot[u]);
+            dot[u] = __dp2a_lo(static_cast<int>(wb.z), static_cast<int>(x.w), dot[u]);
+            dot[u] = __dp2a_hi(static_cast<int>(wb.w), static_cast<int>(x.w), dot[u]);
+        }
+        if (j0 + Q8Bounds<D>::kBatch < hi) at.load(l, base, j0 + Q8Bounds<D>::kBatch, hi);
 #pragma unroll
-            for (int o = LPB / 2; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (j < hi) {
-                float score = __fmul_rn(static_cast<float>(dot), s[u]);
-                if (j == 0 || j == full - 1 || s[u] != s[u]) score = INFINITY;
-                const uint32_t key = q8_key(score);
-                if (S == 1) {
-                    if (sub == 0) keys[j] = key;
-                } else {
-                    for (int r = sub; r < S; r += LPB)
-                        q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
-                }
+        for (int o = LPB / 2; o >= 1; o >>= 1) {
+#pragma unroll
+            for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+        }
+#pragma unroll
+        for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) {
+            const int j = Q8Bounds<D>::block(j0, u);
+            if (j >= hi) continue;
+            float score = __fmul_rn(static_cast<float>(dot[u]), s[u]);
+            if (j == 0 || j == full - 1 || s[u] != s[u]) score = INFINITY;
+            const uint32_t key = q8_key(score);
+            if (S == 1) {
+                if (sub == 0) keys[j] = key;
+            } else {
+                for (int r = sub; r < S; r += LPB)
+                    q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
             }
         }
     }
@@ -233,62 +256,82 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
                                           uint16_t *list) {
     const unsigned FULL = 0xffffffffu;
     constexpr uint32_t kInf = 0xff800000u;  // q8_key(INFINITY)
+    constexpr int R = 8, kHeld = R * kQ8Threads;  // keys of a thread in registers: the first of all
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t mine[R];
+    auto take_keys = [&](int first) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int j = first + i * kQ8Threads + threadIdx.x;
+            mine[i] = j < full ? keys[j] : 0u;  // (0 is below every score's key)
+        }
+    };
+    auto each = [&](auto &&f) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) f(mine[i]);
+        for (int j = kHeld + threadIdx.x; j < full; j += kQ8Threads) f(keys[j]);
+    };
+    take_keys(0);
     uint32_t least = kInf, most = 0, infinite = 0;
-    for (int j = threadIdx.x; j < full; j += kQ8Threads) {
-        const uint32_t key = keys[j];
+    each([&](uint32_t key) {
         infinite += key >= kInf;
-        least = min(least, key);
+        least = min(least, key == 0u ? kInf : key);
         most = max(most, key >= kInf ? 0u : key);
-    }
+    });
     least = __reduce_min_sync(FULL, least);
     most = __reduce_max_sync(FULL, most);
     infinite = __reduce_add_sync(FULL, infinite);
     if (lane == 0) *reinterpret_cast<uint4 *>(sm.part[warp]) = make_uint4(least, most, infinite, 0);
     for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
     __syncthreads();
-    for (int w = 0; w < kQ8Warps; ++w) {
-        least = min(least, sm.part[w][0]);
-        most = max(most, sm.part[w][1]);
-    }
     infinite = 0;
-    for (int w = 0; w < kQ8Warps; ++w) infinite += sm.part[w][2];
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(sm.part[w]);
+        least = min(least, x.x);
+        most = max(most, x.y);
+        infinite += x.z;
+    }
     // All keys above nth belong to them, and the first `take` of those that equal it.
     uint32_t nth = kInf;
     int need = n - static_cast<int>(infinite), take = n;
     while (need > 0) {
         const int shift = max(0, 24 - __clz(most - least));  // (most - least) >> shift is below 256
-        for (int j = threadIdx.x; j < full; j += kQ8Threads) {
-            const uint32_t key = keys[j];
+        each([&](uint32_t key) {
             if (key >= least && key <= most) atomicAdd(&sm.hist[(key - least) >> shift], 1u);
-        }
+        });
         __syncthreads();
         if (warp == 0) {  // a lane has 8 steps, the last lane the largest
             const uint4 a = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane]), b = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane + 4]);
-            const uint32_t c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const int mine = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
-            int from = mine;  // keys in this lane's steps and higher ones
+            const int c[8] = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
+                              static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+            const int all = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
+            int from = all;  // keys in this lane's steps and higher ones
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_down_sync(FULL, from, o);
                 if (lane + o < 32) from += y;
             }
-            int above = from - mine;
+            int above = from - all;
             if (above < need && from >= need) {  // one lane: the n-th largest is in its steps
-                int step = 7;
-                while (above + static_cast<int>(c[step]) < need) above += c[step--];
-                sm.found[0] = 8 * lane + step;
-                sm.found[1] = above;
-                sm.found[2] = c[step];
+                bool found = false;
+#pragma unroll
+                for (int step = 7; step >= 0; --step) {
+                    if (!found && above + c[step] >= need) {
+                        found = true;
+                        *reinterpret_cast<uint4 *>(sm.found) = make_uint4(8 * lane + step, above, c[step], 0);
+                    }
+                    if (!found) above += c[step];
+                }
             }
         }
         __syncthreads();
-        const uint32_t step = sm.found[0];
-        const int above = sm.found[1], in = sm.found[2];
-        least += step << shift;
-        need -= above;
+        const uint4 found = *reinterpret_cast<const uint4 *>(sm.found);
+        const int in = found.z;
+        least += found.x << shift;
+        need -= static_cast<int>(found.y);
         if (need == in || shift == 0) {  // all keys of the step, or equal ones
-            nth = need == in && least > 0 ? least - 1 : least;
+            nth = need == in ? least - 1 : least;
             take = need == in ? 0 : need;
             break;
         }
@@ -296,37 +339,45 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
         for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
         __syncthreads();
     }
-    // In order, a run of blocks for each thread.
-    const int run = (full + kQ8Threads - 1) / kQ8Threads;
-    const int j_lo = min(full, static_cast<int>(threadIdx.x) * run), j_hi = min(full, j_lo + run);
-    uint32_t both = 0;  // above it, and equal to it in the upper half
-    for (int j = j_lo; j < j_hi; ++j) both += keys[j] > nth ? 1u : keys[j] == nth ? 1u << 16 : 0u;
-    uint32_t before = both;  // sums over the threads before this one
+    // In order, kHeld blocks at a time: a warp has 32 of them for each of its registers.
+    int above_before = 0, equal_before = 0;
+    const uint32_t below = (1u << lane) - 1u;
+    for (int first = 0; first < full; first += kHeld) {
+        if (first > 0) take_keys(first);
+        uint32_t above[R], equal[R];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(FULL, before, o);
-        if (lane >= o) before += y;
-    }
-    __syncthreads();  // (part has been read)
-    if (lane == 31) sm.part[warp][0] = before;
-    __syncthreads();
-    before -= both;
-    for (int w = 0; w < warp; ++w) before += sm.part[w][0];
-    int equals = before >> 16, at = static_cast<int>(before & 0xffff) + min(equals, take);
-    for (int j = j_lo; j < j_hi; ++j) {
-        const uint32_t key = keys[j];
-        if (key > nth || (key == nth && equals < take)) {
-            if (at >= lo && at < hi) list[at - lo] = static_cast<uint16_t>(j);
-            ++at;
+        for (int i = 0; i < R; ++i) {
+            above[i] = __ballot_sync(FULL, mine[i] > nth);
+            equal[i] = __ballot_sync(FULL, mine[i] == nth);
+            if (lane == 0) sm.runs[i * kQ8Warps + warp] = __popc(above[i]) | __popc(equal[i]) << 16;
         }
-        equals += key == nth;
+        __syncthreads();
+        uint32_t run = sm.runs[lane], upto = run;  // R * kQ8Warps = 32 of them
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(FULL, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const uint32_t total = __shfl_sync(FULL, upto, 31);
+        upto -= run;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const uint32_t runs = __shfl_sync(FULL, upto, i * kQ8Warps + warp);
+            const int equals = equal_before + static_cast<int>(runs >> 16) + __popc(equal[i] & below);
+            const int at = above_before + static_cast<int>(runs & 0xffff) + __popc(above[i] & below) + min(equals, take);
+            if ((mine[i] > nth || (mine[i] == nth && equals < take)) && at >= lo && at < hi)
+                list[at - lo] = static_cast<uint16_t>(first + i * kQ8Threads + threadIdx.x);
+        }
+        above_before += total & 0xffff;
+        equal_before += total >> 16;
+        __syncthreads();
     }
-    __syncthreads();
 }
 
 template <int D, bool kSparse>
 __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_constant__ Q8StepParams p) {
     constexpr int NV = D / 8;   // 16-byte vectors of a lane for K, and for V, of a block
+    constexpr int NB = 128 / D; // blocks that a warp has in hand: independent chains at D = 64
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const unsigned FULL = 0xffffffffu;
     extern __shared__ uint32_t keys[];    // sparse: of every block; behind them the chosen ones of this CTA
@@ -379,26 +430,52 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     int item = item_lo + warp;
     uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.layer.nblk);
     const uint8_t *codes = p.layer.codes + base * (2 * kQ8Block * D) + lane * 16;
-    uint4 k[NV], v[NV];
-    float2 scale = make_float2(0.f, 0.f);
-    int blk = -1;
-    // The next block of the warp, -1 at the end.
-    auto next_block = [&]() {
-        if (item >= item_hi) return -1;
-        const int j = choose ? static_cast<int>(list[item - item_lo]) : item;
-        item += kQ8Warps;
-        return j;
+    uint4 k[NB][NV], v[NB][NV];
+    float2 scale[NB];
+    int blk[NB];
+    // The next blocks of the warp, -1 where there is none.
+    auto next_blocks = [&](int (&j)[NB]) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            j[n] = item >= item_hi ? -1 : choose ? static_cast<int>(list[item - item_lo]) : item;
+            item += kQ8Warps;
+        }
+    };
+    auto load_k = [&](const int (&j)[NB]) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (j[n] < 0) continue;
+            const uint8_t *c = codes + static_cast<int64_t>(j[n]) * (2 * kQ8Block * D);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) k[n][i] = q8_load(c + i * 512);
+            scale[n] = p.layer.scales[base + j[n]];
+        }
+    };
+    auto load_v = [&](const int (&j)[NB]) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (j[n] < 0) continue;
+            const uint8_t *c = codes + static_cast<int64_t>(j[n]) * (2 * kQ8Block * D) + kQ8Block * D;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[n][i] = q8_load(c + i * 512);
+        }
     };
     auto load_first = [&]() {
-        blk = next_block();
-        if (blk < 0) return;
-        const uint8_t *c = codes + static_cast<int64_t>(blk) * (2 * kQ8Block * D);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) k[i] = q8_load(c + i * 512);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = q8_load(c + kQ8Block * D + i * 512);
-        scale = p.layer.scales[base + blk];
+        next_blocks(blk);
+        load_k(blk);
+        load_v(blk);
     };
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        blk[n] = -1;
+        scale[n] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) k[n][i] = v[n][i] = make_uint4(0, 0, 0, 0);
+    }
+    // The blocks that this CTA scores.
+    const int score_lo = static_cast<int>(static_cast<int64_t>(full) * me / S);
+    const int score_hi = static_cast<int>(static_cast<int64_t>(full) * (me + 1) / S);
+    Q8Bounds<D> bounds;
     // What the other CTAs of the S send: sums of weights and outputs, scores.
     if (p.cluster > 1) {
         if (threadIdx.x == 0) {
@@ -438,7 +515,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     Q8TailPlan plan;
     __nv_bfloat16 *tail = nullptr;   // where they are kept: 64 rows of K, then of V
     if (me == 0) plan.next = p.layer.state[sh];
-    if (!choose) load_first();
+    if (choose) bounds.load(p.layer, base, score_lo, score_hi); else load_first();
     if (me == 0) {
         plan = q8_plan_tail(plan.next, pos, pos + 1, true);
         tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
@@ -510,7 +587,6 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + rr) * D + d0) = x;
             }
         }
-        q8_cp_wait();
     }
     __syncthreads();
     if (p.cluster > 1) cluster_wait();
@@ -540,9 +616,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 *reinterpret_cast<short2 *>(&sm.down[2 * threadIdx.x]) = make_short2(down[0], down[1]);
             }
             __syncthreads();
-            q8_score<D>(p.layer, base, full, me, S, first_rank, sm, keys);
-        }
-        if (choose) {
+            q8_score<D>(p.layer, base, full, score_lo, score_hi, S, first_rank, sm, keys, bounds);
             const bool ok = S == 1 || mbar_wait_cluster(smem_u32(&sm.bar[1]), 0, &sm.abort, p.err, kKernQ8Decode, 2, p.wait_ns);
             if (__syncthreads_and(ok)) {
                 q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
@@ -561,84 +635,102 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     for (int m = 0; m < D / 16; ++m) a.o[m][0] = a.o[m][1] = a.o[m][2] = a.o[m][3] = 0.f;
     const float qs0 = sm.qscale[2 * t], qs1 = sm.qscale[2 * t + 1];
     const float st0 = sm.qstart[2 * t], st1 = sm.qstart[2 * t + 1];
-    while (blk >= 0) {
-        const int ahead = next_block();
-        const uint8_t *c_next = codes + static_cast<int64_t>(ahead) * (2 * kQ8Block * D);
-        float s[4][4];
+    while (blk[0] >= 0) {
+        int ahead[NB];
+        next_blocks(ahead);
+        float s[NB][4][4];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            s[kt][0] = s[kt][2] = st0;
-            s[kt][1] = s[kt][3] = st1;
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                s[n][kt][0] = s[n][kt][2] = st0;
+                s[n][kt][1] = s[n][kt][3] = st1;
+            }
         }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             const uint4 q = *reinterpret_cast<const uint4 *>(&sm.qh[g][32 * c + 8 * t]);
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt) {
-                const uint4 w = k[kt * (D / 32) + c];
-                q8_mma(s[kt], q8_lo(w.x), q8_hi(w.x), q8_lo(w.y), q8_hi(w.y), q.x, q.y);
-                q8_mma(s[kt], q8_lo(w.z), q8_hi(w.z), q8_lo(w.w), q8_hi(w.w), q.z, q.w);
+            for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                for (int kt = 0; kt < 4; ++kt) {
+                    const uint4 w = k[n][kt * (D / 32) + c];
+                    q8_mma(s[n][kt], q8_lo(w.x), q8_hi(w.x), q8_lo(w.y), q8_hi(w.y), q.x, q.y);
+                    q8_mma(s[n][kt], q8_lo(w.z), q8_hi(w.z), q8_lo(w.w), q8_hi(w.w), q.z, q.w);
+                }
             }
         }
-        const float2 sc = scale;
-        if (ahead >= 0) {
+        float2 sc[NB];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) k[i] = q8_load(c_next + i * 512);
-            scale = p.layer.scales[base + ahead];
-        }
-        // S is 2^24 times too small, and 2^8 too large by the queries' power of two.
-        const float c0 = sc.x * 65536.f * qs0, c1 = sc.x * 65536.f * qs1;
+        for (int n = 0; n < NB; ++n) sc[n] = blk[n] >= 0 ? scale[n] : make_float2(0.f, 0.f);
+        load_k(ahead);
         float m0 = kQ8NoRef, m1 = kQ8NoRef;
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            s[kt][0] *= c0;
-            s[kt][1] *= c1;
-            s[kt][2] *= c0;
-            s[kt][3] *= c1;
-            m0 = fmaxf(m0, fmaxf(s[kt][0], s[kt][2]));
-            m1 = fmaxf(m1, fmaxf(s[kt][1], s[kt][3]));
-        }
-        q8_raise<D>(a, m0, m1);
-        uint32_t pb[4][2];
-        float start[4] = {0.f, 0.f, 0.f, 0.f};  // -128 2^-24 times the sum of the weights
+        for (int n = 0; n < NB; ++n) {
+            // S is 2^24 times too small, and 2^8 too large by the queries' power of two.
+            const float c0 = sc[n].x * 65536.f * qs0, c1 = sc[n].x * 65536.f * qs1;
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-            pb[kt][0] = q8_transpose(q8_pack_f16(q8_exp2(s[kt][0] - a.ref[0]), q8_exp2(s[kt][1] - a.ref[1])));
-            pb[kt][1] = q8_transpose(q8_pack_f16(q8_exp2(s[kt][2] - a.ref[0]), q8_exp2(s[kt][3] - a.ref[1])));
-            q8_mma(start, kQ8Zero, kQ8Zero, kQ8Zero, kQ8Zero, pb[kt][0], pb[kt][1]);  // 0x8080: -2^-17 in fp16
-        }
-        a.l[0] = fmaf(start[0], -131072.f, a.l[0]);
-        a.l[1] = fmaf(start[1], -131072.f, a.l[1]);
-        float acc[D / 16][4];
-#pragma unroll
-        for (int m = 0; m < D / 16; ++m) {
-            acc[m][0] = acc[m][2] = start[0];
-            acc[m][1] = acc[m][3] = start[1];
-        }
-#pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 w = v[kt * (D / 32) + i];
-                q8_mma(acc[2 * i], q8_lo(w.x), q8_hi(w.x), q8_lo(w.y), q8_hi(w.y), pb[kt][0], pb[kt][1]);
-                q8_mma(acc[2 * i + 1], q8_lo(w.z), q8_hi(w.z), q8_lo(w.w), q8_hi(w.w), pb[kt][0], pb[kt][1]);
+            for (int kt = 0; kt < 4; ++kt) {
+                s[n][kt][0] *= c0;
+                s[n][kt][1] *= c1;
+                s[n][kt][2] *= c0;
+                s[n][kt][3] *= c1;
+                if (n > 0 && blk[n] < 0) s[n][kt][0] = s[n][kt][1] = s[n][kt][2] = s[n][kt][3] = -INFINITY;
+                m0 = fmaxf(m0, fmaxf(s[n][kt][0], s[n][kt][2]));
+                m1 = fmaxf(m1, fmaxf(s[n][kt][1], s[n][kt][3]));
             }
         }
-        if (ahead >= 0) {
+        q8_raise<D>(a, m0, m1);
+        uint32_t pb[NB][4][2];
+        float acc[NB][D / 16][4];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) v[i] = q8_load(c_next + kQ8Block * D + i * 512);
+        for (int n = 0; n < NB; ++n) {
+            float start[4] = {0.f, 0.f, 0.f, 0.f};  // -128 2^-24 times the sum of the weights
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                pb[n][kt][0] = q8_transpose(q8_pack_f16(q8_exp2(s[n][kt][0] - a.ref[0]), q8_exp2(s[n][kt][1] - a.ref[1])));
+                pb[n][kt][1] = q8_transpose(q8_pack_f16(q8_exp2(s[n][kt][2] - a.ref[0]), q8_exp2(s[n][kt][3] - a.ref[1])));
+                q8_mma(start, kQ8Zero, kQ8Zero, kQ8Zero, kQ8Zero, pb[n][kt][0], pb[n][kt][1]);  // 0x8080: -2^-17 in fp16
+            }
+            a.l[0] = fmaf(start[0], -131072.f, a.l[0]);
+            a.l[1] = fmaf(start[1], -131072.f, a.l[1]);
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+                acc[n][m][0] = acc[n][m][2] = start[0];
+                acc[n][m][1] = acc[n][m][3] = start[1];
+            }
         }
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m)
+        for (int kt = 0; kt < 4; ++kt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a.o[m][e] = fmaf(acc[m][e], sc.y, a.o[m][e]);
-        blk = ahead;
+            for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 w = v[n][kt * (D / 32) + i];
+                    q8_mma(acc[n][2 * i], q8_lo(w.x), q8_hi(w.x), q8_lo(w.y), q8_hi(w.y), pb[n][kt][0], pb[n][kt][1]);
+                    q8_mma(acc[n][2 * i + 1], q8_lo(w.z), q8_hi(w.z), q8_lo(w.w), q8_hi(w.w), pb[n][kt][0], pb[n][kt][1]);
+                }
+            }
+        }
+        load_v(ahead);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a.o[m][e] = fmaf(acc[n][m][e], sc[n].y, a.o[m][e]);
+            blk[n] = ahead[n];
+        }
     }
 
     // ---------------------------------------------------------------- rows in bf16
     // 16 of them a warp, the last warps (which have the fewest blocks) first.  Weights as
     // the sum of two bf16 numbers.
     const int tile = kQ8Warps - 1 - warp;
+    if (me == 0) {
+        q8_cp_wait();
+        __syncthreads();
+    }
     if (me == 0 && 16 * tile <= row) {
         const int r0 = 16 * tile + g, r8 = r0 + 8;
         float s[4] = {0.f, 0.f, 0.f, 0.f};

@@ -168,7 +168,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         // The longest sequences, which have the most CTAs, first.
         std::stable_sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos > y.pos; });
         int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
-        for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(p.seq[i].pos / qa::kQ8Block, a.n_blocks);
+        for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(g.head_dim, p.seq[i].pos / qa::kQ8Block, a.n_blocks);
         p.cluster = qa::q8_plan_step(c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
         p.nseq = n;
         p.ctas = 0;

@@ -7,10 +7,11 @@
 
 namespace qa {
 
-// A sequence's work in a step, in blocks of 16 KB (D = 128): all complete ones, or the chosen
-// ones and the scoring of all (their bounds are 1/64 of their codes).
-inline int q8_step_work(int full, int n_blocks) {
-    return n_blocks > 0 && full > n_blocks ? n_blocks + full / 32 : full;
+// A sequence's work in a step, in blocks of 16 KB (two of them at D = 64): all complete ones,
+// or the chosen ones and the scoring of all (their bounds are 1/64 of their codes).
+inline int q8_step_work(int D, int full, int n_blocks) {
+    const int blocks = n_blocks > 0 && full > n_blocks ? n_blocks + full / 32 : full;
+    return D == 128 ? blocks : (blocks + 1) / 2;
 }
 
 // splits[i], powers of two up to `most`, for n sequences of work[i] blocks for each of Hkv
