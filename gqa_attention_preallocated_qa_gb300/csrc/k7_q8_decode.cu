@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             pos = -1;
         }
     }
-    const int b = p.seq[z].slot, S = p.seq[z].S, unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0;
-    const int me = unit & (S - 1), h = unit / S;
+    const int b = p.seq[z].slot, log_S = p.seq[z].log_S, S = 1 << log_S;
+    const int unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0, me = unit & (S - 1), h = unit >> log_S;
     if (pos < 0) {  // nothing to do here
         if (p.cluster > 1) cluster_arrive();
         griddep_wait();
@@ -421,12 +421,11 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     }
     const uint32_t first_rank = cluster_ctarank() - me;
     const int64_t sh = static_cast<int64_t>(b) * p.layer.Hkv + h, base = sh * p.layer.nblk;
-    const int full = pos / kQ8Block, row = pos % kQ8Block;
+    const int full = static_cast<uint32_t>(pos) / kQ8Block, row = static_cast<uint32_t>(pos) % kQ8Block;
     const bool choose = kSparse && full > p.n_blocks;
     bool listed = true;  // (false: a wait ran out)
     const int items = choose ? p.n_blocks : full;
-    const int item_lo = static_cast<int>(static_cast<int64_t>(items) * me / S);
-    const int item_hi = static_cast<int>(static_cast<int64_t>(items) * (me + 1) / S);
+    const int item_lo = items * me >> log_S, item_hi = items * (me + 1) >> log_S;  // (at most 2^18)
     int item = item_lo + warp;
     uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.layer.nblk);
     const uint8_t *codes = p.layer.codes + base * (2 * kQ8Block * D) + lane * 16;
@@ -473,8 +472,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         for (int i = 0; i < NV; ++i) k[n][i] = v[n][i] = make_uint4(0, 0, 0, 0);
     }
     // The blocks that this CTA scores.
-    const int score_lo = static_cast<int>(static_cast<int64_t>(full) * me / S);
-    const int score_hi = static_cast<int>(static_cast<int64_t>(full) * (me + 1) / S);
+    const int score_lo = full * me >> log_S, score_hi = full * (me + 1) >> log_S;
     Q8Bounds<D> bounds;
     // What the other CTAs of the S send: sums of weights and outputs, scores.
     if (p.cluster > 1) {
@@ -814,7 +812,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     }
     __syncthreads();
     // CTA r of the S finishes outputs r E .. (r + 1) E - 1 of the group's G D.
-    const int E = p.G * D / S;
+    const int E = p.G * D >> log_S, log_E = 31 - __clz(E);
     __nv_bfloat16 *out = p.out + (static_cast<int64_t>(b) * p.Hq + h * p.G) * D;
     const uint32_t to_o = smem_u32(sm.got_o), to_l = smem_u32(&sm.got_l[me][0]), bar = smem_u32(&sm.bar[0]);
     for (int e = 2 * threadIdx.x; e < p.G * D; e += 2 * kQ8Threads) {
@@ -836,8 +834,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             griddep_wait();
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         } else {
-            const int r = e / E;
-            st_async_f32x2(map_rank(to_o + (me * E + e - r * E) * 4, first_rank + r), o.x, o.y, map_rank(bar, first_rank + r));
+            const int r = e >> log_E;
+            st_async_f32x2(map_rank(to_o + (me * E + (e & (E - 1))) * 4, first_rank + r), o.x, o.y, map_rank(bar, first_rank + r));
             if (e % D < 2 * S)  // the head's first S pairs of dims: one CTA each
                 st_async_f32x2(map_rank(to_l + head * 8, first_rank + e % D / 2), most, l, map_rank(bar, first_rank + e % D / 2));
         }

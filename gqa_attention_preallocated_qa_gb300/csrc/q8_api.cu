@@ -164,7 +164,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
     const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
     for (int b0 = 0; b0 < batch; b0 += qa::kQ8MaxSeqPerLaunch) {
         const int n = std::min(qa::kQ8MaxSeqPerLaunch, batch - b0);
-        for (int i = 0; i < n; ++i) p.seq[i] = {a.pos_dev ? g.capacity - 1 : a.positions[b0 + i], b0 + i, 0, 1};
+        for (int i = 0; i < n; ++i) p.seq[i] = {a.pos_dev ? g.capacity - 1 : a.positions[b0 + i], b0 + i, 0, 0};
         // The longest sequences, which have the most CTAs, first.
         std::stable_sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos > y.pos; });
         int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
@@ -175,7 +175,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         p.per_seq = splits[n - 1] == p.cluster ? p.cluster * g.n_kv_heads : 0;
         for (int i = 0; i < n; ++i) {
             p.seq[i].cta0 = p.ctas;
-            p.seq[i].S = splits[i];
+            while (1 << p.seq[i].log_S < splits[i]) ++p.seq[i].log_S;
             p.ctas += splits[i] * g.n_kv_heads;
         }
         p.early = !a.pos_dev && qa::launch_order().layer_settled(at, c, layer, resident) ? 1 : 0;

@@ -49,9 +49,9 @@ struct Q8RowsParams {
 static_assert(sizeof(Q8RowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
 
 // A launched sequence: the position of its new token, its place in the cache, and its
-// first CTA; each kv head has S of them, a power of two.
+// first CTA; each kv head has 2^log_S of them.
 struct alignas(16) Q8Seq {
-    int pos, slot, cta0, S;
+    int pos, slot, cta0, log_S;
 };
 
 struct Q8StepParams {
