@@ -139,11 +139,8 @@ struct alignas(16) Q8StepSmem {
     __half qh[8][D + 8];            // queries, each row times a power of two
     __nv_bfloat16 qb[8][D + 8];     // queries as they are
     float qscale[8], qstart[8];     // log2(e) / sqrt(D) over that power; what S starts from
-    union {
-        __nv_bfloat16 rows[2][kQ8Block][D + 8];   // K and V of the block that the new token is in
-        float o[kQ8Warps][8][D + 8];              // then a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
-    };
-    __nv_bfloat16 fresh[2][D];      // the new rows
+    __nv_bfloat16 rows[2][kQ8Block][D + 8];   // K and V of the block that the new token is in
+    float o[kQ8Warps][8][D + 8];    // a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
     union {
         alignas(16) uint32_t hist[256];   // a sparse step's, for its choice
         Q8SealSmem<D> seal;               // at its end
@@ -380,8 +377,10 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     constexpr int NB = 128 / D; // blocks that a warp has in hand: independent chains at D = 64
     constexpr int LPR = D / 8, RPW = 32 / LPR;
     const unsigned FULL = 0xffffffffu;
-    extern __shared__ uint32_t keys[];    // sparse: of every block; behind them the chosen ones of this CTA
-    __shared__ Q8StepSmem<D> sm;
+    extern __shared__ uint4 smem[];
+    Q8StepSmem<D> &sm = *reinterpret_cast<Q8StepSmem<D> *>(smem);
+    // Sparse: the scores of every block; behind them the chosen blocks of this CTA.
+    uint32_t *keys = reinterpret_cast<uint32_t *>(&sm + 1);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
     // ---------------------------------------------------------------- this CTA's share
@@ -533,8 +532,6 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         if (is_key(r)) {
             *reinterpret_cast<uint4 *>(&sm.rows[0][row][8 * sub]) = x;
             *reinterpret_cast<uint4 *>(&sm.rows[1][row][8 * sub]) = in.v;
-            *reinterpret_cast<uint4 *>(&sm.fresh[0][8 * sub]) = x;
-            *reinterpret_cast<uint4 *>(&sm.fresh[1][8 * sub]) = in.v;
             x = make_uint4(0, 0, 0, 0);
         }
         // fp16 with one power of two per row: the largest magnitude goes to [256, 512),
@@ -783,20 +780,6 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             }
         }
     }
-    const bool completes = me == 0 && row == kQ8Block - 1;  // the block that the token is in
-    Q8Sealed<D> sealed[2];
-    if (completes) {
-        uint4 x[2][D / 16];
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-            q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) {
-                return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
-            });
-        __syncthreads();
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) sealed[kv] = q8_seal_codes<D>(kv, warp, sm.seal, x[kv]);
-    }
-    __syncthreads();  // the rows' shared memory becomes the sums'
 
     // ---------------------------------------------------------------- merge: warps, then CTAs
     if (g == 0) {
@@ -870,14 +853,22 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     if (me == 0) {
         if (threadIdx.x < 2 * LPR) {
             const int kv = threadIdx.x / LPR, d0 = threadIdx.x % LPR * 8;
-            const uint4 x = *reinterpret_cast<const uint4 *>(&sm.fresh[kv][d0]);
+            const uint4 x = *reinterpret_cast<const uint4 *>(&sm.rows[kv][row][d0]);
             *reinterpret_cast<uint4 *>(tail + (kv * kQ8Block + row) * D + d0) = x;
             __nv_bfloat16 *held = kv ? p.v_held : p.k_held;
             if (held) *reinterpret_cast<uint4 *>(held + sh * D + d0) = x;
         }
-        if (completes) {
+        if (row == kQ8Block - 1) {  // the block that the token is in is complete
+            uint4 x[2][D / 16];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) q8_store<D>(p.layer, sh, full, kv, warp, sealed[kv]);
+            for (int kv = 0; kv < 2; ++kv)
+                q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) {
+                    return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
+                });
+            __syncthreads();
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+                q8_store<D>(p.layer, sh, full, kv, warp, q8_seal_codes<D>(kv, warp, sm.seal, x[kv]));
         }
         if (threadIdx.x == 0) p.layer.state[sh] = plan.next;
     }
@@ -892,15 +883,16 @@ static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
     cudaGetDevice(&dev);
     if (dev >= 32 || !((configured.load(std::memory_order_acquire) >> dev) & 1u)) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess && kSparse)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8MaxBlocks * 6);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     sizeof(Q8StepSmem<D>) + (kSparse ? kQ8MaxBlocks * 6 : 0));
         if (e != cudaSuccess) return e;
         if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster);
     cfg.blockDim = dim3(kQ8Threads);
-    cfg.dynamicSmemBytes = kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + (static_cast<size_t>(p.n_blocks) * 2 + 15) / 16 * 16 : 0;
+    cfg.dynamicSmemBytes = sizeof(Q8StepSmem<D>) + (kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + static_cast<size_t>(p.n_blocks) * 2 : 0);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -166,7 +166,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         const int n = std::min(qa::kQ8MaxSeqPerLaunch, batch - b0);
         for (int i = 0; i < n; ++i) p.seq[i] = {a.pos_dev ? g.capacity - 1 : a.positions[b0 + i], b0 + i, 0, 0};
         // The longest sequences, which have the most CTAs, first.
-        std::stable_sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos > y.pos; });
+        std::sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos != y.pos ? x.pos > y.pos : x.slot < y.slot; });
         int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
         for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(g.head_dim, p.seq[i].pos / qa::kQ8Block, a.n_blocks);
         p.cluster = qa::q8_plan_step(c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
