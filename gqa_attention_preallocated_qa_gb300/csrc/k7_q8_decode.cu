@@ -195,10 +195,12 @@ struct Q8Bounds {
     }
 };
 
-// Scores blocks lo .. hi - 1 and sends them to keys[] of all S CTAs; at: their first batch.
+// Scores blocks lo .. hi - 1 and sends them to keys[] of all S CTAs (to none: withhold); at:
+// their first batch.
 template <int D>
 __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int lo, int hi, int S,
-                                         uint32_t first_rank, Q8StepSmem<D> &sm, uint32_t *keys, Q8Bounds<D> &at) {
+                                         uint32_t first_rank, bool withhold, Q8StepSmem<D> &sm, uint32_t *keys,
+                                         Q8Bounds<D> &at) {
     constexpr int LPB = Q8Bounds<D>::kLanes;
     const int sub = threadIdx.x % LPB, d0 = sub % (D / 16) * 16;
     const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
@@ -235,7 +237,7 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
             const uint32_t key = q8_key(score);
             if (S == 1) {
                 if (sub == 0) keys[j] = key;
-            } else {
+            } else if (!withhold) {
                 for (int r = sub; r < S; r += LPB)
                     q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
             }
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const int full = static_cast<uint32_t>(pos) / kQ8Block, row = static_cast<uint32_t>(pos) % kQ8Block;
     const bool choose = kSparse && full > p.n_blocks;
     bool listed = true;  // (false: a wait ran out)
+    const bool withhold = p.fault != 0 && z == 0 && unit == S - 1;  // (test hook)
     const int items = choose ? p.n_blocks : full;
     const int item_lo = items * me >> log_S, item_hi = items * (me + 1) >> log_S;  // (at most 2^18)
     int item = item_lo + warp;
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 *reinterpret_cast<short2 *>(&sm.down[2 * threadIdx.x]) = make_short2(down[0], down[1]);
             }
             __syncthreads();
-            q8_score<D>(p.layer, base, full, score_lo, score_hi, S, first_rank, sm, keys, bounds);
+            q8_score<D>(p.layer, base, full, score_lo, score_hi, S, first_rank, withhold, sm, keys, bounds);
             const bool ok = S == 1 || mbar_wait_cluster(smem_u32(&sm.bar[1]), 0, &sm.abort, p.err, kKernQ8Decode, 2, p.wait_ns);
             if (__syncthreads_and(ok)) {
                 q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             const float inv = 16777216.f / l;
             griddep_wait();
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
-        } else {
+        } else if (!withhold || choose) {
             const int r = e >> log_E;
             st_async_f32x2(map_rank(to_o + (me * E + (e & (E - 1))) * 4, first_rank + r), o.x, o.y, map_rank(bar, first_rank + r));
             if (e % D < 2 * S)  // the head's first S pairs of dims: one CTA each
@@ -875,6 +878,11 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
 }
 
 // ------------------------------------------------------------------ launch
+// Two CTAs per SM at most, as their registers want it: the launch record counts on it
+// (k3_max_resident_ctas), so the shared memory sees to it.
+constexpr size_t kQ8SmemLeast = 77 * 1024;
+static_assert(sizeof(Q8StepSmem<128>) <= kQ8SmemLeast, "of a dense step");
+
 template <int D, bool kSparse>
 static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
     static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
@@ -885,14 +893,14 @@ static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     sizeof(Q8StepSmem<D>) + (kSparse ? kQ8MaxBlocks * 6 : 0));
+                                     kSparse ? sizeof(Q8StepSmem<D>) + kQ8MaxBlocks * 6 : kQ8SmemLeast);
         if (e != cudaSuccess) return e;
         if (dev < 32) configured.fetch_or(1u << dev, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster);
     cfg.blockDim = dim3(kQ8Threads);
-    cfg.dynamicSmemBytes = sizeof(Q8StepSmem<D>) + (kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + static_cast<size_t>(p.n_blocks) * 2 : 0);
+    cfg.dynamicSmemBytes = std::max(kQ8SmemLeast, sizeof(Q8StepSmem<D>) + (kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + static_cast<size_t>(p.n_blocks) * 2 : 0));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -157,7 +157,6 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
     p.Hq = g.n_q_heads;
     p.G = g.n_q_heads / g.n_kv_heads;
     p.cap = g.capacity;
-    p.wait_ns = qa::kWaitTimeoutNs;
     p.eps = g.rms_eps;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.head_dim)));
     const qa::StreamRef at = qa::stream_ref(s, c->device);
@@ -179,6 +178,9 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
             p.ctas += splits[i] * g.n_kv_heads;
         }
         p.early = !a.pos_dev && qa::launch_order().layer_settled(at, c, layer, resident) ? 1 : 0;
+        const qa::FaultPlan f = qa::take_fault(QA_KERNEL_DECODE_ATTN);
+        p.fault = f.fault;
+        p.wait_ns = f.wait_ns;
         if (qa::launch_q8_decode(p, g.head_dim, s) != cudaSuccess) {
             cudaGetLastError();
             return QA_ERR_CUDA;
@@ -398,6 +400,8 @@ QA_API qa_status qa_q8_read(qa_q8_cache *c, int layer, int batch, const int32_t 
     if (T == 0) return QA_OK;
     if (!k_out && !v_out) return QA_ERR_INVALID_ARG;
     if (!aligned16(k_out) || !aligned16(v_out)) return QA_ERR_ALIGNMENT;
+    const int64_t kb = T * c->cfg.n_kv_heads * 2 * c->cfg.head_dim;
+    if (overlap({k_out, kb}, {v_out, kb})) return QA_ERR_INVALID_ARG;
     DeviceScope dev(c->device);
     if (!dev.ok()) return QA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -69,6 +69,7 @@ struct Q8StepParams {
     int nseq, ctas, cluster;             // sequences, CTAs with work, CTAs of a cluster (a multiple of every S)
     int per_seq;                         // CTAs of each sequence where all have the same number, else 0
     int early;                           // nothing that may still run writes this layer
+    int fault;                           // test hook: the last CTA of the first kv head sends nothing (FaultPlan)
     uint64_t wait_ns;                    // limit of every bounded wait
     float eps, scale_log2;               // scale_log2: log2(e) / sqrt(D)
     Q8Seq seq[kQ8MaxSeqPerLaunch];       // by falling S

@@ -272,11 +272,12 @@ qa_status qa_get_device_error(qa_cache *cache, uint32_t *detail);
 
 /* Failure-detection test hook.  Arms the next launch of `kernel`
  * (QA_KERNEL_PREFILL_ATTN, or QA_KERNEL_DECODE_ATTN: decode steps, short
- * chunks and qa_decode_step_noalloc, and those of a 4-bit cache), process-wide: in that launch one tile
+ * chunks and qa_decode_step_noalloc, and those of a 4-bit or 8-bit cache), process-wide: in that launch one tile
  * copy is withheld (prefill: a V tile of the first thread block, or both
  * halves of it in the first CTA pair of the pair form; decode: the first cache
  * chunk of each block of the first sequence's first kv-head group that streams
- * any), so a wait for it can never succeed, and every bounded
+ * any; a step on an 8-bit cache: what the last thread block of the first sequence's first
+ * kv head sends to the others, if it has several), so a wait for it can never succeed, and every bounded
  * wait of the launch gives up after wait_us
  * microseconds (1 .. 2000000) instead of 2 s.  The waiting thread records
  * QA_ERR_DEVICE_TIMEOUT (kernel and site in the detail word) in the error
@@ -528,14 +529,16 @@ qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t 
  *
  * Conventions as above; a call on more than 64 sequences is several launches, and an
  * error of a later one leaves the earlier ones enqueued.  Calls may be made with
- * another device current; the stream belongs to the cache's device.  Every kernel
- * here waits for the one before it on the stream before it reads or writes anything,
- * so calls on this cache are ordered like plain launches, and may be captured into
- * graphs (but qa_q8_prefill).  It lets the next kernel start its set-up once it has
- * waited: the decode calls of the other caches, which read q, k, v and the weights
- * early, must not take what a call on this cache writes (out, k_held, v_held) as their
- * inputs unless another kernel or copy on the stream lies between them.  Outputs must
- * share no byte with inputs or with each other (INVALID_ARG). */
+ * another device current; the stream belongs to the cache's device.  Outputs share no
+ * byte with inputs or with each other (INVALID_ARG).
+ * All calls but qa_q8_prefill may be captured into graphs.  qa_q8_append, qa_q8_read and
+ * qa_q8_prefill are ordered on their stream like plain launches.  Decode and sparse
+ * steps overlap earlier kernels of the stream like qa_decode_step, with the same
+ * condition on other code's kernels between the calls: they read q, k, v and the weights
+ * before an earlier call of this library has finished, so what that writes (out, k_held,
+ * v_held, k_out, v_out) is no input of a later step unless another kernel or copy on the
+ * stream lies between them.  (With device positions, and behind a call that writes the
+ * same layer, a step waits first.) */
 typedef struct qa_q8_cache qa_q8_cache; /* opaque */
 
 /* Kernels counted by qa_q8_stats. */
