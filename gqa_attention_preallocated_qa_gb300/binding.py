@@ -23,7 +23,7 @@ STATUS_NAMES = {0: "QA_OK", 1: "QA_ERR_INVALID_ARG", 2: "QA_ERR_UNSUPPORTED_SHAP
                 7: "QA_ERR_DEVICE_TIMEOUT", 8: "QA_ERR_DEVICE_BOUNDS"}
 KERNELS = ("norm_rope_append", "prefill_attn", "decode_attn", "reset")
 Q4_KERNELS = ("norm_rope", "quantise", "dequantise", "prefill_attn", "decode")
-Q8_KERNELS = ("norm_rope", "write", "read", "prefill_attn", "decode", "sparse")
+Q8_KERNELS = ("write", "read", "prefill_attn", "decode", "sparse")
 
 
 class QaError(RuntimeError):

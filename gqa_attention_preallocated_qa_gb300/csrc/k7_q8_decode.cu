@@ -864,10 +864,10 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         if (row == kQ8Block - 1) {  // the block that the token is in is complete
             uint4 x[2][D / 16];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-                q8_seal_rows<D>(kv, warp, sm.seal, x[kv], [&](int, int r, int d0) {
-                    return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]);
-                });
+            for (int kv = 0; kv < 2; ++kv) {
+                q8_seal_load<D>(kv, warp, x[kv], [&](int, int r, int d0) { return *reinterpret_cast<const uint4 *>(&sm.rows[kv][r][d0]); });
+                q8_seal_sums<D>(kv, warp, sm.seal, x[kv]);
+            }
             __syncthreads();
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv)

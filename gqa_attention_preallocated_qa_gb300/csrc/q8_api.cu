@@ -32,7 +32,7 @@ struct qa_q8_cache {
     __nv_bfloat16 *tail = nullptr;
     qa::Q8Tail *state = nullptr;
     uint32_t *err = nullptr;
-    int32_t *ws_lens = nullptr;     // written by the transform kernel, not read
+    uint32_t *tickets = nullptr;    // of a prefill's rows, [workspace slot][kv head]
     const float2 *rope = nullptr;   // shared (rope_table_take)
     qa::PrefillWorkspace ws;        // what prefill attention needs
     uint64_t cache_bytes = 0, scratch_bytes = 0;
@@ -223,8 +223,8 @@ qa_status step(qa_q8_cache *c, int layer, int batch, const StepCall &a, bool spa
 
 // One launch group of a prefill: up to ws.slots() sequences.
 struct PrefillGroup {
-    qa::K1Params k1;
-    qa::Q8RowsParams older, write;
+    qa::Q8PrefillRowsParams rows;
+    qa::Q8RowsParams older;
     qa::K2Job k2;
 };
 
@@ -233,8 +233,8 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
     const qa_config &g = c->cfg;
     const int D = g.head_dim, Hq = g.n_q_heads, Hkv = g.n_kv_heads;
     const int64_t ws_seq = c->ws.seq_stride();
-    qa::K1Params &k1 = pg.k1;
-    k1 = qa::K1Params{};
+    pg.rows = qa::Q8PrefillRowsParams{};
+    qa::K1Params &k1 = pg.rows.k1;
     k1.q = static_cast<const __nv_bfloat16 *>(q) + row0 * Hq * D;
     k1.k = static_cast<const __nv_bfloat16 *>(k) + row0 * Hkv * D;
     k1.v = static_cast<const __nv_bfloat16 *>(v) + row0 * Hkv * D;
@@ -243,7 +243,6 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
     k1.qp = static_cast<__nv_bfloat16 *>(out) + row0 * Hq * D;
     k1.kc = c->ws.rows(0);
     k1.vc = c->ws.rows(1);
-    k1.lens = c->ws_lens;
     k1.rope = c->rope;
     k1.err = c->err;
     k1.head_stride = c->ws.head_stride();
@@ -253,36 +252,32 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
     k1.cap = g.capacity;
     k1.eps = g.rms_eps;
     k1.nseq = n;
+    pg.rows.layer = layer_of(c, layer);
+    pg.rows.tickets = c->tickets;
+    pg.rows.seq0 = s0;
     pg.older = qa::Q8RowsParams{};
-    pg.older.layer = layer_of(c, layer);
+    pg.older.layer = pg.rows.layer;
     pg.older.rows[0] = c->ws.rows(0);
     pg.older.rows[1] = c->ws.rows(1);
     pg.older.tok = D;
     pg.older.head = c->ws.head_stride();
     pg.older.nseq = n;
     pg.older.seq0 = s0;
-    pg.write = pg.older;
     pg.older.factors = c->ws.factors();
     pg.older.factor_stride = c->ws.factor_stride();
-    bool scaled = false, older = false;  // some chunk sees a complete block; an earlier row
+    bool scaled = false;  // some chunk sees a complete block
     for (int i = 0; i < n; ++i) {
-        const int P = start[s0 + i], N = ntok[s0 + i], first = P / qa::kQ8Block * qa::kQ8Block;
+        const int P = start[s0 + i], N = ntok[s0 + i];
         k1.cu[i + 1] = k1.cu[i] + N;
         k1.start[i] = P;
-        // The rows before the new ones, and the factors of all its tiles.
-        pg.older.ntok[i] = P;
+        pg.rows.item0[i + 1] = pg.rows.item0[i] + (N > 0 ? qa::q8_read_items(P, P + N) : 0);
+        // The complete blocks before the new rows, and the factors of all tiles.
+        pg.older.ntok[i] = P / qa::kQ8Block * qa::kQ8Block;
         pg.older.off[i] = i * ws_seq;
         pg.older.item0[i + 1] = pg.older.item0[i] + (N > 0 ? qa::q8_tile_items(P + N) : 0);
         scaled = scaled || (N > 0 && P >= qa::kQ8Block);
-        older = older || (N > 0 && P > 0);
-        // All rows of the first block are in the workspace by then.
-        pg.write.start[i] = P;
-        pg.write.ntok[i] = N;
-        pg.write.first[i] = first;
-        pg.write.off[i] = i * ws_seq + static_cast<int64_t>(first) * D;
-        pg.write.item0[i + 1] = pg.write.item0[i] + (N > 0 ? qa::q8_write_items(P, P + N) : 0);
     }
-    if (!older) pg.older.item0[n] = 0;  // nothing to read
+    if (!scaled) pg.older.item0[n] = 0;  // nothing to read, no factors
     k1.T = k1.cu[n];
     return k1.T == 0 || c->ws.plan(0, n, start + s0, ntok + s0, k1.cu, k1.qp, c->err, scaled, pg.k2);
 }
@@ -308,7 +303,9 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
     const size_t D = g.head_dim;
     const size_t codes = blocks * 2 * qa::kQ8Block * D, scales = blocks * sizeof(float2), bounds = blocks * 2 * D;
     const size_t tail = heads * 4 * qa::kQ8Block * D * sizeof(__nv_bfloat16), state = heads * sizeof(qa::Q8Tail);
-    const size_t total = align256(codes) + align256(scales) + align256(bounds) + align256(tail) + align256(state) + 256;
+    const size_t tickets = static_cast<size_t>(qa::kMaxSeqPerLaunch) * g.n_kv_heads * sizeof(uint32_t);
+    const size_t total = align256(codes) + align256(scales) + align256(bounds) + align256(tail) + align256(state) +
+                         align256(tickets) + 256;
     bool ok = cudaGetDevice(&c->device) == cudaSuccess &&
               cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess &&
               cudaMalloc(&c->mem, total) == cudaSuccess && cudaMemsetAsync(c->mem, 0, total, nullptr) == cudaSuccess;
@@ -324,16 +321,15 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
         c->bounds = reinterpret_cast<int8_t *>(take(bounds));
         c->tail = reinterpret_cast<__nv_bfloat16 *>(take(tail));
         c->state = reinterpret_cast<qa::Q8Tail *>(take(state));
+        c->tickets = reinterpret_cast<uint32_t *>(take(tickets));
         c->err = reinterpret_cast<uint32_t *>(at);
-        c->ws_lens = reinterpret_cast<int32_t *>(at + 128);
-        static_assert(qa::kMaxSeqPerLaunch * sizeof(int32_t) <= 128, "behind the error word");
         if (cudaMemsetAsync(c->state, 0xff, state, nullptr) != cudaSuccess) return QA_ERR_CUDA;  // no rows kept
         c->rope = qa::rope_table_take(c->device, g.rope_theta, g.head_dim, g.capacity);
         return c->rope && cudaStreamSynchronize(nullptr) == cudaSuccess ? QA_OK : QA_ERR_CUDA;
     }) == QA_OK;
     c->ws.init(g, c->num_sms, true);
     c->cache_bytes = codes + scales + bounds + tail + state;
-    c->scratch_bytes = 256 + c->ws.bytes() + static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
+    c->scratch_bytes = 256 + tickets + c->ws.bytes() + static_cast<size_t>(g.capacity) * (g.head_dim / 2) * sizeof(float2);
     if (!ok) {
         free_all(c);
         delete c;
@@ -468,7 +464,7 @@ QA_API qa_status qa_q8_prefill(qa_q8_cache *c, int layer, int batch, const int32
                 cudaGetLastError();
                 return QA_ERR_CUDA;
             }
-            row0 += groups.back().k1.T;
+            row0 += groups.back().rows.k1.T;
         }
         return QA_OK;
     });
@@ -485,15 +481,12 @@ QA_API qa_status qa_q8_prefill(qa_q8_cache *c, int layer, int batch, const int32
             c->launches[kernel]++;
             return true;
         };
-        if (pg.k1.T == 0) return QA_OK;
-        pg.k1.signal_early = 1;  // what follows waits for it, or runs beside it
-        if (!done(qa::launch_k1(pg.k1, g.head_dim, s), QA_Q8_KERNEL_NORM_ROPE)) return QA_ERR_CUDA;
-        const bool older = pg.older.item0[pg.older.nseq] > 0;  // (of no older row: no factors either)
-        if ((older && !done(qa::launch_q8_read(pg.older, g.head_dim, s), QA_Q8_KERNEL_READ)) ||
-            !done(qa::launch_q8_write(pg.write, g.head_dim, s), QA_Q8_KERNEL_WRITE) ||
+        if (pg.rows.k1.T == 0) return QA_OK;
+        if (!done(qa::launch_q8_prefill_rows(pg.rows, g.head_dim, s), QA_Q8_KERNEL_WRITE) ||
+            (pg.older.item0[pg.older.nseq] > 0 && !done(qa::launch_q8_read(pg.older, g.head_dim, s), QA_Q8_KERNEL_READ)) ||
             !done(c->ws.launch(pg.k2, s), QA_Q8_KERNEL_PREFILL_ATTN)) {
-            // A kernel that signalled early may no longer be followed by one that waits for
-            // it: let it finish before anything else is enqueued.
+            // What was enqueued may no longer be followed by a kernel that waits for it: let
+            // it finish before anything else is enqueued.
             cudaStreamSynchronize(s);
             return QA_ERR_CUDA;
         }

@@ -101,18 +101,32 @@ struct Q8Sealed {
 };
 
 // K (kv 0) or V of a block from its 64 rows: load8(kv, row, d0) gives 8 dims of one.  Four
-// warps take part, kt: the 16 rows of this one.  Two steps, between them __syncthreads():
-// the rows and what they come to, then the codes.
+// warps take part, kt: the 16 rows of this one.  Three steps: the rows, what they come to
+// and, after __syncthreads(), the codes.
+// Load i of a lane is 8 dims of row q8_seal_row(kv, kt, i), from dim q8_seal_dim(kv, i).
+__device__ __forceinline__ int q8_seal_row(int kv, int kt, int i) {
+    const int lane = threadIdx.x & 31;
+    return 16 * kt + (kv == 0 ? (lane >> 2) + 8 * (i & 1) : 2 * (lane & 3) + (i & 1) + 8 * ((i >> 1) & 1));
+}
+template <int D>
+__device__ __forceinline__ int q8_seal_dim(int kv, int i) {
+    const int lane = threadIdx.x & 31;
+    return kv == 0 ? 32 * (i >> 1) + 8 * (lane & 3) : (D / 8) * (lane >> 2) + 8 * (i >> 2);
+}
 template <int D, typename Load>
-__device__ __forceinline__ void q8_seal_rows(int kv, int kt, Q8SealSmem<D> &sm, uint4 (&x)[D / 16], Load &&load8) {
-    constexpr int NX = D / 16;  // loads of 8 dims per lane
-    const unsigned FULL = 0xffffffffu;
+__device__ __forceinline__ void q8_seal_load(int kv, int kt, uint4 (&x)[D / 16], Load &&load8) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int i = 0; i < NX; ++i) {
+    for (int i = 0; i < D / 16; ++i) {
         if (kv == 0) x[i] = load8(0, 16 * kt + g + 8 * (i & 1), 32 * (i >> 1) + 8 * t);
         else x[i] = load8(1, 16 * kt + 2 * t + (i & 1) + 8 * ((i >> 1) & 1), (D / 8) * g + 8 * (i >> 2));
     }
+}
+template <int D>
+__device__ __forceinline__ void q8_seal_sums(int kv, int kt, Q8SealSmem<D> &sm, const uint4 (&x)[D / 16]) {
+    constexpr int NX = D / 16;  // loads of 8 dims per lane
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31, t = lane & 3;
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < NX; ++i) {

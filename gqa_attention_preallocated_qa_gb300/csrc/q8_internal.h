@@ -36,13 +36,13 @@ struct Q8RowsParams {
     __nv_bfloat16 *rows[2];              // of K and V (write: read only; read: either may be null)
     int64_t tok, head;
     int nseq, seq0;                      // seq0: cache slot of launched sequence 0
-    // A read for prefill attention of a chunk at position ntok: codes as they are, with the
-    // factors of their blocks here ([slot][head][factor_stride], all of the sequence's
-    // tiles of 128); null otherwise.
+    // A read for prefill attention: the codes of the first ntok rows (whole blocks) as they
+    // are, with the factors of their blocks and of the rest of the sequence's tiles of 128
+    // here, [launched sequence][head][factor_stride]; null otherwise.
     float4 *factors;
     int factor_stride;
     int start[kQ8MaxSeqPerLaunch], ntok[kQ8MaxSeqPerLaunch];
-    int first[kQ8MaxSeqPerLaunch];       // position of the row at off (write: start, or its block's first)
+    int first[kQ8MaxSeqPerLaunch];       // position of the row at off
     int item0[kQ8MaxSeqPerLaunch + 1];   // first work item (block) of each launched sequence
     int64_t off[kQ8MaxSeqPerLaunch];
 };
@@ -86,6 +86,17 @@ QA_HD int q8_write_items(int start, int end) {
 QA_HD int q8_tile_items(int end) { return (end + 127) / 128 * 2; }
 QA_HD int q8_read_items(int start, int end) { return (end - 1) / kQ8Block - start / kQ8Block + 1; }
 
+// The rows of a prefill: k1 as for K1, its cache pointers and strides the workspace's.
+struct Q8PrefillRowsParams {
+    K1Params k1;
+    Q8Layer layer;
+    uint32_t *tickets;                   // [launched sequence][kv head], zero between launches
+    int seq0;                            // cache slot of launched sequence 0
+    int item0[kMaxSeqPerLaunch + 1];     // first block of each launched sequence
+};
+static_assert(sizeof(Q8PrefillRowsParams) <= 4096, "travels in the 4 KB of kernel parameters");
+
+cudaError_t launch_q8_prefill_rows(const Q8PrefillRowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_write(const Q8RowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8RowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_decode(const Q8StepParams &p, int D, cudaStream_t stream);

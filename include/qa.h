@@ -543,13 +543,12 @@ typedef struct qa_q8_cache qa_q8_cache; /* opaque */
 
 /* Kernels counted by qa_q8_stats. */
 enum {
-    QA_Q8_KERNEL_NORM_ROPE = 0,    /* K1: a prefill's rows into the workspace */
-    QA_Q8_KERNEL_WRITE = 1,        /* K6: rows into the cache */
-    QA_Q8_KERNEL_READ = 2,         /* K6: rows out of the cache */
-    QA_Q8_KERNEL_PREFILL_ATTN = 3, /* K2 on the workspace (and the join of its parts) */
-    QA_Q8_KERNEL_DECODE = 4,       /* K7: decode steps */
-    QA_Q8_KERNEL_SPARSE = 5,       /* K7: sparse steps */
-    QA_Q8_NUM_KERNELS = 6
+    QA_Q8_KERNEL_WRITE = 0,        /* K6: rows into the cache (a prefill's: with norm and rotation) */
+    QA_Q8_KERNEL_READ = 1,         /* K6: rows out of the cache */
+    QA_Q8_KERNEL_PREFILL_ATTN = 2, /* K2 on the workspace (and the join of its parts) */
+    QA_Q8_KERNEL_DECODE = 3,       /* K7: decode steps */
+    QA_Q8_KERNEL_SPARSE = 4,       /* K7: sparse steps */
+    QA_Q8_NUM_KERNELS = 5
 };
 
 /* Allocate an 8-bit cache on the current device, with the geometry that

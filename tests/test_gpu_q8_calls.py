@@ -362,7 +362,7 @@ def test_more_sequences_than_a_launch(qa):
         c.check_read(lens)
         toks = c.tokens(n, 8)
         out, lists = step(qa, c, lens, toks, blocks=2)
-        assert qa.qa_q8_stats(c.h) == {"norm_rope": 0, "write": 2, "read": 2, "prefill_attn": 0, "decode": 0, "sparse": 2}
+        assert qa.qa_q8_stats(c.h) == {"write": 2, "read": 2, "prefill_attn": 0, "decode": 0, "sparse": 2}
         c.ref.write(lens, [1] * n, f64(toks[1]), f64(toks[2]))
         for b, pos in enumerate(lens):
             close(out[b:b + 1], *c.want(b, pos, toks[0][b:b + 1].double(), lists[b].cpu().numpy()), what=f"sequence {b}")
@@ -508,7 +508,7 @@ def test_refusals_change_nothing(qa):
         assert (out == 3.0).all() and (lists == 3).all()
         c.check_read([70, 20])
         qa.qa_q8_append(c.h, 0, [0, 128], [0, 0], None, None)  # no rows: nothing to do
-        assert qa.qa_q8_stats(c.h) == {"norm_rope": 0, "write": 1, "read": 1, "prefill_attn": 0, "decode": 0, "sparse": 0}
+        assert qa.qa_q8_stats(c.h) == {"write": 1, "read": 1, "prefill_attn": 0, "decode": 0, "sparse": 0}
 
 
 @pytest.mark.parametrize("blocks", [0, 4, 8])
