@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
     const int64_t sh = static_cast<int64_t>(p.seq0 + z) * p.layer.Hkv + h;
     const __nv_bfloat16 *src[2] = {p.rows[0] + p.off[z] + h * p.head, p.rows[1] + p.off[z] + h * p.head};
     auto source8 = [&](int kv, int pos, int d0) {
-        return *reinterpret_cast<const uint4 *>((kv ? src[1] : src[0]) + static_cast<int64_t>(pos - p.first[z]) * p.tok + d0);
+        return *reinterpret_cast<const uint4 *>((kv ? src[1] : src[0]) + static_cast<int64_t>(pos - start) * p.tok + d0);
     };
     const int kv_of_warp = threadIdx.x >> 7, kt = threadIdx.x >> 5 & 3;  // four warps for K, four for V
     uint4 x[D / 16];
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
     const float2 scale = p.layer.scales[sh * p.layer.nblk + first];
     auto row8 = [&](int kv, int r, int d0) {  // of the first block: new, kept, or from the codes
         const int pos = first * kQ8Block + r;
-        if (pos >= p.first[z]) return source8(kv, pos, d0);
+        if (pos >= start) return source8(kv, pos, d0);
         if (r < plan.from_rows)
             return *reinterpret_cast<const uint4 *>(q8_tail_rows<D>(p.layer, sh, plan.from, kv) + r * D + d0);
         return q8_row8<D>(codes + kv * kQ8Block * D, kv != 0, kv ? scale.y : scale.x, r, d0);
@@ -93,12 +93,16 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
 // -------------------------------------------------------------------- a prefill's rows
 // RMSNorm and rotation of a block's keys and of the queries that share its kv head, into
 // the attention's workspace and the staging buffer, and the block's codes (or the rows to
-// keep) on the way: each row is read once and written once (K1 and q8_write_kernel after
-// it: 4 x 2048 tokens 32 + 12 us).  A row of keys or queries is on four lanes, 8 dims
-// of every 32 each, as the codes' layout has it: a rotated pair is in one lane, and the
-// sum of squares adds up in the order of norm_rope_row, so that a key gets the same bits
-// from a prefill and from a step.  The rotary rows are shared by the block's 1 + G heads
-// through shared memory.
+// keep) on the way: each row is read once and written once.  A row of keys or queries is
+// on four lanes, 8 dims of every 32 each, as the codes' layout has it: a rotated pair is
+// in one lane, and the sum of squares adds up in the order of norm_rope_row, so that a key
+// gets the same bits from a prefill and from a step.  The rotary rows are shared by the
+// block's 1 + G heads through shared memory.
+//   K1 and q8_write_kernel after it take one pass more over keys and values and one launch
+// more.  A call takes, with them / with this (32/8 heads, D = 128): 1778 tokens of two
+// chunks 119 / 113 us, 64 tokens (2/1 heads, D = 64) 13.6 / 12.5, 4 x 2048 171 / 174.  At 8192
+// tokens this takes 48 us alone, 4.5 TB/s: two CTAs of 8 warps an SM, for their 128
+// registers, fill half of the issue slots; three of them with 80 take 13 us longer.
 template <int D>
 struct alignas(16) Q8RowsSmem {
     // Rotary rows, (cos_a, sin_a, cos_b, sin_b) of two pairs each: pairs 16 c + 4 t + e at
@@ -107,13 +111,6 @@ struct alignas(16) Q8RowsSmem {
     uint4 w[2][D / 8];                // norm weights of queries and keys
     Q8SealSmem<D> seal;
 };
-__device__ __forceinline__ void q8_copy16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void q8_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void q8_copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory"); }
-
 // A row in x[c], c = 0 .. D/32 - 1; w, cs: weights and its rotary row, in shared memory.
 template <int D>
 __device__ __forceinline__ void q8_norm_rope(uint4 (&x)[D / 32], const uint4 *w, float eps, const float4 *cs) {
@@ -179,7 +176,6 @@ __global__ void __launch_bounds__(256, 2) q8_prefill_rows_kernel(const __grid_co
         const int i = threadIdx.x % (D / 8);
         q8_copy16(&sm.w[threadIdx.x / (D / 8)][i], reinterpret_cast<const uint4 *>(threadIdx.x < D / 8 ? k1.wq : k1.wk) + i);
     }
-    q8_copy_commit();
     // Four warps take K, four V.  Of the 2 G turns of 8 query rows (row g or g + 8 of a warp's
     // 16, of one head) the latter, who norm nothing else, take two more.
     const int kv = threadIdx.x >> 7, kt = threadIdx.x >> 5 & 3;
@@ -213,7 +209,7 @@ __global__ void __launch_bounds__(256, 2) q8_prefill_rows_kernel(const __grid_co
     for (int i = 0; i < D / 16; ++i) x[i] = row8(q8_seal_row(kv, kt, i), q8_seal_dim<D>(kv, i));
     uint4 even[D / 32], odd[D / 32];
     load(0, even);
-    q8_copy_wait<0>();  // the rotary rows
+    q8_copy_wait();  // the rotary rows
     __syncthreads();
     if (kv == 0) {
 #pragma unroll
@@ -324,7 +320,7 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const __grid_constant__ Q8
             const int buffer = buffer_of(r);
             const uint4 x = buffer >= 0 ? *reinterpret_cast<const uint4 *>(q8_tail_rows<D>(p.layer, sh, buffer, kv) + r * D + d0)
                                         : q8_row8<D>(codes[kv], kv != 0, kv ? scale.y : scale.x, r, d0);
-            *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(blk * kQ8Block + r - p.first[z]) * p.tok + d0) = x;
+            *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(blk * kQ8Block + r - start) * p.tok + d0) = x;
         }
     }
 }

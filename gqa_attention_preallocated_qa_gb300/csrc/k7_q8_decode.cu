@@ -39,7 +39,6 @@
 // and finds the n-th largest for itself, two bits at a time.
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "norm_rope.cuh"
 #include "q8_device.cuh"
@@ -85,10 +84,6 @@ __device__ __forceinline__ uint4 q8_load(const uint8_t *p) {
                  : "l"(p));
     return x;
 }
-__device__ __forceinline__ void q8_cp_async(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void q8_cp_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // Four bytes into the shared memory of a CTA of the cluster, counted on an mbarrier there.
 __device__ __forceinline__ void q8_send(uint32_t addr, uint32_t x, uint32_t bar) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(x), "r"(bar)
@@ -521,8 +516,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
         for (int e = threadIdx.x; e < plan.from_rows * LPR; e += kQ8Threads) {
             const int r = e / LPR, d0 = e % LPR * 8;
-            q8_cp_async(&sm.rows[0][r][d0], tail + r * D + d0);
-            q8_cp_async(&sm.rows[1][r][d0], tail + (kQ8Block + r) * D + d0);
+            q8_copy16(&sm.rows[0][r][d0], tail + r * D + d0);
+            q8_copy16(&sm.rows[1][r][d0], tail + (kQ8Block + r) * D + d0);
         }
     }
     uint32_t top = 0;
@@ -726,7 +721,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     // the sum of two bf16 numbers.
     const int tile = kQ8Warps - 1 - warp;
     if (me == 0) {
-        q8_cp_wait();
+        q8_copy_wait();
         __syncthreads();
     }
     if (me == 0 && 16 * tile <= row) {

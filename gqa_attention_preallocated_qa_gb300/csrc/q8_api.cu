@@ -117,7 +117,7 @@ bool fill_packed(qa::Q8RowsParams &p, const qa_config &g, int s0, int n, const i
     p.head = g.head_dim;
     p.item0[0] = 0;
     for (int i = 0; i < n; ++i) {
-        p.start[i] = p.first[i] = start[s0 + i];
+        p.start[i] = start[s0 + i];
         p.ntok[i] = ntok[s0 + i];
         p.off[i] = row0 * p.tok;
         p.item0[i + 1] = p.item0[i] + (p.ntok[i] > 0 ? items(p.start[i], p.start[i] + p.ntok[i]) : 0);
@@ -244,12 +244,10 @@ bool plan_prefill(qa_q8_cache *c, int layer, int s0, int n, const int32_t *start
     k1.kc = c->ws.rows(0);
     k1.vc = c->ws.rows(1);
     k1.rope = c->rope;
-    k1.err = c->err;
     k1.head_stride = c->ws.head_stride();
     k1.seq_stride = ws_seq;
     k1.Hq = Hq;
     k1.Hkv = Hkv;
-    k1.cap = g.capacity;
     k1.eps = g.rms_eps;
     k1.nseq = n;
     pg.rows.layer = layer_of(c, layer);

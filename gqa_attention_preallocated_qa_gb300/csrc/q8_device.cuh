@@ -28,8 +28,11 @@ namespace qa {
 constexpr float kQ8Small = 5.421010862427522e-20f;  // 2^-64: smaller blocks hold zeros
 constexpr uint32_t kQ8Zero = 0x80808080u;           // four codes of zero
 
-template <int D>
-__device__ __forceinline__ int q8_block_bytes() { return 2 * kQ8Block * D; }
+// Asynchronous copies of 16 bytes into shared memory, and the wait for this thread's.
+__device__ __forceinline__ void q8_copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void q8_copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Two codes of a word as fp16 subnormals.
 __device__ __forceinline__ uint32_t q8_lo(uint32_t w) { return __byte_perm(w, 0u, 0x4140); }

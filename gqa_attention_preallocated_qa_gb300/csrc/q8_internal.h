@@ -11,12 +11,12 @@
 
 namespace qa {
 
-// Kernel numbers in the error word of an 8-bit cache.
-constexpr uint32_t kKernQ8Rows = 6, kKernQ8Decode = 7;
+// Kernel number in the error word of an 8-bit cache.
+constexpr uint32_t kKernQ8Decode = 7;
 
 constexpr int kQ8MaxSeqPerLaunch = 64;  // sequences carried in the parameters of one launch
 constexpr int kQ8MaxBlocks = 16384;     // blocks of a sequence: the selection's scores fit shared memory
-constexpr int kQ8MaxSplits = 16;    // CTAs that share a (sequence, kv head)
+constexpr int kQ8MaxSplits = 16;        // CTAs that share a (sequence, kv head)
 
 // One layer.  A block's codes are the 64 D bytes of K, then those of V, each in
 // the order that the decode kernel's MMA fragments take them (q8_device.cuh).
@@ -30,7 +30,7 @@ struct Q8Layer {
 };
 
 // Rows in packed [T][Hkv][D] tensors or in a layer laid out [slot][head][position][D]:
-// base + off[z] + token * tok + head * head, in elements.
+// base + off[z] + (position - start[z]) * tok + head * head, in elements.
 struct Q8RowsParams {
     Q8Layer layer;
     __nv_bfloat16 *rows[2];              // of K and V (write: read only; read: either may be null)
@@ -42,7 +42,6 @@ struct Q8RowsParams {
     float4 *factors;
     int factor_stride;
     int start[kQ8MaxSeqPerLaunch], ntok[kQ8MaxSeqPerLaunch];
-    int first[kQ8MaxSeqPerLaunch];       // position of the row at off
     int item0[kQ8MaxSeqPerLaunch + 1];   // first work item (block) of each launched sequence
     int64_t off[kQ8MaxSeqPerLaunch];
 };

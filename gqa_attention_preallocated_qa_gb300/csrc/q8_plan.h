@@ -42,8 +42,14 @@ inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, 
         if (cut(per) <= num_sms / 2 - num_sms / 16) return top;
     for (int per = 1; per <= 4; ++per)
         if (cut(per) <= num_sms) return top;
-    for (int per = 1;; ++per)
-        if (cut(per) <= 2 * num_sms || top == 1) return top;
+    // The fewest that fit; one each where not even those do.
+    int lo = 0, hi = (work[0] + 3) / 4;  // cut(hi) is of ones
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (cut(mid) <= 2 * num_sms) hi = mid; else lo = mid;
+    }
+    cut(hi);
+    return top;
 }
 
 }  // namespace qa
