@@ -156,6 +156,15 @@ struct alignas(16) Q8StepSmem {
     int abort;
 };
 
+// Waits for the sums of the others.  A CTA that has given up waiting, for these or for the
+// scores, stays as long again: what a late one still sends may not find it gone.  (One
+// that missed scores sends no sums, so nothing is sent later than that.)
+__device__ __noinline__ void q8_wait_sums(uint32_t bar, volatile int *abort, uint32_t *err, uint64_t wait_ns) {
+    if (mbar_wait_cluster(bar, 0, abort, err, kKernQ8Decode, 3, wait_ns)) return;
+    int alone = 0;
+    mbar_wait_cluster(bar, 0, &alone, err, kKernQ8Decode, 4, wait_ns);
+}
+
 template <int D>
 __device__ __forceinline__ int q8_slot(int d) {
     const int g = d / (D / 8), r = d % (D / 8);
@@ -814,14 +823,14 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             const float inv = 16777216.f / l;
             griddep_wait();
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
-        } else if (!withhold || choose) {
+        } else if (choose ? listed : !withhold) {
             const int r = e >> log_E;
             st_async_f32x2(map_rank(to_o + (me * E + (e & (E - 1))) * 4, first_rank + r), o.x, o.y, map_rank(bar, first_rank + r));
             if (e % D < 2 * S)  // the head's first S pairs of dims: one CTA each
                 st_async_f32x2(map_rank(to_l + head * 8, first_rank + e % D / 2), most, l, map_rank(bar, first_rank + e % D / 2));
         }
     }
-    if (S > 1) mbar_wait_cluster(bar, 0, &sm.abort, p.err, kKernQ8Decode, 3, p.wait_ns);
+    if (S > 1) q8_wait_sums(bar, &sm.abort, p.err, p.wait_ns);
     griddep_wait();  // everything before has finished: from here on this writes
     if (S > 1) {
         for (int i = 2 * threadIdx.x; i < E; i += 2 * kQ8Threads) {

@@ -548,3 +548,26 @@ def test_a_prefill_whose_wait_runs_out(qa):
             qa.qa_debug_arm_wait_timeout(-1, 0)
         check_prefill(qa, c, [300, 0], [100, 100], 8)
         assert qa.qa_q8_get_device_error(c.h) == (0, 0)
+
+
+@pytest.mark.parametrize("blocks", [0, 8])
+def test_who_gave_up_waiting_stays_for_what_is_late(qa, blocks):
+    """A thread block whose wait ran out leaves after a second limit, in which what the others
+    of its cluster may still send it finds it there."""
+    lens, limit_us = [700, 1100], 20000
+    with Cache(qa, len(lens), 32, 8, 128, 1200) as c:
+        c.fill(lens, 3)
+        toks = c.tokens(len(lens), 8)
+        step(qa, c, lens, toks, blocks=blocks)
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        qa.qa_debug_arm_wait_timeout(2, limit_us)
+        try:
+            begin.record()
+            step(qa, c, lens, toks, blocks=blocks)
+            end.record()
+            st, word = qa.qa_q8_get_device_error(c.h)
+            assert st == 7 and word & 0xff == 1 and word >> 8 & 0xff == 7
+        finally:
+            qa.qa_debug_arm_wait_timeout(-1, 0)
+        assert begin.elapsed_time(end) >= 2 * limit_us * 1e-3
