@@ -669,8 +669,9 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         float m0 = kQ8NoRef, m1 = kQ8NoRef;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            // S is 2^24 times too small, and 2^8 too large by the queries' power of two.
-            const float c0 = sc[n].x * 65536.f * qs0, c1 = sc[n].x * 65536.f * qs1;
+            // S is 2^24 times too small, and 2^8 too large by the queries' power of two.  (The
+            // 2^16 last: the scale alone may be near fp32's largest numbers.)
+            const float c0 = sc[n].x * qs0 * 65536.f, c1 = sc[n].x * qs1 * 65536.f;
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt) {
                 s[n][kt][0] *= c0;

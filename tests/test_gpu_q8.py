@@ -185,6 +185,27 @@ def test_decode_is_attention_over_what_is_held(qa, hq, hkv, d):
         assert qa.qa_q8_get_device_error(c.h)[0] == 0
 
 
+@pytest.mark.parametrize("blocks", [0, 2])
+@pytest.mark.parametrize("q_size,k_size", [(2.0 ** -120, 2.0 ** 120), (2.0 ** 60, 2.0 ** -60)])
+def test_scores_of_ordinary_size_from_queries_and_keys_that_are_not(qa, q_size, k_size, blocks):
+    """A query row of 2^-120 is scaled by 2^115 at most, so fp16 holds it in steps of 2^-139: half
+    a step of 2^-19 of such a value, 128 times, against keys below 5 and log2(e) / sqrt(D) = 0.1275,
+    moves a score by less than 2^-13; 2^-11 + 2 * 2^-13 is below 2^-10."""
+    hq, hkv, d, pos = 8, 2, 128, 300
+    with Cache(qa, 1, hq, hkv, d, 400) as c:
+        k, v = rows(1, pos, hkv, d), rows(2, pos, hkv, d)
+        c.append([0], [pos], k * k_size, v)
+        q, nk, nv = rows(3, 1, hq, d) * q_size, rows(4, 1, hkv, d) * k_size, rows(5, 1, hkv, d)
+        out = torch.empty_like(q)
+        lists = torch.empty(1, hkv, max(blocks, 1), dtype=torch.int32, device="cuda")
+        if blocks:
+            qa.qa_q8_sparse_step(c.h, 0, [pos], blocks, q, nk, nv, None, None, out, lists)
+        else:
+            qa.qa_q8_decode_step(c.h, 0, [pos], q, nk, nv, None, None, out)
+        c.ref.write([pos], [1], f64(nk), f64(nv))
+        close(out, *c.want(0, pos, q.double(), lists[0].cpu().numpy() if blocks else None), p_bits=10)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_steps_follow_each_other_through_blocks(qa, d):
     lens = [60, 126, 0]
