@@ -292,12 +292,15 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
     if (!qa::supported_geometry(g.n_q_heads, g.n_kv_heads, g.head_dim)) return QA_ERR_UNSUPPORTED_SHAPE;
     if (g.capacity > qa::kQ8MaxBlocks * qa::kQ8Block || g.max_batch > 65535 || g.n_q_heads > 65535)
         return QA_ERR_UNSUPPORTED_SHAPE;
+    const int nblk = (g.capacity + qa::kQ8Block - 1) / qa::kQ8Block;
+    const size_t heads = static_cast<size_t>(g.num_layers) * g.max_batch * g.n_kv_heads;  // (below 2^63)
+    if (heads > (size_t(1) << 40) / nblk) return QA_ERR_UNSUPPORTED_SHAPE;  // the sums of bytes below stay in 64 bits
     qa_q8_cache *c = new (std::nothrow) qa_q8_cache();
     if (!c) return QA_ERR_CUDA;
     c->cfg = g;
     for (auto &x : c->launches) x = 0;
-    c->nblk = (g.capacity + qa::kQ8Block - 1) / qa::kQ8Block;
-    const size_t heads = static_cast<size_t>(g.num_layers) * g.max_batch * g.n_kv_heads, blocks = heads * c->nblk;
+    c->nblk = nblk;
+    const size_t blocks = heads * nblk;
     const size_t D = g.head_dim;
     const size_t codes = blocks * 2 * qa::kQ8Block * D, scales = blocks * sizeof(float2), bounds = blocks * 2 * D;
     const size_t tail = heads * 4 * qa::kQ8Block * D * sizeof(__nv_bfloat16), state = heads * sizeof(qa::Q8Tail);

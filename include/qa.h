@@ -552,7 +552,7 @@ enum {
 };
 
 /* Allocate an 8-bit cache on the current device, with the geometry that
- * qa_cache_alloc takes and a capacity of at most 2^20: codes, scales, the least and
+ * qa_cache_alloc takes, a capacity of at most 2^20 and at most 2^40 blocks in all: codes, scales, the least and
  * the largest code of each dimension of a block's keys, and per sequence and kv head
  * 2 x 64 rows of K and V in bf16 (zero-filled); an error word; and the rotary table
  * (shared as qa_q4_cache_alloc says).  Synchronous.

@@ -106,6 +106,15 @@ def test_alloc_rejects_bad_geometry(qa, kw, status):
     assert e.value.status == status
 
 
+@pytest.mark.parametrize("kw", [dict(max_batch=65535, n_q_heads=65535, n_kv_heads=65535, capacity=1 << 20),
+                                dict(max_batch=65535, n_q_heads=8192, n_kv_heads=8192, capacity=128)])
+def test_alloc_rejects_what_64_bits_cannot_count(qa, kw):
+    """The second one's bytes would wrap: 2^31 - 1 layers of 2^30 blocks (less 2^14) of 16 KB."""
+    with pytest.raises(qa.QaError) as e:
+        qa.qa_q8_cache_alloc(**{**dict(num_layers=(1 << 31) - 1, head_dim=128, rope_theta=1e6, rms_eps=1e-6), **kw})
+    assert e.value.status == 2
+
+
 def test_arguments_of_the_native_calls(qa):
     """Tensors, addresses, None; lists, tuples, int32 buffers: all reach the C
     entry point (which refuses the null cache), and nothing else does."""
