@@ -36,7 +36,7 @@
 // order of anything.  The bounds are 2 D bytes a block and kv head (1/64 of its
 // codes): 16 lanes (D = 128) take a block, in 8 two-way integer dot products each.
 // Every CTA of a (sequence, kv head) scores a share, sends the scores to the others,
-// and finds the n-th largest for itself, two bits at a time.
+// and finds the n-th largest for itself.
 #include <algorithm>
 #include <atomic>
 
@@ -137,7 +137,7 @@ struct alignas(16) Q8StepSmem {
     __nv_bfloat16 rows[2][kQ8Block][D + 8];   // K and V of the block that the new token is in
     float o[kQ8Warps][8][D + 8];    // a warp's sums; slot 16 m + 2 g + e of a head's row: dim (D / 8) g + 2 m + e
     union {
-        alignas(16) uint32_t hist[256];   // a sparse step's, for its choice
+        alignas(16) uint32_t hist[4][256];   // a sparse step's, for its choice
         Q8SealSmem<D> seal;               // at its end
     };
     float ref[kQ8Warps][8], l[kQ8Warps][8];
@@ -149,7 +149,6 @@ struct alignas(16) Q8StepSmem {
     uint32_t top[kQ8Warps];
     alignas(16) short up[D], down[D];             // C+, C-
     alignas(16) uint32_t part[kQ8Warps][4];
-    alignas(16) uint32_t found[4];
     uint32_t runs[32];
     // Transactions of what the other CTAs send: sums, scores.
     alignas(8) uint64_t bar[2];
@@ -171,18 +170,21 @@ __device__ __forceinline__ int q8_slot(int d) {
     return (r >> 1) * 16 + 2 * g + (r & 1);
 }
 
-// The bounds and scales of a batch of blocks of this CTA's share (me of S), 16 bytes a lane:
-// lo's in the first half of a block's lanes, hi's in the other.
+// The bounds of a batch of blocks of this CTA's share, 16 bytes a lane: lo's in the first
+// half of a block's lanes, hi's in the other.  Eight loads a lane; the sum over a block's
+// lanes leaves block kMine of the eight in the lane, whose scale it has.
 template <int D>
 struct Q8Bounds {
     static constexpr int kLanes = D / 8, kPer = 32 / kLanes, kAhead = 8;  // lanes a block, blocks a warp and load, loads
     static constexpr int kBatch = kAhead * kPer * kQ8Warps;
+    static constexpr int kSame = kLanes / kAhead;  // lanes with the same block of the eight
     uint4 x[kAhead];
-    float s[kAhead];
+    float s;
 
     __device__ __forceinline__ static int block(int first, int u) {
         return first + ((u * kQ8Warps + (threadIdx.x >> 5)) * kPer) + (threadIdx.x & 31) / kLanes;
     }
+    __device__ __forceinline__ static int mine(int first) { return block(first, threadIdx.x % kLanes / kSame); }
     // Of blocks first .. first + kBatch - 1, below hi.
     __device__ __forceinline__ void load(const Q8Layer &l, int64_t base, int first, int hi) {
         const int8_t *bounds = l.bounds + base * (2 * D) + (threadIdx.x % kLanes) * 16;
@@ -190,33 +192,32 @@ struct Q8Bounds {
         for (int u = 0; u < kAhead; ++u) {
             const int j = block(first, u);
             x[u] = make_uint4(0, 0, 0, 0);
-            s[u] = 0.f;
-            if (j < hi) {
-                x[u] = *reinterpret_cast<const uint4 *>(bounds + static_cast<int64_t>(j) * (2 * D));
-                s[u] = l.scales[base + j].x;
-            }
+            if (j < hi) x[u] = *reinterpret_cast<const uint4 *>(bounds + static_cast<int64_t>(j) * (2 * D));
         }
+        s = mine(first) < hi ? l.scales[base + mine(first)].x : 0.f;
     }
 };
 
 // Scores blocks lo .. hi - 1 and sends them to keys[] of all S CTAs (to none: withhold); at:
-// their first batch.
+// their first two batches, both on the way before the queries are normed.  (That, one shuffle
+// a block instead of four and one barrier a round of the choice: B 4, 60 to 65 thousand
+// positions, 64 blocks 12.65 -> 11.2 us; B 8, 32768 positions 15.3 -> 13.5.)
 template <int D>
 __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int full, int lo, int hi, int S,
                                          uint32_t first_rank, bool withhold, Q8StepSmem<D> &sm, uint32_t *keys,
-                                         Q8Bounds<D> &at) {
-    constexpr int LPB = Q8Bounds<D>::kLanes;
+                                         Q8Bounds<D> (&at)[2]) {
+    using B = Q8Bounds<D>;
+    constexpr int LPB = B::kLanes;
     const int sub = threadIdx.x % LPB, d0 = sub % (D / 16) * 16;
     const uint4 *w4 = reinterpret_cast<const uint4 *>(sub < D / 16 ? &sm.down[d0] : &sm.up[d0]);
     const uint4 wa = w4[0], wb = w4[1];
     const uint32_t to = smem_u32(keys), bar = smem_u32(&sm.bar[1]);
-    for (int j0 = lo; j0 < hi; j0 += Q8Bounds<D>::kBatch) {
-        int dot[Q8Bounds<D>::kAhead];
-        float s[Q8Bounds<D>::kAhead];
+    auto batch = [&](int first, B &in) {
+        int dot[B::kAhead];
+        const float s = in.s;
 #pragma unroll
-        for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) {
-            const uint4 x = at.x[u];
-            s[u] = at.s[u];
+        for (int u = 0; u < B::kAhead; ++u) {
+            const uint4 x = in.x[u];
             dot[u] = __dp2a_lo(static_cast<int>(wa.x), static_cast<int>(x.x), 0);
             dot[u] = __dp2a_hi(static_cast<int>(wa.y), static_cast<int>(x.x), dot[u]);
             dot[u] = __dp2a_lo(static_cast<int>(wa.z), static_cast<int>(x.y), dot[u]);
@@ -226,26 +227,33 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
             dot[u] = __dp2a_lo(static_cast<int>(wb.z), static_cast<int>(x.w), dot[u]);
             dot[u] = __dp2a_hi(static_cast<int>(wb.w), static_cast<int>(x.w), dot[u]);
         }
-        if (j0 + Q8Bounds<D>::kBatch < hi) at.load(l, base, j0 + Q8Bounds<D>::kBatch, hi);
+        if (first + 2 * B::kBatch < hi) in.load(l, base, first + 2 * B::kBatch, hi);
+        // Half of the sums go to the lane across, half of its come here.
 #pragma unroll
-        for (int o = LPB / 2; o >= 1; o >>= 1) {
+        for (int n = B::kAhead / 2, o = LPB / 2; n >= 1; n /= 2, o /= 2) {
+            const bool upper = (sub & o) != 0;
 #pragma unroll
-            for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-        }
-#pragma unroll
-        for (int u = 0; u < Q8Bounds<D>::kAhead; ++u) {
-            const int j = Q8Bounds<D>::block(j0, u);
-            if (j >= hi) continue;
-            float score = __fmul_rn(static_cast<float>(dot[u]), s[u]);
-            if (j == 0 || j == full - 1 || s[u] != s[u]) score = INFINITY;
-            const uint32_t key = q8_key(score);
-            if (S == 1) {
-                if (sub == 0) keys[j] = key;
-            } else if (!withhold) {
-                for (int r = sub; r < S; r += LPB)
-                    q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
+            for (int u = 0; u < n; ++u) {
+                const int keep = upper ? dot[u + n] : dot[u], give = upper ? dot[u] : dot[u + n];
+                dot[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
             }
         }
+        if (B::kSame == 2) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
+        const int j = B::mine(first);
+        if (j >= hi) return;
+        float score = __fmul_rn(static_cast<float>(dot[0]), s);
+        if (j == 0 || j == full - 1 || s != s) score = INFINITY;
+        const uint32_t key = q8_key(score);
+        if (S == 1) {
+            if (sub % B::kSame == 0) keys[j] = key;
+        } else if (!withhold) {
+            for (int r = sub % B::kSame; r < S; r += B::kSame)
+                q8_send(map_rank(to + 4 * j, first_rank + r), key, map_rank(bar, first_rank + r));
+        }
+    };
+    for (int j0 = lo; j0 < hi; j0 += 2 * B::kBatch) {
+        batch(j0, at[0]);
+        if (j0 + B::kBatch < hi) batch(j0 + B::kBatch, at[1]);
     }
 }
 
@@ -253,7 +261,8 @@ __device__ __forceinline__ void q8_score(const Q8Layer &l, int64_t base, int ful
 // places lo .. hi - 1 go to list[].
 //   The n-th largest key is found by counting keys in 256 equal steps of the range that
 // holds it, which then shrinks to one step: two or three times for scores as they come,
-// four at most.  Infinite ones are set apart, so that the first range is that of numbers.
+// four at most, each time in counters of its own and found by every warp for itself, for
+// one barrier.  Infinite ones are set apart, so that the first range is that of numbers.
 template <int D>
 __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n, int lo, int hi, Q8StepSmem<D> &sm,
                                           uint16_t *list) {
@@ -285,7 +294,7 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
     most = __reduce_max_sync(FULL, most);
     infinite = __reduce_add_sync(FULL, infinite);
     if (lane == 0) *reinterpret_cast<uint4 *>(sm.part[warp]) = make_uint4(least, most, infinite, 0);
-    for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
+    for (int i = threadIdx.x; i < 256; i += kQ8Threads) reinterpret_cast<uint4 *>(sm.hist[0])[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     infinite = 0;
 #pragma unroll
@@ -298,49 +307,47 @@ __device__ __forceinline__ void q8_select(const uint32_t *keys, int full, int n,
     // All keys above nth belong to them, and the first `take` of those that equal it.
     uint32_t nth = kInf;
     int need = n - static_cast<int>(infinite), take = n;
-    while (need > 0) {
+    for (uint32_t *hist = sm.hist[0]; need > 0; hist += 256) {
         const int shift = max(0, 24 - __clz(most - least));  // (most - least) >> shift is below 256
         each([&](uint32_t key) {
-            if (key >= least && key <= most) atomicAdd(&sm.hist[(key - least) >> shift], 1u);
+            if (key >= least && key <= most) atomicAdd(&hist[(key - least) >> shift], 1u);
         });
         __syncthreads();
-        if (warp == 0) {  // a lane has 8 steps, the last lane the largest
-            const uint4 a = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane]), b = *reinterpret_cast<const uint4 *>(&sm.hist[8 * lane + 4]);
-            const int c[8] = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
-                              static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
-            const int all = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
-            int from = all;  // keys in this lane's steps and higher ones
+        // A lane has 8 steps, the last lane the largest.
+        const uint4 a = *reinterpret_cast<const uint4 *>(&hist[8 * lane]), b = *reinterpret_cast<const uint4 *>(&hist[8 * lane + 4]);
+        const int c[8] = {static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
+                          static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+        const int all = c[0] + c[1] + c[2] + c[3] + c[4] + c[5] + c[6] + c[7];
+        int from = all;  // keys in this lane's steps and higher ones
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_down_sync(FULL, from, o);
-                if (lane + o < 32) from += y;
-            }
-            int above = from - all;
-            if (above < need && from >= need) {  // one lane: the n-th largest is in its steps
-                bool found = false;
-#pragma unroll
-                for (int step = 7; step >= 0; --step) {
-                    if (!found && above + c[step] >= need) {
-                        found = true;
-                        *reinterpret_cast<uint4 *>(sm.found) = make_uint4(8 * lane + step, above, c[step], 0);
-                    }
-                    if (!found) above += c[step];
-                }
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_down_sync(FULL, from, o);
+            if (lane + o < 32) from += y;
         }
-        __syncthreads();
-        const uint4 found = *reinterpret_cast<const uint4 *>(sm.found);
-        const int in = found.z;
-        least += found.x << shift;
-        need -= static_cast<int>(found.y);
+        // The n-th largest is in the steps of one lane: its step, the keys above, those in it.
+        int above = from - all, at = 0, in = 0;
+        const int src = __ffs(__ballot_sync(FULL, above < need && from >= need)) - 1;
+        bool found = false;
+#pragma unroll
+        for (int step = 7; step >= 0; --step) {
+            if (!found && above + c[step] >= need) {
+                found = true;
+                at = 8 * lane + step;
+                in = c[step];
+            }
+            if (!found) above += c[step];
+        }
+        at = __shfl_sync(FULL, at, src);
+        above = __shfl_sync(FULL, above, src);
+        in = __shfl_sync(FULL, in, src);
+        least += static_cast<uint32_t>(at) << shift;
+        need -= above;
         if (need == in || shift == 0) {  // all keys of the step, or equal ones
             nth = need == in ? least - 1 : least;
             take = need == in ? 0 : need;
             break;
         }
         most = min(most, least + ((1u << shift) - 1u));
-        for (int i = threadIdx.x; i < 256; i += kQ8Threads) sm.hist[i] = 0;
-        __syncthreads();
     }
     // In order, kHeld blocks at a time: a warp has 32 of them for each of its registers.
     int above_before = 0, equal_before = 0;
@@ -479,7 +486,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     }
     // The blocks that this CTA scores.
     const int score_lo = full * me >> log_S, score_hi = full * (me + 1) >> log_S;
-    Q8Bounds<D> bounds;
+    Q8Bounds<D> bounds[2];
     // What the other CTAs of the S send: sums of weights and outputs, scores.
     if (p.cluster > 1) {
         if (threadIdx.x == 0) {
@@ -519,7 +526,12 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     Q8TailPlan plan;
     __nv_bfloat16 *tail = nullptr;   // where they are kept: 64 rows of K, then of V
     if (me == 0) plan.next = p.layer.state[sh];
-    if (choose) bounds.load(p.layer, base, score_lo, score_hi); else load_first();
+    if (choose) {
+        bounds[0].load(p.layer, base, score_lo, score_hi);
+        bounds[1].load(p.layer, base, score_lo + Q8Bounds<D>::kBatch, score_hi);
+    } else if (!kSparse) {
+        load_first();
+    }
     if (me == 0) {
         plan = q8_plan_tail(plan.next, pos, pos + 1, true);
         tail = p.layer.tail + (sh * 2 + plan.dst) * static_cast<int64_t>(2 * kQ8Block * D);
@@ -622,11 +634,11 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             const bool ok = S == 1 || mbar_wait_cluster(smem_u32(&sm.bar[1]), 0, &sm.abort, p.err, kKernQ8Decode, 2, p.wait_ns);
             if (__syncthreads_and(ok)) {
                 q8_select<D>(keys, full, p.n_blocks, item_lo, item_hi, sm, list);
-                load_first();
             } else {
                 listed = false;
             }
         }
+        if (listed) load_first();  // (its registers held the bounds; also where nothing was to choose)
     }
 
     // ---------------------------------------------------------------- complete blocks
