@@ -19,10 +19,13 @@ inline int q8_step_work(int D, int full, int n_blocks) {
 //   A CTA costs its set-up and merge, and a warp its blocks one after the other, so a step
 // alone is fastest with one block a warp, and a chain of steps, which run side by side,
 // with fewer CTAs.  Up to three blocks a warp are taken where that leaves room for several
-// launches, up to four for two of them, and as few as fit the device otherwise.  us, in a chain / alone
-// from call to end on the host (32/8 heads, D = 128): B 4, 2048 keys, 8 splits 6.0 / 19.1,
-// 4 (taken) 5.1 / 18.8, 2 4.2 / 20.6; sparse, B 4, 16 of 64 blocks, 8 splits 8.1 / 21.1, 2
-// (taken) 4.6 / 22.0; B 1, 32 of 1024, 16 splits 7.8 / 23.0, 8 (taken) 5.2 / 23.7.
+// launches, four where four or more CTAs then still share a sequence, up to four for two
+// launches, and as few as fit the device otherwise.  us, in a chain / alone from call to
+// end on the host (32/8 heads, D = 128): sparse, B 4, 16 of 64 blocks, 8 splits 8.1 / 21.1,
+// 2 (taken) 4.6 / 22.0; B 1, 32 of 1024, 16 splits 7.8 / 23.0, 8 (taken) 5.2 / 23.7.
+// Four blocks a warp: B 1, 8192 keys, 16 splits 5.1 / 20.0, 8 (taken) 3.9 / 19.9; B 2, 4096,
+// 8 splits 4.7 / 19.6, 4 (taken) 3.8 / 19.4; but B 4, 2048, 4 splits (taken) 4.7 / 18.6, 2
+// 4.0 / 20.9.  Six: B 4, 2900, 4 splits (taken) 5.6 / 19.6, 2 5.0 / 22.9.
 inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, int *splits) {
     int top = 1;
     // Splits that leave a warp at most `per` blocks; their CTAs.
@@ -40,6 +43,7 @@ inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, 
     };
     for (int per = 1; per <= 3; ++per)
         if (cut(per) <= num_sms / 2 - num_sms / 16) return top;
+    if (cut(4) <= num_sms / 2 - num_sms / 16 && top >= 4) return top;
     for (int per = 1; per <= 4; ++per)
         if (cut(per) <= num_sms) return top;
     // The fewest that fit; one each where not even those do.
