@@ -78,7 +78,7 @@ def _compile(src: str, extra) -> str:
 def _build_calls() -> None:
     """_q4calls: plain C++ against this interpreter's headers, no CUDA."""
     if not can_build_calls():
-        warnings.warn("g++ or Python.h not found: the binding will lack the 4-bit cache's per-token calls")
+        warnings.warn("g++ or Python.h not found: the binding will lack the 4-bit and 8-bit caches' per-token calls")
         return
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [_cxx(), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-fwrapv",

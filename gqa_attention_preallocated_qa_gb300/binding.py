@@ -137,7 +137,7 @@ class _NoCalls:
         self.why = why
 
     def __getattr__(self, name):
-        raise ImportError(f"the 4-bit cache's per-token calls need _q4calls: {self.why}")
+        raise ImportError(f"the 4-bit and 8-bit caches' per-token calls need _q4calls: {self.why}")
 
 
 def _load_calls():

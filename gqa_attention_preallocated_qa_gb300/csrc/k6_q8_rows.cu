@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(256) q8_write_kernel(const __grid_constant__ Q
 // block's 1 + G heads through shared memory.
 //   K1 and q8_write_kernel after it take one pass more over keys and values and one launch
 // more.  A call takes, with them / with this (32/8 heads, D = 128): 1778 tokens of two
-// chunks 119 / 113 us, 64 tokens (2/1 heads, D = 64) 13.6 / 12.5, 4 x 2048 171 / 174.  At 8192
+// chunks 119 / 113 us, 64 tokens (2/1 heads, D = 64) 13.6 / 12.5, 4 x 2048 171 / 176.  At 8192
 // tokens this takes 48 us alone, 4.5 TB/s: two CTAs of 8 warps an SM, for their 128
-// registers, fill half of the issue slots; three of them with 80 take 13 us longer.
+// registers, fill half of the issue slots; with three of 80 registers that call took 187.
 template <int D>
 struct alignas(16) Q8RowsSmem {
     // Rotary rows, (cos_a, sin_a, cos_b, sin_b) of two pairs each: pairs 16 c + 4 t + e at

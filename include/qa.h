@@ -580,8 +580,8 @@ qa_status qa_q8_read(qa_q8_cache *cache, int layer, int batch, const int32_t *st
 
 /* Whole prompts (start 0) or the next chunk of them, with the arguments of
  * qa_q4_prefill: RoPE(RMSNorm(k)) and v are written to their positions, and every new
- * token attends causally to the earlier positions and to its own call's rows.  Values
- * of complete blocks enter the attention as qa_q8_read gives them.
+ * token attends causally to the earlier positions and to its own call's rows.  Rows
+ * of earlier complete blocks enter the attention as n * s, not rounded to bf16.
  * All sequences go through the cache's workspace, up to 8 at a time: calls on several
  * streams wait for each other, and they cannot be captured into a graph (QA_ERR_STATE).
  * A key or value that is not finite and that some new token of the call sees can reach
@@ -628,8 +628,7 @@ qa_status qa_q8_decode_step_device_positions(qa_q8_cache *cache, int layer, int 
  * all below 2^-64, have c = 0.
  * n_blocks: 1 .. ceil(capacity / 64).  blocks: int32 [batch][Hkv][n_blocks] in DEVICE memory, 4-byte
  * aligned; receives the chosen blocks in rising order, then -1 where there were fewer.
- * Its contents are the step's own list until the step has finished.
- * Everything else as qa_q8_decode_step; two launches per 64 sequences. */
+ * Everything else as qa_q8_decode_step. */
 qa_status qa_q8_sparse_step(qa_q8_cache *cache, int layer, int batch, const int32_t *positions,
                             int n_blocks, const void *q, const void *k, const void *v,
                             const void *q_norm_w, const void *k_norm_w, void *out, int32_t *blocks,
