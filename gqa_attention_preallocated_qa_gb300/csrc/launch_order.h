@@ -59,7 +59,6 @@ struct StreamRef {
         }
     };
 
-  private:
     static uint64_t this_thread() {  // ids are not used again, unlike the system's
         static std::atomic<uint64_t> threads{0};
         thread_local const uint64_t id = ++threads;
@@ -142,13 +141,22 @@ class LaunchOrder {
         if (find(stream)) streams_[stream.capture != 0].erase(stream);
     }
 
-    // The device was synchronised (kAllDevices: all of them).
+    // The calling thread has synchronised the device (kAllDevices: all of them): what it
+    // had launched there has finished.  Another thread may have launched since, or be about
+    // to launch what it has recorded, so its records stay; without the finished ones a walk
+    // goes further back, never less far.
     static constexpr int kAllDevices = -1;
     void clear(int device = kAllDevices) {
+        const uint64_t me = StreamRef::this_thread();
         std::lock_guard<std::mutex> lock(mu_);
         auto &run = streams_[0];  // (a synchronisation cannot be part of a capture)
-        for (auto it = run.begin(); it != run.end();)
-            it = device == kAllDevices || it->first.device == device ? run.erase(it) : std::next(it);
+        for (auto it = run.begin(); it != run.end();) {
+            Hist &h = it->second;
+            if ((device == kAllDevices || it->first.device == device) && h.shared)
+                h.recs.erase(std::remove_if(h.recs.begin(), h.recs.end(), [&](const Rec &r) { return r.thread == me; }), h.recs.end());
+            const bool mine = !h.shared && !h.recs.empty() && h.recs.front().thread == me;
+            it = mine && (device == kAllDevices || it->first.device == device) ? run.erase(it) : std::next(it);
+        }
     }
 
     // Launches kept per stream; the walk needs at most resident_max of them.
@@ -160,12 +168,15 @@ class LaunchOrder {
         int layer, ctas, tmax;
         bool early;
         bool passed;  // captured, in the record of what the stream runs
+        uint64_t thread = StreamRef::this_thread();  // that launches it
     };
     struct Hist {
         std::deque<Rec> recs;
         bool truncated = false;
+        bool shared = false;  // several threads' launches
         uint64_t capture = 0;
         void add(const Rec &r) {
+            shared = shared || (!recs.empty() && recs.back().thread != r.thread);
             recs.push_back(r);
             if (recs.size() > kCap) {
                 recs.pop_front();
