@@ -320,6 +320,16 @@ def test_sparse_over_the_longest_cache(qa, n_blocks):
         check_sparse(qa, c, [cap - 1], n_blocks, 5)
 
 
+@pytest.mark.parametrize("d,n_blocks", [(128, 16382), (64, 16384)])
+def test_sparse_with_the_largest_lists(qa, d, n_blocks):
+    """16383 complete blocks: all but one of them, and all."""
+    cap = 1 << 20
+    k = rows(1, cap - 1, 1, d)
+    with Cache(qa, 1, 8, 1, d, cap) as c:
+        c.append([0], [cap - 1], k, k)
+        check_sparse(qa, c, [cap - 1], n_blocks, 5)
+
+
 # ------------------------------------------------------------------ prefill
 def check_prefill(qa, c, start, ntok, seed):
     t = sum(ntok)

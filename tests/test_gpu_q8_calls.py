@@ -239,6 +239,39 @@ def test_on_another_stream(qa):
             close(out[b:b + 1], *c.want(b, pos, toks[0][b:b + 1].double()))
 
 
+def test_two_threads_on_caches_of_their_own(qa):
+    """Each on its own stream: steps of both kinds, rows and a prompt, at once."""
+    import threading
+
+    def work(seed, stream, got):
+        lens = [300, 129]
+        with torch.cuda.stream(stream), Cache(qa, 2, 8, 2, 128, 700) as c:
+            q, k, v = c.tokens(sum(lens), seed)
+            out = torch.empty_like(q)
+            qa.qa_q8_prefill(c.h, 0, [0, 0], lens, q, k, v, c.wq, c.wk, out, stream)
+            got.append(out)
+            for i in range(20):
+                o, lists = step(qa, c, [n + i for n in lens], c.tokens(2, seed + i), blocks=2 if i % 2 else 0, stream=stream)
+                got += [o] + ([lists] if i % 2 else [])
+            kv = torch.empty(2 * 20, 2, 128, device="cuda", dtype=torch.bfloat16)
+            qa.qa_q8_read(c.h, 0, lens, [20, 20], kv, None, stream)
+            got.append(kv)
+            stream.synchronize()
+
+    alone = [[], []]
+    for i in range(2):
+        work(100 * i, torch.cuda.Stream(), alone[i])
+    for _ in range(3):
+        both = [[], []]
+        threads = [threading.Thread(target=work, args=(100 * i, torch.cuda.Stream(), both[i])) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(120)
+        for a, b in zip(alone, both):
+            assert len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_prefill_on_two_streams_shares_the_workspace(qa):
     streams = [torch.cuda.Stream() for _ in range(2)]
     with Cache(qa, 1, 8, 2, 128, 600, layers=2) as c, Cache(qa, 1, 8, 2, 128, 600) as one:
