@@ -18,6 +18,13 @@
 // X must load only after its own wait the cache rows that those launches
 // append to X's layer: at most the sum of their new tokens per sequence, just
 // below X's first new slot (positions only grow between barriers).
+//
+// That is the order of a stream that runs.  In a capture the graph's edges take its
+// place, and X may follow a launch of another stream, whose event its own has waited
+// for: such an edge is programmatic too, so X may start beside that launch and what
+// that one ran beside.  Where X follows a node of this library that is not its stream's
+// last one, nothing is known to have finished: the stream's record begins anew, as
+// one whose older launches are not known.
 #pragma once
 
 #include <algorithm>
@@ -28,6 +35,8 @@
 #include <iterator>
 #include <mutex>
 #include <unordered_map>
+#include <unordered_set>
+#include <vector>
 
 namespace qa {
 
@@ -39,11 +48,13 @@ namespace qa {
 // start after everything before its replay).  They do not end what the stream
 // still runs: a walk of its own launches passes over them, counting the rows
 // that they append as if they had run.
+// `after`: in a capture, the graph's nodes that the next launch follows.
 struct StreamRef {
     uintptr_t handle;
     uint64_t thread = 0;  // of the per-thread stream
     uint64_t capture;
     int device;
+    std::vector<uintptr_t> after;
 
     StreamRef(const void *stream, int device_ = 0, uint64_t capture_ = 0)
         : handle(reinterpret_cast<uintptr_t>(stream)), capture(capture_), device(device_) {
@@ -80,7 +91,12 @@ class LaunchOrder {
     int admit(const StreamRef &stream, const void *cache, int layer, int ctas, int tmax, bool early,
               int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
+        const bool stray = strays(stream);
         Hist &h = hist(stream);
+        if (stray) {
+            h.recs.clear();
+            h.truncated = true;
+        }
         int64_t guard = 0, resident = 0;
         bool bounded = false;
         for (auto it = h.recs.rbegin(); it != h.recs.rend(); ++it) {
@@ -108,6 +124,7 @@ class LaunchOrder {
     // before its own wait.
     bool layer_settled(const StreamRef &stream, const void *cache, int layer, int64_t resident_max) {
         std::lock_guard<std::mutex> lock(mu_);
+        if (strays(stream)) return false;
         const Hist *found = find(stream);
         if (!found) return true;
         const Hist &h = *found;
@@ -129,7 +146,7 @@ class LaunchOrder {
         {
             std::lock_guard<std::mutex> lock(mu_);
             const Hist *found = find(stream);
-            if (!found || found->recs.empty()) return 0;
+            if (!strays(stream) && (!found || found->recs.empty())) return 0;
         }
         return layer_settled(stream, cache, layer, resident_max) ? 1 : 2;
     }
@@ -138,7 +155,23 @@ class LaunchOrder {
     // stream was synchronised.
     void barrier(const StreamRef &stream) {
         std::lock_guard<std::mutex> lock(mu_);
-        if (find(stream)) streams_[stream.capture != 0].erase(stream);
+        if (!find(stream)) return;
+        if (stream.capture == 0) {
+            streams_[0].erase(stream);
+            return;
+        }
+        Hist &h = hist(stream);  // (another stream may yet follow its nodes)
+        h.recs.clear();
+        h.truncated = false;
+    }
+
+    // An admitted launch has become the node that `stream` now follows.
+    void captured(const StreamRef &stream) {
+        std::lock_guard<std::mutex> lock(mu_);
+        if (stream.capture == 0 || stream.after.size() != 1) return;
+        Hist &h = hist(stream);
+        h.last = stream.after[0];
+        h.nodes.insert(h.last);
     }
 
     // The calling thread has synchronised the device (kAllDevices: all of them): what it
@@ -175,6 +208,8 @@ class LaunchOrder {
         bool truncated = false;
         bool shared = false;  // several threads' launches
         uint64_t capture = 0;
+        uintptr_t last = 0;                   // in a capture: the node of its last admitted launch
+        std::unordered_set<uintptr_t> nodes;  // and of all of them
         void add(const Rec &r) {
             shared = shared || (!recs.empty() && recs.back().thread != r.thread);
             recs.push_back(r);
@@ -188,6 +223,17 @@ class LaunchOrder {
         const auto &map = streams_[stream.capture != 0];
         const auto found = map.find(stream);
         return found == map.end() || found->second.capture != stream.capture ? nullptr : &found->second;
+    }
+    // Whether the next launch follows an admitted one other than its stream's last.
+    bool strays(const StreamRef &stream) const {
+        if (stream.capture == 0) return false;
+        const Hist *own = find(stream);
+        for (const uintptr_t node : stream.after) {
+            if (own && own->last == node) continue;
+            for (const auto &h : streams_[1])
+                if (h.second.capture == stream.capture && h.second.nodes.count(node)) return true;
+        }
+        return false;
     }
     Hist &hist(const StreamRef &stream) {
         Hist &h = streams_[stream.capture != 0][stream];

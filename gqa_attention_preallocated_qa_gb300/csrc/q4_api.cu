@@ -188,7 +188,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     // only after its own wait.
     int32_t *next = next_of(c, layer);
     const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
-    const qa::StreamRef at = qa::stream_ref(s, c->device);
+    qa::StreamRef at = qa::stream_ref(s, c->device);
     const bool settled = qa::launch_order().layer_settled(at, c, layer, resident);
     bool follows = !a.pos_dev;
     for (int b = 0; b < batch && follows; ++b)
@@ -244,6 +244,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
             cudaGetLastError();
             return QA_ERR_CUDA;
         }
+        qa::note_launch(at, s);
         c->launches[QA_Q4_KERNEL_DECODE]++;
         for (int i = b0; i < b; ++i)
             if (tokens(i) > 0) next[i] = a.pos_dev ? -1 : a.start[i] + first + tokens(i);

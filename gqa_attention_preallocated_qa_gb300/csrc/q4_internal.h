@@ -114,6 +114,7 @@ bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);
 LaunchOrder &launch_order();
 // `stream` of `device` as the launch record takes it now: captured or not.
 StreamRef stream_ref(cudaStream_t stream, int device);
+void note_launch(StreamRef &at, cudaStream_t stream);
 // Rotary table [capacity][D/2] of (cos, sin), in fp64, stored as fp32.
 void fill_rope_table(float2 *tab, int capacity, int D, float theta);
 

@@ -159,7 +159,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
     p.cap = g.capacity;
     p.eps = g.rms_eps;
     p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(g.head_dim)));
-    const qa::StreamRef at = qa::stream_ref(s, c->device);
+    qa::StreamRef at = qa::stream_ref(s, c->device);
     const int64_t resident = std::max<int64_t>(qa::k3_max_resident_ctas(), 2 * c->num_sms);
     for (int b0 = 0; b0 < batch; b0 += qa::kQ8MaxSeqPerLaunch) {
         const int n = std::min(qa::kQ8MaxSeqPerLaunch, batch - b0);
@@ -186,6 +186,7 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
             return QA_ERR_CUDA;
         }
         qa::launch_order().admit(at, c, layer, p.ctas, 1, p.early != 0, resident);
+        qa::note_launch(at, s);
         c->launches[a.blocks ? QA_Q8_KERNEL_SPARSE : QA_Q8_KERNEL_DECODE]++;
     }
     return QA_OK;
@@ -369,6 +370,7 @@ QA_API qa_status qa_q8_append(qa_q8_cache *c, int layer, int batch, const int32_
     p.rows[0] = static_cast<__nv_bfloat16 *>(const_cast<void *>(k));
     p.rows[1] = static_cast<__nv_bfloat16 *>(const_cast<void *>(v));
     return no_throw([&] {
+        qa::StreamRef at = qa::stream_ref(s, c->device);
         int64_t row0 = 0;
         for (int s0 = 0; s0 < batch; s0 += qa::kQ8MaxSeqPerLaunch) {
             const int n = std::min(qa::kQ8MaxSeqPerLaunch, batch - s0);
@@ -378,7 +380,8 @@ QA_API qa_status qa_q8_append(qa_q8_cache *c, int layer, int batch, const int32_
                     return QA_ERR_CUDA;
                 }
                 // It lets the next launch start once it has itself waited, while it writes.
-                qa::launch_order().admit(qa::stream_ref(s, c->device), c, layer, 1, 1, false, 1);
+                qa::launch_order().admit(at, c, layer, 1, 1, false, 1);
+                qa::note_launch(at, s);
                 c->launches[QA_Q8_KERNEL_WRITE]++;
             }
             for (int i = 0; i < n; ++i) row0 += ntok[s0 + i];

@@ -104,5 +104,6 @@ cudaError_t launch_q8_decode(const Q8StepParams &p, int D, cudaStream_t stream);
 bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);
 LaunchOrder &launch_order();
 StreamRef stream_ref(cudaStream_t stream, int device);
+void note_launch(StreamRef &at, cudaStream_t stream);
 
 }  // namespace qa

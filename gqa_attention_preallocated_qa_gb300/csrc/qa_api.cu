@@ -161,11 +161,22 @@ qa::StreamRef qa::stream_ref(cudaStream_t stream, int device) {
     if (r.handle == 0) return r;  // the legacy stream is never captured
     cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
-    if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess)
+    const cudaGraphNode_t *after = nullptr;
+    const cudaGraphEdgeData *edges = nullptr;  // (asked for: without it programmatic edges are an error)
+    size_t n = 0;
+    if (cudaStreamGetCaptureInfo(stream, &status, &id, nullptr, &after, &edges, &n) != cudaSuccess) {
         cudaGetLastError();
-    else if (status == cudaStreamCaptureStatusActive)
+    } else if (status == cudaStreamCaptureStatusActive) {
         r.capture = id;
+        for (size_t i = 0; i < n; ++i) r.after.push_back(reinterpret_cast<uintptr_t>(after[i]));
+    }
     return r;
+}
+
+void qa::note_launch(StreamRef &at, cudaStream_t stream) {
+    if (at.capture == 0) return;
+    at = stream_ref(stream, at.device);
+    g_order.captured(at);
 }
 
 bool qa::supported_geometry(int n_q_heads, int n_kv_heads, int head_dim) {
@@ -383,7 +394,7 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
     qa::K3Multi m{};
     int nz = 0, row = 0, pos_max = 0;
     const int resident_max = qa::k3_max_resident_ctas();
-    const qa::StreamRef at = qa::stream_ref(s, c->device);
+    qa::StreamRef at = qa::stream_ref(s, c->device);
     const int ov = plan_overlap(c, at, layer, resident_max);
     auto flush = [&]() {
         if (nz == 0) return;
@@ -422,6 +433,7 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
                 for (int z = 0; z < e->first.B; ++z) host[e->second.seq[z]] += e->second.ntok[z];
             return QA_ERR_CUDA;
         }
+        qa::note_launch(at, s);
         c->launches[QA_KERNEL_DECODE_ATTN]++;
     }
     return QA_OK;
@@ -728,7 +740,7 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
             if (mirror[b] + 1 > g.capacity) return QA_ERR_CAPACITY;
     K3Params p = make_k3(c, layer, q, k, v, q_norm_w, k_norm_w, out);
     const int64_t resident_max = qa::k3_max_resident_ctas();
-    const qa::StreamRef at = qa::stream_ref(static_cast<cudaStream_t>(stream), c->device);
+    qa::StreamRef at = qa::stream_ref(static_cast<cudaStream_t>(stream), c->device);
     // Device positions: when no launch that may still be running writes this
     // layer (a multi-layer loop, e.g. a captured layer stack), the kernel reads
     // them at once and overlaps its predecessor like a host-position step;
@@ -768,6 +780,7 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
                 for (int b = 0; b < b0; ++b) mirror[b] += 1;
             return QA_ERR_CUDA;
         }
+        qa::note_launch(at, static_cast<cudaStream_t>(stream));
         c->launches[QA_KERNEL_DECODE_ATTN]++;
     }
     if (!dev_pos)
