@@ -113,8 +113,8 @@ class LaunchOrder {
             }
         }
         if (!bounded && h.truncated) guard = kGuardAll;  // the older launches are not known
-        h.add({cache, layer, std::max(ctas, 1), tmax, early, false});
-        if (stream.capture != 0) streams_[0][stream].add({cache, layer, 0, tmax, true, true});
+        h.add({cache, layer, std::max(ctas, 1), tmax, early, false, next_++});
+        if (stream.capture != 0) streams_[0][stream].add({cache, layer, 0, tmax, true, true, next_++});
         return static_cast<int>(std::min<int64_t>(guard, kGuardAll));
     }
 
@@ -174,21 +174,52 @@ class LaunchOrder {
         h.nodes.insert(h.last);
     }
 
+    // A call that admits launches before it makes them: its records, until it is over, are
+    // of launches that a synchronisation may not have seen.
+    class Call {
+      public:
+        explicit Call(LaunchOrder &order) : order_(order) {
+            std::lock_guard<std::mutex> lock(order_.mu_);
+            first_ = order_.next_++;
+            order_.calls_.push_back(first_);
+        }
+        ~Call() {
+            std::lock_guard<std::mutex> lock(order_.mu_);
+            order_.calls_.erase(std::find(order_.calls_.begin(), order_.calls_.end(), first_));
+        }
+        Call(const Call &) = delete;
+
+      private:
+        LaunchOrder &order_;
+        uint64_t first_;
+    };
+
+    // Every launch recorded before the one of this number has been enqueued.
+    uint64_t mark() {
+        std::lock_guard<std::mutex> lock(mu_);
+        return calls_.empty() ? next_ : *std::min_element(calls_.begin(), calls_.end());
+    }
+
     // The calling thread has synchronised the device (kAllDevices: all of them): what it
-    // had launched there has finished.  Another thread may have launched since, or be about
-    // to launch what it has recorded, so its records stay; without the finished ones a walk
-    // goes further back, never less far.
+    // had launched there has finished, and what any thread had enqueued at a mark() before.
+    // Other records of other threads stay: they may have launched since, or be about to
+    // launch.  Without the finished ones a walk goes further back, never less far.
     static constexpr int kAllDevices = -1;
-    void clear(int device = kAllDevices) {
+    void clear(int device = kAllDevices, uint64_t mark = 0) {
         const uint64_t me = StreamRef::this_thread();
         std::lock_guard<std::mutex> lock(mu_);
         auto &run = streams_[0];  // (a synchronisation cannot be part of a capture)
         for (auto it = run.begin(); it != run.end();) {
             Hist &h = it->second;
-            if ((device == kAllDevices || it->first.device == device) && h.shared)
-                h.recs.erase(std::remove_if(h.recs.begin(), h.recs.end(), [&](const Rec &r) { return r.thread == me; }), h.recs.end());
+            if (device != kAllDevices && it->first.device != device) {
+                ++it;
+                continue;
+            }
             const bool mine = !h.shared && !h.recs.empty() && h.recs.front().thread == me;
-            it = mine && (device == kAllDevices || it->first.device == device) ? run.erase(it) : std::next(it);
+            h.recs.erase(std::remove_if(h.recs.begin(), h.recs.end(), [&](const Rec &r) { return r.thread == me || r.number < mark; }),
+                         h.recs.end());
+            if (mine || h.lost < mark) h.truncated = false;
+            it = h.recs.empty() && !h.truncated ? run.erase(it) : std::next(it);
         }
     }
 
@@ -201,11 +232,13 @@ class LaunchOrder {
         int layer, ctas, tmax;
         bool early;
         bool passed;  // captured, in the record of what the stream runs
+        uint64_t number;
         uint64_t thread = StreamRef::this_thread();  // that launches it
     };
     struct Hist {
         std::deque<Rec> recs;
         bool truncated = false;
+        uint64_t lost = 0;    // the last record that went
         bool shared = false;  // several threads' launches
         uint64_t capture = 0;
         uintptr_t last = 0;                   // in a capture: the node of its last admitted launch
@@ -214,6 +247,7 @@ class LaunchOrder {
             shared = shared || (!recs.empty() && recs.back().thread != r.thread);
             recs.push_back(r);
             if (recs.size() > kCap) {
+                lost = recs.front().number;
                 recs.pop_front();
                 truncated = true;
             }
@@ -242,6 +276,8 @@ class LaunchOrder {
         return h;
     }
     std::mutex mu_;
+    uint64_t next_ = 1;            // the number of the next record
+    std::vector<uint64_t> calls_;  // under way: numbers below all of their records'
     // What each stream runs, and what goes into its capture.
     std::unordered_map<StreamRef, Hist, StreamRef::Hash> streams_[2];
 };

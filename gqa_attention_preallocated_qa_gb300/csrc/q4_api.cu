@@ -194,6 +194,7 @@ qa_status run_decode(qa_q4_cache *c, int layer, int batch, const DecodeCall &a, 
     for (int b = 0; b < batch && follows; ++b)
         if (tokens(b) > 0 && next[b] != a.start[b] + first) follows = false;
 
+    const qa::LaunchOrder::Call call(qa::launch_order());
     int b = 0, row0 = 0;
     while (b < batch) {
         int nz = 0, tm = 0;
@@ -386,8 +387,7 @@ QA_API qa_status qa_q4_cache_alloc(const qa_config *cfg, qa_q4_cache **out) {
 QA_API qa_status qa_q4_cache_free(qa_q4_cache *c) {
     if (!c) return QA_OK;
     DeviceScope dev(c->device);
-    cudaDeviceSynchronize();
-    qa::launch_order().clear(c->device);
+    qa::synchronise_device();
     free_all(c);
     delete c;
     return QA_OK;
@@ -653,11 +653,10 @@ QA_API qa_status qa_q4_get_device_error(qa_q4_cache *c, uint32_t *detail) {
     if (!c) return QA_ERR_INVALID_ARG;
     DeviceScope dev(c->device);
     uint32_t word = 0;
-    if (!dev.ok() || cudaDeviceSynchronize() != cudaSuccess ||
+    if (!dev.ok() || qa::synchronise_device() != cudaSuccess ||
         cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
         return QA_ERR_CUDA;
-    qa::launch_order().clear(c->device);
     if (detail) *detail = word;
     switch (word & 0xffu) {
         case 0: return QA_OK;

@@ -115,6 +115,7 @@ LaunchOrder &launch_order();
 // `stream` of `device` as the launch record takes it now: captured or not.
 StreamRef stream_ref(cudaStream_t stream, int device);
 void note_launch(StreamRef &at, cudaStream_t stream);
+cudaError_t synchronise_device();
 // Rotary table [capacity][D/2] of (cos, sin), in fp64, stored as fp32.
 void fill_rope_table(float2 *tab, int capacity, int D, float theta);
 

@@ -345,8 +345,7 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
 QA_API qa_status qa_q8_cache_free(qa_q8_cache *c) {
     if (!c) return QA_OK;
     DeviceScope dev(c->device);
-    cudaDeviceSynchronize();
-    qa::launch_order().clear(c->device);
+    qa::synchronise_device();
     free_all(c);
     delete c;
     return QA_OK;
@@ -537,11 +536,10 @@ QA_API qa_status qa_q8_get_device_error(qa_q8_cache *c, uint32_t *detail) {
     if (!c) return QA_ERR_INVALID_ARG;
     DeviceScope dev(c->device);
     uint32_t word = 0;
-    if (!dev.ok() || cudaDeviceSynchronize() != cudaSuccess ||
+    if (!dev.ok() || qa::synchronise_device() != cudaSuccess ||
         cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
         return QA_ERR_CUDA;
-    qa::launch_order().clear(c->device);
     if (detail) *detail = word;
     switch (word & 0xffu) {
         case 0: return QA_OK;

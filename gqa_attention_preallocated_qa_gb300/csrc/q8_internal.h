@@ -105,5 +105,6 @@ bool supported_geometry(int n_q_heads, int n_kv_heads, int head_dim);
 LaunchOrder &launch_order();
 StreamRef stream_ref(cudaStream_t stream, int device);
 void note_launch(StreamRef &at, cudaStream_t stream);
+cudaError_t synchronise_device();
 
 }  // namespace qa

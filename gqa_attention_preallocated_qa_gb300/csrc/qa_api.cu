@@ -54,12 +54,6 @@ namespace {
 // recent launches per stream of a device, shared by every cache of the process.
 qa::LaunchOrder g_order;
 
-// After a synchronisation of the current device.
-void order_synchronised() {
-    int device = 0;
-    if (cudaGetDevice(&device) == cudaSuccess) g_order.clear(device);
-}
-
 // Failure-detection test hook (qa_debug_arm_wait_timeout): the kernel index
 // whose next launch withholds a copy (-1: none) and that launch's wait limit.
 std::atomic<int> g_fault_kernel{-1};
@@ -171,6 +165,15 @@ qa::StreamRef qa::stream_ref(cudaStream_t stream, int device) {
         for (size_t i = 0; i < n; ++i) r.after.push_back(reinterpret_cast<uintptr_t>(after[i]));
     }
     return r;
+}
+
+cudaError_t qa::synchronise_device() {
+    const uint64_t mark = g_order.mark();
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) g_order.clear(device, mark);
+    return e;
 }
 
 void qa::note_launch(StreamRef &at, cudaStream_t stream) {
@@ -417,6 +420,7 @@ qa_status run_multi(qa_cache *c, int layer, int batch, const int32_t *lens, int 
         row += lens[b];
     }
     flush();
+    const qa::LaunchOrder::Call call(g_order);
     for (auto &l : launches) {
         int tm = 0;
         for (int z = 0; z < l.first.B; ++z) tm = std::max(tm, l.second.ntok[z]);
@@ -606,8 +610,7 @@ QA_API qa_status qa_cache_alloc(const qa_config *cfg, qa_cache **out) {
 
 QA_API qa_status qa_cache_free(qa_cache *c) {
     if (!c) return QA_OK;
-    cudaDeviceSynchronize();
-    order_synchronised();
+    qa::synchronise_device();
     free_all(c);
     delete c;
     return QA_OK;
@@ -749,6 +752,7 @@ qa_status decode_step(qa_cache *c, int layer, int batch, const void *q, const vo
     const bool settled =
         dev_pos && g_order.layer_settled(at, c, layer, resident_max);
     p.dev_pos = dev_pos ? (settled ? 2 : 1) : 0;
+    const qa::LaunchOrder::Call call(g_order);
     for (int b0 = 0; b0 < batch; b0 += qa::kK3MaxSeqPerLaunch) {
         const int nb = std::min(qa::kK3MaxSeqPerLaunch, batch - b0);
         int pos_max = 0;
@@ -870,11 +874,10 @@ QA_API qa_status qa_cache_lengths(qa_cache *c, int layer, int32_t *lens_host) {
 QA_API qa_status qa_get_device_error(qa_cache *c, uint32_t *detail) {
     if (!c) return QA_ERR_INVALID_ARG;
     uint32_t word = 0;
-    if (cudaDeviceSynchronize() != cudaSuccess ||
+    if (qa::synchronise_device() != cudaSuccess ||
         cudaMemcpy(&word, c->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
         cudaMemset(c->err, 0, sizeof(word)) != cudaSuccess)
         return QA_ERR_CUDA;
-    order_synchronised();
     if (detail) *detail = word;
     switch (word & 0xffu) {
         case 0: return QA_OK;
