@@ -73,6 +73,7 @@ SIGNATURES = {
                                               _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "qa_noalloc_get_device_error": (ctypes.c_int, [_u32p, _vp]),
     "qa_prefill_attend": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i32p, _vp, _vp, _vp]),
+    "qa_set_early_reads": (ctypes.c_int, [ctypes.c_int]),
     "qa_debug_arm_wait_timeout": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint32]),
     "qa_q4_cache_alloc": (ctypes.c_int, [ctypes.POINTER(qa_config), ctypes.POINTER(_vp)]),
     "qa_q4_cache_free": (ctypes.c_int, [_vp]),
@@ -268,6 +269,11 @@ def qa_prefill_attend(cache, layer, prompt_lens, qprime, out, stream=None) -> No
     _check(lib.qa_prefill_attend(cache, layer, len(prompt_lens), _i32(prompt_lens), _ptr(qprime),
                                  _ptr(out), _stream(stream)),
            "qa_prefill_attend")
+
+
+def qa_set_early_reads(on: bool) -> None:
+    """False: steps start when everything before them on the stream has finished."""
+    _check(lib.qa_set_early_reads(int(on)), "qa_set_early_reads")
 
 
 def qa_debug_arm_wait_timeout(kernel: int, wait_us: int) -> None:

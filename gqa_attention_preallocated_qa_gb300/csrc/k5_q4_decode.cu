@@ -889,7 +889,7 @@ static void q4_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&attr)[2], i
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].val.programmaticStreamSerializationAllowed = early_reads();
     cfg.attrs = attr;
     cfg.numAttrs = 2;
 }

@@ -59,6 +59,8 @@ qa::LaunchOrder g_order;
 std::atomic<int> g_fault_kernel{-1};
 std::atomic<uint64_t> g_fault_wait_ns{qa::kWaitTimeoutNs};
 
+std::atomic<bool> g_early_reads{true};
+
 __global__ void qa_reset_kernel(int32_t *lens, int n_lens, uint32_t *seq_cnt, int n_seq) {
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_lens; i += gridDim.x * blockDim.x)
         lens[i] = 0;
@@ -175,6 +177,8 @@ cudaError_t qa::synchronise_device() {
     if (e == cudaSuccess) g_order.clear(device, mark);
     return e;
 }
+
+bool qa::early_reads() { return g_early_reads.load(std::memory_order_relaxed); }
 
 void qa::note_launch(StreamRef &at, cudaStream_t stream) {
     if (at.capture == 0) return;
@@ -809,6 +813,12 @@ QA_API qa_status qa_cache_set_decode_overlap(qa_cache *c, int launches) {
     if (!c || launches < 1 || launches > 8) return QA_ERR_INVALID_ARG;
     c->overlap = launches;
     c->overlap_fixed = true;
+    return QA_OK;
+}
+
+QA_API qa_status qa_set_early_reads(int on) {
+    if (on != 0 && on != 1) return QA_ERR_INVALID_ARG;
+    g_early_reads.store(on != 0, std::memory_order_relaxed);
     return QA_OK;
 }
 

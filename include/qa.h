@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define QA_ABI_VERSION 6
+#define QA_ABI_VERSION 7
 
 typedef enum {
     QA_OK = 0,
@@ -152,7 +152,11 @@ qa_status qa_prefill(qa_cache *cache, int layer, int batch, const int32_t *promp
  * cache rows they append to its layer only after its wait.  Kernels of other
  * code enqueued between these calls on the same stream must not let their
  * successors start before they themselves have waited for their predecessor
- * (the usual use of programmatic dependent launch).
+ * (the usual use of programmatic dependent launch), and one that writes this
+ * step's q, k, v or weights not before it has stored them: a kernel that signals
+ * between its wait and its stores releases a step that reads what was there
+ * before.  A kernel that never signals fulfils both.  For callers whose kernels
+ * do not, see qa_set_early_reads.
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (a sequence already holds
  * `capacity` tokens; nothing is evicted or wrapped), CUDA (a launch failed;
  * with more than 64 sequences the launches before it were enqueued and their
@@ -222,6 +226,15 @@ qa_status qa_cache_set_window(qa_cache *cache, int layer, int window);
  * Host-side only, takes effect for launches after the call.
  * Errors: INVALID_ARG (launches outside 1..8). */
 qa_status qa_cache_set_decode_overlap(qa_cache *cache, int launches);
+
+/* Whether the launches that overlap earlier kernels of their stream do so: decode
+ * and sparse steps and short chunks on caches of any kind, process-wide.  on = 1 is
+ * the default.  With 0 such a launch starts when everything before it on its stream
+ * has finished, so it reads what that wrote, whenever it signalled; results are the
+ * same, and a chain of steps loses their overlap.  Host-side only, takes effect for
+ * launches after the call; a captured launch keeps what held at its capture.
+ * Errors: INVALID_ARG (not 0 or 1). */
+qa_status qa_set_early_reads(int on);
 
 /* Copy one layer's device lengths into the host copy (synchronises `stream`),
  * after decode steps that advanced them on the device. */
@@ -384,11 +397,11 @@ qa_status qa_noalloc_get_device_error(uint32_t *detail, void *stream);
  * stream belongs to the cache's device.  qa_q4_append and qa_q4_read are
  * ordered on their stream like plain launches.  Decode steps, and in a prefill
  * the sequences of few tokens (qa_q4_prefill says which), overlap earlier
- * kernels of the stream like qa_decode_step, with the same condition on other
+ * kernels of the stream like qa_decode_step, with the same conditions on other
  * code's kernels between the calls.  They read q, k, v and the weights before
  * an earlier decode step or prefill has finished: what such a call writes (out,
  * k_held, v_held) is no input of a later one unless another kernel or copy on
- * the stream lies between them. */
+ * the stream that fulfils those conditions lies between them. */
 typedef struct qa_q4_cache qa_q4_cache; /* opaque */
 
 /* Kernels counted by qa_q4_stats. */
@@ -534,11 +547,12 @@ qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t 
  * All calls but qa_q8_prefill may be captured into graphs.  qa_q8_append, qa_q8_read and
  * qa_q8_prefill are ordered on their stream like plain launches.  Decode and sparse
  * steps overlap earlier kernels of the stream like qa_decode_step, with the same
- * condition on other code's kernels between the calls: they read q, k, v and the weights
- * before an earlier call of this library has finished, so what that writes (out, k_held,
+ * conditions on other code's kernels between the calls: they read q, k, v and the weights
+ * before the kernel in front of them has finished.  So a kernel that writes these does not
+ * signal before it has stored them, and what a call of this library writes (out, k_held,
  * v_held, k_out, v_out) is no input of a later step unless another kernel or copy on the
- * stream lies between them.  (With device positions, and behind a call that writes the
- * same layer, a step waits first.) */
+ * stream that fulfils those conditions lies between them.  (With device positions, and
+ * behind a call that writes the same layer, a step waits first.) */
 typedef struct qa_q8_cache qa_q8_cache; /* opaque */
 
 /* Kernels counted by qa_q8_stats. */
