@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     }
     const int b = p.seq[z].slot, log_S = p.seq[z].log_S, S = 1 << log_S;
     const int unit = static_cast<int>(blockIdx.x) - p.seq[z].cta0, me = unit & (S - 1), h = unit >> log_S;
+    __syncwarp();  // (thread 0 may have been setting the error: the cluster's barriers want whole warps)
     if (pos < 0) {  // nothing to do here
         if (p.cluster > 1) cluster_arrive();
         griddep_wait();
