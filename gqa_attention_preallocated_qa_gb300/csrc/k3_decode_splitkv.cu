@@ -373,6 +373,7 @@ __device__ __forceinline__ void k3_body(const K3Params &p, const float2 *cs_arr,
             ++issued_early;
         }
     }
+    __syncwarp();  // (lane 0's set-up: the barrier wants whole warps)
     cluster_arrive();  // peers may push into this CTA once they have waited on this
 
     // ---------------------------------------------------------------- prologue
