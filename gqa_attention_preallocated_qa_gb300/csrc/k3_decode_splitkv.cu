@@ -50,6 +50,8 @@
 
 namespace qa {
 
+bool early_reads();  // (launch_order.h)
+
 constexpr int kK3Stages = kK3ConsumerWarps;  // one ring stage per consumer warp
 
 // Floats a CTA receives in the split merge, maximised over the split count S:

@@ -40,6 +40,9 @@
 
 namespace qa {
 
+// Whether steps overlap earlier kernels of their stream (qa_set_early_reads).
+bool early_reads();
+
 // A stream by what its handle stands for.  The legacy default stream (NULL, or
 // the handle 1) and the per-thread one (2) have the same handle on every device,
 // and the latter in every thread, but each device, and each thread, has its own.

@@ -30,9 +30,6 @@ struct FaultPlan {
 // Takes (and disarms) the armed fault for `kernel` (QA_KERNEL_* index), if any.
 FaultPlan take_fault(int kernel);
 
-// Whether steps overlap earlier kernels of their stream (qa_set_early_reads).
-bool early_reads();
-
 // ---------------------------------------------------------------- K1
 // Sequences per prefill launch (K1 and K2 take their per-sequence data as
 // kernel parameters; longer batches are split into several launches).
