@@ -18,8 +18,11 @@
 // constant times P) gives in every lane of a column, together with the sum of the
 // weights as they were rounded to fp16.  Scales multiply the block's sums: one FMA
 // per accumulator and 64 keys.
-//   The running maximum lags: weights are 2^(t - ref), and ref moves only when one
-// would pass 2^8.
+//   The running maximum lags: weights are 2^(t - ref), and ref moves only when one would
+// pass 2^15, which fp16 still holds, to where the largest is 2^7.  So a warp's largest
+// weight is 2^7 at least, and what fp16 cannot hold of another is below 2^-32 of it
+// (a step of its smallest numbers is 2^-24).  Outputs are summed 2^32 times too small, so
+// that 2^17 keys of the largest bf16 numbers stay in range.
 //   S CTAs (a power of two) of a cluster share a (sequence, kv head); each sends its
 // sums to the CTAs that finish them, through distributed shared memory.
 //
@@ -47,7 +50,8 @@ namespace qa {
 
 constexpr int kQ8Warps = 4, kQ8Threads = kQ8Warps * 32;
 constexpr float kQ8NoRef = -3e38f;   // no key yet
-constexpr float kQ8Lag = 8.f;
+constexpr float kQ8Lift = 7.f;       // the largest weight's exponent where ref is set,
+constexpr float kQ8Most = 15.f;      // and the one that it may grow to
 
 // A (16x16 fp16) * B (16x8 fp16), fp32 accumulators.
 __device__ __forceinline__ void q8_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -91,7 +95,7 @@ __device__ __forceinline__ void q8_send(uint32_t addr, uint32_t x, uint32_t bar)
 }
 
 // Sums of a warp: columns (heads) 2 t and 2 t + 1 of the MMAs (t = lane % 4); o[m] holds
-// dims (D / 8) g + 2 m and + 1 of both heads, 2^24 times too small.
+// dims (D / 8) g + 2 m and + 1 of both heads, 2^32 times too small.
 template <int D>
 struct Q8Acc {
     float ref[2], l[2];
@@ -102,13 +106,13 @@ template <int D>
 __device__ __forceinline__ void q8_raise(Q8Acc<D> &a, float m0, float m1) {
     // m0, m1: this lane's largest scores of its two heads
     const unsigned FULL = 0xffffffffu;
-    if (!__any_sync(FULL, m0 > a.ref[0] + kQ8Lag || m1 > a.ref[1] + kQ8Lag)) return;
+    if (!__any_sync(FULL, m0 > a.ref[0] + kQ8Most || m1 > a.ref[1] + kQ8Most)) return;
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(FULL, m0, o));
         m1 = fmaxf(m1, __shfl_xor_sync(FULL, m1, o));
     }
-    const float r0 = m0 > a.ref[0] + kQ8Lag ? m0 : a.ref[0], r1 = m1 > a.ref[1] + kQ8Lag ? m1 : a.ref[1];
+    const float r0 = m0 > a.ref[0] + kQ8Most ? m0 - kQ8Lift : a.ref[0], r1 = m1 > a.ref[1] + kQ8Most ? m1 - kQ8Lift : a.ref[1];
     const float f0 = q8_exp2(a.ref[0] - r0), f1 = q8_exp2(a.ref[1] - r1);
     a.ref[0] = r0;
     a.ref[1] = r1;
@@ -731,17 +735,18 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         load_v(ahead);
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
+            const float by = sc[n].y * 0.00390625f;  // (acc is 2^24 times too small)
 #pragma unroll
             for (int m = 0; m < D / 16; ++m)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a.o[m][e] = fmaf(acc[n][m][e], sc[n].y, a.o[m][e]);
+                for (int e = 0; e < 4; ++e) a.o[m][e] = fmaf(acc[n][m][e], by, a.o[m][e]);
             blk[n] = ahead[n];
         }
     }
 
     // ---------------------------------------------------------------- rows in bf16
     // 16 of them a warp, the last warps (which have the fewest blocks) first.  Weights as
-    // the sum of two bf16 numbers.
+    // the sum of two bf16 numbers, 2^32 times too small.
     const int tile = kQ8Warps - 1 - warp;
     if (me == 0) {
         q8_copy_wait();
@@ -768,7 +773,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float w0 = q8_exp2(s[2 * e] - a.ref[0]), w1 = q8_exp2(s[2 * e + 1] - a.ref[1]);
+            constexpr float kSmall = 2.3283064365386963e-10f;
+            const float w0 = q8_exp2(s[2 * e] - a.ref[0]) * kSmall, w1 = q8_exp2(s[2 * e + 1] - a.ref[1]) * kSmall;
             const uint32_t x = pack_bf16(w0, w1);
             hi[e] = q8_transpose(x);
             lo[e] = q8_transpose(pack_bf16(w0 - bf16lo(x), w1 - bf16hi(x)));
@@ -777,8 +783,8 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
         float l[4] = {0.f, 0.f, 0.f, 0.f};
         q8_mma_bf16(l, kOne, kOne, kOne, kOne, hi[0], hi[1]);
         q8_mma_bf16(l, kOne, kOne, kOne, kOne, lo[0], lo[1]);
-        a.l[0] += l[0];
-        a.l[1] += l[1];
+        a.l[0] = fmaf(l[0], 4294967296.f, a.l[0]);
+        a.l[1] = fmaf(l[1], 4294967296.f, a.l[1]);
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {  // 8 dims of the lane's D / 8, of 4 keys
             uint4 x[4];
@@ -797,7 +803,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 q8_mma_bf16(acc, a0, a1, a2, a3, hi[0], hi[1]);
                 q8_mma_bf16(acc, a0, a1, a2, a3, lo[0], lo[1]);
 #pragma unroll
-                for (int f = 0; f < 4; ++f) a.o[4 * i + e][f] = fmaf(acc[f], 5.9604644775390625e-08f, a.o[4 * i + e][f]);
+                for (int f = 0; f < 4; ++f) a.o[4 * i + e][f] += acc[f];
             }
         }
     }
@@ -834,7 +840,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
             l = fmaf(f[w], sm.l[w][head], l);
         }
         if (S == 1) {
-            const float inv = 16777216.f / l;
+            const float inv = 4294967296.f / l;
             griddep_wait();
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         } else if (choose ? listed : !withhold) {
@@ -859,7 +865,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
                 o.y = fmaf(f, x.y, o.y);
                 l = fmaf(f, y.y, l);
             }
-            const float inv = 16777216.f / l;
+            const float inv = 4294967296.f / l;
             *reinterpret_cast<uint32_t *>(out + e) = pack_bf16(o.x * inv, o.y * inv);
         }
     }
