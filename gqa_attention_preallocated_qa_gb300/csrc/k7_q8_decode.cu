@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const unsigned FULL = 0xffffffffu;
     extern __shared__ uint4 smem[];
     Q8StepSmem<D> &sm = *reinterpret_cast<Q8StepSmem<D> *>(smem);
-    // Sparse: the scores of every block; behind them the chosen blocks of this CTA.
+    // Sparse: the scores of every block (n_scores); behind them the chosen blocks of this CTA.
     uint32_t *keys = reinterpret_cast<uint32_t *>(&sm + 1);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
     const int items = choose ? p.n_blocks : full;
     const int item_lo = items * me >> log_S, item_hi = items * (me + 1) >> log_S;  // (at most 2^18)
     int item = item_lo + warp;
-    uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.layer.nblk);
+    uint16_t *list = reinterpret_cast<uint16_t *>(keys + p.n_scores);
     const uint8_t *codes = p.layer.codes + base * (2 * kQ8Block * D) + lane * 16;
     uint4 k[NB][NV], v[NB][NV];
     float2 scale[NB];
@@ -907,6 +907,13 @@ __global__ void __launch_bounds__(kQ8Threads, 2) q8_decode_kernel(const __grid_c
 constexpr size_t kQ8SmemLeast = 77 * 1024;
 static_assert(sizeof(Q8StepSmem<128>) <= kQ8SmemLeast, "of a dense step");
 
+template <int D>
+static size_t q8_smem(const Q8StepParams &p) {
+    const size_t choice = p.n_scores > 0 ? static_cast<size_t>(p.n_scores) * 4 + static_cast<size_t>(p.n_blocks) * 2 : 0;
+    return std::max(kQ8SmemLeast, sizeof(Q8StepSmem<D>) + choice);
+}
+size_t q8_step_smem(const Q8StepParams &p, int D) { return D == 128 ? q8_smem<128>(p) : q8_smem<64>(p); }
+
 template <int D, bool kSparse>
 static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
     static std::atomic<unsigned> configured{0u};  // devices 0..31 set up (one bit each)
@@ -924,7 +931,7 @@ static cudaError_t q8_launch(const Q8StepParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((p.ctas + p.cluster - 1) / p.cluster * p.cluster);
     cfg.blockDim = dim3(kQ8Threads);
-    cfg.dynamicSmemBytes = std::max(kQ8SmemLeast, sizeof(Q8StepSmem<D>) + (kSparse ? static_cast<size_t>(p.layer.nblk) * 4 + static_cast<size_t>(p.n_blocks) * 2 : 0));
+    cfg.dynamicSmemBytes = q8_smem<D>(p);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

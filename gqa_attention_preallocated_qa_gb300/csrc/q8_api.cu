@@ -24,6 +24,7 @@ struct qa_q8_cache {
     qa_config cfg{};
     int device = 0;
     int num_sms = 0;
+    int sm_smem = 0, reserved_smem = 0;  // shared memory of an SM, and what it keeps of it for each CTA
     int nblk = 0;              // blocks of one (sequence, kv head)
     void *mem = nullptr;       // one allocation: all of the following
     uint8_t *codes = nullptr;
@@ -168,7 +169,10 @@ qa_status run_step(qa_q8_cache *c, int layer, int batch, const StepCall &a, cuda
         std::sort(p.seq, p.seq + n, [](const qa::Q8Seq &x, const qa::Q8Seq &y) { return x.pos != y.pos ? x.pos > y.pos : x.slot < y.slot; });
         int work[qa::kQ8MaxSeqPerLaunch], splits[qa::kQ8MaxSeqPerLaunch];
         for (int i = 0; i < n; ++i) work[i] = qa::q8_step_work(g.head_dim, p.seq[i].pos / qa::kQ8Block, a.n_blocks);
-        p.cluster = qa::q8_plan_step(c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits);
+        const int longest = p.seq[0].pos / qa::kQ8Block;
+        p.n_scores = a.blocks && longest > a.n_blocks ? longest : 0;
+        const int per_sm = qa::q8_ctas_per_sm(c->sm_smem, c->reserved_smem, qa::q8_step_smem(p, g.head_dim));
+        p.cluster = qa::q8_plan_step(c->num_sms, g.n_kv_heads, qa::kQ8MaxSplits, n, work, splits, per_sm);
         p.nseq = n;
         p.ctas = 0;
         p.per_seq = splits[n - 1] == p.cluster ? p.cluster * g.n_kv_heads : 0;
@@ -310,6 +314,8 @@ QA_API qa_status qa_q8_cache_alloc(const qa_config *cfg, qa_q8_cache **out) {
                          align256(tickets) + 256;
     bool ok = cudaGetDevice(&c->device) == cudaSuccess &&
               cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device) == cudaSuccess &&
+              cudaDeviceGetAttribute(&c->sm_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, c->device) == cudaSuccess &&
+              cudaDeviceGetAttribute(&c->reserved_smem, cudaDevAttrReservedSharedMemoryPerBlock, c->device) == cudaSuccess &&
               cudaMalloc(&c->mem, total) == cudaSuccess && cudaMemsetAsync(c->mem, 0, total, nullptr) == cudaSuccess;
     ok = ok && no_throw([&] {
         uint8_t *at = static_cast<uint8_t *>(c->mem);

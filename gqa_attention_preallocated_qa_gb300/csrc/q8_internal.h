@@ -64,6 +64,7 @@ struct Q8StepParams {
     int32_t *blocks;                     // [batch][Hkv][n_blocks]: receives the chosen blocks (null: all are)
     uint32_t *err;
     int n_blocks;
+    int n_scores;                        // blocks of the longest sequence that has to choose (0: none has)
     int Hq, G, cap;
     int nseq, ctas, cluster;             // sequences, CTAs with work, CTAs of a cluster (a multiple of every S)
     int per_seq;                         // CTAs of each sequence where all have the same number, else 0
@@ -98,6 +99,7 @@ static_assert(sizeof(Q8PrefillRowsParams) <= 4096, "travels in the 4 KB of kerne
 cudaError_t launch_q8_prefill_rows(const Q8PrefillRowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_write(const Q8RowsParams &p, int D, cudaStream_t stream);
 cudaError_t launch_q8_read(const Q8RowsParams &p, int D, cudaStream_t stream);
+size_t q8_step_smem(const Q8StepParams &p, int D);  // shared memory of a CTA, bytes
 cudaError_t launch_q8_decode(const Q8StepParams &p, int D, cudaStream_t stream);
 
 // Shared with the other caches' host sides.

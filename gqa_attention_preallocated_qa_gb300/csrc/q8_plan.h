@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 namespace qa {
@@ -14,8 +15,16 @@ inline int q8_step_work(int D, int full, int n_blocks) {
     return D == 128 ? blocks : (blocks + 1) / 2;
 }
 
+// CTAs of a launch that one SM holds: two, for their registers, where its shared memory has
+// room for them.  (A sparse step's has four bytes for each block of its longest sequence and
+// two for each that it chooses: D = 128 has one CTA an SM from some 780 thousand positions,
+// with 4096 chosen blocks from 650 thousand.)
+inline int q8_ctas_per_sm(size_t sm_bytes, size_t reserved, size_t cta_bytes) {
+    return sm_bytes / 2 >= reserved + cta_bytes ? 2 : 1;
+}
+
 // splits[i], powers of two up to `most`, for n sequences of work[i] blocks for each of Hkv
-// kv heads; returns the largest.  One SM holds two CTAs of four warps.
+// kv heads; returns the largest.  One SM holds per_sm CTAs of four warps.
 //   A CTA costs its set-up and merge, and a warp its blocks one after the other, so a step
 // alone is fastest with one block a warp, and a chain of steps, which run side by side,
 // with fewer CTAs.  Up to three blocks a warp are taken where that leaves room for several
@@ -26,7 +35,7 @@ inline int q8_step_work(int D, int full, int n_blocks) {
 // Four blocks a warp: B 1, 8192 keys, 16 splits 5.1 / 20.0, 8 (taken) 3.9 / 19.9; B 2, 4096,
 // 8 splits 4.7 / 19.6, 4 (taken) 3.8 / 19.4; but B 4, 2048, 4 splits (taken) 4.7 / 18.6, 2
 // 4.0 / 20.9.  Six: B 4, 2900, 4 splits (taken) 5.6 / 19.6, 2 5.0 / 22.9.
-inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, int *splits) {
+inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, int *splits, int per_sm = 2) {
     int top = 1;
     // Splits that leave a warp at most `per` blocks; their CTAs.
     auto cut = [&](int per) {
@@ -50,7 +59,7 @@ inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, 
     int lo = 0, hi = (work[0] + 3) / 4;  // cut(hi) is of ones
     while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
-        if (cut(mid) <= 2 * num_sms) hi = mid; else lo = mid;
+        if (cut(mid) <= per_sm * num_sms) hi = mid; else lo = mid;
     }
     cut(hi);
     return top;
