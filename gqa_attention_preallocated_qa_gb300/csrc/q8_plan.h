@@ -35,6 +35,8 @@ inline int q8_ctas_per_sm(size_t sm_bytes, size_t reserved, size_t cta_bytes) {
 // Four blocks a warp: B 1, 8192 keys, 16 splits 5.1 / 20.0, 8 (taken) 3.9 / 19.9; B 2, 4096,
 // 8 splits 4.7 / 19.6, 4 (taken) 3.8 / 19.4; but B 4, 2048, 4 splits (taken) 4.7 / 18.6, 2
 // 4.0 / 20.9.  Six: B 4, 2900, 4 splits (taken) 5.6 / 19.6, 2 5.0 / 22.9.
+// D = 64 takes the same rules with two blocks as one (a warp has two in hand); it has no
+// sweep of its own.
 inline int q8_plan_step(int num_sms, int Hkv, int most, int n, const int *work, int *splits, int per_sm = 2) {
     int top = 1;
     // Splits that leave a warp at most `per` blocks; their CTAs.

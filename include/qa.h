@@ -544,7 +544,8 @@ qa_status qa_q4_memory_info(qa_q4_cache *cache, uint64_t *cache_bytes, uint64_t 
  * error of a later one leaves the earlier ones enqueued.  Calls may be made with
  * another device current; the stream belongs to the cache's device.  Outputs share no
  * byte with inputs or with each other (INVALID_ARG).
- * All calls but qa_q8_prefill may be captured into graphs.  qa_q8_append, qa_q8_read and
+ * All calls but qa_q8_prefill may be captured into graphs, on one stream or on several
+ * that wait for each other's events.  qa_q8_append, qa_q8_read and
  * qa_q8_prefill are ordered on their stream like plain launches.  Decode and sparse
  * steps overlap earlier kernels of the stream like qa_decode_step, with the same
  * conditions on other code's kernels between the calls: they read q, k, v and the weights
@@ -612,6 +613,11 @@ qa_status qa_q8_prefill(qa_q8_cache *cache, int layer, int batch, const int32_t 
  * normed and rotated).
  * k_held, v_held: both NULL, or [batch][Hkv][D] that receive the new rows as the step
  * attends to them.
+ * Weights of complete blocks are rounded to fp16: 2^-11 of a weight, or 2^-32 of the
+ * largest where that is more.  A value's code carries an offset that is taken away again,
+ * which costs 3.02 * 2^-17 of the block's largest value at most, in the block's share of
+ * the weights.  A value that is not finite in a row held as it came makes its dimension of
+ * the heads that see it infinite or NaN.
  * Errors: INVALID_ARG, ALIGNMENT, CAPACITY (a position at or above the capacity), CUDA. */
 qa_status qa_q8_decode_step(qa_q8_cache *cache, int layer, int batch, const int32_t *positions,
                             const void *q, const void *k, const void *v, const void *q_norm_w,
@@ -620,9 +626,10 @@ qa_status qa_q8_decode_step(qa_q8_cache *cache, int layer, int batch, const int3
 
 /* The same with positions in DEVICE memory (int32 [batch]), read when the previous
  * kernel on the stream has finished: for graph capture, where the caller advances
- * them inside the graph.  A position outside 0..capacity-1 leaves its sequence alone
- * and sets QA_ERR_DEVICE_BOUNDS (qa_q8_get_device_error).  The split count is planned
- * for a full cache. */
+ * them inside the graph.  (So such steps do not overlap each other, unlike those with
+ * host positions.)  A position outside 0..capacity-1 leaves its sequence alone and sets
+ * QA_ERR_DEVICE_BOUNDS (qa_q8_get_device_error).  The split count is planned for a full
+ * cache. */
 qa_status qa_q8_decode_step_device_positions(qa_q8_cache *cache, int layer, int batch,
                                              const int32_t *positions, const void *q, const void *k,
                                              const void *v, const void *q_norm_w,
