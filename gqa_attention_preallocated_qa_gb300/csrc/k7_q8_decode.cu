@@ -106,13 +106,15 @@ template <int D>
 __device__ __forceinline__ void q8_raise(Q8Acc<D> &a, float m0, float m1) {
     // m0, m1: this lane's largest scores of its two heads
     const unsigned FULL = 0xffffffffu;
-    if (!__any_sync(FULL, m0 > a.ref[0] + kQ8Most || m1 > a.ref[1] + kQ8Most)) return;
+    // (The differences are the weights' exponents, and exact for scores of any size; a sum with
+    // the limit is not, and from 2^24 on would let a weight pass fp16's largest number.)
+    if (!__any_sync(FULL, m0 - a.ref[0] > kQ8Most || m1 - a.ref[1] > kQ8Most)) return;
 #pragma unroll
     for (int o = 4; o <= 16; o <<= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(FULL, m0, o));
         m1 = fmaxf(m1, __shfl_xor_sync(FULL, m1, o));
     }
-    const float r0 = m0 > a.ref[0] + kQ8Most ? m0 - kQ8Lift : a.ref[0], r1 = m1 > a.ref[1] + kQ8Most ? m1 - kQ8Lift : a.ref[1];
+    const float r0 = m0 - a.ref[0] > kQ8Most ? m0 - kQ8Lift : a.ref[0], r1 = m1 - a.ref[1] > kQ8Most ? m1 - kQ8Lift : a.ref[1];
     const float f0 = q8_exp2(a.ref[0] - r0), f1 = q8_exp2(a.ref[1] - r1);
     a.ref[0] = r0;
     a.ref[1] = r1;

@@ -129,3 +129,29 @@ def test_values_of_the_largest_size(qa, d):
     n = 6
     score = [2.4 * (j // BLOCK) for j in range(n * BLOCK)]
     check(qa, d, score, [2.0 ** 126 * (1 if j % 3 else -1) for j in range(n * BLOCK)], (0.0, 2.0 ** 126))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [23, 24, 25, 26, 27, 28])
+def test_scores_whose_steps_are_larger_than_one(qa, d, size):
+    """Scores near 2^size differ between blocks by up to 32, in steps of fp32 there: the weights
+    are what rounding leaves of them, and the outputs stay between the values."""
+    n, batch = 48, 8
+    gen = torch.Generator(device="cuda").manual_seed(size)
+    with Cache(qa, batch, 8, 2, d, n * BLOCK + 10) as c:
+        # dimension 0 has the score, dimension 1 what it differs by
+        by = 2.0 ** size * d ** 0.5 / math.log2(math.e)
+        q = torch.zeros(batch, 8, d, device="cuda")
+        q[:, :, 0] = by ** 0.5
+        q[:, :, 1] = by ** 0.5 * 2.0 ** (5 - size)
+        k = torch.zeros(batch, n * BLOCK + 1, 2, d, device="cuda")
+        k[..., 0] = by ** 0.5
+        code = torch.randint(0, 128, (batch, n, 1, 2), generator=gen, device="cuda") / 127
+        k[:, :-1, :, 1] = by ** 0.5 * code.expand(-1, -1, BLOCK, -1).reshape(batch, n * BLOCK, 2)
+        v = 1 + torch.rand(k.shape, generator=gen, device="cuda")
+        q, k, v = q.bfloat16(), k.bfloat16(), v.bfloat16()
+        qa.qa_q8_append(c.h, 0, [0] * batch, [n * BLOCK] * batch, k[:, :-1].flatten(0, 1).contiguous(), v[:, :-1].flatten(0, 1).contiguous())
+        out = torch.empty_like(q)
+        qa.qa_q8_decode_step(c.h, 0, [n * BLOCK] * batch, q, k[:, -1].contiguous(), v[:, -1].contiguous(), None, None, out)
+        assert torch.isfinite(out).all()
+        assert float(out.min()) >= 1 - 2.0 ** -6 and float(out.max()) <= 2 + 2.0 ** -5
